@@ -262,6 +262,134 @@ qsa_status qsa_split_touched_pages(const int32_t* indices, int64_t n_indices, co
                                    int32_t n_sections, const int32_t* section_bytes,
                                    void* stream);
 
+/* ---------------------------------------------------------------- serving step
+ * The operators that a step over a paged cache runs around the attention calls: the batch's page
+ * tables and slot maps, the rotation of q and k to their positions together with the write of the new
+ * K/V rows (as they are, or in 4 bits), and attention with a sliding window and a few first tokens that
+ * stay visible (further below).  The paged entries above read the same tables and caches. */
+
+/* Element type of the serving-step operators' rows. */
+typedef enum qsa_dtype { QSA_BF16 = 0, QSA_FP16 = 1 } qsa_dtype;
+
+/* Page tables and slot maps from request lengths.  Request i holds past_lens[i] cached tokens and brings
+ * new_lens[i] tokens in this step (negative lengths count as 0).  With P(x) = min(ceil(x / page_size),
+ * pages_per_req), it takes P(past + new) - P(past) pages from the free list, requests in order.
+ *   past_lens, new_lens [n_requests] int32
+ *   page_table  [n_requests, pages_per_req] int32, in and out: entries P(past) .. P(past + new) - 1 of
+ *               row i receive the new pages (-1 where the list has run out); the others stay.
+ *   free_pages  [n_free] int32 free physical pages; free_head [1] int32: entries taken so far.
+ *   free_head_out [1] int32: free_head plus the pages taken; may be free_head itself, so that a step
+ *               captured in a CUDA graph takes further pages on every replay.
+ *   cu_seqlens_q [n_requests + 1] int32: exclusive sums of the new lengths, cut off at max_rows.
+ *   kv_lens     [n_requests] int32: past + new (cut off at 2^31 - 1).
+ *   positions   [max_rows] int32, nullable: position of each row in its request.
+ *   slots       [max_rows] int32, nullable: physical slot of each row, page * page_size +
+ *               position mod page_size; -1 where the page is missing, past pages_per_req, or (when
+ *               n_pages > 0) not below n_pages.
+ *               Rows past the last request get -1 in both: qsa_rope_append leaves such rows out.
+ *   shortfall   [1] int32, nullable: pages wanted beyond the end of the free list (0 = none missing).
+ * One kernel launch, no host read.  Calls that share a free list are ordered by the caller.
+ * Errors: QSA_ERR_INVALID_ARG for null or misaligned pointers (4 bytes) and sizes below 1 (n_free,
+ * n_pages, max_rows: below 0); QSA_ERR_UNSUPPORTED for more than 16384 requests, or 2^31 rows or free
+ * pages. */
+qsa_status qsa_page_plan(const int32_t* past_lens, const int32_t* new_lens, int32_t* page_table,
+                         const int32_t* free_pages, int64_t n_free, const int32_t* free_head,
+                         int32_t* free_head_out, int32_t* cu_seqlens_q, int32_t* kv_lens,
+                         int32_t* positions, int32_t* slots, int32_t* shortfall, int32_t n_requests,
+                         int32_t pages_per_req, int32_t page_size, int64_t n_pages, int64_t max_rows,
+                         void* stream);
+
+/* Rotary positions.  Pair i of a head's rotated part at position x turns by x * theta_i:
+ *   a' = m (a cos - b sin),   b' = m (b cos + a sin)
+ * with (a, b) = dims (i, i + rot_dim / 2) of the part in the half layout and (2 i, 2 i + 1) in the
+ * interleaved one; m is the magnitude.  transpose = 1 turns by -x theta_i with the same m: the matrix
+ * transposed, which takes the gradient of the rotated rows to the gradient of the rows.  The part is
+ * dims rot_offset .. rot_offset + rot_dim - 1; the other dims pass through unchanged.
+ *   steps: HOST pointer to rot_dim / 2 fixed-point numbers, 2^64 * (theta_i / 2 pi mod 1), kept by
+ *          the caller (qsa_rope_steps makes them); the angle is then exact to 2^-33 turns at any
+ *          31-bit position. */
+typedef enum qsa_rope_layout { QSA_ROPE_HALF = 0, QSA_ROPE_INTERLEAVED = 1 } qsa_rope_layout;
+typedef struct qsa_rope_spec {
+  const uint64_t* steps;    /* host, [rot_dim / 2] */
+  int32_t rot_dim;          /* even, 0 (nothing turns) .. 512 */
+  int32_t rot_offset;
+  int32_t layout;           /* qsa_rope_layout */
+  int32_t transpose;        /* 0 or 1 */
+  float magnitude;          /* 1 unless the frequencies are scaled */
+} qsa_rope_spec;
+
+/* Frequencies theta_i = base^(-2 i / rot_dim) and their scalings for contexts `factor` times as long:
+ *   LINEAR  theta / factor
+ *   NTK     base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *   TURNS   k theta + (1 - k) theta / factor, where k rises from 0 at pairs that make beta_slow turns over
+ *           original_len tokens to 1 at those that make beta_fast, linearly in the turns
+ *   YARN    the same ends, with k falling linearly in the pair index i from floor(i(beta_fast)), at least 0,
+ *           to ceil(i(beta_slow)), at most rot_dim - 1, i(t) being the pair that makes t turns over
+ *           original_len; magnitude 0.1 ln(factor) + 1 when factor > 1 (Peng et al., "YaRN: Efficient
+ *           Context Window Extension of Large Language Models", 2023)
+ * The magnitude of the other kinds is 1. */
+typedef enum qsa_rope_scale {
+  QSA_ROPE_SCALE_NONE = 0, QSA_ROPE_SCALE_LINEAR = 1, QSA_ROPE_SCALE_NTK = 2,
+  QSA_ROPE_SCALE_YARN = 3, QSA_ROPE_SCALE_TURNS = 4
+} qsa_rope_scale;
+typedef struct qsa_rope_scaling {
+  int32_t kind;             /* qsa_rope_scale */
+  double factor;            /* > 0 */
+  double original_len;      /* YARN, TURNS: > 0 */
+  double beta_fast;         /* YARN, TURNS: > beta_slow > 0 */
+  double beta_slow;
+} qsa_rope_scaling;
+
+/* Host only: steps [rot_dim / 2] and magnitude of a rotation (scaling NULL = none). */
+qsa_status qsa_rope_steps(const qsa_rope_scaling* scaling, int32_t rot_dim, double base, uint64_t* steps,
+                          float* magnitude);
+
+/* Rotates rows: x [n_rows, n_heads, head_dim] of type dtype (qsa_dtype), heads contiguous, rows x_stride
+ * elements apart (0 = one row for all); out likewise with out_stride >= n_heads * head_dim; out may be x with the same
+ * stride, and may not overlap it otherwise.  positions [n_rows] int32; rows with a negative position
+ * are left out: their output is not written.  The arithmetic is fp32, rounded once.
+ * Any head_dim, offset, stride and alignment is taken; rows whose units of 16 dims start on 16-byte
+ * boundaries run the fast kernel. */
+qsa_status qsa_rope(const void* x, void* out, const int32_t* positions, const qsa_rope_spec* rope,
+                    int64_t n_rows, int32_t n_heads, int32_t head_dim, int64_t x_stride,
+                    int64_t out_stride, int32_t dtype, void* stream);
+
+/* Rotates q into q_out and k into the cache, and copies v into the cache.
+ *   q [n_rows, n_qheads, head_dim] (n_qheads = 0: none), k, v [n_rows, n_kvheads, head_dim], rows
+ *   q_stride, k_stride, v_stride elements apart (slices of one projected row are fine).
+ *   k_cache, v_cache [n_slots, n_kvheads, head_dim]; v and v_cache both NULL for a cache of latent rows.
+ *   slots [n_rows] int32: cache slot of each row; rows with a slot < 0 or >= n_slots write no cache row.
+ *   Rows of one call that share a slot leave an unspecified one of them there.
+ *   rope NULL: nothing turns (positions may be NULL then).
+ * Otherwise as qsa_rope. */
+qsa_status qsa_rope_append(const void* q, void* q_out, const void* k, const void* v, void* k_cache,
+                           void* v_cache, const int32_t* positions, const int32_t* slots,
+                           const qsa_rope_spec* rope, int64_t n_rows, int64_t n_slots, int32_t n_qheads,
+                           int32_t n_kvheads, int32_t head_dim, int64_t q_stride, int64_t q_out_stride,
+                           int64_t k_stride, int64_t v_stride, int32_t dtype, void* stream);
+
+/* The same into a cache held in 4 bits.  A head's row of head_dim values is stored as head_dim / 2 bytes of
+ * e2m1 codes (sign, 2 exponent bits of bias 1, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6; the even dim in the
+ * low half of the byte) and head_dim / 16 e4m3 scales, one per 16 dims:
+ *   s = e4m3(max |x| / g / 6),  code = e2m1(x / g / s)   (0 where s = 0),  value = e2m1(code) s g
+ * rounded to nearest, ties to even, beyond the range to the largest value; g = k_global or v_global.
+ * x is the rotated row in fp32.  e2m1 has no NaN or infinity: they are stored as values of the largest
+ * magnitude that the block's scale gives.
+ *   k_cache, v_cache [n_slots, n_kvheads, head_dim / 2] bytes; k_scale, v_scale [n_slots, n_kvheads,
+ *   head_dim / 16] e4m3 bytes
+ *   k_seen, v_seen [n_rows, n_kvheads, head_dim] of type dtype, nullable: the values that the cache now
+ *   holds for the rows it stored, for attention over the step's own rows that agrees with later reads.
+ * QSA_ERR_UNSUPPORTED unless head_dim % 32 = 0, rot_offset % 16 = 0 and rot_dim % 32 = 0 (interleaved:
+ * % 16); QSA_ERR_INVALID_ARG unless every pointer is 16-byte aligned (scales: any) and every stride a multiple
+ * of 8. */
+qsa_status qsa_rope_append_fp4(const void* q, void* q_out, const void* k, const void* v, void* k_cache,
+                               uint8_t* k_scale, void* v_cache, uint8_t* v_scale, float k_global,
+                               float v_global, void* k_seen, void* v_seen, const int32_t* positions,
+                               const int32_t* slots, const qsa_rope_spec* rope, int64_t n_rows,
+                               int64_t n_slots, int32_t n_qheads, int32_t n_kvheads, int32_t head_dim,
+                               int64_t q_stride, int64_t q_out_stride, int64_t k_stride,
+                               int64_t v_stride, int32_t dtype, void* stream);
+
 /* Allocation-free variant of qsa_sparse_prefill (same arguments, same results).  The pages
  * have no counterpart: it exists for callers that must not allocate device memory -- code
  * whose GPU memory is owned entirely by a framework's pool, latency-critical loops where an

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from collections import namedtuple
 from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -27,7 +28,8 @@ EXPORTED = ["qsa_sparse_prefill", "qsa_sparse_prefill_ex", "qsa_union_workspace_
             "qsa_sparse_prefill_paged", "qsa_sparse_mla_prefill", "qsa_select_mla_geometry",
             "qsa_page_mark", "qsa_page_split", "qsa_split_touched_pages",
             "qsa_sparse_prefill_fp8", "qsa_debug_stall_next_call", "qsa_sparse_mla_prefill_paged",
-            "qsa_sparse_prefill_fp8_paged"]
+            "qsa_sparse_prefill_fp8_paged",
+            "qsa_page_plan", "qsa_rope_steps", "qsa_rope", "qsa_rope_append", "qsa_rope_append_fp4"]
 
 # Size of the library-owned scratch array used by qsa_sparse_prefill_noalloc (include/qsa.h).
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -52,6 +54,18 @@ class Counters(ctypes.Structure):
 
     def as_dict(self):
         return {name: int(getattr(self, name)) for name, _ in self._fields_}
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double)]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("rot_offset", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("transpose", ctypes.c_int32), ("magnitude", ctypes.c_float)]
 
 
 _lib = None
@@ -103,6 +117,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qsa_sparse_mla_prefill_paged.restype = ctypes.c_int
     lib.qsa_probe_gather_ceiling.argtypes = [vp, i64, vp, i64, i32, i32, ctypes.POINTER(f32), vp]
     lib.qsa_probe_gather_ceiling.restype = ctypes.c_int
+    lib.qsa_page_plan.argtypes = [vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i64, i64, vp]
+    lib.qsa_page_plan.restype = ctypes.c_int
+    f64 = ctypes.c_double
+    lib.qsa_rope_steps.argtypes = [ctypes.POINTER(RopeScaling), i32, f64, vp, ctypes.POINTER(f32)]
+    lib.qsa_rope_steps.restype = ctypes.c_int
+    lib.qsa_rope.argtypes = [vp, vp, vp, vp, i64, i32, i32, i64, i64, i32, vp]
+    lib.qsa_rope.restype = ctypes.c_int
+    lib.qsa_rope_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, i64,
+                                    i64, i64, i64, i32, vp]
+    lib.qsa_rope_append.restype = ctypes.c_int
+    lib.qsa_rope_append_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, f32, f32, vp, vp, vp, vp, vp, i64,
+                                        i64, i32, i32, i32, i64, i64, i64, i64, i32, vp]
+    lib.qsa_rope_append_fp4.restype = ctypes.c_int
     for name in ("qsa_union_workspace_bytes", "qsa_workspace_bytes"):
         getattr(lib, name).argtypes = [i64, i32, i32]
         getattr(lib, name).restype = sz
@@ -550,3 +577,283 @@ def device_status(stream=None) -> int:
 
 def version() -> str:
     return load_library().qsa_version().decode()
+
+
+# ------------------------------------------------------------------------------ serving step
+
+_DTYPE_CODES = None          # {torch.bfloat16: 0, torch.float16: 1}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "turns": 4}
+
+
+def _dtype_code(dtype, name):
+    global _DTYPE_CODES
+    if _DTYPE_CODES is None:
+        import torch
+        _DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1}
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _tensor(t, dtype, name, shape, device):
+    """Checks a required contiguous CUDA tensor on `device`; None in shape = any extent."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    got = t.shape
+    if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(got)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, dtype, name, shape, device):
+    """Checks rows [n, heads, dim] whose heads are contiguous; returns the row stride in elements."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    got = t.shape
+    if len(got) != 3 or any(w is not None and w != g for w, g in zip(shape, got)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(got)}")
+    n, heads, dim = got
+    stride = t.stride()
+    if (dim > 1 and stride[2] != 1) or (heads > 1 and stride[1] != dim):
+        raise ValueError(f"{name} must have contiguous heads (strides (any, {dim}, 1)), got {stride}")
+    return stride[0] if n > 1 else heads * dim
+
+
+class _Launch:
+    """Makes the tensors' device current for a call and gives the stream to launch on.  Tensors made
+    for a call on another stream than the current one are recorded on it."""
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise ValueError("tensors must be CUDA tensors")
+        self.device, self.stream = device, stream
+        self.before = torch.cuda.current_device()
+        if self.before != device.index:
+            torch.cuda.set_device(device.index)
+        if stream is None:
+            self.ptr = torch.cuda.current_stream(device).cuda_stream
+        else:
+            self.ptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        if self.before != self.device.index:
+            import torch
+            torch.cuda.set_device(self.before)
+
+    def own(self, t):
+        if self.stream is not None and hasattr(self.stream, "cuda_stream"):
+            t.record_stream(self.stream)
+        elif self.stream is not None:
+            import torch
+            t.record_stream(torch.cuda.ExternalStream(self.ptr, device=self.device))
+        return t
+
+
+PagePlan = namedtuple("PagePlan", "cu_seqlens_q kv_lens positions slots free_head shortfall")
+
+
+def page_plan(past_lens, new_lens, page_table, free_pages, free_head, page_size: int, max_rows: int,
+              *, n_pages: int = 0, free_head_out=None, cu_seqlens_q=None, kv_lens=None,
+              positions=None, slots=None, shortfall=None, stream=None) -> PagePlan:
+    """Page tables and slot maps of a step from its requests' lengths (qsa_page_plan).
+
+    past_lens, new_lens [n_requests] int32; page_table [n_requests, pages_per_req] int32 is
+    updated in place with pages taken from free_pages [n_free] int32, of which free_head [1] int32
+    are taken already; free_head_out = free_head updates it in place (None = a new tensor).
+    Returns cu_seqlens_q [n_requests + 1], kv_lens [n_requests], positions and slots [max_rows] (-1 on
+    rows past the last request), free_head [1] and shortfall [1], all int32."""
+    import torch
+    i32, dev = torch.int32, past_lens.device
+    n = past_lens.shape[0]
+    _tensor(past_lens, i32, "past_lens", (n,), dev)
+    _tensor(new_lens, i32, "new_lens", (n,), dev)
+    _tensor(page_table, i32, "page_table", (n, None), dev)
+    _tensor(free_pages, i32, "free_pages", (None,), dev)
+    _tensor(free_head, i32, "free_head", (1,), dev)
+    max_rows = int(max_rows)
+    if max_rows < 0:
+        raise ValueError("max_rows must not be negative")
+    with _Launch(dev, stream) as on:
+        outs = [("cu_seqlens_q", cu_seqlens_q, n + 1), ("kv_lens", kv_lens, n),
+                ("positions", positions, max_rows), ("slots", slots, max_rows),
+                ("free_head_out", free_head_out, 1), ("shortfall", shortfall, 1)]
+        # the outputs that the caller did not bring share one allocation, each 16-byte aligned
+        room = sum((m + 3) & ~3 for _, t, m in outs if t is None)
+        if room:
+            block = torch.empty(room, dtype=i32, device=dev)
+            if stream is not None:
+                on.own(block)
+        made, at = [], 0
+        for name, t, m in outs:
+            if t is None:
+                t = block[at:at + m]
+                at += (m + 3) & ~3
+            else:
+                _tensor(t, i32, name, (m,), dev)
+            made.append(t)
+        cu, kv, pos, slot, head, short = made
+        st = load_library().qsa_page_plan(
+            past_lens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(), free_pages.data_ptr(),
+            free_pages.shape[0], free_head.data_ptr(), head.data_ptr(), cu.data_ptr(), kv.data_ptr(),
+            pos.data_ptr(), slot.data_ptr(), short.data_ptr(), n, page_table.shape[1],
+            int(page_size), int(n_pages), max_rows, on.ptr)
+    _check(st, "qsa_page_plan")
+    return PagePlan(cu, kv, pos, slot, head, short)
+
+
+class RopeTable:
+    """The frequencies of a rotation (qsa_rope_steps), made once and kept with the model: rot_dim / 2
+    fixed-point steps on the host and the magnitude of the rotated values."""
+
+    def __init__(self, rot_dim: int, steps, magnitude: float):
+        self.rot_dim, self.magnitude = int(rot_dim), float(magnitude)
+        self._steps = (ctypes.c_uint64 * max(1, self.rot_dim // 2))(*steps)
+        self._address = ctypes.addressof(self._steps)
+
+    @property
+    def steps(self):
+        """Turns per token of every pair, in units of 2^-64."""
+        return list(self._steps)[:self.rot_dim // 2]
+
+    def spec(self, layout: str, rot_offset: int, transpose: bool = False) -> RopeSpec:
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
+        return RopeSpec(self._address, self.rot_dim, int(rot_offset), ROPE_LAYOUTS[layout],
+                        1 if transpose else 0, self.magnitude)
+
+
+def rope_table(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+               original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+               magnitude: Optional[float] = None) -> RopeTable:
+    """Frequencies base^(-2 i / rot_dim), scaled for long contexts: "none", "linear", "ntk", "yarn" or
+    "turns" (the formulas are in include/qsa.h).  magnitude None = the scaling's own.  Host only."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    rot_dim = int(rot_dim)
+    steps = (ctypes.c_uint64 * max(1, rot_dim // 2))()
+    own = ctypes.c_float(1.0)
+    s = RopeScaling(ROPE_SCALINGS[scaling], float(factor), float(original_len), float(beta_fast),
+                    float(beta_slow))
+    st = load_library().qsa_rope_steps(ctypes.byref(s), rot_dim, float(base), ctypes.addressof(steps),
+                                       ctypes.byref(own))
+    _check(st, "qsa_rope_steps")
+    return RopeTable(rot_dim, steps, own.value if magnitude is None else magnitude)
+
+
+def rope(x, positions, table: RopeTable, *, layout: str = "half", rot_offset: int = 0,
+         transpose: bool = False, out=None, stream=None):
+    """Rotates x [R, H, D] (bf16 or fp16, contiguous heads) to positions [R] int32 (qsa_rope).
+
+    transpose=True applies the transposed rotation, which takes the output's gradient to the
+    input's.  Rows with a negative position are not written.  out may be x."""
+    import torch
+    R, H, D = x.shape
+    dev, code = x.device, _dtype_code(x.dtype, "x")
+    xs = _rows(x, x.dtype, "x", (R, H, D), dev)
+    _tensor(positions, torch.int32, "positions", (R,), dev)
+    spec = table.spec(layout, rot_offset, transpose)
+    with _Launch(dev, stream) as on:
+        if out is None:
+            out = torch.empty((R, H, D), dtype=x.dtype, device=dev)
+            if stream is not None:
+                on.own(out)
+        os_ = _rows(out, x.dtype, "out", (R, H, D), dev)
+        if R == 0:
+            return out              # (an empty tensor has no address)
+        st = load_library().qsa_rope(x.data_ptr(), out.data_ptr(), positions.data_ptr(),
+                                     ctypes.byref(spec), R, H, D, xs, os_, code, on.ptr)
+    _check(st, "qsa_rope")
+    return out
+
+
+def _append_args(q, k, v, positions, slots, table, layout, rot_offset, q_out, on, stream):
+    import torch
+    R, Hkv, D = k.shape
+    dev, dt = k.device, k.dtype
+    ks = _rows(k, dt, "k", (R, Hkv, D), dev)
+    vs = 0 if v is None else _rows(v, dt, "v", (R, Hkv, D), dev)
+    _tensor(slots, torch.int32, "slots", (R,), dev)
+    if positions is not None:
+        _tensor(positions, torch.int32, "positions", (R,), dev)
+    elif table is not None:
+        raise ValueError("positions are needed with a rope table")
+    Hq = qs = qos = 0
+    if q is not None:
+        Hq = q.shape[1]
+        qs = _rows(q, dt, "q", (R, Hq, D), dev)
+        if q_out is None:
+            q_out = torch.empty((R, Hq, D), dtype=dt, device=dev)
+            if stream is not None:
+                on.own(q_out)
+        qos = _rows(q_out, dt, "q_out", (R, Hq, D), dev)
+    spec = None if table is None else ctypes.byref(table.spec(layout, rot_offset))
+    return R, Hq, Hkv, D, qs, qos, ks, vs, q_out, spec
+
+
+def rope_append(q, k, v, k_cache, v_cache, positions, slots, table: Optional[RopeTable], *,
+                layout: str = "half", rot_offset: int = 0, q_out=None, stream=None):
+    """Rotates q into q_out and k into the cache, and copies v into the cache (qsa_rope_append).
+
+    q [R, Hq, D] or None, k, v [R, Hkv, D] (bf16 or fp16, contiguous heads, any row stride); k_cache,
+    v_cache [n_slots, Hkv, D]; v and v_cache None for a cache of latent rows.  positions, slots [R]
+    int32: rows with a negative position are left out, rows with a slot outside the cache write no
+    cache row.  table None: nothing turns.  Returns q_out (a new tensor unless given; may be q)."""
+    dev, code = k.device, _dtype_code(k.dtype, "k")
+    if (v is None) != (v_cache is None):
+        raise ValueError("v and v_cache come together")
+    with _Launch(dev, stream) as on:
+        R, Hq, Hkv, D, qs, qos, ks, vs, q_out, spec = _append_args(
+            q, k, v, positions, slots, table, layout, rot_offset, q_out, on, stream)
+        _tensor(k_cache, k.dtype, "k_cache", (None, Hkv, D), dev)
+        if v_cache is not None:
+            _tensor(v_cache, k.dtype, "v_cache", (k_cache.shape[0], Hkv, D), dev)
+        if R == 0:
+            return q_out
+        st = load_library().qsa_rope_append(
+            _ptr(q), _ptr(q_out), k.data_ptr(), _ptr(v), k_cache.data_ptr(), _ptr(v_cache),
+            _ptr(positions), slots.data_ptr(), spec, R, k_cache.shape[0], Hq, Hkv, D, qs, qos, ks, vs,
+            code, on.ptr)
+    _check(st, "qsa_rope_append")
+    return q_out
+
+
+def rope_append_fp4(q, k, v, k_cache, k_scale, v_cache, v_scale, positions, slots,
+                    table: Optional[RopeTable], *, k_global: float = 1.0, v_global: float = 1.0,
+                    layout: str = "half", rot_offset: int = 0, q_out=None, k_seen=None, v_seen=None,
+                    stream=None):
+    """rope_append into a cache held in 4 bits (qsa_rope_append_fp4): k_cache, v_cache [n_slots, Hkv,
+    D / 2] uint8 e2m1 pairs, k_scale, v_scale [n_slots, Hkv, D / 16] uint8 e4m3 block scales, k_global,
+    v_global the caches' fp32 scales.  k_seen, v_seen [R, Hkv, D] (optional) receive the values that the
+    cache now holds.  Returns q_out."""
+    import torch
+    dev, code = k.device, _dtype_code(k.dtype, "k")
+    with _Launch(dev, stream) as on:
+        R, Hq, Hkv, D, qs, qos, ks, vs, q_out, spec = _append_args(
+            q, k, v, positions, slots, table, layout, rot_offset, q_out, on, stream)
+        S = k_cache.shape[0]
+        for t, name, w in ((k_cache, "k_cache", D // 2), (v_cache, "v_cache", D // 2),
+                           (k_scale, "k_scale", D // 16), (v_scale, "v_scale", D // 16)):
+            _tensor(t, torch.uint8, name, (S, Hkv, w), dev)
+        for t, name in ((k_seen, "k_seen"), (v_seen, "v_seen")):
+            if t is not None:
+                _tensor(t, k.dtype, name, (R, Hkv, D), dev)
+        if R == 0:
+            return q_out
+        st = load_library().qsa_rope_append_fp4(
+            _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+            k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(), float(k_global),
+            float(v_global), _ptr(k_seen), _ptr(v_seen), _ptr(positions), slots.data_ptr(), spec, R, S,
+            Hq, Hkv, D, qs, qos, ks, vs, code, on.ptr)
+    _check(st, "qsa_rope_append_fp4")
+    return q_out

@@ -18,16 +18,9 @@ std::atomic<uint64_t> g_calls_per_token{0}, g_calls_union{0}, g_union_fallbacks{
     g_step_downs{0}, g_launches{0};
 std::atomic<int> g_stall_next{0};   // armed by qsa_debug_stall_next_call
 
-constexpr size_t kWsAlign = 256;
+}  // namespace
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
-
-int pow2_at_least(int v) {
-  int p = 32;
-  while (p < v) p <<= 1;
-  return p;
-}
+namespace qsa {
 
 // Per-call union workspaces come from a library-owned stream-ordered memory pool per device
 // whose release threshold is unbounded: a freed workspace stays in the pool for the next call
@@ -55,6 +48,72 @@ cudaError_t ws_alloc(void** ptr, size_t bytes, cudaStream_t stream) {
   });
   return have[dev] ? cudaMallocFromPoolAsync(ptr, bytes, pools[dev], stream)
                    : cudaMallocAsync(ptr, bytes, stream);
+}
+
+// QSA_LOG=1: one stderr line per attention call with the geometry the selector chose.
+bool log_geometry() {
+  static const bool on = [] {
+    const char* e = std::getenv("QSA_LOG");
+    return e != nullptr && std::strcmp(e, "1") == 0;
+  }();
+  return on;
+}
+
+// Device checks: compute capability 10.3 and the SM count (cached per device).
+qsa_status device_sms(int32_t* sms) {
+  static std::atomic<int32_t> cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return QSA_ERR_CUDA;
+  if (dev >= 0 && dev < 64) {
+    const int32_t c = cache[dev].load();
+    if (c > 0) {
+      *sms = c;
+      return QSA_OK;
+    }
+  }
+  int major = 0, minor = 0, n = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return QSA_ERR_CUDA;
+  if (major != 10 || minor != 3) return QSA_ERR_UNSUPPORTED;
+  if (dev >= 0 && dev < 64) cache[dev].store(n);
+  *sms = n;
+  return QSA_OK;
+}
+
+cudaError_t smem_opt_in(const void* kernel, int bytes, int which) {
+  static std::atomic<bool> done[64][kOptCount];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < 64;
+  if (known && done[dev][which].load()) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) done[dev][which].store(true);
+  return e;
+}
+
+void count_launches(uint64_t n) { g_launches.fetch_add(n); }
+bool take_stall_request() { return g_stall_next.exchange(0) != 0; }
+
+}  // namespace qsa
+
+namespace {
+
+using qsa::device_sms;
+using qsa::log_geometry;
+using qsa::ws_alloc;
+
+constexpr size_t kWsAlign = 256;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+int pow2_at_least(int v) {
+  int p = 32;
+  while (p < v) p <<= 1;
+  return p;
 }
 
 struct WsLayout {
@@ -272,38 +331,6 @@ bool gather_engine_is_tma() {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// QSA_LOG=1: one stderr line per attention call with the geometry the selector chose.
-bool log_geometry() {
-  static const bool on = [] {
-    const char* e = std::getenv("QSA_LOG");
-    return e != nullptr && std::strcmp(e, "1") == 0;
-  }();
-  return on;
-}
-
-// Device checks: compute capability 10.3 and the SM count (cached per device).
-qsa_status device_sms(int32_t* sms) {
-  static std::atomic<int32_t> cache[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return QSA_ERR_CUDA;
-  if (dev >= 0 && dev < 64) {
-    const int32_t c = cache[dev].load();
-    if (c > 0) {
-      *sms = c;
-      return QSA_OK;
-    }
-  }
-  int major = 0, minor = 0, n = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return QSA_ERR_CUDA;
-  if (major != 10 || minor != 3) return QSA_ERR_UNSUPPORTED;
-  if (dev >= 0 && dev < 64) cache[dev].store(n);
-  *sms = n;
-  return QSA_OK;
-}
 
 // FP8 caches: e4m3 bytes with per-page, per-KV-head fp32 scales.
 struct Fp8Cache {

@@ -267,6 +267,71 @@ cudaError_t launch_page_split(const void* src, void* dst, const uint8_t* mark, i
                               int32_t src_page_size, int32_t dst_page_size,
                               const PageSections& sec, cudaStream_t stream);
 
+// ---------------------------------------------------------------------------- serving step
+// Page tables and slot maps built from request lengths (plan.cu).
+constexpr int kPlanMaxRequests = 16384;      // prefix sums in one CTA's shared memory
+struct PagePlanParams {
+  const int32_t* past_lens;     // [n_requests]
+  const int32_t* new_lens;      // [n_requests]
+  int32_t* page_table;          // [n_requests, pages_per_req], in and out
+  const int32_t* free_pages;    // [n_free]
+  const int32_t* free_head;     // [1]
+  int32_t* free_head_out;       // [1], may be free_head
+  int32_t* cu_seqlens_q;        // [n_requests + 1]
+  int32_t* kv_lens;             // [n_requests]
+  int32_t* positions;           // [max_rows], nullable
+  int32_t* slots;               // [max_rows], nullable
+  int32_t* shortfall;           // [1], nullable
+  int64_t n_free, n_pages, max_rows;
+  int32_t n_requests, pages_per_req, page_size;
+  int32_t page_shift;           // log2(page_size) when a power of two, else -1
+  int32_t vec_rows;             // positions and slots are 16-byte aligned
+  int32_t cluster;              // CTAs (one cluster)
+};
+int page_plan_smem_bytes(int32_t n_requests);
+cudaError_t launch_page_plan(PagePlanParams p, cudaStream_t stream);
+
+// Rotary positions and cache writes (rope.cu).  A null q or n_qheads = 0 leaves the queries out,
+// n_kvheads = 0 the cache.
+constexpr int kRopeMaxPairs = 256;
+struct RopeParams {
+  const void* q;                // [n_rows, n_qheads, head_dim], rows q_stride elements apart
+  void* q_out;
+  const void* k;
+  const void* v;
+  void* k_cache;                // [n_slots, n_kvheads, head_dim], or e2m1 codes in pairs
+  void* v_cache;
+  uint8_t* k_scale;             // 4-bit caches: e4m3 block scales [n_slots, n_kvheads, head_dim / 16]
+  uint8_t* v_scale;
+  void* k_seen;                 // 4-bit caches, nullable: the values the codes stand for
+  void* v_seen;
+  const int32_t* positions;     // [n_rows], nullable when rot_dim = 0
+  const int32_t* slots;         // [n_rows]
+  int64_t n_rows, n_slots;
+  int64_t q_stride, q_out_stride, k_stride, v_stride;   // elements
+  int32_t n_qheads, n_kvheads, head_dim;
+  int32_t n_vheads;             // n_kvheads, or 0 when the cache has no V (latent rows)
+  int32_t rot_dim, rot_offset, interleaved;
+  int32_t heads_per_share;
+  float magnitude, sin_sign;    // factor on the cosines, and on the sines (negative: transpose)
+  float k_global, v_global;
+  uint64_t steps[kRopeMaxPairs];   // 2^64 turns per token of each pair
+};
+bool rope_is_aligned(const RopeParams& p);
+cudaError_t launch_rope(RopeParams p, bool fp16, bool fp4, int num_sms, cudaStream_t stream);
+
+// Dynamic shared-memory opt-in of a kernel to `bytes`, its largest use, once per device and kernel (so
+// calls made during a graph capture only enqueue).
+enum OptInKernel { kOptPlan, kOptCount };
+cudaError_t smem_opt_in(const void* kernel, int bytes, int which);
+
+// Host helpers of api.cpp for the other units' entry points.
+qsa_status device_sms(int32_t* sms);
+cudaError_t ws_alloc(void** ptr, size_t bytes, cudaStream_t stream);
+void count_launches(uint64_t n);
+bool take_stall_request();      // failure-detection hook: armed by qsa_debug_stall_next_call
+bool log_geometry();            // QSA_LOG=1
+
 // Device address of the attention kernels' status word (prefill.cu), for kernels in other units.
 cudaError_t device_status_address(int32_t** addr);
 

@@ -1,0 +1,377 @@
+// Rotary positions, and the write of new K/V rows into the cache, as they are or in 4 bits.
+//
+// Pair (a, b) of a head at position x turns by the angle x * theta_i: a' = m (a cos - b sin),
+// b' = m (b cos + a sin).  The pairs are dims (i, i + rot/2) in the half layout and (2i, 2i + 1) in the
+// interleaved one.  theta_i comes as a step: the fraction of a full turn per token, as a 64-bit
+// fixed-point number.  x * step modulo 2^64 is then the angle's fraction of a turn, exact to 2^-33
+// turns at any 31-bit position, from one integer product (theta_i * x in fp32 is off by 2^-24 of the
+// whole angle, 0.06 rad at a million).  Its upper half, as a signed number of half turns, goes to
+// sincospi.
+//
+// The operator reads and writes every element once and does a handful of operations on each, so it is
+// bound by memory.  A thread owns one 16-dim unit (8 pairs) of a row: it computes its 8 sines and
+// cosines once and applies them to that unit of every head of its share, with 16-byte loads and
+// stores.  Calls with few rows give each thread fewer heads, so that enough threads run.
+//
+// 4-bit rows: a block of 16 dims is stored as 16 e2m1 codes (two in a byte, the even dim in the low
+// half) and one e4m3 scale s = e4m3(max|x| / (6 g)), g being the cache's fp32 scale; a code is
+// e2m1((x / g) / s), both rounded to nearest, ties to even.  The rotated values are quantised from fp32.
+// Quotients are true divisions, so that values on the border between two codes fall as the formula says.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "internal.h"
+
+namespace qsa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+__device__ __forceinline__ float2 unpack2(uint32_t v, __nv_bfloat16) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t v, __half) {
+  __half2 h;
+  memcpy(&h, &v, 4);
+  return __half22float2(h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  uint32_t r;
+  memcpy(&r, &h, 4);
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  uint32_t r;
+  memcpy(&r, &h, 4);
+  return r;
+}
+// Plain loads and stores: q may be rotated in place.
+template <typename T>
+__device__ __forceinline__ uint4 load_raw(const void* base, int64_t elem) {
+  return *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + elem);
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 t = unpack2(w[k], T{});
+    f[2 * k] = t.x;
+    f[2 * k + 1] = t.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(void* base, int64_t elem, const float* f) {
+  *reinterpret_cast<uint4*>(static_cast<T*>(base) + elem) =
+      make_uint4(pack2(f[0], f[1], T{}), pack2(f[2], f[3], T{}), pack2(f[4], f[5], T{}),
+                 pack2(f[6], f[7], T{}));
+}
+
+// Sine and cosine of the angle at position `pos`, times the magnitude.
+__device__ __forceinline__ void angle_of(const RopeParams& p, int i, int32_t pos, float& c, float& s) {
+  const uint64_t turn = static_cast<uint64_t>(static_cast<uint32_t>(pos)) * p.steps[i];
+  const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+  sincospif(half_turns, &s, &c);
+  c *= p.magnitude;
+  s *= p.sin_sign;   // the magnitude, negative for the transpose
+}
+
+// Two e2m1 codes of a pair of values (b in the upper half of the byte).
+__device__ __forceinline__ uint32_t e2m1x2(float a, float b) {
+  uint16_t r;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.u16.u8 %0, t;\n\t}"
+      : "=h"(r)
+      : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint8_t e4m3_of(float a) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(a));
+  return static_cast<uint8_t>(r);
+}
+__device__ __forceinline__ float e4m3_value(uint8_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(c)));
+  __half2 h;
+  memcpy(&h, &r, 4);
+  return __low2float(h);
+}
+__device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(r) : "r"(byte));
+  __half2 h;
+  memcpy(&h, &r, 4);
+  return __half22float2(h);
+}
+
+__device__ __forceinline__ float amax8(const float* f) {
+  float m = fabsf(f[0]);
+#pragma unroll
+  for (int k = 1; k < 8; ++k) m = fmaxf(m, fabsf(f[k]));
+  return m;
+}
+
+// Eight dims of a block with scale s (a float that is an e4m3 value): four code bytes; f becomes the
+// values that the codes stand for.
+__device__ __forceinline__ uint32_t quantise8(float* f, float s, float g) {
+  uint32_t w = 0;
+  const float sg = s * g;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = s > 0.0f ? __fdiv_rn(__fdiv_rn(f[2 * k], g), s) : 0.0f;
+    const float b = s > 0.0f ? __fdiv_rn(__fdiv_rn(f[2 * k + 1], g), s) : 0.0f;
+    const uint32_t byte = e2m1x2(a, b);
+    const float2 v = e2m1x2_values(byte);
+    f[2 * k] = v.x * sg;
+    f[2 * k + 1] = v.y * sg;
+    w |= byte << (8 * k);
+  }
+  return w;
+}
+
+// The two 8-dim halves of a K or V unit (dims da.. and db..) into the 4-bit cache row `cell`; ma and mb
+// are the largest magnitudes of the 16-dim blocks that the halves lie in.
+template <typename T>
+__device__ __forceinline__ void write_fp4(const RopeParams& p, bool is_v, int64_t row, int32_t kvh,
+                                          int64_t cell, int da, int db, float ma, float mb, float* f) {
+  const float g = is_v ? p.v_global : p.k_global;
+  const uint8_t ca = e4m3_of(__fdiv_rn(__fdiv_rn(ma, g), 6.0f));
+  const uint8_t cb = e4m3_of(__fdiv_rn(__fdiv_rn(mb, g), 6.0f));
+  const uint32_t wa = quantise8(f, e4m3_value(ca), g);
+  const uint32_t wb = quantise8(f + 8, e4m3_value(cb), g);
+  uint8_t* const codes = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + cell * (p.head_dim / 2);
+  uint8_t* const scales = (is_v ? p.v_scale : p.k_scale) + cell * (p.head_dim / 16);
+  *reinterpret_cast<uint32_t*>(codes + da / 2) = wa;
+  *reinterpret_cast<uint32_t*>(codes + db / 2) = wb;
+  // one lane writes each block's scale: the one that holds the block's first dim
+  if ((da & 15) == 0) scales[da / 16] = ca;
+  if ((db & 15) == 0) scales[db / 16] = cb;
+  void* const seen = is_v ? p.v_seen : p.k_seen;
+  if (seen) {
+    const int64_t at = (row * p.n_kvheads + kvh) * p.head_dim;
+    store8<T>(seen, at + da, f);
+    store8<T>(seen, at + db, f + 8);
+  }
+}
+
+// Aligned rows: thread = (row, 16-dim unit); blockIdx.y is a share of the heads (q, then k, then v).
+// Units 0 .. rot/16 - 1 of a q or k head hold the rotated pairs, the others the dims that pass
+// through; V units are plain 16-dim groups.
+template <typename T, bool FP4, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int kBatch = 4;   // heads loaded before the first is stored
+  const int units = p.head_dim >> 4, rot_units = p.rot_dim >> 4;
+  const int64_t total = p.n_rows * units;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRopeThreads;
+  const int h0 = blockIdx.y * p.heads_per_share;
+  const int h1 = min(h0 + p.heads_per_share, p.n_qheads + p.n_kvheads + p.n_vheads);
+  const int q1 = min(h1, p.n_qheads);
+  // whole warps stay in the loop (the 4-bit half layout exchanges maxima between lanes)
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRopeThreads + (threadIdx.x & ~31); t0 < total;
+       t0 += stride) {
+    const int64_t t = t0 + (threadIdx.x & 31);
+    const bool here = t < total;
+    const int64_t row = (here ? t : total - 1) / units;
+    const int u = static_cast<int>((here ? t : total - 1) - row * units);
+    const int32_t pos = p.positions ? __ldg(p.positions + row) : 0;
+    const bool live = here && pos >= 0;
+
+    const bool turns = u < rot_units;
+    int da, db;
+    if (turns) {
+      da = p.rot_offset + (INTERLEAVED ? 16 * u : 8 * u);
+      db = INTERLEAVED ? da + 8 : da + p.rot_dim / 2;
+    } else {
+      const int d = 16 * (u - rot_units);
+      da = d < p.rot_offset ? d : d + p.rot_dim;
+      db = da + 8;
+    }
+    float cs[8], sn[8];
+    if (turns && live && h0 < p.n_qheads + p.n_kvheads) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) angle_of(p, 8 * u + k, pos, cs[k], sn[k]);
+    }
+    auto rotate = [&](float* f) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int ia = INTERLEAVED ? 2 * k : k, ib = INTERLEAVED ? 2 * k + 1 : k + 8;
+        const float a = f[ia], b = f[ib];
+        f[ia] = a * cs[k] - b * sn[k];
+        f[ib] = b * cs[k] + a * sn[k];
+      }
+    };
+    if (live) {
+      for (int h = h0; h < q1; h += kBatch) {
+        const int64_t at = row * p.q_stride + static_cast<int64_t>(h) * p.head_dim;
+        const int64_t to = row * p.q_out_stride + static_cast<int64_t>(h) * p.head_dim;
+        uint4 ra[kBatch], rb[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          if (h + k < q1) {
+            ra[k] = load_raw<T>(p.q, at + k * p.head_dim + da);
+            rb[k] = load_raw<T>(p.q, at + k * p.head_dim + db);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          if (h + k < q1) {
+            float f[16];
+            unpack8<T>(ra[k], f);
+            unpack8<T>(rb[k], f + 8);
+            if (turns) rotate(f);
+            store8<T>(p.q_out, to + k * p.head_dim + da, f);
+            store8<T>(p.q_out, to + k * p.head_dim + db, f + 8);
+          }
+        }
+      }
+    }
+    if (h1 <= p.n_qheads) continue;
+    const int32_t slot = __ldg(p.slots + row);
+    const bool stored = live && slot >= 0 && slot < p.n_slots;
+    for (int h = max(h0, p.n_qheads); h < h1; ++h) {
+      const bool is_v = h >= p.n_qheads + p.n_kvheads;
+      const int kvh = is_v ? h - p.n_qheads - p.n_kvheads : h - p.n_qheads;
+      const int ea = is_v ? 16 * u : da, eb = is_v ? 16 * u + 8 : db;
+      const int64_t cell = static_cast<int64_t>(slot) * p.n_kvheads + kvh;
+      float f[16];
+      if (stored) {
+        const int64_t at = row * (is_v ? p.v_stride : p.k_stride) + static_cast<int64_t>(kvh) * p.head_dim;
+        const void* const src = is_v ? p.v : p.k;
+        const uint4 ra = load_raw<T>(src, at + ea), rb = load_raw<T>(src, at + eb);
+        unpack8<T>(ra, f);
+        unpack8<T>(rb, f + 8);
+        if (turns && !is_v) rotate(f);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) f[k] = 0.0f;
+      }
+      if constexpr (FP4) {
+        float ma = amax8(f), mb = amax8(f + 8);
+        if constexpr (!INTERLEAVED) {
+          // a rotated half shares its block with the neighbouring unit's
+          const float na = __shfl_xor_sync(0xffffffffu, ma, 1), nb = __shfl_xor_sync(0xffffffffu, mb, 1);
+          const bool split = turns && !is_v;
+          const float whole = fmaxf(ma, mb);
+          ma = split ? fmaxf(ma, na) : whole;
+          mb = split ? fmaxf(mb, nb) : whole;
+        } else {
+          ma = mb = fmaxf(ma, mb);
+        }
+        if (stored) write_fp4<T>(p, is_v, row, kvh, cell, ea, eb, ma, mb, f);
+      } else if (stored) {
+        void* const cache = is_v ? p.v_cache : p.k_cache;
+        store8<T>(cache, cell * p.head_dim + ea, f);
+        store8<T>(cache, cell * p.head_dim + eb, f + 8);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ void from_float(float f, __nv_bfloat16& v) { v = __float2bfloat16_rn(f); }
+__device__ __forceinline__ void from_float(float f, __half& v) { v = __float2half_rn(f); }
+
+// Rows of any width, offset, stride and alignment: thread = (row, head, pair or passing dim).
+template <typename T>
+__global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const __grid_constant__ RopeParams p) {
+  const int pairs = p.rot_dim >> 1, per_head = p.head_dim - pairs;
+  const int heads = p.n_qheads + p.n_kvheads + p.n_vheads;
+  const int64_t total = p.n_rows * heads * per_head;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRopeThreads;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x; t < total; t += stride) {
+    const int e = static_cast<int>(t % per_head);
+    const int64_t rh = t / per_head;
+    const int h = static_cast<int>(rh % heads);
+    const int64_t row = rh / heads;
+    const int32_t pos = p.positions ? __ldg(p.positions + row) : 0;
+    if (pos < 0) continue;
+    const T* src;
+    T* dst;
+    const bool is_v = h >= p.n_qheads + p.n_kvheads;
+    if (h < p.n_qheads) {
+      src = static_cast<const T*>(p.q) + row * p.q_stride + static_cast<int64_t>(h) * p.head_dim;
+      dst = static_cast<T*>(p.q_out) + row * p.q_out_stride + static_cast<int64_t>(h) * p.head_dim;
+    } else {
+      const int32_t slot = __ldg(p.slots + row);
+      if (slot < 0 || slot >= p.n_slots) continue;
+      const int kvh = is_v ? h - p.n_qheads - p.n_kvheads : h - p.n_qheads;
+      src = static_cast<const T*>(is_v ? p.v : p.k) + row * (is_v ? p.v_stride : p.k_stride) +
+            static_cast<int64_t>(kvh) * p.head_dim;
+      dst = static_cast<T*>(is_v ? p.v_cache : p.k_cache) +
+            (static_cast<int64_t>(slot) * p.n_kvheads + kvh) * p.head_dim;
+    }
+    if (e >= pairs || is_v) {
+      // passing dims: everything but the rotated range, or for V all of it (the first `pairs`
+      // threads of a V head take two dims)
+      if (is_v) {
+        dst[e] = src[e];
+        if (e < pairs) dst[per_head + e] = src[per_head + e];
+      } else {
+        const int d = e - pairs, at = d < p.rot_offset ? d : d + p.rot_dim;
+        dst[at] = src[at];
+      }
+      continue;
+    }
+    const int ia = p.rot_offset + (p.interleaved ? 2 * e : e), ib = p.interleaved ? ia + 1 : ia + pairs;
+    float c, s;
+    angle_of(p, e, pos, c, s);
+    const float a = to_float(src[ia]), b = to_float(src[ib]);
+    from_float(a * c - b * s, dst[ia]);
+    from_float(b * c + a * s, dst[ib]);
+  }
+}
+
+template <typename T>
+cudaError_t launch_rows(const RopeParams& p, bool fp4, dim3 grid, cudaStream_t stream) {
+  if (fp4) {
+    if (p.interleaved) rope_rows_kernel<T, true, true><<<grid, kRopeThreads, 0, stream>>>(p);
+    else rope_rows_kernel<T, true, false><<<grid, kRopeThreads, 0, stream>>>(p);
+  } else {
+    if (p.interleaved) rope_rows_kernel<T, false, true><<<grid, kRopeThreads, 0, stream>>>(p);
+    else rope_rows_kernel<T, false, false><<<grid, kRopeThreads, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+
+// Whether the 16-byte kernel serves the call: every unit starts on a 16-byte boundary.
+bool rope_is_aligned(const RopeParams& p) {
+  return p.head_dim % 16 == 0 && p.rot_dim % 16 == 0 && p.rot_offset % 16 == 0 && p.q_stride % 8 == 0 &&
+         p.q_out_stride % 8 == 0 && p.k_stride % 8 == 0 && p.v_stride % 8 == 0 && aligned(p.q, 16) &&
+         aligned(p.q_out, 16) && aligned(p.k, 16) && aligned(p.v, 16) && aligned(p.k_cache, 16) &&
+         aligned(p.v_cache, 16) && aligned(p.k_seen, 16) && aligned(p.v_seen, 16);
+}
+
+cudaError_t launch_rope(RopeParams p, bool fp16, bool fp4, int num_sms, cudaStream_t stream) {
+  const int heads = p.n_qheads + p.n_kvheads + p.n_vheads;
+  if (!fp4 && !rope_is_aligned(p)) {
+    const int64_t total = p.n_rows * heads * (p.head_dim - p.rot_dim / 2);
+    const int64_t want = (total + kRopeThreads - 1) / kRopeThreads, cap = static_cast<int64_t>(num_sms) * 32;
+    const unsigned grid = static_cast<unsigned>(want < cap ? want : cap);
+    if (fp16) rope_any_kernel<__half><<<grid, kRopeThreads, 0, stream>>>(p);
+    else rope_any_kernel<__nv_bfloat16><<<grid, kRopeThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
+  // Shares of the heads: as few as still give every SM about 1024 threads, since each share computes
+  // a row's angles again.
+  const int64_t threads = p.n_rows * (p.head_dim / 16);
+  int64_t shares = (static_cast<int64_t>(num_sms) * 1024 + threads - 1) / threads;
+  if (shares > heads) shares = heads;
+  p.heads_per_share = static_cast<int32_t>((heads + shares - 1) / shares);
+  shares = (heads + p.heads_per_share - 1) / p.heads_per_share;
+  const int64_t blocks = (threads + kRopeThreads - 1) / kRopeThreads;
+  const int64_t cap = static_cast<int64_t>(num_sms) * 64;
+  const dim3 grid(static_cast<unsigned>(blocks < cap ? blocks : cap), static_cast<unsigned>(shares));
+  return fp16 ? launch_rows<__half>(p, fp4, grid, stream) : launch_rows<__nv_bfloat16>(p, fp4, grid, stream);
+}
+
+}  // namespace qsa

@@ -1,0 +1,270 @@
+// C-ABI entry points of the serving-step operators: page plans and rotary positions with the cache
+// writes.  Every argument error is caught here, before any CUDA call.
+#include <cmath>
+#include <cstring>
+
+#include "internal.h"
+
+namespace {
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int32_t shift_of(int32_t v) {
+  for (int32_t s = 0; s < 31; ++s)
+    if ((int32_t{1} << s) == v) return s;
+  return -1;
+}
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr int32_t kMaxHeads = 32768;      // query and KV heads each (blockIdx.y holds a head share)
+constexpr int32_t kMaxHeadDim = 16384;
+
+// The rotation's own arguments (rope may be null where nothing turns).
+qsa_status rope_args(const qsa_rope_spec* rope, int32_t head_dim, qsa::RopeParams* p) {
+  p->magnitude = 1.0f;
+  p->sin_sign = 1.0f;
+  if (!rope) return QSA_OK;
+  if (rope->rot_dim < 0 || rope->rot_dim % 2 != 0 || rope->rot_offset < 0 ||
+      static_cast<int64_t>(rope->rot_dim) + rope->rot_offset > head_dim ||
+      (rope->layout != QSA_ROPE_HALF && rope->layout != QSA_ROPE_INTERLEAVED) ||
+      (rope->transpose != 0 && rope->transpose != 1) || !std::isfinite(rope->magnitude))
+    return QSA_ERR_INVALID_ARG;
+  if (rope->rot_dim > 0 && !rope->steps) return QSA_ERR_INVALID_ARG;
+  if (rope->rot_dim / 2 > qsa::kRopeMaxPairs) return QSA_ERR_UNSUPPORTED;
+  p->rot_dim = rope->rot_dim;
+  p->rot_offset = rope->rot_dim > 0 ? rope->rot_offset : 0;
+  p->interleaved = rope->layout == QSA_ROPE_INTERLEAVED;
+  p->magnitude = rope->magnitude;
+  p->sin_sign = rope->transpose ? -rope->magnitude : rope->magnitude;
+  if (rope->rot_dim > 0) std::memcpy(p->steps, rope->steps, sizeof(uint64_t) * (rope->rot_dim / 2));
+  return QSA_OK;
+}
+
+qsa_status run_rope(qsa::RopeParams& p, const qsa_rope_spec* rope, int32_t dtype, bool fp4, void* stream) {
+  if (p.n_rows < 0 || p.n_qheads < 0 || p.n_kvheads < 0 || p.head_dim < 1 ||
+      (dtype != QSA_BF16 && dtype != QSA_FP16))
+    return QSA_ERR_INVALID_ARG;
+  if (p.n_qheads + static_cast<int64_t>(p.n_kvheads) < 1) return QSA_ERR_INVALID_ARG;
+  if (p.n_qheads > kMaxHeads / 2 || p.n_kvheads > kMaxHeads / 4 || p.head_dim > kMaxHeadDim ||
+      p.n_rows > INT32_MAX)
+    return QSA_ERR_UNSUPPORTED;
+  const int64_t q_width = static_cast<int64_t>(p.n_qheads) * p.head_dim;
+  const int64_t kv_width = static_cast<int64_t>(p.n_kvheads) * p.head_dim;
+  if (p.n_qheads > 0) {
+    if (!p.q || !p.q_out || p.q_stride < 0 || p.q_out_stride < q_width) return QSA_ERR_INVALID_ARG;
+    if (p.q == p.q_out && p.q_stride != p.q_out_stride) return QSA_ERR_INVALID_ARG;
+    if (!aligned_to(p.q, 2) || !aligned_to(p.q_out, 2)) return QSA_ERR_INVALID_ARG;
+  }
+  if (p.n_kvheads > 0) {
+    if (!p.k || !p.k_cache || !p.slots || p.k_stride < 0 || p.n_slots < 0) return QSA_ERR_INVALID_ARG;
+    if ((p.v == nullptr) != (p.v_cache == nullptr) || (p.v && p.v_stride < 0)) return QSA_ERR_INVALID_ARG;
+    if (!aligned_to(p.k, 2) || !aligned_to(p.v, 2)) return QSA_ERR_INVALID_ARG;
+    if (!fp4 && (!aligned_to(p.k_cache, 2) || !aligned_to(p.v_cache, 2))) return QSA_ERR_INVALID_ARG;
+    (void)kv_width;
+  }
+  p.n_vheads = p.v ? p.n_kvheads : 0;
+  const qsa_status st = rope_args(rope, p.head_dim, &p);
+  if (st != QSA_OK) return st;
+  if (p.rot_dim > 0 && !p.positions) return QSA_ERR_INVALID_ARG;
+  if (fp4) {
+    // 16-dim blocks of aligned rows; rotated halves have to fill whole blocks
+    if (p.head_dim % 32 != 0 || p.rot_offset % 16 != 0 || p.rot_dim % (p.interleaved ? 16 : 32) != 0)
+      return QSA_ERR_UNSUPPORTED;
+    if (!p.interleaved && p.rot_dim == 0) p.interleaved = 1;   // nothing turns: whole blocks per thread
+    if (!qsa::rope_is_aligned(p)) return QSA_ERR_INVALID_ARG;
+  }
+  if (p.n_rows == 0) return QSA_OK;
+  int32_t sms = 0;
+  const qsa_status ds = qsa::device_sms(&sms);
+  if (ds != QSA_OK) return ds;
+  if (qsa::launch_rope(p, dtype == QSA_FP16, fp4, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return QSA_ERR_CUDA;
+  qsa::count_launches(1);
+  return QSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+qsa_status qsa_page_plan(const int32_t* past_lens, const int32_t* new_lens, int32_t* page_table,
+                         const int32_t* free_pages, int64_t n_free, const int32_t* free_head,
+                         int32_t* free_head_out, int32_t* cu_seqlens_q, int32_t* kv_lens,
+                         int32_t* positions, int32_t* slots, int32_t* shortfall, int32_t n_requests,
+                         int32_t pages_per_req, int32_t page_size, int64_t n_pages, int64_t max_rows,
+                         void* stream) {
+  if (!past_lens || !new_lens || !page_table || !free_head || !free_head_out || !cu_seqlens_q || !kv_lens ||
+      (n_free > 0 && !free_pages))
+    return QSA_ERR_INVALID_ARG;
+  if (n_requests < 1 || pages_per_req < 1 || page_size < 1 || n_pages < 0 || n_free < 0 || max_rows < 0)
+    return QSA_ERR_INVALID_ARG;
+  for (const void* a : {static_cast<const void*>(past_lens), static_cast<const void*>(new_lens),
+                        static_cast<const void*>(page_table), static_cast<const void*>(free_pages),
+                        static_cast<const void*>(free_head), static_cast<const void*>(free_head_out),
+                        static_cast<const void*>(cu_seqlens_q), static_cast<const void*>(kv_lens),
+                        static_cast<const void*>(positions), static_cast<const void*>(slots),
+                        static_cast<const void*>(shortfall)})
+    if (!aligned_to(a, 4)) return QSA_ERR_INVALID_ARG;
+  if (n_requests > qsa::kPlanMaxRequests || max_rows > INT32_MAX || n_free > INT32_MAX)
+    return QSA_ERR_UNSUPPORTED;
+  int32_t sms = 0;
+  const qsa_status st = qsa::device_sms(&sms);
+  if (st != QSA_OK) return st;
+  qsa::PagePlanParams p{};
+  p.past_lens = past_lens;
+  p.new_lens = new_lens;
+  p.page_table = page_table;
+  p.free_pages = free_pages;
+  p.free_head = free_head;
+  p.free_head_out = free_head_out;
+  p.cu_seqlens_q = cu_seqlens_q;
+  p.kv_lens = kv_lens;
+  p.positions = positions;
+  p.slots = slots;
+  p.shortfall = shortfall;
+  p.n_free = n_free;
+  p.n_pages = n_pages;
+  p.max_rows = max_rows;
+  p.n_requests = n_requests;
+  p.pages_per_req = pages_per_req;
+  p.page_size = page_size;
+  p.page_shift = shift_of(page_size);
+  p.vec_rows = aligned_to(positions, 16) && aligned_to(slots, 16);
+  if (qsa::launch_page_plan(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return QSA_ERR_CUDA;
+  qsa::count_launches(1);
+  return QSA_OK;
+}
+
+qsa_status qsa_rope_steps(const qsa_rope_scaling* scaling, int32_t rot_dim, double base, uint64_t* steps,
+                          float* magnitude) {
+  if (!steps || !magnitude || rot_dim < 2 || rot_dim % 2 != 0 || !std::isfinite(base) || base <= 0.0)
+    return QSA_ERR_INVALID_ARG;
+  if (rot_dim / 2 > qsa::kRopeMaxPairs) return QSA_ERR_UNSUPPORTED;
+  const qsa_rope_scaling none{QSA_ROPE_SCALE_NONE, 1.0, 0.0, 0.0, 0.0};
+  const qsa_rope_scaling& s = scaling ? *scaling : none;
+  const double f = s.kind == QSA_ROPE_SCALE_NONE ? 1.0 : s.factor;
+  if (!std::isfinite(f) || f <= 0.0) return QSA_ERR_INVALID_ARG;
+  const bool ramp = s.kind == QSA_ROPE_SCALE_YARN || s.kind == QSA_ROPE_SCALE_TURNS;
+  if (ramp && (!(s.original_len > 0.0) || !std::isfinite(s.original_len) || !(s.beta_slow > 0.0) ||
+               !(s.beta_fast > s.beta_slow) || !std::isfinite(s.beta_fast)))
+    return QSA_ERR_INVALID_ARG;
+  double low = 0.0, high = 0.0, b = base;
+  switch (s.kind) {
+    case QSA_ROPE_SCALE_NONE:
+    case QSA_ROPE_SCALE_LINEAR:
+    case QSA_ROPE_SCALE_TURNS: break;
+    case QSA_ROPE_SCALE_NTK:
+      if (rot_dim < 4) return QSA_ERR_INVALID_ARG;
+      b = base * std::pow(f, static_cast<double>(rot_dim) / (rot_dim - 2));
+      if (!std::isfinite(b)) return QSA_ERR_INVALID_ARG;
+      break;
+    case QSA_ROPE_SCALE_YARN: {
+      if (base <= 1.0) return QSA_ERR_INVALID_ARG;
+      // the pair that makes t turns over the original length
+      auto pair_at = [&](double t) {
+        return rot_dim * std::log(s.original_len / (kTwoPi * t)) / (2.0 * std::log(base));
+      };
+      low = std::fmax(std::floor(pair_at(s.beta_fast)), 0.0);
+      high = std::fmin(std::ceil(pair_at(s.beta_slow)), rot_dim - 1.0);
+      break;
+    }
+    default: return QSA_ERR_INVALID_ARG;
+  }
+  for (int32_t i = 0; i < rot_dim / 2; ++i) {
+    double w = std::pow(b, -2.0 * i / rot_dim);      // radians per token
+    double keep = 1.0;                               // share of the unscaled frequency
+    if (s.kind == QSA_ROPE_SCALE_LINEAR) keep = 0.0;
+    if (s.kind == QSA_ROPE_SCALE_YARN)
+      keep = 1.0 - std::fmin(std::fmax((i - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
+    if (s.kind == QSA_ROPE_SCALE_TURNS)
+      keep = std::fmin(std::fmax((s.original_len * w / kTwoPi - s.beta_slow) / (s.beta_fast - s.beta_slow),
+                                 0.0), 1.0);
+    w = keep * w + (1.0 - keep) * w / f;
+    const double turns = w / kTwoPi;
+    steps[i] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));
+  }
+  *magnitude = s.kind == QSA_ROPE_SCALE_YARN && f > 1.0 ? static_cast<float>(0.1 * std::log(f) + 1.0) : 1.0f;
+  return QSA_OK;
+}
+
+qsa_status qsa_rope(const void* x, void* out, const int32_t* positions, const qsa_rope_spec* rope,
+                    int64_t n_rows, int32_t n_heads, int32_t head_dim, int64_t x_stride,
+                    int64_t out_stride, int32_t dtype, void* stream) {
+  if (!rope || !positions) return QSA_ERR_INVALID_ARG;
+  qsa::RopeParams p{};
+  p.q = x;
+  p.q_out = out;
+  p.positions = positions;
+  p.n_rows = n_rows;
+  p.n_qheads = n_heads;
+  p.head_dim = head_dim;
+  p.q_stride = x_stride;
+  p.q_out_stride = out_stride;
+  return run_rope(p, rope, dtype, false, stream);
+}
+
+qsa_status qsa_rope_append(const void* q, void* q_out, const void* k, const void* v, void* k_cache,
+                           void* v_cache, const int32_t* positions, const int32_t* slots,
+                           const qsa_rope_spec* rope, int64_t n_rows, int64_t n_slots, int32_t n_qheads,
+                           int32_t n_kvheads, int32_t head_dim, int64_t q_stride, int64_t q_out_stride,
+                           int64_t k_stride, int64_t v_stride, int32_t dtype, void* stream) {
+  if (n_kvheads < 1) return QSA_ERR_INVALID_ARG;
+  qsa::RopeParams p{};
+  p.q = q;
+  p.q_out = q_out;
+  p.k = k;
+  p.v = v;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.positions = positions;
+  p.slots = slots;
+  p.n_rows = n_rows;
+  p.n_slots = n_slots;
+  p.n_qheads = n_qheads;
+  p.n_kvheads = n_kvheads;
+  p.head_dim = head_dim;
+  p.q_stride = q_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  return run_rope(p, rope, dtype, false, stream);
+}
+
+qsa_status qsa_rope_append_fp4(const void* q, void* q_out, const void* k, const void* v, void* k_cache,
+                               uint8_t* k_scale, void* v_cache, uint8_t* v_scale, float k_global,
+                               float v_global, void* k_seen, void* v_seen, const int32_t* positions,
+                               const int32_t* slots, const qsa_rope_spec* rope, int64_t n_rows,
+                               int64_t n_slots, int32_t n_qheads, int32_t n_kvheads, int32_t head_dim,
+                               int64_t q_stride, int64_t q_out_stride, int64_t k_stride,
+                               int64_t v_stride, int32_t dtype, void* stream) {
+  if (n_kvheads < 1 || !v || !k_scale || !v_scale) return QSA_ERR_INVALID_ARG;
+  if (!(k_global > 0.0f) || !(v_global > 0.0f) || !std::isfinite(k_global) || !std::isfinite(v_global))
+    return QSA_ERR_INVALID_ARG;
+  qsa::RopeParams p{};
+  p.q = q;
+  p.q_out = q_out;
+  p.k = k;
+  p.v = v;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.k_seen = k_seen;
+  p.v_seen = v_seen;
+  p.k_global = k_global;
+  p.v_global = v_global;
+  p.positions = positions;
+  p.slots = slots;
+  p.n_rows = n_rows;
+  p.n_slots = n_slots;
+  p.n_qheads = n_qheads;
+  p.n_kvheads = n_kvheads;
+  p.head_dim = head_dim;
+  p.q_stride = q_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  return run_rope(p, rope, dtype, true, stream);
+}
+
+}  // extern "C"
