@@ -390,6 +390,59 @@ qsa_status qsa_rope_append_fp4(const void* q, void* q_out, const void* k, const 
                                int64_t q_stride, int64_t q_out_stride, int64_t k_stride,
                                int64_t v_stride, int32_t dtype, void* stream);
 
+/* Attention with a sliding window and a few first tokens that stay visible (sinks), over a paged cache:
+ * prompt rows, prompt chunks and decode rows of one ragged batch in one call.  The rows of request i are
+ * the last ones of its kv_lens[i] tokens: row r stands at position
+ *   p = kv_lens[i] - (cu_seqlens_q[i + 1] - cu_seqlens_q[i]) + (r - cu_seqlens_q[i])
+ * and sees the positions j <= p that have j > p - window (window = 0: all of them) or j < n_sink.  The
+ * step's own K/V rows are in the cache before the call (qsa_rope_append writes them).
+ *   q   [n_rows, n_qheads, head_dim], out likewise, of type dtype (qsa_dtype); lse [n_rows, n_qheads]
+ *       fp32, nullable: the natural logarithm of sum exp(scale q.k) over the seen keys
+ *   k_cache, v_cache [n_pages * page_size, n_kvheads, head_dim] of type dtype
+ *   cu_seqlens_q, kv_lens, page_table as in qsa_sparse_prefill_paged, kv_lens not nullable; n_pages >= 1 is
+ *       the size of the caches.  A position past pages_per_req pages, or on a page < 0 or >= n_pages, is not
+ *       seen.  Any page size; multiples of 8 are read in larger pieces.
+ * A row that sees nothing (kv_len < rows puts first rows at negative positions) gets out = 0 and lse = -inf.
+ * Rows behind cu_seqlens_q[n_requests] (a padded batch) are left as they were.
+ * What the cache holds at positions that no row sees (the rest of a page, tokens that left the window)
+ * does not matter, NaN and infinities included.  A non-finite value that a row sees makes that row's
+ * output non-finite, and may do so to the rows of up to 127 neighbouring (token, head) pairs of the same request and
+ * KV head.
+ *   scale > 0.  head_dim 64, 128 or 256; n_qheads / n_kvheads <= 128.
+ *   workspace: calls with few rows split the keys over the SMs and join the parts; they need
+ *       qsa_window_workspace_bytes (for the device's SM count; 0 = no split), 256-byte aligned.  NULL: taken from
+ *       the library's pool on `stream`.  Calls that overlap need a workspace each.
+ * Sums, maxima and outputs are held in fp32, the weights of the P.V product are rounded to 16 bits.
+ * Results do not depend on timing, but a row's depend on the split, and so on the batch it is in.
+ * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED (other head dims, caches of 2^31 rows and more),
+ * QSA_ERR_WORKSPACE; a wait inside the kernel that runs out is reported by qsa_get_device_status. */
+qsa_status qsa_window_attention_paged(const void* q, const void* k_cache, const void* v_cache,
+                                      const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                                      const int32_t* page_table, void* out, float* lse, int64_t n_rows,
+                                      int32_t n_requests, int32_t pages_per_req, int32_t page_size,
+                                      int64_t n_pages, int32_t n_qheads, int32_t n_kvheads,
+                                      int32_t head_dim, float scale, int32_t window, int32_t n_sink,
+                                      int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same over a cache held in 4 bits, as qsa_rope_append_fp4 writes it: k_cache, v_cache [n_pages *
+ * page_size, n_kvheads, head_dim / 2] bytes, k_scale, v_scale [n_pages * page_size, n_kvheads, head_dim / 16] e4m3
+ * bytes (16-byte aligned, like the caches).  The values enter the products exactly, in fp16; q is rounded
+ * to fp16 (|q| must stay below 65504), the weights are rounded to fp16. */
+qsa_status qsa_window_attention_fp4_paged(const void* q, const void* k_cache, const uint8_t* k_scale,
+                                          const void* v_cache, const uint8_t* v_scale, float k_global,
+                                          float v_global, const int32_t* cu_seqlens_q,
+                                          const int32_t* kv_lens, const int32_t* page_table, void* out,
+                                          float* lse, int64_t n_rows, int32_t n_requests,
+                                          int32_t pages_per_req, int32_t page_size, int64_t n_pages,
+                                          int32_t n_qheads, int32_t n_kvheads, int32_t head_dim,
+                                          float scale, int32_t window, int32_t n_sink, int32_t dtype,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Host only: bytes of workspace of a window-attention call (num_sms <= 0 asks the current device). */
+size_t qsa_window_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t pages_per_req,
+                                  int32_t page_size, int32_t n_qheads, int32_t n_kvheads,
+                                  int32_t head_dim, int32_t window, int32_t n_sink, int32_t num_sms);
+
 /* Allocation-free variant of qsa_sparse_prefill (same arguments, same results).  The pages
  * have no counterpart: it exists for callers that must not allocate device memory -- code
  * whose GPU memory is owned entirely by a framework's pool, latency-critical loops where an

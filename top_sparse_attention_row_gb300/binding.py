@@ -29,7 +29,8 @@ EXPORTED = ["qsa_sparse_prefill", "qsa_sparse_prefill_ex", "qsa_union_workspace_
             "qsa_page_mark", "qsa_page_split", "qsa_split_touched_pages",
             "qsa_sparse_prefill_fp8", "qsa_debug_stall_next_call", "qsa_sparse_mla_prefill_paged",
             "qsa_sparse_prefill_fp8_paged",
-            "qsa_page_plan", "qsa_rope_steps", "qsa_rope", "qsa_rope_append", "qsa_rope_append_fp4"]
+            "qsa_page_plan", "qsa_rope_steps", "qsa_rope", "qsa_rope_append", "qsa_rope_append_fp4",
+            "qsa_window_attention_paged", "qsa_window_attention_fp4_paged", "qsa_window_workspace_bytes"]
 
 # Size of the library-owned scratch array used by qsa_sparse_prefill_noalloc (include/qsa.h).
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -130,6 +131,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qsa_rope_append_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, f32, f32, vp, vp, vp, vp, vp, i64,
                                         i64, i32, i32, i32, i64, i64, i64, i64, i32, vp]
     lib.qsa_rope_append_fp4.restype = ctypes.c_int
+    shape = [i64, i32, i32, i32, i64, i32, i32, i32, f32, i32, i32, i32, vp, sz, vp]
+    lib.qsa_window_attention_paged.argtypes = [vp] * 8 + shape
+    lib.qsa_window_attention_paged.restype = ctypes.c_int
+    lib.qsa_window_attention_fp4_paged.argtypes = [vp] * 5 + [f32, f32] + [vp] * 5 + shape
+    lib.qsa_window_attention_fp4_paged.restype = ctypes.c_int
+    lib.qsa_window_workspace_bytes.argtypes = [i64] + [i32] * 9
+    lib.qsa_window_workspace_bytes.restype = sz
     for name in ("qsa_union_workspace_bytes", "qsa_workspace_bytes"):
         getattr(lib, name).argtypes = [i64, i32, i32]
         getattr(lib, name).restype = sz
@@ -857,3 +865,103 @@ def rope_append_fp4(q, k, v, k_cache, k_scale, v_cache, v_scale, positions, slot
             Hq, Hkv, D, qs, qos, ks, vs, code, on.ptr)
     _check(st, "qsa_rope_append_fp4")
     return q_out
+
+
+def _window_args(q, caches, k_rows, cu_seqlens_q, kv_lens, page_table, page_size, window, n_sink, out, lse,
+                 want_lse, workspace, on, stream):
+    import torch
+    R, Hq, D = q.shape
+    dev, Hkv = q.device, k_rows.shape[1]
+    _tensor(q, q.dtype, "q", (R, Hq, D), dev)
+    n = page_table.shape[0]
+    _tensor(page_table, torch.int32, "page_table", (n, None), dev)
+    _tensor(cu_seqlens_q, torch.int32, "cu_seqlens_q", (n + 1,), dev)
+    _tensor(kv_lens, torch.int32, "kv_lens", (n,), dev)
+    S = k_rows.shape[0]
+    for t, dtype, name, w in caches:
+        _tensor(t, dtype, name, (S, Hkv, w), dev)
+    page_size = int(page_size)
+    if page_size < 1 or S % page_size:
+        raise ValueError(f"the caches' {S} slots are not whole pages of {page_size}")
+    made = []
+    if out is None:
+        out = torch.empty_like(q)
+        made.append(out)
+    else:
+        _tensor(out, q.dtype, "out", (R, Hq, D), dev)
+    if lse is None:
+        if want_lse:
+            lse = torch.empty((R, Hq), dtype=torch.float32, device=dev)
+            made.append(lse)
+    else:
+        _tensor(lse, torch.float32, "lse", (R, Hq), dev)
+    ws_bytes = 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {dev}")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    elif R:
+        ws_bytes = load_library().qsa_window_workspace_bytes(R, n, page_table.shape[1], page_size, Hq,
+                                                             Hkv, D, int(window), int(n_sink), 0)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+            made.append(workspace)
+    if stream is not None:
+        for t in made:
+            on.own(t)
+    shape = (R, n, page_table.shape[1], page_size, S // page_size, Hq, Hkv, D)
+    return out, lse, workspace, ws_bytes, shape
+
+
+def window_attention_paged(q, k_cache, v_cache, cu_seqlens_q, kv_lens, page_table, page_size: int,
+                           scale: float, *, window: int = 0, n_sink: int = 0, out=None, lse=None,
+                           want_lse: bool = True, workspace=None, stream=None):
+    """Sliding-window attention with sink tokens over a paged cache (qsa_window_attention_paged).
+
+    q [R, Hq, D] bf16 or fp16 (D 64, 128 or 256); k_cache, v_cache [n_pages * page_size, Hkv, D] of the
+    same type; cu_seqlens_q [n_requests + 1], kv_lens [n_requests], page_table [n_requests,
+    pages_per_req] int32.  A row at position p sees the positions up to p that are among the last
+    `window` (0 = all) or the first n_sink.  Rows behind the last request are left as they were (in an
+    `out` that is not given: uninitialised).  Returns out [R, Hq, D] and lse [R, Hq] fp32 (None unless
+    wanted)."""
+    code = _dtype_code(q.dtype, "q")
+    with _Launch(q.device, stream) as on:
+        D = q.shape[-1]
+        out, lse, ws, ws_bytes, shape = _window_args(
+            q, ((k_cache, q.dtype, "k_cache", D), (v_cache, q.dtype, "v_cache", D)), k_cache, cu_seqlens_q,
+            kv_lens, page_table, page_size, window, n_sink, out, lse, want_lse, workspace, on, stream)
+        if shape[0] == 0:
+            return out, lse
+        st = load_library().qsa_window_attention_paged(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cu_seqlens_q.data_ptr(),
+            kv_lens.data_ptr(), page_table.data_ptr(), out.data_ptr(), _ptr(lse), *shape, float(scale),
+            int(window), int(n_sink), code, _ptr(ws), ws_bytes, on.ptr)
+    _check(st, "qsa_window_attention_paged")
+    return out, lse
+
+
+def window_attention_fp4_paged(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, kv_lens, page_table,
+                               page_size: int, scale: float, *, k_global: float = 1.0,
+                               v_global: float = 1.0, window: int = 0, n_sink: int = 0, out=None,
+                               lse=None, want_lse: bool = True, workspace=None, stream=None):
+    """window_attention_paged over a cache held in 4 bits, as rope_append_fp4 writes it
+    (qsa_window_attention_fp4_paged): k_cache, v_cache [n_pages * page_size, Hkv, D / 2] uint8, k_scale,
+    v_scale [n_pages * page_size, Hkv, D / 16] uint8, k_global, v_global the caches' fp32 scales."""
+    import torch
+    code = _dtype_code(q.dtype, "q")
+    with _Launch(q.device, stream) as on:
+        D = q.shape[-1]
+        u8 = torch.uint8
+        out, lse, ws, ws_bytes, shape = _window_args(
+            q, ((k_cache, u8, "k_cache", D // 2), (v_cache, u8, "v_cache", D // 2),
+                (k_scale, u8, "k_scale", D // 16), (v_scale, u8, "v_scale", D // 16)), k_cache, cu_seqlens_q,
+            kv_lens, page_table, page_size, window, n_sink, out, lse, want_lse, workspace, on, stream)
+        if shape[0] == 0:
+            return out, lse
+        st = load_library().qsa_window_attention_fp4_paged(
+            q.data_ptr(), k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(),
+            float(k_global), float(v_global), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
+            page_table.data_ptr(), out.data_ptr(), _ptr(lse), *shape, float(scale), int(window), int(n_sink),
+            code, _ptr(ws), ws_bytes, on.ptr)
+    _check(st, "qsa_window_attention_fp4_paged")
+    return out, lse

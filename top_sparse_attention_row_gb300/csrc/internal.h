@@ -320,9 +320,40 @@ struct RopeParams {
 bool rope_is_aligned(const RopeParams& p);
 cudaError_t launch_rope(RopeParams p, bool fp16, bool fp4, int num_sms, cudaStream_t stream);
 
+// Sliding-window attention over a paged cache (window.cuh).
+constexpr int kWinTile = 128;                // keys per MMA tile, and rows of the query tile
+struct WindowParams {
+  const void* q;                // [n_rows, n_qheads, D] bf16 or fp16
+  void* out;
+  float* lse;                   // nullable
+  float* part_o;                // splits > 1: [n_rows, n_qheads, splits, D] normalised partial outputs
+  float* part_lse;              // [n_rows, n_qheads, splits] their log-sum-exps
+  int32_t* status;              // device status word (0x100 | wait site on a timeout)
+  const uint8_t* k_codes;       // 4-bit caches: e2m1 pairs [slots, n_kvheads, D / 2]
+  const uint8_t* v_codes;
+  const uint8_t* k_scale;       // e4m3 block scales [slots, n_kvheads, D / 16]
+  const uint8_t* v_scale;
+  PagedAddr pa;                 // kv_lens is required, n_pages > 0
+  int64_t n_rows;
+  int64_t n_units;              // tiles x KV heads x splits
+  int32_t n_qheads, n_kvheads, group;
+  int32_t tile_tokens;          // tokens of a query tile: 128 / group, at least 1
+  int32_t n_tiles;              // upper bound: n_rows / tile_tokens + n_requests
+  int32_t splits;
+  int32_t window;               // 0 = none
+  int32_t n_sink;
+  int32_t box;                  // keys per TMA box (8 .. 64), or 0: gathers of four rows
+  int32_t n_slots;              // n_pages * page_size
+  int32_t stall_first_item;     // failure-detection test: the scheduler withholds its records
+  float scale_log2;             // scale * log2(e) (times the K cache's scale)
+  float v_mult;                 // V cache's scale
+};
+cudaError_t launch_window(const WindowParams& p, int head_dim, bool fp16, bool fp4, const void* k_cache,
+                          const void* v_cache, int num_sms, cudaStream_t stream);
+
 // Dynamic shared-memory opt-in of a kernel to `bytes`, its largest use, once per device and kernel (so
 // calls made during a graph capture only enqueue).
-enum OptInKernel { kOptPlan, kOptCount };
+enum OptInKernel { kOptPlan, kOptWindow, kOptCount = kOptWindow + 12 };
 cudaError_t smem_opt_in(const void* kernel, int bytes, int which);
 
 // Host helpers of api.cpp for the other units' entry points.

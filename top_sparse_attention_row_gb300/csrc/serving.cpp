@@ -1,6 +1,8 @@
 // C-ABI entry points of the serving-step operators: page plans and rotary positions with the cache
 // writes.  Every argument error is caught here, before any CUDA call.
+#include <climits>
 #include <cmath>
+#include <cstdio>
 #include <cstring>
 
 #include "internal.h"
@@ -83,9 +85,208 @@ qsa_status run_rope(qsa::RopeParams& p, const qsa_rope_spec* rope, int32_t dtype
   return QSA_OK;
 }
 
+// Splits of the key axis.  A unit's time is its key tiles; a split one also writes, and the join reads,
+// its partial rows in fp32 (two tiles' worth of bytes when all 128 rows are in use, in proportion
+// otherwise), and the join is one more launch, about three tiles long.  The count with the shortest
+// last-finishing SM wins, the smaller one where two tie.
+struct WindowPlan {
+  int32_t tile_tokens, n_tiles, splits;
+  int64_t n_units;
+};
+constexpr int32_t kMaxSplits = 128;
+WindowPlan plan_window(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, int32_t group,
+                       int64_t max_keys, int32_t window, int32_t n_sink, int32_t sms) {
+  WindowPlan w{};
+  w.tile_tokens = qsa::kWinTile / group;
+  w.n_tiles = static_cast<int32_t>(n_rows / w.tile_tokens + n_requests);
+  // units with rows: every request has at most one partial tile
+  int64_t tiles = (n_rows + w.tile_tokens - 1) / w.tile_tokens + n_requests - 1;
+  if (tiles > n_rows) tiles = n_rows;
+  int64_t keys = max_keys;
+  if (window > 0) {
+    const int64_t seen = static_cast<int64_t>(window) + w.tile_tokens + n_sink + 64;
+    if (seen < keys) keys = seen;
+  }
+  const int64_t kt = (keys + qsa::kWinTile - 1) / qsa::kWinTile;
+  const int64_t items = tiles * n_kvheads;
+  const int64_t rows_per = n_rows < tiles * w.tile_tokens ? (n_rows + tiles - 1) / tiles : w.tile_tokens;
+  const double partial = 2.0 * static_cast<double>(rows_per * group) / qsa::kWinTile;
+  double best = 0.0;
+  w.splits = 1;
+  for (int64_t s = 1; s <= kt && s <= kMaxSplits; ++s) {
+    const int64_t waves = (items * s + sms - 1) / sms;
+    const double cost = waves * ((kt + s - 1) / s + (s > 1 ? partial : 0.0)) + (s > 1 ? 3.0 : 0.0);
+    if (s == 1 || cost < best) {
+      best = cost;
+      w.splits = static_cast<int32_t>(s);
+    }
+  }
+  w.n_units = static_cast<int64_t>(w.n_tiles) * n_kvheads * w.splits;
+  return w;
+}
+
+// Partial outputs and log-sum-exps of a split call.
+size_t window_ws_bytes(int64_t n_rows, int32_t n_qheads, int32_t head_dim, int32_t splits) {
+  if (splits <= 1) return 0;
+  const size_t n = static_cast<size_t>(n_rows) * n_qheads * splits;
+  return n * head_dim * 4 + (n * 4 + 255) / 256 * 256;
+}
+
+struct Fp4Cache {
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+  float k_global, v_global;
+};
+
+qsa_status check_window(int64_t n_rows, int32_t n_requests, int32_t pages_per_req, int32_t page_size,
+                        int64_t n_pages, int32_t n_qheads, int32_t n_kvheads, int32_t head_dim,
+                        int32_t window, int32_t n_sink) {
+  if (n_rows < 0 || n_requests < 1 || pages_per_req < 1 || page_size < 1 || n_pages < 1 || n_qheads < 1 ||
+      n_kvheads < 1 || n_qheads % n_kvheads != 0 || window < 0 || n_sink < 0)
+    return QSA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return QSA_ERR_UNSUPPORTED;
+  if (n_qheads / n_kvheads > qsa::kWinTile) return QSA_ERR_UNSUPPORTED;
+  if (n_rows + n_requests >= INT32_MAX) return QSA_ERR_UNSUPPORTED;
+  if (n_pages > INT32_MAX / page_size || n_pages * page_size > (INT32_MAX - 1) / n_kvheads)
+    return QSA_ERR_UNSUPPORTED;
+  return QSA_OK;
+}
+
+qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, const Fp4Cache* fp4,
+                      const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* page_table,
+                      void* out, float* lse, int64_t n_rows, int32_t n_requests, int32_t pages_per_req,
+                      int32_t page_size, int64_t n_pages, int32_t n_qheads, int32_t n_kvheads,
+                      int32_t head_dim, float scale, int32_t window, int32_t n_sink, int32_t dtype,
+                      void* workspace, size_t workspace_bytes, void* stream_v) {
+  if (!q || !k_cache || !v_cache || !cu_seqlens_q || !kv_lens || !page_table || !out) return QSA_ERR_INVALID_ARG;
+  if (!aligned_to(q, 16) || !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !aligned_to(out, 16) ||
+      !aligned_to(cu_seqlens_q, 4) || !aligned_to(kv_lens, 4) || !aligned_to(page_table, 4) ||
+      !aligned_to(lse, 4))
+    return QSA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.0f) || (dtype != QSA_BF16 && dtype != QSA_FP16))
+    return QSA_ERR_INVALID_ARG;
+  qsa_status st = check_window(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads,
+                               head_dim, window, n_sink);
+  if (st != QSA_OK) return st;
+  if (n_rows == 0) return QSA_OK;
+  int32_t sms = 0;
+  st = qsa::device_sms(&sms);
+  if (st != QSA_OK) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+  const int32_t group = n_qheads / n_kvheads;
+  const WindowPlan w = plan_window(n_rows, n_requests, n_kvheads, group,
+                                   static_cast<int64_t>(pages_per_req) * page_size, window, n_sink, sms);
+  qsa::WindowParams p{};
+  p.q = q;
+  p.out = out;
+  p.lse = lse;
+  if (qsa::device_status_address(&p.status) != cudaSuccess) return QSA_ERR_CUDA;
+  p.pa.page_table = page_table;
+  p.pa.cu_seqlens_q = cu_seqlens_q;
+  p.pa.kv_lens = kv_lens;
+  p.pa.n_requests = n_requests;
+  p.pa.pages_per_req = pages_per_req;
+  p.pa.page_size = page_size;
+  p.pa.page_shift = shift_of(page_size);
+  p.pa.n_pages = n_pages;
+  p.n_rows = n_rows;
+  p.n_units = w.n_units;
+  p.n_qheads = n_qheads;
+  p.n_kvheads = n_kvheads;
+  p.group = group;
+  p.tile_tokens = w.tile_tokens;
+  p.n_tiles = w.n_tiles;
+  p.splits = w.splits;
+  p.window = window;
+  p.n_sink = n_sink;
+  int32_t box = 1;      // keys per copy: the largest power of two <= 64 that divides the page size
+  while (box < 64 && page_size % (2 * box) == 0) box *= 2;
+  p.box = box >= 8 ? box : 0;
+  p.n_slots = static_cast<int32_t>(n_pages * page_size);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.v_mult = 1.0f;
+  if (fp4) {
+    p.k_codes = static_cast<const uint8_t*>(k_cache);
+    p.v_codes = static_cast<const uint8_t*>(v_cache);
+    p.k_scale = fp4->k_scale;
+    p.v_scale = fp4->v_scale;
+    p.scale_log2 *= fp4->k_global;
+    p.v_mult = fp4->v_global;
+    if (!(p.scale_log2 > 0.0f) || !std::isfinite(p.scale_log2)) return QSA_ERR_INVALID_ARG;
+  }
+  if (qsa::log_geometry())
+    std::fprintf(stderr,
+                 "qsa: window d=%d rows=%lld requests=%d heads=%d/%d window=%d sinks=%d%s -> tile_tokens=%d "
+                 "box=%d splits=%d units=%lld\n",
+                 head_dim, static_cast<long long>(n_rows), n_requests, n_qheads, n_kvheads, window, n_sink,
+                 fp4 ? " fp4" : "", p.tile_tokens, p.box, p.splits, static_cast<long long>(p.n_units));
+  void* ws = workspace;
+  bool own = false;
+  const size_t need = window_ws_bytes(n_rows, n_qheads, head_dim, p.splits);
+  if (need > 0) {
+    if (ws) {
+      if (workspace_bytes < need || !aligned_to(ws, 256)) return QSA_ERR_WORKSPACE;
+    } else {
+      if (qsa::ws_alloc(&ws, need, stream) != cudaSuccess) return QSA_ERR_CUDA;
+      own = true;
+    }
+    p.part_o = static_cast<float*>(ws);
+    p.part_lse = p.part_o + static_cast<size_t>(n_rows) * n_qheads * p.splits * head_dim;
+  }
+  p.stall_first_item = qsa::take_stall_request() ? 1 : 0;
+  const cudaError_t e = qsa::launch_window(p, head_dim, dtype == QSA_FP16, fp4 != nullptr, k_cache, v_cache, sms,
+                                           stream);
+  if (own) cudaFreeAsync(ws, stream);
+  if (e != cudaSuccess) return QSA_ERR_CUDA;
+  qsa::count_launches(p.splits > 1 ? 2 : 1);
+  return QSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t qsa_window_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t pages_per_req,
+                                  int32_t page_size, int32_t n_qheads, int32_t n_kvheads,
+                                  int32_t head_dim, int32_t window, int32_t n_sink, int32_t num_sms) {
+  if (check_window(n_rows, n_requests, pages_per_req, page_size, 1, n_qheads, n_kvheads, head_dim, window,
+                   n_sink) != QSA_OK || n_rows == 0)
+    return 0;
+  if (num_sms <= 0 && qsa::device_sms(&num_sms) != QSA_OK) return 0;
+  const WindowPlan w = plan_window(n_rows, n_requests, n_kvheads, n_qheads / n_kvheads,
+                                   static_cast<int64_t>(pages_per_req) * page_size, window, n_sink, num_sms);
+  return window_ws_bytes(n_rows, n_qheads, head_dim, w.splits);
+}
+
+qsa_status qsa_window_attention_paged(const void* q, const void* k_cache, const void* v_cache,
+                                      const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                                      const int32_t* page_table, void* out, float* lse, int64_t n_rows,
+                                      int32_t n_requests, int32_t pages_per_req, int32_t page_size,
+                                      int64_t n_pages, int32_t n_qheads, int32_t n_kvheads,
+                                      int32_t head_dim, float scale, int32_t window, int32_t n_sink,
+                                      int32_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_window(q, k_cache, v_cache, nullptr, cu_seqlens_q, kv_lens, page_table, out, lse, n_rows, n_requests,
+                    pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim, scale, window, n_sink,
+                    dtype, workspace, workspace_bytes, stream);
+}
+
+qsa_status qsa_window_attention_fp4_paged(const void* q, const void* k_cache, const uint8_t* k_scale,
+                                          const void* v_cache, const uint8_t* v_scale, float k_global,
+                                          float v_global, const int32_t* cu_seqlens_q,
+                                          const int32_t* kv_lens, const int32_t* page_table, void* out,
+                                          float* lse, int64_t n_rows, int32_t n_requests,
+                                          int32_t pages_per_req, int32_t page_size, int64_t n_pages,
+                                          int32_t n_qheads, int32_t n_kvheads, int32_t head_dim,
+                                          float scale, int32_t window, int32_t n_sink, int32_t dtype,
+                                          void* workspace, size_t workspace_bytes, void* stream) {
+  if (!k_scale || !v_scale || !aligned_to(k_scale, 16) || !aligned_to(v_scale, 16)) return QSA_ERR_INVALID_ARG;
+  if (!(k_global > 0.0f) || !(v_global > 0.0f) || !std::isfinite(k_global) || !std::isfinite(v_global))
+    return QSA_ERR_INVALID_ARG;
+  const Fp4Cache f{k_scale, v_scale, k_global, v_global};
+  return run_window(q, k_cache, v_cache, &f, cu_seqlens_q, kv_lens, page_table, out, lse, n_rows, n_requests,
+                    pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim, scale, window, n_sink,
+                    dtype, workspace, workspace_bytes, stream);
+}
 
 qsa_status qsa_page_plan(const int32_t* past_lens, const int32_t* new_lens, int32_t* page_table,
                          const int32_t* free_pages, int64_t n_free, const int32_t* free_head,

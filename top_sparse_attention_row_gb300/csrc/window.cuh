@@ -1,0 +1,1079 @@
+// Attention with a sliding window and a few first tokens that stay visible, over a paged cache: prompt
+// rows, prompt chunks and decode rows of one ragged batch in one kernel.
+//
+// Row r of request i stands at position p = kv_len - new + (r - cu[i]) and sees the positions j <= p with
+// j > p - window (window 0: all of them) or j < n_sink:
+//   S = scale q.k_j,  m = max S,  O = sum_j exp(S_j - m) v_j / l,  l = sum_j exp(S_j - m),  lse = m + ln l.
+//
+//  * One work unit is a query tile of one request and KV head -- 128 rows, the `group` query heads of
+//    each of 128 / group consecutive tokens, so that every K and V row is read once for all of them --
+//    and, with splits, a contiguous range of its keys.  A persistent CTA per SM runs units round robin.
+//  * The keys a unit sees are the sinks and one range [lo, hi): both are laid side by side in a virtual
+//    index v (position v below S0, v + shift from S0 on), which is cut into tiles of 128 keys.  A
+//    window of 4096 costs 33 tiles whatever the context is; boxes that no row sees are not loaded.
+//  * S = Q.K^T (tcgen05, M = 128 rows, N = 128 keys, both operands in shared memory) goes to one of two
+//    tensor-memory buffers; the softmax overwrites it with P in 16 bits, which P.V takes as its A operand
+//    from tensor memory; O stays in tensor memory (D columns).  S of tile j + 1 is issued before
+//    P.V of tile j, so the tensor core works while the softmax does.
+//  * Softmax: two warpgroups, each thread one row and half of the tile's keys; the two halves of a row
+//    exchange their maxima through shared memory.  The running maximum is raised only when a tile
+//    exceeds it by 2^8, so that O is seldom rescaled; O and l share it, the result is exact.  S, m, l and
+//    O are fp32; P is rounded to 16 bits for the matrix product (half a step of a weight that is at most
+//    2^8), and l sums the unrounded weights.
+//  * K and V are staged as 128-byte-swizzled 64-dim blocks of 128 keys in a ring that the MMA consumes in
+//    the order K0 K1 V0 K2 V1 ...  Four producer warps issue TMA boxes of up to 64 keys (page sizes that
+//    are multiples of 8), or gathers of four rows for other page sizes.
+//  * 4-bit caches: eight warps bring the codes and scales with cp.async some entries ahead, each into
+//    its own staging area, and write them to the ring as fp16: e2m1 times an e4m3 scale has six
+//    significant bits, so that is exact; the caches' global scales multiply the logits and the output.
+//    The MMAs run fp16 there (q is rounded to fp16, as for FP8 caches).
+//  * Keys that no row of the unit sees (the rest of a page, positions that left the window, missing
+//    pages) get weight 0 and V rows of zeros, so that whatever the cache holds there stays out.
+//  * Every mbarrier wait is bounded (2 s); a timeout records a code in the device status word, all roles
+//    leave their loops, copies and MMAs in flight are drained, tensor memory is freed.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+#include <cstring>
+#include <type_traits>
+
+#include "internal.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace qsa {
+
+CUresult encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base,
+                           const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box);
+
+template <int D, bool FP4>
+struct WinCfg {
+  static constexpr int kStageDims = D < 128 ? D : 128;
+  static constexpr int kNBS = kStageDims / 64;             // 64-dim blocks of a stage
+  static constexpr int kSPT = D / kStageDims;              // stages of a K or V tile (one ring entry)
+  static constexpr int kStageBytes = kWinTile * kStageDims * 2;
+  static constexpr int kQBytes = kWinTile * D * 2;
+  static constexpr int kStages = FP4 ? (D == 256 ? 3 : D == 128 ? 4 : 6) : (D == 256 ? 5 : D == 128 ? 6 : 12);
+  static constexpr int kEntryBars = 16;                    // > entries in flight
+  static constexpr int kRecords = FP4 ? 8 : 4;
+  static constexpr int kBadSlots = FP4 ? 16 : 8;           // > tiles the producers may be ahead
+  static constexpr int kThreads = FP4 ? 640 : 512;
+  static constexpr int kProducers = FP4 ? 8 : 4;
+  static constexpr int kQWarps = FP4 ? 3 : 1;              // warps that write the query tile
+  static constexpr int kDepth = D == 256 ? 3 : D == 128 ? 6 : 8;   // 4-bit entries in flight per warp
+  static constexpr int kStaging = 16 * (D / 2 + D / 16);   // bytes of one entry's 16 keys
+  // offsets
+  static constexpr int kRing = kQBytes;
+  static constexpr int kStagingAt = kRing + kStages * kStageBytes;
+  static constexpr int kMaxAt = kStagingAt + (FP4 ? 8 * kDepth * kStaging : 0);   // [2][2][128] float
+  static constexpr int kBadAt = kMaxAt + 2048;             // [kBadSlots][8] uint32
+  static constexpr int kRecAt = kBadAt + kBadSlots * 32;   // [kRecords][16] int32
+  static constexpr int kBarAt = kRecAt + kRecords * 64;
+  // full[kStages], entry[16], sfull[2], pfull[2], pvdone[2], qfull, qempty, ofree, fin, recfull/empty
+  static constexpr int kBars = kStages + kEntryBars + 10 + 2 * kRecords;
+  static constexpr int kTmemSlot = kBarAt + 8 * kBars;
+  static constexpr int kSmem = kTmemSlot + 16;
+  static_assert(kSmem <= kSmemLimit, "shared memory");
+  static_assert(kStages / kSPT + 2 < kEntryBars, "entry barriers");
+};
+
+namespace window_detail {
+
+constexpr unsigned long long kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
+constexpr float kRaise = 8.0f;          // log2 units by which a tile may exceed the running maximum
+constexpr float kLn2f = 0.6931471805599453f;
+enum Site : int32_t {
+  kWRecEmpty = 0x41, kWRecFull, kWQEmpty, kWQFull, kWStageEmpty, kWStageFull, kWSFull, kWPFull, kWPvDone,
+  kWOFree, kWDrain
+};
+
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Bounded wait for phase `parity` of a barrier.  False on timeout or abort.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                         int32_t* status, int32_t site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = now_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (now_ns() - t0 > kWaitNs) {
+      *abort_flag = 1;
+      atomicCAS(status, 0, 0x100 | site);
+      return false;
+    }
+  }
+}
+// Bounded wait that ignores the abort flag (copies and MMAs in flight finish before memory is given up).
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, int32_t* status, unsigned long long ns) {
+  const unsigned long long t0 = now_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (now_ns() - t0 > ns) {
+      atomicCAS(status, 0, 0x100 | kWDrain);
+      return;
+    }
+  }
+}
+
+// A work unit, written by the scheduler warp and read by every role.
+struct Unit {
+  int32_t tiles;       // key tiles of this unit (0: nothing to see, < 0: no more units)
+  int32_t tile0;       // first of them
+  int32_t req, kvh, split;
+  int32_t row0, tokens;
+  int32_t p_first;     // position of the first token
+  int32_t s0, shift;   // virtual index v: position v below s0, v + shift from s0 on
+  int32_t lo, hi;      // positions some row sees: [lo, hi) and those below n_sink and hi
+  int32_t pad[4];
+};
+static_assert(sizeof(Unit) == 64, "unit record");
+
+__device__ __forceinline__ Unit load_unit(const Unit* u) {
+  Unit r;
+  const int4* s = reinterpret_cast<const int4*>(u);
+  int4 a = s[0], b = s[1], c = s[2];
+  r.tiles = a.x; r.tile0 = a.y; r.req = a.z; r.kvh = a.w;
+  r.split = b.x; r.row0 = b.y; r.tokens = b.z; r.p_first = b.w;
+  r.s0 = c.x; r.shift = c.y; r.lo = c.z; r.hi = c.w;
+  return r;
+}
+
+// Tiles before request i in the virtual tile numbering: cu / T + i leaves every request at least
+// ceil(rows / T) numbers (at most one of them empty), and is increasing, so the owner of a number is
+// found by search without any prefix sum of tile counts.
+__device__ __forceinline__ int32_t first_tile(const WindowParams& p, int32_t i) {
+  return __ldg(p.pa.cu_seqlens_q + i) / p.tile_tokens + i;
+}
+__device__ __forceinline__ int32_t tile_owner(const WindowParams& p, int32_t tile, int lane) {
+  int32_t lo = 0, hi = p.pa.n_requests - 1;
+  while (lo < hi) {
+    const int32_t step = (hi - lo + 32) / 32;
+    const int32_t cand = lo + lane * step;
+    const uint32_t m = __ballot_sync(0xffffffffu, cand <= hi && first_tile(p, cand) <= tile);
+    const int last = m ? 31 - __clz(m) : 0;
+    lo = lo + last * step;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
+// Unit `n` of the call, or tiles = -2 for a number without rows.  Warp-uniform; every lane takes part.
+__device__ __forceinline__ Unit make_unit(const WindowParams& p, int64_t n, int lane) {
+  Unit u{};
+  u.split = static_cast<int32_t>(n % p.splits);
+  const int64_t tk = n / p.splits;
+  u.kvh = static_cast<int32_t>(tk / p.n_tiles);
+  // a request's later tiles see more keys where there is no window: they go first
+  const int32_t tile = p.n_tiles - 1 - static_cast<int32_t>(tk - static_cast<int64_t>(u.kvh) * p.n_tiles);
+  u.req = tile_owner(p, tile, lane);
+  const int64_t r0 = __ldg(p.pa.cu_seqlens_q + u.req);
+  int64_t r1 = __ldg(p.pa.cu_seqlens_q + u.req + 1);
+  if (r1 > p.n_rows) r1 = p.n_rows;
+  const int64_t t0 = static_cast<int64_t>(tile - first_tile(p, u.req)) * p.tile_tokens;
+  if (r0 < 0 || t0 < 0 || r0 + t0 >= r1) {
+    u.tiles = -2;
+    return u;
+  }
+  const int64_t rows = r1 - r0;
+  u.row0 = static_cast<int32_t>(r0 + t0);
+  u.tokens = static_cast<int32_t>(rows - t0 < p.tile_tokens ? rows - t0 : p.tile_tokens);
+  const int64_t kv = __ldg(p.pa.kv_lens + u.req);
+  const int64_t p_first = kv - rows + t0;
+  u.p_first = static_cast<int32_t>(p_first);
+  const int64_t cap = static_cast<int64_t>(p.pa.pages_per_req) * p.pa.page_size;
+  int64_t hi = p_first + u.tokens;
+  if (hi > cap) hi = cap;
+  int64_t lo = p.window > 0 ? p_first - p.window + 1 : 0;
+  if (lo < 0) lo = 0;
+  if (lo > hi) lo = hi > 0 ? hi : 0;
+  const int64_t grain = p.box > 0 ? p.box : 4;
+  const int64_t lo_al = lo / grain * grain;
+  int64_t sinks = p.n_sink < lo ? p.n_sink : lo;
+  int64_t s0 = (sinks + grain - 1) / grain * grain, shift = lo_al - s0;
+  if (shift <= 0) {   // the sinks reach the window: one run from 0
+    s0 = 0;
+    shift = 0;
+  }
+  const int64_t keys = hi > 0 ? hi - shift : 0;   // virtual length
+  const int64_t all = (keys + kWinTile - 1) / kWinTile;
+  const int64_t a = all * u.split / p.splits, b = all * (u.split + 1) / p.splits;
+  u.tile0 = static_cast<int32_t>(a);
+  u.tiles = static_cast<int32_t>(b - a);
+  u.s0 = static_cast<int32_t>(s0);
+  u.shift = static_cast<int32_t>(shift);
+  u.lo = static_cast<int32_t>(lo);
+  u.hi = static_cast<int32_t>(hi > 0 ? hi : 0);
+  return u;
+}
+
+__device__ __forceinline__ int32_t position_of(const Unit& u, int32_t v) { return v >= u.s0 ? v + u.shift : v; }
+__device__ __forceinline__ bool seen(const WindowParams& p, const Unit& u, int32_t pos) {
+  return pos < u.hi && (pos >= u.lo || pos < p.n_sink);
+}
+
+// Ring entry e of a unit with nt tiles (K0 K1 V0 K2 V1 ... V(nt-1)): its tile, and whether it is V.
+__device__ __forceinline__ void entry_of(int e, int nt, int& tile, bool& is_v) {
+  if (e == 0) {
+    tile = 0;
+    is_v = false;
+  } else if (e == 2 * nt - 1) {
+    tile = nt - 1;
+    is_v = true;
+  } else {
+    is_v = (e & 1) == 0;
+    tile = is_v ? e / 2 - 1 : (e + 1) / 2;
+  }
+}
+
+__device__ __forceinline__ uint32_t pack16(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  uint32_t r;
+  memcpy(&r, &v, 4);
+  return r;
+}
+__device__ __forceinline__ uint32_t pack16(float a, float b, __half) {
+  const __half2 v = __floats2half2_rn(a, b);
+  uint32_t r;
+  memcpy(&r, &v, 4);
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_as_f16x2(uint32_t v) {
+  const __half2 h = __floats2half2_rn(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  uint32_t r;
+  memcpy(&r, &h, 4);
+  return r;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+template <int N>
+__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void* src, bool ok) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(ok ? N : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most `left` of this thread's copy groups are in flight.
+__device__ __forceinline__ void cp_async_wait(int left) {
+  switch (left) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+  }
+}
+// Two e2m1 codes (byte `k` of w) as fp16, times a pair of equal scales: exact.
+__device__ __forceinline__ uint32_t e2m1_scaled(uint32_t w, int k, __half2 s) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3, c;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
+      : "=r"(r)
+      : "r"(w >> (8 * k)));
+  __half2 h;
+  memcpy(&h, &r, 4);
+  h = __hmul2(h, s);
+  memcpy(&r, &h, 4);
+  return r;
+}
+
+}  // namespace window_detail
+
+template <int D, typename T, bool FP4>
+__global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
+    window_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                            const __grid_constant__ CUtensorMap tmQ1, const __grid_constant__ CUtensorMap tmQT,
+                            const __grid_constant__ WindowParams p) {
+  using namespace window_detail;
+  using C = WinCfg<D, FP4>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  const uint32_t b_full = base + C::kBarAt;
+  const uint32_t b_entry = b_full + 8 * C::kStages;
+  const uint32_t b_sfull = b_entry + 8 * C::kEntryBars;
+  const uint32_t b_pfull = b_sfull + 16;
+  const uint32_t b_pvdone = b_pfull + 16;
+  const uint32_t b_qfull = b_pvdone + 16;
+  const uint32_t b_qempty = b_qfull + 8;
+  const uint32_t b_ofree = b_qempty + 8;
+  const uint32_t b_fin = b_ofree + 8;
+  const uint32_t b_recfull = b_fin + 8;
+  const uint32_t b_recempty = b_recfull + 8 * C::kRecords;
+  float* const maxima = reinterpret_cast<float*>(smem + C::kMaxAt);
+  uint32_t* const bad_keys = reinterpret_cast<uint32_t*>(smem + C::kBadAt);
+  Unit* const recs = reinterpret_cast<Unit*>(smem + C::kRecAt);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kTmemSlot);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* const status = p.status;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if ((base & 1023u) != 0) {   // the swizzle needs 1024-byte aligned tiles; uniform over the grid
+    if (threadIdx.x == 0) atomicCAS(status, 0, 0x100 | kWDrain);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) mbar_init(b_full + 8 * s, C::kProducers);
+    for (int e = 0; e < C::kEntryBars; ++e) mbar_init(b_entry + 8 * e, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(b_sfull + 8 * b, 1);
+      mbar_init(b_pfull + 8 * b, 8);
+      mbar_init(b_pvdone + 8 * b, 1);     // two, by tile parity: S of tile j shows that P.V of j - 2 is done
+    }
+    mbar_init(b_qfull, C::kQWarps);
+    mbar_init(b_qempty, 1);
+    mbar_init(b_ofree, 8);
+    mbar_init(b_fin, 1);
+    for (int r = 0; r < C::kRecords; ++r) {
+      mbar_init(b_recfull + 8 * r, 1);
+      mbar_init(b_recempty + 8 * r, 8 + 1 + C::kProducers + (C::kQWarps - 1));
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (!FP4 && warp == 12 && lane == 0) {
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+    prefetch_tmap(&tmQ1);
+    prefetch_tmap(&tmQT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tm_o = tmem + 256;           // S buffers: columns 0-127 and 128-255; O: from 256
+
+  auto finish_role = [&]() {
+    tc_fence_before();
+    __syncthreads();
+  };
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax + epilogue
+    if constexpr (FP4) regs_inc<136>();
+    const int wg = warp >> 2, w = warp & 3, row = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+    const float sc = p.scale_log2;
+    const float raise = kRaise / sc;
+    uint32_t it = 0, js = 0, eb = 0;          // records, tiles and ring entries so far
+    bool bad = false;
+    for (;; ++it) {
+      const uint32_t rb = it % C::kRecords;
+      bad |= !wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, status, kWRecFull);
+      // the two warps that share 32 rows leave together or not at all
+      if (named_bar_any(1 + w, 64, bad || *abort_flag)) break;
+      const Unit u = load_unit(recs + rb);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_recempty + 8 * rb);
+      if (u.tiles < 0) break;
+      const int live_rows = u.tokens * p.group;
+      const bool warp_live = w * 32 < live_rows;
+      const int tok = row / p.group;
+      const int32_t pos = u.p_first + tok;    // of this thread's row
+      // positions this row sees: [row_lo, pos] and those below row_sink
+      int32_t row_lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+      int32_t row_sink = min(p.n_sink, pos + 1);
+      if (pos < 0) {
+        row_lo = INT32_MAX;
+        row_sink = 0;
+      }
+      const int32_t p_last = u.p_first + u.tokens - 1;
+      const int32_t lo_last = p.window > 0 && p_last >= p.window ? p_last - p.window + 1 : 0;
+      float m = -INFINITY, l = 0.0f;
+      bool left = false;                      // the pair of warps agreed to leave
+      for (int j = 0; j < u.tiles; ++j) {
+        const uint32_t jt = js + j, sb = jt & 1;
+        const uint32_t tm_s = tmem + lanes + sb * 128 + wg * 64;
+        const int32_t v0 = (u.tile0 + j) * kWinTile;
+        const int32_t first = position_of(u, v0), last = position_of(u, v0 + kWinTile - 1);
+        const bool one_run = v0 >= u.s0 || v0 + kWinTile <= u.s0;
+        // every key of the tile seen by some row; by every row
+        const bool whole = one_run && first >= u.lo && last < u.hi;
+        bad |= !wait_for(b_sfull + 8 * sb, (jt >> 1) & 1, abort_flag, status, kWSFull);
+        tc_fence_after();
+        const uint32_t* const holes = bad_keys + (jt % C::kBadSlots) * 8;
+        const uint4 h0 = *reinterpret_cast<const uint4*>(holes), h1 = *reinterpret_cast<const uint4*>(holes + 4);
+        const bool any_hole = (h0.x | h0.y | h0.z | h0.w | h1.x | h1.y | h1.z | h1.w) != 0;
+        if (warp_live) {
+          float s[64];
+          tmem_ld32(tm_s, s);
+          tmem_ld32(tm_s + 32, s + 32);
+          tc_wait_ld();
+          if (!(whole && first >= lo_last && last <= u.p_first)) {
+            const int32_t c0 = v0 + wg * 64;   // this thread's first key
+            // columns [c_lo, c_hi] of the window and those below c_sink
+            const int32_t c_lo = row_lo == INT32_MAX ? INT32_MAX : max(row_lo - u.shift, u.s0) - c0;
+            const int32_t c_hi = pos >= 0 ? min(pos, u.hi - 1) - u.shift - c0 : -1;
+            const int32_t c_sink = min(row_sink, u.hi) - c0;
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (!((c >= c_lo && c <= c_hi) || c < c_sink)) s[c] = -INFINITY;
+          }
+          if (any_hole) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+              const int key = wg * 64 + c;
+              int word, bit;
+              if constexpr (FP4) {
+                word = key >> 4;
+                bit = key & 15;
+              } else if (p.box > 0) {
+                const int o = key / p.box * C::kNBS;
+                word = (o & 3) * 2;
+                bit = o >> 2;
+              } else {
+                const int o = (key >> 2) * C::kNBS;
+                word = (o & 3) * 2 + ((key & 3) >> 1);
+                bit = (key & 1) * 16 + (o >> 2);
+              }
+              if ((holes[word] >> bit) & 1) s[c] = -INFINITY;
+            }
+          }
+          float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
+#pragma unroll
+          for (int c = 4; c < 64; c += 4) {
+            t0 = fmaxf(t0, s[c]);
+            t1 = fmaxf(t1, s[c + 1]);
+            t2 = fmaxf(t2, s[c + 2]);
+            t3 = fmaxf(t3, s[c + 3]);
+          }
+          float tile_max = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+          float* const mx = maxima + sb * 256;
+          mx[wg * 128 + row] = tile_max;
+          if (named_bar_any(1 + w, 64, bad)) {
+            left = true;
+            break;
+          }
+          tile_max = fmaxf(tile_max, mx[(wg ^ 1) * 128 + row]);
+          const bool need = tile_max > m + raise || (m == -INFINITY && tile_max > -INFINITY);
+          if (__any_sync(0xffffffffu, need)) {
+            const float nm = need ? tile_max : m;
+            const float f = m == -INFINITY ? 0.0f : fast_exp2((m - nm) * sc);
+            if (j > 0) {
+              bad |= !wait_for(b_pvdone + 8 * (sb ^ 1), ((jt - 1) >> 1) & 1, abort_flag, status, kWPvDone);
+              tc_fence_after();
+              const float g = need ? f : 1.0f;
+#pragma unroll
+              for (int c = 0; c < D / 2; c += 16) {
+                float o[16];
+                tmem_ld16(tm_o + lanes + wg * (D / 2) + c, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] *= g;
+                tmem_st16(tm_o + lanes + wg * (D / 2) + c, o);
+              }
+            }
+            if (need) {
+              l *= f;
+              m = nm;
+            }
+          }
+          const float neg = m == -INFINITY ? 0.0f : -m * sc;
+          float a0 = 0.0f, a1 = 0.0f, a2 = 0.0f, a3 = 0.0f;
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            const float e0 = fast_exp2(fmaf(s[c], sc, neg)), e1 = fast_exp2(fmaf(s[c + 1], sc, neg));
+            const float e2 = fast_exp2(fmaf(s[c + 2], sc, neg)), e3 = fast_exp2(fmaf(s[c + 3], sc, neg));
+            a0 += e0;
+            a1 += e1;
+            a2 += e2;
+            a3 += e3;
+            if constexpr (FP4) {
+              pk[c / 2] = pack16(e0, e1, __half{});
+              pk[c / 2 + 1] = pack16(e2, e3, __half{});
+            } else {
+              pk[c / 2] = pack16(e0, e1, T{});
+              pk[c / 2 + 1] = pack16(e2, e3, T{});
+            }
+          }
+          l += (a0 + a1) + (a2 + a3);
+          tmem_st32(tm_s, pk);
+          tc_wait_st();
+        }
+        if (!FP4 && !whole) {
+          // V rows that no row sees are zeroed before P.V reads them
+          int e;
+          if (u.tiles == 1) e = 1;
+          else e = j == u.tiles - 1 ? 2 * j + 1 : 2 * j + 2;
+          const int32_t v = v0 + row;
+          const bool clear = !seen(p, u, position_of(u, v));
+          // P.V of the tile before is done, so every earlier fill of these stages has landed: the parity
+          // below means this one
+          if (j > 0) bad |= !wait_for(b_pvdone + 8 * (sb ^ 1), ((jt - 1) >> 1) & 1, abort_flag, status, kWPvDone);
+#pragma unroll
+          for (int h = 0; h < C::kSPT; ++h) {
+            const uint32_t half = (eb + e) * C::kSPT + h, st = half % C::kStages;
+            bad |= !wait_for(b_full + 8 * st, (half / C::kStages) & 1, abort_flag, status, kWStageFull);
+            if (clear) {
+#pragma unroll
+              for (int b = 0; b < C::kNBS; ++b) {
+                if ((C::kSPT * C::kNBS > 1) && ((h * C::kNBS + b) & 1) != wg) continue;
+                if (C::kSPT * C::kNBS == 1 && wg) continue;
+                const uint32_t at = base + C::kRing + st * C::kStageBytes + b * 16384 + row * 128;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) st_shared_v4(at + 16 * k, make_uint4(0u, 0u, 0u, 0u));
+              }
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_pfull + 8 * sb);
+      }
+      if (left) break;                        // nothing of this call is written any more
+      // epilogue
+      if (u.tiles > 0) {
+        const uint32_t jl = js + u.tiles - 1;
+        bad |= !wait_for(b_pvdone + 8 * (jl & 1), (jl >> 1) & 1, abort_flag, status, kWPvDone);
+        tc_fence_after();
+      }
+      if (warp_live) {
+        // the two halves' sums; the buffer of the other parity than the last tile's maxima
+        float* const mx = maxima + ((js + u.tiles) & 1) * 256;
+        mx[wg * 128 + row] = l;
+        if (named_bar_any(1 + w, 64, bad)) break;
+        l += mx[(wg ^ 1) * 128 + row];
+      }
+      const bool store = row < live_rows;
+      const int64_t token = static_cast<int64_t>(u.row0) + tok;
+      const int32_t head = u.kvh * p.group + (row - tok * p.group);
+      const int64_t rh = token * p.n_qheads + head;
+      const bool empty = l == 0.0f && m == -INFINITY;
+      const float inv = empty ? 0.0f : p.v_mult / l;
+      if (store && wg == 0) {
+        const float lse = empty ? -INFINITY : m * sc * kLn2f + logf(l);
+        if (p.splits > 1) p.part_lse[rh * p.splits + u.split] = lse;
+        else if (p.lse) p.lse[rh] = lse;
+      }
+      if (warp_live) {
+        T* const out = static_cast<T*>(p.out) + rh * D + wg * (D / 2);
+        float* const part = p.splits > 1 ? p.part_o + (rh * p.splits + u.split) * D + wg * (D / 2) : nullptr;
+#pragma unroll
+        for (int c = 0; c < D / 2; c += 32) {
+          float o[32];
+          if (u.tiles > 0) {
+            tmem_ld32(tm_o + lanes + wg * (D / 2) + c, o);
+            tc_wait_ld();
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = empty ? 0.0f : o[k] * inv;
+          if (store && p.splits > 1) {
+            if (!empty) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                *reinterpret_cast<float4*>(part + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            }
+          } else if (store) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+              *reinterpret_cast<uint4*>(out + c + k) =
+                  make_uint4(pack16(o[k], o[k + 1], T{}), pack16(o[k + 2], o[k + 3], T{}),
+                             pack16(o[k + 4], o[k + 5], T{}), pack16(o[k + 6], o[k + 7], T{}));
+          }
+        }
+      }
+      if (u.tiles > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_ofree);
+      }
+      js += u.tiles;
+      eb += 2 * u.tiles;
+    }
+    finish_role();
+    return;
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA issuer, tensor-memory owner
+    if constexpr (FP4) regs_dec<64>();
+    constexpr bool kF16 = FP4 || std::is_same<T, __half>::value;
+    constexpr uint32_t kIdescQK = kF16 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t kIdescPV = kF16 ? idesc_f16_f32(128, C::kStageDims, false, true)
+                                       : idesc_bf16_f32(128, C::kStageDims, false, true);
+    constexpr uint32_t kHi = sw128_desc_hi(1024);
+    const uint32_t q_lo = sw128_desc_lo(base, 16);
+    const uint32_t k_lo = sw128_desc_lo(base + C::kRing, 16);
+    const uint32_t v_lo = sw128_desc_lo(base + C::kRing, 16384);
+    uint32_t st = 0, par = 0, entry = 0, js = 0, qit = 0;
+    bool stop = false;
+    // waits for the stages of the next entry; st and par move past it
+    auto take_entry = [&](uint32_t* stage) -> bool {
+      bool ok = true;
+#pragma unroll
+      for (int h = 0; h < C::kSPT; ++h) {
+        stage[h] = st;
+        ok = ok && wait_for(b_full + 8 * st, par, abort_flag, status, kWStageFull);
+        if (++st == C::kStages) {
+          st = 0;
+          par ^= 1;
+        }
+      }
+      return __all_sync(0xffffffffu, ok);
+    };
+    auto issue_qk = [&](uint32_t jt, bool last) -> bool {
+      uint32_t stage[C::kSPT];
+      if (!take_entry(stage)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int h = kk / (C::kStageDims / 16), kq = kk % (C::kStageDims / 16);
+          const uint32_t b_off = (kq >> 2) * 16384 + (kq & 3) * 32;
+          const uint32_t a_off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          tc_mma_w(tmem + (jt & 1) * 128, q_lo + (a_off >> 4), kHi,
+                   k_lo + stage[h] * (C::kStageBytes >> 4) + (b_off >> 4), kHi, kIdescQK, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(b_entry + 8 * (entry % C::kEntryBars));
+        tc_commit(b_sfull + 8 * (jt & 1));
+        if (last) tc_commit(b_qempty);
+      }
+      __syncwarp();
+      ++entry;
+      return true;
+    };
+    for (uint32_t it = 0;; ++it) {
+      const uint32_t rb = it % C::kRecords;
+      if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, status,
+                                            kWRecFull))) {
+        stop = true;
+        break;
+      }
+      const int nt = recs[rb].tiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_recempty + 8 * rb);
+      if (nt < 0) break;
+      if (nt == 0) continue;
+      if (!__all_sync(0xffffffffu, wait_for(b_qfull, qit & 1, abort_flag, status, kWQFull))) {
+        stop = true;
+        break;
+      }
+      if (!issue_qk(js, nt == 1)) {
+        stop = true;
+        break;
+      }
+      for (int j = 0; j < nt; ++j) {
+        const uint32_t jt = js + j;
+        if (j + 1 < nt && !issue_qk(jt + 1, j + 2 == nt)) {
+          stop = true;
+          break;
+        }
+        uint32_t stage[C::kSPT];
+        bool ok = wait_for(b_pfull + 8 * (jt & 1), (jt >> 1) & 1, abort_flag, status, kWPFull);
+        if (j == 0) ok = ok && wait_for(b_ofree, (qit & 1) ^ 1, abort_flag, status, kWOFree);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!take_entry(stage) || !ok) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t a0 = tmem + (jt & 1) * 128;
+#pragma unroll
+          for (int h = 0; h < C::kSPT; ++h) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t a = a0 + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8);
+              tc_mma_ta(tm_o + h * 128, a, v_lo + stage[h] * (C::kStageBytes >> 4) + kk * (2048 >> 4), kHi,
+                        kIdescPV, j > 0 || kk > 0 ? 1u : 0u);
+            }
+          }
+          tc_commit(b_entry + 8 * (entry % C::kEntryBars));
+          tc_commit(b_pvdone + 8 * (jt & 1));
+        }
+        __syncwarp();
+        ++entry;
+      }
+      if (stop) break;
+      js += nt;
+      ++qit;
+    }
+    if (lane == 0) {
+      tc_commit(b_fin);
+      drain(b_fin, 0, status, stop ? kDrainNs : kWaitNs);
+    }
+    __syncwarp();
+    finish_role();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+    return;
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ scheduler (warp 9), query tile
+    if constexpr (FP4) regs_dec<64>();
+    if (warp - 9 >= C::kQWarps) {
+      finish_role();
+      return;
+    }
+    uint32_t qit = 0;
+    int64_t n = blockIdx.x;
+    for (uint32_t it = 0;; ++it) {
+      const uint32_t rb = it % C::kRecords, ph = (it / C::kRecords) & 1;
+      Unit u;
+      if (warp == 9) {
+        if (p.stall_first_item && it == 0) break;
+        u.tiles = -1;
+        for (; n < p.n_units; n += gridDim.x) {
+          u = make_unit(p, n, lane);
+          if (u.tiles >= 0) break;
+          u.tiles = -1;
+        }
+        n += gridDim.x;
+        if (!__all_sync(0xffffffffu, wait_for(b_recempty + 8 * rb, ph ^ 1, abort_flag, status, kWRecEmpty))) break;
+        if (lane == 0) {
+          recs[rb] = u;
+          mbar_arrive(b_recfull + 8 * rb);
+        }
+        __syncwarp();
+      } else {
+        if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, ph, abort_flag, status, kWRecFull))) break;
+        u = load_unit(recs + rb);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_recempty + 8 * rb);
+      }
+      if (u.tiles < 0) break;
+      if (u.tiles == 0) continue;
+      if (!__all_sync(0xffffffffu, wait_for(b_qempty, (qit & 1) ^ 1, abort_flag, status, kWQEmpty))) break;
+      if constexpr (!FP4) {
+        // a whole tile in one box per 64-dim block, a partial one token by token
+        const bool full = u.tokens == p.tile_tokens;
+        const uint32_t tok_bytes = static_cast<uint32_t>(p.group) * 128u;
+        if (lane == 0) mbar_arrive_expect_tx(b_qfull, static_cast<uint32_t>(u.tokens) * tok_bytes * (D / 64));
+        __syncwarp();
+        const int loads = full ? D / 64 : u.tokens * (D / 64);
+        for (int i = lane; i < loads; i += 32) {
+          const int b = i % (D / 64), t = i / (D / 64);
+          tma_load_3d(base + b * 16384 + t * tok_bytes, full ? &tmQT : &tmQ1, b * 64, u.kvh * p.group, u.row0 + t,
+                      b_qfull);
+        }
+      } else {
+        // rows to fp16 in the swizzled layout (generic stores)
+        const int chunks = u.tokens * p.group * (D / 8);
+        for (int i = (warp - 9) * 32 + lane; i < chunks; i += 32 * C::kQWarps) {
+          const int r = i / (D / 8), c = i % (D / 8);
+          const int64_t token = static_cast<int64_t>(u.row0) + r / p.group;
+          const int32_t head = u.kvh * p.group + r % p.group;
+          uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (token * p.n_qheads + head) * D +
+                                                         c * 8));
+          if constexpr (!std::is_same<T, __half>::value)
+            x = make_uint4(bf16x2_as_f16x2(x.x), bf16x2_as_f16x2(x.y), bf16x2_as_f16x2(x.z), bf16x2_as_f16x2(x.w));
+          st_shared_v4(base + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4), x);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_qfull);
+      }
+      ++qit;
+    }
+    if (!FP4 && *abort_flag && qit > 0 && lane == 0) drain(b_qfull, (qit - 1) & 1, status, kDrainNs);
+    __syncwarp();
+    finish_role();
+    return;
+  } else if constexpr (!FP4) {
+    // ------------------------------------------------------------ K/V producers (TMA)
+    const int pw = warp - 12;
+    const int per = p.box > 0 ? p.box : 4;                  // keys of one copy
+    const int op = lane * 4 + pw;
+    const int kb = op / C::kNBS * per, blk = op % C::kNBS;  // its first key and 64-dim block
+    const bool active = op < kWinTile / per * C::kNBS;
+    uint32_t st = 0, par = 0, half = 0, jt = 0;
+    int64_t last_half = -1;
+    bool stop = false;
+    struct Rows {   // physical rows of this lane's copy: slots of up to four keys
+      int32_t r[4];
+      bool wanted;
+      uint32_t hole;
+    };
+    for (uint32_t it = 0; !stop; ++it) {
+      const uint32_t rb = it % C::kRecords;
+      if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, status,
+                                            kWRecFull))) {
+        stop = true;
+        break;
+      }
+      const Unit u = load_unit(recs + rb);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_recempty + 8 * rb);
+      if (u.tiles < 0) break;
+      // Where tile j's keys of this lane lie: a slot, or the row past the cache's end (which TMA fills
+      // with zeros) where there is no page.
+      auto locate = [&](int j) {
+        Rows x{};
+        if (!active) return x;
+        const int32_t v = (u.tile0 + j) * kWinTile + kb;
+        const int32_t pos = position_of(u, v);
+        if (p.box > 0) {
+          // a box is one run of positions inside one page
+          x.wanted = pos < u.hi && (pos + per > u.lo || pos < p.n_sink);
+          if (x.wanted) {
+            const int64_t s = paged_slot(p.pa, u.req, INT32_MAX, pos);
+            x.hole = s < 0;
+            x.r[0] = s < 0 ? p.n_slots : static_cast<int32_t>(s);
+          }
+        } else {
+          x.wanted = true;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const bool look = seen(p, u, pos + k);
+            const int64_t s = look ? paged_slot(p.pa, u.req, INT32_MAX, pos + k) : -1;
+            x.hole |= (look && s < 0 ? 1u : 0u) << k;
+            x.r[k] = s < 0 ? p.n_slots * p.n_kvheads : static_cast<int32_t>(s) * p.n_kvheads + u.kvh;
+          }
+        }
+        return x;
+      };
+      auto issue = [&](const Rows& x, bool is_v) -> bool {
+        const uint32_t loads = __ballot_sync(0xffffffffu, x.wanted);
+        const uint32_t bytes = __popc(loads) * per * 128;
+#pragma unroll
+        for (int h = 0; h < C::kSPT; ++h, ++half) {
+          if (half >= C::kStages) {
+            const uint32_t before = (half - C::kStages) / C::kSPT;   // the entry that held this stage
+            if (!__all_sync(0xffffffffu, wait_for(b_entry + 8 * (before % C::kEntryBars),
+                                                  (before / C::kEntryBars) & 1, abort_flag, status, kWStageEmpty)))
+              return false;
+          }
+          if (h == 0 && !is_v) {
+            uint32_t w0, w1 = 0;
+            if (p.box > 0) {
+              w0 = __ballot_sync(0xffffffffu, x.hole != 0);
+            } else {
+              w0 = (__ballot_sync(0xffffffffu, x.hole & 1) & 0xffffu) | (__ballot_sync(0xffffffffu, x.hole & 2) << 16);
+              w1 = (__ballot_sync(0xffffffffu, x.hole & 4) & 0xffffu) | (__ballot_sync(0xffffffffu, x.hole & 8) << 16);
+            }
+            if (lane == 0)
+              *reinterpret_cast<uint2*>(bad_keys + (jt % C::kBadSlots) * 8 + pw * 2) = make_uint2(w0, w1);
+          }
+          const uint32_t bar = b_full + 8 * st;
+          if (lane == 0) {
+            if (bytes) mbar_arrive_expect_tx(bar, bytes); else mbar_arrive(bar);
+          }
+          __syncwarp();
+          if (x.wanted) {
+            const uint32_t dst = base + C::kRing + st * C::kStageBytes + blk * 16384 + kb * 128;
+            const void* const tm = is_v ? static_cast<const void*>(&tmV) : static_cast<const void*>(&tmK);
+            const int32_t d0 = h * 128 + blk * 64;
+            if (p.box > 0) tma_load_3d(dst, tm, d0, u.kvh, x.r[0], bar);
+            else tma_gather4(dst, tm, d0, x.r[0], x.r[1], x.r[2], x.r[3], bar);
+          }
+          last_half = half;
+          if (++st == C::kStages) {
+            st = 0;
+            par ^= 1;
+          }
+        }
+        if (!is_v) ++jt;
+        return true;
+      };
+      if (u.tiles == 0) continue;
+      Rows k_next = locate(0);
+      if (!issue(k_next, false)) {
+        stop = true;
+        break;
+      }
+      Rows v_rows = k_next;
+      if (u.tiles > 1) k_next = locate(1);
+      for (int j = 0; j < u.tiles; ++j) {
+        if (j + 1 < u.tiles && !issue(k_next, false)) {
+          stop = true;
+          break;
+        }
+        if (!issue(v_rows, true)) {
+          stop = true;
+          break;
+        }
+        v_rows = k_next;
+        if (j + 2 < u.tiles) k_next = locate(j + 2);
+      }
+    }
+    if (stop && lane == 0) {
+      // copies of this warp that may still be in flight: the last kStages fills
+      for (int64_t h = last_half - C::kStages + 1; h <= last_half; ++h)
+        if (h >= 0)
+          drain(b_full + 8 * static_cast<uint32_t>(h % C::kStages), static_cast<uint32_t>(h / C::kStages) & 1, status,
+                kDrainNs / C::kStages);
+    }
+    __syncwarp();
+    finish_role();
+    return;
+  } else {
+    // ------------------------------------------------------------ 4-bit caches: copy ahead, convert
+    regs_dec<72>();
+    const int wi = warp - 12;                               // keys 16 wi .. 16 wi + 15 of every tile
+    const uint32_t staging = base + C::kStagingAt + wi * C::kDepth * C::kStaging;
+    Unit u{};
+    u.tiles = 0;
+    int e = 0;                                              // next entry of u to copy
+    uint32_t it = 0, issued = 0, done = 0, jt = 0;
+    bool ended = false, stop = false;
+    const int64_t row_codes = static_cast<int64_t>(p.n_kvheads) * (D / 2);
+    const int64_t row_scales = static_cast<int64_t>(p.n_kvheads) * (D / 16);
+    while (!stop) {
+      // keep kDepth entries in flight; a record that is not there yet is only waited for when nothing is
+      // pending (the other roles may need the pending entries to get to releasing older records)
+      while (!ended && issued - done < C::kDepth) {
+        if (e == 2 * u.tiles) {
+          const uint32_t rb = it % C::kRecords, ph = (it / C::kRecords) & 1;
+          if (issued != done) {
+            if (!__all_sync(0xffffffffu, mbar_test(b_recfull + 8 * rb, ph))) break;
+          } else if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, ph, abort_flag, status, kWRecFull))) {
+            stop = true;
+            break;
+          }
+          u = load_unit(recs + rb);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_recempty + 8 * rb);
+          ++it;
+          e = 0;
+          if (u.tiles < 0) {
+            ended = true;
+            break;
+          }
+          continue;
+        }
+        int tile;
+        bool is_v;
+        entry_of(e, u.tiles, tile, is_v);
+        const int32_t v = (u.tile0 + tile) * kWinTile + wi * 16 + (lane & 15);
+        const int32_t pos = position_of(u, v);
+        const bool look = seen(p, u, pos);
+        const int32_t slot = look ? static_cast<int32_t>(paged_slot(p.pa, u.req, INT32_MAX, pos)) : -1;
+        if (!is_v) {
+          const uint32_t holes = __ballot_sync(0xffffffffu, look && slot < 0) & 0xffffu;
+          if (lane == 0) bad_keys[(jt % C::kBadSlots) * 8 + wi] = holes;
+          ++jt;
+        }
+        const uint32_t to = staging + (issued % C::kDepth) * C::kStaging;
+        const uint8_t* const codes = (is_v ? p.v_codes : p.k_codes) + static_cast<int64_t>(u.kvh) * (D / 2);
+        const uint8_t* const scales = (is_v ? p.v_scale : p.k_scale) + static_cast<int64_t>(u.kvh) * (D / 16);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const int ch = i * 32 + lane, key = ch / (D / 32), part = ch % (D / 32);
+          const int32_t s = __shfl_sync(0xffffffffu, slot, key);
+          cp_async_zfill<16>(to + ch * 16, codes + (s < 0 ? 0 : s) * row_codes + part * 16, s >= 0);
+        }
+        if (lane < 16)
+          cp_async_zfill<D / 16>(to + 16 * (D / 2) + lane * (D / 16), scales + (slot < 0 ? 0 : slot) * row_scales,
+                                 slot >= 0);
+        cp_async_commit();
+        ++issued;
+        ++e;
+      }
+      if (stop || issued == done) break;
+      cp_async_wait(static_cast<int>(issued - done) - 1);
+      __syncwarp();
+      const uint32_t half0 = done * C::kSPT;
+      bool ok = true;
+#pragma unroll
+      for (int h = 0; h < C::kSPT; ++h) {
+        const uint32_t half = half0 + h;
+        if (half >= C::kStages) {
+          const uint32_t before = (half - C::kStages) / C::kSPT;
+          ok = ok && wait_for(b_entry + 8 * (before % C::kEntryBars), (before / C::kEntryBars) & 1, abort_flag, status,
+                              kWStageEmpty);
+        }
+      }
+      if (!__all_sync(0xffffffffu, ok)) {
+        stop = true;
+        break;
+      }
+      const uint32_t from = staging + (done % C::kDepth) * C::kStaging;
+      constexpr int kUnits = 16 * (D / 64);                 // (key, 64-dim block)
+#pragma unroll
+      for (int i = 0; i < (kUnits + 31) / 32; ++i) {
+        const int n = i * 32 + lane;
+        if (kUnits < 32 && n >= kUnits) break;
+        const int key = n / (D / 64), blk = n % (D / 64);
+        const uint4 c0 = ld_shared_v4(from + key * (D / 2) + blk * 32);
+        const uint4 c1 = ld_shared_v4(from + key * (D / 2) + blk * 32 + 16);
+        const uint32_t sc4 = ld_shared_u32(from + 16 * (D / 2) + key * (D / 16) + blk * 4);
+        const uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(sc4)), s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(sc4 >> 16));
+        __half2 sa, sb;
+        memcpy(&sa, &s01, 4);
+        memcpy(&sb, &s23, 4);
+        const __half2 sc[4] = {__low2half2(sa), __high2half2(sa), __low2half2(sb), __high2half2(sb)};
+        const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        const uint32_t half = half0 + blk / C::kNBS;
+        const int r = wi * 16 + key;
+        const uint32_t row = base + C::kRing + (half % C::kStages) * C::kStageBytes + (blk % C::kNBS) * 16384 + r * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          st_shared_v4(row + ((c ^ (r & 7)) << 4),
+                       make_uint4(e2m1_scaled(words[c], 0, sc[c / 2]), e2m1_scaled(words[c], 1, sc[c / 2]),
+                                  e2m1_scaled(words[c], 2, sc[c / 2]), e2m1_scaled(words[c], 3, sc[c / 2])));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+#pragma unroll
+        for (int h = 0; h < C::kSPT; ++h) mbar_arrive(b_full + 8 * ((half0 + h) % C::kStages));
+      }
+      ++done;
+    }
+    cp_async_wait(0);
+    __syncwarp();
+    finish_role();
+    return;
+  }
+}
+
+// ---------------------------------------------------------------------------- host side
+template <int D, typename T, bool FP4>
+cudaError_t launch_window_instance(const WindowParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   const CUtensorMap& tq1, const CUtensorMap& tqt, int grid, int which,
+                                   cudaStream_t stream) {
+  using C = WinCfg<D, FP4>;
+  auto kern = window_attention_kernel<D, T, FP4>;
+  const cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern), C::kSmem, kOptWindow + which);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, C::kThreads, C::kSmem, stream>>>(tk, tv, tq1, tqt, p);
+  return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_window_dim(const WindowParams& p, bool fp16, bool fp4, const CUtensorMap& tk,
+                              const CUtensorMap& tv, const CUtensorMap& tq1, const CUtensorMap& tqt, int grid,
+                              cudaStream_t stream) {
+  constexpr int at = D == 64 ? 0 : D == 128 ? 4 : 8;
+  if (fp4)
+    return fp16 ? launch_window_instance<D, __half, true>(p, tk, tv, tq1, tqt, grid, at, stream)
+                : launch_window_instance<D, __nv_bfloat16, true>(p, tk, tv, tq1, tqt, grid, at + 1, stream);
+  return fp16 ? launch_window_instance<D, __half, false>(p, tk, tv, tq1, tqt, grid, at + 2, stream)
+              : launch_window_instance<D, __nv_bfloat16, false>(p, tk, tv, tq1, tqt, grid, at + 3, stream);
+}
+// one translation unit per head dim
+cudaError_t launch_window_d64(const WindowParams&, bool, bool, const CUtensorMap&, const CUtensorMap&,
+                              const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+cudaError_t launch_window_d128(const WindowParams&, bool, bool, const CUtensorMap&, const CUtensorMap&,
+                               const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+cudaError_t launch_window_d256(const WindowParams&, bool, bool, const CUtensorMap&, const CUtensorMap&,
+                               const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+
+}  // namespace qsa
