@@ -349,7 +349,7 @@ struct WindowParams {
   float v_mult;                 // V cache's scale
 };
 cudaError_t launch_window(const WindowParams& p, int head_dim, bool fp16, bool fp4, const void* k_cache,
-                          const void* v_cache, int num_sms, cudaStream_t stream);
+                          const void* v_cache, cudaStream_t stream);
 
 // Dynamic shared-memory opt-in of a kernel to `bytes`, its largest use, once per device and kernel (so
 // calls made during a graph capture only enqueue).

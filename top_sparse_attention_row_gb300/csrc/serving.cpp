@@ -85,10 +85,11 @@ qsa_status run_rope(qsa::RopeParams& p, const qsa_rope_spec* rope, int32_t dtype
   return QSA_OK;
 }
 
-// Splits of the key axis.  A unit's time is its key tiles; a split one also writes, and the join reads,
-// its partial rows in fp32 (two tiles' worth of bytes when all 128 rows are in use, in proportion
-// otherwise), and the join is one more launch, about three tiles long.  The count with the shortest
-// last-finishing SM wins, the smaller one where two tie.
+// Splits of the key axis, by a model of the call's time in key tiles.  A unit takes its tiles, about three
+// tiles' time of its own (query tile, first softmax, output), and when split its partial rows in fp32, which
+// it writes and the join reads (two tiles' worth of bytes when all 128 rows are in use).  Units are handed
+// out as SMs become free: the average load and half a unit of waiting for the last.  The join is one more
+// launch, about three tiles long.  The smallest count among the best wins.
 struct WindowPlan {
   int32_t tile_tokens, n_tiles, splits;
   int64_t n_units;
@@ -114,8 +115,9 @@ WindowPlan plan_window(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, in
   double best = 0.0;
   w.splits = 1;
   for (int64_t s = 1; s <= kt && s <= kMaxSplits; ++s) {
-    const int64_t waves = (items * s + sms - 1) / sms;
-    const double cost = waves * ((kt + s - 1) / s + (s > 1 ? partial : 0.0)) + (s > 1 ? 3.0 : 0.0);
+    const double unit = static_cast<double>((kt + s - 1) / s) + 3.0 + (s > 1 ? partial : 0.0);
+    const double load = static_cast<double>(items * s) / sms;
+    const double cost = (load <= 1.0 ? unit : (load + 0.5) * unit) + (s > 1 ? 3.0 : 0.0);
     if (s == 1 || cost < best) {
       best = cost;
       w.splits = static_cast<int32_t>(s);
@@ -176,6 +178,7 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   const int32_t group = n_qheads / n_kvheads;
   const WindowPlan w = plan_window(n_rows, n_requests, n_kvheads, group,
                                    static_cast<int64_t>(pages_per_req) * page_size, window, n_sink, sms);
+  if (w.n_units > INT32_MAX) return QSA_ERR_UNSUPPORTED;
   qsa::WindowParams p{};
   p.q = q;
   p.out = out;
@@ -234,7 +237,7 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
     p.part_lse = p.part_o + static_cast<size_t>(n_rows) * n_qheads * p.splits * head_dim;
   }
   p.stall_first_item = qsa::take_stall_request() ? 1 : 0;
-  const cudaError_t e = qsa::launch_window(p, head_dim, dtype == QSA_FP16, fp4 != nullptr, k_cache, v_cache, sms,
+  const cudaError_t e = qsa::launch_window(p, head_dim, dtype == QSA_FP16, fp4 != nullptr, k_cache, v_cache,
                                            stream);
   if (own) cudaFreeAsync(ws, stream);
   if (e != cudaSuccess) return QSA_ERR_CUDA;

@@ -19,6 +19,7 @@ constexpr int kJoinWarps = 4;
 template <int D, typename T>
 __global__ void __launch_bounds__(kJoinWarps * 32) window_join_kernel(const __grid_constant__ WindowParams p) {
   constexpr int kPer = D / 32;
+  pdl_wait();   // first thing in every thread: the grid must not end before the attention kernel has
   const int lane = threadIdx.x & 31;
   const int64_t rh = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   if (rh >= p.n_rows * p.n_qheads) return;
@@ -26,18 +27,42 @@ __global__ void __launch_bounds__(kJoinWarps * 32) window_join_kernel(const __gr
   if (row < __ldg(p.pa.cu_seqlens_q) || row >= __ldg(p.pa.cu_seqlens_q + p.pa.n_requests)) return;
   const float* const ls = p.part_lse + rh * p.splits;
   const float* const os = p.part_o + rh * p.splits * D + lane * kPer;
-  float m = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ls[s]);
+  // lane s holds the weight of split s (up to 128 splits: four per lane)
+  float w[4], m = -INFINITY;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    w[g] = g * 32 + lane < p.splits ? ls[g * 32 + lane] : -INFINITY;
+    m = fmaxf(m, w[g]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float acc[kPer], total = 0.0f;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float l = ls[s];
-    if (l == -INFINITY) continue;          // nothing seen there: its output was not written
-    const float w = __expf(l - m);
-    total += w;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[k] += w * os[static_cast<int64_t>(s) * D + k];
+  for (int g = 0; g < 4; ++g) {
+    w[g] = w[g] == -INFINITY ? 0.0f : __expf(w[g] - m);
+    total += w[g];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int n = min(p.splits - g * 32, 32);
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+      const float ws = __shfl_sync(0xffffffffu, w[g], s);
+      float x[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; k += 2) {
+        const float2 t = *reinterpret_cast<const float2*>(os + static_cast<int64_t>(g * 32 + s) * D + k);
+        x[k] = t.x;
+        x[k + 1] = t.y;
+      }
+      // a split that saw nothing wrote no output: whatever is there stays out
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] += ws == 0.0f ? 0.0f : ws * x[k];
+    }
   }
   const float inv = m == -INFINITY ? 0.0f : 1.0f / total;
   T* const out = static_cast<T*>(p.out) + rh * D + lane * kPer;
@@ -47,13 +72,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32) window_join_kernel(const __gr
   if (lane == 0 && p.lse) p.lse[rh] = m == -INFINITY ? -INFINITY : m + logf(total);
 }
 
-template <typename T>
-void launch_join(const WindowParams& p, int head_dim, cudaStream_t stream) {
+template <int D, typename T>
+cudaError_t launch_join_dim(const WindowParams& p, cudaStream_t stream) {
+  // launched while the attention kernel runs (programmatic dependent launch): it waits for that grid's end
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   const int64_t rows = p.n_rows * p.n_qheads;
-  const unsigned grid = static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps);
-  if (head_dim == 64) window_join_kernel<64, T><<<grid, kJoinWarps * 32, 0, stream>>>(p);
-  else if (head_dim == 128) window_join_kernel<128, T><<<grid, kJoinWarps * 32, 0, stream>>>(p);
-  else window_join_kernel<256, T><<<grid, kJoinWarps * 32, 0, stream>>>(p);
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, window_join_kernel<D, T>, p);
+}
+template <typename T>
+cudaError_t launch_join(const WindowParams& p, int head_dim, cudaStream_t stream) {
+  return head_dim == 64    ? launch_join_dim<64, T>(p, stream)
+         : head_dim == 128 ? launch_join_dim<128, T>(p, stream)
+                           : launch_join_dim<256, T>(p, stream);
 }
 
 }  // namespace
@@ -78,7 +116,7 @@ CUresult encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, c
 }
 
 cudaError_t launch_window(const WindowParams& p, int head_dim, bool fp16, bool fp4, const void* k_cache,
-                          const void* v_cache, int num_sms, cudaStream_t stream) {
+                          const void* v_cache, cudaStream_t stream) {
   // (the element type only decides how many bits are moved: 16 either way)
   const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap tk{}, tv{}, tq1{}, tqt{};
@@ -108,13 +146,12 @@ cudaError_t launch_window(const WindowParams& p, int head_dim, bool fp16, bool f
     }
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
   }
-  const int grid = static_cast<int>(p.n_units < num_sms ? p.n_units : num_sms);
+  const int grid = static_cast<int>(p.n_units);
   const cudaError_t e = head_dim == 64    ? launch_window_d64(p, fp16, fp4, tk, tv, tq1, tqt, grid, stream)
                         : head_dim == 128 ? launch_window_d128(p, fp16, fp4, tk, tv, tq1, tqt, grid, stream)
                                           : launch_window_d256(p, fp16, fp4, tk, tv, tq1, tqt, grid, stream);
   if (e != cudaSuccess || p.splits <= 1) return e;
-  if (fp16) launch_join<__half>(p, head_dim, stream); else launch_join<__nv_bfloat16>(p, head_dim, stream);
-  return cudaGetLastError();
+  return fp16 ? launch_join<__half>(p, head_dim, stream) : launch_join<__nv_bfloat16>(p, head_dim, stream);
 }
 
 }  // namespace qsa

@@ -7,7 +7,9 @@
 //
 //  * One work unit is a query tile of one request and KV head -- 128 rows, the `group` query heads of
 //    each of 128 / group consecutive tokens, so that every K and V row is read once for all of them --
-//    and, with splits, a contiguous range of its keys.  A persistent CTA per SM runs units round robin.
+//    and, with splits, a contiguous range of its keys.  The grid has a block per unit, and the block on
+//    an SM takes over the units of blocks that have not started (cluster launch control), so that the
+//    SMs stay busy with units of unequal length and no counter in memory is needed.
 //  * The keys a unit sees are the sinks and one range [lo, hi): both are laid side by side in a virtual
 //    index v (position v below S0, v + shift from S0 on), which is cut into tiles of 128 keys.  A
 //    window of 4096 costs 33 tiles whatever the context is; boxes that no row sees are not loaded.
@@ -73,9 +75,10 @@ struct WinCfg {
   static constexpr int kBadAt = kMaxAt + 2048;             // [kBadSlots][8] uint32
   static constexpr int kRecAt = kBadAt + kBadSlots * 32;   // [kRecords][16] int32
   static constexpr int kBarAt = kRecAt + kRecords * 64;
-  // full[kStages], entry[16], sfull[2], pfull[2], pvdone[2], qfull, qempty, ofree, fin, recfull/empty
-  static constexpr int kBars = kStages + kEntryBars + 10 + 2 * kRecords;
-  static constexpr int kTmemSlot = kBarAt + 8 * kBars;
+  // full[kStages], entry[16], sfull[2], pfull[2], pvdone[2], qfull, qempty, ofree, fin, next, recfull/empty
+  static constexpr int kBars = kStages + kEntryBars + 11 + 2 * kRecords;
+  static constexpr int kNextAt = (kBarAt + 8 * kBars + 15) / 16 * 16;   // answer of the launch control
+  static constexpr int kTmemSlot = kNextAt + 16;
   static constexpr int kSmem = kTmemSlot + 16;
   static_assert(kSmem <= kSmemLimit, "shared memory");
   static_assert(kStages / kSPT + 2 < kEntryBars, "entry barriers");
@@ -88,7 +91,7 @@ constexpr float kRaise = 8.0f;          // log2 units by which a tile may exceed
 constexpr float kLn2f = 0.6931471805599453f;
 enum Site : int32_t {
   kWRecEmpty = 0x41, kWRecFull, kWQEmpty, kWQFull, kWStageEmpty, kWStageFull, kWSFull, kWPFull, kWPvDone,
-  kWOFree, kWDrain
+  kWOFree, kWNext, kWDrain
 };
 
 __device__ __forceinline__ unsigned long long now_ns() {
@@ -165,13 +168,13 @@ __device__ __forceinline__ int32_t tile_owner(const WindowParams& p, int32_t til
 }
 
 // Unit `n` of the call, or tiles = -2 for a number without rows.  Warp-uniform; every lane takes part.
-__device__ __forceinline__ Unit make_unit(const WindowParams& p, int64_t n, int lane) {
+__device__ __forceinline__ Unit make_unit(const WindowParams& p, uint32_t n, int lane) {
   Unit u{};
-  u.split = static_cast<int32_t>(n % p.splits);
-  const int64_t tk = n / p.splits;
+  const uint32_t tk = p.splits > 1 ? n / p.splits : n;
+  u.split = static_cast<int32_t>(n - tk * p.splits);
   u.kvh = static_cast<int32_t>(tk / p.n_tiles);
   // a request's later tiles see more keys where there is no window: they go first
-  const int32_t tile = p.n_tiles - 1 - static_cast<int32_t>(tk - static_cast<int64_t>(u.kvh) * p.n_tiles);
+  const int32_t tile = p.n_tiles - 1 - static_cast<int32_t>(tk - static_cast<uint32_t>(u.kvh) * p.n_tiles);
   u.req = tile_owner(p, tile, lane);
   const int64_t r0 = __ldg(p.pa.cu_seqlens_q + u.req);
   int64_t r1 = __ldg(p.pa.cu_seqlens_q + u.req + 1);
@@ -323,7 +326,8 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
   const uint32_t b_qempty = b_qfull + 8;
   const uint32_t b_ofree = b_qempty + 8;
   const uint32_t b_fin = b_ofree + 8;
-  const uint32_t b_recfull = b_fin + 8;
+  const uint32_t b_next = b_fin + 8;
+  const uint32_t b_recfull = b_next + 8;
   const uint32_t b_recempty = b_recfull + 8 * C::kRecords;
   float* const maxima = reinterpret_cast<float*>(smem + C::kMaxAt);
   uint32_t* const bad_keys = reinterpret_cast<uint32_t*>(smem + C::kBadAt);
@@ -349,6 +353,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     mbar_init(b_qempty, 1);
     mbar_init(b_ofree, 8);
     mbar_init(b_fin, 1);
+    mbar_init(b_next, 1);
     for (int r = 0; r < C::kRecords; ++r) {
       mbar_init(b_recfull + 8 * r, 1);
       mbar_init(b_recempty + 8 * r, 8 + 1 + C::kProducers + (C::kQWarps - 1));
@@ -369,6 +374,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_launch_dependents();                    // the join's launch overlaps (it waits for this grid's end)
   const uint32_t tmem = *tmem_slot;
   const uint32_t tm_o = tmem + 256;           // S buffers: columns 0-127 and 128-255; O: from 256
 
@@ -734,19 +740,48 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       return;
     }
     uint32_t qit = 0;
-    int64_t n = blockIdx.x;
+    // Units: this block's own, then those of blocks that have not started.  The answer for the next one
+    // is asked for before the present one is worked out.
+    int32_t n = blockIdx.x;
+    uint32_t asked = 0;
+    bool more = true, pending = false;       // more: no answer has said "none" yet
+    auto ask = [&]() {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(b_next, 16);
+        clc_try_cancel(base + C::kNextAt, b_next);
+      }
+      __syncwarp();
+      pending = true;
+    };
+    auto answer = [&]() -> int32_t {
+      const bool ok = mbar_try_wait(b_next, asked & 1) || wait_for(b_next, asked & 1, abort_flag, status, kWNext);
+      pending = false;
+      ++asked;
+      if (!__all_sync(0xffffffffu, ok)) {
+        more = false;
+        return -1;
+      }
+      const int32_t x = clc_answer(base + C::kNextAt);
+      fence_proxy_async_smem();              // the next answer is written by the async proxy
+      __syncwarp();
+      more = x >= 0;
+      return x;
+    };
+    if (warp == 9 && !p.stall_first_item) ask();
     for (uint32_t it = 0;; ++it) {
       const uint32_t rb = it % C::kRecords, ph = (it / C::kRecords) & 1;
       Unit u;
       if (warp == 9) {
         if (p.stall_first_item && it == 0) break;
+        // (n is the unit in hand, and the answer for the one after it is pending)
         u.tiles = -1;
-        for (; n < p.n_units; n += gridDim.x) {
-          u = make_unit(p, n, lane);
+        while (n >= 0) {
+          u = make_unit(p, static_cast<uint32_t>(n), lane);
+          n = pending ? answer() : -1;
+          if (more) ask();
           if (u.tiles >= 0) break;
           u.tiles = -1;
         }
-        n += gridDim.x;
         if (!__all_sync(0xffffffffu, wait_for(b_recempty + 8 * rb, ph ^ 1, abort_flag, status, kWRecEmpty))) break;
         if (lane == 0) {
           recs[rb] = u;
@@ -795,6 +830,20 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     }
     if (!FP4 && *abort_flag && qit > 0 && lane == 0) drain(b_qfull, (qit - 1) & 1, status, kDrainNs);
     __syncwarp();
+    if (warp == 9 && (*abort_flag || p.stall_first_item)) {
+      // the call is given up: blocks that have not started are taken off the grid, so that their waits do
+      // not run out one after the other
+      *abort_flag = 1;
+      while (more) {
+        if (!pending) ask();
+        drain(b_next, asked & 1, status, kDrainNs);
+        pending = false;
+        ++asked;
+        more = clc_answer(base + C::kNextAt) >= 0;
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+    }
     finish_role();
     return;
   } else if constexpr (!FP4) {
