@@ -136,8 +136,6 @@ def test_rope_table_refusals(B):
             B.rope_table(**kw)
     with pytest.raises(ValueError):
         B.rope_table(64, scaling="other")
-    with pytest.raises(ValueError):
-        B.rope_table(64).spec("other", 0)
     t = B.RopeTable(4, [1, 2 ** 64 - 1], 1.5)      # a caller's own frequencies
     assert t.steps == [1, 2 ** 64 - 1] and t.magnitude == 1.5
 
@@ -165,6 +163,27 @@ def test_binding_refuses_cpu_and_mismatched_tensors(B):
         B.rope(x.transpose(1, 2).contiguous().transpose(1, 2), i(3), t)          # heads not contiguous
     with pytest.raises(ValueError):
         B.rope_append(None, x, x, x, None, i(3), i(3), t)                        # v without its cache
+    with pytest.raises(TypeError):
+        B.rope(x, i(3), None)
+    with pytest.raises(TypeError):
+        B.rope(x, [0, 1, 2], t)
+    with pytest.raises(TypeError):
+        B.rope(x, i(3), t, unknown=1)
+    q, c, cu, kv, tab = torch.zeros(3, 2, 64).half(), torch.zeros(128, 1, 64).half(), i(2), i(1), i(1, 2)
+    with pytest.raises(ValueError):
+        B.window_attention_paged(q, c, c, cu, kv, tab, 64, 0.1)                  # not on a GPU
+    with pytest.raises(ValueError):
+        B.window_attention_paged(q, c, c, cu, kv, tab, 48, 0.1)                  # not whole pages
+    with pytest.raises(ValueError):
+        B.window_attention_paged(q, c, c[:64], cu, kv, tab, 64, 0.1)
+    with pytest.raises(ValueError):
+        B.window_attention_paged(q, c, c, kv, kv, tab, 64, 0.1)
+    with pytest.raises(TypeError):
+        B.window_attention_paged(q, c.float(), c, cu, kv, tab, 64, 0.1)
+    with pytest.raises(AttributeError):
+        B.no_such_call
+    for name in B.SERVING:
+        assert name in getattr(B, name).__doc__ or getattr(B, name).__text_signature__
 
 
 def test_oracle_fp4_grid_and_ties():

@@ -8,7 +8,6 @@ to run when the library has not been built -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from collections import namedtuple
 from typing import Optional
@@ -589,147 +588,32 @@ def version() -> str:
 
 
 # ------------------------------------------------------------------------------ serving step
-# A decode step makes these calls with kernels of a few microseconds, so the checks are written to
-# cost little where nothing is wrong.
+# A decode step makes these calls with kernels of a few microseconds, so their argument checks, output
+# tensors and streams are handled in C++ (csrc/torch_serving.cpp, built into the module _serving): same
+# checks and errors as above.  They are attributes of this module, loaded with the library on first use:
+#   page_plan, rope, rope_append, rope_append_fp4, window_attention_paged, window_attention_fp4_paged
 
-_DTYPE_CODES = None          # {torch.bfloat16: 0, torch.float16: 1}
-ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+SERVING = ("page_plan", "rope", "rope_append", "rope_append_fp4", "window_attention_paged",
+           "window_attention_fp4_paged")
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "turns": 4}
-
-
-def _dtype_code(dtype, name):
-    global _DTYPE_CODES
-    if _DTYPE_CODES is None:
-        import torch
-        _DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1}
-    code = _DTYPE_CODES.get(dtype)
-    if code is None:
-        raise TypeError(f"{name} must be bfloat16 or float16, got {dtype}")
-    return code
-
-
-def _tensor(t, dtype, name, shape, device):
-    """Checks a contiguous tensor on `device`."""
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
-        return
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _rows(t, dtype, name, shape, device):
-    """Checks rows [n, heads, dim] whose heads are contiguous; returns the row stride in elements."""
-    n, heads, dim = shape
-    if t.dtype is dtype and t.shape == shape and t.device == device:
-        a, b, c = t.stride()
-        if (c == 1 or dim == 1) and (b == dim or heads == 1):
-            return a if n > 1 else heads * dim
-        raise ValueError(f"{name} must have contiguous heads (strides (any, {dim}, 1)), got {t.stride()}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _on_device_of(at):
-    """Runs a call with the device of its positional argument `at` as the current one."""
-    def wrap(f):
-        @functools.wraps(f)
-        def call(*args, **kw):
-            import torch
-            t = args[at]
-            if t.is_cuda and t.get_device() != torch.cuda.current_device():
-                with torch.cuda.device(t.device):
-                    return f(*args, **kw)
-            return f(*args, **kw)
-        return call
-    return wrap
-
-
-def _launch_stream(device, stream):
-    """The raw stream to launch on; the device is the current one."""
-    if not device.type == "cuda":
-        raise ValueError("tensors must be CUDA tensors")
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _record(stream, device, tensors):
-    """Tensors made for a call on a given stream, which may not be the current one."""
-    if stream is not None:
-        import torch
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        for t in tensors:
-            t.record_stream(stream)
-
 
 PagePlan = namedtuple("PagePlan", "cu_seqlens_q kv_lens positions slots free_head shortfall")
 
 
-@_on_device_of(0)
-def page_plan(past_lens, new_lens, page_table, free_pages, free_head, page_size: int, max_rows: int,
-              *, n_pages: int = 0, free_head_out=None, cu_seqlens_q=None, kv_lens=None,
-              positions=None, slots=None, shortfall=None, stream=None) -> PagePlan:
-    """Page tables and slot maps of a step from its requests' lengths (qsa_page_plan).
-
-    past_lens, new_lens [n_requests] int32; page_table [n_requests, pages_per_req] int32 is
-    updated in place with pages taken from free_pages [n_free] int32, of which free_head [1] int32
-    are taken already; free_head_out = free_head updates it in place (None = a new tensor).
-    Returns cu_seqlens_q [n_requests + 1], kv_lens [n_requests], positions and slots [max_rows] (-1 on
-    rows past the last request), free_head [1] and shortfall [1], all int32."""
-    import torch
-    i32, dev = torch.int32, past_lens.device
-    max_rows = int(max_rows)
-    if max_rows < 0:
-        raise ValueError("max_rows must not be negative")
-    n, one = past_lens.shape[0], (1,)
-    ppr, n_free = page_table.shape[-1], free_pages.shape[0]
-    _tensor(past_lens, i32, "past_lens", (n,), dev)
-    _tensor(new_lens, i32, "new_lens", (n,), dev)
-    _tensor(page_table, i32, "page_table", (n, ppr), dev)
-    _tensor(free_pages, i32, "free_pages", (n_free,), dev)
-    _tensor(free_head, i32, "free_head", one, dev)
-    on = _launch_stream(dev, stream)
-    if cu_seqlens_q is None and kv_lens is None and positions is None and slots is None and shortfall is None:
-        # one allocation; positions and slots each on a 16-byte boundary
-        pad = -max_rows % 4
-        block = torch.empty(2 * (max_rows + pad) + 2 * n + 3, dtype=i32, device=dev)
-        _record(stream, dev, (block,))
-        positions, _, slots, _, cu_seqlens_q, kv_lens, shortfall, head = block.split_with_sizes(
-            (max_rows, pad, max_rows, pad, n + 1, n, 1, 1))
-        if free_head_out is None:
-            free_head_out = head
-        else:
-            _tensor(free_head_out, i32, "free_head_out", one, dev)
-    else:
-        made = []
-
-        def out(t, name, m):
-            if t is None:
-                t = torch.empty(m, dtype=i32, device=dev)
-                made.append(t)
-            else:
-                _tensor(t, i32, name, (m,), dev)
-            return t
-        cu_seqlens_q, kv_lens = out(cu_seqlens_q, "cu_seqlens_q", n + 1), out(kv_lens, "kv_lens", n)
-        positions, slots = out(positions, "positions", max_rows), out(slots, "slots", max_rows)
-        shortfall, free_head_out = out(shortfall, "shortfall", 1), out(free_head_out, "free_head_out", 1)
-        _record(stream, dev, made)
-    st = load_library().qsa_page_plan(
-        past_lens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(), free_pages.data_ptr(), n_free,
-        free_head.data_ptr(), free_head_out.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
-        positions.data_ptr(), slots.data_ptr(), shortfall.data_ptr(), n, ppr, page_size, n_pages, max_rows, on)
-    if st:
-        _check(st, "qsa_page_plan")
-    return PagePlan(cu_seqlens_q, kv_lens, positions, slots, free_head_out, shortfall)
+def __getattr__(name):
+    if name not in SERVING:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import torch  # noqa: F401  (its libraries come before the extension's)
+    load_library()
+    try:
+        from . import _serving
+    except ImportError as e:
+        raise RuntimeError("the _serving extension is not built; run __graft_entry__.build() or "
+                           "python -m top_sparse_attention_row_gb300.build") from e
+    _serving.set_plan_type(PagePlan)
+    for n in SERVING:
+        globals()[n] = getattr(_serving, n)
+    return globals()[name]
 
 
 class RopeTable:
@@ -739,24 +623,14 @@ class RopeTable:
     def __init__(self, rot_dim: int, steps, magnitude: float):
         self.rot_dim, self.magnitude = int(rot_dim), float(magnitude)
         self._steps = (ctypes.c_uint64 * max(1, self.rot_dim // 2))(*steps)
-        self._specs = {}
+        # what the extension reads: the address of the steps (which live as long as this table), their part
+        # of the head and the magnitude
+        self._raw = (ctypes.addressof(self._steps), self.rot_dim, self.magnitude)
 
     @property
     def steps(self):
         """Turns per token of every pair, in units of 2^-64."""
         return list(self._steps)[:self.rot_dim // 2]
-
-    def spec(self, layout: str, rot_offset: int, transpose: bool = False):
-        """The argument of the C entries (a reference to a qsa_rope_spec that this table keeps)."""
-        key = (layout, rot_offset, transpose)
-        got = self._specs.get(key)
-        if got is None:
-            if layout not in ROPE_LAYOUTS:
-                raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
-            spec = RopeSpec(ctypes.addressof(self._steps), self.rot_dim, int(rot_offset),
-                            ROPE_LAYOUTS[layout], 1 if transpose else 0, self.magnitude)
-            got = self._specs[key] = ctypes.byref(spec)
-        return got
 
 
 def rope_table(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
@@ -777,225 +651,9 @@ def rope_table(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", fa
     return RopeTable(rot_dim, steps, own.value if magnitude is None else magnitude)
 
 
-@_on_device_of(0)
-def rope(x, positions, table: RopeTable, *, layout: str = "half", rot_offset: int = 0,
-         transpose: bool = False, out=None, stream=None):
-    """Rotates x [R, H, D] (bf16 or fp16, contiguous heads) to positions [R] int32 (qsa_rope).
-
-    transpose=True applies the transposed rotation, which takes the output's gradient to the
-    input's.  Rows with a negative position are not written.  out may be x."""
-    import torch
-    shape = R, H, D = x.shape
-    dev, dt = x.device, x.dtype
-    code = _dtype_code(dt, "x")
-    xs = _rows(x, dt, "x", shape, dev)
-    _tensor(positions, torch.int32, "positions", (R,), dev)
-    on = _launch_stream(dev, stream)
-    if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
-        _record(stream, dev, (out,))
-    os_ = _rows(out, dt, "out", shape, dev)
-    if R == 0:
-        return out              # (an empty tensor has no address)
-    st = load_library().qsa_rope(x.data_ptr(), out.data_ptr(), positions.data_ptr(),
-                                 table.spec(layout, rot_offset, transpose), R, H, D, xs, os_, code, on)
-    if st:
-        _check(st, "qsa_rope")
-    return out
-
-
-def _append_args(q, k, v, positions, slots, table, layout, rot_offset, q_out, stream):
-    import torch
-    shape = R, Hkv, D = k.shape
-    dev, dt = k.device, k.dtype
-    ks = _rows(k, dt, "k", shape, dev)
-    vs = 0 if v is None else _rows(v, dt, "v", shape, dev)
-    _tensor(slots, torch.int32, "slots", (R,), dev)
-    if positions is not None:
-        _tensor(positions, torch.int32, "positions", (R,), dev)
-    elif table is not None:
-        raise ValueError("positions are needed with a rope table")
-    Hq = qs = qos = 0
-    if q is not None:
-        Hq = q.shape[1]
-        qs = _rows(q, dt, "q", (R, Hq, D), dev)
-        if q_out is None:
-            q_out = torch.empty((R, Hq, D), dtype=dt, device=dev)
-            _record(stream, dev, (q_out,))
-        qos = _rows(q_out, dt, "q_out", (R, Hq, D), dev)
-    spec = None if table is None else table.spec(layout, rot_offset)
-    return R, Hq, Hkv, D, qs, qos, ks, vs, q_out, spec
-
-
-@_on_device_of(1)
-def rope_append(q, k, v, k_cache, v_cache, positions, slots, table: Optional[RopeTable], *,
-                layout: str = "half", rot_offset: int = 0, q_out=None, stream=None):
-    """Rotates q into q_out and k into the cache, and copies v into the cache (qsa_rope_append).
-
-    q [R, Hq, D] or None, k, v [R, Hkv, D] (bf16 or fp16, contiguous heads, any row stride); k_cache,
-    v_cache [n_slots, Hkv, D]; v and v_cache None for a cache of latent rows.  positions, slots [R]
-    int32: rows with a negative position are left out, rows with a slot outside the cache write no
-    cache row.  table None: nothing turns.  Returns q_out (a new tensor unless given; may be q)."""
-    dev, dt = k.device, k.dtype
-    code = _dtype_code(dt, "k")
-    if (v is None) != (v_cache is None):
-        raise ValueError("v and v_cache come together")
-    on = _launch_stream(dev, stream)
-    R, Hq, Hkv, D, qs, qos, ks, vs, q_out, spec = _append_args(
-        q, k, v, positions, slots, table, layout, rot_offset, q_out, stream)
-    S = k_cache.shape[0]
-    _tensor(k_cache, dt, "k_cache", (S, Hkv, D), dev)
-    if v_cache is not None:
-        _tensor(v_cache, dt, "v_cache", (S, Hkv, D), dev)
-    if R == 0:
-        return q_out
-    st = load_library().qsa_rope_append(
-        _ptr(q), _ptr(q_out), k.data_ptr(), _ptr(v), k_cache.data_ptr(), _ptr(v_cache), _ptr(positions),
-        slots.data_ptr(), spec, R, S, Hq, Hkv, D, qs, qos, ks, vs, code, on)
-    if st:
-        _check(st, "qsa_rope_append")
-    return q_out
-
-
-@_on_device_of(1)
-def rope_append_fp4(q, k, v, k_cache, k_scale, v_cache, v_scale, positions, slots,
-                    table: Optional[RopeTable], *, k_global: float = 1.0, v_global: float = 1.0,
-                    layout: str = "half", rot_offset: int = 0, q_out=None, k_seen=None, v_seen=None,
-                    stream=None):
-    """rope_append into a cache held in 4 bits (qsa_rope_append_fp4): k_cache, v_cache [n_slots, Hkv,
-    D / 2] uint8 e2m1 pairs, k_scale, v_scale [n_slots, Hkv, D / 16] uint8 e4m3 block scales, k_global,
-    v_global the caches' fp32 scales.  k_seen, v_seen [R, Hkv, D] (optional) receive the values that the
-    cache now holds.  Returns q_out."""
-    import torch
-    dev, dt = k.device, k.dtype
-    code = _dtype_code(dt, "k")
-    on = _launch_stream(dev, stream)
-    R, Hq, Hkv, D, qs, qos, ks, vs, q_out, spec = _append_args(
-        q, k, v, positions, slots, table, layout, rot_offset, q_out, stream)
-    S, u8 = k_cache.shape[0], torch.uint8
-    codes, scales = (S, Hkv, D // 2), (S, Hkv, D // 16)
-    _tensor(k_cache, u8, "k_cache", codes, dev)
-    _tensor(v_cache, u8, "v_cache", codes, dev)
-    _tensor(k_scale, u8, "k_scale", scales, dev)
-    _tensor(v_scale, u8, "v_scale", scales, dev)
-    if k_seen is not None:
-        _tensor(k_seen, dt, "k_seen", (R, Hkv, D), dev)
-    if v_seen is not None:
-        _tensor(v_seen, dt, "v_seen", (R, Hkv, D), dev)
-    if R == 0:
-        return q_out
-    st = load_library().qsa_rope_append_fp4(
-        _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), k_scale.data_ptr(),
-        v_cache.data_ptr(), v_scale.data_ptr(), k_global, v_global, _ptr(k_seen), _ptr(v_seen),
-        _ptr(positions), slots.data_ptr(), spec, R, S, Hq, Hkv, D, qs, qos, ks, vs, code, on)
-    if st:
-        _check(st, "qsa_rope_append_fp4")
-    return q_out
-
-
-@functools.lru_cache(maxsize=1024)
 def window_workspace_bytes(n_rows: int, n_requests: int, pages_per_req: int, page_size: int, n_qheads: int,
                            n_kvheads: int, head_dim: int, window: int, n_sink: int, num_sms: int = 0) -> int:
     """Bytes of workspace of a window-attention call (qsa_window_workspace_bytes); 0 = no split.
     num_sms 0 asks the current device."""
     return int(load_library().qsa_window_workspace_bytes(n_rows, n_requests, pages_per_req, page_size, n_qheads,
                                                          n_kvheads, head_dim, window, n_sink, num_sms))
-
-
-def _window_args(q, k_rows, cu_seqlens_q, kv_lens, page_table, page_size, window, n_sink, out, lse,
-                 want_lse, workspace, stream):
-    import torch
-    qshape = R, Hq, D = q.shape
-    dev, dt, i32 = q.device, q.dtype, torch.int32
-    n, ppr = page_table.shape
-    S, Hkv = k_rows.shape[0], k_rows.shape[1]
-    _tensor(q, dt, "q", qshape, dev)
-    _tensor(page_table, i32, "page_table", (n, ppr), dev)
-    _tensor(cu_seqlens_q, i32, "cu_seqlens_q", (n + 1,), dev)
-    _tensor(kv_lens, i32, "kv_lens", (n,), dev)
-    if page_size < 1 or S % page_size:
-        raise ValueError(f"the caches' {S} slots are not whole pages of {page_size}")
-    if out is None:
-        out = torch.empty_like(q)
-        _record(stream, dev, (out,))
-    else:
-        _tensor(out, dt, "out", qshape, dev)
-    if lse is None:
-        if want_lse:
-            lse = torch.empty((R, Hq), dtype=torch.float32, device=dev)
-            _record(stream, dev, (lse,))
-    else:
-        _tensor(lse, torch.float32, "lse", (R, Hq), dev)
-    ws_bytes = 0
-    if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous and on {dev}")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    elif R:
-        ws_bytes = window_workspace_bytes(R, n, ppr, page_size, Hq, Hkv, D, window, n_sink)
-        if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-            _record(stream, dev, (workspace,))
-    return out, lse, workspace, ws_bytes, (R, n, ppr, page_size, S // page_size, Hq, Hkv, D)
-
-
-@_on_device_of(0)
-def window_attention_paged(q, k_cache, v_cache, cu_seqlens_q, kv_lens, page_table, page_size: int,
-                           scale: float, *, window: int = 0, n_sink: int = 0, out=None, lse=None,
-                           want_lse: bool = True, workspace=None, stream=None):
-    """Sliding-window attention with sink tokens over a paged cache (qsa_window_attention_paged).
-
-    q [R, Hq, D] bf16 or fp16 (D 64, 128 or 256); k_cache, v_cache [n_pages * page_size, Hkv, D] of the
-    same type; cu_seqlens_q [n_requests + 1], kv_lens [n_requests], page_table [n_requests,
-    pages_per_req] int32.  A row at position p sees the positions up to p that are among the last
-    `window` (0 = all) or the first n_sink.  Rows behind the last request are left as they were (in an
-    `out` that is not given: uninitialised).  Returns out [R, Hq, D] and lse [R, Hq] fp32 (None unless
-    wanted)."""
-    dt, dev = q.dtype, q.device
-    code = _dtype_code(dt, "q")
-    on = _launch_stream(dev, stream)
-    out, lse, ws, ws_bytes, shape = _window_args(q, k_cache, cu_seqlens_q, kv_lens, page_table, page_size,
-                                                 window, n_sink, out, lse, want_lse, workspace, stream)
-    rows = (k_cache.shape[0], shape[6], shape[7])
-    _tensor(k_cache, dt, "k_cache", rows, dev)
-    _tensor(v_cache, dt, "v_cache", rows, dev)
-    if shape[0] == 0:
-        return out, lse
-    st = load_library().qsa_window_attention_paged(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
-        page_table.data_ptr(), out.data_ptr(), _ptr(lse), *shape, scale, window, n_sink, code, _ptr(ws),
-        ws_bytes, on)
-    if st:
-        _check(st, "qsa_window_attention_paged")
-    return out, lse
-
-
-@_on_device_of(0)
-def window_attention_fp4_paged(q, k_cache, k_scale, v_cache, v_scale, cu_seqlens_q, kv_lens, page_table,
-                               page_size: int, scale: float, *, k_global: float = 1.0,
-                               v_global: float = 1.0, window: int = 0, n_sink: int = 0, out=None,
-                               lse=None, want_lse: bool = True, workspace=None, stream=None):
-    """window_attention_paged over a cache held in 4 bits, as rope_append_fp4 writes it
-    (qsa_window_attention_fp4_paged): k_cache, v_cache [n_pages * page_size, Hkv, D / 2] uint8, k_scale,
-    v_scale [n_pages * page_size, Hkv, D / 16] uint8, k_global, v_global the caches' fp32 scales."""
-    import torch
-    dev, u8 = q.device, torch.uint8
-    code = _dtype_code(q.dtype, "q")
-    on = _launch_stream(dev, stream)
-    out, lse, ws, ws_bytes, shape = _window_args(q, k_cache, cu_seqlens_q, kv_lens, page_table, page_size,
-                                                 window, n_sink, out, lse, want_lse, workspace, stream)
-    S, Hkv, D = k_cache.shape[0], shape[6], shape[7]
-    codes, scales = (S, Hkv, D // 2), (S, Hkv, D // 16)
-    _tensor(k_cache, u8, "k_cache", codes, dev)
-    _tensor(v_cache, u8, "v_cache", codes, dev)
-    _tensor(k_scale, u8, "k_scale", scales, dev)
-    _tensor(v_scale, u8, "v_scale", scales, dev)
-    if shape[0] == 0:
-        return out, lse
-    st = load_library().qsa_window_attention_fp4_paged(
-        q.data_ptr(), k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(), k_global,
-        v_global, cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), out.data_ptr(), _ptr(lse),
-        *shape, scale, window, n_sink, code, _ptr(ws), ws_bytes, on)
-    if st:
-        _check(st, "qsa_window_attention_fp4_paged")
-    return out, lse

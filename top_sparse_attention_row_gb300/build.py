@@ -1,4 +1,5 @@
-"""Builds libqsa.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Builds libqsa.so (the C-ABI library) in-tree with nvcc for sm_103a, and the Python extension
+_serving (argument checks of the serving-step calls, csrc/torch_serving.cpp) with the host compiler.
 
 Usage: ``python -m top_sparse_attention_row_gb300.build`` or ``build()`` from Python.
 Translation units compile in parallel; objects go to ``_build/`` next to this file.
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,9 @@ LIB = os.path.join(PKG, "libqsa.so")
 SOURCES = ["prefill.cu", "mla.cu", "union.cu", "api.cpp", "noalloc.cu", "probe.cu", "pages.cu",
            "serving.cpp", "plan.cu", "rope.cu", "window.cu", "window_d64.cu", "window_d128.cu",
            "window_d256.cu"]
+
+EXT_SOURCE = "torch_serving.cpp"
+EXT = os.path.join(PKG, "_serving" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
@@ -44,16 +49,46 @@ def _compile(nvcc: str, src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _compile_extension() -> str:
+    """The extension's object file; it is linked against libqsa.so once that is there."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    obj = os.path.join(BUILD, "torch_serving.o")
+    abi = int(getattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", True))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           "-I", os.path.join(ROOT, "include"), "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {EXT_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_extension(obj: str):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = EXT + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", PKG, "-lqsa", "-L", lib, "-ltorch_python",
+           "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of {os.path.basename(EXT)} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+
+
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    srcs = [os.path.join(CSRC, s) for s in SOURCES] + [
+    srcs = [os.path.join(CSRC, s) for s in SOURCES + [EXT_SOURCE]] + [
         os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".h", ".cuh"))
     ] + [os.path.join(ROOT, "include", "qsa.h")]
-    if (not force and os.path.exists(LIB)
-            and os.path.getmtime(LIB) >= max(os.path.getmtime(s) for s in srcs)):
+    newest = max(os.path.getmtime(s) for s in srcs)
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, EXT)):
         return LIB
     nvcc = _nvcc()
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ext_obj = ex.submit(_compile_extension)
         objs = list(ex.map(lambda s: _compile(nvcc, s, verbose_ptxas), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lrt", "-ldl", "-lpthread"]
@@ -61,6 +96,7 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_extension(ext_obj.result())
     return LIB
 
 
