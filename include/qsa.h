@@ -408,7 +408,7 @@ qsa_status qsa_rope_append_fp4(const void* q, void* q_out, const void* k, const 
  * does not matter, NaN and infinities included.  A non-finite value that a row sees makes that row's
  * output non-finite, and may do so to the rows of up to 127 neighbouring (token, head) pairs of the same request and
  * KV head.
- *   scale > 0.  head_dim 64, 128 or 256; n_qheads / n_kvheads <= 128.
+ *   scale > 0.  head_dim 64, 128 or 256; n_qheads / n_kvheads <= 128 (4-bit caches of 256 dims: <= 64).
  *   workspace: calls with few rows split the keys over the SMs and join the parts; they need
  *       qsa_window_workspace_bytes (for the device's SM count; 0 = no split), 256-byte aligned.  NULL: taken from
  *       the library's pool on `stream`.  Calls that overlap need a workspace each.
@@ -438,10 +438,12 @@ qsa_status qsa_window_attention_fp4_paged(const void* q, const void* k_cache, co
                                           float scale, int32_t window, int32_t n_sink, int32_t dtype,
                                           void* workspace, size_t workspace_bytes, void* stream);
 
-/* Host only: bytes of workspace of a window-attention call (num_sms <= 0 asks the current device). */
+/* Host only: bytes of workspace of a window-attention call (fp4 1 for a 4-bit cache; num_sms <= 0 asks the
+ * current device). */
 size_t qsa_window_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t pages_per_req,
                                   int32_t page_size, int32_t n_qheads, int32_t n_kvheads,
-                                  int32_t head_dim, int32_t window, int32_t n_sink, int32_t num_sms);
+                                  int32_t head_dim, int32_t window, int32_t n_sink, int32_t fp4,
+                                  int32_t num_sms);
 
 /* Allocation-free variant of qsa_sparse_prefill (same arguments, same results).  The pages
  * have no counterpart: it exists for callers that must not allocate device memory -- code

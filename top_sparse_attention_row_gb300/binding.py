@@ -136,7 +136,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qsa_window_attention_paged.restype = ctypes.c_int
     lib.qsa_window_attention_fp4_paged.argtypes = [vp] * 5 + [f32, f32] + [vp] * 5 + shape
     lib.qsa_window_attention_fp4_paged.restype = ctypes.c_int
-    lib.qsa_window_workspace_bytes.argtypes = [i64] + [i32] * 9
+    lib.qsa_window_workspace_bytes.argtypes = [i64] + [i32] * 10
     lib.qsa_window_workspace_bytes.restype = sz
     for name in ("qsa_union_workspace_bytes", "qsa_workspace_bytes"):
         getattr(lib, name).argtypes = [i64, i32, i32]
@@ -652,8 +652,9 @@ def rope_table(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", fa
 
 
 def window_workspace_bytes(n_rows: int, n_requests: int, pages_per_req: int, page_size: int, n_qheads: int,
-                           n_kvheads: int, head_dim: int, window: int, n_sink: int, num_sms: int = 0) -> int:
+                           n_kvheads: int, head_dim: int, window: int, n_sink: int, *, fp4: bool = False,
+                           num_sms: int = 0) -> int:
     """Bytes of workspace of a window-attention call (qsa_window_workspace_bytes); 0 = no split.
-    num_sms 0 asks the current device."""
+    fp4: a 4-bit cache; num_sms 0 asks the current device."""
     return int(load_library().qsa_window_workspace_bytes(n_rows, n_requests, pages_per_req, page_size, n_qheads,
-                                                         n_kvheads, head_dim, window, n_sink, num_sms))
+                                                         n_kvheads, head_dim, window, n_sink, int(fp4), num_sms))

@@ -342,6 +342,7 @@ struct WindowParams {
   int32_t splits;
   int32_t window;               // 0 = none
   int32_t n_sink;
+  int32_t out_32;               // out is 32-byte aligned
   int32_t box;                  // keys per TMA box (8 .. 64), or 0: gathers of four rows
   int32_t n_slots;              // n_pages * page_size
   int32_t stall_first_item;     // failure-detection test: the scheduler withholds its records

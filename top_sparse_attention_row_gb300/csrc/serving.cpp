@@ -95,10 +95,10 @@ struct WindowPlan {
   int64_t n_units;
 };
 constexpr int32_t kMaxSplits = 128;
-WindowPlan plan_window(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, int32_t group,
+WindowPlan plan_window(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, int32_t group, int32_t tile_rows,
                        int64_t max_keys, int32_t window, int32_t n_sink, int32_t sms) {
   WindowPlan w{};
-  w.tile_tokens = qsa::kWinTile / group;
+  w.tile_tokens = tile_rows / group;
   w.n_tiles = static_cast<int32_t>(n_rows / w.tile_tokens + n_requests);
   // units with rows: every request has at most one partial tile
   int64_t tiles = (n_rows + w.tile_tokens - 1) / w.tile_tokens + n_requests - 1;
@@ -127,6 +127,9 @@ WindowPlan plan_window(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, in
   return w;
 }
 
+// Rows of the query tile (WinCfg::kRows of the kernels).
+int32_t window_tile_rows(int32_t head_dim, bool fp4) { return fp4 && head_dim == 256 ? 64 : qsa::kWinTile; }
+
 // Partial outputs and log-sum-exps of a split call.
 size_t window_ws_bytes(int64_t n_rows, int32_t n_qheads, int32_t head_dim, int32_t splits) {
   if (splits <= 1) return 0;
@@ -142,12 +145,12 @@ struct Fp4Cache {
 
 qsa_status check_window(int64_t n_rows, int32_t n_requests, int32_t pages_per_req, int32_t page_size,
                         int64_t n_pages, int32_t n_qheads, int32_t n_kvheads, int32_t head_dim,
-                        int32_t window, int32_t n_sink) {
+                        int32_t window, int32_t n_sink, bool fp4) {
   if (n_rows < 0 || n_requests < 1 || pages_per_req < 1 || page_size < 1 || n_pages < 1 || n_qheads < 1 ||
       n_kvheads < 1 || n_qheads % n_kvheads != 0 || window < 0 || n_sink < 0)
     return QSA_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return QSA_ERR_UNSUPPORTED;
-  if (n_qheads / n_kvheads > qsa::kWinTile) return QSA_ERR_UNSUPPORTED;
+  if (n_qheads / n_kvheads > window_tile_rows(head_dim, fp4)) return QSA_ERR_UNSUPPORTED;
   if (n_rows + n_requests >= INT32_MAX) return QSA_ERR_UNSUPPORTED;
   if (n_pages > INT32_MAX / page_size || n_pages * page_size > (INT32_MAX - 1) / n_kvheads)
     return QSA_ERR_UNSUPPORTED;
@@ -168,7 +171,7 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   if (!std::isfinite(scale) || !(scale > 0.0f) || (dtype != QSA_BF16 && dtype != QSA_FP16))
     return QSA_ERR_INVALID_ARG;
   qsa_status st = check_window(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads,
-                               head_dim, window, n_sink);
+                               head_dim, window, n_sink, fp4 != nullptr);
   if (st != QSA_OK) return st;
   if (n_rows == 0) return QSA_OK;
   int32_t sms = 0;
@@ -176,7 +179,7 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   if (st != QSA_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
   const int32_t group = n_qheads / n_kvheads;
-  const WindowPlan w = plan_window(n_rows, n_requests, n_kvheads, group,
+  const WindowPlan w = plan_window(n_rows, n_requests, n_kvheads, group, window_tile_rows(head_dim, fp4 != nullptr),
                                    static_cast<int64_t>(pages_per_req) * page_size, window, n_sink, sms);
   if (w.n_units > INT32_MAX) return QSA_ERR_UNSUPPORTED;
   qsa::WindowParams p{};
@@ -200,6 +203,7 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   p.tile_tokens = w.tile_tokens;
   p.n_tiles = w.n_tiles;
   p.splits = w.splits;
+  p.out_32 = aligned_to(out, 32);
   p.window = window;
   p.n_sink = n_sink;
   int32_t box = 1;      // keys per copy: the largest power of two <= 64 that divides the page size
@@ -251,12 +255,13 @@ extern "C" {
 
 size_t qsa_window_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t pages_per_req,
                                   int32_t page_size, int32_t n_qheads, int32_t n_kvheads,
-                                  int32_t head_dim, int32_t window, int32_t n_sink, int32_t num_sms) {
+                                  int32_t head_dim, int32_t window, int32_t n_sink, int32_t fp4,
+                                  int32_t num_sms) {
   if (check_window(n_rows, n_requests, pages_per_req, page_size, 1, n_qheads, n_kvheads, head_dim, window,
-                   n_sink) != QSA_OK || n_rows == 0)
+                   n_sink, fp4 != 0) != QSA_OK || n_rows == 0)
     return 0;
   if (num_sms <= 0 && qsa::device_sms(&num_sms) != QSA_OK) return 0;
-  const WindowPlan w = plan_window(n_rows, n_requests, n_kvheads, n_qheads / n_kvheads,
+  const WindowPlan w = plan_window(n_rows, n_requests, n_kvheads, n_qheads / n_kvheads, window_tile_rows(head_dim, fp4 != 0),
                                    static_cast<int64_t>(pages_per_req) * page_size, window, n_sink, num_sms);
   return window_ws_bytes(n_rows, n_qheads, head_dim, w.splits);
 }

@@ -410,7 +410,7 @@ PyObject* window(PyObject* args, PyObject* kw, bool fp4) {
         fail(PyExc_ValueError, "workspace must be contiguous and on " + dev.str());
       ws_bytes = ws.nbytes();
     } else if (R > 0) {
-      ws_bytes = qsa_window_workspace_bytes(R, nr, pr, ps, hq, hkv, dim, w, k, 0);
+      ws_bytes = qsa_window_workspace_bytes(R, nr, pr, ps, hq, hkv, dim, w, k, fp4 ? 1 : 0, 0);
       if (ws_bytes > 0) ws = on.empty({static_cast<int64_t>(ws_bytes)}, at::kByte);
     }
     if (R > 0) {

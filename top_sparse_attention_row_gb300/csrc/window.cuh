@@ -58,12 +58,22 @@ struct WinCfg {
   static constexpr int kNBS = kStageDims / 64;             // 64-dim blocks of a stage
   static constexpr int kSPT = D / kStageDims;              // stages of a K or V tile (one ring entry)
   static constexpr int kStageBytes = kWinTile * kStageDims * 2;
-  static constexpr int kQBytes = kWinTile * D * 2;
-  static constexpr int kStages = FP4 ? (D == 256 ? 3 : D == 128 ? 4 : 6) : (D == 256 ? 5 : D == 128 ? 6 : 12);
+  // Rows of the query tile.  A 4-bit cache of 256 dims keeps 64: the other half of the tile's shared memory
+  // holds a fourth ring stage and the copies ahead (the MMA's rows 64-127 then read other staged data, and
+  // are not used).
+  static constexpr int kRows = FP4 && D == 256 ? 64 : kWinTile;
+  static constexpr int kQBlock = kRows * 128;              // bytes of a 64-dim block of the query tile
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kStages = FP4 ? (D == 64 ? 6 : 4) : (D == 256 ? 5 : D == 128 ? 6 : 12);
   static constexpr int kEntryBars = 16;                    // > entries in flight
   static constexpr int kRecords = FP4 ? 8 : 4;
   static constexpr int kBadSlots = FP4 ? 16 : 8;           // > tiles the producers may be ahead
   static constexpr int kThreads = FP4 ? 640 : 512;
+  // registers per thread at launch, and after the split: softmax warpgroups, MMA and scheduler, producers
+  static constexpr int kLaunchRegs = FP4 ? 96 : 128;
+  static constexpr int kSoftmaxRegs = FP4 ? 128 : 168, kUtilRegs = FP4 ? 64 : 88, kProducerRegs = FP4 ? 80 : 88;
+  static_assert(256 * kSoftmaxRegs + 128 * kUtilRegs + (kThreads - 384) * kProducerRegs <= kThreads * kLaunchRegs,
+                "register split within the launch's registers");
   static constexpr int kProducers = FP4 ? 8 : 4;
   static constexpr int kQWarps = FP4 ? 3 : 1;              // warps that write the query tile
   static constexpr int kDepth = D == 256 ? 3 : D == 128 ? 6 : 8;   // 4-bit entries in flight per warp
@@ -73,15 +83,17 @@ struct WinCfg {
   static constexpr int kStagingAt = kRing + kStages * kStageBytes;
   static constexpr int kMaxAt = kStagingAt + (FP4 ? 8 * kDepth * kStaging : 0);   // [2][2][128] float
   static constexpr int kBadAt = kMaxAt + 2048;             // [kBadSlots][8] uint32
-  static constexpr int kRecAt = kBadAt + kBadSlots * 32;   // [kRecords][16] int32
+  static constexpr int kRecAt = kBadAt + kBadSlots * 32;   // [kRecords] Unit
   static constexpr int kBarAt = kRecAt + kRecords * 64;
-  // full[kStages], entry[16], sfull[2], pfull[2], pvdone[2], qfull, qempty, ofree, fin, next, recfull/empty
-  static constexpr int kBars = kStages + kEntryBars + 11 + 2 * kRecords;
+  static constexpr int kFixBars = 8;                       // > V tiles that may be zeroed ahead of the MMA
+  // landed[16], done[16] (by entry), pfull[2], qfull, qempty, ofree, fin, next, vready[8], recfull/empty
+  static constexpr int kBars = 2 * kEntryBars + 7 + kFixBars + 2 * kRecords;
   static constexpr int kNextAt = (kBarAt + 8 * kBars + 15) / 16 * 16;   // answer of the launch control
   static constexpr int kTmemSlot = kNextAt + 16;
   static constexpr int kSmem = kTmemSlot + 16;
   static_assert(kSmem <= kSmemLimit, "shared memory");
   static_assert(kStages / kSPT + 2 < kEntryBars, "entry barriers");
+  static_assert(kStages / kSPT / 2 + 1 < kFixBars, "zeroing barriers");
 };
 
 namespace window_detail {
@@ -90,8 +102,8 @@ constexpr unsigned long long kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
 constexpr float kRaise = 8.0f;          // log2 units by which a tile may exceed the running maximum
 constexpr float kLn2f = 0.6931471805599453f;
 enum Site : int32_t {
-  kWRecEmpty = 0x41, kWRecFull, kWQEmpty, kWQFull, kWStageEmpty, kWStageFull, kWSFull, kWPFull, kWPvDone,
-  kWOFree, kWNext, kWDrain
+  kWRecEmpty = 0x41, kWRecFull, kWQEmpty, kWQFull, kWStageEmpty, kWLanded, kWSFull, kWPFull, kWPvDone,
+  kWOFree, kWNext, kWVReady, kWDrain
 };
 
 __device__ __forceinline__ unsigned long long now_ns() {
@@ -134,17 +146,20 @@ struct Unit {
   int32_t p_first;     // position of the first token
   int32_t s0, shift;   // virtual index v: position v below s0, v + shift from s0 on
   int32_t lo, hi;      // positions some row sees: [lo, hi) and those below n_sink and hi
-  int32_t pad[4];
+  // tiles of this unit, counted from tile0: [some0, some1) have only keys that some row sees, [all0, all1) only
+  // keys that every row sees (the sinks' tiles count as neither)
+  int32_t some0, some1, all0, all1;
 };
 static_assert(sizeof(Unit) == 64, "unit record");
 
 __device__ __forceinline__ Unit load_unit(const Unit* u) {
   Unit r;
   const int4* s = reinterpret_cast<const int4*>(u);
-  int4 a = s[0], b = s[1], c = s[2];
+  const int4 a = s[0], b = s[1], c = s[2], d = s[3];
   r.tiles = a.x; r.tile0 = a.y; r.req = a.z; r.kvh = a.w;
   r.split = b.x; r.row0 = b.y; r.tokens = b.z; r.p_first = b.w;
   r.s0 = c.x; r.shift = c.y; r.lo = c.z; r.hi = c.w;
+  r.some0 = d.x; r.some1 = d.y; r.all0 = d.z; r.all1 = d.w;
   return r;
 }
 
@@ -213,6 +228,16 @@ __device__ __forceinline__ Unit make_unit(const WindowParams& p, uint32_t n, int
   u.shift = static_cast<int32_t>(shift);
   u.lo = static_cast<int32_t>(lo);
   u.hi = static_cast<int32_t>(hi > 0 ? hi : 0);
+  // the window's run is v >= s0, positions from lo (every row: from the last row's) to hi (the first row's)
+  const int64_t p_last = p_first + u.tokens - 1;
+  int64_t lo_last = p.window > 0 ? p_last - p.window + 1 : 0;
+  if (lo_last < lo) lo_last = lo;
+  const int64_t run0 = lo - u.shift > s0 ? lo - u.shift : u.s0, all_from = lo_last - u.shift > run0 ? lo_last - u.shift : run0;
+  const int64_t all_to = (p_first + 1 < hi ? p_first + 1 : hi) - u.shift;
+  u.some0 = static_cast<int32_t>((run0 + kWinTile - 1) / kWinTile - a);
+  u.some1 = static_cast<int32_t>((u.hi - u.shift) / kWinTile - a);
+  u.all0 = static_cast<int32_t>((all_from + kWinTile - 1) / kWinTile - a);
+  u.all1 = static_cast<int32_t>((all_to > 0 ? all_to : 0) / kWinTile - a);
   return u;
 }
 
@@ -221,6 +246,9 @@ __device__ __forceinline__ bool seen(const WindowParams& p, const Unit& u, int32
   return pos < u.hi && (pos >= u.lo || pos < p.n_sink);
 }
 
+// The ring entries of tile j of a unit with nt tiles.
+__device__ __forceinline__ uint32_t k_entry(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ uint32_t v_entry(int j, int nt) { return j == nt - 1 ? 2 * j + 1 : 2 * j + 2; }
 // Ring entry e of a unit with nt tiles (K0 K1 V0 K2 V1 ... V(nt-1)): its tile, and whether it is V.
 __device__ __forceinline__ void entry_of(int e, int nt, int& tile, bool& is_v) {
   if (e == 0) {
@@ -252,6 +280,12 @@ __device__ __forceinline__ uint32_t bf16x2_as_f16x2(uint32_t v) {
   uint32_t r;
   memcpy(&r, &h, 4);
   return r;
+}
+// One 32-byte store (the address is a multiple of 32).
+__device__ __forceinline__ void st_global_v8(uint32_t* to, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
@@ -317,15 +351,16 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
   using C = WinCfg<D, FP4>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
-  const uint32_t b_full = base + C::kBarAt;
-  const uint32_t b_entry = b_full + 8 * C::kStages;
-  const uint32_t b_sfull = b_entry + 8 * C::kEntryBars;
-  const uint32_t b_pfull = b_sfull + 16;
-  const uint32_t b_pvdone = b_pfull + 16;
-  const uint32_t b_qfull = b_pvdone + 16;
+  // Of ring entry e, at e % kEntryBars: its copies have landed; its MMAs are done (so its stages are free, and
+  // S of a K entry or O up to a V entry can be read).
+  const uint32_t b_landed = base + C::kBarAt;
+  const uint32_t b_done = b_landed + 8 * C::kEntryBars;
+  const uint32_t b_pfull = b_done + 8 * C::kEntryBars;
+  const uint32_t b_qfull = b_pfull + 16;
   const uint32_t b_qempty = b_qfull + 8;
   const uint32_t b_ofree = b_qempty + 8;
-  const uint32_t b_fin = b_ofree + 8;
+  const uint32_t b_vready = b_ofree + 8;
+  const uint32_t b_fin = b_vready + 8 * C::kFixBars;
   const uint32_t b_next = b_fin + 8;
   const uint32_t b_recfull = b_next + 8;
   const uint32_t b_recempty = b_recfull + 8 * C::kRecords;
@@ -342,13 +377,13 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     return;
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) mbar_init(b_full + 8 * s, C::kProducers);
-    for (int e = 0; e < C::kEntryBars; ++e) mbar_init(b_entry + 8 * e, 1);
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(b_sfull + 8 * b, 1);
-      mbar_init(b_pfull + 8 * b, 8);
-      mbar_init(b_pvdone + 8 * b, 1);     // two, by tile parity: S of tile j shows that P.V of j - 2 is done
+    for (int e = 0; e < C::kEntryBars; ++e) {
+      mbar_init(b_landed + 8 * e, FP4 ? C::kProducers : C::kProducers * C::kSPT);
+      mbar_init(b_done + 8 * e, 1);
     }
+    mbar_init(b_pfull, 8);
+    mbar_init(b_pfull + 8, 8);
+    for (int k = 0; k < C::kFixBars; ++k) mbar_init(b_vready + 8 * k, 2);
     mbar_init(b_qfull, C::kQWarps);
     mbar_init(b_qempty, 1);
     mbar_init(b_ofree, 8);
@@ -356,7 +391,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     mbar_init(b_next, 1);
     for (int r = 0; r < C::kRecords; ++r) {
       mbar_init(b_recfull + 8 * r, 1);
-      mbar_init(b_recempty + 8 * r, 8 + 1 + C::kProducers + (C::kQWarps - 1));
+      mbar_init(b_recempty + 8 * r, 8 + 1 + C::kProducers + 2);   // and warps 10 and 11
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -378,6 +413,9 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t tm_o = tmem + 256;           // S buffers: columns 0-127 and 128-255; O: from 256
 
+  auto wait_entry = [&](uint32_t bars, uint32_t e, int32_t site) -> bool {
+    return wait_for(bars + 8 * (e % C::kEntryBars), (e / C::kEntryBars) & 1, abort_flag, status, site);
+  };
   auto finish_role = [&]() {
     tc_fence_before();
     __syncthreads();
@@ -385,7 +423,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax + epilogue
-    if constexpr (FP4) regs_inc<136>();
+    regs_inc<C::kSoftmaxRegs>();
     const int wg = warp >> 2, w = warp & 3, row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
     const float sc = p.scale_log2;
@@ -412,19 +450,13 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         row_lo = INT32_MAX;
         row_sink = 0;
       }
-      const int32_t p_last = u.p_first + u.tokens - 1;
-      const int32_t lo_last = p.window > 0 && p_last >= p.window ? p_last - p.window + 1 : 0;
       float m = -INFINITY, l = 0.0f;
       bool left = false;                      // the pair of warps agreed to leave
       for (int j = 0; j < u.tiles; ++j) {
         const uint32_t jt = js + j, sb = jt & 1;
         const uint32_t tm_s = tmem + lanes + sb * 128 + wg * 64;
         const int32_t v0 = (u.tile0 + j) * kWinTile;
-        const int32_t first = position_of(u, v0), last = position_of(u, v0 + kWinTile - 1);
-        const bool one_run = v0 >= u.s0 || v0 + kWinTile <= u.s0;
-        // every key of the tile seen by some row; by every row
-        const bool whole = one_run && first >= u.lo && last < u.hi;
-        bad |= !wait_for(b_sfull + 8 * sb, (jt >> 1) & 1, abort_flag, status, kWSFull);
+        bad |= !wait_entry(b_done, eb + k_entry(j), kWSFull);
         tc_fence_after();
         const uint32_t* const holes = bad_keys + (jt % C::kBadSlots) * 8;
         const uint4 h0 = *reinterpret_cast<const uint4*>(holes), h1 = *reinterpret_cast<const uint4*>(holes + 4);
@@ -434,34 +466,39 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           tmem_ld32(tm_s, s);
           tmem_ld32(tm_s + 32, s + 32);
           tc_wait_ld();
-          if (!(whole && first >= lo_last && last <= u.p_first)) {
-            const int32_t c0 = v0 + wg * 64;   // this thread's first key
-            // columns [c_lo, c_hi] of the window and those below c_sink
-            const int32_t c_lo = row_lo == INT32_MAX ? INT32_MAX : max(row_lo - u.shift, u.s0) - c0;
-            const int32_t c_hi = pos >= 0 ? min(pos, u.hi - 1) - u.shift - c0 : -1;
-            const int32_t c_sink = min(row_sink, u.hi) - c0;
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (!((c >= c_lo && c <= c_hi) || c < c_sink)) s[c] = -INFINITY;
-          }
-          if (any_hole) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c) {
-              const int key = wg * 64 + c;
-              int word, bit;
-              if constexpr (FP4) {
-                word = key >> 4;
-                bit = key & 15;
-              } else if (p.box > 0) {
-                const int o = key / p.box * C::kNBS;
-                word = (o & 3) * 2;
-                bit = o >> 2;
-              } else {
-                const int o = (key >> 2) * C::kNBS;
-                word = (o & 3) * 2 + ((key & 3) >> 1);
-                bit = (key & 1) * 16 + (o >> 2);
+          if (j < u.all0 || j >= u.all1 || any_hole) {
+            // the keys of this thread's half that its row sees, as bits
+            const int32_t c0 = v0 + wg * 64;
+            const int32_t c_lo = row_lo == INT32_MAX ? 64 : max(max(row_lo - u.shift, u.s0) - c0, 0);
+            const int32_t c_hi = pos >= 0 ? min(min(pos, u.hi - 1) - u.shift - c0, 63) : -1;
+            const int32_t c_sink = min(min(row_sink, u.hi) - c0, 64);
+            uint64_t keep = c_sink >= 64 ? ~0ull : c_sink > 0 ? (1ull << c_sink) - 1 : 0ull;
+            if (c_lo <= c_hi) keep |= (~0ull >> (63 - c_hi)) & (~0ull << c_lo);
+            if (any_hole) {
+#pragma unroll 1
+              for (int c = 0; c < 64; ++c) {
+                const int key = wg * 64 + c;
+                int word, bit;
+                if constexpr (FP4) {
+                  word = key >> 4;
+                  bit = key & 15;
+                } else if (p.box > 0) {
+                  const int o = key / p.box * C::kNBS;
+                  word = (o & 3) * 2;
+                  bit = o >> 2;
+                } else {
+                  const int o = (key >> 2) * C::kNBS;
+                  word = (o & 3) * 2 + ((key & 3) >> 1);
+                  bit = (key & 1) * 16 + (o >> 2);
+                }
+                if ((holes[word] >> bit) & 1) keep &= ~(1ull << c);
               }
-              if ((holes[word] >> bit) & 1) s[c] = -INFINITY;
+            }
+            const uint32_t k0 = static_cast<uint32_t>(keep), k1 = static_cast<uint32_t>(keep >> 32);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              s[c] = k0 & (1u << c) ? s[c] : -INFINITY;
+              s[c + 32] = k1 & (1u << c) ? s[c + 32] : -INFINITY;
             }
           }
           float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
@@ -485,7 +522,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
             const float nm = need ? tile_max : m;
             const float f = m == -INFINITY ? 0.0f : fast_exp2((m - nm) * sc);
             if (j > 0) {
-              bad |= !wait_for(b_pvdone + 8 * (sb ^ 1), ((jt - 1) >> 1) & 1, abort_flag, status, kWPvDone);
+              bad |= !wait_entry(b_done, eb + v_entry(j - 1, u.tiles), kWPvDone);
               tc_fence_after();
               const float g = need ? f : 1.0f;
 #pragma unroll
@@ -526,33 +563,6 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           tmem_st32(tm_s, pk);
           tc_wait_st();
         }
-        if (!FP4 && !whole) {
-          // V rows that no row sees are zeroed before P.V reads them
-          int e;
-          if (u.tiles == 1) e = 1;
-          else e = j == u.tiles - 1 ? 2 * j + 1 : 2 * j + 2;
-          const int32_t v = v0 + row;
-          const bool clear = !seen(p, u, position_of(u, v));
-          // P.V of the tile before is done, so every earlier fill of these stages has landed: the parity
-          // below means this one
-          if (j > 0) bad |= !wait_for(b_pvdone + 8 * (sb ^ 1), ((jt - 1) >> 1) & 1, abort_flag, status, kWPvDone);
-#pragma unroll
-          for (int h = 0; h < C::kSPT; ++h) {
-            const uint32_t half = (eb + e) * C::kSPT + h, st = half % C::kStages;
-            bad |= !wait_for(b_full + 8 * st, (half / C::kStages) & 1, abort_flag, status, kWStageFull);
-            if (clear) {
-#pragma unroll
-              for (int b = 0; b < C::kNBS; ++b) {
-                if ((C::kSPT * C::kNBS > 1) && ((h * C::kNBS + b) & 1) != wg) continue;
-                if (C::kSPT * C::kNBS == 1 && wg) continue;
-                const uint32_t at = base + C::kRing + st * C::kStageBytes + b * 16384 + row * 128;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) st_shared_v4(at + 16 * k, make_uint4(0u, 0u, 0u, 0u));
-              }
-            }
-          }
-          fence_proxy_async_smem();
-        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_pfull + 8 * sb);
@@ -560,8 +570,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       if (left) break;                        // nothing of this call is written any more
       // epilogue
       if (u.tiles > 0) {
-        const uint32_t jl = js + u.tiles - 1;
-        bad |= !wait_for(b_pvdone + 8 * (jl & 1), (jl >> 1) & 1, abort_flag, status, kWPvDone);
+        bad |= !wait_entry(b_done, eb + 2 * u.tiles - 1, kWPvDone);
         tc_fence_after();
       }
       if (warp_live) {
@@ -582,34 +591,47 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         if (p.splits > 1) p.part_lse[rh * p.splits + u.split] = lse;
         else if (p.lse) p.lse[rh] = lse;
       }
-      if (warp_live) {
-        T* const out = static_cast<T*>(p.out) + rh * D + wg * (D / 2);
-        float* const part = p.splits > 1 ? p.part_o + (rh * p.splits + u.split) * D + wg * (D / 2) : nullptr;
+      const uint32_t tm_row = tm_o + lanes + wg * (D / 2);
+      if (warp_live && p.splits > 1) {
+        float* const part = p.part_o + (rh * p.splits + u.split) * D + wg * (D / 2);
+#pragma unroll
+        for (int c = 0; c < D / 2; c += 32) {
+          if (u.tiles == 0) break;
+          float o[32];
+          tmem_ld32(tm_row + c, o);
+          tc_wait_ld();
+          if (store && !empty) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(part + c + k) = make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv);
+          }
+        }
+      }
+      if (warp_live && p.splits == 1) {
+        uint32_t* const out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + rh * D + wg * (D / 2));
 #pragma unroll
         for (int c = 0; c < D / 2; c += 32) {
           float o[32];
           if (u.tiles > 0) {
-            tmem_ld32(tm_o + lanes + wg * (D / 2) + c, o);
+            tmem_ld32(tm_row + c, o);
             tc_wait_ld();
           }
+          uint32_t v[16];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = empty ? 0.0f : o[k] * inv;
-          if (store && p.splits > 1) {
-            if (!empty) {
+          for (int k = 0; k < 16; ++k) v[k] = empty ? 0u : pack16(o[2 * k] * inv, o[2 * k + 1] * inv, T{});
+          if (!store) continue;
+          // a thread writes its own row: 32-byte stores fill whole sectors
+          if (p.out_32) {
+            st_global_v8(out + c / 2, v);
+            st_global_v8(out + c / 2 + 8, v + 8);
+          } else {
 #pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<float4*>(part + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-            }
-          } else if (store) {
-#pragma unroll
-            for (int k = 0; k < 32; k += 8)
-              *reinterpret_cast<uint4*>(out + c + k) =
-                  make_uint4(pack16(o[k], o[k + 1], T{}), pack16(o[k + 2], o[k + 3], T{}),
-                             pack16(o[k + 4], o[k + 5], T{}), pack16(o[k + 6], o[k + 7], T{}));
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<uint4*>(out + c / 2 + k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
           }
         }
       }
-      if (u.tiles > 0) {
+      if (u.tiles > 0) {      // O may be overwritten
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_ofree);
@@ -621,30 +643,26 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     return;
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer, tensor-memory owner
-    if constexpr (FP4) regs_dec<64>();
+    regs_dec<C::kUtilRegs>();
     constexpr bool kF16 = FP4 || std::is_same<T, __half>::value;
     constexpr uint32_t kIdescQK = kF16 ? idesc_f16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, false);
     constexpr uint32_t kIdescPV = kF16 ? idesc_f16_f32(128, C::kStageDims, false, true)
                                        : idesc_bf16_f32(128, C::kStageDims, false, true);
+    constexpr uint32_t kIdescPV2 = kF16 ? idesc_f16_f32(128, 256, false, true) : idesc_bf16_f32(128, 256, false, true);
     constexpr uint32_t kHi = sw128_desc_hi(1024);
     const uint32_t q_lo = sw128_desc_lo(base, 16);
     const uint32_t k_lo = sw128_desc_lo(base + C::kRing, 16);
     const uint32_t v_lo = sw128_desc_lo(base + C::kRing, 16384);
-    uint32_t st = 0, par = 0, entry = 0, js = 0, qit = 0;
+    uint32_t st = 0, entry = 0, js = 0, qit = 0, fixes = 0;
     bool stop = false;
-    // waits for the stages of the next entry; st and par move past it
+    // waits for the next entry's copies; st moves past its stages
     auto take_entry = [&](uint32_t* stage) -> bool {
-      bool ok = true;
 #pragma unroll
       for (int h = 0; h < C::kSPT; ++h) {
         stage[h] = st;
-        ok = ok && wait_for(b_full + 8 * st, par, abort_flag, status, kWStageFull);
-        if (++st == C::kStages) {
-          st = 0;
-          par ^= 1;
-        }
+        if (++st == C::kStages) st = 0;
       }
-      return __all_sync(0xffffffffu, ok);
+      return __all_sync(0xffffffffu, wait_entry(b_landed, entry, kWLanded));
     };
     auto issue_qk = [&](uint32_t jt, bool last) -> bool {
       uint32_t stage[C::kSPT];
@@ -655,12 +673,11 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         for (int kk = 0; kk < D / 16; ++kk) {
           const int h = kk / (C::kStageDims / 16), kq = kk % (C::kStageDims / 16);
           const uint32_t b_off = (kq >> 2) * 16384 + (kq & 3) * 32;
-          const uint32_t a_off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          const uint32_t a_off = (kk >> 2) * C::kQBlock + (kk & 3) * 32;
           tc_mma_w(tmem + (jt & 1) * 128, q_lo + (a_off >> 4), kHi,
                    k_lo + stage[h] * (C::kStageBytes >> 4) + (b_off >> 4), kHi, kIdescQK, kk > 0 ? 1u : 0u);
         }
-        tc_commit(b_entry + 8 * (entry % C::kEntryBars));
-        tc_commit(b_sfull + 8 * (jt & 1));
+        tc_commit(b_done + 8 * (entry % C::kEntryBars));
         if (last) tc_commit(b_qempty);
       }
       __syncwarp();
@@ -674,7 +691,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         stop = true;
         break;
       }
-      const int nt = recs[rb].tiles;
+      const int nt = recs[rb].tiles, some0 = recs[rb].some0, some1 = recs[rb].some1;
       __syncwarp();
       if (lane == 0) mbar_arrive(b_recempty + 8 * rb);
       if (nt < 0) break;
@@ -696,6 +713,10 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         uint32_t stage[C::kSPT];
         bool ok = wait_for(b_pfull + 8 * (jt & 1), (jt >> 1) & 1, abort_flag, status, kWPFull);
         if (j == 0) ok = ok && wait_for(b_ofree, (qit & 1) ^ 1, abort_flag, status, kWOFree);
+        if (!FP4 && (j < some0 || j >= some1)) {   // V rows that no row sees have been zeroed
+          ok = ok && wait_for(b_vready + 8 * (fixes % C::kFixBars), (fixes / C::kFixBars) & 1, abort_flag, status, kWVReady);
+          ++fixes;
+        }
         ok = __all_sync(0xffffffffu, ok);
         if (!take_entry(stage) || !ok) {
           stop = true;
@@ -704,17 +725,26 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         tc_fence_after();
         if (lane == 0) {
           const uint32_t a0 = tmem + (jt & 1) * 128;
-#pragma unroll
-          for (int h = 0; h < C::kSPT; ++h) {
+          if (C::kSPT == 2 && stage[0] + 1 == stage[C::kSPT - 1]) {
+            // both halves of the dims lie one after the other: one MMA of N = 256 per 16 keys
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
               const uint32_t a = a0 + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8);
-              tc_mma_ta(tm_o + h * 128, a, v_lo + stage[h] * (C::kStageBytes >> 4) + kk * (2048 >> 4), kHi,
-                        kIdescPV, j > 0 || kk > 0 ? 1u : 0u);
+              tc_mma_ta(tm_o, a, v_lo + stage[0] * (C::kStageBytes >> 4) + kk * (2048 >> 4), kHi, kIdescPV2,
+                        j > 0 || kk > 0 ? 1u : 0u);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < C::kSPT; ++h) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t a = a0 + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8);
+                tc_mma_ta(tm_o + h * 128, a, v_lo + stage[h] * (C::kStageBytes >> 4) + kk * (2048 >> 4), kHi,
+                          kIdescPV, j > 0 || kk > 0 ? 1u : 0u);
+              }
             }
           }
-          tc_commit(b_entry + 8 * (entry % C::kEntryBars));
-          tc_commit(b_pvdone + 8 * (jt & 1));
+          tc_commit(b_done + 8 * (entry % C::kEntryBars));
         }
         __syncwarp();
         ++entry;
@@ -733,9 +763,46 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     tmem_dealloc(tmem, 512);
     return;
   } else if (warp < 12) {
-    // ------------------------------------------------------------ scheduler (warp 9), query tile
-    if constexpr (FP4) regs_dec<64>();
-    if (warp - 9 >= C::kQWarps) {
+    // ------------------------------------------------------------ scheduler (warp 9), query tile; warps 10
+    // and 11: zero V rows (16-bit caches), a share of the query tile (4-bit caches)
+    regs_dec<C::kUtilRegs>();
+    if (!FP4 && warp > 9) {
+      uint32_t eb = 0, st0 = 0, fixes = 0;   // ring entries so far, the first stage of entry eb, tiles zeroed
+      for (uint32_t it = 0;; ++it) {
+        const uint32_t rb = it % C::kRecords;
+        if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, status,
+                                              kWRecFull)))
+          break;
+        const Unit u = load_unit(recs + rb);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_recempty + 8 * rb);
+        if (u.tiles < 0) break;
+        bool ok = true;
+        for (int j = 0; j < u.tiles && ok; ++j) {
+          if (j >= u.some0 && j < u.some1) continue;
+          const uint32_t e = v_entry(j, u.tiles);
+          ok = __all_sync(0xffffffffu, wait_entry(b_landed, eb + e, kWLanded));
+          if (!ok) break;
+          for (int k = 0; k < kWinTile / 64; ++k) {
+            const int row = k * 64 + (warp - 10) * 32 + lane;
+            if (seen(p, u, position_of(u, (u.tile0 + j) * kWinTile + row))) continue;
+#pragma unroll
+            for (int b = 0; b < D / 64; ++b) {
+              const uint32_t st = (st0 + e * C::kSPT + b / C::kNBS) % C::kStages;
+              const uint32_t at = base + C::kRing + st * C::kStageBytes + (b % C::kNBS) * 16384 + row * 128;
+#pragma unroll
+              for (int c = 0; c < 8; ++c) st_shared_v4(at + ((c ^ lane) & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_vready + 8 * (fixes % C::kFixBars));
+          ++fixes;
+        }
+        if (!ok) break;
+        eb += 2 * u.tiles;
+        st0 = (st0 + 2 * u.tiles * C::kSPT) % C::kStages;
+      }
       finish_role();
       return;
     }
@@ -820,7 +887,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
                                                          c * 8));
           if constexpr (!std::is_same<T, __half>::value)
             x = make_uint4(bf16x2_as_f16x2(x.x), bf16x2_as_f16x2(x.y), bf16x2_as_f16x2(x.z), bf16x2_as_f16x2(x.w));
-          st_shared_v4(base + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4), x);
+          st_shared_v4(base + (c >> 3) * C::kQBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4), x);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -848,13 +915,13 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     return;
   } else if constexpr (!FP4) {
     // ------------------------------------------------------------ K/V producers (TMA)
+    regs_dec<C::kProducerRegs>();
     const int pw = warp - 12;
     const int per = p.box > 0 ? p.box : 4;                  // keys of one copy
     const int op = lane * 4 + pw;
     const int kb = op / C::kNBS * per, blk = op % C::kNBS;  // its first key and 64-dim block
     const bool active = op < kWinTile / per * C::kNBS;
-    uint32_t st = 0, par = 0, half = 0, jt = 0;
-    int64_t last_half = -1;
+    uint32_t st = 0, half = 0, entry = 0, jt = 0;
     bool stop = false;
     struct Rows {   // physical rows of this lane's copy: slots of up to four keys
       int32_t r[4];
@@ -906,9 +973,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         for (int h = 0; h < C::kSPT; ++h, ++half) {
           if (half >= C::kStages) {
             const uint32_t before = (half - C::kStages) / C::kSPT;   // the entry that held this stage
-            if (!__all_sync(0xffffffffu, wait_for(b_entry + 8 * (before % C::kEntryBars),
-                                                  (before / C::kEntryBars) & 1, abort_flag, status, kWStageEmpty)))
-              return false;
+            if (!__all_sync(0xffffffffu, wait_entry(b_done, before, kWStageEmpty))) return false;
           }
           if (h == 0 && !is_v) {
             uint32_t w0, w1 = 0;
@@ -921,7 +986,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
             if (lane == 0)
               *reinterpret_cast<uint2*>(bad_keys + (jt % C::kBadSlots) * 8 + pw * 2) = make_uint2(w0, w1);
           }
-          const uint32_t bar = b_full + 8 * st;
+          const uint32_t bar = b_landed + 8 * (entry % C::kEntryBars);
           if (lane == 0) {
             if (bytes) mbar_arrive_expect_tx(bar, bytes); else mbar_arrive(bar);
           }
@@ -933,12 +998,9 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
             if (p.box > 0) tma_load_3d(dst, tm, d0, u.kvh, x.r[0], bar);
             else tma_gather4(dst, tm, d0, x.r[0], x.r[1], x.r[2], x.r[3], bar);
           }
-          last_half = half;
-          if (++st == C::kStages) {
-            st = 0;
-            par ^= 1;
-          }
+          if (++st == C::kStages) st = 0;
         }
+        ++entry;
         if (!is_v) ++jt;
         return true;
       };
@@ -964,18 +1026,17 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       }
     }
     if (stop && lane == 0) {
-      // copies of this warp that may still be in flight: the last kStages fills
-      for (int64_t h = last_half - C::kStages + 1; h <= last_half; ++h)
-        if (h >= 0)
-          drain(b_full + 8 * static_cast<uint32_t>(h % C::kStages), static_cast<uint32_t>(h / C::kStages) & 1, status,
-                kDrainNs / C::kStages);
+      // copies that may still be in flight: of the entries that fit the ring, and one cut short
+      const uint32_t n = C::kStages / C::kSPT + 2;
+      for (uint32_t e = entry > n ? entry - n : 0; e < entry; ++e)
+        drain(b_landed + 8 * (e % C::kEntryBars), (e / C::kEntryBars) & 1, status, kDrainNs / n);
     }
     __syncwarp();
     finish_role();
     return;
   } else {
     // ------------------------------------------------------------ 4-bit caches: copy ahead, convert
-    regs_dec<72>();
+    regs_dec<C::kProducerRegs>();
     const int wi = warp - 12;                               // keys 16 wi .. 16 wi + 15 of every tile
     const uint32_t staging = base + C::kStagingAt + wi * C::kDepth * C::kStaging;
     Unit u{};
@@ -985,6 +1046,22 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     bool ended = false, stop = false;
     const int64_t row_codes = static_cast<int64_t>(p.n_kvheads) * (D / 2);
     const int64_t row_scales = static_cast<int64_t>(p.n_kvheads) * (D / 16);
+    // The page of this lane's key (key lane & 15 of the warp's) in the next K tile is looked up one tile
+    // ahead, so that its load is not waited for; V reuses its K tile's slot.
+    int32_t next_page = -1, next_offset = 0;                // page id (-1: none), position in the page
+    bool next_look = false;
+    int32_t slot_even = -1, slot_odd = -1;                  // slots of the last two tiles
+    auto look_up = [&](int tile) {
+      const int32_t pos = position_of(u, (u.tile0 + tile) * kWinTile + wi * 16 + (lane & 15));
+      next_look = seen(p, u, pos);
+      next_page = -1;
+      if (next_look) {
+        const int32_t page = p.pa.page_shift >= 0 ? pos >> p.pa.page_shift : pos / p.pa.page_size;
+        next_offset = pos - page * p.pa.page_size;
+        if (page < p.pa.pages_per_req)
+          next_page = __ldg(p.pa.page_table + static_cast<int64_t>(u.req) * p.pa.pages_per_req + page);
+      }
+    };
     while (!stop) {
       // keep kDepth entries in flight; a record that is not there yet is only waited for when nothing is
       // pending (the other roles may need the pending entries to get to releasing older records)
@@ -1006,19 +1083,21 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
             ended = true;
             break;
           }
+          if (u.tiles > 0) look_up(0);
           continue;
         }
         int tile;
         bool is_v;
         entry_of(e, u.tiles, tile, is_v);
-        const int32_t v = (u.tile0 + tile) * kWinTile + wi * 16 + (lane & 15);
-        const int32_t pos = position_of(u, v);
-        const bool look = seen(p, u, pos);
-        const int32_t slot = look ? static_cast<int32_t>(paged_slot(p.pa, u.req, INT32_MAX, pos)) : -1;
+        int32_t slot;
         if (!is_v) {
-          const uint32_t holes = __ballot_sync(0xffffffffu, look && slot < 0) & 0xffffu;
+          slot = next_page >= 0 && next_page < p.pa.n_pages ? next_page * p.pa.page_size + next_offset : -1;
+          const uint32_t holes = __ballot_sync(0xffffffffu, next_look && slot < 0) & 0xffffu;
           if (lane == 0) bad_keys[(jt % C::kBadSlots) * 8 + wi] = holes;
           ++jt;
+          if (tile & 1) slot_odd = slot; else slot_even = slot;
+        } else {
+          slot = tile & 1 ? slot_odd : slot_even;
         }
         const uint32_t to = staging + (issued % C::kDepth) * C::kStaging;
         const uint8_t* const codes = (is_v ? p.v_codes : p.k_codes) + static_cast<int64_t>(u.kvh) * (D / 2);
@@ -1033,6 +1112,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           cp_async_zfill<D / 16>(to + 16 * (D / 2) + lane * (D / 16), scales + (slot < 0 ? 0 : slot) * row_scales,
                                  slot >= 0);
         cp_async_commit();
+        if (!is_v && tile + 1 < u.tiles) look_up(tile + 1);
         ++issued;
         ++e;
       }
@@ -1040,26 +1120,17 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       cp_async_wait(static_cast<int>(issued - done) - 1);
       __syncwarp();
       const uint32_t half0 = done * C::kSPT;
-      bool ok = true;
-#pragma unroll
-      for (int h = 0; h < C::kSPT; ++h) {
-        const uint32_t half = half0 + h;
-        if (half >= C::kStages) {
-          const uint32_t before = (half - C::kStages) / C::kSPT;
-          ok = ok && wait_for(b_entry + 8 * (before % C::kEntryBars), (before / C::kEntryBars) & 1, abort_flag, status,
-                              kWStageEmpty);
+      if (half0 + C::kSPT > C::kStages) {                   // the entry that held the last of the stages
+        const uint32_t before = (half0 + C::kSPT - 1 - C::kStages) / C::kSPT;
+        if (!__all_sync(0xffffffffu, wait_entry(b_done, before, kWStageEmpty))) {
+          stop = true;
+          break;
         }
-      }
-      if (!__all_sync(0xffffffffu, ok)) {
-        stop = true;
-        break;
       }
       const uint32_t from = staging + (done % C::kDepth) * C::kStaging;
       constexpr int kUnits = 16 * (D / 64);                 // (key, 64-dim block)
-#pragma unroll
-      for (int i = 0; i < (kUnits + 31) / 32; ++i) {
-        const int n = i * 32 + lane;
-        if (kUnits < 32 && n >= kUnits) break;
+#pragma unroll 1
+      for (int n = lane; n < kUnits; n += 32) {
         const int key = n / (D / 64), blk = n % (D / 64);
         const uint4 c0 = ld_shared_v4(from + key * (D / 2) + blk * 32);
         const uint4 c1 = ld_shared_v4(from + key * (D / 2) + blk * 32 + 16);
@@ -1081,10 +1152,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-#pragma unroll
-        for (int h = 0; h < C::kSPT; ++h) mbar_arrive(b_full + 8 * ((half0 + h) % C::kStages));
-      }
+      if (lane == 0) mbar_arrive(b_landed + 8 * (done % C::kEntryBars));
       ++done;
     }
     cp_async_wait(0);
@@ -1101,8 +1169,15 @@ cudaError_t launch_window_instance(const WindowParams& p, const CUtensorMap& tk,
                                    cudaStream_t stream) {
   using C = WinCfg<D, FP4>;
   auto kern = window_attention_kernel<D, T, FP4>;
-  const cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern), C::kSmem, kOptWindow + which);
+  cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern), C::kSmem, kOptWindow + which);
   if (e != cudaSuccess) return e;
+  // The warpgroups' register shares add up to kThreads x kLaunchRegs: a kernel compiled to fewer would wait
+  // for registers that the block does not own.
+  static const int regs = [&] {
+    cudaFuncAttributes a{};
+    return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (regs < C::kLaunchRegs) return cudaErrorInvalidConfiguration;
   kern<<<grid, C::kThreads, C::kSmem, stream>>>(tk, tv, tq1, tqt, p);
   return cudaGetLastError();
 }
