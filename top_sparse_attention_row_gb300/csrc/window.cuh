@@ -1046,6 +1046,12 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     bool ended = false, stop = false;
     const int64_t row_codes = static_cast<int64_t>(p.n_kvheads) * (D / 2);
     const int64_t row_scales = static_cast<int64_t>(p.n_kvheads) * (D / 16);
+    // A key's codes are kParts 16-byte parts.  Lanes convert neighbouring keys of one part, so the parts are
+    // exchanged by the key's place: eight keys' loads then cover all banks.
+    constexpr int kParts = D / 32;
+    auto staged = [](int key, int part) -> uint32_t {
+      return key * (D / 2) + ((part ^ (key / (8 / kParts) & (kParts - 1))) << 4);
+    };
     // The page of this lane's key (key lane & 15 of the warp's) in the next K tile is looked up one tile
     // ahead, so that its load is not waited for; V reuses its K tile's slot.
     int32_t next_page = -1, next_offset = 0;                // page id (-1: none), position in the page
@@ -1104,9 +1110,9 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         const uint8_t* const scales = (is_v ? p.v_scale : p.k_scale) + static_cast<int64_t>(u.kvh) * (D / 16);
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-          const int ch = i * 32 + lane, key = ch / (D / 32), part = ch % (D / 32);
+          const int ch = i * 32 + lane, key = ch / kParts, part = ch % kParts;
           const int32_t s = __shfl_sync(0xffffffffu, slot, key);
-          cp_async_zfill<16>(to + ch * 16, codes + (s < 0 ? 0 : s) * row_codes + part * 16, s >= 0);
+          cp_async_zfill<16>(to + staged(key, part), codes + (s < 0 ? 0 : s) * row_codes + part * 16, s >= 0);
         }
         if (lane < 16)
           cp_async_zfill<D / 16>(to + 16 * (D / 2) + lane * (D / 16), scales + (slot < 0 ? 0 : slot) * row_scales,
@@ -1131,9 +1137,11 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       constexpr int kUnits = 16 * (D / 64);                 // (key, 64-dim block)
 #pragma unroll 1
       for (int n = lane; n < kUnits; n += 32) {
-        const int key = n / (D / 64), blk = n % (D / 64);
-        const uint4 c0 = ld_shared_v4(from + key * (D / 2) + blk * 32);
-        const uint4 c1 = ld_shared_v4(from + key * (D / 2) + blk * 32 + 16);
+        // neighbouring lanes take neighbouring keys: their rows differ in the swizzle, so that eight lanes'
+        // stores cover all banks
+        const int key = n % 16, blk = n / 16;
+        const uint4 c0 = ld_shared_v4(from + staged(key, 2 * blk));
+        const uint4 c1 = ld_shared_v4(from + staged(key, 2 * blk + 1));
         const uint32_t sc4 = ld_shared_u32(from + 16 * (D / 2) + key * (D / 16) + blk * 4);
         const uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(sc4)), s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(sc4 >> 16));
         __half2 sa, sb;
