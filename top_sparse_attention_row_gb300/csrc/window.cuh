@@ -25,8 +25,8 @@
 //  * K and V are staged as 128-byte-swizzled 64-dim blocks of 128 keys in a ring that the MMA consumes in
 //    the order K0 K1 V0 K2 V1 ...  Four producer warps issue TMA boxes of up to 64 keys (page sizes that
 //    are multiples of 8), or gathers of four rows for other page sizes.
-//  * 4-bit caches: eight warps bring the codes and scales with cp.async some entries ahead, each into
-//    its own staging area, and write them to the ring as fp16: e2m1 times an e4m3 scale has six
+//  * 4-bit caches: four warps bring the codes and scales with cp.async some entries ahead into a staging
+//    ring, and eight warps write them to the ring of stages as fp16: e2m1 times an e4m3 scale has six
 //    significant bits, so that is exact; the caches' global scales multiply the logits and the output.
 //    The MMAs run fp16 there (q is rounded to fp16, as for FP8 caches).
 //  * Keys that no row of the unit sees (the rest of a page, positions that left the window, missing
@@ -66,28 +66,32 @@ struct WinCfg {
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kStages = FP4 ? (D == 64 ? 6 : 4) : (D == 256 ? 5 : D == 128 ? 6 : 12);
   static constexpr int kEntryBars = 16;                    // > entries in flight
-  static constexpr int kRecords = FP4 ? 8 : 4;
+  static constexpr int kRecords = 4;
   static constexpr int kBadSlots = FP4 ? 16 : 8;           // > tiles the producers may be ahead
-  static constexpr int kThreads = FP4 ? 640 : 512;
-  // registers per thread at launch, and after the split: softmax warpgroups, MMA and scheduler, producers
-  static constexpr int kLaunchRegs = FP4 ? 96 : 128;
-  static constexpr int kSoftmaxRegs = FP4 ? 128 : 168, kUtilRegs = FP4 ? 64 : 88, kProducerRegs = FP4 ? 80 : 88;
-  static_assert(256 * kSoftmaxRegs + 128 * kUtilRegs + (kThreads - 384) * kProducerRegs <= kThreads * kLaunchRegs,
+  static constexpr int kThreads = FP4 ? 768 : 512;
+  // registers per thread at launch, and after the split: softmax warpgroups; MMA and scheduler; copies; 4-bit
+  // conversion
+  static constexpr int kLaunchRegs = FP4 ? 80 : 128;
+  static constexpr int kSoftmaxRegs = FP4 ? 120 : 168, kUtilRegs = FP4 ? 64 : 88, kProducerRegs = FP4 ? 72 : 88;
+  static constexpr int kConvertRegs = 48;
+  static_assert(256 * kSoftmaxRegs + 128 * (kUtilRegs + kProducerRegs) + (FP4 ? 256 * kConvertRegs : 0) <=
+                    kThreads * kLaunchRegs,
                 "register split within the launch's registers");
-  static constexpr int kProducers = FP4 ? 8 : 4;
+  static constexpr int kProducers = 4;
   static constexpr int kQWarps = FP4 ? 3 : 1;              // warps that write the query tile
-  static constexpr int kDepth = D == 256 ? 3 : D == 128 ? 6 : 8;   // 4-bit entries in flight per warp
-  static constexpr int kStaging = 16 * (D / 2 + D / 16);   // bytes of one entry's 16 keys
+  static constexpr int kDepth = D == 256 ? 3 : D == 128 ? 6 : 8;   // 4-bit entries staged
+  static constexpr int kStaging = kWinTile * (D / 2 + D / 16);     // bytes of one
   // offsets
   static constexpr int kRing = kQBytes;
   static constexpr int kStagingAt = kRing + kStages * kStageBytes;
-  static constexpr int kMaxAt = kStagingAt + (FP4 ? 8 * kDepth * kStaging : 0);   // [2][2][128] float
+  static constexpr int kMaxAt = kStagingAt + (FP4 ? kDepth * kStaging : 0);   // [2][2][128] float
   static constexpr int kBadAt = kMaxAt + 2048;             // [kBadSlots][8] uint32
   static constexpr int kRecAt = kBadAt + kBadSlots * 32;   // [kRecords] Unit
   static constexpr int kBarAt = kRecAt + kRecords * 64;
   static constexpr int kFixBars = 8;                       // > V tiles that may be zeroed ahead of the MMA
-  // landed[16], done[16] (by entry), pfull[2], qfull, qempty, ofree, fin, next, vready[8], recfull/empty
-  static constexpr int kBars = 2 * kEntryBars + 7 + kFixBars + 2 * kRecords;
+  // landed[16], done[16] (by entry), pfull[2], qfull, qempty, ofree, fin, next, vready[8], recfull/empty,
+  // staged/unstaged[kDepth] (4-bit caches)
+  static constexpr int kBars = 2 * kEntryBars + 7 + kFixBars + 2 * kRecords + (FP4 ? 2 * kDepth : 0);
   static constexpr int kNextAt = (kBarAt + 8 * kBars + 15) / 16 * 16;   // answer of the launch control
   static constexpr int kTmemSlot = kNextAt + 16;
   static constexpr int kSmem = kTmemSlot + 16;
@@ -103,7 +107,7 @@ constexpr float kRaise = 8.0f;          // log2 units by which a tile may exceed
 constexpr float kLn2f = 0.6931471805599453f;
 enum Site : int32_t {
   kWRecEmpty = 0x41, kWRecFull, kWQEmpty, kWQFull, kWStageEmpty, kWLanded, kWSFull, kWPFull, kWPvDone,
-  kWOFree, kWNext, kWVReady, kWDrain
+  kWOFree, kWNext, kWVReady, kWStaged, kWUnstaged, kWDrain
 };
 
 __device__ __forceinline__ unsigned long long now_ns() {
@@ -249,20 +253,6 @@ __device__ __forceinline__ bool seen(const WindowParams& p, const Unit& u, int32
 // The ring entries of tile j of a unit with nt tiles.
 __device__ __forceinline__ uint32_t k_entry(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ uint32_t v_entry(int j, int nt) { return j == nt - 1 ? 2 * j + 1 : 2 * j + 2; }
-// Ring entry e of a unit with nt tiles (K0 K1 V0 K2 V1 ... V(nt-1)): its tile, and whether it is V.
-__device__ __forceinline__ void entry_of(int e, int nt, int& tile, bool& is_v) {
-  if (e == 0) {
-    tile = 0;
-    is_v = false;
-  } else if (e == 2 * nt - 1) {
-    tile = nt - 1;
-    is_v = true;
-  } else {
-    is_v = (e & 1) == 0;
-    tile = is_v ? e / 2 - 1 : (e + 1) / 2;
-  }
-}
-
 __device__ __forceinline__ uint32_t pack16(float a, float b, __nv_bfloat16) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   uint32_t r;
@@ -313,19 +303,9 @@ __device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void* src, bo
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(ok ? N : 0)
                  : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits until at most `left` of this thread's copy groups are in flight.
-__device__ __forceinline__ void cp_async_wait(int left) {
-  switch (left) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-  }
+// Arrives on `bar` once this thread's earlier cp.async copies have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 // Two e2m1 codes (byte `k` of w) as fp16, times a pair of equal scales: exact.
 __device__ __forceinline__ uint32_t e2m1_scaled(uint32_t w, int k, __half2 s) {
@@ -364,11 +344,14 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
   const uint32_t b_next = b_fin + 8;
   const uint32_t b_recfull = b_next + 8;
   const uint32_t b_recempty = b_recfull + 8 * C::kRecords;
+  const uint32_t b_staged = b_recempty + 8 * C::kRecords;      // 4-bit caches: an entry's copies are staged, converted
+  const uint32_t b_unstaged = b_staged + 8 * C::kDepth;
   float* const maxima = reinterpret_cast<float*>(smem + C::kMaxAt);
   uint32_t* const bad_keys = reinterpret_cast<uint32_t*>(smem + C::kBadAt);
   Unit* const recs = reinterpret_cast<Unit*>(smem + C::kRecAt);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kTmemSlot);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* const last_entry = tmem_slot + 2;         // 4-bit caches: number of entries once known
   int32_t* const status = p.status;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -378,7 +361,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
   }
   if (threadIdx.x == 0) {
     for (int e = 0; e < C::kEntryBars; ++e) {
-      mbar_init(b_landed + 8 * e, FP4 ? C::kProducers : C::kProducers * C::kSPT);
+      mbar_init(b_landed + 8 * e, FP4 ? 8 : C::kProducers * C::kSPT);
       mbar_init(b_done + 8 * e, 1);
     }
     mbar_init(b_pfull, 8);
@@ -392,6 +375,13 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     for (int r = 0; r < C::kRecords; ++r) {
       mbar_init(b_recfull + 8 * r, 1);
       mbar_init(b_recempty + 8 * r, 8 + 1 + C::kProducers + 2);   // and warps 10 and 11
+    }
+    if constexpr (FP4) {
+      for (int k = 0; k < C::kDepth; ++k) {
+        mbar_init(b_staged + 8 * k, 128);
+        mbar_init(b_unstaged + 8 * k, 8);
+      }
+      *last_entry = 0xffffffffu;
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -1035,114 +1025,125 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     finish_role();
     return;
   } else {
-    // ------------------------------------------------------------ 4-bit caches: copy ahead, convert
-    regs_dec<C::kProducerRegs>();
-    const int wi = warp - 12;                               // keys 16 wi .. 16 wi + 15 of every tile
-    const uint32_t staging = base + C::kStagingAt + wi * C::kDepth * C::kStaging;
-    Unit u{};
-    u.tiles = 0;
-    int e = 0;                                              // next entry of u to copy
-    uint32_t it = 0, issued = 0, done = 0, jt = 0;
-    bool ended = false, stop = false;
-    const int64_t row_codes = static_cast<int64_t>(p.n_kvheads) * (D / 2);
-    const int64_t row_scales = static_cast<int64_t>(p.n_kvheads) * (D / 16);
     // A key's codes are kParts 16-byte parts.  Lanes convert neighbouring keys of one part, so the parts are
     // exchanged by the key's place: eight keys' loads then cover all banks.
     constexpr int kParts = D / 32;
     auto staged = [](int key, int part) -> uint32_t {
       return key * (D / 2) + ((part ^ (key / (8 / kParts) & (kParts - 1))) << 4);
     };
-    // The page of this lane's key (key lane & 15 of the warp's) in the next K tile is looked up one tile
-    // ahead, so that its load is not waited for; V reuses its K tile's slot.
-    int32_t next_page = -1, next_offset = 0;                // page id (-1: none), position in the page
-    bool next_look = false;
-    int32_t slot_even = -1, slot_odd = -1;                  // slots of the last two tiles
-    auto look_up = [&](int tile) {
-      const int32_t pos = position_of(u, (u.tile0 + tile) * kWinTile + wi * 16 + (lane & 15));
-      next_look = seen(p, u, pos);
-      next_page = -1;
-      if (next_look) {
-        const int32_t page = p.pa.page_shift >= 0 ? pos >> p.pa.page_shift : pos / p.pa.page_size;
-        next_offset = pos - page * p.pa.page_size;
-        if (page < p.pa.pages_per_req)
-          next_page = __ldg(p.pa.page_table + static_cast<int64_t>(u.req) * p.pa.pages_per_req + page);
-      }
-    };
-    while (!stop) {
-      // keep kDepth entries in flight; a record that is not there yet is only waited for when nothing is
-      // pending (the other roles may need the pending entries to get to releasing older records)
-      while (!ended && issued - done < C::kDepth) {
-        if (e == 2 * u.tiles) {
-          const uint32_t rb = it % C::kRecords, ph = (it / C::kRecords) & 1;
-          if (issued != done) {
-            if (!__all_sync(0xffffffffu, mbar_test(b_recfull + 8 * rb, ph))) break;
-          } else if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, ph, abort_flag, status, kWRecFull))) {
-            stop = true;
-            break;
-          }
-          u = load_unit(recs + rb);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b_recempty + 8 * rb);
-          ++it;
-          e = 0;
-          if (u.tiles < 0) {
-            ended = true;
-            break;
-          }
-          if (u.tiles > 0) look_up(0);
-          continue;
-        }
-        int tile;
-        bool is_v;
-        entry_of(e, u.tiles, tile, is_v);
-        int32_t slot;
-        if (!is_v) {
-          slot = next_page >= 0 && next_page < p.pa.n_pages ? next_page * p.pa.page_size + next_offset : -1;
-          const uint32_t holes = __ballot_sync(0xffffffffu, next_look && slot < 0) & 0xffffu;
-          if (lane == 0) bad_keys[(jt % C::kBadSlots) * 8 + wi] = holes;
-          ++jt;
-          if (tile & 1) slot_odd = slot; else slot_even = slot;
-        } else {
-          slot = tile & 1 ? slot_odd : slot_even;
-        }
-        const uint32_t to = staging + (issued % C::kDepth) * C::kStaging;
-        const uint8_t* const codes = (is_v ? p.v_codes : p.k_codes) + static_cast<int64_t>(u.kvh) * (D / 2);
-        const uint8_t* const scales = (is_v ? p.v_scale : p.k_scale) + static_cast<int64_t>(u.kvh) * (D / 16);
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const int ch = i * 32 + lane, key = ch / kParts, part = ch % kParts;
-          const int32_t s = __shfl_sync(0xffffffffu, slot, key);
-          cp_async_zfill<16>(to + staged(key, part), codes + (s < 0 ? 0 : s) * row_codes + part * 16, s >= 0);
-        }
-        if (lane < 16)
-          cp_async_zfill<D / 16>(to + 16 * (D / 2) + lane * (D / 16), scales + (slot < 0 ? 0 : slot) * row_scales,
-                                 slot >= 0);
-        cp_async_commit();
-        if (!is_v && tile + 1 < u.tiles) look_up(tile + 1);
-        ++issued;
-        ++e;
-      }
-      if (stop || issued == done) break;
-      cp_async_wait(static_cast<int>(issued - done) - 1);
-      __syncwarp();
-      const uint32_t half0 = done * C::kSPT;
-      if (half0 + C::kSPT > C::kStages) {                   // the entry that held the last of the stages
-        const uint32_t before = (half0 + C::kSPT - 1 - C::kStages) / C::kSPT;
-        if (!__all_sync(0xffffffffu, wait_entry(b_done, before, kWStageEmpty))) {
+    if (warp < 16) {
+      // ---------------------------------------------------------- 4-bit caches: copies into the staging ring
+      regs_dec<C::kProducerRegs>();
+      const int pw = warp - 12;                             // keys 32 pw .. 32 pw + 31 of every tile
+      uint32_t n = 0, slot_at = 0, turn = 0, jt = 0;        // entries copied; n % kDepth, n / kDepth
+      bool stop = false;
+      const uint32_t row_codes = static_cast<uint32_t>(p.n_kvheads) * (D / 2);
+      const uint32_t row_scales = static_cast<uint32_t>(p.n_kvheads) * (D / 16);
+      for (uint32_t it = 0; !stop; ++it) {
+        const uint32_t rb = it % C::kRecords;
+        if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, status,
+                                              kWRecFull))) {
           stop = true;
           break;
         }
+        const Unit u = load_unit(recs + rb);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_recempty + 8 * rb);
+        if (u.tiles < 0) break;
+        const uint8_t* const k_codes = p.k_codes + static_cast<int64_t>(u.kvh) * (D / 2) + lane % kParts * 16;
+        const uint8_t* const v_codes = p.v_codes + static_cast<int64_t>(u.kvh) * (D / 2) + lane % kParts * 16;
+        const uint8_t* const k_scale = p.k_scale + static_cast<int64_t>(u.kvh) * (D / 16);
+        const uint8_t* const v_scale = p.v_scale + static_cast<int64_t>(u.kvh) * (D / 16);
+        // The page of this lane's key in the next K tile is looked up one tile ahead, so that its load is not
+        // waited for; V takes its K tile's slot.
+        int32_t page = -1, offset = 0;
+        bool look = false;
+        auto look_up = [&](int tile) {
+          const int32_t pos = position_of(u, (u.tile0 + tile) * kWinTile + pw * 32 + lane);
+          look = seen(p, u, pos);
+          page = -1;
+          if (look) {
+            const int32_t e = p.pa.page_shift >= 0 ? pos >> p.pa.page_shift : pos / p.pa.page_size;
+            offset = pos - e * p.pa.page_size;
+            if (e < p.pa.pages_per_req)
+              page = __ldg(p.pa.page_table + static_cast<int64_t>(u.req) * p.pa.pages_per_req + e);
+          }
+        };
+        auto copy = [&](int32_t slot, const uint8_t* codes, const uint8_t* scales) -> bool {
+          if (n >= C::kDepth &&
+              !__all_sync(0xffffffffu, wait_for(b_unstaged + 8 * slot_at, (turn & 1) ^ 1, abort_flag, status, kWUnstaged)))
+            return false;
+          const uint32_t to = base + C::kStagingAt + slot_at * C::kStaging;
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) {
+            const int key = i * (32 / kParts) + lane / kParts;
+            const int32_t s = __shfl_sync(0xffffffffu, slot, key);
+            cp_async_zfill<16>(to + staged(pw * 32 + key, lane % kParts),
+                               codes + static_cast<uint64_t>(static_cast<uint32_t>(max(s, 0))) * row_codes, s >= 0);
+          }
+          cp_async_zfill<D / 16>(to + kWinTile * (D / 2) + (pw * 32 + lane) * (D / 16),
+                                 scales + static_cast<uint64_t>(static_cast<uint32_t>(max(slot, 0))) * row_scales, slot >= 0);
+          cp_async_arrive(b_staged + 8 * slot_at);
+          ++n;
+          if (++slot_at == C::kDepth) {
+            slot_at = 0;
+            ++turn;
+          }
+          return true;
+        };
+        int32_t slot = -1;
+        if (u.tiles > 0) look_up(0);
+        for (int t = 0; t <= u.tiles && u.tiles > 0; ++t) {  // K of tile t, then V of tile t - 1
+          const int32_t before = slot;
+          if (t < u.tiles) {
+            slot = page >= 0 && page < p.pa.n_pages ? page * p.pa.page_size + offset : -1;
+            const uint32_t holes = __ballot_sync(0xffffffffu, look && slot < 0);
+            if (lane == 0)
+              *reinterpret_cast<uint2*>(bad_keys + (jt % C::kBadSlots) * 8 + pw * 2) = make_uint2(holes & 0xffffu, holes >> 16);
+            ++jt;
+            if (!copy(slot, k_codes, k_scale)) {
+              stop = true;
+              break;
+            }
+            if (t + 1 < u.tiles) look_up(t + 1);
+          }
+          if (t > 0 && !copy(before, v_codes, v_scale)) {
+            stop = true;
+            break;
+          }
+        }
       }
-      const uint32_t from = staging + (done % C::kDepth) * C::kStaging;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!stop) {
+        *last_entry = n;                                    // (every copying warp has the same count)
+        mbar_arrive(b_staged + 8 * slot_at);
+      }
+      __syncwarp();
+      finish_role();
+      return;
+    }
+    // ------------------------------------------------------------ 4-bit caches: conversion to fp16
+    regs_dec<C::kConvertRegs>();
+    const int wi = warp - 16;                               // keys 16 wi .. 16 wi + 15 of every tile
+    uint32_t slot_at = 0, turn = 0;
+    for (uint32_t n = 0;; ++n) {
+      if (!__all_sync(0xffffffffu, wait_for(b_staged + 8 * slot_at, turn & 1, abort_flag, status, kWStaged))) break;
+      if (n == *last_entry) break;
+      const uint32_t half0 = n * C::kSPT;
+      if (half0 + C::kSPT > C::kStages) {                   // the entry that held the last of the stages
+        const uint32_t before = (half0 + C::kSPT - 1 - C::kStages) / C::kSPT;
+        if (!__all_sync(0xffffffffu, wait_entry(b_done, before, kWStageEmpty))) break;
+      }
+      const uint32_t from = base + C::kStagingAt + slot_at * C::kStaging;
       constexpr int kUnits = 16 * (D / 64);                 // (key, 64-dim block)
 #pragma unroll 1
-      for (int n = lane; n < kUnits; n += 32) {
+      for (int k = lane; k < kUnits; k += 32) {
         // neighbouring lanes take neighbouring keys: their rows differ in the swizzle, so that eight lanes'
         // stores cover all banks
-        const int key = n % 16, blk = n / 16;
-        const uint4 c0 = ld_shared_v4(from + staged(key, 2 * blk));
-        const uint4 c1 = ld_shared_v4(from + staged(key, 2 * blk + 1));
-        const uint32_t sc4 = ld_shared_u32(from + 16 * (D / 2) + key * (D / 16) + blk * 4);
+        const int r = wi * 16 + k % 16, blk = k / 16;
+        const uint4 c0 = ld_shared_v4(from + staged(r, 2 * blk));
+        const uint4 c1 = ld_shared_v4(from + staged(r, 2 * blk + 1));
+        const uint32_t sc4 = ld_shared_u32(from + kWinTile * (D / 2) + r * (D / 16) + blk * 4);
         const uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(sc4)), s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(sc4 >> 16));
         __half2 sa, sb;
         memcpy(&sa, &s01, 4);
@@ -1150,7 +1151,6 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         const __half2 sc[4] = {__low2half2(sa), __high2half2(sa), __low2half2(sb), __high2half2(sb)};
         const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
         const uint32_t half = half0 + blk / C::kNBS;
-        const int r = wi * 16 + key;
         const uint32_t row = base + C::kRing + (half % C::kStages) * C::kStageBytes + (blk % C::kNBS) * 16384 + r * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -1160,10 +1160,15 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_landed + 8 * (done % C::kEntryBars));
-      ++done;
+      if (lane == 0) {
+        mbar_arrive(b_landed + 8 * (n % C::kEntryBars));
+        mbar_arrive(b_unstaged + 8 * slot_at);
+      }
+      if (++slot_at == C::kDepth) {
+        slot_at = 0;
+        ++turn;
+      }
     }
-    cp_async_wait(0);
     __syncwarp();
     finish_role();
     return;
