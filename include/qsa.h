@@ -409,11 +409,11 @@ qsa_status qsa_rope_append_fp4(const void* q, void* q_out, const void* k, const 
  * output non-finite, and may do so to the rows of up to 127 neighbouring (token, head) pairs of the same request and
  * KV head.
  *   scale > 0.  head_dim 64, 128 or 256; n_qheads / n_kvheads <= 128 (4-bit caches of 256 dims: <= 64).
- *   workspace: calls with few rows split the keys over the SMs and join the parts; they need
- *       qsa_window_workspace_bytes (for the device's SM count; 0 = no split), 256-byte aligned.  NULL: taken from
+ *   workspace: calls with few query tiles for the SMs cut the keys into equal shares and join the parts; they
+ *       need qsa_window_workspace_bytes (for the device's SM count; 0 = none), 256-byte aligned.  NULL: taken from
  *       the library's pool on `stream`.  Calls that overlap need a workspace each.
  * Sums, maxima and outputs are held in fp32, the weights of the P.V product are rounded to 16 bits.
- * Results do not depend on timing, but a row's depend on the split, and so on the batch it is in.
+ * Results do not depend on timing, but a row's sums depend on where the shares are cut, and so on its batch.
  * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED (other head dims, caches of 2^31 rows and more),
  * QSA_ERR_WORKSPACE; a wait inside the kernel that runs out is reported by qsa_get_device_status. */
 qsa_status qsa_window_attention_paged(const void* q, const void* k_cache, const void* v_cache,

@@ -321,13 +321,19 @@ bool rope_is_aligned(const RopeParams& p);
 cudaError_t launch_rope(RopeParams p, bool fp16, bool fp4, int num_sms, cudaStream_t stream);
 
 // Sliding-window attention over a paged cache (window.cuh).
+// Equal shares: the unit that begins in a block and goes on in the next ones (first: slot of its first part,
+// -1 = none; more: blocks it goes on in, whose first slot holds their part).
+struct JoinRecord {
+  int32_t first, more, row0, tokens, kvh, pad0, pad1, pad2;
+};
 constexpr int kWinTile = 128;                // keys per MMA tile, and rows of the query tile
 struct WindowParams {
   const void* q;                // [n_rows, n_qheads, D] bf16 or fp16
   void* out;
   float* lse;                   // nullable
-  float* part_o;                // splits > 1: [n_rows, n_qheads, splits, D] normalised partial outputs
-  float* part_lse;              // [n_rows, n_qheads, splits] their log-sum-exps
+  float* part_o;                // equal shares: [2 shares, 128 rows, D] normalised partial outputs
+  float* part_lse;              // [2 shares, 128 rows] their log-sum-exps
+  struct JoinRecord* joins;     // [shares]
   int32_t* status;              // device status word (0x100 | wait site on a timeout)
   const uint8_t* k_codes;       // 4-bit caches: e2m1 pairs [slots, n_kvheads, D / 2]
   const uint8_t* v_codes;
@@ -335,11 +341,11 @@ struct WindowParams {
   const uint8_t* v_scale;
   PagedAddr pa;                 // kv_lens is required, n_pages > 0
   int64_t n_rows;
-  int64_t n_units;              // tiles x KV heads x splits
+  int64_t n_units;              // whole units: tiles x KV heads
   int32_t n_qheads, n_kvheads, group;
   int32_t tile_tokens;          // tokens of a query tile: 128 / group, at least 1
   int32_t n_tiles;              // upper bound: n_rows / tile_tokens + n_requests
-  int32_t splits;
+  int32_t shares;               // equal shares: blocks of the grid; 0 = whole units
   int32_t window;               // 0 = none
   int32_t n_sink;
   int32_t out_32;               // out is 32-byte aligned

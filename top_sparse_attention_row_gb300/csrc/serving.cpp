@@ -85,21 +85,22 @@ qsa_status run_rope(qsa::RopeParams& p, const qsa_rope_spec* rope, int32_t dtype
   return QSA_OK;
 }
 
-// Splits of the key axis, by a model of the call's time in key tiles.  A unit takes its tiles, about three
-// tiles' time of its own (query tile, first softmax, output), and when split its partial rows in fp32, which
-// it writes and the join reads (two tiles' worth of bytes when all 128 rows are in use).  Units are handed
-// out as SMs become free: the average load and half a unit of waiting for the last.  The join is one more
-// launch, about three tiles long.  The smallest count among the best wins.
+// How the units of a call are dealt out, by a model of its time in key tiles.  A unit takes its tiles and about
+// three tiles' time of its own (query tile, first softmax, output).  Whole units run in rounds; equal shares
+// divide the tiles evenly, but a block then has one more unit begun or ended, writes up to two partial ones
+// in fp32 (a tile's worth of bytes each when all 128 rows are in use) that the join reads again, and the
+// join is one more launch, about three tiles long.
 struct WindowPlan {
-  int32_t tile_tokens, n_tiles, splits;
+  int32_t tile_tokens, n_tiles, shares;
   int64_t n_units;
 };
-constexpr int32_t kMaxSplits = 128;
+constexpr int32_t kMaxShareTiles = 1 << 16;    // every block sums all units' tiles
 WindowPlan plan_window(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, int32_t group, int32_t tile_rows,
                        int64_t max_keys, int32_t window, int32_t n_sink, int32_t sms) {
   WindowPlan w{};
   w.tile_tokens = tile_rows / group;
   w.n_tiles = static_cast<int32_t>(n_rows / w.tile_tokens + n_requests);
+  w.n_units = static_cast<int64_t>(w.n_tiles) * n_kvheads;
   // units with rows: every request has at most one partial tile
   int64_t tiles = (n_rows + w.tile_tokens - 1) / w.tile_tokens + n_requests - 1;
   if (tiles > n_rows) tiles = n_rows;
@@ -110,31 +111,23 @@ WindowPlan plan_window(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, in
   }
   const int64_t kt = (keys + qsa::kWinTile - 1) / qsa::kWinTile;
   const int64_t items = tiles * n_kvheads;
+  if (kt <= 1 || w.n_tiles > kMaxShareTiles) return w;
   const int64_t rows_per = n_rows < tiles * w.tile_tokens ? (n_rows + tiles - 1) / tiles : w.tile_tokens;
-  const double partial = 2.0 * static_cast<double>(rows_per * group) / qsa::kWinTile;
-  double best = 0.0;
-  w.splits = 1;
-  for (int64_t s = 1; s <= kt && s <= kMaxSplits; ++s) {
-    const double unit = static_cast<double>((kt + s - 1) / s) + 3.0 + (s > 1 ? partial : 0.0);
-    const double load = static_cast<double>(items * s) / sms;
-    const double cost = (load <= 1.0 ? unit : (load + 0.5) * unit) + (s > 1 ? 3.0 : 0.0);
-    if (s == 1 || cost < best) {
-      best = cost;
-      w.splits = static_cast<int32_t>(s);
-    }
-  }
-  w.n_units = static_cast<int64_t>(w.n_tiles) * n_kvheads * w.splits;
+  const double partial = static_cast<double>(rows_per * group) / qsa::kWinTile;
+  const double load = static_cast<double>(items) / sms;
+  const double whole = std::ceil(load) * (kt + 3.0);
+  const int64_t shares = items * kt < sms ? items * kt : sms;
+  const double even = static_cast<double>(items) * kt / shares + (load + 1.0) * 3.0 + 4.0 * partial + 3.0;
+  if (even < whole) w.shares = static_cast<int32_t>(shares);
   return w;
 }
 
 // Rows of the query tile (WinCfg::kRows of the kernels).
 int32_t window_tile_rows(int32_t head_dim, bool fp4) { return fp4 && head_dim == 256 ? 64 : qsa::kWinTile; }
 
-// Partial outputs and log-sum-exps of a split call.
-size_t window_ws_bytes(int64_t n_rows, int32_t n_qheads, int32_t head_dim, int32_t splits) {
-  if (splits <= 1) return 0;
-  const size_t n = static_cast<size_t>(n_rows) * n_qheads * splits;
-  return n * head_dim * 4 + (n * 4 + 255) / 256 * 256;
+// Partial outputs, their log-sum-exps and the join records of a call in equal shares.
+size_t window_ws_bytes(int32_t head_dim, int32_t shares) {
+  return static_cast<size_t>(shares) * (2 * qsa::kWinTile * (static_cast<size_t>(head_dim) + 1) * 4 + sizeof(qsa::JoinRecord));
 }
 
 struct Fp4Cache {
@@ -202,7 +195,7 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   p.group = group;
   p.tile_tokens = w.tile_tokens;
   p.n_tiles = w.n_tiles;
-  p.splits = w.splits;
+  p.shares = w.shares;
   p.out_32 = aligned_to(out, 32);
   p.window = window;
   p.n_sink = n_sink;
@@ -224,12 +217,12 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   if (qsa::log_geometry())
     std::fprintf(stderr,
                  "qsa: window d=%d rows=%lld requests=%d heads=%d/%d window=%d sinks=%d%s -> tile_tokens=%d "
-                 "box=%d splits=%d units=%lld\n",
+                 "box=%d shares=%d units=%lld\n",
                  head_dim, static_cast<long long>(n_rows), n_requests, n_qheads, n_kvheads, window, n_sink,
-                 fp4 ? " fp4" : "", p.tile_tokens, p.box, p.splits, static_cast<long long>(p.n_units));
+                 fp4 ? " fp4" : "", p.tile_tokens, p.box, p.shares, static_cast<long long>(p.n_units));
   void* ws = workspace;
   bool own = false;
-  const size_t need = window_ws_bytes(n_rows, n_qheads, head_dim, p.splits);
+  const size_t need = window_ws_bytes(head_dim, p.shares);
   if (need > 0) {
     if (ws) {
       if (workspace_bytes < need || !aligned_to(ws, 256)) return QSA_ERR_WORKSPACE;
@@ -238,14 +231,15 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
       own = true;
     }
     p.part_o = static_cast<float*>(ws);
-    p.part_lse = p.part_o + static_cast<size_t>(n_rows) * n_qheads * p.splits * head_dim;
+    p.part_lse = p.part_o + static_cast<size_t>(p.shares) * 2 * qsa::kWinTile * head_dim;
+    p.joins = reinterpret_cast<qsa::JoinRecord*>(p.part_lse + static_cast<size_t>(p.shares) * 2 * qsa::kWinTile);
   }
   p.stall_first_item = qsa::take_stall_request() ? 1 : 0;
   const cudaError_t e = qsa::launch_window(p, head_dim, dtype == QSA_FP16, fp4 != nullptr, k_cache, v_cache,
                                            stream);
   if (own) cudaFreeAsync(ws, stream);
   if (e != cudaSuccess) return QSA_ERR_CUDA;
-  qsa::count_launches(p.splits > 1 ? 2 : 1);
+  qsa::count_launches(p.shares > 0 ? 2 : 1);
   return QSA_OK;
 }
 
@@ -263,7 +257,7 @@ size_t qsa_window_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t pa
   if (num_sms <= 0 && qsa::device_sms(&num_sms) != QSA_OK) return 0;
   const WindowPlan w = plan_window(n_rows, n_requests, n_kvheads, n_qheads / n_kvheads, window_tile_rows(head_dim, fp4 != 0),
                                    static_cast<int64_t>(pages_per_req) * page_size, window, n_sink, num_sms);
-  return window_ws_bytes(n_rows, n_qheads, head_dim, w.splits);
+  return window_ws_bytes(head_dim, w.shares);
 }
 
 qsa_status qsa_window_attention_paged(const void* q, const void* k_cache, const void* v_cache,

@@ -1,4 +1,4 @@
-// Window attention: tensor maps, kernel choice and the join of split key ranges.
+// Window attention: tensor maps, kernel choice and the join of units that several blocks share.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -10,66 +10,71 @@
 namespace qsa {
 namespace {
 
-constexpr int kJoinWarps = 4;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 16;      // blocks that share a unit's rows
 
-// Joins the splits of a row and head: with L_s the split's log-sum-exp and O_s its normalised output,
-// lse = ln sum exp(L_s) and O = sum exp(L_s - lse) O_s.  A warp per row and head; the splits are added in
-// order, so the result does not depend on which finished first.  Rows behind the last request stay as
-// they were.
+// Joins the parts of a unit (equal shares): with L_s a part's log-sum-exp and O_s its normalised output,
+// lse = ln sum exp(L_s) and O = sum exp(L_s - lse) O_s.  Block (c, y) takes rows y, y + 16, .. of the unit
+// that begins in block c of the attention grid and goes on in the following ones; D / 4 threads share a row
+// and the groups of threads its parts, which are added in a fixed order, so the result does not depend on
+// timing.
 template <int D, typename T>
-__global__ void __launch_bounds__(kJoinWarps * 32) window_join_kernel(const __grid_constant__ WindowParams p) {
-  constexpr int kPer = D / 32;
+__global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_constant__ WindowParams p) {
+  constexpr int kCols = D / 4, kGroups = kJoinThreads / kCols;
+  __shared__ float4 sums[kGroups][kCols];
   pdl_wait();   // first thing in every thread: the grid must not end before the attention kernel has
-  const int lane = threadIdx.x & 31;
-  const int64_t rh = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
-  if (rh >= p.n_rows * p.n_qheads) return;
-  const int64_t row = rh / p.n_qheads;
-  if (row < __ldg(p.pa.cu_seqlens_q) || row >= __ldg(p.pa.cu_seqlens_q + p.pa.n_requests)) return;
-  const float* const ls = p.part_lse + rh * p.splits;
-  const float* const os = p.part_o + rh * p.splits * D + lane * kPer;
-  // lane s holds the weight of split s (up to 128 splits: four per lane)
-  float w[4], m = -INFINITY;
+  const JoinRecord j = p.joins[blockIdx.x];
+  if (j.first < 0) return;
+  const int tid = threadIdx.x, lane = tid & 31, col = tid % kCols, group = tid / kCols;
+  const int parts = j.more + 1;
+  auto slot = [&](int s) { return s == 0 ? j.first : 2 * (static_cast<int>(blockIdx.x) + s); };
+  for (int row = blockIdx.y; row < j.tokens * p.group; row += kJoinRows) {
+    // every warp works out the parts' total weight
+    float m = -INFINITY, total = 0.0f;
+    for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.part_lse[slot(s) * kWinTile + row]);
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    w[g] = g * 32 + lane < p.splits ? ls[g * 32 + lane] : -INFINITY;
-    m = fmaxf(m, w[g]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float acc[kPer], total = 0.0f;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    w[g] = w[g] == -INFINITY ? 0.0f : __expf(w[g] - m);
-    total += w[g];
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int n = min(p.splits - g * 32, 32);
-#pragma unroll 8
-    for (int s = 0; s < n; ++s) {
-      const float ws = __shfl_sync(0xffffffffu, w[g], s);
-      float x[kPer];
-#pragma unroll
-      for (int k = 0; k < kPer; k += 2) {
-        const float2 t = *reinterpret_cast<const float2*>(os + static_cast<int64_t>(g * 32 + s) * D + k);
-        x[k] = t.x;
-        x[k + 1] = t.y;
-      }
-      // a split that saw nothing wrote no output: whatever is there stays out
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[k] += ws == 0.0f ? 0.0f : ws * x[k];
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int s = lane; s < parts; s += 32) {
+      const float l = p.part_lse[slot(s) * kWinTile + row];
+      total += l == -INFINITY ? 0.0f : __expf(l - m);
     }
-  }
-  const float inv = m == -INFINITY ? 0.0f : 1.0f / total;
-  T* const out = static_cast<T*>(p.out) + rh * D + lane * kPer;
 #pragma unroll
-  for (int k = 0; k < kPer; k += 2)
-    *reinterpret_cast<uint32_t*>(out + k) = window_detail::pack16(acc[k] * inv, acc[k + 1] * inv, T{});
-  if (lane == 0 && p.lse) p.lse[rh] = m == -INFINITY ? -INFINITY : m + logf(total);
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const float inv = m == -INFINITY ? 0.0f : 1.0f / total;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int s = group; s < parts; s += kGroups) {
+      const int64_t at = slot(s) * kWinTile + row;
+      const float l = p.part_lse[at];
+      const float4 x = *reinterpret_cast<const float4*>(p.part_o + at * D + col * 4);
+      // a part that saw nothing of this row wrote no output: whatever is there stays out
+      const float w = l == -INFINITY ? 0.0f : __expf(l - m) * inv;
+      if (w != 0.0f) {
+        acc.x += w * x.x;
+        acc.y += w * x.y;
+        acc.z += w * x.z;
+        acc.w += w * x.w;
+      }
+    }
+    sums[group][col] = acc;
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g) {
+        const float4 x = sums[g][col];
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+      }
+      const int tok = row / p.group;
+      const int64_t rh = (static_cast<int64_t>(j.row0) + tok) * p.n_qheads + j.kvh * p.group + (row - tok * p.group);
+      *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + rh * D + col * 4) =
+          make_uint2(window_detail::pack16(acc.x, acc.y, T{}), window_detail::pack16(acc.z, acc.w, T{}));
+      if (col == 0 && p.lse) p.lse[rh] = m == -INFINITY ? -INFINITY : m + logf(total);
+    }
+    __syncthreads();
+  }
 }
 
 template <int D, typename T>
@@ -79,9 +84,8 @@ cudaError_t launch_join_dim(const WindowParams& p, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  const int64_t rows = p.n_rows * p.n_qheads;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.shares), kJoinRows);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -146,11 +150,11 @@ cudaError_t launch_window(const WindowParams& p, int head_dim, bool fp16, bool f
     }
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
   }
-  const int grid = static_cast<int>(p.n_units);
+  const int grid = p.shares > 0 ? p.shares : static_cast<int>(p.n_units);
   const cudaError_t e = head_dim == 64    ? launch_window_d64(p, fp16, fp4, tk, tv, tq1, tqt, grid, stream)
                         : head_dim == 128 ? launch_window_d128(p, fp16, fp4, tk, tv, tq1, tqt, grid, stream)
                                           : launch_window_d256(p, fp16, fp4, tk, tv, tq1, tqt, grid, stream);
-  if (e != cudaSuccess || p.splits <= 1) return e;
+  if (e != cudaSuccess || p.shares == 0) return e;
   return fp16 ? launch_join<__half>(p, head_dim, stream) : launch_join<__nv_bfloat16>(p, head_dim, stream);
 }
 

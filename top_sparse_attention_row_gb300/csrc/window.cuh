@@ -6,10 +6,13 @@
 //   S = scale q.k_j,  m = max S,  O = sum_j exp(S_j - m) v_j / l,  l = sum_j exp(S_j - m),  lse = m + ln l.
 //
 //  * One work unit is a query tile of one request and KV head -- 128 rows, the `group` query heads of
-//    each of 128 / group consecutive tokens, so that every K and V row is read once for all of them --
-//    and, with splits, a contiguous range of its keys.  The grid has a block per unit, and the block on
-//    an SM takes over the units of blocks that have not started (cluster launch control), so that the
-//    SMs stay busy with units of unequal length and no counter in memory is needed.
+//    each of 128 / group consecutive tokens, so that every K and V row is read once for all of them.
+//  * Units are dealt out in one of two ways.  Whole units: the grid has a block per unit, and the block on an
+//    SM takes over the units of blocks that have not started (cluster launch control), so that the SMs stay
+//    busy with units of unequal length and no counter in memory is needed.  Equal shares: with few units
+//    for the SMs, the key tiles of all units are laid end to end (each block sums the units' tiles when it
+//    starts) and cut into one equal run per block; a block's first and last unit may be parts, whose
+//    normalised fp32 rows and log-sum-exps go to a workspace and are joined by a second kernel.
 //  * The keys a unit sees are the sinks and one range [lo, hi): both are laid side by side in a virtual
 //    index v (position v below S0, v + shift from S0 on), which is cut into tiles of 128 keys.  A
 //    window of 4096 costs 33 tiles whatever the context is; boxes that no row sees are not loaded.
@@ -93,7 +96,8 @@ struct WinCfg {
   // staged/unstaged[kDepth] (4-bit caches)
   static constexpr int kBars = 2 * kEntryBars + 7 + kFixBars + 2 * kRecords + (FP4 ? 2 * kDepth : 0);
   static constexpr int kNextAt = (kBarAt + 8 * kBars + 15) / 16 * 16;   // answer of the launch control
-  static constexpr int kTmemSlot = kNextAt + 16;
+  static constexpr int kShareAt = kNextAt + 16;            // Share
+  static constexpr int kTmemSlot = kShareAt + 32;
   static constexpr int kSmem = kTmemSlot + 16;
   static_assert(kSmem <= kSmemLimit, "shared memory");
   static_assert(kStages / kSPT + 2 < kEntryBars, "entry barriers");
@@ -145,7 +149,8 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, int32_t* st
 struct Unit {
   int32_t tiles;       // key tiles of this unit (0: nothing to see, < 0: no more units)
   int32_t tile0;       // first of them
-  int32_t req, kvh, split;
+  int32_t req, kvh;
+  int32_t part;        // slot of the partial result, -1: the unit is whole
   int32_t row0, tokens;
   int32_t p_first;     // position of the first token
   int32_t s0, shift;   // virtual index v: position v below s0, v + shift from s0 on
@@ -161,7 +166,7 @@ __device__ __forceinline__ Unit load_unit(const Unit* u) {
   const int4* s = reinterpret_cast<const int4*>(u);
   const int4 a = s[0], b = s[1], c = s[2], d = s[3];
   r.tiles = a.x; r.tile0 = a.y; r.req = a.z; r.kvh = a.w;
-  r.split = b.x; r.row0 = b.y; r.tokens = b.z; r.p_first = b.w;
+  r.part = b.x; r.row0 = b.y; r.tokens = b.z; r.p_first = b.w;
   r.s0 = c.x; r.shift = c.y; r.lo = c.z; r.hi = c.w;
   r.some0 = d.x; r.some1 = d.y; r.all0 = d.z; r.all1 = d.w;
   return r;
@@ -186,19 +191,17 @@ __device__ __forceinline__ int32_t tile_owner(const WindowParams& p, int32_t til
   return lo;
 }
 
-// Unit `n` of the call, or tiles = -2 for a number without rows.  Warp-uniform; every lane takes part.
-__device__ __forceinline__ Unit make_unit(const WindowParams& p, uint32_t n, int lane) {
+// The unit of virtual tile `tile`, which belongs to request `req`: all its key tiles, or tiles = -2 for a
+// number without rows.  (kvh is left to the caller.)
+__device__ __forceinline__ Unit make_unit(const WindowParams& p, int32_t req, int32_t tile) {
   Unit u{};
-  const uint32_t tk = p.splits > 1 ? n / p.splits : n;
-  u.split = static_cast<int32_t>(n - tk * p.splits);
-  u.kvh = static_cast<int32_t>(tk / p.n_tiles);
-  // a request's later tiles see more keys where there is no window: they go first
-  const int32_t tile = p.n_tiles - 1 - static_cast<int32_t>(tk - static_cast<uint32_t>(u.kvh) * p.n_tiles);
-  u.req = tile_owner(p, tile, lane);
-  const int64_t r0 = __ldg(p.pa.cu_seqlens_q + u.req);
-  int64_t r1 = __ldg(p.pa.cu_seqlens_q + u.req + 1);
+  u.req = req;
+  u.part = -1;
+  const int64_t r0 = __ldg(p.pa.cu_seqlens_q + req);
+  int64_t r1 = __ldg(p.pa.cu_seqlens_q + req + 1);
+  const int64_t kv = __ldg(p.pa.kv_lens + req);
   if (r1 > p.n_rows) r1 = p.n_rows;
-  const int64_t t0 = static_cast<int64_t>(tile - first_tile(p, u.req)) * p.tile_tokens;
+  const int64_t t0 = static_cast<int64_t>(tile - (static_cast<int32_t>(r0) / p.tile_tokens + req)) * p.tile_tokens;
   if (r0 < 0 || t0 < 0 || r0 + t0 >= r1) {
     u.tiles = -2;
     return u;
@@ -206,43 +209,120 @@ __device__ __forceinline__ Unit make_unit(const WindowParams& p, uint32_t n, int
   const int64_t rows = r1 - r0;
   u.row0 = static_cast<int32_t>(r0 + t0);
   u.tokens = static_cast<int32_t>(rows - t0 < p.tile_tokens ? rows - t0 : p.tile_tokens);
-  const int64_t kv = __ldg(p.pa.kv_lens + u.req);
   const int64_t p_first = kv - rows + t0;
   u.p_first = static_cast<int32_t>(p_first);
   const int64_t cap = static_cast<int64_t>(p.pa.pages_per_req) * p.pa.page_size;
   int64_t hi = p_first + u.tokens;
   if (hi > cap) hi = cap;
+  if (hi < 0) hi = 0;
   int64_t lo = p.window > 0 ? p_first - p.window + 1 : 0;
   if (lo < 0) lo = 0;
-  if (lo > hi) lo = hi > 0 ? hi : 0;
-  const int64_t grain = p.box > 0 ? p.box : 4;
-  const int64_t lo_al = lo / grain * grain;
-  int64_t sinks = p.n_sink < lo ? p.n_sink : lo;
-  int64_t s0 = (sinks + grain - 1) / grain * grain, shift = lo_al - s0;
+  if (lo > hi) lo = hi;
+  const int32_t grain = p.box > 0 ? p.box : 4;            // a power of two
+  const int64_t lo_al = lo & ~static_cast<int64_t>(grain - 1);
+  const int64_t sinks = p.n_sink < lo ? p.n_sink : lo;
+  int64_t s0 = (sinks + grain - 1) & ~static_cast<int64_t>(grain - 1), shift = lo_al - s0;
   if (shift <= 0) {   // the sinks reach the window: one run from 0
     s0 = 0;
     shift = 0;
   }
-  const int64_t keys = hi > 0 ? hi - shift : 0;   // virtual length
-  const int64_t all = (keys + kWinTile - 1) / kWinTile;
-  const int64_t a = all * u.split / p.splits, b = all * (u.split + 1) / p.splits;
-  u.tile0 = static_cast<int32_t>(a);
-  u.tiles = static_cast<int32_t>(b - a);
+  u.tiles = static_cast<int32_t>((hi - shift + kWinTile - 1) / kWinTile);   // hi - shift: the virtual length
   u.s0 = static_cast<int32_t>(s0);
   u.shift = static_cast<int32_t>(shift);
   u.lo = static_cast<int32_t>(lo);
-  u.hi = static_cast<int32_t>(hi > 0 ? hi : 0);
+  u.hi = static_cast<int32_t>(hi);
   // the window's run is v >= s0, positions from lo (every row: from the last row's) to hi (the first row's)
   const int64_t p_last = p_first + u.tokens - 1;
   int64_t lo_last = p.window > 0 ? p_last - p.window + 1 : 0;
   if (lo_last < lo) lo_last = lo;
-  const int64_t run0 = lo - u.shift > s0 ? lo - u.shift : u.s0, all_from = lo_last - u.shift > run0 ? lo_last - u.shift : run0;
-  const int64_t all_to = (p_first + 1 < hi ? p_first + 1 : hi) - u.shift;
-  u.some0 = static_cast<int32_t>((run0 + kWinTile - 1) / kWinTile - a);
-  u.some1 = static_cast<int32_t>((u.hi - u.shift) / kWinTile - a);
-  u.all0 = static_cast<int32_t>((all_from + kWinTile - 1) / kWinTile - a);
-  u.all1 = static_cast<int32_t>((all_to > 0 ? all_to : 0) / kWinTile - a);
+  const int64_t run0 = lo - shift > s0 ? lo - shift : s0, all_from = lo_last - shift > run0 ? lo_last - shift : run0;
+  const int64_t all_to = (p_first + 1 < hi ? p_first + 1 : hi) - shift;
+  u.some0 = static_cast<int32_t>((run0 + kWinTile - 1) / kWinTile);
+  u.some1 = static_cast<int32_t>((hi - shift) / kWinTile);
+  u.all0 = static_cast<int32_t>((all_from + kWinTile - 1) / kWinTile);
+  u.all1 = static_cast<int32_t>((all_to > 0 ? all_to : 0) / kWinTile);
   return u;
+}
+// Key tiles [a, b) of a unit.
+__device__ __forceinline__ void cut(Unit& u, int32_t a, int32_t b) {
+  u.tile0 = a;
+  u.tiles = b - a;
+  u.some0 -= a;
+  u.some1 -= a;
+  u.all0 -= a;
+  u.all1 -= a;
+}
+
+// Equal shares: where a block's run of key tiles starts.  A unit counts as its tiles, at least one (a unit that
+// sees nothing still writes its rows).
+struct Share {
+  int64_t size;        // tiles of a share
+  int64_t left;        // of this block's
+  int32_t kvh, tile;   // first unit
+  int32_t offset;      // first tile in it
+};
+// Worked out by all threads of the block; `scratch` has room for 34 int64.  Ends with a barrier.
+template <int THREADS>
+__device__ __forceinline__ void find_share(const WindowParams& p, int64_t* scratch, Share* out) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto weight = [&](int32_t tile) -> int32_t {
+    if (tile >= p.n_tiles) return 0;
+    int32_t lo = 0, hi = p.pa.n_requests - 1;             // the last request whose first tile is <= tile
+    while (lo < hi) {
+      const int32_t mid = (lo + hi + 1) >> 1;
+      if (first_tile(p, mid) <= tile) lo = mid; else hi = mid - 1;
+    }
+    const int32_t t = make_unit(p, lo, tile).tiles;
+    return t == -2 ? 0 : t > 0 ? t : 1;
+  };
+  auto warp_sum = [&](int64_t v) -> int64_t {             // inclusive over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t w = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += w;
+    }
+    return v;
+  };
+  const int32_t w0 = weight(tid);
+  int64_t mine = w0;
+  for (int32_t t = tid + THREADS; t < p.n_tiles; t += THREADS) mine += weight(t);
+  const int64_t in_warp = warp_sum(mine);
+  if (lane == 31) scratch[warp] = in_warp;
+  if (tid == 0) out->left = 0;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) total += scratch[w];
+  __syncthreads();
+  const int64_t all = total * p.n_kvheads, size = (all + p.shares - 1) / p.shares;
+  const int64_t from = size * blockIdx.x;
+  if (from < all) {                                       // uniform over the block
+    const int32_t kvh = static_cast<int32_t>(from / total);
+    const int64_t want = from - kvh * total;
+    int64_t before = 0;
+    for (int32_t c = 0; c < p.n_tiles; c += THREADS) {
+      const int32_t w = c == 0 ? w0 : weight(c + tid);
+      const int64_t incl = warp_sum(w);
+      if (lane == 31) scratch[warp] = incl;
+      __syncthreads();
+      int64_t base = before;
+#pragma unroll
+      for (int k = 0; k < THREADS / 32; ++k) {
+        if (k < warp) base += scratch[k];
+        before += scratch[k];
+      }
+      if (w > 0 && base + incl - w <= want && want < base + incl) {
+        out->size = size;
+        out->left = size < all - from ? size : all - from;
+        out->kvh = kvh;
+        out->tile = c + tid;
+        out->offset = static_cast<int32_t>(want - (base + incl - w));
+      }
+      __syncthreads();
+      if (before > want) break;
+    }
+  }
+  __syncthreads();
 }
 
 __device__ __forceinline__ int32_t position_of(const Unit& u, int32_t v) { return v >= u.s0 ? v + u.shift : v; }
@@ -396,6 +476,8 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     prefetch_tmap(&tmQ1);
     prefetch_tmap(&tmQT);
   }
+  Share* const share = reinterpret_cast<Share*>(smem + C::kShareAt);
+  if (p.shares > 0) find_share<C::kThreads>(p, reinterpret_cast<int64_t*>(smem + C::kMaxAt), share);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -578,12 +660,12 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       const float inv = empty ? 0.0f : p.v_mult / l;
       if (store && wg == 0) {
         const float lse = empty ? -INFINITY : m * sc * kLn2f + logf(l);
-        if (p.splits > 1) p.part_lse[rh * p.splits + u.split] = lse;
+        if (u.part >= 0) p.part_lse[u.part * kWinTile + row] = lse;
         else if (p.lse) p.lse[rh] = lse;
       }
       const uint32_t tm_row = tm_o + lanes + wg * (D / 2);
-      if (warp_live && p.splits > 1) {
-        float* const part = p.part_o + (rh * p.splits + u.split) * D + wg * (D / 2);
+      if (warp_live && u.part >= 0) {
+        float* const part = p.part_o + static_cast<int64_t>(u.part * kWinTile + row) * D + wg * (D / 2);
 #pragma unroll
         for (int c = 0; c < D / 2; c += 32) {
           if (u.tiles == 0) break;
@@ -597,7 +679,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           }
         }
       }
-      if (warp_live && p.splits == 1) {
+      if (warp_live && u.part < 0) {
         uint32_t* const out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + rh * D + wg * (D / 2));
 #pragma unroll
         for (int c = 0; c < D / 2; c += 32) {
@@ -824,20 +906,77 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       more = x >= 0;
       return x;
     };
-    if (warp == 9 && !p.stall_first_item) ask();
+    // whole units: number n of the call
+    auto whole_unit = [&](uint32_t n) -> Unit {
+      const uint32_t kvh = n / static_cast<uint32_t>(p.n_tiles);
+      // a request's later tiles see more keys where there is no window: they go first
+      const int32_t tile = p.n_tiles - 1 - static_cast<int32_t>(n - kvh * static_cast<uint32_t>(p.n_tiles));
+      Unit u = make_unit(p, tile_owner(p, tile, lane), tile);
+      u.kvh = static_cast<int32_t>(kvh);
+      return u;
+    };
+    // equal shares: the next unit of this block's run, whole or a part
+    Share sh = *share;
+    int64_t at = p.shares > 0 ? sh.size * blockIdx.x : 0;
+    bool first_unit = true;
+    JoinRecord join{-1, 0, 0, 0, 0, 0, 0, 0};
+    auto shared_unit = [&]() -> Unit {
+      Unit u{};
+      u.tiles = -1;
+      while (sh.left > 0 && sh.kvh < p.n_kvheads) {
+        const int32_t tile = sh.tile;
+        u = make_unit(p, tile_owner(p, tile, lane), tile);
+        u.kvh = sh.kvh;
+        if (++sh.tile == p.n_tiles) {
+          sh.tile = 0;
+          ++sh.kvh;
+        }
+        if (u.tiles == -2) {
+          u.tiles = -1;
+          continue;
+        }
+        const int32_t w = u.tiles > 0 ? u.tiles : 1, off = sh.offset;
+        if (off >= w) {         // (row offsets that do not increase)
+          sh.offset = 0;
+          u.tiles = -1;
+          continue;
+        }
+        const int32_t take = sh.left < w - off ? static_cast<int32_t>(sh.left) : w - off;
+        if (take < w) {
+          u.part = static_cast<int32_t>(2 * blockIdx.x) + (first_unit ? 0 : 1);
+          if (off == 0) {     // its later parts are the first ones of the blocks that follow
+            const int64_t last = (at + w - 1) / sh.size;
+            join = JoinRecord{u.part, static_cast<int32_t>(last - blockIdx.x), u.row0, u.tokens, u.kvh, 0, 0, 0};
+          }
+          cut(u, off, off + take);
+        }
+        first_unit = false;
+        sh.left -= take;
+        at += take;
+        sh.offset = 0;
+        return u;
+      }
+      return u;
+    };
+    if (warp == 9 && p.shares == 0 && !p.stall_first_item) ask();
+    if (p.shares > 0) more = false;          // no block is taken over
     for (uint32_t it = 0;; ++it) {
       const uint32_t rb = it % C::kRecords, ph = (it / C::kRecords) & 1;
       Unit u;
       if (warp == 9) {
         if (p.stall_first_item && it == 0) break;
-        // (n is the unit in hand, and the answer for the one after it is pending)
-        u.tiles = -1;
-        while (n >= 0) {
-          u = make_unit(p, static_cast<uint32_t>(n), lane);
-          n = pending ? answer() : -1;
-          if (more) ask();
-          if (u.tiles >= 0) break;
+        if (p.shares > 0) {
+          u = shared_unit();
+        } else {
+          // (n is the unit in hand, and the answer for the one after it is pending)
           u.tiles = -1;
+          while (n >= 0) {
+            u = whole_unit(static_cast<uint32_t>(n));
+            n = pending ? answer() : -1;
+            if (more) ask();
+            if (u.tiles >= 0) break;
+            u.tiles = -1;
+          }
         }
         if (!__all_sync(0xffffffffu, wait_for(b_recempty + 8 * rb, ph ^ 1, abort_flag, status, kWRecEmpty))) break;
         if (lane == 0) {
@@ -887,7 +1026,8 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     }
     if (!FP4 && *abort_flag && qit > 0 && lane == 0) drain(b_qfull, (qit - 1) & 1, status, kDrainNs);
     __syncwarp();
-    if (warp == 9 && (*abort_flag || p.stall_first_item)) {
+    if (warp == 9 && lane == 0 && p.shares > 0) p.joins[blockIdx.x] = join;
+    if (warp == 9 && p.shares == 0 && (*abort_flag || p.stall_first_item)) {
       // the call is given up: blocks that have not started are taken off the grid, so that their waits do
       // not run out one after the other
       *abort_flag = 1;
