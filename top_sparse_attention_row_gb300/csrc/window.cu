@@ -12,12 +12,14 @@ namespace {
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 16;      // blocks that share a unit's rows
+constexpr int kJoinWarpParts = 16; // parts up to which a warp takes a row
 
 // Joins the parts of a unit (equal shares): with L_s a part's log-sum-exp and O_s its normalised output,
-// lse = ln sum exp(L_s) and O = sum exp(L_s - lse) O_s.  Block (c, y) takes rows y, y + 16, .. of the unit
-// that begins in block c of the attention grid and goes on in the following ones; D / 4 threads share a row
-// and the groups of threads its parts, which are added in a fixed order, so the result does not depend on
-// timing.
+// lse = ln sum exp(L_s) and O = sum exp(L_s - lse) O_s.  The blocks (c, y) take the rows of the unit that
+// begins in block c of the attention grid and goes on in the following ones.  Two parts are the rule for
+// units of many rows, and then a warp takes a row; a long unit of few rows has a part in every block, and
+// then a block takes a row, D / 4 threads across it and the groups of threads each some of the parts.
+// Parts are added in a fixed order, so the result does not depend on timing.
 template <int D, typename T>
 __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_constant__ WindowParams p) {
   constexpr int kCols = D / 4, kGroups = kJoinThreads / kCols;
@@ -28,6 +30,43 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
   const int tid = threadIdx.x, lane = tid & 31, col = tid % kCols, group = tid / kCols;
   const int parts = j.more + 1;
   auto slot = [&](int s) { return s == 0 ? j.first : 2 * (static_cast<int>(blockIdx.x) + s); };
+  if (parts <= kJoinWarpParts) {
+    constexpr int kPer = D / 32;
+    const int row = blockIdx.y * (kJoinThreads / 32) + (tid >> 5);
+    if (row >= j.tokens * p.group) return;
+    const float l = lane < parts ? p.part_lse[slot(lane) * kWinTile + row] : -INFINITY;
+    float m = l;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float w = l == -INFINITY ? 0.0f : __expf(l - m);
+    float total = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const float inv = m == -INFINITY ? 0.0f : 1.0f / total;
+    float acc[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
+#pragma unroll 2
+    for (int s = 0; s < parts; ++s) {
+      const float ws = __shfl_sync(0xffffffffu, w, s) * inv;
+      const float* const src = p.part_o + static_cast<int64_t>(slot(s) * kWinTile + row) * D + lane * kPer;
+#pragma unroll
+      for (int k = 0; k < kPer; k += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(src + k);
+        if (ws != 0.0f) {
+          acc[k] += ws * x.x;
+          acc[k + 1] += ws * x.y;
+        }
+      }
+    }
+    const int tok = row / p.group;
+    const int64_t rh = (static_cast<int64_t>(j.row0) + tok) * p.n_qheads + j.kvh * p.group + (row - tok * p.group);
+    uint32_t* const out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + rh * D + lane * kPer);
+#pragma unroll
+    for (int k = 0; k < kPer / 2; ++k) out[k] = window_detail::pack16(acc[2 * k], acc[2 * k + 1], T{});
+    if (lane == 0 && p.lse) p.lse[rh] = m == -INFINITY ? -INFINITY : m + logf(total);
+    return;
+  }
   for (int row = blockIdx.y; row < j.tokens * p.group; row += kJoinRows) {
     // every warp works out the parts' total weight
     float m = -INFINITY, total = 0.0f;

@@ -673,9 +673,11 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           tmem_ld32(tm_row + c, o);
           tc_wait_ld();
           if (store && !empty) {
+            uint32_t v[32];
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(part + c + k) = make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv);
+            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(o[k] * inv);
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) st_global_v8(reinterpret_cast<uint32_t*>(part) + c + k, v + k);
           }
         }
       }
