@@ -376,3 +376,20 @@ def test_append_fp4_with_rotation(B, dim, rot, offset, layout):
     _, scv, vv = S.fp4_quantise(v.double().cpu().numpy(), 0.25)
     assert np.array_equal(S.fp4_values(vc.cpu().numpy(), vs.cpu().numpy(), 0.25)[slots], vv)
     assert torch.equal(q_out, B.rope(q, i32(pos), table, layout=layout, rot_offset=offset))
+
+
+def test_append_fp4_non_finite_values_saturate(B):
+    """Infinities keep their sign at the largest magnitude, NaN takes the largest magnitude too, and the
+    other blocks of the row are as they would be."""
+    import torch
+    k = torch.ones((2, 1, 64), device="cuda").bfloat16()
+    k[0, 0, 3], k[0, 0, 20], k[0, 0, 21], k[1, 0, 40] = float("inf"), float("-inf"), 2.0, float("nan")
+    u8 = lambda n: torch.zeros((2, 1, n), dtype=torch.uint8, device="cuda")  # noqa: E731
+    kc, ks, vc, vs = u8(32), u8(4), u8(32), u8(4)
+    seen = torch.empty_like(k)
+    B.rope_append_fp4(None, k, k, kc, ks, vc, vs, None, i32([0, 1]), None, k_seen=seen)
+    torch.cuda.synchronize()
+    got = seen.float().cpu().numpy()[:, 0]
+    assert got[0, 3] == 6 * 448 and got[0, 20] == -6 * 448 and np.all(got[0, [0, 1, 2, 21, 22]] == 0)
+    assert np.all(got[0, 32:] == got[1, 0]) and abs(got[1, 0] - 1) <= 2 ** -4      # scale e4m3(1 / 6), code 6
+    assert abs(got[1, 40]) == 6 * S.E4M3[ks.cpu().numpy()[1, 0, 2]] and np.isfinite(got).all()

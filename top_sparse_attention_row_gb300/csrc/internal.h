@@ -315,6 +315,8 @@ struct RopeParams {
   int32_t heads_per_share;
   float magnitude, sin_sign;    // factor on the cosines, and on the sines (negative: transpose)
   float k_global, v_global;
+  float k_inverse, v_inverse;   // 1 / the global scales where they are powers of two, else 0
+  int32_t wide_q, wide_kv, wide_seen;   // 32-byte accesses
   uint64_t steps[kRopeMaxPairs];   // 2^64 turns per token of each pair
 };
 bool rope_is_aligned(const RopeParams& p);

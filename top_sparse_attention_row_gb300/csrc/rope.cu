@@ -16,10 +16,13 @@
 // 4-bit rows: a block of 16 dims is stored as 16 e2m1 codes (two in a byte, the even dim in the low
 // half) and one e4m3 scale s = e4m3(max|x| / (6 g)), g being the cache's fp32 scale; a code is
 // e2m1((x / g) / s), both rounded to nearest, ties to even.  The rotated values are quantised from fp32.
-// Quotients are true divisions, so that values on the border between two codes fall as the formula says.
+// A quotient that is a border between two codes (x = border times scales: common, since all have few bits)
+// falls as the formula says: see quantise8.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -28,7 +31,7 @@
 namespace qsa {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 __device__ __forceinline__ float2 unpack2(uint32_t v, __nv_bfloat16) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
@@ -50,10 +53,21 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
   memcpy(&r, &h, 4);
   return r;
 }
-// Plain loads and stores: q may be rotated in place.
+// (plain loads: q may be rotated in place)
+// The two 8-element halves of a unit at elements `a` and `b`; b = a + 8 where `joined`, and one 32-byte access
+// then takes both where the rows allow it.
 template <typename T>
-__device__ __forceinline__ uint4 load_raw(const void* base, int64_t elem) {
-  return *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + elem);
+__device__ __forceinline__ void load_halves(const void* base, int64_t row, int a, int b, bool joined, uint4& ra, uint4& rb) {
+  const T* const p = static_cast<const T*>(base) + row;
+  if (joined) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(ra.x), "=r"(ra.y), "=r"(ra.z), "=r"(ra.w), "=r"(rb.x), "=r"(rb.y), "=r"(rb.z), "=r"(rb.w)
+                 : "l"(p + a)
+                 : "memory");
+  } else {
+    ra = *reinterpret_cast<const uint4*>(p + a);
+    rb = *reinterpret_cast<const uint4*>(p + b);
+  }
 }
 template <typename T>
 __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
@@ -66,10 +80,19 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
   }
 }
 template <typename T>
-__device__ __forceinline__ void store8(void* base, int64_t elem, const float* f) {
-  *reinterpret_cast<uint4*>(static_cast<T*>(base) + elem) =
-      make_uint4(pack2(f[0], f[1], T{}), pack2(f[2], f[3], T{}), pack2(f[4], f[5], T{}),
-                 pack2(f[6], f[7], T{}));
+__device__ __forceinline__ void store_halves(void* base, int64_t row, int a, int b, bool joined, const float* f) {
+  T* const p = static_cast<T*>(base) + row;
+  uint32_t w[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = pack2(f[2 * k], f[2 * k + 1], T{});
+  if (joined) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + a), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(p + a) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(p + b) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 // Sine and cosine of the angle at position `pos`, times the magnitude.
@@ -116,16 +139,23 @@ __device__ __forceinline__ float amax8(const float* f) {
   return m;
 }
 
-// Eight dims of a block with scale s (a float that is an e4m3 value): four code bytes; f becomes the
-// values that the codes stand for.
+// Eight dims of a block with scale s (a float that is an e4m3 value), already in units of the cache's
+// scale: four code bytes; f becomes the values that the codes stand for.  A code is the e2m1 value nearest to
+// f / s.  f times the rounded 1 / s is within 2 ulp of the quotient, which decides alike everywhere but at a
+// border; there it is rounded to 20 bits first, which the borders (3 bits) survive and which takes a product
+// that missed its border by those 2 ulp back to it, so that the tie goes to the even code.  (A quotient off a
+// border by less than 2^-21 of itself is taken for a tie; values of at most 11 bits have none.)
 __device__ __forceinline__ uint32_t quantise8(float* f, float s, float g) {
   uint32_t w = 0;
+  const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
   const float sg = s * g;
+  auto code = [&](float x) -> float {
+    const float v = s > 0.0f ? fminf(fmaxf(x * r, -8.0f), 8.0f) : 0.0f;   // (and NaN becomes -8)
+    return __uint_as_float((__float_as_uint(v) + 8u) & ~15u);
+  };
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float a = s > 0.0f ? __fdiv_rn(__fdiv_rn(f[2 * k], g), s) : 0.0f;
-    const float b = s > 0.0f ? __fdiv_rn(__fdiv_rn(f[2 * k + 1], g), s) : 0.0f;
-    const uint32_t byte = e2m1x2(a, b);
+    const uint32_t byte = e2m1x2(code(f[2 * k]), code(f[2 * k + 1]));
     const float2 v = e2m1x2_values(byte);
     f[2 * k] = v.x * sg;
     f[2 * k + 1] = v.y * sg;
@@ -135,27 +165,29 @@ __device__ __forceinline__ uint32_t quantise8(float* f, float s, float g) {
 }
 
 // The two 8-dim halves of a K or V unit (dims da.. and db..) into the 4-bit cache row `cell`; ma and mb
-// are the largest magnitudes of the 16-dim blocks that the halves lie in.
+// are the largest magnitudes of the 16-dim blocks that the halves lie in.  All in units of the cache's scale.
 template <typename T>
 __device__ __forceinline__ void write_fp4(const RopeParams& p, bool is_v, int64_t row, int32_t kvh,
-                                          int64_t cell, int da, int db, float ma, float mb, float* f) {
+                                          int64_t cell, int da, int db, bool joined, float ma, float mb, float* f) {
   const float g = is_v ? p.v_global : p.k_global;
-  const uint8_t ca = e4m3_of(__fdiv_rn(__fdiv_rn(ma, g), 6.0f));
-  const uint8_t cb = e4m3_of(__fdiv_rn(__fdiv_rn(mb, g), 6.0f));
+  const uint8_t ca = e4m3_of(__fdiv_rn(ma, 6.0f));
+  const uint8_t cb = db == da + 8 ? ca : e4m3_of(__fdiv_rn(mb, 6.0f));
   const uint32_t wa = quantise8(f, e4m3_value(ca), g);
   const uint32_t wb = quantise8(f + 8, e4m3_value(cb), g);
   uint8_t* const codes = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + cell * (p.head_dim / 2);
   uint8_t* const scales = (is_v ? p.v_scale : p.k_scale) + cell * (p.head_dim / 16);
-  *reinterpret_cast<uint32_t*>(codes + da / 2) = wa;
-  *reinterpret_cast<uint32_t*>(codes + db / 2) = wb;
+  if (db == da + 8) {
+    *reinterpret_cast<uint2*>(codes + da / 2) = make_uint2(wa, wb);
+  } else {
+    *reinterpret_cast<uint32_t*>(codes + da / 2) = wa;
+    *reinterpret_cast<uint32_t*>(codes + db / 2) = wb;
+  }
   // one lane writes each block's scale: the one that holds the block's first dim
   if ((da & 15) == 0) scales[da / 16] = ca;
   if ((db & 15) == 0) scales[db / 16] = cb;
   void* const seen = is_v ? p.v_seen : p.k_seen;
   if (seen) {
-    const int64_t at = (row * p.n_kvheads + kvh) * p.head_dim;
-    store8<T>(seen, at + da, f);
-    store8<T>(seen, at + db, f + 8);
+    store_halves<T>(seen, (row * p.n_kvheads + kvh) * p.head_dim, da, db, joined && p.wide_seen, f);
   }
 }
 
@@ -163,11 +195,12 @@ __device__ __forceinline__ void write_fp4(const RopeParams& p, bool is_v, int64_
 // Units 0 .. rot/16 - 1 of a q or k head hold the rotated pairs, the others the dims that pass
 // through; V units are plain 16-dim groups.
 template <typename T, bool FP4, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, FP4 ? 4 : 5) rope_rows_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kBatch = 4;   // heads loaded before the first is stored
   const int units = p.head_dim >> 4, rot_units = p.rot_dim >> 4;
   const int64_t total = p.n_rows * units;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRopeThreads;
+  const bool narrow = total <= INT32_MAX;
   const int h0 = blockIdx.y * p.heads_per_share;
   const int h1 = min(h0 + p.heads_per_share, p.n_qheads + p.n_kvheads + p.n_vheads);
   const int q1 = min(h1, p.n_qheads);
@@ -176,8 +209,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
        t0 += stride) {
     const int64_t t = t0 + (threadIdx.x & 31);
     const bool here = t < total;
-    const int64_t row = (here ? t : total - 1) / units;
-    const int u = static_cast<int>((here ? t : total - 1) - row * units);
+    const int64_t tc = here ? t : total - 1;
+    const int64_t row = narrow ? static_cast<uint32_t>(tc) / static_cast<uint32_t>(units) : tc / units;
+    const int u = static_cast<int>(tc - row * units);
     const int32_t pos = p.positions ? __ldg(p.positions + row) : 0;
     const bool live = here && pos >= 0;
 
@@ -191,6 +225,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
       da = d < p.rot_offset ? d : d + p.rot_dim;
       db = da + 8;
     }
+    const bool joined = INTERLEAVED || !turns;   // db = da + 8
     float cs[8], sn[8];
     if (turns && live && h0 < p.n_qheads + p.n_kvheads) {
 #pragma unroll
@@ -211,12 +246,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
         const int64_t to = row * p.q_out_stride + static_cast<int64_t>(h) * p.head_dim;
         uint4 ra[kBatch], rb[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          if (h + k < q1) {
-            ra[k] = load_raw<T>(p.q, at + k * p.head_dim + da);
-            rb[k] = load_raw<T>(p.q, at + k * p.head_dim + db);
-          }
-        }
+        for (int k = 0; k < kBatch; ++k)
+          if (h + k < q1) load_halves<T>(p.q, at + k * p.head_dim, da, db, joined && p.wide_q, ra[k], rb[k]);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           if (h + k < q1) {
@@ -224,8 +255,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
             unpack8<T>(ra[k], f);
             unpack8<T>(rb[k], f + 8);
             if (turns) rotate(f);
-            store8<T>(p.q_out, to + k * p.head_dim + da, f);
-            store8<T>(p.q_out, to + k * p.head_dim + db, f + 8);
+            store_halves<T>(p.q_out, to + k * p.head_dim, da, db, joined && p.wide_q, f);
           }
         }
       }
@@ -238,11 +268,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
       const int kvh = is_v ? h - p.n_qheads - p.n_kvheads : h - p.n_qheads;
       const int ea = is_v ? 16 * u : da, eb = is_v ? 16 * u + 8 : db;
       const int64_t cell = static_cast<int64_t>(slot) * p.n_kvheads + kvh;
+      const bool whole = joined || is_v;
       float f[16];
       if (stored) {
         const int64_t at = row * (is_v ? p.v_stride : p.k_stride) + static_cast<int64_t>(kvh) * p.head_dim;
-        const void* const src = is_v ? p.v : p.k;
-        const uint4 ra = load_raw<T>(src, at + ea), rb = load_raw<T>(src, at + eb);
+        uint4 ra, rb;
+        load_halves<T>(is_v ? p.v : p.k, at, ea, eb, whole && p.wide_kv, ra, rb);
         unpack8<T>(ra, f);
         unpack8<T>(rb, f + 8);
         if (turns && !is_v) rotate(f);
@@ -251,6 +282,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
         for (int k = 0; k < 16; ++k) f[k] = 0.0f;
       }
       if constexpr (FP4) {
+        const float g = is_v ? p.v_global : p.k_global, inv = is_v ? p.v_inverse : p.k_inverse;
+        if (inv != 0.0f) {       // a power of two: the product is the quotient
+#pragma unroll
+          for (int k = 0; k < 16; ++k) f[k] *= inv;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) f[k] = __fdiv_rn(f[k], g);
+        }
         float ma = amax8(f), mb = amax8(f + 8);
         if constexpr (!INTERLEAVED) {
           // a rotated half shares its block with the neighbouring unit's
@@ -262,11 +301,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
         } else {
           ma = mb = fmaxf(ma, mb);
         }
-        if (stored) write_fp4<T>(p, is_v, row, kvh, cell, ea, eb, ma, mb, f);
+        if (stored) write_fp4<T>(p, is_v, row, kvh, cell, ea, eb, whole, ma, mb, f);
       } else if (stored) {
-        void* const cache = is_v ? p.v_cache : p.k_cache;
-        store8<T>(cache, cell * p.head_dim + ea, f);
-        store8<T>(cache, cell * p.head_dim + eb, f + 8);
+        store_halves<T>(is_v ? p.v_cache : p.k_cache, cell * p.head_dim, ea, eb, whole && p.wide_kv, f);
       }
     }
   }
@@ -361,6 +398,19 @@ cudaError_t launch_rope(RopeParams p, bool fp16, bool fp4, int num_sms, cudaStre
     else rope_any_kernel<__nv_bfloat16><<<grid, kRopeThreads, 0, stream>>>(p);
     return cudaGetLastError();
   }
+  // 32-byte accesses where every unit of a row starts on a 32-byte boundary
+  auto wide = [](const void* a, const void* b, int64_t stride_a, int64_t stride_b) {
+    return aligned(a, 32) && aligned(b, 32) && stride_a % 16 == 0 && stride_b % 16 == 0;
+  };
+  p.wide_q = wide(p.q, p.q_out, p.q_stride, p.q_out_stride);
+  p.wide_kv = wide(p.k, p.v, p.k_stride, p.v_stride) && (fp4 || wide(p.k_cache, p.v_cache, 0, 0));
+  p.wide_seen = wide(p.k_seen, p.v_seen, 0, 0);
+  auto inverse = [](float g) {   // 1 / g where that is exact and normal, else 0
+    int e = 0;
+    return std::frexp(g, &e) == 0.5f && e > -124 && e < 124 ? 1.0f / g : 0.0f;
+  };
+  p.k_inverse = inverse(p.k_global);
+  p.v_inverse = inverse(p.v_global);
   // Shares of the heads: as few as still give every SM about 1024 threads, since each share computes
   // a row's angles again.
   const int64_t threads = p.n_rows * (p.head_dim / 16);
