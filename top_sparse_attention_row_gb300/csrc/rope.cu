@@ -104,13 +104,36 @@ __device__ __forceinline__ void angle_of(const RopeParams& p, int i, int32_t pos
   s *= p.sin_sign;   // the magnitude, negative for the transpose
 }
 
-// Two e2m1 codes of a pair of values (b in the upper half of the byte).
-__device__ __forceinline__ uint32_t e2m1x2(float a, float b) {
-  uint16_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.u16.u8 %0, t;\n\t}"
-      : "=h"(r)
-      : "f"(a), "f"(b));
+// Eight values as e2m1 codes, nearest with ties to even, four bits each from the lowest on.
+__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
+}
+// The values of eight codes.
+__device__ __forceinline__ void e2m1x8_values(uint32_t w, float* v) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 t = unpack2(h[k], __half{});
+    v[2 * k] = t.x;
+    v[2 * k + 1] = t.y;
+  }
 }
 __device__ __forceinline__ uint8_t e4m3_of(float a) {
   uint16_t r;
@@ -120,17 +143,14 @@ __device__ __forceinline__ uint8_t e4m3_of(float a) {
 __device__ __forceinline__ float e4m3_value(uint8_t c) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(c)));
-  __half2 h;
-  memcpy(&h, &r, 4);
-  return __low2float(h);
+  return unpack2(r, __half{}).x;
 }
-__device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(r) : "r"(byte));
-  __half2 h;
-  memcpy(&h, &r, 4);
-  return __half22float2(h);
-}
+// Rounded to 20 significant bits.  Quotients are formed as products with a reciprocal, within 2 ulp of the
+// quotient, and decide alike everywhere but on the border between two codes (few bits): this takes a product
+// that missed its border by those 2 ulp back to it, so that the tie goes to the even code.  A quotient off a
+// border by less than 2^-21 of itself is taken for a tie; rows of at most 11 bits have none.  (Infinity stays
+// what it is; NaN must not come here.)
+__device__ __forceinline__ float snap(float v) { return __uint_as_float((__float_as_uint(v) + 8u) & ~15u); }
 
 __device__ __forceinline__ float amax8(const float* f) {
   float m = fabsf(f[0]);
@@ -139,65 +159,64 @@ __device__ __forceinline__ float amax8(const float* f) {
   return m;
 }
 
-// Eight dims of a block with scale s (a float that is an e4m3 value), already in units of the cache's
-// scale: four code bytes; f becomes the values that the codes stand for.  A code is the e2m1 value nearest to
-// f / s.  f times the rounded 1 / s is within 2 ulp of the quotient, which decides alike everywhere but at a
-// border; there it is rounded to 20 bits first, which the borders (3 bits) survive and which takes a product
-// that missed its border by those 2 ulp back to it, so that the tie goes to the even code.  (A quotient off a
-// border by less than 2^-21 of itself is taken for a tie; values of at most 11 bits have none.)
-__device__ __forceinline__ uint32_t quantise8(float* f, float s, float g) {
-  uint32_t w = 0;
-  const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
-  const float sg = s * g;
-  auto code = [&](float x) -> float {
-    const float v = s > 0.0f ? fminf(fmaxf(x * r, -8.0f), 8.0f) : 0.0f;   // (and NaN becomes -8)
-    return __uint_as_float((__float_as_uint(v) + 8u) & ~15u);
-  };
+// Eight dims of a block whose scale's e4m3 value is s: code words; the quotient of f by the scales is f r.
+__device__ __forceinline__ uint32_t quantise8(const float* f, float r) {
+  float v[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t byte = e2m1x2(code(f[2 * k]), code(f[2 * k + 1]));
-    const float2 v = e2m1x2_values(byte);
-    f[2 * k] = v.x * sg;
-    f[2 * k + 1] = v.y * sg;
-    w |= byte << (8 * k);
-  }
-  return w;
+  for (int k = 0; k < 8; ++k) v[k] = snap(fmaxf(f[k] * r, -8.0f));   // (NaN becomes -8, and so -6)
+  return r > 0.0f ? e2m1x8(v) : 0u;
 }
 
 // The two 8-dim halves of a K or V unit (dims da.. and db..) into the 4-bit cache row `cell`; ma and mb
-// are the largest magnitudes of the 16-dim blocks that the halves lie in.  All in units of the cache's scale.
-template <typename T>
-__device__ __forceinline__ void write_fp4(const RopeParams& p, bool is_v, int64_t row, int32_t kvh,
-                                          int64_t cell, int da, int db, bool joined, float ma, float mb, float* f) {
-  const float g = is_v ? p.v_global : p.k_global;
-  const uint8_t ca = e4m3_of(__fdiv_rn(ma, 6.0f));
-  const uint8_t cb = db == da + 8 ? ca : e4m3_of(__fdiv_rn(mb, 6.0f));
-  const uint32_t wa = quantise8(f, e4m3_value(ca), g);
-  const uint32_t wb = quantise8(f + 8, e4m3_value(cb), g);
+// are the largest magnitudes of the 16-dim blocks that the halves lie in (ONE: the same block).  f and the
+// magnitudes are in units of 1 / inv.
+template <typename T, bool ONE>
+__device__ __forceinline__ void write_fp4(const RopeParams& p, bool is_v, int64_t row, int32_t kvh, int64_t cell, int da,
+                                          int db, float inv, float ma, float mb, float* f) {
+  constexpr float kSixth = 1.0f / 6.0f;
+  auto scale_of = [&](float m) { return e4m3_of(snap(m * inv * kSixth)); };
+  auto reciprocal = [&](float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return s > 0.0f ? r * inv : 0.0f;
+  };
+  const uint8_t ca = scale_of(ma), cb = ONE ? ca : scale_of(mb);
+  const float sa = e4m3_value(ca), sb = ONE ? sa : e4m3_value(cb);
+  const float ra = reciprocal(sa), rb = ONE ? ra : reciprocal(sb);
+  const uint32_t wa = quantise8(f, ra), wb = quantise8(f + 8, rb);
   uint8_t* const codes = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + cell * (p.head_dim / 2);
   uint8_t* const scales = (is_v ? p.v_scale : p.k_scale) + cell * (p.head_dim / 16);
-  if (db == da + 8) {
+  if constexpr (ONE) {
     *reinterpret_cast<uint2*>(codes + da / 2) = make_uint2(wa, wb);
+    scales[da / 16] = ca;
   } else {
     *reinterpret_cast<uint32_t*>(codes + da / 2) = wa;
     *reinterpret_cast<uint32_t*>(codes + db / 2) = wb;
+    // one lane writes each block's scale: the one that holds the block's first dim
+    if ((da & 15) == 0) scales[da / 16] = ca;
+    if ((db & 15) == 0) scales[db / 16] = cb;
   }
-  // one lane writes each block's scale: the one that holds the block's first dim
-  if ((da & 15) == 0) scales[da / 16] = ca;
-  if ((db & 15) == 0) scales[db / 16] = cb;
   void* const seen = is_v ? p.v_seen : p.k_seen;
   if (seen) {
-    store_halves<T>(seen, (row * p.n_kvheads + kvh) * p.head_dim, da, db, joined && p.wide_seen, f);
+    const float g = is_v ? p.v_global : p.k_global;
+    e2m1x8_values(wa, f);
+    e2m1x8_values(wb, f + 8);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      f[k] *= sa * g;
+      f[k + 8] *= sb * g;
+    }
+    store_halves<T>(seen, (row * p.n_kvheads + kvh) * p.head_dim, da, db, db == da + 8 && p.wide_seen, f);
   }
 }
 
 // Aligned rows: thread = (row, 16-dim unit); blockIdx.y is a share of the heads (q, then k, then v).
 // Units 0 .. rot/16 - 1 of a q or k head hold the rotated pairs, the others the dims that pass
-// through; V units are plain 16-dim groups.
-template <typename T, bool FP4, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads, FP4 ? 4 : 5) rope_rows_kernel(const __grid_constant__ RopeParams p) {
+// through; V units are plain 16-dim groups.  TURNS false: no pair turns (INTERLEAVED is true then).
+template <typename T, bool FP4, bool INTERLEAVED, bool TURNS>
+__global__ void __launch_bounds__(kRopeThreads, !TURNS ? (FP4 ? 7 : 8) : FP4 ? 4 : 5) rope_rows_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kBatch = 4;   // heads loaded before the first is stored
-  const int units = p.head_dim >> 4, rot_units = p.rot_dim >> 4;
+  const int units = p.head_dim >> 4, rot_units = TURNS ? p.rot_dim >> 4 : 0;
   const int64_t total = p.n_rows * units;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRopeThreads;
   const bool narrow = total <= INT32_MAX;
@@ -215,14 +234,14 @@ __global__ void __launch_bounds__(kRopeThreads, FP4 ? 4 : 5) rope_rows_kernel(co
     const int32_t pos = p.positions ? __ldg(p.positions + row) : 0;
     const bool live = here && pos >= 0;
 
-    const bool turns = u < rot_units;
+    const bool turns = TURNS && u < rot_units;
     int da, db;
     if (turns) {
       da = p.rot_offset + (INTERLEAVED ? 16 * u : 8 * u);
       db = INTERLEAVED ? da + 8 : da + p.rot_dim / 2;
     } else {
       const int d = 16 * (u - rot_units);
-      da = d < p.rot_offset ? d : d + p.rot_dim;
+      da = !TURNS || d < p.rot_offset ? d : d + p.rot_dim;
       db = da + 8;
     }
     const bool joined = INTERLEAVED || !turns;   // db = da + 8
@@ -263,7 +282,21 @@ __global__ void __launch_bounds__(kRopeThreads, FP4 ? 4 : 5) rope_rows_kernel(co
     if (h1 <= p.n_qheads) continue;
     const int32_t slot = __ldg(p.slots + row);
     const bool stored = live && slot >= 0 && slot < p.n_slots;
-    for (int h = max(h0, p.n_qheads); h < h1; ++h) {
+    // K and V heads, two loaded before the first is worked on
+    constexpr int kAhead = 2;
+    uint4 raw[kAhead][2];
+    for (int h = max(h0, p.n_qheads), n = 0; h < h1; ++h, n ^= 1) {
+      if (n == 0 && stored) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          if (h + k >= h1) continue;
+          const bool is_v = h + k >= p.n_qheads + p.n_kvheads;
+          const int kvh = h + k - p.n_qheads - (is_v ? p.n_kvheads : 0);
+          const int64_t at = row * (is_v ? p.v_stride : p.k_stride) + static_cast<int64_t>(kvh) * p.head_dim;
+          load_halves<T>(is_v ? p.v : p.k, at, is_v ? 16 * u : da, is_v ? 16 * u + 8 : db, (joined || is_v) && p.wide_kv,
+                         raw[k][0], raw[k][1]);
+        }
+      }
       const bool is_v = h >= p.n_qheads + p.n_kvheads;
       const int kvh = is_v ? h - p.n_qheads - p.n_kvheads : h - p.n_qheads;
       const int ea = is_v ? 16 * u : da, eb = is_v ? 16 * u + 8 : db;
@@ -271,37 +304,33 @@ __global__ void __launch_bounds__(kRopeThreads, FP4 ? 4 : 5) rope_rows_kernel(co
       const bool whole = joined || is_v;
       float f[16];
       if (stored) {
-        const int64_t at = row * (is_v ? p.v_stride : p.k_stride) + static_cast<int64_t>(kvh) * p.head_dim;
-        uint4 ra, rb;
-        load_halves<T>(is_v ? p.v : p.k, at, ea, eb, whole && p.wide_kv, ra, rb);
-        unpack8<T>(ra, f);
-        unpack8<T>(rb, f + 8);
+        unpack8<T>(n == 0 ? raw[0][0] : raw[1][0], f);
+        unpack8<T>(n == 0 ? raw[0][1] : raw[1][1], f + 8);
         if (turns && !is_v) rotate(f);
       } else {
 #pragma unroll
         for (int k = 0; k < 16; ++k) f[k] = 0.0f;
       }
       if constexpr (FP4) {
-        const float g = is_v ? p.v_global : p.k_global, inv = is_v ? p.v_inverse : p.k_inverse;
-        if (inv != 0.0f) {       // a power of two: the product is the quotient
-#pragma unroll
-          for (int k = 0; k < 16; ++k) f[k] *= inv;
-        } else {
+        float inv = is_v ? p.v_inverse : p.k_inverse;
+        if (inv == 0.0f) {       // not a power of two: true quotients by the cache's scale
+          const float g = is_v ? p.v_global : p.k_global;
 #pragma unroll
           for (int k = 0; k < 16; ++k) f[k] = __fdiv_rn(f[k], g);
+          inv = 1.0f;
         }
         float ma = amax8(f), mb = amax8(f + 8);
         if constexpr (!INTERLEAVED) {
           // a rotated half shares its block with the neighbouring unit's
           const float na = __shfl_xor_sync(0xffffffffu, ma, 1), nb = __shfl_xor_sync(0xffffffffu, mb, 1);
           const bool split = turns && !is_v;
-          const float whole = fmaxf(ma, mb);
-          ma = split ? fmaxf(ma, na) : whole;
-          mb = split ? fmaxf(mb, nb) : whole;
+          const float both = fmaxf(ma, mb);
+          ma = split ? fmaxf(ma, na) : both;
+          mb = split ? fmaxf(mb, nb) : both;
         } else {
           ma = mb = fmaxf(ma, mb);
         }
-        if (stored) write_fp4<T>(p, is_v, row, kvh, cell, ea, eb, whole, ma, mb, f);
+        if (stored) write_fp4<T, INTERLEAVED>(p, is_v, row, kvh, cell, ea, eb, inv, ma, mb, f);
       } else if (stored) {
         store_halves<T>(is_v ? p.v_cache : p.k_cache, cell * p.head_dim, ea, eb, whole && p.wide_kv, f);
       }
@@ -364,15 +393,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const __grid_con
   }
 }
 
-template <typename T>
-cudaError_t launch_rows(const RopeParams& p, bool fp4, dim3 grid, cudaStream_t stream) {
-  if (fp4) {
-    if (p.interleaved) rope_rows_kernel<T, true, true><<<grid, kRopeThreads, 0, stream>>>(p);
-    else rope_rows_kernel<T, true, false><<<grid, kRopeThreads, 0, stream>>>(p);
-  } else {
-    if (p.interleaved) rope_rows_kernel<T, false, true><<<grid, kRopeThreads, 0, stream>>>(p);
-    else rope_rows_kernel<T, false, false><<<grid, kRopeThreads, 0, stream>>>(p);
-  }
+template <typename T, bool FP4>
+cudaError_t launch_rows(const RopeParams& p, dim3 grid, cudaStream_t stream) {
+  if (p.rot_dim == 0) rope_rows_kernel<T, FP4, true, false><<<grid, kRopeThreads, 0, stream>>>(p);
+  else if (p.interleaved) rope_rows_kernel<T, FP4, true, true><<<grid, kRopeThreads, 0, stream>>>(p);
+  else rope_rows_kernel<T, FP4, false, true><<<grid, kRopeThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -421,7 +446,8 @@ cudaError_t launch_rope(RopeParams p, bool fp16, bool fp4, int num_sms, cudaStre
   const int64_t blocks = (threads + kRopeThreads - 1) / kRopeThreads;
   const int64_t cap = static_cast<int64_t>(num_sms) * 64;
   const dim3 grid(static_cast<unsigned>(blocks < cap ? blocks : cap), static_cast<unsigned>(shares));
-  return fp16 ? launch_rows<__half>(p, fp4, grid, stream) : launch_rows<__nv_bfloat16>(p, fp4, grid, stream);
+  if (fp4) return fp16 ? launch_rows<__half, true>(p, grid, stream) : launch_rows<__nv_bfloat16, true>(p, grid, stream);
+  return fp16 ? launch_rows<__half, false>(p, grid, stream) : launch_rows<__nv_bfloat16, false>(p, grid, stream);
 }
 
 }  // namespace qsa

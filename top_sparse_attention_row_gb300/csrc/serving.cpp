@@ -72,7 +72,6 @@ qsa_status run_rope(qsa::RopeParams& p, const qsa_rope_spec* rope, int32_t dtype
     // 16-dim blocks of aligned rows; rotated halves have to fill whole blocks
     if (p.head_dim % 32 != 0 || p.rot_offset % 16 != 0 || p.rot_dim % (p.interleaved ? 16 : 32) != 0)
       return QSA_ERR_UNSUPPORTED;
-    if (!p.interleaved && p.rot_dim == 0) p.interleaved = 1;   // nothing turns: whole blocks per thread
     if (!qsa::rope_is_aligned(p)) return QSA_ERR_INVALID_ARG;
   }
   if (p.n_rows == 0) return QSA_OK;
