@@ -132,3 +132,347 @@ def test_page_sizes(B, ps, fp4):
 def test_head_groups(B, hq, hkv):
     for fp4 in (False, True):
         Batch([(400, 37), (90, 1)], hq, hkv, 64, 16, fp4=fp4, seed=hq).check(B, 90, 2)
+
+
+# ------------------------------------------------------------------------------ masks and bad places
+
+def unseen_slots(b, window, sink):
+    """Cache slots that no row sees."""
+    seen = np.zeros(b.n_pages * b.ps, bool)
+    for i, kv in enumerate(b.kv):
+        new = b.cu[i + 1] - b.cu[i]
+        for p in range(max(kv - new, 0), kv):
+            lo = 0 if window <= 0 else max(0, p - window + 1)
+            js = np.concatenate([np.arange(min(sink, lo)), np.arange(lo, p + 1)])
+            js = js[js < b.table.shape[1] * b.ps]
+            page = b.table[i][js // b.ps]
+            js, page = js[page >= 0], page[page >= 0]
+            seen[page * b.ps + js % b.ps] = True
+    return np.flatnonzero(~seen)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf"), 3e38])
+@pytest.mark.parametrize("dim,window,sink", [(64, 0, 0), (128, 70, 3), (256, 70, 3), (256, 1, 0), (128, 200, 150)])
+def test_anything_in_unseen_places(B, dim, window, sink, value):
+    """The rest of a page, tokens that left the window, unused pages: NaN, infinities and the largest
+    values there change nothing."""
+    import torch
+    b = Batch([(300, 1), (95, 30), (777, 2), (5, 5)], 4, 2, dim, 64, seed=dim)
+    want = b.check(B, window, sink)
+    at = torch.from_numpy(unseen_slots(b, window, sink)).cuda()
+    b.k[at], b.v[at] = value, value
+    got = b.call(B, window, sink)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_anything_in_unseen_places_of_a_4_bit_cache(B, dim):
+    import torch
+    b = Batch([(300, 1), (95, 30), (777, 2), (5, 5)], 4, 2, dim, 64, fp4=True, seed=dim)
+    want = b.check(B, 70, 3)
+    at = torch.from_numpy(unseen_slots(b, 70, 3)).cuda()
+    b.ks[at], b.vs[at], b.k[at], b.v[at] = 0x7F, 0xFF, 0x77, 0xFF       # NaN scales
+    got = b.call(B, 70, 3)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("dim", [64, 256])
+def test_rows_that_see_nothing(B, dim, fp4):
+    """kv_len below the row count puts first rows at negative positions; empty requests and kv_len 0."""
+    b = Batch([(40, 40), (10, 10), (300, 3), (20, 20)], 4, 2, dim, 16, fp4=fp4, seed=1)
+    b.kv = np.array([25, 0, 300, 1])
+    out, lse = b.check(B, 0, 0)
+    assert float(out[:15].abs().max()) == 0 and bool((lse[:15] == -np.inf).all())
+    b.check(B, 8, 2)
+    e = Batch([(70, 0), (50, 50), (9, 0), (9, 0), (300, 7), (1, 0)], 4, 2, dim, 16, fp4=fp4, seed=2)
+    e.check(B, 0, 0)
+    e.check(B, 33, 1)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("ps", [1, 3, 16, 64])
+def test_missing_and_bad_pages(B, ps, fp4):
+    """Entries below 0, past the pool, and positions past the table's row are not seen, wherever they lie."""
+    b = Batch([(400, 60), (333, 1), (200, 5)], 4, 2, 128, ps, fp4=fp4, seed=ps)
+    rng = np.random.default_rng(ps)
+    hit = rng.random(b.table.shape) < 0.2
+    b.table = np.where(hit, rng.choice([-1, -7, b.n_pages, 2 ** 31 - 1], b.table.shape), b.table)
+    b.check(B, 0, 0)
+    b.check(B, 120, 9)
+    b.table = b.table[:, :max(1, b.table.shape[1] // 2)]
+    b.check(B, 0, 0)
+    b.check(B, 120, 9)
+    b.table[:] = -1                                   # no page at all
+    out, lse = b.check(B, 50, 2)
+    assert float(out.abs().max()) == 0
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_padded_batch_leaves_its_last_rows(B, fp4):
+    import torch
+    b = Batch([(100, 3), (300, 1)], 4, 2, 256, 64, fp4=fp4, pad_rows=37)
+    out = torch.full_like(b.q, 7.0)
+    lse = torch.full((b.R, 4), 5.0, device="cuda")
+    b.check(B, 64, 4, out=out, lse=lse)
+    assert bool((out[4:] == 7).all()) and bool((lse[4:] == 5).all())
+    c = Batch([(1500, 600)], 4, 2, 64, 64, fp4=fp4, pad_rows=300)       # whole units
+    out = torch.full_like(c.q, 7.0)
+    c.check(B, 64, 4, out=out, rows=range(0, 600, 7))
+    assert bool((out[600:] == 7).all())
+
+
+# ------------------------------------------------------------------------------ numerics
+
+@pytest.mark.parametrize("dim", [64, 256])
+@pytest.mark.parametrize("order", ["up", "down", "spike"])
+def test_rising_logits(B, dim, order):
+    """Logits that climb by far more than 2^8 from tile to tile, so that O is rescaled again and again."""
+    import torch
+    b = Batch([(900, 40), (640, 1)], 4, 1, dim, 64, seed=4)
+    n = b.n_pages * b.ps
+    ramp = {"up": np.arange(n), "down": n - np.arange(n), "spike": (np.arange(n) % 200 == 0) * n}[order] / n
+    pos = np.zeros(n)
+    for i, kv in enumerate(b.kv):
+        js = np.arange(kv)
+        pos[b.table[i][js // b.ps] * b.ps + js % b.ps] = ramp[js * n // 1000]
+    # q and k along one direction: logits up to 300
+    b.q = torch.zeros_like(b.q)
+    b.q[..., 0] = 16.0
+    b.k[..., 0] = torch.from_numpy(300 * np.sqrt(dim) / 16 * pos).to(b.dt).cuda()[:, None]
+    b.q64, b.k64 = b.q.double().cpu().numpy(), b.k.double().cpu().numpy()
+    b.check(B, 0, 0)
+    b.check(B, 333, 2)
+
+
+@pytest.mark.parametrize("dim,n", [(128, 20000), (256, 9000)])
+@pytest.mark.parametrize("fp4", [False, True])
+def test_long_context_in_equal_shares(B, dim, n, fp4):
+    """One and three decode rows over a long cache: every SM takes a share of the keys."""
+    assert B.window_workspace_bytes(1, 1, n // 64, 64, 4, 1, dim, 0, 0, fp4=fp4, num_sms=152) > 0
+    Batch([(n, 1)], 4, 1, dim, 64, fp4=fp4, seed=1).check(B, 0, 0)
+    Batch([(n, 1), (3, 1), (n // 3, 1)], 4, 1, dim, 64, fp4=fp4, seed=2).check(B, 0, 0)
+    Batch([(n, 3)], 4, 1, dim, 64, fp4=fp4, seed=3).check(B, n // 2, 700)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("dim,hq,hkv", [(64, 8, 8), (128, 16, 2), (256, 6, 1)])
+def test_long_prompt(B, dim, hq, hkv, dtype):
+    """Enough query tiles for whole units, and a few more than SMs for equal shares with full tiles."""
+    rng = np.random.default_rng(0)
+    b = Batch([(3500, 2900)], hq, hkv, dim, 64, dtype, seed=dim)
+    rows = rng.choice(2900, 60, replace=False)
+    b.check(B, 0, 0, rows=rows)
+    b.check(B, 500, 4, rows=rows)
+
+
+def test_many_requests(B):
+    rng = np.random.default_rng(9)
+    lens = [(int(n), int(min(n, m))) for n, m in zip(rng.integers(1, 200, 400), rng.integers(0, 4, 400))]
+    for fp4 in (False, True):
+        Batch(lens, 2, 1, 64, 16, fp4=fp4, seed=5).check(B, 40, 2)
+
+
+def test_random_batches(B):
+    """Shapes drawn at random over the whole range."""
+    rng = np.random.default_rng(11)
+    for k in range(24):
+        n = int(rng.integers(1, 9))
+        lens = []
+        for _ in range(n):
+            new = int(rng.choice([0, 1, 1, rng.integers(1, 150)]))
+            lens.append((new + int(rng.integers(0, 700)), new))
+        if sum(m for _, m in lens) == 0:
+            lens[0] = (lens[0][0] + 1, 1)
+        hkv = int(rng.choice([1, 2, 3]))
+        b = Batch(lens, hkv * int(rng.choice([1, 2, 5, 7, 16])), hkv, int(rng.choice([64, 128, 256])),
+                  int(rng.choice([1, 5, 8, 16, 40, 64, 128])), str(rng.choice(["bfloat16", "float16"])),
+                  fp4=bool(rng.integers(2)), seed=100 + k, pad_rows=int(rng.integers(0, 3)))
+        b.check(B, int(rng.choice([0, 1, 17, 128, 300])), int(rng.choice([0, 1, 4, 64, 129])))
+
+
+def test_results_repeat_bit_for_bit(B):
+    import torch
+    for fp4 in (False, True):
+        b = Batch([(5000, 1), (900, 200)], 8, 2, 128, 64, fp4=fp4)
+        first = b.call(B, 700, 4)
+        for _ in range(5):
+            again = b.call(B, 700, 4)
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_offsets_past_32_bits(B):
+    """A cache of more than 4 GiB, the pages in use at its end."""
+    import torch
+    for fp4 in (False, True):
+        b = Batch([(200, 3), (90, 1)], 2, 2, 256, 64, fp4=fp4)
+        rows = (1 << 32) // (b.k.stride(0) * b.k.element_size()) + 64
+        far = -(-rows // 64)                               # pages in front
+        grow = lambda t: torch.cat([torch.zeros((far * 64, *t.shape[1:]), dtype=t.dtype, device="cuda"), t])  # noqa: E731
+        want = b.check(B, 100, 4)
+        b.k, b.v = grow(b.k), grow(b.v)
+        if fp4:
+            b.ks, b.vs = grow(b.ks), grow(b.vs)
+        b.table = np.where(b.table >= 0, b.table + far, -1)
+        got = b.call(B, 100, 4)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ------------------------------------------------------------------------------ how it is called
+
+def test_outputs_workspaces_and_alignment(B):
+    import torch
+    b = Batch([(3000, 1), (800, 20)], 6, 1, 256, 64)
+    want = b.check(B, 0, 0)
+    odd = torch.empty(b.q.numel() + 8, dtype=b.dt, device="cuda")[8:].view(b.q.shape)      # 16-byte aligned only
+    got = b.call(B, 0, 0, out=odd, want_lse=False)
+    assert got[1] is None and got[0].data_ptr() % 32 == 16 and torch.equal(got[0], want[0])
+    args = (b.R, 2, b.table.shape[1], 64, 6, 1, 256, 0, 0)
+    n = B.window_workspace_bytes(*args)
+    assert n > 0
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")                          # NaN everywhere
+    assert torch.equal(b.call(B, 0, 0, workspace=ws)[0], want[0])
+    for bad in (ws[:n - 1], ws[8:]):
+        with pytest.raises(RuntimeError, match="WORKSPACE"):
+            b.call(B, 0, 0, workspace=bad)
+    # the C entry without a workspace takes one from the library's pool
+    lib, out = B.load_library(), torch.empty_like(b.q)
+    cu, kv, table = i32(b.cu), i32(b.kv), i32(b.table)
+    st = lib.qsa_window_attention_paged(
+        b.q.data_ptr(), b.k.data_ptr(), b.v.data_ptr(), cu.data_ptr(), kv.data_ptr(), table.data_ptr(), out.data_ptr(),
+        None, b.R, 2, b.table.shape[1], 64, b.n_pages, 6, 1, 256, b.scale, 0, 0, 0, None, 0,
+        torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and torch.equal(out, want[0])
+    assert b.call(B, 0, 0, out=odd[:0] if False else None)[0].shape == b.q.shape
+    empty = Batch([(30, 0)], 6, 1, 256, 64)
+    assert empty.call(B, 0, 0)[0].shape == (0, 6, 256)
+
+
+def test_two_streams_at_once(B):
+    import torch
+    bs = [Batch([(4000 + 7 * k, 1), (700, 30)], 6, 1, 256, 64, seed=k) for k in range(2)]
+    want = [b.check(B, 0, 0) for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    got = [[b.call(B, 0, 0, stream=s) for b, s in zip(bs, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for g, w in zip(pair, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+    with torch.cuda.stream(streams[0]):
+        a = bs[1].call(B, 0, 0)
+    streams[0].synchronize()
+    assert torch.equal(a[0], want[1][0])
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_decode_steps_replay_from_a_graph(B, fp4):
+    """Plan, append and attention of a decode step captured once; the lengths grow with every replay, past
+    page and tile borders, and every step agrees with the oracle on the rows so far."""
+    import torch
+    rng = np.random.default_rng(3)
+    n, hq, hkv, dim, ps, ppr, steps = 3, 4, 2, 64, 16, 24, 150
+    start = np.array([0, 100, 250])
+    table, free, head = i32(np.full((n, ppr), -1)), i32(rng.permutation(n * ppr)), i32([0])
+    past, new = i32(np.zeros(n)), i32(start)
+    s = n * ppr * ps
+    dt = torch.bfloat16
+    caches = ([torch.zeros((s, hkv, w), dtype=torch.uint8, device="cuda") for w in (dim // 2, dim // 16) * 2] if fp4 else
+              [torch.zeros((s, hkv, dim), dtype=dt, device="cuda") for _ in range(2)])
+    rope = B.rope_table(dim, 10000.0)
+
+    def step(qkv, plan):
+        q, k, v = (t.unflatten(1, (-1, dim)) for t in qkv.split([hq * dim, hkv * dim, hkv * dim], 1))
+        if fp4:
+            kc, ks, vc, vs = caches
+            q = B.rope_append_fp4(q, k, v, kc, ks, vc, vs, plan.positions, plan.slots, rope)
+            return q, B.window_attention_fp4_paged(q, kc, ks, vc, vs, plan.cu_seqlens_q, plan.kv_lens, table, ps, 0.125,
+                                                   window=120, n_sink=3)
+        q = B.rope_append(q, k, v, *caches, plan.positions, plan.slots, rope)
+        return q, B.window_attention_paged(q, *caches, plan.cu_seqlens_q, plan.kv_lens, table, ps, 0.125, window=120,
+                                           n_sink=3)
+
+    width = (hq + 2 * hkv) * dim
+    plan = B.page_plan(past, new, table, free, head, ps, int(start.sum()), free_head_out=head)     # the prompts
+    step(torch.randn((int(start.sum()), width), device="cuda").to(dt), plan)
+    past.copy_(plan.kv_lens)
+    new.fill_(1)
+    qkv = torch.randn((n, width), device="cuda").to(dt)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):                     # opt-ins outside the capture, on tables of their own
+        t2, h2 = table.clone(), head.clone()
+        B.page_plan(past, new, t2, free, h2, ps, n, free_head_out=h2)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        plan = B.page_plan(past, new, table, free, head, ps, n, free_head_out=head)
+        q, (out, lse) = step(qkv, plan)
+        past.copy_(plan.kv_lens)
+    for t in range(steps):
+        qkv.copy_(torch.from_numpy(rng.standard_normal((n, width))).to(dt))
+        g.replay()
+        torch.cuda.synchronize()
+        assert B.device_status() == 0 and int(plan.shortfall) == 0
+        if t % 29 and t != steps - 1:
+            continue
+        b = Batch.__new__(Batch)
+        b.dt, b.dim, b.ps, b.fp4, b.scale = dt, dim, ps, fp4, 0.125
+        b.cu, b.kv, b.table = np.arange(n + 1), start + t + 1, table.cpu().numpy()
+        assert np.array_equal(plan.kv_lens.cpu().numpy(), b.kv)
+        b.q64 = q.double().cpu().numpy()
+        c = [x.cpu().numpy() if fp4 else x.double().cpu().numpy() for x in caches]
+        b.k64, b.v64 = (S.fp4_values(c[0], c[1], 1.0), S.fp4_values(c[2], c[3], 1.0)) if fp4 else c
+        b.compare(out, lse, 120, 3)
+
+
+def test_prefill_and_decode_agree_with_dense_attention(B):
+    """Prompt rows fed in chunks through plan, append and attention give what dense causal attention of the
+    rotated rows gives; the last rows fed one by one give the same again."""
+    import torch
+    rng = np.random.default_rng(5)
+    hq, hkv, dim, ps, n = 4, 2, 128, 32, 400
+    q, k, v = (torch.from_numpy(rng.standard_normal((n, h, dim))).bfloat16().cuda() for h in (hq, hkv, hkv))
+    w, mag = S.rope_frequencies(64, 10000.0)
+    qr, kr = (S.rope(x.double().cpu().numpy(), np.arange(n), w, mag, True, 32) for x in (q, k))
+    rope = B.rope_table(64, 10000.0)
+    table, free, head = i32(np.full((1, 16), -1)), i32(rng.permutation(16)), i32([0])
+    kc, vc = (torch.full((16 * ps, hkv, dim), float("nan"), device="cuda").bfloat16() for _ in range(2))
+    rows, at = [], 0
+    for m in [1, 150, 37, 200] + [1] * 12:
+        plan = B.page_plan(i32([at]), i32([m]), table, free, head, ps, m, free_head_out=head)
+        s = slice(at, at + m)
+        x = B.rope_append(q[s], k[s], v[s], kc, vc, plan.positions, plan.slots, rope, layout="interleaved", rot_offset=32)
+        out, lse = B.window_attention_paged(x, kc, vc, plan.cu_seqlens_q, plan.kv_lens, table, ps, dim ** -0.5)
+        rows.append(out)
+        at += m
+    got = torch.cat(rows).double().cpu().numpy()
+    vd = v.double().cpu().numpy()
+    s = np.einsum("rhd,jhd->hrj", qr, np.repeat(kr, 2, 1)) * dim ** -0.5
+    s = np.where(np.tril(np.ones((n, n), bool)), s, -np.inf)
+    e = np.exp(s - s.max(-1, keepdims=True))
+    e /= e.sum(-1, keepdims=True)
+    want = np.einsum("hrj,jhd->rhd", e, np.repeat(vd, 2, 1))
+    a = np.einsum("hrj,jhd->rhd", e, np.repeat(np.abs(vd), 2, 1))
+    # weights, output, and q and k rounded to bf16 (half a step 2^-8 each): the latter move a logit by at most
+    # 2 * 2^-8 sum |q k| scale, with sum |q k| scale <= 0.64 sqrt(dim) on average for N(0, 1) rows, taken twofold
+    u = 2.0 ** -8
+    bound = u * a + u * np.abs(want) + 2 * (2 * u * 2 * 0.64 * np.sqrt(dim)) * a
+    assert np.all(np.abs(got - want) <= bound)
+
+
+def test_stalled_call_times_out_and_the_context_recovers(B):
+    import time
+    import torch
+    for lens in ([(700, 1)], [(3000, 2500)]):                # equal shares, whole units
+        b = Batch(lens, 4, 4, 128, 64)
+        B.debug_stall_next_call()
+        t0 = time.time()
+        b.call(B, 0, 0)
+        torch.cuda.synchronize()
+        assert B.device_status() == 0x142                    # the wait for a unit's record
+        assert 1.0 < time.time() - t0 < 20.0
+        b.check(B, 0, 0, rows=range(0, b.R, 97))

@@ -210,3 +210,52 @@ def test_oracle_rope_is_a_rotation():
     a, b = rng.standard_normal((1, 1, 8)), rng.standard_normal((1, 1, 8))
     dot = lambda p, r: float(np.sum(S.rope(a, [p], w, 1.0, False, 0) * S.rope(b, [r], w, 1.0, False, 0)))  # noqa: E731
     assert abs(dot(10, 3) - dot(107, 100)) < 1e-12
+
+
+def window_args(**kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, cu=FAKE, kv=FAKE, table=FAKE, out=FAKE, lse=None, rows=0, n=2, ppr=4, ps=64, n_pages=8,
+             hq=6, hkv=1, d=256, scale=0.0625, window=0, sink=0, dtype=0, ws=None, ws_bytes=0, stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return list(a.values())
+
+
+WINDOW_REFUSALS = [
+    ({}, OK), (dict(window=7, sink=3, dtype=1), OK), (dict(d=64), OK), (dict(d=128), OK),
+    (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(cu=None), INVALID),
+    (dict(kv=None), INVALID), (dict(table=None), INVALID), (dict(out=None), INVALID), (dict(q=FAKE + 8), INVALID),
+    (dict(out=FAKE + 8), INVALID), (dict(lse=FAKE + 2), INVALID), (dict(rows=-1), INVALID), (dict(n=0), INVALID),
+    (dict(ppr=0), INVALID), (dict(ps=0), INVALID), (dict(n_pages=0), INVALID), (dict(hq=5, hkv=2), INVALID),
+    (dict(window=-1), INVALID), (dict(sink=-1), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID), (dict(dtype=2), INVALID),
+    (dict(d=96), UNSUPPORTED), (dict(hq=129), UNSUPPORTED), (dict(rows=(1 << 31) - 2), UNSUPPORTED),
+    (dict(n_pages=1 << 26), UNSUPPORTED), (dict(n_pages=1 << 24, hkv=2), UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("kw,status", WINDOW_REFUSALS)
+def test_window_attention_refusals(B, kw, status):
+    assert B.load_library().qsa_window_attention_paged(*window_args(**kw)) == status
+
+
+@pytest.mark.parametrize("kw,extra,status", [
+    (dict(), {}, OK), (dict(), dict(ks=None), INVALID), (dict(), dict(vs=FAKE + 4), INVALID), (dict(), dict(kg=0.0), INVALID),
+    (dict(), dict(vg=math.inf), INVALID), (dict(hq=64), {}, OK), (dict(hq=65), {}, UNSUPPORTED), (dict(hq=128, d=128), {}, OK),
+])
+def test_window_attention_fp4_refusals(B, kw, extra, status):
+    q, k, v, *rest = window_args(**kw)
+    e = dict(ks=FAKE, vs=FAKE, kg=1.0, vg=1.0)
+    e.update(extra)
+    assert B.load_library().qsa_window_attention_fp4_paged(q, k, e["ks"], v, e["vs"], e["kg"], e["vg"], *rest) == status
+
+
+def test_window_workspace_bytes(B):
+    """Equal shares where there are few query tiles, whole units where there are many."""
+    f = lambda rows, n, ppr, **kw: B.window_workspace_bytes(rows, n, ppr, 64, 24, 2, 256, 0, 0, num_sms=152, **kw)  # noqa: E731
+    one = 2 * 128 * 257 * 4 + 32
+    assert f(1, 1, 512) == 152 * one and f(1, 1, 40) == 40 * one     # two KV heads of 20 tiles each
+    assert f(1, 1, 2) == 0                                           # one tile: nothing to share
+    assert f(48, 48, 512, fp4=True) == 152 * one
+    assert f(100000, 1, 2000) == 0
+    assert B.window_workspace_bytes(0, 1, 4, 64, 24, 2, 256, 0, 0, num_sms=152) == 0
+    assert B.window_workspace_bytes(1, 1, 4, 64, 24, 5, 256, 0, 0, num_sms=152) == 0

@@ -93,7 +93,8 @@ struct WindowPlan {
   int32_t tile_tokens, n_tiles, shares;
   int64_t n_units;
 };
-constexpr int32_t kMaxShareTiles = 1 << 16;    // every block sums all units' tiles
+constexpr int32_t kMaxShareTiles = 1 << 14;    // every block sums all units' tiles
+constexpr double kMaxShareLoad = 16.0;         // rounds from which whole units leave few SMs idle
 WindowPlan plan_window(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, int32_t group, int32_t tile_rows,
                        int64_t max_keys, int32_t window, int32_t n_sink, int32_t sms) {
   WindowPlan w{};
@@ -114,6 +115,7 @@ WindowPlan plan_window(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, in
   const int64_t rows_per = n_rows < tiles * w.tile_tokens ? (n_rows + tiles - 1) / tiles : w.tile_tokens;
   const double partial = static_cast<double>(rows_per * group) / qsa::kWinTile;
   const double load = static_cast<double>(items) / sms;
+  if (load > kMaxShareLoad) return w;
   const double whole = std::ceil(load) * (kt + 3.0);
   const int64_t shares = items * kt < sms ? items * kt : sms;
   const double even = static_cast<double>(items) * kt / shares + (load + 1.0) * 3.0 + 4.0 * partial + 3.0;

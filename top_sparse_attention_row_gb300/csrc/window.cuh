@@ -853,10 +853,12 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         if (u.tiles < 0) break;
         bool ok = true;
         for (int j = 0; j < u.tiles && ok; ++j) {
-          if (j >= u.some0 && j < u.some1) continue;
+          // (every V entry is waited for, so that no barrier is more than one phase ahead of this warp: a
+          // parity tells no more than that)
           const uint32_t e = v_entry(j, u.tiles);
           ok = __all_sync(0xffffffffu, wait_entry(b_landed, eb + e, kWLanded));
           if (!ok) break;
+          if (j >= u.some0 && j < u.some1) continue;
           for (int k = 0; k < kWinTile / 64; ++k) {
             const int row = k * 64 + (warp - 10) * 32 + lane;
             if (seen(p, u, position_of(u, (u.tile0 + j) * kWinTile + row))) continue;
