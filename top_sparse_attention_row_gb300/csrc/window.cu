@@ -10,9 +10,9 @@
 namespace qsa {
 namespace {
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
 constexpr int kJoinRows = 16;      // blocks that share a unit's rows
-constexpr int kJoinWarpParts = 16; // parts up to which a warp takes a row
+constexpr int kJoinWarpParts = 8;  // parts up to which a warp takes a row
 
 // Joins the parts of a unit (equal shares): with L_s a part's log-sum-exp and O_s its normalised output,
 // lse = ln sum exp(L_s) and O = sum exp(L_s - lse) O_s.  The blocks (c, y) take the rows of the unit that
@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
   auto slot = [&](int s) { return s == 0 ? j.first : 2 * (static_cast<int>(blockIdx.x) + s); };
   if (parts <= kJoinWarpParts) {
     constexpr int kPer = D / 32;
-    const int row = blockIdx.y * (kJoinThreads / 32) + (tid >> 5);
+    const int row = blockIdx.y * (kJoinThreads / 32) + (tid >> 5);   // 16 x 16 rows are more than a unit has
     if (row >= j.tokens * p.group) return;
     const float l = lane < parts ? p.part_lse[slot(lane) * kWinTile + row] : -INFINITY;
     float m = l;
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
     float acc[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
-#pragma unroll 2
+#pragma unroll 4
     for (int s = 0; s < parts; ++s) {
       const float ws = __shfl_sync(0xffffffffu, w, s) * inv;
       const float* const src = p.part_o + static_cast<int64_t>(slot(s) * kWinTile + row) * D + lane * kPer;
@@ -68,32 +68,55 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
     return;
   }
   for (int row = blockIdx.y; row < j.tokens * p.group; row += kJoinRows) {
-    // every warp works out the parts' total weight
+    // the first parts' rows are on their way while every warp works out the parts' total weight
+    constexpr int kFirst = 4, kLaneParts = 5;              // (a unit has at most 152 parts, 160 fit)
+    float4 x[kFirst];
+    float lx[kFirst], l[kLaneParts];
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) {
+      const int s = group + i * kGroups;
+      lx[i] = -INFINITY;
+      if (s < parts) {
+        const int64_t at = slot(s) * kWinTile + row;
+        lx[i] = p.part_lse[at];
+        x[i] = *reinterpret_cast<const float4*>(p.part_o + at * D + col * 4);
+      }
+    }
     float m = -INFINITY, total = 0.0f;
-    for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.part_lse[slot(s) * kWinTile + row]);
+#pragma unroll
+    for (int i = 0; i < kLaneParts; ++i) {
+      const int s = lane + 32 * i;
+      l[i] = s < parts ? p.part_lse[slot(s) * kWinTile + row] : -INFINITY;
+      m = fmaxf(m, l[i]);
+    }
+    for (int s = lane + 32 * kLaneParts; s < parts; s += 32) m = fmaxf(m, p.part_lse[slot(s) * kWinTile + row]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int s = lane; s < parts; s += 32) {
-      const float l = p.part_lse[slot(s) * kWinTile + row];
-      total += l == -INFINITY ? 0.0f : __expf(l - m);
+#pragma unroll
+    for (int i = 0; i < kLaneParts; ++i) total += l[i] == -INFINITY ? 0.0f : __expf(l[i] - m);
+    for (int s = lane + 32 * kLaneParts; s < parts; s += 32) {
+      const float v = p.part_lse[slot(s) * kWinTile + row];
+      total += v == -INFINITY ? 0.0f : __expf(v - m);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     const float inv = m == -INFINITY ? 0.0f : 1.0f / total;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // a part that saw nothing of this row wrote no output: whatever is there stays out
+    auto add = [&](float v, const float4& o) {
+      if (v == -INFINITY) return;
+      const float w = __expf(v - m) * inv;
+      acc.x += w * o.x;
+      acc.y += w * o.y;
+      acc.z += w * o.z;
+      acc.w += w * o.w;
+    };
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) add(lx[i], x[i]);
 #pragma unroll 4
-    for (int s = group; s < parts; s += kGroups) {
+    for (int s = group + kFirst * kGroups; s < parts; s += kGroups) {
       const int64_t at = slot(s) * kWinTile + row;
-      const float l = p.part_lse[at];
-      const float4 x = *reinterpret_cast<const float4*>(p.part_o + at * D + col * 4);
-      // a part that saw nothing of this row wrote no output: whatever is there stays out
-      const float w = l == -INFINITY ? 0.0f : __expf(l - m) * inv;
-      if (w != 0.0f) {
-        acc.x += w * x.x;
-        acc.y += w * x.y;
-        acc.z += w * x.z;
-        acc.w += w * x.w;
-      }
+      add(p.part_lse[at], *reinterpret_cast<const float4*>(p.part_o + at * D + col * 4));
     }
     sums[group][col] = acc;
     __syncthreads();
