@@ -45,7 +45,11 @@ Functions and the passages they follow:
   one scale per page and KV head, dequantised as e4m3(x) * scale ("DSA prefill
   ... triton_sparse_mla", Robustness and Accuracy Tests: dequantised rows).
 
-Every function is pinned by ``tests/test_oracle_pins.py`` against facts that
+* ``serving`` -- the serving step's operators: page plans, rotary positions, 4-bit cache rows and
+  sliding-window attention (definitions of this library, stated in include/qsa.h; pinned by
+  ``tests/test_serving_args.py`` and by agreement with dense attention).
+
+Every other function is pinned by ``tests/test_oracle_pins.py`` against facts that
 do not come from this package: dense causal attention from a library routine
 (sparse must equal dense when the selection is the whole causal prefix), a
 library log-sum-exp, closed forms, invariances, and brute-force set

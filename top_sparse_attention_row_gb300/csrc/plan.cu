@@ -188,6 +188,10 @@ cudaError_t launch_page_plan(PagePlanParams p, cudaStream_t stream) {
   const int64_t work = rows > p.n_requests ? rows : p.n_requests;
   p.cluster = 1;
   while (p.cluster < 8 && static_cast<int64_t>(p.cluster) * 2048 < work) p.cluster *= 2;
+  if (p.cluster == 1) {
+    page_plan_kernel<<<1, kThreadsPlan, smem, stream>>>(p);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

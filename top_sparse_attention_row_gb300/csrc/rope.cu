@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kRopeThreads, !TURNS ? (FP4 ? 7 : 8) : FP4 ? 4
         f[ib] = b * cs[k] + a * sn[k];
       }
     };
-    if (live) {
+    if (live && (turns || p.q != p.q_out)) {     // (in place, passing dims stay where they are)
       for (int h = h0; h < q1; h += kBatch) {
         const int64_t at = row * p.q_stride + static_cast<int64_t>(h) * p.head_dim;
         const int64_t to = row * p.q_out_stride + static_cast<int64_t>(h) * p.head_dim;
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const __grid_con
         if (e < pairs) dst[per_head + e] = src[per_head + e];
       } else {
         const int d = e - pairs, at = d < p.rot_offset ? d : d + p.rot_dim;
-        dst[at] = src[at];
+        if (src != dst) dst[at] = src[at];
       }
       continue;
     }
