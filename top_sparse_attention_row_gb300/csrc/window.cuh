@@ -91,17 +91,19 @@ struct WinCfg {
   static constexpr int kBadAt = kMaxAt + 2048;             // [kBadSlots][8] uint32
   static constexpr int kRecAt = kBadAt + kBadSlots * 32;   // [kRecords] Unit
   static constexpr int kBarAt = kRecAt + kRecords * 64;
-  static constexpr int kFixBars = 8;                       // > V tiles that may be zeroed ahead of the MMA
-  // landed[16], done[16] (by entry), pfull[2], qfull, qempty, ofree, fin, next, vready[8], recfull/empty,
-  // staged/unstaged[kDepth] (4-bit caches)
-  static constexpr int kBars = 2 * kEntryBars + 7 + kFixBars + 2 * kRecords + (FP4 ? 2 * kDepth : 0);
+  static constexpr int kTileBars = 8;                      // > tiles in flight
+  // done[16] (by entry), kready[8], pvready[8], vlanded[8] (by tile), qfull, qempty, ofree, fin, next,
+  // recfull/empty, staged/unstaged[kDepth] (4-bit caches)
+  static constexpr int kBars = kEntryBars + 3 * kTileBars + 5 + 2 * kRecords + (FP4 ? 2 * kDepth : 0);
   static constexpr int kNextAt = (kBarAt + 8 * kBars + 15) / 16 * 16;   // answer of the launch control
   static constexpr int kShareAt = kNextAt + 16;            // Share
-  static constexpr int kTmemSlot = kShareAt + 32;
+  static constexpr int kTagAt = kShareAt + 32;             // [kDepth] uint32 (4-bit caches)
+  static constexpr int kTmemSlot = kTagAt + (FP4 ? 32 : 0);
   static constexpr int kSmem = kTmemSlot + 16;
   static_assert(kSmem <= kSmemLimit, "shared memory");
   static_assert(kStages / kSPT + 2 < kEntryBars, "entry barriers");
-  static_assert(kStages / kSPT / 2 + 1 < kFixBars, "zeroing barriers");
+  static_assert(kStages / kSPT / 2 + 1 < kTileBars, "tile barriers");
+  static_assert(kRows == kWinTile || FP4, "query rows");
 };
 
 namespace window_detail {
@@ -111,7 +113,7 @@ constexpr float kRaise = 8.0f;          // log2 units by which a tile may exceed
 constexpr float kLn2f = 0.6931471805599453f;
 enum Site : int32_t {
   kWRecEmpty = 0x41, kWRecFull, kWQEmpty, kWQFull, kWStageEmpty, kWLanded, kWSFull, kWPFull, kWPvDone,
-  kWOFree, kWNext, kWVReady, kWStaged, kWUnstaged, kWDrain
+  kWOFree, kWNext, kWStaged, kWUnstaged, kWDrain
 };
 
 __device__ __forceinline__ unsigned long long now_ns() {
@@ -411,16 +413,17 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
   using C = WinCfg<D, FP4>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
-  // Of ring entry e, at e % kEntryBars: its copies have landed; its MMAs are done (so its stages are free, and
-  // S of a K entry or O up to a V entry can be read).
-  const uint32_t b_landed = base + C::kBarAt;
-  const uint32_t b_done = b_landed + 8 * C::kEntryBars;
-  const uint32_t b_pfull = b_done + 8 * C::kEntryBars;
-  const uint32_t b_qfull = b_pfull + 16;
+  // Ring entry e's MMAs are done (so its stages are free, and S of a K entry or O up to a V entry can be
+  // read): at e % kEntryBars.  By tile, at tile % kTileBars: K is staged; V is staged and P written (one
+  // wait for the P.V); V of a tile with unseen keys has landed and can be zeroed.
+  const uint32_t b_done = base + C::kBarAt;
+  const uint32_t b_kready = b_done + 8 * C::kEntryBars;
+  const uint32_t b_pvready = b_kready + 8 * C::kTileBars;
+  const uint32_t b_vlanded = b_pvready + 8 * C::kTileBars;
+  const uint32_t b_qfull = b_vlanded + 8 * C::kTileBars;
   const uint32_t b_qempty = b_qfull + 8;
   const uint32_t b_ofree = b_qempty + 8;
-  const uint32_t b_vready = b_ofree + 8;
-  const uint32_t b_fin = b_vready + 8 * C::kFixBars;
+  const uint32_t b_fin = b_ofree + 8;
   const uint32_t b_next = b_fin + 8;
   const uint32_t b_recfull = b_next + 8;
   const uint32_t b_recempty = b_recfull + 8 * C::kRecords;
@@ -428,10 +431,11 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
   const uint32_t b_unstaged = b_staged + 8 * C::kDepth;
   float* const maxima = reinterpret_cast<float*>(smem + C::kMaxAt);
   uint32_t* const bad_keys = reinterpret_cast<uint32_t*>(smem + C::kBadAt);
+  uint32_t* const tags = reinterpret_cast<uint32_t*>(smem + C::kTagAt);   // 4-bit caches: of the staged entries
+  constexpr uint32_t kLastTag = 0xffffffffu;
   Unit* const recs = reinterpret_cast<Unit*>(smem + C::kRecAt);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kTmemSlot);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile uint32_t* const last_entry = tmem_slot + 2;         // 4-bit caches: number of entries once known
   int32_t* const status = p.status;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -440,13 +444,13 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     return;
   }
   if (threadIdx.x == 0) {
-    for (int e = 0; e < C::kEntryBars; ++e) {
-      mbar_init(b_landed + 8 * e, FP4 ? 8 : C::kProducers * C::kSPT);
-      mbar_init(b_done + 8 * e, 1);
+    constexpr int kArrivals = FP4 ? 8 : C::kProducers * C::kSPT;   // of the warps that stage an entry
+    for (int e = 0; e < C::kEntryBars; ++e) mbar_init(b_done + 8 * e, 1);
+    for (int t = 0; t < C::kTileBars; ++t) {
+      mbar_init(b_kready + 8 * t, kArrivals);
+      mbar_init(b_pvready + 8 * t, kArrivals + 8);                 // and the softmax warps
+      mbar_init(b_vlanded + 8 * t, kArrivals);
     }
-    mbar_init(b_pfull, 8);
-    mbar_init(b_pfull + 8, 8);
-    for (int k = 0; k < C::kFixBars; ++k) mbar_init(b_vready + 8 * k, 2);
     mbar_init(b_qfull, C::kQWarps);
     mbar_init(b_qempty, 1);
     mbar_init(b_ofree, 8);
@@ -458,10 +462,9 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     }
     if constexpr (FP4) {
       for (int k = 0; k < C::kDepth; ++k) {
-        mbar_init(b_staged + 8 * k, 128);
+        mbar_init(b_staged + 8 * k, 128 + 1);                      // and the one that writes the tag
         mbar_init(b_unstaged + 8 * k, 8);
       }
-      *last_entry = 0xffffffffu;
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -485,8 +488,11 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t tm_o = tmem + 256;           // S buffers: columns 0-127 and 128-255; O: from 256
 
-  auto wait_entry = [&](uint32_t bars, uint32_t e, int32_t site) -> bool {
-    return wait_for(bars + 8 * (e % C::kEntryBars), (e / C::kEntryBars) & 1, abort_flag, status, site);
+  auto wait_done = [&](uint32_t e, int32_t site) -> bool {
+    return wait_for(b_done + 8 * (e % C::kEntryBars), (e / C::kEntryBars) & 1, abort_flag, status, site);
+  };
+  auto wait_tile = [&](uint32_t bars, uint32_t t, int32_t site) -> bool {
+    return wait_for(bars + 8 * (t % C::kTileBars), (t / C::kTileBars) & 1, abort_flag, status, site);
   };
   auto finish_role = [&]() {
     tc_fence_before();
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         const uint32_t jt = js + j, sb = jt & 1;
         const uint32_t tm_s = tmem + lanes + sb * 128 + wg * 64;
         const int32_t v0 = (u.tile0 + j) * kWinTile;
-        bad |= !wait_entry(b_done, eb + k_entry(j), kWSFull);
+        bad |= !wait_done(eb + k_entry(j), kWSFull);
         tc_fence_after();
         const uint32_t* const holes = bad_keys + (jt % C::kBadSlots) * 8;
         const uint4 h0 = *reinterpret_cast<const uint4*>(holes), h1 = *reinterpret_cast<const uint4*>(holes + 4);
@@ -594,7 +600,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
             const float nm = need ? tile_max : m;
             const float f = m == -INFINITY ? 0.0f : fast_exp2((m - nm) * sc);
             if (j > 0) {
-              bad |= !wait_entry(b_done, eb + v_entry(j - 1, u.tiles), kWPvDone);
+              bad |= !wait_done(eb + v_entry(j - 1, u.tiles), kWPvDone);
               tc_fence_after();
               const float g = need ? f : 1.0f;
 #pragma unroll
@@ -637,12 +643,12 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_pfull + 8 * sb);
+        if (lane == 0) mbar_arrive(b_pvready + 8 * (jt % C::kTileBars));
       }
       if (left) break;                        // nothing of this call is written any more
       // epilogue
       if (u.tiles > 0) {
-        bad |= !wait_entry(b_done, eb + 2 * u.tiles - 1, kWPvDone);
+        bad |= !wait_done(eb + 2 * u.tiles - 1, kWPvDone);
         tc_fence_after();
       }
       if (warp_live) {
@@ -727,20 +733,20 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     const uint32_t q_lo = sw128_desc_lo(base, 16);
     const uint32_t k_lo = sw128_desc_lo(base + C::kRing, 16);
     const uint32_t v_lo = sw128_desc_lo(base + C::kRing, 16384);
-    uint32_t st = 0, entry = 0, js = 0, qit = 0, fixes = 0;
+    uint32_t st = 0, entry = 0, js = 0, qit = 0;
     bool stop = false;
-    // waits for the next entry's copies; st moves past its stages
-    auto take_entry = [&](uint32_t* stage) -> bool {
+    // the stages of the next entry; st moves past them
+    auto take_stages = [&](uint32_t* stage) {
 #pragma unroll
       for (int h = 0; h < C::kSPT; ++h) {
         stage[h] = st;
         if (++st == C::kStages) st = 0;
       }
-      return __all_sync(0xffffffffu, wait_entry(b_landed, entry, kWLanded));
     };
     auto issue_qk = [&](uint32_t jt, bool last) -> bool {
       uint32_t stage[C::kSPT];
-      if (!take_entry(stage)) return false;
+      take_stages(stage);
+      if (!__all_sync(0xffffffffu, wait_tile(b_kready, jt, kWLanded))) return false;
       tc_fence_after();
       if (lane == 0) {
 #pragma unroll
@@ -765,7 +771,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         stop = true;
         break;
       }
-      const int nt = recs[rb].tiles, some0 = recs[rb].some0, some1 = recs[rb].some1;
+      const int nt = recs[rb].tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(b_recempty + 8 * rb);
       if (nt < 0) break;
@@ -785,14 +791,10 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           break;
         }
         uint32_t stage[C::kSPT];
-        bool ok = wait_for(b_pfull + 8 * (jt & 1), (jt >> 1) & 1, abort_flag, status, kWPFull);
+        take_stages(stage);
+        bool ok = wait_tile(b_pvready, jt, kWPFull);
         if (j == 0) ok = ok && wait_for(b_ofree, (qit & 1) ^ 1, abort_flag, status, kWOFree);
-        if (!FP4 && (j < some0 || j >= some1)) {   // V rows that no row sees have been zeroed
-          ok = ok && wait_for(b_vready + 8 * (fixes % C::kFixBars), (fixes / C::kFixBars) & 1, abort_flag, status, kWVReady);
-          ++fixes;
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!take_entry(stage) || !ok) {
+        if (!__all_sync(0xffffffffu, ok)) {
           stop = true;
           break;
         }
@@ -841,7 +843,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     // and 11: zero V rows (16-bit caches), a share of the query tile (4-bit caches)
     regs_dec<C::kUtilRegs>();
     if (!FP4 && warp > 9) {
-      uint32_t eb = 0, st0 = 0, fixes = 0;   // ring entries so far, the first stage of entry eb, tiles zeroed
+      uint32_t js = 0, st0 = 0;          // tiles so far, the first stage of the next entry
       for (uint32_t it = 0;; ++it) {
         const uint32_t rb = it % C::kRecords;
         if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, status,
@@ -852,13 +854,15 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         if (lane == 0) mbar_arrive(b_recempty + 8 * rb);
         if (u.tiles < 0) break;
         bool ok = true;
-        for (int j = 0; j < u.tiles && ok; ++j) {
-          // (every V entry is waited for, so that no barrier is more than one phase ahead of this warp: a
-          // parity tells no more than that)
-          const uint32_t e = v_entry(j, u.tiles);
-          ok = __all_sync(0xffffffffu, wait_entry(b_landed, eb + e, kWLanded));
+        for (int j = 0; j < u.tiles; ++j) {
+          // V of these tiles lands on this barrier, in every other tile the producers' copies do so on the
+          // MMA's; a barrier per tile keeps its phases apart only if each is waited for, so whole tiles are
+          // signed off by the producers here too
+          const uint32_t jt = js + j;
+          ok = __all_sync(0xffffffffu, wait_tile(b_vlanded, jt, kWLanded));
           if (!ok) break;
           if (j >= u.some0 && j < u.some1) continue;
+          const uint32_t e = v_entry(j, u.tiles);
           for (int k = 0; k < kWinTile / 64; ++k) {
             const int row = k * 64 + (warp - 10) * 32 + lane;
             if (seen(p, u, position_of(u, (u.tile0 + j) * kWinTile + row))) continue;
@@ -872,11 +876,11 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(b_vready + 8 * (fixes % C::kFixBars));
-          ++fixes;
+          // in place of the producers' arrivals
+          if (lane < C::kProducers * C::kSPT / 2) mbar_arrive(b_pvready + 8 * (jt % C::kTileBars));
         }
         if (!ok) break;
-        eb += 2 * u.tiles;
+        js += u.tiles;
         st0 = (st0 + 2 * u.tiles * C::kSPT) % C::kStages;
       }
       finish_role();
@@ -1055,7 +1059,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     const int op = lane * 4 + pw;
     const int kb = op / C::kNBS * per, blk = op % C::kNBS;  // its first key and 64-dim block
     const bool active = op < kWinTile / per * C::kNBS;
-    uint32_t st = 0, half = 0, entry = 0, jt = 0;
+    uint32_t st = 0, half = 0, js = 0;
     bool stop = false;
     struct Rows {   // physical rows of this lane's copy: slots of up to four keys
       int32_t r[4];
@@ -1100,14 +1104,18 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         }
         return x;
       };
-      auto issue = [&](const Rows& x, bool is_v) -> bool {
+      // K (is_v: V) of tile j
+      auto issue = [&](const Rows& x, int j, bool is_v) -> bool {
+        const uint32_t jt = js + j;
+        const bool whole = j >= u.some0 && j < u.some1;
+        const uint32_t bars = !is_v ? b_kready : whole ? b_pvready : b_vlanded;
         const uint32_t loads = __ballot_sync(0xffffffffu, x.wanted);
         const uint32_t bytes = __popc(loads) * per * 128;
 #pragma unroll
         for (int h = 0; h < C::kSPT; ++h, ++half) {
           if (half >= C::kStages) {
             const uint32_t before = (half - C::kStages) / C::kSPT;   // the entry that held this stage
-            if (!__all_sync(0xffffffffu, wait_entry(b_done, before, kWStageEmpty))) return false;
+            if (!__all_sync(0xffffffffu, wait_done(before, kWStageEmpty))) return false;
           }
           if (h == 0 && !is_v) {
             uint32_t w0, w1 = 0;
@@ -1120,9 +1128,10 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
             if (lane == 0)
               *reinterpret_cast<uint2*>(bad_keys + (jt % C::kBadSlots) * 8 + pw * 2) = make_uint2(w0, w1);
           }
-          const uint32_t bar = b_landed + 8 * (entry % C::kEntryBars);
+          const uint32_t bar = bars + 8 * (jt % C::kTileBars);
           if (lane == 0) {
             if (bytes) mbar_arrive_expect_tx(bar, bytes); else mbar_arrive(bar);
+            if (is_v && whole) mbar_arrive(b_vlanded + 8 * (jt % C::kTileBars));
           }
           __syncwarp();
           if (x.wanted) {
@@ -1134,36 +1143,37 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           }
           if (++st == C::kStages) st = 0;
         }
-        ++entry;
-        if (!is_v) ++jt;
         return true;
       };
       if (u.tiles == 0) continue;
       Rows k_next = locate(0);
-      if (!issue(k_next, false)) {
+      if (!issue(k_next, 0, false)) {
         stop = true;
         break;
       }
       Rows v_rows = k_next;
       if (u.tiles > 1) k_next = locate(1);
       for (int j = 0; j < u.tiles; ++j) {
-        if (j + 1 < u.tiles && !issue(k_next, false)) {
+        if (j + 1 < u.tiles && !issue(k_next, j + 1, false)) {
           stop = true;
           break;
         }
-        if (!issue(v_rows, true)) {
+        if (!issue(v_rows, j, true)) {
           stop = true;
           break;
         }
         v_rows = k_next;
         if (j + 2 < u.tiles) k_next = locate(j + 2);
       }
+      js += u.tiles;
     }
     if (stop && lane == 0) {
-      // copies that may still be in flight: of the entries that fit the ring, and one cut short
-      const uint32_t n = C::kStages / C::kSPT + 2;
-      for (uint32_t e = entry > n ? entry - n : 0; e < entry; ++e)
-        drain(b_landed + 8 * (e % C::kEntryBars), (e / C::kEntryBars) & 1, status, kDrainNs / n);
+      // copies that may still be in flight: of the last tiles (a P.V barrier may also lack its softmax
+      // arrivals; the limit is a thousand times what a copy takes)
+      for (uint32_t t = js > 0 ? js - 1 : 0, k = 0; k < 4; ++k) {
+        drain(b_kready + 8 * ((t + k) % C::kTileBars), ((t + k) / C::kTileBars) & 1, status, kDrainNs / 100);
+        drain(b_pvready + 8 * ((t + k) % C::kTileBars), ((t + k) / C::kTileBars) & 1, status, kDrainNs / 100);
+      }
     }
     __syncwarp();
     finish_role();
@@ -1213,7 +1223,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
               page = __ldg(p.pa.page_table + static_cast<int64_t>(u.req) * p.pa.pages_per_req + e);
           }
         };
-        auto copy = [&](int32_t slot, const uint8_t* codes, const uint8_t* scales) -> bool {
+        auto copy = [&](int32_t slot, const uint8_t* codes, const uint8_t* scales, uint32_t tag) -> bool {
           if (n >= C::kDepth &&
               !__all_sync(0xffffffffu, wait_for(b_unstaged + 8 * slot_at, (turn & 1) ^ 1, abort_flag, status, kWUnstaged)))
             return false;
@@ -1228,6 +1238,10 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           cp_async_zfill<D / 16>(to + kWinTile * (D / 2) + (pw * 32 + lane) * (D / 16),
                                  scales + static_cast<uint64_t>(static_cast<uint32_t>(max(slot, 0))) * row_scales, slot >= 0);
           cp_async_arrive(b_staged + 8 * slot_at);
+          if (pw == 0 && lane == 0) {
+            tags[slot_at] = tag;
+            mbar_arrive(b_staged + 8 * slot_at);
+          }
           ++n;
           if (++slot_at == C::kDepth) {
             slot_at = 0;
@@ -1245,21 +1259,27 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
             if (lane == 0)
               *reinterpret_cast<uint2*>(bad_keys + (jt % C::kBadSlots) * 8 + pw * 2) = make_uint2(holes & 0xffffu, holes >> 16);
             ++jt;
-            if (!copy(slot, k_codes, k_scale)) {
+            if (!copy(slot, k_codes, k_scale, 2 * (jt - 1))) {
               stop = true;
               break;
             }
             if (t + 1 < u.tiles) look_up(t + 1);
           }
-          if (t > 0 && !copy(before, v_codes, v_scale)) {
+          if (t > 0 && !copy(before, v_codes, v_scale, 2 * (t < u.tiles ? jt - 2 : jt - 1) + 1)) {
             stop = true;
             break;
           }
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!stop && n >= C::kDepth) {                        // (the tag's slot has been read)
+        stop = !__all_sync(0xffffffffu, wait_for(b_unstaged + 8 * slot_at, (turn & 1) ^ 1, abort_flag, status, kWUnstaged));
+      }
       if (!stop) {
-        *last_entry = n;                                    // (every copying warp has the same count)
+        if (pw == 0 && lane == 0) {
+          tags[slot_at] = kLastTag;
+          mbar_arrive(b_staged + 8 * slot_at);
+        }
         mbar_arrive(b_staged + 8 * slot_at);
       }
       __syncwarp();
@@ -1272,11 +1292,12 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     uint32_t slot_at = 0, turn = 0;
     for (uint32_t n = 0;; ++n) {
       if (!__all_sync(0xffffffffu, wait_for(b_staged + 8 * slot_at, turn & 1, abort_flag, status, kWStaged))) break;
-      if (n == *last_entry) break;
+      const uint32_t tag = tags[slot_at];                   // 2 tile + 1 for V, of the call's tiles
+      if (tag == kLastTag) break;
       const uint32_t half0 = n * C::kSPT;
       if (half0 + C::kSPT > C::kStages) {                   // the entry that held the last of the stages
         const uint32_t before = (half0 + C::kSPT - 1 - C::kStages) / C::kSPT;
-        if (!__all_sync(0xffffffffu, wait_entry(b_done, before, kWStageEmpty))) break;
+        if (!__all_sync(0xffffffffu, wait_done(before, kWStageEmpty))) break;
       }
       const uint32_t from = base + C::kStagingAt + slot_at * C::kStaging;
       constexpr int kUnits = 16 * (D / 64);                 // (key, 64-dim block)
@@ -1305,7 +1326,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(b_landed + 8 * (n % C::kEntryBars));
+        mbar_arrive((tag & 1 ? b_pvready : b_kready) + 8 * ((tag >> 1) % C::kTileBars));
         mbar_arrive(b_unstaged + 8 * slot_at);
       }
       if (++slot_at == C::kDepth) {
