@@ -1059,7 +1059,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     const int op = lane * 4 + pw;
     const int kb = op / C::kNBS * per, blk = op % C::kNBS;  // its first key and 64-dim block
     const bool active = op < kWinTile / per * C::kNBS;
-    uint32_t st = 0, half = 0, js = 0;
+    uint32_t st = 0, half = 0, js = 0, last_tile = 0;
     bool stop = false;
     struct Rows {   // physical rows of this lane's copy: slots of up to four keys
       int32_t r[4];
@@ -1107,6 +1107,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       // K (is_v: V) of tile j
       auto issue = [&](const Rows& x, int j, bool is_v) -> bool {
         const uint32_t jt = js + j;
+        last_tile = jt;
         const bool whole = j >= u.some0 && j < u.some1;
         const uint32_t bars = !is_v ? b_kready : whole ? b_pvready : b_vlanded;
         const uint32_t loads = __ballot_sync(0xffffffffu, x.wanted);
@@ -1170,9 +1171,9 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     if (stop && lane == 0) {
       // copies that may still be in flight: of the last tiles (a P.V barrier may also lack its softmax
       // arrivals; the limit is a thousand times what a copy takes)
-      for (uint32_t t = js > 0 ? js - 1 : 0, k = 0; k < 4; ++k) {
-        drain(b_kready + 8 * ((t + k) % C::kTileBars), ((t + k) / C::kTileBars) & 1, status, kDrainNs / 100);
-        drain(b_pvready + 8 * ((t + k) % C::kTileBars), ((t + k) / C::kTileBars) & 1, status, kDrainNs / 100);
+      for (uint32_t t = last_tile > 5 ? last_tile - 5 : 0; t <= last_tile; ++t) {
+        drain(b_kready + 8 * (t % C::kTileBars), (t / C::kTileBars) & 1, status, kDrainNs / 100);
+        drain(b_pvready + 8 * (t % C::kTileBars), (t / C::kTileBars) & 1, status, kDrainNs / 100);
       }
     }
     __syncwarp();
