@@ -353,6 +353,25 @@ __device__ __forceinline__ uint32_t bf16x2_as_f16x2(uint32_t v) {
   memcpy(&r, &h, 4);
   return r;
 }
+// Two floats at a time (one instruction each).
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split_pair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // One 32-byte store (the address is a multiple of 32).
 __device__ __forceinline__ void st_global_v8(uint32_t* to, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -529,7 +548,6 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         row_sink = 0;
       }
       float m = -INFINITY, l = 0.0f;
-      bool left = false;                      // the pair of warps agreed to leave
       for (int j = 0; j < u.tiles; ++j) {
         const uint32_t jt = js + j, sb = jt & 1;
         const uint32_t tm_s = tmem + lanes + sb * 128 + wg * 64;
@@ -590,10 +608,8 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           float tile_max = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
           float* const mx = maxima + sb * 256;
           mx[wg * 128 + row] = tile_max;
-          if (named_bar_any(1 + w, 64, bad)) {
-            left = true;
-            break;
-          }
+          // (a warp whose wait ran out stays in step until the unit's end, so this barrier needs no vote)
+          named_bar_sync(1 + w, 64);
           tile_max = fmaxf(tile_max, mx[(wg ^ 1) * 128 + row]);
           const bool need = tile_max > m + raise || (m == -INFINITY && tile_max > -INFINITY);
           if (__any_sync(0xffffffffu, need)) {
@@ -619,16 +635,20 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
             }
           }
           const float neg = m == -INFINITY ? 0.0f : -m * sc;
-          float a0 = 0.0f, a1 = 0.0f, a2 = 0.0f, a3 = 0.0f;
+          const uint64_t sc2 = pair_of(sc, sc), neg2 = pair_of(neg, neg);
+          uint64_t a0 = 0, a1 = 0;                 // sums of pairs
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 64; c += 4) {
-            const float e0 = fast_exp2(fmaf(s[c], sc, neg)), e1 = fast_exp2(fmaf(s[c + 1], sc, neg));
-            const float e2 = fast_exp2(fmaf(s[c + 2], sc, neg)), e3 = fast_exp2(fmaf(s[c + 3], sc, neg));
-            a0 += e0;
-            a1 += e1;
-            a2 += e2;
-            a3 += e3;
+            float e0, e1, e2, e3;
+            split_pair(fma_pair(pair_of(s[c], s[c + 1]), sc2, neg2), e0, e1);
+            split_pair(fma_pair(pair_of(s[c + 2], s[c + 3]), sc2, neg2), e2, e3);
+            e0 = fast_exp2(e0);
+            e1 = fast_exp2(e1);
+            e2 = fast_exp2(e2);
+            e3 = fast_exp2(e3);
+            a0 = add_pair(a0, pair_of(e0, e1));
+            a1 = add_pair(a1, pair_of(e2, e3));
             if constexpr (FP4) {
               pk[c / 2] = pack16(e0, e1, __half{});
               pk[c / 2 + 1] = pack16(e2, e3, __half{});
@@ -637,7 +657,9 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
               pk[c / 2 + 1] = pack16(e2, e3, T{});
             }
           }
-          l += (a0 + a1) + (a2 + a3);
+          float l0, l1;
+          split_pair(add_pair(a0, a1), l0, l1);
+          l += l0 + l1;
           tmem_st32(tm_s, pk);
           tc_wait_st();
         }
@@ -645,7 +667,6 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(b_pvready + 8 * (jt % C::kTileBars));
       }
-      if (left) break;                        // nothing of this call is written any more
       // epilogue
       if (u.tiles > 0) {
         bad |= !wait_done(eb + 2 * u.tiles - 1, kWPvDone);
