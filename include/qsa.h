@@ -359,7 +359,8 @@ qsa_status qsa_rope(const void* x, void* out, const int32_t* positions, const qs
  *   q_stride, k_stride, v_stride elements apart (slices of one projected row are fine).
  *   k_cache, v_cache [n_slots, n_kvheads, head_dim]; v and v_cache both NULL for a cache of latent rows.
  *   slots [n_rows] int32: cache slot of each row; rows with a slot < 0 or >= n_slots write no cache row.
- *   Rows of one call that share a slot leave an unspecified one of them there.
+ *   Rows of one call that share a slot leave an unspecified one of them there.  The caches may not overlap the
+ *   rows.
  *   rope NULL: nothing turns (positions may be NULL then).
  * Otherwise as qsa_rope. */
 qsa_status qsa_rope_append(const void* q, void* q_out, const void* k, const void* v, void* k_cache,
@@ -414,8 +415,9 @@ qsa_status qsa_rope_append_fp4(const void* q, void* q_out, const void* k, const 
  *       the library's pool on `stream`.  Calls that overlap need a workspace each.
  * Sums, maxima and outputs are held in fp32, the weights of the P.V product are rounded to 16 bits.
  * Results do not depend on timing, but a row's sums depend on where the shares are cut, and so on its batch.
- * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED (other head dims, caches of 2^31 rows and more),
- * QSA_ERR_WORKSPACE; a wait inside the kernel that runs out is reported by qsa_get_device_status. */
+ * out may not overlap the inputs.
+ * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED (other head dims, caches of 2^31 rows and more, page-table
+ * rows of more than 2^31 - 257 positions), QSA_ERR_WORKSPACE; a wait inside the kernel that runs out is reported by qsa_get_device_status. */
 qsa_status qsa_window_attention_paged(const void* q, const void* k_cache, const void* v_cache,
                                       const int32_t* cu_seqlens_q, const int32_t* kv_lens,
                                       const int32_t* page_table, void* out, float* lse, int64_t n_rows,

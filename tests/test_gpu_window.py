@@ -134,6 +134,55 @@ def test_head_groups(B, hq, hkv):
         Batch([(400, 37), (90, 1)], hq, hkv, 64, 16, fp4=fp4, seed=hq).check(B, 90, 2)
 
 
+@pytest.mark.parametrize("hq", [33, 64])
+def test_large_groups_over_a_4_bit_cache_of_256_dims(B, hq):
+    """Query tiles of 64 rows there: one token of 33 or 64 heads."""
+    Batch([(300, 9), (90, 1)], hq, 1, 256, 16, fp4=True, seed=hq).check(B, 90, 2)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_non_finite_queries_stay_in_their_rows(B, fp4):
+    import torch
+    b = Batch([(400, 37), (90, 1)], 4, 2, 128, 16, fp4=fp4)
+    want = b.check(B, 0, 0)
+    b.q[5, 1, 7], b.q[30, 3], b.q[37, 0, 0] = float("nan"), float("inf"), float("-inf")
+    got = b.call(B, 0, 0)
+    torch.cuda.synchronize()
+    rest = torch.ones(want[1].shape, dtype=torch.bool, device="cuda")
+    rest[5, 1] = rest[30, 3] = rest[37, 0] = False
+    assert torch.equal(got[0][rest], want[0][rest]) and torch.equal(got[1][rest], want[1][rest])
+    assert bool(got[0][5, 1].isnan().all()) and bool(got[1][5, 1].isnan())
+
+
+def test_first_call_inside_a_capture(B):
+    """A fresh process whose very first calls are captured."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from top_sparse_attention_row_gb300 import binding as B
+i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+q = torch.randn((1, 6, 256), device="cuda").bfloat16()
+k, v = (torch.randn((4096, 1, 256), device="cuda").bfloat16() for _ in range(2))
+args = (i(0, 1), i(4000), torch.arange(64, device="cuda").int()[None], 64, 0.0625)
+past, new, table, free, head = i(5), i(1), i(7, 0)[None].contiguous(), i(3, 4), i(0)
+rope, pos, slot = B.rope_table(256), i(9), i(11)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    plan = B.page_plan(past, new, table, free, head, 4, 1)
+    x = B.rope_append(q, k[:1], v[:1], k, v, pos, slot, rope)
+    out, lse = B.window_attention_paged(x, k, v, *args)
+g.replay()
+torch.cuda.synchronize()
+a, b = out.clone(), lse.clone()
+want = B.window_attention_paged(x, k, v, *args)
+torch.cuda.synchronize()
+assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and int(plan.slots) == 1 and B.device_status() == 0
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 # ------------------------------------------------------------------------------ masks and bad places
 
 def unseen_slots(b, window, sink):

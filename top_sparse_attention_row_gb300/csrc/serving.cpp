@@ -146,6 +146,8 @@ qsa_status check_window(int64_t n_rows, int32_t n_requests, int32_t pages_per_re
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return QSA_ERR_UNSUPPORTED;
   if (n_qheads / n_kvheads > window_tile_rows(head_dim, fp4)) return QSA_ERR_UNSUPPORTED;
   if (n_rows + n_requests >= INT32_MAX) return QSA_ERR_UNSUPPORTED;
+  // positions, rounded up to whole key tiles, are held in 32 bits
+  if (static_cast<int64_t>(pages_per_req) * page_size > INT32_MAX - 2 * qsa::kWinTile) return QSA_ERR_UNSUPPORTED;
   if (n_pages > INT32_MAX / page_size || n_pages * page_size > (INT32_MAX - 1) / n_kvheads)
     return QSA_ERR_UNSUPPORTED;
   return QSA_OK;
