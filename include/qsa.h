@@ -287,6 +287,8 @@ typedef enum qsa_dtype { QSA_BF16 = 0, QSA_FP16 = 1 } qsa_dtype;
  *               position mod page_size; -1 where the page is missing, past pages_per_req, or (when
  *               n_pages > 0) not below n_pages.
  *               Rows past the last request get -1 in both: qsa_rope_append leaves such rows out.
+ *               max_rows is at least the sum of the new lengths where every request's rows are to be
+ *               used: the request that it cuts keeps the kv_lens of all its tokens.
  *   shortfall   [1] int32, nullable: pages wanted beyond the end of the free list (0 = none missing).
  * One kernel launch, no host read.  Calls that share a free list are ordered by the caller.
  * Errors: QSA_ERR_INVALID_ARG for null or misaligned pointers (4 bytes) and sizes below 1 (n_free,
@@ -359,8 +361,8 @@ qsa_status qsa_rope(const void* x, void* out, const int32_t* positions, const qs
  *   q_stride, k_stride, v_stride elements apart (slices of one projected row are fine).
  *   k_cache, v_cache [n_slots, n_kvheads, head_dim]; v and v_cache both NULL for a cache of latent rows.
  *   slots [n_rows] int32: cache slot of each row; rows with a slot < 0 or >= n_slots write no cache row.
- *   Rows of one call that share a slot leave an unspecified one of them there.  The caches may not overlap the
- *   rows.
+ *   Two rows of one call may not share a slot of the cache (its contents would be a mix of both).  The caches
+ *   may not overlap the rows.
  *   rope NULL: nothing turns (positions may be NULL then).
  * Otherwise as qsa_rope. */
 qsa_status qsa_rope_append(const void* q, void* q_out, const void* k, const void* v, void* k_cache,

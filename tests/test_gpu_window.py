@@ -275,6 +275,31 @@ def test_padded_batch_leaves_its_last_rows(B, fp4):
 
 # ------------------------------------------------------------------------------ numerics
 
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("cu,kv", [([0, 40, 5, 60], [1500, 1200, 900]), ([60, 40, 20, 0], [1500, 1200, 900]),
+                                   ([50, -3, 20, 61], [-7, 1500, 2 ** 31 - 1]), ([0, 0, 0, 0], [1, 2, 3]),
+                                   ([0, 2 ** 31 - 1, 7, 2 ** 31 - 1], [-2 ** 31, 1500, 1500])])
+def test_offsets_and_lengths_that_make_no_sense_stay_in_bounds(B, cu, kv, fp4):
+    """Row offsets that do not increase or leave the rows, negative and huge lengths: no promise about the
+    outputs, but the tensors around them stay as they are and the next call is right."""
+    import torch
+    b = Batch([(1500, 20), (1200, 20), (900, 20)], 4, 2, 128, 16, fp4=fp4)
+    want = b.check(B, 0, 0)
+    good = b.cu, b.kv
+    room = torch.full((3, *want[0].shape), 7.0, dtype=b.dt, device="cuda")
+    lroom = torch.full((3, *want[1].shape), 7.0, device="cuda")
+    b.cu, b.kv = np.array(cu), np.array(kv)
+    for window, sink in ((0, 0), (100, 3), (2 ** 31 - 1, 2 ** 31 - 1)):
+        b.call(B, window, sink, out=room[1], lse=lroom[1])
+    torch.cuda.synchronize()
+    assert B.device_status() == 0
+    for x in (room, lroom):
+        assert bool((x[0] == 7).all()) and bool((x[2] == 7).all())
+    b.cu, b.kv = good
+    again = b.check(B, 0, 0)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
 @pytest.mark.parametrize("dim", [64, 256])
 @pytest.mark.parametrize("order", ["up", "down", "spike"])
 def test_rising_logits(B, dim, order):

@@ -229,7 +229,7 @@ WINDOW_REFUSALS = [
     (dict(window=-1), INVALID), (dict(sink=-1), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID), (dict(dtype=2), INVALID),
     (dict(d=96), UNSUPPORTED), (dict(hq=129), UNSUPPORTED), (dict(rows=(1 << 31) - 2), UNSUPPORTED),
-    (dict(ppr=1 << 25), UNSUPPORTED), (dict(n_pages=1 << 26), UNSUPPORTED), (dict(n_pages=1 << 24, hkv=2), UNSUPPORTED),
+    (dict(ppr=1 << 25), UNSUPPORTED), (dict(n_pages=1 << 26), UNSUPPORTED), (dict(rows=(1 << 63) - 1), UNSUPPORTED), (dict(n_pages=1 << 24, hkv=2), UNSUPPORTED),
 ]
 
 

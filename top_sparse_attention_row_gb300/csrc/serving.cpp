@@ -51,7 +51,6 @@ qsa_status run_rope(qsa::RopeParams& p, const qsa_rope_spec* rope, int32_t dtype
       p.n_rows > INT32_MAX)
     return QSA_ERR_UNSUPPORTED;
   const int64_t q_width = static_cast<int64_t>(p.n_qheads) * p.head_dim;
-  const int64_t kv_width = static_cast<int64_t>(p.n_kvheads) * p.head_dim;
   if (p.n_qheads > 0) {
     if (!p.q || !p.q_out || p.q_stride < 0 || p.q_out_stride < q_width) return QSA_ERR_INVALID_ARG;
     if (p.q == p.q_out && p.q_stride != p.q_out_stride) return QSA_ERR_INVALID_ARG;
@@ -62,7 +61,6 @@ qsa_status run_rope(qsa::RopeParams& p, const qsa_rope_spec* rope, int32_t dtype
     if ((p.v == nullptr) != (p.v_cache == nullptr) || (p.v && p.v_stride < 0)) return QSA_ERR_INVALID_ARG;
     if (!aligned_to(p.k, 2) || !aligned_to(p.v, 2)) return QSA_ERR_INVALID_ARG;
     if (!fp4 && (!aligned_to(p.k_cache, 2) || !aligned_to(p.v_cache, 2))) return QSA_ERR_INVALID_ARG;
-    (void)kv_width;
   }
   p.n_vheads = p.v ? p.n_kvheads : 0;
   const qsa_status st = rope_args(rope, p.head_dim, &p);
@@ -145,7 +143,7 @@ qsa_status check_window(int64_t n_rows, int32_t n_requests, int32_t pages_per_re
     return QSA_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return QSA_ERR_UNSUPPORTED;
   if (n_qheads / n_kvheads > window_tile_rows(head_dim, fp4)) return QSA_ERR_UNSUPPORTED;
-  if (n_rows + n_requests >= INT32_MAX) return QSA_ERR_UNSUPPORTED;
+  if (n_rows >= INT32_MAX - n_requests) return QSA_ERR_UNSUPPORTED;
   // positions, rounded up to whole key tiles, are held in 32 bits
   if (static_cast<int64_t>(pages_per_req) * page_size > INT32_MAX - 2 * qsa::kWinTile) return QSA_ERR_UNSUPPORTED;
   if (n_pages > INT32_MAX / page_size || n_pages * page_size > (INT32_MAX - 1) / n_kvheads)

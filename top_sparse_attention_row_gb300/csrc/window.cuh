@@ -112,7 +112,7 @@ constexpr unsigned long long kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
 constexpr float kRaise = 8.0f;          // log2 units by which a tile may exceed the running maximum
 constexpr float kLn2f = 0.6931471805599453f;
 enum Site : int32_t {
-  kWRecEmpty = 0x41, kWRecFull, kWQEmpty, kWQFull, kWStageEmpty, kWLanded, kWSFull, kWPFull, kWPvDone,
+  kWRecEmpty = 0x41, kWRecFull, kWQEmpty, kWQFull, kWStageEmpty, kWLanded, kWSFull, kWPvReady, kWPvDone,
   kWOFree, kWNext, kWStaged, kWUnstaged, kWDrain
 };
 
@@ -459,7 +459,10 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if ((base & 1023u) != 0) {   // the swizzle needs 1024-byte aligned tiles; uniform over the grid
-    if (threadIdx.x == 0) atomicCAS(status, 0, 0x100 | kWDrain);
+    if (threadIdx.x == 0) {
+      atomicCAS(status, 0, 0x100 | kWDrain);
+      if (p.shares > 0) p.joins[blockIdx.x] = JoinRecord{-1, 0, 0, 0, 0, 0, 0, 0};
+    }
     return;
   }
   if (threadIdx.x == 0) {
@@ -813,7 +816,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         }
         uint32_t stage[C::kSPT];
         take_stages(stage);
-        bool ok = wait_tile(b_pvready, jt, kWPFull);
+        bool ok = wait_tile(b_pvready, jt, kWPvReady);
         if (j == 0) ok = ok && wait_for(b_ofree, (qit & 1) ^ 1, abort_flag, status, kWOFree);
         if (!__all_sync(0xffffffffu, ok)) {
           stop = true;
@@ -974,7 +977,8 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         if (take < w) {
           u.part = static_cast<int32_t>(2 * blockIdx.x) + (first_unit ? 0 : 1);
           if (off == 0) {     // its later parts are the first ones of the blocks that follow
-            const int64_t last = (at + w - 1) / sh.size;
+            int64_t last = (at + w - 1) / sh.size;
+            if (last >= p.shares) last = p.shares - 1;   // (row offsets that do not increase)
             join = JoinRecord{u.part, static_cast<int32_t>(last - blockIdx.x), u.row0, u.tokens, u.kvh, 0, 0, 0};
           }
           cut(u, off, off + take);
