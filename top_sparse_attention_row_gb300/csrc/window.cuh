@@ -110,6 +110,7 @@ namespace window_detail {
 
 constexpr unsigned long long kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
 constexpr float kRaise = 8.0f;          // log2 units by which a tile may exceed the running maximum
+constexpr int32_t kShortUnit = 4;        // key tiles
 constexpr float kLn2f = 0.6931471805599453f;
 enum Site : int32_t {
   kWRecEmpty = 0x41, kWRecFull, kWQEmpty, kWQFull, kWStageEmpty, kWLanded, kWSFull, kWPvReady, kWPvDone,
@@ -911,22 +912,21 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       return;
     }
     uint32_t qit = 0;
-    // Units: this block's own, then those of blocks that have not started.  The answer for the next one
-    // is asked for before the present one is worked out.
-    int32_t n = blockIdx.x;
+    // Units: this block's own, then those of blocks that have not started.  The next one is asked for when the
+    // softmax begins the present one, so that a block holds one unit in advance and the last units go to the
+    // blocks that are free; after a short unit at once, so that its successor's loads need not wait.
+    int32_t n = blockIdx.x, last_tiles = 0;
     uint32_t asked = 0;
-    bool more = true, pending = false;       // more: no answer has said "none" yet
+    bool more = true;                        // no answer has said "none" yet
     auto ask = [&]() {
       if (lane == 0) {
         mbar_arrive_expect_tx(b_next, 16);
         clc_try_cancel(base + C::kNextAt, b_next);
       }
       __syncwarp();
-      pending = true;
     };
     auto answer = [&]() -> int32_t {
       const bool ok = mbar_try_wait(b_next, asked & 1) || wait_for(b_next, asked & 1, abort_flag, status, kWNext);
-      pending = false;
       ++asked;
       if (!__all_sync(0xffffffffu, ok)) {
         more = false;
@@ -940,9 +940,8 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     };
     // whole units: number n of the call
     auto whole_unit = [&](uint32_t n) -> Unit {
-      const uint32_t kvh = n / static_cast<uint32_t>(p.n_tiles);
-      // a request's later tiles see more keys where there is no window: they go first
-      const int32_t tile = p.n_tiles - 1 - static_cast<int32_t>(n - kvh * static_cast<uint32_t>(p.n_tiles));
+      const uint32_t back = n / static_cast<uint32_t>(p.n_kvheads), kvh = n - back * static_cast<uint32_t>(p.n_kvheads);
+      const int32_t tile = p.n_tiles - 1 - static_cast<int32_t>(back);
       Unit u = make_unit(p, tile_owner(p, tile, lane), tile);
       u.kvh = static_cast<int32_t>(kvh);
       return u;
@@ -991,7 +990,6 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       }
       return u;
     };
-    if (warp == 9 && p.shares == 0 && !p.stall_first_item) ask();
     if (p.shares > 0) more = false;          // no block is taken over
     for (uint32_t it = 0;; ++it) {
       const uint32_t rb = it % C::kRecords, ph = (it / C::kRecords) & 1;
@@ -1001,15 +999,24 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         if (p.shares > 0) {
           u = shared_unit();
         } else {
-          // (n is the unit in hand, and the answer for the one after it is pending)
           u.tiles = -1;
+          if (it > 0) {
+            const uint32_t before = it - 1;
+            if (last_tiles > kShortUnit &&
+                !__all_sync(0xffffffffu, wait_for(b_recempty + 8 * (before % C::kRecords), (before / C::kRecords) & 1,
+                                                  abort_flag, status, kWRecEmpty)))
+              break;
+            ask();
+            n = answer();
+          }
           while (n >= 0) {
             u = whole_unit(static_cast<uint32_t>(n));
-            n = pending ? answer() : -1;
-            if (more) ask();
             if (u.tiles >= 0) break;
-            u.tiles = -1;
+            u.tiles = -1;              // a number without rows
+            ask();
+            n = answer();
           }
+          last_tiles = u.tiles;
         }
         if (!__all_sync(0xffffffffu, wait_for(b_recempty + 8 * rb, ph ^ 1, abort_flag, status, kWRecEmpty))) break;
         if (lane == 0) {
@@ -1065,9 +1072,8 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       // not run out one after the other
       *abort_flag = 1;
       while (more) {
-        if (!pending) ask();
+        ask();
         drain(b_next, asked & 1, status, kDrainNs);
-        pending = false;
         ++asked;
         more = clc_answer(base + C::kNextAt) >= 0;
         fence_proxy_async_smem();
