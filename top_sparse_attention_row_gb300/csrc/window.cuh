@@ -75,8 +75,8 @@ struct WinCfg {
   // registers per thread at launch, and after the split: softmax warpgroups; MMA and scheduler; copies; 4-bit
   // conversion
   static constexpr int kLaunchRegs = FP4 ? 80 : 128;
-  static constexpr int kSoftmaxRegs = FP4 ? 120 : 168, kUtilRegs = FP4 ? 64 : 88, kProducerRegs = FP4 ? 72 : 88;
-  static constexpr int kConvertRegs = 48;
+  static constexpr int kSoftmaxRegs = FP4 ? 128 : 168, kUtilRegs = FP4 ? 64 : 88, kProducerRegs = FP4 ? 72 : 88;
+  static constexpr int kConvertRegs = 40;
   static_assert(256 * kSoftmaxRegs + 128 * (kUtilRegs + kProducerRegs) + (FP4 ? 256 * kConvertRegs : 0) <=
                     kThreads * kLaunchRegs,
                 "register split within the launch's registers");
@@ -529,10 +529,8 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
     const float sc = p.scale_log2;
     const float raise = kRaise / sc;
-    // Loops that run once a unit, or seldom, are not unrolled: their instructions would have to be fetched anew
-    // each time (unrolled: decode batch 129.1 -> 126.6 us, causal prompts of 128 dims 215 -> 205 us rolled).  The 4-bit
-    // kernels gain nothing, and their conversion warps lose by the other register assignment (233 -> 258 us).
-    constexpr int kUnroll = FP4 ? 8 : 1;
+    // (loops that run once a unit, or seldom, are not unrolled: their instructions would have to be fetched anew each
+    // time; unrolled: decode batch 129.1 -> 126.6 us, causal prompts of 128 dims 215 -> 205 us rolled)
     uint32_t it = 0, js = 0, eb = 0;          // records, tiles and ring entries so far
     bool bad = false;
     for (;; ++it) {
@@ -619,7 +617,8 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           // (a warp whose wait ran out stays in step until the unit's end, so this barrier needs no vote)
           named_bar_sync(1 + w, 64);
           tile_max = fmaxf(tile_max, mx[(wg ^ 1) * 128 + row]);
-          const bool need = tile_max > m + raise || (m == -INFINITY && tile_max > -INFINITY);
+          // (rows past the unit's hold anything: they must not make the warp rescale)
+          const bool need = row < live_rows && (tile_max > m + raise || (m == -INFINITY && tile_max > -INFINITY));
           if (__any_sync(0xffffffffu, need)) {
             const float nm = need ? tile_max : m;
             const float f = m == -INFINITY ? 0.0f : fast_exp2((m - nm) * sc);
@@ -627,7 +626,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
               bad |= !wait_done(eb + v_entry(j - 1, u.tiles), kWPvDone);
               tc_fence_after();
               const float g = need ? f : 1.0f;
-#pragma unroll kUnroll
+#pragma unroll 1
               for (int c = 0; c < D / 2; c += 16) {
                 float o[16];
                 tmem_ld16(tm_o + lanes + wg * (D / 2) + c, o);
@@ -701,7 +700,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       const uint32_t tm_row = tm_o + lanes + wg * (D / 2);
       if (warp_live && u.part >= 0) {
         float* const part = p.part_o + static_cast<int64_t>(u.part * kWinTile + row) * D + wg * (D / 2);
-#pragma unroll kUnroll
+#pragma unroll 1
         for (int c = 0; c < D / 2; c += 32) {
           if (u.tiles == 0) break;
           float o[32];
@@ -718,7 +717,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       }
       if (warp_live && u.part < 0) {
         uint32_t* const out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + rh * D + wg * (D / 2));
-#pragma unroll kUnroll
+#pragma unroll 1
         for (int c = 0; c < D / 2; c += 32) {
           float o[32];
           if (u.tiles > 0) {
