@@ -331,6 +331,15 @@ def test_long_context_in_equal_shares(B, dim, n, fp4):
     Batch([(n, 3)], 4, 1, dim, 64, fp4=fp4, seed=3).check(B, n // 2, 700)
 
 
+@pytest.mark.parametrize("fp4", [False, True])
+def test_ragged_units_in_equal_shares(B, fp4):
+    """More units than blocks, of no tile to many: shares that begin and end inside units, empty ones among them."""
+    rng = np.random.default_rng(5)
+    lens = [(int(rng.choice([0, 1, 5, 128, 129, 700, rng.integers(1, 5000)])), 1) for _ in range(230)]
+    Batch(lens + [(5000, 1)], 3, 1, 64, 64, fp4=fp4).check(B, 0, 0)
+    Batch(lens[:120] + [(5000, 40)], 4, 2, 64, 16, fp4=fp4).check(B, 0, 0)
+
+
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 @pytest.mark.parametrize("dim,hq,hkv", [(64, 8, 8), (128, 16, 2), (256, 6, 1)])
 def test_long_prompt(B, dim, hq, hkv, dtype):

@@ -348,6 +348,7 @@ struct WindowParams {
   int32_t tile_tokens;          // tokens of a query tile: 128 / group, at least 1
   int32_t n_tiles;              // upper bound: n_rows / tile_tokens + n_requests
   int32_t shares;               // equal shares: blocks of the grid; 0 = whole units
+  int32_t unit_cost;            // what a unit counts in a share beside its tiles
   int32_t window;               // 0 = none
   int32_t n_sink;
   int32_t out_32;               // out is 32-byte aligned

@@ -83,16 +83,20 @@ qsa_status run_rope(qsa::RopeParams& p, const qsa_rope_spec* rope, int32_t dtype
 }
 
 // How the units of a call are dealt out, by a model of its time in key tiles.  A unit takes its tiles and about
-// three tiles' time of its own (query tile, first softmax, output).  Whole units run in rounds; equal shares
-// divide the tiles evenly, but a block then has one more unit begun or ended, writes up to two partial ones
-// in fp32 (a tile's worth of bytes each when all 128 rows are in use) that the join reads again, and the
-// join is one more launch, about three tiles long.
+// three tiles' time of its own (query tile, first softmax, output).  Whole units: blocks that become free take the
+// next one, and about half a unit's time passes while the last ones finish.  Equal shares divide that time evenly,
+// but a block then has one more unit begun or ended, writes up to two partial ones in fp32 (a tile's worth of bytes
+// each when all 128 rows are in use) that the join reads again, and the join is one more launch, about three tiles
+// long.  The lengths behind the page table are not known here, and where they are shorter, shares have less to gain:
+// they are taken where the model gives them 7 %.  Measured (us, whole / shares): 128 decode rows with contexts of 1k
+// to 8k, 24/2 heads of 256 dims, window 4096: 146 / 127; 48 decode rows over 16k to 32k keys in 4 bits: 449 / 224; a
+// chunk of 512 rows at 8000, 256 dims: 103 / 89, 128 dims, 32/8 heads: 67 / 74; the last 8192 rows of a 32k prompt:
+// 150 / 153; 256 decode rows of 1k to 4k, 128 dims: 338 / 356; a prompt of 2048 rows: 44 / 60.
 struct WindowPlan {
-  int32_t tile_tokens, n_tiles, shares;
+  int32_t tile_tokens, n_tiles, shares, unit_cost;
   int64_t n_units;
 };
 constexpr int32_t kMaxShareTiles = 1 << 14;    // every block sums all units' tiles
-constexpr double kMaxShareLoad = 16.0;         // rounds from which whole units leave few SMs idle
 WindowPlan plan_window(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, int32_t group, int32_t tile_rows,
                        int64_t max_keys, int32_t window, int32_t n_sink, int32_t sms) {
   WindowPlan w{};
@@ -112,12 +116,15 @@ WindowPlan plan_window(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, in
   if (kt <= 1 || w.n_tiles > kMaxShareTiles) return w;
   const int64_t rows_per = n_rows < tiles * w.tile_tokens ? (n_rows + tiles - 1) / tiles : w.tile_tokens;
   const double partial = static_cast<double>(rows_per * group) / qsa::kWinTile;
-  const double load = static_cast<double>(items) / sms;
-  if (load > kMaxShareLoad) return w;
-  const double whole = std::ceil(load) * (kt + 3.0);
+  const double load = static_cast<double>(items) / sms, unit = kt + 3.0;
+  const double whole = load > 1.0 ? (load + 0.5) * unit : unit;
   const int64_t shares = items * kt < sms ? items * kt : sms;
-  const double even = static_cast<double>(items) * kt / shares + (load + 1.0) * 3.0 + 4.0 * partial + 3.0;
-  if (even < whole) w.shares = static_cast<int32_t>(shares);
+  const double even = static_cast<double>(items) * unit / shares + 3.0 + 6.0 * partial + 3.0;
+  if (even < 0.93 * whole) {
+    w.shares = static_cast<int32_t>(shares);
+    // with fewer units than shares, every share has one or two, and the tiles are divided
+    w.unit_cost = items > shares ? 3 : 0;
+  }
   return w;
 }
 
@@ -197,6 +204,7 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   p.tile_tokens = w.tile_tokens;
   p.n_tiles = w.n_tiles;
   p.shares = w.shares;
+  p.unit_cost = w.unit_cost;
   p.out_32 = aligned_to(out, 32);
   p.window = window;
   p.n_sink = n_sink;

@@ -256,13 +256,13 @@ __device__ __forceinline__ void cut(Unit& u, int32_t a, int32_t b) {
   u.all1 -= a;
 }
 
-// Equal shares: where a block's run of key tiles starts.  A unit counts as its tiles, at least one (a unit that
-// sees nothing still writes its rows).
+// Equal shares: where a block's run of the units starts.  A unit counts as unit_cost for its beginning and end,
+// then its tiles (at least one in all); a share that ends inside the former takes nothing of the unit.
 struct Share {
-  int64_t size;        // tiles of a share
+  int64_t size;        // of a share, more than unit_cost
   int64_t left;        // of this block's
   int32_t kvh, tile;   // first unit
-  int32_t offset;      // first tile in it
+  int32_t offset;      // where the share starts in it
 };
 // Worked out by all threads of the block; `scratch` has room for 34 int64.  Ends with a barrier.
 template <int THREADS>
@@ -276,7 +276,7 @@ __device__ __forceinline__ void find_share(const WindowParams& p, int64_t* scrat
       if (first_tile(p, mid) <= tile) lo = mid; else hi = mid - 1;
     }
     const int32_t t = make_unit(p, lo, tile).tiles;
-    return t == -2 ? 0 : t > 0 ? t : 1;
+    return t == -2 ? 0 : max(t + p.unit_cost, 1);
   };
   auto warp_sum = [&](int64_t v) -> int64_t {             // inclusive over the lanes
 #pragma unroll
@@ -297,7 +297,8 @@ __device__ __forceinline__ void find_share(const WindowParams& p, int64_t* scrat
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) total += scratch[w];
   __syncthreads();
-  const int64_t all = total * p.n_kvheads, size = (all + p.shares - 1) / p.shares;
+  const int64_t all = total * p.n_kvheads, even = (all + p.shares - 1) / p.shares;
+  const int64_t size = even > p.unit_cost ? even : p.unit_cost + 1;   // every share inside a unit has tiles of it
   const int64_t from = size * blockIdx.x;
   if (from < all) {                                       // uniform over the block
     const int32_t kvh = static_cast<int32_t>(from / total);
@@ -970,26 +971,31 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           u.tiles = -1;
           continue;
         }
-        const int32_t w = u.tiles > 0 ? u.tiles : 1, off = sh.offset;
+        const int32_t w = max(u.tiles + p.unit_cost, 1), off = sh.offset;
+        sh.offset = 0;
         if (off >= w) {         // (row offsets that do not increase)
-          sh.offset = 0;
           u.tiles = -1;
           continue;
         }
         const int32_t take = sh.left < w - off ? static_cast<int32_t>(sh.left) : w - off;
-        if (take < w) {
+        const int64_t end = at - off + w;
+        const int32_t a = off > p.unit_cost ? off - p.unit_cost : 0, b = off + take - p.unit_cost;
+        sh.left -= take;
+        at += take;
+        if (u.tiles == 0 ? off > 0 : b <= a) {
+          u.tiles = -1;
+          continue;
+        }
+        if (u.tiles > 0 && b - a < u.tiles) {
           u.part = static_cast<int32_t>(2 * blockIdx.x) + (first_unit ? 0 : 1);
-          if (off == 0) {     // its later parts are the first ones of the blocks that follow
-            int64_t last = (at + w - 1) / sh.size;
+          if (a == 0) {         // its later parts are the first ones of the blocks that follow
+            int64_t last = (end - 1) / sh.size;
             if (last >= p.shares) last = p.shares - 1;   // (row offsets that do not increase)
             join = JoinRecord{u.part, static_cast<int32_t>(last - blockIdx.x), u.row0, u.tokens, u.kvh, 0, 0, 0};
           }
-          cut(u, off, off + take);
+          cut(u, a, b);
         }
         first_unit = false;
-        sh.left -= take;
-        at += take;
-        sh.offset = 0;
         return u;
       }
       return u;
@@ -1074,7 +1080,6 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     if (warp == 9 && p.shares == 0 && (*abort_flag || p.stall_first_item)) {
       // the call is given up: blocks that have not started are taken off the grid, so that their waits do
       // not run out one after the other
-      *abort_flag = 1;
       while (more) {
         ask();
         drain(b_next, asked & 1, status, kDrainNs);
