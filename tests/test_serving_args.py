@@ -212,6 +212,18 @@ def test_oracle_rope_is_a_rotation():
     assert abs(dot(10, 3) - dot(107, 100)) < 1e-12
 
 
+def test_copies_of_a_rope_table_have_their_own_steps(B):
+    import copy
+    import ctypes
+    import pickle
+    t = B.rope_table(64, 500.0, scaling="yarn", factor=4.0, original_len=4096.0)
+    for c in (copy.copy(t), copy.deepcopy(t), pickle.loads(pickle.dumps(t))):
+        assert c.steps == t.steps and (c.rot_dim, c.magnitude) == (t.rot_dim, t.magnitude)
+        assert c._raw[0] == ctypes.addressof(c._steps) != t._raw[0]
+    with pytest.raises(AttributeError):
+        t.magnitude = 2.0
+
+
 def window_args(**kw):
     a = dict(q=FAKE, k=FAKE, v=FAKE, cu=FAKE, kv=FAKE, table=FAKE, out=FAKE, lse=None, rows=0, n=2, ppr=4, ps=64, n_pages=8,
              hq=6, hkv=1, d=256, scale=0.0625, window=0, sink=0, dtype=0, ws=None, ws_bytes=0, stream=None)

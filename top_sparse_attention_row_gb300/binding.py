@@ -621,11 +621,22 @@ class RopeTable:
     fixed-point steps on the host and the magnitude of the rotated values."""
 
     def __init__(self, rot_dim: int, steps, magnitude: float):
-        self.rot_dim, self.magnitude = int(rot_dim), float(magnitude)
-        self._steps = (ctypes.c_uint64 * max(1, self.rot_dim // 2))(*steps)
+        rot_dim = int(rot_dim)
+        self._steps = (ctypes.c_uint64 * max(1, rot_dim // 2))(*steps)
         # what the extension reads: the address of the steps (which live as long as this table), their part
         # of the head and the magnitude
-        self._raw = (ctypes.addressof(self._steps), self.rot_dim, self.magnitude)
+        self._raw = (ctypes.addressof(self._steps), rot_dim, float(magnitude))
+
+    def __reduce__(self):          # a copy has steps of its own
+        return RopeTable, (self.rot_dim, self.steps, self.magnitude)
+
+    @property
+    def rot_dim(self) -> int:
+        return self._raw[1]
+
+    @property
+    def magnitude(self) -> float:
+        return self._raw[2]
 
     @property
     def steps(self):
