@@ -358,6 +358,17 @@ def test_many_requests(B):
         Batch(lens, 2, 1, 64, 16, fp4=fp4, seed=5).check(B, 40, 2)
 
 
+@pytest.mark.parametrize("fp4", [False, True])
+def test_tens_of_thousands_of_requests(B, fp4):
+    """More units than shares are dealt out for, short and long ones in no order."""
+    rng = np.random.default_rng(21)
+    lens = [(int(n), 1) for n in rng.integers(1, 60, 20000)]
+    lens[17], lens[12345], lens[19999] = (2000, 30), (1500, 1), (700, 2)
+    b = Batch(lens, 2, 1, 64, 16, fp4=fp4, seed=3)
+    rows = np.unique(np.concatenate([np.arange(0, b.R, 211), np.arange(17, 47), [12374], np.arange(b.R - 3, b.R)]))
+    b.check(B, 0, 0, rows=rows)
+
+
 def test_random_batches(B):
     """Shapes drawn at random over the whole range."""
     rng = np.random.default_rng(11)
