@@ -377,7 +377,9 @@ qsa_status qsa_rope_append(const void* q, void* q_out, const void* k, const void
  *   s = e4m3(max |x| / g / 6),  code = e2m1(x / g / s)   (0 where s = 0),  value = e2m1(code) s g
  * rounded to nearest, ties to even, beyond the range to the largest value; g = k_global or v_global.
  * x is the rotated row in fp32.  e2m1 has no NaN or infinity: they are stored as values of the largest
- * magnitude that the block's scale gives.
+ * magnitude that the block's scale gives, infinities making that scale the largest one.  A NaN beside
+ * numbers does not enter the block's maximum; a block of NaN alone gets the scale NaN (0x7f) and codes 0, and so
+ * reads back as NaN.
  *   k_cache, v_cache [n_slots, n_kvheads, head_dim / 2] bytes; k_scale, v_scale [n_slots, n_kvheads,
  *   head_dim / 16] e4m3 bytes
  *   k_seen, v_seen [n_rows, n_kvheads, head_dim] of type dtype, nullable: the values that the cache now

@@ -393,3 +393,57 @@ def test_append_fp4_non_finite_values_saturate(B):
     assert got[0, 3] == 6 * 448 and got[0, 20] == -6 * 448 and np.all(got[0, [0, 1, 2, 21, 22]] == 0)
     assert np.all(got[0, 32:] == got[1, 0]) and abs(got[1, 0] - 1) <= 2 ** -4      # scale e4m3(1 / 6), code 6
     assert abs(got[1, 40]) == 6 * S.E4M3[ks.cpu().numpy()[1, 0, 2]] and np.isfinite(got).all()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved", None])
+def test_append_fp4_blocks_of_nan_alone_read_back_as_nan(B, layout):
+    """K and V blocks whose values are all NaN get the scale NaN and codes 0, turned or not; a block with a
+    number in it stays finite, and the other blocks are what they are without the NaN."""
+    import torch
+    dim, rot = 128, 64
+    rng = np.random.default_rng(2)
+    table = None if layout is None else B.rope_table(rot, 10000.0)
+    how = {} if layout is None else dict(layout=layout, rot_offset=32)
+    pos = None if layout is None else i32([0, 9, 700])
+    k, v = (torch.from_numpy(rng.standard_normal((3, 2, dim))).bfloat16().cuda() for _ in range(2))
+    # rows 0 and 2: whole rotated part and a passing block; row 1: one value of a passing block
+    bad_k, bad_v = k.clone(), v.clone()
+    for r, h in ((0, 1), (2, 0)):
+        bad_k[r, h, 32:96], bad_k[r, h, :16], bad_v[r, h, 48:80] = float("nan"), float("nan"), float("nan")
+    bad_k[1, 0, 100] = float("nan")
+    got = []
+    for a, b in ((k, v), (bad_k, bad_v)):
+        u8 = lambda n: torch.full((3, 2, n), 0xAA, dtype=torch.uint8, device="cuda")  # noqa: E731
+        kc, vc, ks, vs = u8(dim // 2), u8(dim // 2), u8(dim // 16), u8(dim // 16)
+        seen = [torch.empty_like(k) for _ in range(2)]
+        B.rope_append_fp4(None, a, b, kc, ks, vc, vs, pos, i32([0, 1, 2]), table, k_global=0.5, v_global=0.25,
+                          k_seen=seen[0], v_seen=seen[1], **how)
+        torch.cuda.synchronize()
+        got.append([x.cpu() for x in (ks, vs)] + [x.cpu().unflatten(-1, (-1, 8)) for x in (kc, vc)] +
+                   [x.float().cpu().unflatten(-1, (-1, 16)) for x in seen])
+    for w in (0, 1):
+        src = (bad_k, bad_v)[w].float().cpu().unflatten(-1, (-1, 16))
+        gone = src.isnan().all(-1)
+        assert int(gone.sum()) == (10 if w == 0 else 4)
+        scale, codes, seen = got[1][w], got[1][2 + w], got[1][4 + w]
+        assert bool((scale[gone] == 0x7F).all()) and not bool(codes[gone].any()) and bool(seen[gone].isnan().all())
+        assert bool(seen[~gone].isfinite().all()) and bool((scale[~gone] != 0x7F).all())
+        same = ~src.isnan().any(-1)
+        for a, b in ((scale, got[0][w]), (codes, got[0][2 + w]), (seen, got[0][4 + w])):
+            assert torch.equal(a[same], b[same])
+
+
+def test_attention_over_a_4_bit_cache_shows_nan_rows(B):
+    """A K row of NaN alone, written by the append, makes the rows that see it NaN and no others."""
+    import torch
+    n, dim = 200, 64
+    q, k, v = (torch.randn((n, 1, dim), device="cuda").bfloat16() for _ in range(3))
+    k[150] = float("nan")
+    u8 = lambda w: torch.zeros((256, 1, w), dtype=torch.uint8, device="cuda")  # noqa: E731
+    kc, vc, ks, vs = u8(dim // 2), u8(dim // 2), u8(dim // 16), u8(dim // 16)
+    B.rope_append_fp4(None, k, v, kc, ks, vc, vs, None, i32(np.arange(n)), None)
+    out, lse = B.window_attention_fp4_paged(q, kc, ks, vc, vs, i32([0, n]), i32([n]), i32([[0, 1, 2, 3]]), 64, 0.125,
+                                            window=30)
+    torch.cuda.synchronize()
+    hit = out.isnan().any(-1)[:, 0].cpu().numpy()
+    assert np.array_equal(np.flatnonzero(hit), np.arange(150, 180)) and bool(out[150:180].isnan().all())

@@ -175,7 +175,8 @@ template <typename T, bool ONE>
 __device__ __forceinline__ void write_fp4(const RopeParams& p, bool is_v, int64_t row, int32_t kvh, int64_t cell, int da,
                                           int db, float inv, float ma, float mb, float* f) {
   constexpr float kSixth = 1.0f / 6.0f;
-  auto scale_of = [&](float m) { return e4m3_of(snap(m * inv * kSixth)); };
+  // (a block of NaN alone has no largest magnitude: its scale is e4m3's NaN, so that reads show it, its codes are 0)
+  auto scale_of = [&](float m) { return e4m3_of(m == m ? snap(m * inv * kSixth) : m); };
   auto reciprocal = [&](float s) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
