@@ -447,3 +447,24 @@ def test_attention_over_a_4_bit_cache_shows_nan_rows(B):
     torch.cuda.synchronize()
     hit = out.isnan().any(-1)[:, 0].cpu().numpy()
     assert np.array_equal(np.flatnonzero(hit), np.arange(150, 180)) and bool(out[150:180].isnan().all())
+
+
+@pytest.mark.parametrize("exponent", [-126, -124, -101, -99, 0, 98, 100, 123, 127])
+def test_append_fp4_global_scales_at_the_ends_of_the_range(B, exponent):
+    """Powers of two from the smallest to the largest: zeros stay zeros and values come out as the oracle's,
+    beside the smallest values that a block scale stands for too."""
+    import torch
+    g = 2.0 ** exponent
+    rng = np.random.default_rng(4)
+    x = np.clip(rng.standard_normal((4, 1, 64)), -3, 3) * g                # block scales up to 1/2
+    x[0, 0, 1:16], x[0, 0, 0] = 0.0, 2.0 ** -7 * g                         # scale 2^-9, all others 0
+    x[1, 0, ::3] = 0.0
+    k = torch.from_numpy(x).bfloat16().cuda()
+    u8 = lambda n: torch.zeros((4, 1, n), dtype=torch.uint8, device="cuda")  # noqa: E731
+    kc, vc, ks, vs = u8(32), u8(32), u8(4), u8(4)
+    B.rope_append_fp4(None, k, k, kc, ks, vc, vs, None, i32([0, 1, 2, 3]), None, k_global=g, v_global=g)
+    torch.cuda.synchronize()
+    codes, sc, _ = S.fp4_quantise(k.double().cpu().numpy(), g)
+    want = np.where(np.repeat(sc == 0, 8, axis=-1), 0, S.fp4_pack(codes))
+    for c, s in ((kc, ks), (vc, vs)):
+        assert np.array_equal(s.cpu().numpy(), sc) and np.array_equal(c.cpu().numpy(), want)

@@ -432,9 +432,11 @@ cudaError_t launch_rope(RopeParams p, bool fp16, bool fp4, int num_sms, cudaStre
   p.wide_q = wide(p.q, p.q_out, p.q_stride, p.q_out_stride);
   p.wide_kv = wide(p.k, p.v, p.k_stride, p.v_stride) && (fp4 || wide(p.k_cache, p.v_cache, 0, 0));
   p.wide_seen = wide(p.k_seen, p.v_seen, 0, 0);
-  auto inverse = [](float g) {   // 1 / g where that is exact and normal, else 0
+  // 1 / g where g is a power of two and g and 1 / g times any block scale or its reciprocal (2^-9 .. 2^9) are normal
+  // and finite; else 0, and the rows are divided by g
+  auto inverse = [](float g) {
     int e = 0;
-    return std::frexp(g, &e) == 0.5f && e > -124 && e < 124 ? 1.0f / g : 0.0f;
+    return std::frexp(g, &e) == 0.5f && e > -100 && e < 100 ? 1.0f / g : 0.0f;
   };
   p.k_inverse = inverse(p.k_global);
   p.v_inverse = inverse(p.v_global);
