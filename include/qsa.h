@@ -376,7 +376,8 @@ qsa_status qsa_rope_append(const void* q, void* q_out, const void* k, const void
  * low half of the byte) and head_dim / 16 e4m3 scales, one per 16 dims:
  *   s = e4m3(max |x| / g / 6),  code = e2m1(x / g / s)   (0 where s = 0),  value = e2m1(code) s g
  * rounded to nearest, ties to even, beyond the range to the largest value; g = k_global or v_global.
- * x is the rotated row in fp32.  e2m1 has no NaN or infinity: they are stored as values of the largest
+ * x is the rotated row in fp32; x / g is rounded to fp32 (a power of two divides exactly, up to fp32's range), and
+ * what follows decides as the exact quotients do.  e2m1 has no NaN or infinity: they are stored as values of the largest
  * magnitude that the block's scale gives, infinities making that scale the largest one.  A NaN beside
  * numbers does not enter the block's maximum; a block of NaN alone gets the scale NaN (0x7f) and codes 0, and so
  * reads back as NaN.

@@ -468,3 +468,44 @@ def test_append_fp4_global_scales_at_the_ends_of_the_range(B, exponent):
     want = np.where(np.repeat(sc == 0, 8, axis=-1), 0, S.fp4_pack(codes))
     for c, s in ((kc, ks), (vc, vs)):
         assert np.array_equal(s.cpu().numpy(), sc) and np.array_equal(c.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("magnitude", [1.0, 1.0 + 2.0 ** -23, 1.0 + 2.0 ** -22, 1.0 - 2.0 ** -24, 1.0 - 2.0 ** -23, 1.3])
+@pytest.mark.parametrize("kg,vg", [(0.5, 0.25), (0.1, 0.37), (3.0, 1e-3)])
+def test_append_fp4_values_next_to_borders(B, layout, magnitude, kg, vg):
+    """Blocks that lie on the borders between codes, and between scales, and one fp32 step beside them.  At
+    position 0 a rotated value is its fp32 product with the magnitude (a cos 0 m - b sin 0 m = a m), so the
+    rows' exact values are known; x / g is rounded to fp32, and from there on the float64 oracle decides."""
+    import torch
+    rng = np.random.default_rng(6)
+    dim, rows = 128, 60
+    t = B.RopeTable(dim, [0] * (dim // 2), magnitude)
+    border = np.array([.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0])
+    x = np.empty((2, rows, 1, dim // 16, 16))
+    for w in (0, 1):
+        for r in range(rows):
+            for b in range(dim // 16):
+                i = int(rng.integers(20, 100))                          # scales of all sizes
+                s, up = S.E4M3[i], S.E4M3[i + 1]
+                x[w, r, 0, b] = rng.choice(border, 16) * rng.choice([-1, 1], 16) * s
+                x[w, r, 0, b, rng.integers(16)] = 6 * (s if (r + b) % 2 else (s + up) / 2)
+    k, v = (torch.from_numpy(a.reshape(rows, 1, dim)).half().cuda() for a in x)
+    u8 = lambda n: torch.zeros((rows, 1, n), dtype=torch.uint8, device="cuda")  # noqa: E731
+    kc, vc, ks, vs = u8(dim // 2), u8(dim // 2), u8(dim // 16), u8(dim // 16)
+    seen = [torch.empty_like(k) for _ in range(2)]
+    B.rope_append_fp4(None, k, v, kc, ks, vc, vs, i32(np.zeros(rows)), i32(np.arange(rows)), t, k_global=kg, v_global=vg,
+                      layout=layout, k_seen=seen[0], v_seen=seen[1])
+    torch.cuda.synchronize()
+    for src, m, g, c, s, sn in ((k, magnitude, kg, kc, ks, seen[0]), (v, 1.0, vg, vc, vs, seen[1])):
+        y = src.float().cpu().numpy() * np.float32(m) / np.float32(g)          # fp32, each rounded
+        assert y.dtype == np.float32
+        codes, sc, values = S.fp4_quantise(y.astype(np.float64), 1.0)
+        assert np.array_equal(s.cpu().numpy(), sc)
+        # (a block whose scale is 0 stores code 0, whatever the sign)
+        want = np.where(np.repeat(sc == 0, 8, axis=-1), 0, S.fp4_pack(codes))
+        assert np.array_equal(c.cpu().numpy(), want)
+        # values: the scales' product and the code's are rounded to fp32, then to fp16 (half a step, or 2^-25)
+        values = values * float(np.float32(g))
+        got = sn.double().cpu().numpy()
+        assert np.all(np.abs(got - values) <= np.abs(values) * (2.0 ** -11 + 2.0 ** -22) + 2.0 ** -25)

@@ -17,8 +17,8 @@
 // half) and one e4m3 scale s = e4m3(max|x| / (6 g)), g being the cache's fp32 scale; a code is
 // e2m1((x / g) / s), both rounded to nearest, ties to even.  The rotated values are quantised from fp32.
 // 8192 rows of 2 + 2 heads of 256 dims take 11.9 us, bound by the conversions and their latency (38 MB).
-// A quotient that is a border between two codes (x = border times scales: common, since all have few bits)
-// falls as the formula says: see quantise8.
+// Codes and scales fall as the formula says, ties (x = border times scales: common, since all have few bits)
+// and values next to them included: see quantise8.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -146,13 +146,6 @@ __device__ __forceinline__ float e4m3_value(uint8_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(c)));
   return unpack2(r, __half{}).x;
 }
-// Rounded to 20 significant bits.  Quotients are formed as products with a reciprocal, within 2 ulp of the
-// quotient, and decide alike everywhere but on the border between two codes (few bits): this takes a product
-// that missed its border by those 2 ulp back to it, so that the tie goes to the even code.  A quotient off a
-// border by less than 2^-21 of itself is taken for a tie; rows of at most 11 bits have none.  (Infinity stays
-// what it is; NaN must not come here.)
-__device__ __forceinline__ float snap(float v) { return __uint_as_float((__float_as_uint(v) + 8u) & ~15u); }
-
 __device__ __forceinline__ float amax8(const float* f) {
   float m = fabsf(f[0]);
 #pragma unroll
@@ -160,32 +153,67 @@ __device__ __forceinline__ float amax8(const float* f) {
   return m;
 }
 
-// Eight dims of a block whose scale's e4m3 value is s: code words; the quotient of f by the scales is f r.
-__device__ __forceinline__ uint32_t quantise8(const float* f, float r) {
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split_pair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Quotients of f by the divisor d (few bits), r being 1 / d to within some ulp.  The product p = f r is corrected
+// by its residual: f - p d is exact in fp32, so p + (f - p d) r is the quotient to 2^-44 of itself before its one
+// rounding.  That decides as the exact quotient does, ties included: a border between two codes or scales has at
+// most 5 bits, so border times d is a float, another float f is at least 2^-24 of it away, and the quotient's
+// neighbourhood that rounds to the border is narrower (half a step, by more than 2^-28 of the border).
+// p is kept within +-8, past the largest code, so that infinities and overflowing products keep their sign.
+
+// Eight dims of a block whose scales are d: code words.  (NaN is converted to 6.)
+__device__ __forceinline__ uint32_t quantise8(const float* f, float d, float r) {
   float v[8];
+  const uint64_t d2 = pair_of(d, d), r2 = pair_of(r, r);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = snap(fmaxf(f[k] * r, -8.0f));   // (NaN becomes -8, and so -6)
+  for (int k = 0; k < 8; k += 2) {
+    const float p0 = fminf(fmaxf(f[k] * r, -8.0f), 8.0f), p1 = fminf(fmaxf(f[k + 1] * r, -8.0f), 8.0f);
+    const uint64_t left = fma_pair(pair_of(-p0, -p1), d2, pair_of(f[k], f[k + 1]));
+    const float2 q = split_pair(fma_pair(left, r2, pair_of(p0, p1)));
+    v[k] = copysignf(q.x, f[k]);             // (-0 has come out as 0)
+    v[k + 1] = copysignf(q.y, f[k + 1]);
+  }
   return r > 0.0f ? e2m1x8(v) : 0u;
+}
+// The scale of a block with the largest magnitude m, in the cache's units.  A block of NaN alone has none: its scale
+// is e4m3's NaN, so that reads show it, and its codes are 0.
+__device__ __forceinline__ uint8_t scale_code(float m) {
+  constexpr float kSixth = 1.0f / 6.0f;
+  const float t = fminf(m, 4096.0f);         // (past 6 x 448 all are alike)
+  const float p = t * kSixth, q = fmaf(fmaf(-6.0f, p, t), kSixth, p);
+  return e4m3_of(m == m ? q : m);
 }
 
 // The two 8-dim halves of a K or V unit (dims da.. and db..) into the 4-bit cache row `cell`; ma and mb
 // are the largest magnitudes of the 16-dim blocks that the halves lie in (ONE: the same block).  f and the
-// magnitudes are in units of 1 / inv.
+// magnitudes are in units of `unit` = 1 / inv, both exact.
 template <typename T, bool ONE>
 __device__ __forceinline__ void write_fp4(const RopeParams& p, bool is_v, int64_t row, int32_t kvh, int64_t cell, int da,
-                                          int db, float inv, float ma, float mb, float* f) {
-  constexpr float kSixth = 1.0f / 6.0f;
-  // (a block of NaN alone has no largest magnitude: its scale is e4m3's NaN, so that reads show it, its codes are 0)
-  auto scale_of = [&](float m) { return e4m3_of(m == m ? snap(m * inv * kSixth) : m); };
+                                          int db, float unit, float inv, float ma, float mb, float* f) {
   auto reciprocal = [&](float s) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
     return s > 0.0f ? r * inv : 0.0f;
   };
-  const uint8_t ca = scale_of(ma), cb = ONE ? ca : scale_of(mb);
+  const uint8_t ca = scale_code(ma * inv), cb = ONE ? ca : scale_code(mb * inv);
   const float sa = e4m3_value(ca), sb = ONE ? sa : e4m3_value(cb);
   const float ra = reciprocal(sa), rb = ONE ? ra : reciprocal(sb);
-  const uint32_t wa = quantise8(f, ra), wb = quantise8(f + 8, rb);
+  const uint32_t wa = quantise8(f, sa * unit, ra), wb = quantise8(f + 8, sb * unit, rb);
   uint8_t* const codes = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + cell * (p.head_dim / 2);
   uint8_t* const scales = (is_v ? p.v_scale : p.k_scale) + cell * (p.head_dim / 16);
   if constexpr (ONE) {
@@ -314,12 +342,11 @@ __global__ void __launch_bounds__(kRopeThreads, !TURNS ? (FP4 ? 7 : 8) : FP4 ? 4
         for (int k = 0; k < 16; ++k) f[k] = 0.0f;
       }
       if constexpr (FP4) {
-        float inv = is_v ? p.v_inverse : p.k_inverse;
-        if (inv == 0.0f) {       // not a power of two: true quotients by the cache's scale
-          const float g = is_v ? p.v_global : p.k_global;
+        float inv = is_v ? p.v_inverse : p.k_inverse, unit = is_v ? p.v_global : p.k_global;
+        if (inv == 0.0f) {       // not a power of two: quotients by the cache's scale, rounded to fp32
 #pragma unroll
-          for (int k = 0; k < 16; ++k) f[k] = __fdiv_rn(f[k], g);
-          inv = 1.0f;
+          for (int k = 0; k < 16; ++k) f[k] = __fdiv_rn(f[k], unit);
+          inv = unit = 1.0f;
         }
         float ma = amax8(f), mb = amax8(f + 8);
         if constexpr (!INTERLEAVED) {
@@ -332,7 +359,7 @@ __global__ void __launch_bounds__(kRopeThreads, !TURNS ? (FP4 ? 7 : 8) : FP4 ? 4
         } else {
           ma = mb = fmaxf(ma, mb);
         }
-        if (stored) write_fp4<T, INTERLEAVED>(p, is_v, row, kvh, cell, ea, eb, inv, ma, mb, f);
+        if (stored) write_fp4<T, INTERLEAVED>(p, is_v, row, kvh, cell, ea, eb, unit, inv, ma, mb, f);
       } else if (stored) {
         store_halves<T>(is_v ? p.v_cache : p.k_cache, cell * p.head_dim, ea, eb, whole && p.wide_kv, f);
       }
