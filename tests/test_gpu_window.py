@@ -154,6 +154,24 @@ def test_non_finite_queries_stay_in_their_rows(B, fp4):
     assert bool(got[0][5, 1].isnan().all()) and bool(got[1][5, 1].isnan())
 
 
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("n,rows", [(60000, 1), (20000, 3), (900, 1)])
+def test_non_finite_queries_in_equal_shares(B, n, rows, fp4):
+    """Units in more parts than a warp joins, and in few: a NaN row is NaN in out and lse, the others are as
+    they were."""
+    import torch
+    b = Batch([(n, rows), (40, 2)], 4, 1, 64, 64, fp4=fp4, seed=rows)
+    assert B.window_workspace_bytes(rows + 2, 2, b.table.shape[1], 64, 4, 1, 64, 0, 0, fp4=fp4, num_sms=152) > 0
+    want = b.check(B, 0, 0)
+    b.q[0, 1, 3], b.q[rows + 1, 2], b.q[rows, 0, 0] = float("nan"), float("nan"), float("inf")
+    out, lse = b.call(B, 0, 0)
+    torch.cuda.synchronize()
+    bad = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[rows + 1, 2] = bad[rows, 0] = True
+    assert torch.equal(out[~bad], want[0][~bad]) and torch.equal(lse[~bad], want[1][~bad])
+    assert bool(out[bad].isnan().all()) and bool(lse[bad].isnan().all())
+
+
 def test_first_call_inside_a_capture(B):
     """A fresh process whose very first calls are captured."""
     import subprocess

@@ -19,7 +19,8 @@ constexpr int kJoinWarpParts = 8;  // parts up to which a warp takes a row
 // begins in block c of the attention grid and goes on in the following ones.  Two parts are the rule for
 // units of many rows, and then a warp takes a row; a long unit of few rows has a part in every block, and
 // then a block takes a row, D / 4 threads across it and the groups of threads each some of the parts.
-// Parts are added in a fixed order, so the result does not depend on timing.
+// Parts are added in a fixed order, so the result does not depend on timing.  A part that is NaN makes the row NaN,
+// its lse too (the maximum passes over NaN, the sum of the weights does not).
 template <int D, typename T>
 __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_constant__ WindowParams p) {
   constexpr int kCols = D / 4, kGroups = kJoinThreads / kCols;
@@ -64,7 +65,7 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
     uint32_t* const out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + rh * D + lane * kPer);
 #pragma unroll
     for (int k = 0; k < kPer / 2; ++k) out[k] = window_detail::pack16(acc[2 * k], acc[2 * k + 1], T{});
-    if (lane == 0 && p.lse) p.lse[rh] = m == -INFINITY ? -INFINITY : m + logf(total);
+    if (lane == 0 && p.lse) p.lse[rh] = total == 0.0f ? -INFINITY : m + logf(total);
     return;
   }
   for (int row = blockIdx.y; row < j.tokens * p.group; row += kJoinRows) {
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
       const int64_t rh = (static_cast<int64_t>(j.row0) + tok) * p.n_qheads + j.kvh * p.group + (row - tok * p.group);
       *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + rh * D + col * 4) =
           make_uint2(window_detail::pack16(acc.x, acc.y, T{}), window_detail::pack16(acc.z, acc.w, T{}));
-      if (col == 0 && p.lse) p.lse[rh] = m == -INFINITY ? -INFINITY : m + logf(total);
+      if (col == 0 && p.lse) p.lse[rh] = total == 0.0f ? -INFINITY : m + logf(total);
     }
     __syncthreads();
   }
