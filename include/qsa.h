@@ -411,9 +411,11 @@ qsa_status qsa_rope_append_fp4(const void* q, void* q_out, const void* k, const 
  * A row that sees nothing (kv_len < rows puts first rows at negative positions) gets out = 0 and lse = -inf.
  * Rows behind cu_seqlens_q[n_requests] (a padded batch) are left as they were.
  * What the cache holds at positions that no row sees (the rest of a page, tokens that left the window)
- * does not matter, NaN and infinities included.  A non-finite value that a row sees makes that row's
- * output non-finite, and may do so to the rows of up to 127 neighbouring (token, head) pairs of the same request and
- * KV head.
+ * does not matter, NaN and infinities included.  A row that sees a NaN, or a key whose logit is NaN or +inf, comes out
+ * as NaN, lse included; an infinite value that a row sees makes that row's output non-finite in its dim.  A key whose
+ * logit is -inf has weight 0, and a row whose keys all have that is as one that sees nothing.  A non-finite value in V
+ * may also reach the rows of up to 127 neighbouring (token, head) pairs of the same request and KV head (0 times
+ * infinity); one in K does not.
  *   scale > 0.  head_dim 64, 128 or 256; n_qheads / n_kvheads <= 128 (4-bit caches of 256 dims: <= 64).
  *   workspace: calls with few query tiles for the SMs cut the keys into equal shares and join the parts; they
  *       need qsa_window_workspace_bytes (for the device's SM count; 0 = none), 256-byte aligned.  NULL: taken from

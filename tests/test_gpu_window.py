@@ -172,6 +172,91 @@ def test_non_finite_queries_in_equal_shares(B, n, rows, fp4):
     assert bool(out[bad].isnan().all()) and bool(lse[bad].isnan().all())
 
 
+LAYOUTS = {      # how a call is dealt out: whole units, equal shares joined by warps, by blocks
+    "whole": ([(2600, 2600), (300, 300)], 8, 2), "few parts": ([(900, 1), (40, 2)], 4, 1),
+    "many parts": ([(60000, 1), (40, 2)], 4, 1)}
+
+
+@pytest.mark.parametrize("how", LAYOUTS)
+@pytest.mark.parametrize("what", ["k nan", "k inf", "k -inf", "v inf", "v -inf", "v nan"])
+def test_non_finite_values_that_rows_see(B, how, what):
+    """One element of the key at position 20 of the first request, q there positive for all: the logit is NaN, inf
+    or -inf.  With v, the element's dim is non-finite in every row that sees it; rows of other requests and
+    KV heads, and with k also the earlier rows, stay as they are."""
+    import torch
+    lens, hq, hkv = LAYOUTS[how]
+    b = Batch(lens, hq, hkv, 64, 64, seed=3)
+    R = b.R
+    ws = B.window_workspace_bytes(R, 2, b.table.shape[1], 64, hq, hkv, 64, 0, 0, num_sms=152)
+    assert (ws == 0) == (how == "whole")
+    b.q[..., 5] = b.q[..., 5].abs() + 0.5
+    want = b.call(B, 0, 0)
+    value = float(what.split()[1])
+    slot = int(b.table[0][0]) * 64 + 20
+    (b.k if what[0] == "k" else b.v)[slot, 0, 5] = value
+    out, lse = b.call(B, 0, 0)
+    torch.cuda.synchronize()
+    first, new = int(b.kv[0]), int(b.cu[1])
+    sees = np.arange(R) >= max(0, 20 - (first - new))
+    sees[new:] = False
+    hit = torch.zeros((R, hq), dtype=torch.bool, device="cuda")
+    hit[torch.from_numpy(sees).cuda(), :hq // hkv] = True
+    if what in ("k nan", "k inf"):
+        assert bool(out[hit].isnan().all()) and bool(lse[hit].isnan().all())
+        assert torch.equal(out[~hit], want[0][~hit]) and torch.equal(lse[~hit], want[1][~hit])
+    elif what == "k -inf":        # weight 0: as a batch that has the key's logit far below the others
+        b.k[slot, 0, 5] = -1e30
+        far = b.call(B, 0, 0)
+        torch.cuda.synchronize()
+        rows = torch.arange(R, device="cuda") != 20       # (the row at 20 sees earlier keys as well)
+        assert bool(out.isfinite().all()) and bool(lse.isfinite().all())
+        assert torch.equal(out[rows], far[0][rows]) and torch.equal(lse[rows], far[1][rows])
+    else:
+        got = out[hit][:, 5].float()
+        assert not bool(got.isfinite().any())
+        if what != "v nan" and how != "whole":            # decode rows: weights that are not 0
+            near = lens[0][1] == 1 and first < 2000
+            assert not near or bool((got == value).all())
+        dims = torch.arange(64, device="cuda") != 5
+        assert torch.equal(out[..., dims], want[0][..., dims]) and torch.equal(lse, want[1])
+        other = torch.ones_like(hit)
+        other[:new, :hq // hkv] = False
+        assert torch.equal(out[other], want[0][other])
+
+
+@pytest.mark.parametrize("n", [3, 900, 60000])
+def test_rows_whose_logits_are_all_minus_infinity(B, n):
+    """As rows that see nothing: out 0, lse -inf."""
+    import torch
+    b = Batch([(n, 1), (50, 3)], 4, 1, 128, 64)
+    want = b.call(B, 0, 0)
+    b.q[0, :, 0] = 1.0
+    at = torch.from_numpy(np.concatenate([np.arange(64) + 64 * p for p in b.table[0] if p >= 0])).cuda()
+    b.k[at, 0, 0] = -float("inf")
+    out, lse = b.call(B, 0, 0)
+    torch.cuda.synchronize()
+    assert float(out[0].abs().max()) == 0 and bool((lse[0] == -float("inf")).all())
+    assert torch.equal(out[1:], want[0][1:]) and torch.equal(lse[1:], want[1][1:])
+
+
+def test_infinite_values_of_vanishing_weight_are_not_lost_in_a_join(B):
+    """An infinite V whose part of a shared unit has a weight that fp32 cannot hold: inf or NaN, on both ways of
+    joining."""
+    import torch
+    for n in (900, 60000):
+        b = Batch([(n, 1)], 1, 1, 64, 64, seed=n)
+        b.q[:] = 0.0
+        b.q[..., 0] = 16.0
+        b.k[..., 0] = 0.0
+        far, near = int(b.table[0][0]) * 64 + 5, int(b.table[0][-1]) * 64 + (n - 1) % 64
+        b.k[near, 0, 0] = 100.0                                  # 200 above the others
+        b.v[far, 0, 7] = float("inf")
+        out, lse = b.call(B, 0, 0)
+        torch.cuda.synchronize()
+        assert not bool(out[0, 0, 7].isfinite()) and bool(lse.isfinite().all())
+        assert bool(out[0, 0, 8:].isfinite().all())
+
+
 def test_first_call_inside_a_capture(B):
     """A fresh process whose very first calls are captured."""
     import subprocess

@@ -44,6 +44,8 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     const float inv = m == -INFINITY ? 0.0f : 1.0f / total;
+    // a part that saw nothing of this row wrote no output: whatever is there stays out
+    const uint32_t saw = __ballot_sync(0xffffffffu, l != -INFINITY);
     float acc[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
@@ -54,7 +56,7 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
 #pragma unroll
       for (int k = 0; k < kPer; k += 2) {
         const float2 x = *reinterpret_cast<const float2*>(src + k);
-        if (ws != 0.0f) {
+        if (saw >> s & 1) {
           acc[k] += ws * x.x;
           acc[k + 1] += ws * x.y;
         }
@@ -103,9 +105,8 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     const float inv = m == -INFINITY ? 0.0f : 1.0f / total;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    // a part that saw nothing of this row wrote no output: whatever is there stays out
     auto add = [&](float v, const float4& o) {
-      if (v == -INFINITY) return;
+      if (v == -INFINITY) return;      // (saw nothing, as above)
       const float w = __expf(v - m) * inv;
       acc.x += w * o.x;
       acc.y += w * o.y;
