@@ -424,6 +424,38 @@ def test_rising_logits(B, dim, order):
     b.check(B, 333, 2)
 
 
+@pytest.mark.parametrize("dtype,fp4", [("float16", False), ("float16", True), ("bfloat16", True), ("bfloat16", False)])
+@pytest.mark.parametrize("n,rows,heads", [(6000, 6000, 16), (60000, 1, 1)])
+def test_a_long_tail_far_below_one_key(B, n, rows, heads, dtype, fp4):
+    """One key 18 nats above all others (v 0 there, 1 elsewhere): the others' weights, 2^-26 each, still add up, in
+    whole units and in shares.  A weight is off by half a step u_w of itself, in fp16 or by 2^-32 of the
+    largest where that is more; the output by its own half step (or fp16's least, 2^-25)."""
+    import torch
+    b = Batch([(n, rows)], heads, heads, 64, 64, dtype, fp4=fp4)
+    ws = B.window_workspace_bytes(rows, 1, b.table.shape[1], 64, heads, heads, 64, 0, 0, fp4=fp4, num_sms=152)
+    assert (ws == 0) == (rows > 1)
+    peak = int(b.table[0][0]) * 64 + 7
+    b.q[:] = 0.0
+    b.q[..., 0] = 96.0                                     # logit 96 k / 8
+    if fp4:
+        b.k[:], b.ks[:], b.v[:], b.vs[:] = 0, 0x38, 0x22, 0x40          # v = 1.0 * 2.0 * 0.5
+        b.k[peak, :, 0], b.v[peak] = 7, 0                               # k = 6 * 1.0 * 0.25
+    else:
+        b.k[:], b.v[:] = 0.0, 1.0
+        b.k[peak, :, 0], b.v[peak] = 1.5, 0.0
+    out, lse = b.call(B, 0, 0)
+    torch.cuda.synchronize()
+    p = np.arange(n - rows, n)
+    tail = np.where(p >= 7, p, 1) * np.exp(-18.0)
+    o = np.where(p >= 7, tail / (1 + tail), 1.0)[:, None, None]
+    z = np.where(p >= 7, 18.0 + np.log1p(tail), np.log(p + 1.0))[:, None]
+    u = torch.finfo(b.dt).eps / 2
+    uw = 2.0 ** -11 if fp4 or dtype == "float16" else 2.0 ** -8
+    bound = o * (uw + u + 2.0 ** -18) + (n * 2.0 ** -32 if uw == 2.0 ** -11 else 0.0) + 2.0 ** -25
+    assert np.all(np.abs(out.double().cpu().numpy() - o) <= bound)
+    assert np.all(np.abs(lse.double().cpu().numpy() - z) <= 2.0 ** -19 * np.abs(z) + 2.0 ** -22)
+
+
 @pytest.mark.parametrize("dim,n", [(128, 20000), (256, 9000)])
 @pytest.mark.parametrize("fp4", [False, True])
 def test_long_context_in_equal_shares(B, dim, n, fp4):

@@ -25,8 +25,8 @@
 //  * Softmax: two warpgroups, each thread one row and half of the tile's keys; the two halves of a row
 //    exchange their maxima through shared memory.  The running maximum is raised only when a tile
 //    exceeds it by 2^8, so that O is seldom rescaled; O and l share it, the result is exact.  S, m, l and
-//    O are fp32; P is rounded to 16 bits for the matrix product (half a step of a weight that is at most
-//    2^8), and l sums the unrounded weights.
+//    O are fp32; P is rounded to 16 bits for the matrix product (half a step of a weight; see kLiftFp16 for
+//    those far below the maximum), and l sums the unrounded weights.
 //  * K and V are staged as 128-byte-swizzled 64-dim blocks of 128 keys in a ring that the MMA consumes in
 //    the order K0 K1 V0 K2 V1 ...  Four producer warps issue TMA boxes of up to 64 keys (page sizes that
 //    are multiples of 8), or gathers of four rows for other page sizes.
@@ -118,6 +118,10 @@ namespace window_detail {
 
 constexpr unsigned long long kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
 constexpr float kRaise = 8.0f;          // log2 units by which a tile may exceed the running maximum
+// Weights in fp16 are multiplied by 2^7 (l too, which lse undoes): at most 2^15 with kRaise, so that those far
+// below the maximum do not fall out of fp16's range.  Below 2^-21 of the maximum they are rounded to whole 2^-31,
+// below 2^-32 they are lost; unscaled, 6000 keys 18 nats below another one counted in l, but not in O.
+constexpr float kLiftFp16 = 7.0f;       // (log2)
 constexpr int32_t kShortUnit = 4;        // key tiles
 constexpr float kLn2f = 0.6931471805599453f;
 enum Site : int32_t {
@@ -538,6 +542,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
     const float sc = p.scale_log2;
     const float raise = kRaise / sc;
+    constexpr float kLift = FP4 || std::is_same<T, __half>::value ? kLiftFp16 : 0.0f;
     // (loops that run once a unit, or seldom, are not unrolled: their instructions would have to be fetched anew each
     // time; unrolled: decode batch 129.1 -> 126.6 us, causal prompts of 128 dims 215 -> 205 us rolled)
     uint32_t it = 0, js = 0, eb = 0;          // records, tiles and ring entries so far
@@ -650,7 +655,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
               m = nm;
             }
           }
-          const float neg = m == -INFINITY ? 0.0f : -m * sc;
+          const float neg = m == -INFINITY ? 0.0f : kLift - m * sc;
           const uint64_t sc2 = pair_of(sc, sc), neg2 = pair_of(neg, neg);
           uint64_t a0 = 0, a1 = 0;                 // sums of pairs
           uint32_t pk[32];
@@ -702,7 +707,8 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       const bool empty = l == 0.0f && m == -INFINITY;
       const float inv = empty ? 0.0f : p.v_mult / l;
       if (store && wg == 0) {
-        const float lse = empty ? -INFINITY : m * sc * kLn2f + logf(l);
+        constexpr float kUnlift = kLift > 0.0f ? 0x1p-7f : 1.0f;
+        const float lse = empty ? -INFINITY : m * sc * kLn2f + logf(l * kUnlift);
         if (u.part >= 0) p.part_lse[u.part * kWinTile + row] = lse;
         else if (p.lse) p.lse[rh] = lse;
       }
