@@ -281,7 +281,7 @@ typedef enum qsa_dtype { QSA_BF16 = 0, QSA_FP16 = 1 } qsa_dtype;
  *   free_head_out [1] int32: free_head plus the pages taken; may be free_head itself, so that a step
  *               captured in a CUDA graph takes further pages on every replay.
  *   cu_seqlens_q [n_requests + 1] int32: exclusive sums of the new lengths, cut off at max_rows.
- *   kv_lens     [n_requests] int32: past + new (cut off at 2^31 - 1).
+ *   kv_lens     [n_requests] int32: past + new (cut off at 2^31 - 1); may be past_lens or new_lens itself.
  *   positions   [max_rows] int32, nullable: position of each row in its request.
  *   slots       [max_rows] int32, nullable: physical slot of each row, page * page_size +
  *               position mod page_size; -1 where the page is missing, past pages_per_req, or (when
@@ -290,7 +290,8 @@ typedef enum qsa_dtype { QSA_BF16 = 0, QSA_FP16 = 1 } qsa_dtype;
  *               max_rows is at least the sum of the new lengths where every request's rows are to be
  *               used: the request that it cuts keeps the kv_lens of all its tokens.
  *   shortfall   [1] int32, nullable: pages wanted beyond the end of the free list (0 = none missing).
- * One kernel launch, no host read.  Calls that share a free list are ordered by the caller.
+ * One kernel launch, no host read.  Calls that share a free list are ordered by the caller.  Outputs may not overlap
+ * the inputs or each other, but for free_head_out and kv_lens as said there.
  * Errors: QSA_ERR_INVALID_ARG for null or misaligned pointers (4 bytes) and sizes below 1 (n_free,
  * n_pages, max_rows: below 0); QSA_ERR_UNSUPPORTED for more than 16384 requests, or 2^31 rows or free
  * pages. */

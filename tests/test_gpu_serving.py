@@ -93,6 +93,26 @@ def test_page_plan_shortage_bounds_and_bad_lengths(B):
     check_plan(B, np.array([5, 2 ** 31 - 1, 1]), big, np.full((3, 2), 1), np.arange(9), 0, 64, 100)
 
 
+@pytest.mark.parametrize("n,new_max", [(5, 3), (1500, 4), (9000, 3), (300, 400)])
+@pytest.mark.parametrize("which", ["past", "new"])
+def test_page_plan_updates_lengths_in_place(B, n, new_max, which):
+    """kv_lens written over the lengths it is made from, by one CTA and by a cluster."""
+    import torch
+    rng = np.random.default_rng(n)
+    past, new, table, free, n_pages = plan_case(rng, n, new_max, 200, 16)
+    want = S.page_plan(past, new, table, free, 0, 16, int(new.sum()) + 3, n_pages)
+    for _ in range(20):
+        lens = dict(past=i32(past), new=i32(new))
+        t = i32(table)
+        got = B.page_plan(lens["past"], lens["new"], t, i32(free), i32([0]), 16, int(new.sum()) + 3, n_pages=n_pages,
+                          kv_lens=lens[which])
+        torch.cuda.synchronize()
+        for a, b in zip((t, got.cu_seqlens_q, lens[which], got.positions, got.slots, got.free_head), want):
+            assert np.array_equal(a.cpu().numpy().reshape(np.shape(b)), b)
+        other = "new" if which == "past" else "past"
+        assert np.array_equal(lens[other].cpu().numpy(), dict(past=past, new=new)[other])
+
+
 def test_page_plan_replays_from_a_graph(B):
     """Captured once with the head in place: every replay takes the next pages."""
     import torch

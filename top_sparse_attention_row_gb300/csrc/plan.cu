@@ -11,8 +11,8 @@
 // and memory latency (64 decode requests 5.5 us, 256 prompt chunks of up to 2048 rows 12.6 us).  One kernel does all of it: a single cluster of up to 8 CTAs, each of which
 // repeats the prefix sums over all requests in its own shared memory (two loads per request) and
 // then takes its share of the fresh pages and of the rows.  The cluster barrier orders every read of
-// the free-list head before its one write, so the head may be updated in place and a captured step
-// replays.
+// the free-list head before its one write, and of the lengths before kv_lens, so head and lengths may be
+// updated in place and a captured step replays.
 #include <cstdint>
 
 #include "internal.h"
@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(kThreadsPlan, 1) page_plan_kernel(const PagePl
     int64_t pi = 0, ni = 0;
     int32_t need = 0;
     if (i < n) {
-      pi = max(__ldg(p.past_lens + i), 0);
-      ni = max(__ldg(p.new_lens + i), 0);
+      pi = max(__ldcg(p.past_lens + i), 0);
+      ni = max(__ldcg(p.new_lens + i), 0);
       need = pages_of(p, pi + ni) - pages_of(p, pi);
     }
     const int64_t r = warp_inclusive(ni, lane), g = warp_inclusive(need, lane);
@@ -97,10 +97,8 @@ __global__ void __launch_bounds__(kThreadsPlan, 1) page_plan_kernel(const PagePl
       past[i] = static_cast<int32_t>(pi);
       cu[i + 1] = static_cast<int32_t>(end < p.max_rows ? end : p.max_rows);
       first[i + 1] = saturate(g0 + g);
-      if (rank == 0) {
-        p.cu_seqlens_q[i + 1] = cu[i + 1];
-        p.kv_lens[i] = saturate(pi + ni);
-      }
+      if (rank == 0) p.cu_seqlens_q[i + 1] = cu[i + 1];
+      if (p.cluster == 1) p.kv_lens[i] = saturate(pi + ni);     // (this thread alone has read the lengths)
     }
     __syncthreads();   // the totals are overwritten by the next round
   }
@@ -119,6 +117,11 @@ __global__ void __launch_bounds__(kThreadsPlan, 1) page_plan_kernel(const PagePl
 
   const int64_t stride = static_cast<int64_t>(p.cluster) * kThreadsPlan;
   const int64_t self = static_cast<int64_t>(rank) * kThreadsPlan + tid;
+  // kv_lens may be past_lens or new_lens: where several CTAs read those, it is written behind the barrier
+  if (p.cluster > 1) {
+    for (int64_t i = self; i < n; i += stride)
+      p.kv_lens[i] = saturate(static_cast<int64_t>(past[i]) + max(__ldcg(p.new_lens + i), 0));
+  }
   // Fresh page k of the step goes to its request's next table entry (-1 past the end of the list).
   const int32_t n_fresh = first[n];
   for (int64_t k = self; k < n_fresh; k += stride) {

@@ -450,7 +450,8 @@ Page tables and slot maps of a step from its requests' lengths (qsa_page_plan).
 
 past_lens, new_lens [n_requests] int32; page_table [n_requests, pages_per_req] int32 is
 updated in place with pages taken from free_pages [n_free] int32, of which free_head [1] int32
-are taken already; free_head_out = free_head updates it in place (None = a new tensor).
+are taken already; free_head_out = free_head updates it in place (None = a new tensor), and so does
+kv_lens = past_lens with the lengths.
 Returns cu_seqlens_q [n_requests + 1], kv_lens [n_requests], positions and slots [max_rows] (-1 on
 rows past the last request), free_head [1] and shortfall [1], all int32.)doc";
 constexpr char k_doc_rope[] = R"doc(rope(x, positions, table, *, layout="half", rot_offset=0, transpose=False, out=None, stream=None)
