@@ -293,8 +293,8 @@ typedef enum qsa_dtype { QSA_BF16 = 0, QSA_FP16 = 1 } qsa_dtype;
  * One kernel launch, no host read.  Calls that share a free list are ordered by the caller.  Outputs may not overlap
  * the inputs or each other, but for free_head_out and kv_lens as said there.
  * Errors: QSA_ERR_INVALID_ARG for null or misaligned pointers (4 bytes) and sizes below 1 (n_free,
- * n_pages, max_rows: below 0); QSA_ERR_UNSUPPORTED for more than 16384 requests, or 2^31 rows or free
- * pages. */
+ * n_pages, max_rows: below 0); QSA_ERR_UNSUPPORTED for more than 16384 requests, or 2^31 rows, free
+ * pages or table entries. */
 qsa_status qsa_page_plan(const int32_t* past_lens, const int32_t* new_lens, int32_t* page_table,
                          const int32_t* free_pages, int64_t n_free, const int32_t* free_head,
                          int32_t* free_head_out, int32_t* cu_seqlens_q, int32_t* kv_lens,

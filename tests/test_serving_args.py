@@ -40,6 +40,13 @@ def test_page_plan_refusals(B, kw, status):
     assert B.load_library().qsa_page_plan(*plan_args(**kw)) == status
 
 
+def test_page_plan_refuses_tables_whose_pages_pass_32_bits(B):
+    """A step's fresh pages are numbered in 32 bits."""
+    f = B.load_library().qsa_page_plan
+    assert f(*plan_args(n=16384, ppr=131072)) == UNSUPPORTED
+    assert f(*plan_args(n=2, ppr=1 << 30)) == UNSUPPORTED
+
+
 def rope_spec(B, **kw):
     steps = (ctypes.c_uint64 * 256)()
     a = dict(steps=ctypes.addressof(steps), rot_dim=64, rot_offset=0, layout=0, transpose=0, magnitude=1.0)

@@ -317,7 +317,9 @@ qsa_status qsa_page_plan(const int32_t* past_lens, const int32_t* new_lens, int3
                         static_cast<const void*>(positions), static_cast<const void*>(slots),
                         static_cast<const void*>(shortfall)})
     if (!aligned_to(a, 4)) return QSA_ERR_INVALID_ARG;
-  if (n_requests > qsa::kPlanMaxRequests || max_rows > INT32_MAX || n_free > INT32_MAX)
+  // the kernel numbers a step's fresh pages in 32 bits: no more than the table has entries
+  if (n_requests > qsa::kPlanMaxRequests || max_rows > INT32_MAX || n_free > INT32_MAX ||
+      static_cast<int64_t>(n_requests) * pages_per_req > INT32_MAX)
     return QSA_ERR_UNSUPPORTED;
   int32_t sms = 0;
   const qsa_status st = qsa::device_sms(&sms);
