@@ -147,6 +147,14 @@ def test_rope_table_refusals(B):
     assert t.steps == [1, 2 ** 64 - 1] and t.magnitude == 1.5
 
 
+def test_rope_table_wants_a_step_for_every_pair(B):
+    """Too few would leave pairs unturned, silently."""
+    for rot, steps in ((8, [1, 2, 3]), (8, [1, 2, 3, 4, 5]), (8, []), (7, [1, 2, 3]), (-2, []), (0, [1])):
+        with pytest.raises(ValueError):
+            B.RopeTable(rot, steps, 1.0)
+    assert B.RopeTable(0, [], 1.0).steps == [] and B.RopeTable(8, range(4), 1.0).steps == [0, 1, 2, 3]
+
+
 def test_binding_refuses_cpu_and_mismatched_tensors(B):
     import torch
     i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731

@@ -621,7 +621,11 @@ class RopeTable:
     fixed-point steps on the host and the magnitude of the rotated values."""
 
     def __init__(self, rot_dim: int, steps, magnitude: float):
-        rot_dim = int(rot_dim)
+        rot_dim, steps = int(rot_dim), list(steps)
+        if rot_dim < 0 or rot_dim % 2 != 0:
+            raise ValueError(f"rot_dim must be even and not negative, got {rot_dim}")
+        if len(steps) != rot_dim // 2:
+            raise ValueError(f"a rotation of {rot_dim} dims has {rot_dim // 2} steps, got {len(steps)}")
         self._steps = (ctypes.c_uint64 * max(1, rot_dim // 2))(*steps)
         # what the extension reads: the address of the steps (which live as long as this table), their part
         # of the head and the magnitude
