@@ -1,5 +1,6 @@
 """Builds libqsa.so (the C-ABI library) in-tree with nvcc for sm_103a, and the Python extension
 _serving (argument checks of the serving-step calls, csrc/torch_serving.cpp) with the host compiler.
+The library needs nvcc alone; where PyTorch is not installed, the extension is left out.
 
 Usage: ``python -m top_sparse_attention_row_gb300.build`` or ``build()`` from Python.
 Translation units compile in parallel; objects go to ``_build/`` next to this file.
@@ -7,11 +8,13 @@ Translation units compile in parallel; objects go to ``_build/`` next to this fi
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -34,6 +37,15 @@ def _nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def torch_root() -> Optional[str]:
+    """PyTorch's folder, or None where it is not installed."""
+    try:
+        spec = importlib.util.find_spec("torch")
+    except (ImportError, ValueError):
+        return None
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
 
 
 def _compile(nvcc: str, src: str, verbose_ptxas: bool) -> str:
@@ -84,11 +96,13 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
         os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".h", ".cuh"))
     ] + [os.path.join(ROOT, "include", "qsa.h")]
     newest = max(os.path.getmtime(s) for s in srcs)
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, EXT)):
+    with_ext = torch_root() is not None
+    targets = (LIB, EXT) if with_ext else (LIB,)
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in targets):
         return LIB
     nvcc = _nvcc()
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ext_obj = ex.submit(_compile_extension)
+        ext_obj = ex.submit(_compile_extension) if with_ext else None
         objs = list(ex.map(lambda s: _compile(nvcc, s, verbose_ptxas), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lrt", "-ldl", "-lpthread"]
@@ -96,7 +110,10 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_extension(ext_obj.result())
+    if ext_obj is None:
+        sys.stderr.write("PyTorch is not installed: the _serving extension (binding.py's serving-step calls) is not built\n")
+    else:
+        _link_extension(ext_obj.result())
     return LIB
 
 
