@@ -27,6 +27,7 @@ def made(monkeypatch, tmp_path):
     monkeypatch.setattr(b, "BUILD", str(tmp_path / "_build"))
     monkeypatch.setattr(b, "LIB", str(tmp_path / "libqsa.so"))
     monkeypatch.setattr(b, "EXT", str(tmp_path / "_serving.so"))
+    monkeypatch.setattr(b, "EXT_STAMP", str(tmp_path / "_build" / "_serving.made_for"), raising=False)
     monkeypatch.setattr(b, "_nvcc", lambda: "/usr/local/cuda/bin/nvcc")
     monkeypatch.setattr(b.subprocess, "run", run)
     b.ran = ran
@@ -61,3 +62,25 @@ def test_an_extension_that_does_not_compile_is_an_error(made, monkeypatch):
     with pytest.raises(RuntimeError, match="g\\+\\+ failed"):
         made.build()
     assert os.path.exists(made.LIB)
+
+
+def test_the_extension_is_built_again_for_another_torch(made, monkeypatch, tmp_path):
+    """It is compiled against PyTorch's headers: another version, or place, needs another extension."""
+    made.build()
+    del made.ran[:]
+    other = tmp_path / "torch"
+    other.mkdir()
+    (other / "version.py").write_text("__version__ = '0.0.1'")
+    monkeypatch.setattr(made, "torch_root", lambda: str(other))
+    made.build()
+    assert "_serving.so" in made.ran
+    del made.ran[:]
+    made.build()
+    assert made.ran == []
+    (other / "version.py").write_text("__version__ = '0.0.2'")
+    made.build()
+    assert "_serving.so" in made.ran
+    os.remove(made.EXT_STAMP)                       # not known what it was built against
+    del made.ran[:]
+    made.build()
+    assert "_serving.so" in made.ran

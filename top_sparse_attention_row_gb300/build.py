@@ -28,6 +28,8 @@ SOURCES = ["prefill.cu", "mla.cu", "union.cu", "api.cpp", "noalloc.cu", "probe.c
 EXT_SOURCE = "torch_serving.cpp"
 EXT = os.path.join(PKG, "_serving" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
+EXT_STAMP = os.path.join(BUILD, "_serving.made_for")       # beside the objects: what EXT was built against
+
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 
@@ -46,6 +48,20 @@ def torch_root() -> Optional[str]:
     except (ImportError, ValueError):
         return None
     return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+
+
+def _made_for(root: str) -> str:
+    """What an extension is compiled against beside the sources: PyTorch's place and version, and the interpreter."""
+    with open(os.path.join(root, "version.py")) as f:
+        return f"{root}\n{f.read()}\n{sys.version}\n{sysconfig.get_config_var('EXT_SUFFIX')}\n"
+
+
+def _extension_is_for(root: str) -> bool:
+    try:
+        with open(EXT_STAMP) as f:
+            return f.read() == _made_for(root)
+    except OSError:
+        return False
 
 
 def _compile(nvcc: str, src: str, verbose_ptxas: bool) -> str:
@@ -96,9 +112,11 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
         os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".h", ".cuh"))
     ] + [os.path.join(ROOT, "include", "qsa.h")]
     newest = max(os.path.getmtime(s) for s in srcs)
-    with_ext = torch_root() is not None
+    root = torch_root()
+    with_ext = root is not None
     targets = (LIB, EXT) if with_ext else (LIB,)
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in targets):
+    current = all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in targets)
+    if not force and current and (not with_ext or _extension_is_for(root)):
         return LIB
     nvcc = _nvcc()
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
@@ -114,6 +132,8 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
         sys.stderr.write("PyTorch is not installed: the _serving extension (binding.py's serving-step calls) is not built\n")
     else:
         _link_extension(ext_obj.result())
+        with open(EXT_STAMP, "w") as f:
+            f.write(_made_for(root))
     return LIB
 
 
