@@ -309,8 +309,9 @@ qsa_status qsa_page_plan(const int32_t* past_lens, const int32_t* new_lens, int3
  * transposed, which takes the gradient of the rotated rows to the gradient of the rows.  The part is
  * dims rot_offset .. rot_offset + rot_dim - 1; the other dims pass through unchanged.
  *   steps: HOST pointer to rot_dim / 2 fixed-point numbers, 2^64 * (theta_i / 2 pi mod 1), kept by
- *          the caller (qsa_rope_steps makes them); the angle is then exact to 2^-33 turns at any
- *          31-bit position. */
+ *          the caller.  A step's angle at a 31-bit position is taken exactly, but for the last rounding of its half
+ *          turns to fp32 (2^-25 of one).  qsa_rope_steps makes the steps in doubles: theta_i <= 1 comes within
+ *          2^-53 turns per token of the formula's, which adds up to 2^-22 turns at position 2^31. */
 typedef enum qsa_rope_layout { QSA_ROPE_HALF = 0, QSA_ROPE_INTERLEAVED = 1 } qsa_rope_layout;
 typedef struct qsa_rope_spec {
   const uint64_t* steps;    /* host, [rot_dim / 2] */

@@ -147,6 +147,38 @@ def test_rope_table_refusals(B):
     assert t.steps == [1, 2 ** 64 - 1] and t.magnitude == 1.5
 
 
+PI = "3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803"
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(scaling="linear", factor=4.0), dict(scaling="ntk", factor=8.0)])
+@pytest.mark.parametrize("rot,base", [(64, 10000.0), (128, 500000.0), (256, 1000000.0), (10, 2.5)])
+def test_rope_steps_against_80_digits(B, rot, base, kw):
+    """A step's error per token, and an angle's at the largest position.  In doubles, with e = 2 i / rot and the base b
+    (for ntk b f^(rot / (rot - 2))): e is rounded (moves b^-e by e ln b 2^-53 of itself), b too (e times the roundings
+    of its own power, (1 + 2 ln f + 2 + 1) 2^-53), pow is good to 2^-52, and 2 pi, its quotient and the
+    scaling's round 2^-53 each: theta (e (ln b + 2 ln f + 4) + 6) 2^-53 / 2 pi, and 2^-64 from the cut to an
+    integer.  theta falls with e faster than the bracket grows: 6 / 2 pi = 2^-0.06 covers all pairs."""
+    from decimal import Decimal as D, localcontext
+    got = B.rope_table(rot, base, **kw).steps
+    with localcontext() as c:
+        c.prec = 80
+        f, b = D(kw.get("factor", 1.0)), D(base)
+        if kw.get("scaling") == "ntk":
+            b = b * f ** (D(rot) / D(rot - 2))
+        for i, step in enumerate(got):
+            e = D(2 * i) / D(rot)
+            turns = b ** -e / (2 * D(PI))
+            if kw.get("scaling") == "linear":
+                turns /= f
+            off = D(step) / D(2) ** 64 - turns
+            bound = float(turns) * (float(e) * (math.log(float(b)) + 2 * math.log(float(f)) + 4) + 6) * 2.0 ** -53
+            assert abs(float(off)) <= bound + 2.0 ** -64 <= 2.0 ** -53
+            pos = 2 ** 31 - 1
+            far = D((pos * step) % 2 ** 64) / D(2) ** 64 - (pos * turns) % 1
+            far = abs(float(far))
+            assert min(far, 1 - far) <= 2.0 ** -22
+
+
 def test_rope_table_wants_a_step_for_every_pair(B):
     """Too few would leave pairs unturned, silently."""
     for rot, steps in ((8, [1, 2, 3]), (8, [1, 2, 3, 4, 5]), (8, []), (7, [1, 2, 3]), (-2, []), (0, [1])):

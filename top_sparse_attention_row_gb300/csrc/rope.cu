@@ -3,10 +3,10 @@
 // Pair (a, b) of a head at position x turns by the angle x * theta_i: a' = m (a cos - b sin),
 // b' = m (b cos + a sin).  The pairs are dims (i, i + rot/2) in the half layout and (2i, 2i + 1) in the
 // interleaved one.  theta_i comes as a step: the fraction of a full turn per token, as a 64-bit
-// fixed-point number.  x * step modulo 2^64 is then the angle's fraction of a turn, exact to 2^-33
-// turns at any 31-bit position, from one integer product (theta_i * x in fp32 is off by 2^-24 of the
-// whole angle, 0.06 rad at a million).  Its upper half, as a signed number of half turns, goes to
-// sincospi.
+// fixed-point number.  x * step modulo 2^64, one integer product, is then that step's angle as a fraction of
+// a turn at any 31-bit position (theta_i * x in fp32 is off by 2^-24 of the whole angle, 0.06 rad at a
+// million; the steps themselves are made in doubles, 2^-53 turns per token).  Its upper half, as a signed
+// number of half turns, is rounded to fp32 (2^-25 half turns) and goes to sincospi.
 //
 // The operator reads and writes every element once and does a handful of operations on each, so it is
 // bound by memory (8192 rows of 26 heads of 256 dims 42.6 us, 5.5 TB/s: 81 % of the measured copy rate).  A thread owns one 16-dim unit (8 pairs) of a row: it computes its 8 sines and
