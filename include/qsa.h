@@ -352,8 +352,10 @@ qsa_status qsa_rope_steps(const qsa_rope_scaling* scaling, int32_t rot_dim, doub
  * elements apart (0 = one row for all); out likewise with out_stride >= n_heads * head_dim; out may be x with the same
  * stride, and may not overlap it otherwise.  positions [n_rows] int32; rows with a negative position
  * are left out: their output is not written.  The arithmetic is fp32, rounded once.
- * Any head_dim, offset, stride and alignment is taken; rows whose units of 16 dims start on 16-byte
- * boundaries run the fast kernel. */
+ * Any offset, stride and alignment is taken; rows whose units of 16 dims start on 16-byte boundaries run the
+ * fast kernel.
+ * Errors: QSA_ERR_INVALID_ARG; QSA_ERR_UNSUPPORTED for head_dim or n_heads above 16384 (KV heads of the calls
+ * below: 8192), rot_dim above 512, 2^31 rows and more. */
 qsa_status qsa_rope(const void* x, void* out, const int32_t* positions, const qsa_rope_spec* rope,
                     int64_t n_rows, int32_t n_heads, int32_t head_dim, int64_t x_stride,
                     int64_t out_stride, int32_t dtype, void* stream);

@@ -85,6 +85,15 @@ def test_rope_append_refusals(B, spec, kw, status):
     assert B.load_library().qsa_rope_append(*append_args(B, s, **kw)) == status
 
 
+def test_rope_append_limits_of_heads(B):
+    """What the header states: 16384 query heads, 8192 KV heads, 16384 dims."""
+    f, s = B.load_library().qsa_rope_append, rope_spec(B)
+    for ok, bad in ((dict(hq=16384), dict(hq=16385)), (dict(hkv=8192), dict(hkv=8193)), (dict(d=16384), dict(d=16385))):
+        wide = dict(qs=1 << 40, qos=1 << 40, ks=1 << 40, vs=1 << 40)
+        assert f(*append_args(B, s, **wide, **ok)) == OK
+        assert f(*append_args(B, s, **wide, **bad)) == UNSUPPORTED
+
+
 def test_rope_refusals(B):
     f = B.load_library().qsa_rope
     s = rope_spec(B)

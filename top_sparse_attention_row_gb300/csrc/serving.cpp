@@ -18,7 +18,7 @@ int32_t shift_of(int32_t v) {
 }
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
-constexpr int32_t kMaxHeads = 32768;      // query and KV heads each (blockIdx.y holds a head share)
+constexpr int32_t kMaxQHeads = 16384, kMaxKvHeads = 8192;   // blockIdx.y holds a share of the q, k and v heads
 constexpr int32_t kMaxHeadDim = 16384;
 
 // The rotation's own arguments (rope may be null where nothing turns).
@@ -47,7 +47,7 @@ qsa_status run_rope(qsa::RopeParams& p, const qsa_rope_spec* rope, int32_t dtype
       (dtype != QSA_BF16 && dtype != QSA_FP16))
     return QSA_ERR_INVALID_ARG;
   if (p.n_qheads + static_cast<int64_t>(p.n_kvheads) < 1) return QSA_ERR_INVALID_ARG;
-  if (p.n_qheads > kMaxHeads / 2 || p.n_kvheads > kMaxHeads / 4 || p.head_dim > kMaxHeadDim ||
+  if (p.n_qheads > kMaxQHeads || p.n_kvheads > kMaxKvHeads || p.head_dim > kMaxHeadDim ||
       p.n_rows > INT32_MAX)
     return QSA_ERR_UNSUPPORTED;
   const int64_t q_width = static_cast<int64_t>(p.n_qheads) * p.head_dim;
