@@ -486,6 +486,60 @@ def test_long_prompt(B, dim, hq, hkv, dtype):
     b.check(B, 500, 4, rows=rows)
 
 
+def dealt_out(B, b, hq, hkv, window, sink, fp4):
+    """"whole" units or "shares", as on a device of 152 SMs."""
+    n = B.window_workspace_bytes(b.R, len(b.kv), b.table.shape[1], b.ps, hq, hkv, b.dim, window, sink, fp4=fp4, num_sms=152)
+    return "shares" if n else "whole"
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens,heads,window,sink", [
+    ([(4000, 4000)], 12, 200, 3), ([(1400, 1400), (700, 150), (90, 90), (40, 1)], 24, 0, 0)])
+def test_several_whole_units_per_block(B, dim, lens, heads, window, sink, fp4):
+    """More than twice as many query tiles as SMs, so that blocks take over unit after unit: every ring, record and
+    barrier goes round several times, with units of unequal length among them."""
+    rng = np.random.default_rng(dim)
+    b = Batch(lens, heads, heads, dim, 64, fp4=fp4, seed=dim)
+    tile = 64 if fp4 and dim == 256 else 128
+    assert sum(-(-m // tile) for _, m in lens) * heads > 2 * 152
+    assert dealt_out(B, b, heads, heads, window, sink, fp4) == "whole"
+    rows = np.unique(np.concatenate([rng.choice(b.R, 24, replace=False), [0, 127, 128, b.R - 1]]))
+    b.check(B, window, sink, rows=rows)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("dim", [64, 256])
+def test_equal_shares_over_more_tiles_than_threads(B, dim, fp4):
+    """Every block adds up the units' tiles, its threads one each at a time: here in several rounds, with many requests
+    that bring no row, and shares that begin in the later rounds."""
+    rng = np.random.default_rng(dim)
+    some = [(int(rng.integers(1, 400)), 1) for _ in range(600)]
+    some[50], some[599] = (9000, 1), (2500, 1)
+    sparse = [(int(rng.integers(1, 300)), int(rng.random() < 0.1)) for _ in range(2500)]
+    sparse[2400], sparse[7] = (6000, 3), (3000, 2)
+    for lens in (some, sparse):
+        b = Batch(lens, 4, 1, dim, 64, fp4=fp4, seed=dim)
+        assert b.R // (128 // 4) + len(lens) > 512 and dealt_out(B, b, 4, 1, 0, 0, fp4) == "shares"
+        if lens is sparse:
+            assert len(lens) > 3 * 768
+        b.check(B, 0, 0)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("dim,hq,hkv", [(128, 32, 8), (256, 24, 2)])
+def test_a_prompt_in_tables_of_any_width(B, dim, hq, hkv, fp4):
+    """How a call is dealt out goes by the table's width; what it computes does not."""
+    b = Batch([(1024, 1024)], hq, hkv, dim, 64, fp4=fp4, seed=1)
+    rows = np.arange(0, 1024, 79)
+    narrow, ways = b.table, set()
+    for wide in (1, 4, 64):
+        b.table = np.concatenate([narrow, np.full((1, narrow.shape[1] * (wide - 1)), -1)], 1)
+        ways.add(dealt_out(B, b, hq, hkv, 0, 0, fp4))
+        b.check(B, 0, 0, rows=rows)
+    assert "shares" in ways
+
+
 def test_many_requests(B):
     rng = np.random.default_rng(9)
     lens = [(int(n), int(min(n, m))) for n, m in zip(rng.integers(1, 200, 400), rng.integers(0, 4, 400))]
