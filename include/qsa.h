@@ -420,7 +420,8 @@ qsa_status qsa_rope_append_fp4(const void* q, void* q_out, const void* k, const 
  * logit is -inf has weight 0, and a row whose keys all have that is as one that sees nothing.  A non-finite value in V
  * may also reach the rows of up to 127 neighbouring (token, head) pairs of the same request and KV head (0 times
  * infinity); one in K does not.
- *   scale > 0.  head_dim 64, 128 or 256; n_qheads / n_kvheads <= 128 (4-bit caches of 256 dims: <= 64).
+ *   scale > 0, scale log2(e) (times k_global) a positive number of fp32.  head_dim 64, 128 or 256; n_qheads /
+ * n_kvheads <= 128 (4-bit caches of 256 dims: <= 64).
  *   workspace: calls with few query tiles for the SMs cut the keys into equal shares and join the parts; they
  *       need qsa_window_workspace_bytes (for the device's SM count; 0 = none), 256-byte aligned.  NULL: taken from
  *       the library's pool on `stream`.  Calls that overlap need a workspace each.

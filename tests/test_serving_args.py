@@ -317,6 +317,16 @@ def test_window_attention_fp4_refusals(B, kw, extra, status):
     assert B.load_library().qsa_window_attention_fp4_paged(q, k, e["ks"], v, e["vs"], e["kg"], e["vg"], *rest) == status
 
 
+def test_window_attention_refuses_scales_that_leave_fp32(B):
+    """The kernel multiplies by scale log2(e), for a 4-bit cache by k_global too."""
+    lib = B.load_library()
+    assert lib.qsa_window_attention_paged(*window_args(scale=2.3e38)) == OK
+    assert lib.qsa_window_attention_paged(*window_args(scale=2.4e38)) == INVALID
+    for scale, kg, status in ((0.1, 1.0, OK), (1e30, 1e30, INVALID), (1e-30, 1e-30, INVALID), (1e30, 1e-30, OK)):
+        q, k, v, *rest = window_args(scale=scale)
+        assert lib.qsa_window_attention_fp4_paged(q, k, FAKE, v, FAKE, kg, 1.0, *rest) == status
+
+
 def test_window_workspace_bytes(B):
     """Equal shares where there are few query tiles, whole units where there are many."""
     f = lambda rows, n, ppr, **kw: B.window_workspace_bytes(rows, n, ppr, 64, 24, 2, 256, 0, 0, num_sms=152, **kw)  # noqa: E731

@@ -169,7 +169,9 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
       !aligned_to(cu_seqlens_q, 4) || !aligned_to(kv_lens, 4) || !aligned_to(page_table, 4) ||
       !aligned_to(lse, 4))
     return QSA_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !(scale > 0.0f) || (dtype != QSA_BF16 && dtype != QSA_FP16))
+  // (scale log2(e), with a 4-bit cache's scale, is what the kernel multiplies by)
+  const float scale_log2 = scale * 1.4426950408889634f * (fp4 ? fp4->k_global : 1.0f);
+  if (!(scale > 0.0f) || !(scale_log2 > 0.0f) || !std::isfinite(scale_log2) || (dtype != QSA_BF16 && dtype != QSA_FP16))
     return QSA_ERR_INVALID_ARG;
   qsa_status st = check_window(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads,
                                head_dim, window, n_sink, fp4 != nullptr);
@@ -212,16 +214,14 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   while (box < 64 && page_size % (2 * box) == 0) box *= 2;
   p.box = box >= 8 ? box : 0;
   p.n_slots = static_cast<int32_t>(n_pages * page_size);
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.v_mult = 1.0f;
   if (fp4) {
     p.k_codes = static_cast<const uint8_t*>(k_cache);
     p.v_codes = static_cast<const uint8_t*>(v_cache);
     p.k_scale = fp4->k_scale;
     p.v_scale = fp4->v_scale;
-    p.scale_log2 *= fp4->k_global;
     p.v_mult = fp4->v_global;
-    if (!(p.scale_log2 > 0.0f) || !std::isfinite(p.scale_log2)) return QSA_ERR_INVALID_ARG;
   }
   if (qsa::log_geometry())
     std::fprintf(stderr,
