@@ -759,3 +759,26 @@ def test_stalled_call_times_out_and_the_context_recovers(B):
         assert B.device_status() == 0x142                    # the wait for a unit's record
         assert 1.0 < time.time() - t0 < 20.0
         b.check(B, 0, 0, rows=range(0, b.R, 97))
+
+
+def test_a_unit_that_takes_longer_than_the_least_limit_of_waits(B):
+    """600 million positions, all on one page, dealt out whole beside 1100 short requests: some waits last as long as that
+    unit, some seconds, and none of them may be taken for a stall.  (Its own sums are beyond what fp32 can
+    add up one by one and are not looked at.)"""
+    import torch
+    rng = np.random.default_rng(2)
+    n, ps, D = 1100, 1 << 16, 64
+    kv = rng.integers(1, 200, n)
+    kv[0] = 600_000_000
+    table = np.zeros((n, -(-int(kv[0]) // ps)), np.int64)
+    q = torch.randn((n, 1, D), device="cuda").bfloat16()
+    k, v = (torch.randn((ps, 1, D), device="cuda").bfloat16() for _ in range(2))
+    assert B.window_workspace_bytes(n, n, table.shape[1], ps, 1, 1, D, 0, 0, num_sms=152) == 0      # whole units
+    out, lse = B.window_attention_paged(q, k, v, i32(np.arange(n + 1)), i32(kv), i32(table), ps, D ** -0.5)
+    torch.cuda.synchronize()
+    assert B.device_status() == 0 and bool(out.isfinite().all()) and bool(lse.isfinite().all())
+    b = Batch.__new__(Batch)
+    b.dt, b.dim, b.ps, b.fp4, b.scale = torch.bfloat16, D, ps, False, D ** -0.5
+    b.cu, b.kv, b.table = np.arange(n + 1), kv, table
+    b.q64, b.k64, b.v64 = (x.double().cpu().numpy() for x in (q, k, v))
+    b.compare(out, lse, 0, 0, rows=range(1, n, 31))

@@ -349,6 +349,7 @@ struct WindowParams {
   int32_t n_tiles;              // upper bound: n_rows / tile_tokens + n_requests
   int32_t shares;               // equal shares: blocks of the grid; 0 = whole units
   int32_t unit_cost;            // what a unit counts in a share beside its tiles
+  int32_t key_tiles;            // upper bound of a unit's key tiles
   int32_t window;               // 0 = none
   int32_t n_sink;
   int32_t out_32;               // out is 32-byte aligned

@@ -94,6 +94,7 @@ qsa_status run_rope(qsa::RopeParams& p, const qsa_rope_spec* rope, int32_t dtype
 // 150 / 153; 256 decode rows of 1k to 4k, 128 dims: 338 / 356; a prompt of 2048 rows: 44 / 60.
 struct WindowPlan {
   int32_t tile_tokens, n_tiles, shares, unit_cost;
+  int32_t key_tiles;             // a unit has at most as many
   int64_t n_units;
 };
 constexpr int32_t kMaxShareTiles = 1 << 14;    // every block sums all units' tiles
@@ -113,6 +114,7 @@ WindowPlan plan_window(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, in
   }
   const int64_t kt = (keys + qsa::kWinTile - 1) / qsa::kWinTile;
   const int64_t items = tiles * n_kvheads;
+  w.key_tiles = static_cast<int32_t>(kt);
   if (kt <= 1 || w.n_tiles > kMaxShareTiles) return w;
   const int64_t rows_per = n_rows < tiles * w.tile_tokens ? (n_rows + tiles - 1) / tiles : w.tile_tokens;
   const double partial = static_cast<double>(rows_per * group) / qsa::kWinTile;
@@ -207,6 +209,7 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   p.n_tiles = w.n_tiles;
   p.shares = w.shares;
   p.unit_cost = w.unit_cost;
+  p.key_tiles = w.key_tiles;
   p.out_32 = aligned_to(out, 32);
   p.window = window;
   p.n_sink = n_sink;

@@ -42,7 +42,7 @@
 //    exponentials take 660, and ~6100 a unit (4096 causal rows, 32 heads of 128 dims: 127 us, 1.08 PFLOP/s).
 //    4-bit caches: shared memory again, fp16 tiles written and read (48 rows over 16k to 32k keys of 256 dims:
 //    225 us, 2.9 TB/s).
-//  * Every mbarrier wait is bounded (2 s); a timeout records a code in the device status word, all roles
+//  * Every mbarrier wait is bounded (2 s, and more for very long units); a timeout records a code in the device status word, all roles
 //    leave their loops, copies and MMAs in flight are drained, tensor memory is freed.
 #pragma once
 
@@ -106,7 +106,7 @@ struct WinCfg {
   static constexpr int kNextAt = (kBarAt + 8 * kBars + 15) / 16 * 16;   // answer of the launch control
   static constexpr int kShareAt = kNextAt + 16;            // Share
   static constexpr int kTagAt = kShareAt + 32;             // [kDepth] uint32 (4-bit caches)
-  static constexpr int kTmemSlot = kTagAt + (FP4 ? 32 : 0);
+  static constexpr int kTmemSlot = (kTagAt + (FP4 ? 32 : 0) + 15) / 16 * 16;   // address, abort flag, limit of waits
   static constexpr int kSmem = kTmemSlot + 16;
   static_assert(kSmem <= kSmemLimit, "shared memory");
   static_assert(kStages / kSPT + 2 < kEntryBars, "entry barriers");
@@ -116,7 +116,9 @@ struct WinCfg {
 
 namespace window_detail {
 
-constexpr unsigned long long kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
+// A wait's limit: 2 s, and 20 us for every key tile that a unit of the call may have, since some waits last as long as
+// a unit (a tile takes 1 to 3 us).
+constexpr unsigned long long kWaitNs = 2000000000ull, kWaitNsPerTile = 20000ull, kDrainNs = 200000000ull;
 constexpr float kRaise = 8.0f;          // log2 units by which a tile may exceed the running maximum
 // Weights in fp16 are multiplied by 2^7 (l too, which lse undoes): at most 2^15 with kRaise, so that those far
 // below the maximum do not fall out of fp16's range.  Below 2^-21 of the maximum they are rounded to whole 2^-31,
@@ -134,7 +136,7 @@ __device__ __forceinline__ unsigned long long now_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Bounded wait for phase `parity` of a barrier.  False on timeout or abort.
+// Bounded wait for phase `parity` of a barrier.  False on timeout or abort.  (The limit lies behind the abort flag.)
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                          int32_t* status, int32_t site) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -142,7 +144,7 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
-    if (now_ns() - t0 > kWaitNs) {
+    if (now_ns() - t0 > *reinterpret_cast<volatile unsigned long long*>(abort_flag + 1)) {
       *abort_flag = 1;
       atomicCAS(status, 0, 0x100 | site);
       return false;
@@ -503,6 +505,8 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       }
     }
     *abort_flag = 0;
+    *reinterpret_cast<volatile unsigned long long*>(abort_flag + 1) =
+        kWaitNs + kWaitNsPerTile * static_cast<unsigned long long>(p.key_tiles);
     fence_mbar_init();
   }
   if (warp == 8) {
