@@ -163,6 +163,11 @@ __device__ __forceinline__ float2 split_pair(uint64_t v) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
   return r;
 }
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -174,17 +179,16 @@ __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
 // rounding.  That decides as the exact quotient does, ties included: a border between two codes or scales has at
 // most 5 bits, so border times d is a float, another float f is at least 2^-24 of it away, and the quotient's
 // neighbourhood that rounds to the border is narrower (half a step, by more than 2^-28 of the border).
-// p is kept within +-8, past the largest code, so that infinities and overflowing products keep their sign.
+// (Infinities and products that overflow must not come here.)
 
 // Eight dims of a block whose scales are d: code words.  (NaN is converted to 6.)
 __device__ __forceinline__ uint32_t quantise8(const float* f, float d, float r) {
   float v[8];
-  const uint64_t d2 = pair_of(d, d), r2 = pair_of(r, r);
+  const uint64_t d2 = pair_of(-d, -d), r2 = pair_of(r, r);
 #pragma unroll
   for (int k = 0; k < 8; k += 2) {
-    const float p0 = fminf(fmaxf(f[k] * r, -8.0f), 8.0f), p1 = fminf(fmaxf(f[k + 1] * r, -8.0f), 8.0f);
-    const uint64_t left = fma_pair(pair_of(-p0, -p1), d2, pair_of(f[k], f[k + 1]));
-    const float2 q = split_pair(fma_pair(left, r2, pair_of(p0, p1)));
+    const uint64_t x = pair_of(f[k], f[k + 1]), p = mul_pair(x, r2);
+    const float2 q = split_pair(fma_pair(fma_pair(p, d2, x), r2, p));
     v[k] = copysignf(q.x, f[k]);             // (-0 has come out as 0)
     v[k + 1] = copysignf(q.y, f[k + 1]);
   }
@@ -213,6 +217,15 @@ __device__ __forceinline__ void write_fp4(const RopeParams& p, bool is_v, int64_
   const uint8_t ca = scale_code(ma * inv), cb = ONE ? ca : scale_code(mb * inv);
   const float sa = e4m3_value(ca), sb = ONE ? sa : e4m3_value(cb);
   const float ra = reciprocal(sa), rb = ONE ? ra : reciprocal(sb);
+  // beside the largest scale stand infinities and values far past the largest code: kept at 8 times the scale
+  auto limit = [&](float* x, uint8_t code) {
+    if (code != 0x7E) return;
+    const float most = 8.0f * 448.0f * unit;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = fminf(fmaxf(x[k], -most), most);      // (NaN becomes -most)
+  };
+  limit(f, ca);
+  limit(f + 8, cb);
   const uint32_t wa = quantise8(f, sa * unit, ra), wb = quantise8(f + 8, sb * unit, rb);
   uint8_t* const codes = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + cell * (p.head_dim / 2);
   uint8_t* const scales = (is_v ? p.v_scale : p.k_scale) + cell * (p.head_dim / 16);
