@@ -329,6 +329,9 @@ struct JoinRecord {
   int32_t first, more, row0, tokens, kvh, pad0, pad1, pad2;
 };
 constexpr int kWinTile = 128;                // keys per MMA tile, and rows of the query tile
+// A wait's limit inside the kernel, and what is added to it for every key tile that a unit of the call may have: some
+// waits last as long as a unit (a tile takes 1 to 3 us).
+constexpr unsigned long long kWinWaitNs = 2000000000ull, kWinWaitNsPerTile = 20000ull;
 struct WindowParams {
   const void* q;                // [n_rows, n_qheads, D] bf16 or fp16
   void* out;
@@ -349,13 +352,13 @@ struct WindowParams {
   int32_t n_tiles;              // upper bound: n_rows / tile_tokens + n_requests
   int32_t shares;               // equal shares: blocks of the grid; 0 = whole units
   int32_t unit_cost;            // what a unit counts in a share beside its tiles
-  int32_t key_tiles;            // upper bound of a unit's key tiles
   int32_t window;               // 0 = none
   int32_t n_sink;
   int32_t out_32;               // out is 32-byte aligned
   int32_t box;                  // keys per TMA box (8 .. 64), or 0: gathers of four rows
   int32_t n_slots;              // n_pages * page_size
   int32_t stall_first_item;     // failure-detection test: the scheduler withholds its records
+  unsigned long long wait_ns;   // limit of the waits inside the kernel
   float scale_log2;             // scale * log2(e) (times the K cache's scale)
   float v_mult;                 // V cache's scale
 };

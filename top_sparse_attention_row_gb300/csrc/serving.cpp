@@ -209,7 +209,7 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   p.n_tiles = w.n_tiles;
   p.shares = w.shares;
   p.unit_cost = w.unit_cost;
-  p.key_tiles = w.key_tiles;
+  p.wait_ns = qsa::kWinWaitNs + qsa::kWinWaitNsPerTile * static_cast<unsigned long long>(w.key_tiles);
   p.out_32 = aligned_to(out, 32);
   p.window = window;
   p.n_sink = n_sink;

@@ -42,8 +42,8 @@
 //    exponentials take 660, and ~6100 a unit (4096 causal rows, 32 heads of 128 dims: 127 us, 1.08 PFLOP/s).
 //    4-bit caches: shared memory again, fp16 tiles written and read (48 rows over 16k to 32k keys of 256 dims:
 //    225 us, 2.9 TB/s).
-//  * Every mbarrier wait is bounded (2 s, and more for very long units); a timeout records a code in the device status word, all roles
-//    leave their loops, copies and MMAs in flight are drained, tensor memory is freed.
+//  * Every mbarrier wait is bounded (2 s, and more for very long units); a timeout records a code in the device status
+//    word, all roles leave their loops, copies and MMAs in flight are drained, tensor memory is freed.
 #pragma once
 
 #include <cuda.h>
@@ -106,7 +106,7 @@ struct WinCfg {
   static constexpr int kNextAt = (kBarAt + 8 * kBars + 15) / 16 * 16;   // answer of the launch control
   static constexpr int kShareAt = kNextAt + 16;            // Share
   static constexpr int kTagAt = kShareAt + 32;             // [kDepth] uint32 (4-bit caches)
-  static constexpr int kTmemSlot = (kTagAt + (FP4 ? 32 : 0) + 15) / 16 * 16;   // address, abort flag, limit of waits
+  static constexpr int kTmemSlot = kTagAt + (FP4 ? 32 : 0);
   static constexpr int kSmem = kTmemSlot + 16;
   static_assert(kSmem <= kSmemLimit, "shared memory");
   static_assert(kStages / kSPT + 2 < kEntryBars, "entry barriers");
@@ -116,9 +116,7 @@ struct WinCfg {
 
 namespace window_detail {
 
-// A wait's limit: 2 s, and 20 us for every key tile that a unit of the call may have, since some waits last as long as
-// a unit (a tile takes 1 to 3 us).
-constexpr unsigned long long kWaitNs = 2000000000ull, kWaitNsPerTile = 20000ull, kDrainNs = 200000000ull;
+constexpr unsigned long long kDrainNs = 200000000ull;
 constexpr float kRaise = 8.0f;          // log2 units by which a tile may exceed the running maximum
 // Weights in fp16 are multiplied by 2^7 (l too, which lse undoes): at most 2^15 with kRaise, so that those far
 // below the maximum do not fall out of fp16's range.  Below 2^-21 of the maximum they are rounded to whole 2^-31,
@@ -136,17 +134,17 @@ __device__ __forceinline__ unsigned long long now_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Bounded wait for phase `parity` of a barrier.  False on timeout or abort.  (The limit lies behind the abort flag.)
+// Bounded wait for phase `parity` of a barrier.  False on timeout or abort.
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                         int32_t* status, int32_t site) {
+                                         const WindowParams& p, int32_t site) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = now_ns();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
-    if (now_ns() - t0 > *reinterpret_cast<volatile unsigned long long*>(abort_flag + 1)) {
+    if (now_ns() - t0 > p.wait_ns) {
       *abort_flag = 1;
-      atomicCAS(status, 0, 0x100 | site);
+      atomicCAS(p.status, 0, 0x100 | site);
       return false;
     }
   }
@@ -505,8 +503,6 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       }
     }
     *abort_flag = 0;
-    *reinterpret_cast<volatile unsigned long long*>(abort_flag + 1) =
-        kWaitNs + kWaitNsPerTile * static_cast<unsigned long long>(p.key_tiles);
     fence_mbar_init();
   }
   if (warp == 8) {
@@ -529,10 +525,10 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
   const uint32_t tm_o = tmem + 256;           // S buffers: columns 0-127 and 128-255; O: from 256
 
   auto wait_done = [&](uint32_t e, int32_t site) -> bool {
-    return wait_for(b_done + 8 * (e % C::kEntryBars), (e / C::kEntryBars) & 1, abort_flag, status, site);
+    return wait_for(b_done + 8 * (e % C::kEntryBars), (e / C::kEntryBars) & 1, abort_flag, p, site);
   };
   auto wait_tile = [&](uint32_t bars, uint32_t t, int32_t site) -> bool {
-    return wait_for(bars + 8 * (t % C::kTileBars), (t / C::kTileBars) & 1, abort_flag, status, site);
+    return wait_for(bars + 8 * (t % C::kTileBars), (t / C::kTileBars) & 1, abort_flag, p, site);
   };
   auto finish_role = [&]() {
     tc_fence_before();
@@ -553,7 +549,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     bool bad = false;
     for (;; ++it) {
       const uint32_t rb = it % C::kRecords;
-      bad |= !wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, status, kWRecFull);
+      bad |= !wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, p, kWRecFull);
       // the two warps that share 32 rows leave together or not at all
       if (named_bar_any(1 + w, 64, bad || *abort_flag)) break;
       const Unit u = load_unit(recs + rb);
@@ -813,7 +809,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     };
     for (uint32_t it = 0;; ++it) {
       const uint32_t rb = it % C::kRecords;
-      if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, status,
+      if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, p,
                                             kWRecFull))) {
         stop = true;
         break;
@@ -823,7 +819,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       if (lane == 0) mbar_arrive(b_recempty + 8 * rb);
       if (nt < 0) break;
       if (nt == 0) continue;
-      if (!__all_sync(0xffffffffu, wait_for(b_qfull, qit & 1, abort_flag, status, kWQFull))) {
+      if (!__all_sync(0xffffffffu, wait_for(b_qfull, qit & 1, abort_flag, p, kWQFull))) {
         stop = true;
         break;
       }
@@ -840,7 +836,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         uint32_t stage[C::kSPT];
         take_stages(stage);
         bool ok = wait_tile(b_pvready, jt, kWPvReady);
-        if (j == 0) ok = ok && wait_for(b_ofree, (qit & 1) ^ 1, abort_flag, status, kWOFree);
+        if (j == 0) ok = ok && wait_for(b_ofree, (qit & 1) ^ 1, abort_flag, p, kWOFree);
         if (!__all_sync(0xffffffffu, ok)) {
           stop = true;
           break;
@@ -878,7 +874,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     }
     if (lane == 0) {
       tc_commit(b_fin);
-      drain(b_fin, 0, status, stop ? kDrainNs : kWaitNs);
+      drain(b_fin, 0, status, stop ? kDrainNs : kWinWaitNs);
     }
     __syncwarp();
     finish_role();
@@ -893,7 +889,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       uint32_t js = 0, st0 = 0;          // tiles so far, the first stage of the next entry
       for (uint32_t it = 0;; ++it) {
         const uint32_t rb = it % C::kRecords;
-        if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, status,
+        if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, p,
                                               kWRecFull)))
           break;
         const Unit u = load_unit(recs + rb);
@@ -948,7 +944,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       __syncwarp();
     };
     auto answer = [&]() -> int32_t {
-      const bool ok = mbar_try_wait(b_next, asked & 1) || wait_for(b_next, asked & 1, abort_flag, status, kWNext);
+      const bool ok = mbar_try_wait(b_next, asked & 1) || wait_for(b_next, asked & 1, abort_flag, p, kWNext);
       ++asked;
       if (!__all_sync(0xffffffffu, ok)) {
         more = false;
@@ -1032,7 +1028,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
             const uint32_t before = it - 1;
             if (last_tiles > kShortUnit &&
                 !__all_sync(0xffffffffu, wait_for(b_recempty + 8 * (before % C::kRecords), (before / C::kRecords) & 1,
-                                                  abort_flag, status, kWRecEmpty)))
+                                                  abort_flag, p, kWRecEmpty)))
               break;
             ask();
             n = answer();
@@ -1046,21 +1042,21 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           }
           last_tiles = u.tiles;
         }
-        if (!__all_sync(0xffffffffu, wait_for(b_recempty + 8 * rb, ph ^ 1, abort_flag, status, kWRecEmpty))) break;
+        if (!__all_sync(0xffffffffu, wait_for(b_recempty + 8 * rb, ph ^ 1, abort_flag, p, kWRecEmpty))) break;
         if (lane == 0) {
           recs[rb] = u;
           mbar_arrive(b_recfull + 8 * rb);
         }
         __syncwarp();
       } else {
-        if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, ph, abort_flag, status, kWRecFull))) break;
+        if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, ph, abort_flag, p, kWRecFull))) break;
         u = load_unit(recs + rb);
         __syncwarp();
         if (lane == 0) mbar_arrive(b_recempty + 8 * rb);
       }
       if (u.tiles < 0) break;
       if (u.tiles == 0) continue;
-      if (!__all_sync(0xffffffffu, wait_for(b_qempty, (qit & 1) ^ 1, abort_flag, status, kWQEmpty))) break;
+      if (!__all_sync(0xffffffffu, wait_for(b_qempty, (qit & 1) ^ 1, abort_flag, p, kWQEmpty))) break;
       if constexpr (!FP4) {
         // a whole tile in one box per 64-dim block, a partial one token by token
         const bool full = u.tokens == p.tile_tokens;
@@ -1126,7 +1122,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     };
     for (uint32_t it = 0; !stop; ++it) {
       const uint32_t rb = it % C::kRecords;
-      if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, status,
+      if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, p,
                                             kWRecFull))) {
         stop = true;
         break;
@@ -1254,7 +1250,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       const uint32_t row_scales = static_cast<uint32_t>(p.n_kvheads) * (D / 16);
       for (uint32_t it = 0; !stop; ++it) {
         const uint32_t rb = it % C::kRecords;
-        if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, status,
+        if (!__all_sync(0xffffffffu, wait_for(b_recfull + 8 * rb, (it / C::kRecords) & 1, abort_flag, p,
                                               kWRecFull))) {
           stop = true;
           break;
@@ -1284,7 +1280,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         };
         auto copy = [&](int32_t slot, const uint8_t* codes, const uint8_t* scales, uint32_t tag) -> bool {
           if (n >= C::kDepth &&
-              !__all_sync(0xffffffffu, wait_for(b_unstaged + 8 * slot_at, (turn & 1) ^ 1, abort_flag, status, kWUnstaged)))
+              !__all_sync(0xffffffffu, wait_for(b_unstaged + 8 * slot_at, (turn & 1) ^ 1, abort_flag, p, kWUnstaged)))
             return false;
           const uint32_t to = base + C::kStagingAt + slot_at * C::kStaging;
 #pragma unroll
@@ -1332,7 +1328,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (!stop && n >= C::kDepth) {                        // (the tag's slot has been read)
-        stop = !__all_sync(0xffffffffu, wait_for(b_unstaged + 8 * slot_at, (turn & 1) ^ 1, abort_flag, status, kWUnstaged));
+        stop = !__all_sync(0xffffffffu, wait_for(b_unstaged + 8 * slot_at, (turn & 1) ^ 1, abort_flag, p, kWUnstaged));
       }
       if (!stop) {
         if (pw == 0 && lane == 0) {
@@ -1350,7 +1346,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     const int wi = warp - 16;                               // keys 16 wi .. 16 wi + 15 of every tile
     uint32_t slot_at = 0, turn = 0;
     for (uint32_t n = 0;; ++n) {
-      if (!__all_sync(0xffffffffu, wait_for(b_staged + 8 * slot_at, turn & 1, abort_flag, status, kWStaged))) break;
+      if (!__all_sync(0xffffffffu, wait_for(b_staged + 8 * slot_at, turn & 1, abort_flag, p, kWStaged))) break;
       const uint32_t tag = tags[slot_at];                   // 2 tile + 1 for V, of the call's tiles
       if (tag == kLastTag) break;
       const uint32_t half0 = n * C::kSPT;
