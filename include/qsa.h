@@ -425,7 +425,7 @@ qsa_status qsa_rope_append_fp4(const void* q, void* q_out, const void* k, const 
  *   workspace: calls with few query tiles for the SMs cut the keys into equal shares and join the parts; they
  *       need qsa_window_workspace_bytes (for the device's SM count; 0 = none), 256-byte aligned.  NULL: taken from
  *       the library's pool on `stream`.  Calls that overlap need a workspace each.
- * Sums, maxima and outputs are held in fp32 (sums are added tile by tile, 128 keys each: an error of up to 2^-25 of
+ * Sums, maxima and outputs are held in fp32 (sums are added tile by tile, 128 keys each: an error of up to 2^-24 of
  * the sum with every tile), the weights of the P.V product are rounded to 16 bits (in fp16, to no less
  * than 2^-32 of the row's largest weight so far).
  * Results do not depend on timing, but a row's sums depend on where the shares are cut, and so on its batch.

@@ -8,9 +8,10 @@
 //
 // The work is two prefix sums over the requests and two searches through them (one per fresh page,
 // one per row); the data is a few bytes per request, page and row, so the call is bound by launch
-// and memory latency (64 decode requests 5.5 us, 256 prompt chunks of up to 2048 rows 12.6 us).  One kernel does all of it: a single cluster of up to 8 CTAs, each of which
-// repeats the prefix sums over all requests in its own shared memory (two loads per request) and
-// then takes its share of the fresh pages and of the rows.  The cluster barrier orders every read of
+// and memory latency (64 decode requests 5.6 us).  One kernel does all of it: a single cluster of up to 8 CTAs,
+// each of which repeats the prefix sums over all requests in its own shared memory (two loads per request) and
+// then takes its share of the fresh pages and of the rows; with many rows those 8 SMs' searches are what takes the time
+// (256 prompt chunks of up to 2048 rows 12.7 us).  The cluster barrier orders every read of
 // the free-list head before its one write, and of the lengths before kv_lens, so head and lengths may be
 // updated in place and a captured step replays.
 #include <cstdint>

@@ -9,14 +9,16 @@
 // number of half turns, is rounded to fp32 (2^-25 half turns) and goes to sincospi.
 //
 // The operator reads and writes every element once and does a handful of operations on each, so it is
-// bound by memory (8192 rows of 26 heads of 256 dims 42.6 us, 5.5 TB/s: 81 % of the measured copy rate).  A thread owns one 16-dim unit (8 pairs) of a row: it computes its 8 sines and
-// cosines once and applies them to that unit of every head of its share, with 16-byte loads and
-// stores.  Calls with few rows give each thread fewer heads, so that enough threads run.
+// bound by memory (8192 rows of 24 q, 2 k and 2 v heads of 256 dims 42.6 us, 5.5 TB/s: 81 % of the measured copy
+// rate).  A thread owns one 16-dim unit (8 pairs) of a row: it computes its 8 sines and cosines once and applies them
+// to that unit of every head of its share, with 16-byte loads and stores.  Calls with few rows give each thread
+// fewer heads, so that enough threads run.
 //
 // 4-bit rows: a block of 16 dims is stored as 16 e2m1 codes (two in a byte, the even dim in the low
 // half) and one e4m3 scale s = e4m3(max|x| / (6 g)), g being the cache's fp32 scale; a code is
 // e2m1((x / g) / s), both rounded to nearest, ties to even.  The rotated values are quantised from fp32.
-// 8192 rows of 2 + 2 heads of 256 dims take 11.9 us, bound by the conversions and their latency (38 MB).
+// 8192 rows of 2 + 2 heads of 256 dims take 11.5 us, where their 38 MB need 5.6: a thread's loads, maximum, scale and
+// codes follow one another, two heads deep.
 // Codes and scales fall as the formula says, ties (x = border times scales: common, since all have few bits)
 // and values next to them included: see quantise8.
 #include <cuda_bf16.h>
@@ -385,7 +387,9 @@ __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ void from_float(float f, __nv_bfloat16& v) { v = __float2bfloat16_rn(f); }
 __device__ __forceinline__ void from_float(float f, __half& v) { v = __float2half_rn(f); }
 
-// Rows of any width, offset, stride and alignment: thread = (row, head, pair or passing dim).
+// Rows of any width, offset, stride and alignment: thread = (row, head, pair or passing dim), 2 bytes at a time, the
+// angles anew for every head.  Far from memory's rate: 8192 rows of 28 heads of 96 dims, 24 of them turned, take 105 us
+// (88 MB); with 32 at an offset of 16 the kernel above takes 20.
 template <typename T>
 __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const __grid_constant__ RopeParams p) {
   const int pairs = p.rot_dim >> 1, per_head = p.head_dim - pairs;

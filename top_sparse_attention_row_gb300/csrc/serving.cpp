@@ -87,8 +87,11 @@ qsa_status run_rope(qsa::RopeParams& p, const qsa_rope_spec* rope, int32_t dtype
 // next one, and about half a unit's time passes while the last ones finish.  Equal shares divide that time evenly,
 // but a block then has one more unit begun or ended, writes up to two partial ones in fp32 (a tile's worth of bytes
 // each when all 128 rows are in use) that the join reads again, and the join is one more launch, about three tiles
-// long.  The lengths behind the page table are not known here, and where they are shorter, shares have less to gain:
-// they are taken where the model gives them 7 %.  Measured (us, whole / shares): 128 decode rows with contexts of 1k
+// long.  Shares are taken where the model gives them 7 %.  The lengths behind the page table are not known here: every
+// unit is taken to see as many keys as the table has room for (or the window).  Where that is far from the lengths, the
+// choice can fall on the slower way: prompts of 1024 and 2048 rows, 32/8 heads of 128 dims, take 21 and 43 us in a table
+// of just their length (whole units), 33 and 64 in one four times as wide or more (shares); 24/2 heads of 256 dims 25
+// and 50, and 39 and 68.  Measured (us, whole / shares): 128 decode rows with contexts of 1k
 // to 8k, 24/2 heads of 256 dims, window 4096: 146 / 127; 48 decode rows over 16k to 32k keys in 4 bits: 449 / 224; a
 // chunk of 512 rows at 8000, 256 dims: 103 / 89, 128 dims, 32/8 heads: 67 / 74; the last 8192 rows of a 32k prompt:
 // 150 / 153; 256 decode rows of 1k to 4k, 128 dims: 338 / 356; a prompt of 2048 rows: 44 / 60.

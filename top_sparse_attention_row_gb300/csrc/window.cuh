@@ -10,8 +10,7 @@
 //  * Units are dealt out in one of two ways.  Whole units: the grid has a block per unit, and the block on an
 //    SM takes over the units of blocks that have not started (cluster launch control), so that the SMs stay
 //    busy with units of unequal length and no counter in memory is needed.  A block holds one unit in advance,
-//    and the longest of all heads go first (with four in advance the SMs were busy 77 % of the time: causal
-//    prompt of 4096 rows 160 us, now 128).  Equal shares: with few units for the SMs, the key tiles of all units
+//    and the longest of all heads go first, so that the last units go to the blocks that are free.  Equal shares: with few units for the SMs, the key tiles of all units
 //    are laid end to end (each block sums the units' tiles when it starts) and cut into one equal run per block;
 //    a block's first and last unit may be parts, whose normalised fp32 rows and log-sum-exps go to a workspace
 //    and are joined by a second kernel.
@@ -36,12 +35,12 @@
 //    The MMAs run fp16 there (q is rounded to fp16, as for FP8 caches).
 //  * Keys that no row of the unit sees (the rest of a page, positions that left the window, missing
 //    pages) get weight 0 and V rows of zeros, so that whatever the cache holds there stays out.
-//  * What bounds it.  Decode: HBM (512 rows over 4000 keys of 256 dims 0.61 ms, 6.9 TB/s).  Prompts of 256 dims:
-//    shared memory, 320 KB a tile = 2560 of ~2700 cycles, where the tensor pipe needs 2048 (8192 rows at 24k,
-//    window 4096: 150 us, 1.37 PFLOP/s).  64 and 128 dims: the softmax, ~2030 cycles a tile, of which the
-//    exponentials take 660, and ~6100 a unit (4096 causal rows, 32 heads of 128 dims: 127 us, 1.08 PFLOP/s).
-//    4-bit caches: shared memory again, fp16 tiles written and read (48 rows over 16k to 32k keys of 256 dims:
-//    225 us, 2.9 TB/s).
+//  * What bounds it.  Decode: HBM (128 rows over 1k to 8k keys, 24/2 heads of 256 dims, window 4096: 130 us, 5.7 TB/s;
+//    the larger the batch the nearer).  Prompts of 256 dims: shared memory, 320 KB a tile = 2560 of ~2700 cycles,
+//    where the tensor pipe needs 2048 (8192 rows at 24k, window 4096: 151 us, 1.37 PFLOP/s).  64 and 128 dims: the
+//    softmax, ~2030 cycles a tile, of which the exponentials take 660, and ~6100 a unit (six requests of 1 to 2047
+//    rows, 32/8 heads of 128 dims, window 1024: 57 us, 0.70 PFLOP/s).  4-bit caches: shared memory again, fp16 tiles
+//    written and read (48 rows over 16k to 32k keys of 256 dims: 224 us, 2.9 TB/s of codes and scales).
 //  * Every mbarrier wait is bounded (2 s, and more for very long units); a timeout records a code in the device status
 //    word, all roles leave their loops, copies and MMAs in flight are drained, tensor memory is freed.
 #pragma once
@@ -544,7 +543,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     const float raise = kRaise / sc;
     constexpr float kLift = FP4 || std::is_same<T, __half>::value ? kLiftFp16 : 0.0f;
     // (loops that run once a unit, or seldom, are not unrolled: their instructions would have to be fetched anew each
-    // time; unrolled: decode batch 129.1 -> 126.6 us, causal prompts of 128 dims 215 -> 205 us rolled)
+    // time)
     uint32_t it = 0, js = 0, eb = 0;          // records, tiles and ring entries so far
     bool bad = false;
     for (;; ++it) {
