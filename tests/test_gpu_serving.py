@@ -113,6 +113,23 @@ def test_page_plan_updates_lengths_in_place(B, n, new_max, which):
         assert np.array_equal(lens[other].cpu().numpy(), dict(past=past, new=new)[other])
 
 
+def test_page_plan_into_a_callers_unaligned_arrays(B):
+    """positions and slots that start 4 bytes past a 16-byte boundary, one row more and less than fours."""
+    import torch
+    rng = np.random.default_rng(3)
+    past, new, table, free, n_pages = plan_case(rng, 40, 30, 100, 8)
+    for extra in (0, 1, 2, 3):
+        rows = int(new.sum()) + extra
+        pos, slots = (torch.full((rows + 6,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+        B.page_plan(i32(past), i32(new), i32(table), i32(free), i32([0]), 8, rows, n_pages=n_pages,
+                    positions=pos[1:1 + rows], slots=slots[3:3 + rows])
+        torch.cuda.synchronize()
+        want = S.page_plan(past, new, table, free, 0, 8, rows, n_pages)
+        for got, at, w in ((pos, 1, want[3]), (slots, 3, want[4])):
+            got = got.cpu().numpy()
+            assert np.array_equal(got[at:at + rows], w) and np.all(got[:at] == -9) and np.all(got[at + rows:] == -9)
+
+
 def test_page_plan_replays_from_a_graph(B):
     """Captured once with the head in place: every replay takes the next pages."""
     import torch
@@ -300,6 +317,28 @@ def test_rope_append_latent_rows_and_unaligned_views(B):
     want[at] = S.rope(ks, pos.tolist(), w, mag, True, 512)
     sums[at] = pair_sums(ks, 64, 512, True)
     assert_rotated(kc, want, sums, torch.bfloat16, mag)
+
+
+@pytest.mark.parametrize("heads,dim,rot,offset", [(4, 128, 128, 0), (3, 96, 32, 16), (2, 40, 10, 6)])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rope_in_and_out_of_slices(B, heads, dim, rot, offset, layout):
+    """Rows inside wider rows, as input, as output and in place: the same values, and nothing beside them."""
+    import torch
+    t = B.rope_table(rot, 10000.0)
+    how = dict(layout=layout, rot_offset=offset)
+    R, width = 37, (heads + 3) * dim
+    wide = torch.randn((R, width), device="cuda").bfloat16()
+    part = lambda w: w[:, dim:dim + heads * dim].unflatten(1, (heads, dim))  # noqa: E731
+    pos = i32(np.arange(R) * 97 - 97)                             # the first row is left out
+    want = B.rope(part(wide).contiguous(), pos, t, out=part(wide).contiguous(), **how)
+    into = wide.clone()
+    B.rope(part(wide), pos, t, out=part(into), **how)
+    same = wide.clone()
+    B.rope(part(same), pos, t, out=part(same), **how)
+    torch.cuda.synchronize()
+    for got in (into, same):
+        assert torch.equal(part(got), want)
+        assert torch.equal(got[:, :dim], wide[:, :dim]) and torch.equal(got[:, dim + heads * dim:], wide[:, dim + heads * dim:])
 
 
 def test_rope_broadcast_rows_empty_calls_and_streams(B):
