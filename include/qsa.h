@@ -461,6 +461,100 @@ size_t qsa_window_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t pa
                                   int32_t head_dim, int32_t window, int32_t n_sink, int32_t fp4,
                                   int32_t num_sms);
 
+/* Bounds of the pages of a K cache, from which qsa_page_select chooses: for every page that the step's rows reach, the
+ * smallest and the largest value of each key dim over the page's filled positions.  The rows of request i are its last
+ * cu_seqlens_q[i + 1] - cu_seqlens_q[i] positions of kv_lens[i], as in qsa_window_attention_paged; the pages that hold
+ * them are read anew from the cache, so the call may be repeated, and after lengths went back the pages' next call
+ * brings their bounds in line.  Called after the step's rows have been written (qsa_rope_append), before qsa_page_select.
+ *   k_cache  [n_pages * page_size, n_kvheads, head_dim] of type dtype (qsa_dtype)
+ *   bounds   [n_pages, n_kvheads, 2, head_dim] of type dtype: the minima, then the maxima.  Other pages are left as
+ *            they were.  A NaN in a key makes both bounds of its dim NaN.
+ *   Positions past pages_per_req pages, or on a page < 0 or >= n_pages, are left out.  Two requests whose new rows lie
+ *   in one page may not be in one call.  bounds may not overlap the other arrays.
+ * Any page size; head_dim 64, 128 or 256; 16-byte aligned arrays.
+ * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED (other head dims, caches of 2^31 rows (slot x KV head) and more). */
+qsa_status qsa_page_bounds(const void* k_cache, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                           const int32_t* page_table, void* bounds, int32_t n_requests, int32_t pages_per_req,
+                           int32_t page_size, int64_t n_pages, int32_t n_kvheads, int32_t head_dim, int32_t dtype,
+                           void* stream);
+
+/* Chooses pages for every row and KV head by what they can hold for its queries.  A row at position p (as in
+ * qsa_window_attention_paged) may choose the pages 0 .. p / page_size of its request that exist (below pages_per_req,
+ * with a page id from 0 to n_pages - 1).  It takes those below n_first and above p / page_size - n_last, and of the
+ * others the ones with the highest scores,
+ *   score = max over the query heads of the KV head of  sum_d max(q_d lo_d, q_d hi_d),
+ * ties going to the lower page, up to n_select in all.  The sum is the most that q.k can be for a key of the page.
+ * What is chosen does not depend on roundings: scores are compared as their values in 64-bit arithmetic are (those that
+ * agree in all of their bits but the last count as equal).  A NaN score stands above all others.
+ *   q [n_rows, n_qheads, head_dim], bounds as qsa_page_bounds writes them, of type dtype
+ *   pages [n_rows, n_kvheads, n_select] int32: the chosen pages of the request's table (not page ids) in increasing
+ *         order, then -1.  Rows behind cu_seqlens_q[n_requests] are left as they were.
+ *   n_first >= 0, n_last >= 1 (the row's own page, which may be partly filled, is always taken where it exists),
+ *   n_first + n_last <= n_select.
+ *   workspace: qsa_page_select_workspace_bytes, 256-byte aligned; NULL: taken from the library's pool on `stream`.
+ *   Calls that overlap need a workspace each.
+ * pages_per_req <= 32768, n_qheads / n_kvheads <= 128, head_dim 64, 128 or 256; 16-byte aligned q and bounds.
+ * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED (beyond the limits above, n_rows * n_kvheads of 2^31 and more),
+ * QSA_ERR_WORKSPACE; a wait inside the kernel that runs out is reported by qsa_get_device_status. */
+qsa_status qsa_page_select(const void* q, const void* bounds, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                           const int32_t* page_table, int32_t* pages, int64_t n_rows, int32_t n_requests,
+                           int32_t pages_per_req, int32_t page_size, int64_t n_pages, int32_t n_qheads,
+                           int32_t n_kvheads, int32_t head_dim, int32_t n_select, int32_t n_first, int32_t n_last,
+                           int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Host only: bytes of workspace of a qsa_page_select call (0 = none). */
+size_t qsa_page_select_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t pages_per_req, int32_t n_qheads,
+                                       int32_t n_kvheads, int32_t head_dim);
+
+/* Attention of every row over the positions of its listed pages, as qsa_page_select lists them or any other way: the row
+ * at position p sees, with the query heads of a KV head, the positions j <= p whose page j / page_size is in its list.
+ *   pages [n_rows, n_kvheads, n_select] int32 pages of the request's table, in any order; entries < 0 or >=
+ *         pages_per_req, and pages whose id is < 0 or >= n_pages, are not seen; a page that is listed twice counts once
+ *   page_size is a multiple of 8, pages_per_req <= 32768.
+ *   workspace: qsa_selected_workspace_bytes, 256-byte aligned; NULL: taken from the library's pool on `stream`.
+ * The other arguments, rows that see nothing, rows behind the last request, non-finite values and precision are as in
+ * qsa_window_attention_paged (a non-finite value in V may also reach the rows of up to 127 neighbouring (token, head)
+ * pairs that do not list its page).  Neighbouring rows that list the same pages read them once.
+ * Errors: as qsa_window_attention_paged; QSA_ERR_UNSUPPORTED for other page sizes too. */
+qsa_status qsa_selected_attention_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* pages,
+                                        const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                                        const int32_t* page_table, void* out, float* lse, int64_t n_rows,
+                                        int32_t n_requests, int32_t pages_per_req, int32_t page_size,
+                                        int64_t n_pages, int32_t n_select, int32_t n_qheads, int32_t n_kvheads,
+                                        int32_t head_dim, float scale, int32_t dtype, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* Host only: bytes of workspace of a qsa_selected_attention_paged call (num_sms <= 0 asks the current device). */
+size_t qsa_selected_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t pages_per_req, int32_t page_size,
+                                    int32_t n_select, int32_t n_qheads, int32_t n_kvheads, int32_t head_dim,
+                                    int32_t num_sms);
+
+/* Attention of a ragged batch whose requests begin alike (one system prompt, several answers to one prompt): every row
+ * sees all positions up to its own, as in qsa_window_attention_paged without a window, but the positions that the
+ * requests of a group share are read once for all of their rows.
+ *   cu_groups [n_groups + 1] int32, non-decreasing: group g holds the requests cu_groups[g] .. cu_groups[g + 1] - 1;
+ *             requests outside every group share nothing
+ *   prefix_lens [n_groups] int32: positions below prefix_lens[g] hold the same keys and values for all requests of the
+ *             group; they are read through its first request's page table.  What a request of the group does not have
+ *             as past (positions from the smallest kv_len - rows of the group on) is not shared, whatever
+ *             prefix_lens says.
+ *   workspace: qsa_prefix_workspace_bytes, 256-byte aligned; NULL: taken from the library's pool on `stream`.
+ * The other arguments, rows that see nothing, rows behind the last request, non-finite values and precision are as in
+ * qsa_window_attention_paged (a non-finite value in V may also reach rows of other requests of the group).
+ * Errors: as qsa_window_attention_paged. */
+qsa_status qsa_prefix_attention_paged(const void* q, const void* k_cache, const void* v_cache,
+                                      const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* page_table,
+                                      const int32_t* cu_groups, const int32_t* prefix_lens, void* out, float* lse,
+                                      int64_t n_rows, int32_t n_requests, int32_t n_groups, int32_t pages_per_req,
+                                      int32_t page_size, int64_t n_pages, int32_t n_qheads, int32_t n_kvheads,
+                                      int32_t head_dim, float scale, int32_t dtype, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Host only: bytes of workspace of a qsa_prefix_attention_paged call (num_sms <= 0 asks the current device). */
+size_t qsa_prefix_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t n_groups, int32_t pages_per_req,
+                                  int32_t page_size, int32_t n_qheads, int32_t n_kvheads, int32_t head_dim,
+                                  int32_t num_sms);
+
 /* Allocation-free variant of qsa_sparse_prefill (same arguments, same results).  The pages
  * have no counterpart: it exists for callers that must not allocate device memory -- code
  * whose GPU memory is owned entirely by a framework's pool, latency-critical loops where an

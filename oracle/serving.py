@@ -158,3 +158,67 @@ def window_attention(q, k, v, cu, kv_lens, table, page_size, scale, window=0, n_
                 o[r, h] = (e / e.sum()) @ v[at, h // (Hq // Hkv)]
                 lse[r, h] = m + math.log(e.sum())
     return o, lse
+
+
+def page_bounds(k, cu, kv_lens, table, page_size, bounds):
+    """bounds [n_pages, Hkv, 2, D] with the pages that the new rows reach taken anew from k [slots, Hkv, D]."""
+    b = np.array(bounds, dtype=np.float64)
+    for i, kv in enumerate(kv_lens):
+        new = cu[i + 1] - cu[i]
+        if new <= 0 or kv <= 0:
+            continue
+        for e in range(max(kv - new, 0) // page_size, (kv - 1) // page_size + 1):
+            page = table[i, e] if e < table.shape[1] else -1
+            if 0 <= page < b.shape[0]:
+                rows = k[page * page_size:page * page_size + min(page_size, kv - e * page_size)]
+                b[page, :, 0], b[page, :, 1] = rows.min(0), rows.max(0)
+    return b
+
+
+def page_select(q, bounds, cu, kv_lens, table, page_size, n_select, n_first, n_last):
+    """Pages [R, Hkv, n_select] of every row and KV head, -1 behind the last; rows outside every request: -2."""
+    R, Hq, _ = q.shape
+    n_pages, Hkv = bounds.shape[:2]
+    out = np.full((R, Hkv, n_select), -2, dtype=np.int64)
+    for i, kv in enumerate(kv_lens):
+        for r in range(cu[i], cu[i + 1]):
+            p = kv - (cu[i + 1] - cu[i]) + (r - cu[i])
+            mine = p // page_size if p >= 0 else -1
+            for h in range(Hkv):
+                ranked = []
+                for e in range(min(mine + 1, table.shape[1])):
+                    if not 0 <= table[i, e] < n_pages:
+                        continue
+                    lo, hi = bounds[table[i, e], h]
+                    x = q[r, h * (Hq // Hkv):(h + 1) * (Hq // Hkv)]
+                    s = np.where(x > 0, x * hi, x * lo).sum(-1).max()
+                    taken = e < n_first or e > mine - n_last
+                    ranked.append((not taken, not np.isnan(s), 0.0 if np.isnan(s) else -s, e))
+                pages = sorted(e for *_, e in sorted(ranked)[:n_select])
+                out[r, h] = pages + [-1] * (n_select - len(pages))
+    return out
+
+
+def selected_attention(q, k, v, pages, cu, kv_lens, table, page_size, scale):
+    """Every row over the positions up to its own whose page is listed for its KV head; rows outside every
+    request come back as NaN."""
+    R, Hq, _ = q.shape
+    Hkv, n_pages = k.shape[1], k.shape[0] // page_size
+    o, lse = np.full((R, Hq, v.shape[2]), np.nan), np.full((R, Hq), np.nan)
+    for i, kv in enumerate(kv_lens):
+        for r in range(cu[i], cu[i + 1]):
+            p = kv - (cu[i + 1] - cu[i]) + (r - cu[i])
+            for h in range(Hq):
+                g = h // (Hq // Hkv)
+                at = [table[i, e] * page_size + j for e in sorted(set(int(x) for x in pages[r, g]))
+                      if 0 <= e < table.shape[1] and 0 <= table[i, e] < n_pages
+                      for j in range(page_size) if e * page_size + j <= p]
+                if not at:
+                    o[r, h], lse[r, h] = 0.0, -np.inf
+                    continue
+                s = k[at, g] @ q[r, h] * scale
+                m = s.max()
+                e = np.exp(s - m)
+                o[r, h] = (e / e.sum()) @ v[at, g]
+                lse[r, h] = m + math.log(e.sum())
+    return o, lse

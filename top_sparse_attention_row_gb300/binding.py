@@ -30,7 +30,10 @@ EXPORTED = ["qsa_sparse_prefill", "qsa_sparse_prefill_ex", "qsa_union_workspace_
             "qsa_sparse_prefill_fp8", "qsa_debug_stall_next_call", "qsa_sparse_mla_prefill_paged",
             "qsa_sparse_prefill_fp8_paged",
             "qsa_page_plan", "qsa_rope_steps", "qsa_rope", "qsa_rope_append", "qsa_rope_append_fp4",
-            "qsa_window_attention_paged", "qsa_window_attention_fp4_paged", "qsa_window_workspace_bytes"]
+            "qsa_window_attention_paged", "qsa_window_attention_fp4_paged", "qsa_window_workspace_bytes",
+            "qsa_page_bounds", "qsa_page_select", "qsa_page_select_workspace_bytes",
+            "qsa_selected_attention_paged", "qsa_selected_workspace_bytes",
+            "qsa_prefix_attention_paged", "qsa_prefix_workspace_bytes"]
 
 # Size of the library-owned scratch array used by qsa_sparse_prefill_noalloc (include/qsa.h).
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -138,6 +141,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qsa_window_attention_fp4_paged.restype = ctypes.c_int
     lib.qsa_window_workspace_bytes.argtypes = [i64] + [i32] * 10
     lib.qsa_window_workspace_bytes.restype = sz
+    lib.qsa_page_bounds.argtypes = [vp] * 5 + [i32, i32, i32, i64, i32, i32, i32, vp]
+    lib.qsa_page_bounds.restype = ctypes.c_int
+    lib.qsa_page_select.argtypes = [vp] * 6 + [i64, i32, i32, i32, i64] + [i32] * 7 + [vp, sz, vp]
+    lib.qsa_page_select.restype = ctypes.c_int
+    lib.qsa_page_select_workspace_bytes.argtypes = [i64] + [i32] * 5
+    lib.qsa_page_select_workspace_bytes.restype = sz
+    lib.qsa_selected_attention_paged.argtypes = [vp] * 9 + [i64, i32, i32, i32, i64] + [i32] * 4 + [f32, i32, vp, sz, vp]
+    lib.qsa_selected_attention_paged.restype = ctypes.c_int
+    lib.qsa_selected_workspace_bytes.argtypes = [i64] + [i32] * 8
+    lib.qsa_selected_workspace_bytes.restype = sz
+    lib.qsa_prefix_attention_paged.argtypes = [vp] * 10 + [i64, i32, i32, i32, i32, i64, i32, i32, i32, f32, i32, vp, sz, vp]
+    lib.qsa_prefix_attention_paged.restype = ctypes.c_int
+    lib.qsa_prefix_workspace_bytes.argtypes = [i64] + [i32] * 8
+    lib.qsa_prefix_workspace_bytes.restype = sz
     for name in ("qsa_union_workspace_bytes", "qsa_workspace_bytes"):
         getattr(lib, name).argtypes = [i64, i32, i32]
         getattr(lib, name).restype = sz
@@ -591,10 +608,12 @@ def version() -> str:
 # A decode step makes these calls with kernels of a few microseconds, so their argument checks, output
 # tensors and streams are handled in C++ (csrc/torch_serving.cpp, built into the module _serving): same
 # checks and errors as above.  They are attributes of this module, loaded with the library on first use:
-#   page_plan, rope, rope_append, rope_append_fp4, window_attention_paged, window_attention_fp4_paged
+#   page_plan, rope, rope_append, rope_append_fp4, window_attention_paged, window_attention_fp4_paged,
+#   page_bounds, page_select, selected_attention_paged, prefix_attention_paged
 
 SERVING = ("page_plan", "rope", "rope_append", "rope_append_fp4", "window_attention_paged",
-           "window_attention_fp4_paged")
+           "window_attention_fp4_paged", "page_bounds", "page_select", "selected_attention_paged",
+           "prefix_attention_paged")
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "turns": 4}
 
 PagePlan = namedtuple("PagePlan", "cu_seqlens_q kv_lens positions slots free_head shortfall")
@@ -673,3 +692,26 @@ def window_workspace_bytes(n_rows: int, n_requests: int, pages_per_req: int, pag
     fp4: a 4-bit cache; num_sms 0 asks the current device."""
     return int(load_library().qsa_window_workspace_bytes(n_rows, n_requests, pages_per_req, page_size, n_qheads,
                                                          n_kvheads, head_dim, window, n_sink, int(fp4), num_sms))
+
+
+def page_select_workspace_bytes(n_rows: int, n_requests: int, pages_per_req: int, n_qheads: int, n_kvheads: int,
+                                head_dim: int) -> int:
+    """Bytes of workspace of a page_select call (qsa_page_select_workspace_bytes)."""
+    return int(load_library().qsa_page_select_workspace_bytes(n_rows, n_requests, pages_per_req, n_qheads, n_kvheads,
+                                                              head_dim))
+
+
+def selected_workspace_bytes(n_rows: int, n_requests: int, pages_per_req: int, page_size: int, n_select: int,
+                             n_qheads: int, n_kvheads: int, head_dim: int, *, num_sms: int = 0) -> int:
+    """Bytes of workspace of a selected_attention_paged call (qsa_selected_workspace_bytes); num_sms 0 asks the
+    current device."""
+    return int(load_library().qsa_selected_workspace_bytes(n_rows, n_requests, pages_per_req, page_size, n_select,
+                                                           n_qheads, n_kvheads, head_dim, num_sms))
+
+
+def prefix_workspace_bytes(n_rows: int, n_requests: int, n_groups: int, pages_per_req: int, page_size: int,
+                           n_qheads: int, n_kvheads: int, head_dim: int, *, num_sms: int = 0) -> int:
+    """Bytes of workspace of a prefix_attention_paged call (qsa_prefix_workspace_bytes); num_sms 0 asks the current
+    device."""
+    return int(load_library().qsa_prefix_workspace_bytes(n_rows, n_requests, n_groups, pages_per_req, page_size,
+                                                         n_qheads, n_kvheads, head_dim, num_sms))

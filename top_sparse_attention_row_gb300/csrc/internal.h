@@ -365,9 +365,44 @@ struct WindowParams {
 cudaError_t launch_window(const WindowParams& p, int head_dim, bool fp16, bool fp4, const void* k_cache,
                           const void* v_cache, cudaStream_t stream);
 
+// Page bounds and the choice of pages by them (choose.cu).
+struct BoundsParams {
+  const void* k_cache;          // [n_pages * page_size, n_kvheads, D]
+  void* bounds;                 // [n_pages, n_kvheads, 2, D]: minima, maxima
+  PagedAddr pa;
+  int32_t n_kvheads, head_dim;
+};
+cudaError_t launch_page_bounds(const BoundsParams& p, bool fp16, int num_sms, cudaStream_t stream);
+constexpr int kMaxChoosePages = 32768;       // of a request
+struct ChooseParams {
+  const void* q;                // [n_rows, n_qheads, D]
+  const void* bounds;
+  int32_t* out;                 // [n_rows, n_kvheads, n_select]
+  PagedAddr pa;
+  int64_t n_rows;
+  int32_t n_qheads, n_kvheads, group, head_dim;
+  int32_t n_select, n_first, n_last;
+};
+cudaError_t launch_page_select(const ChooseParams& p, bool fp16, cudaStream_t stream);
+
+// Attention over listed pages (selected.cu).
+struct SelectedParams {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  void* out;
+  float* lse;                   // nullable
+  const int32_t* pages;         // [n_rows, n_kvheads, n_select]
+  PagedAddr pa;
+  int64_t n_rows;
+  int32_t n_qheads, n_kvheads, group, n_select;
+  float scale_log2;
+};
+cudaError_t launch_selected(const SelectedParams& p, int head_dim, bool fp16, cudaStream_t stream);
+
 // Dynamic shared-memory opt-in of a kernel to `bytes`, its largest use, once per device and kernel (so
 // calls made during a graph capture only enqueue).
-enum OptInKernel { kOptPlan, kOptWindow, kOptCount = kOptWindow + 12 };
+enum OptInKernel { kOptPlan, kOptWindow, kOptChoose = kOptWindow + 12, kOptCount = kOptChoose + 6 };
 cudaError_t smem_opt_in(const void* kernel, int bytes, int which);
 
 // Host helpers of api.cpp for the other units' entry points.

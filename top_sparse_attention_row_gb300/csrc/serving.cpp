@@ -1,5 +1,5 @@
-// C-ABI entry points of the serving-step operators: page plans and rotary positions with the cache
-// writes.  Every argument error is caught here, before any CUDA call.
+// C-ABI entry points of the serving-step operators: page plans, rotary positions with the cache writes, attention over
+// paged caches, pages chosen by content and shared prompts.  Every argument error is caught here, before any CUDA call.
 #include <climits>
 #include <cmath>
 #include <cstdio>
@@ -163,6 +163,20 @@ qsa_status check_window(int64_t n_rows, int32_t n_requests, int32_t pages_per_re
   return QSA_OK;
 }
 
+qsa::PagedAddr paged_addr(const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* page_table,
+                          int32_t n_requests, int32_t pages_per_req, int32_t page_size, int64_t n_pages) {
+  qsa::PagedAddr pa{};
+  pa.page_table = page_table;
+  pa.cu_seqlens_q = cu_seqlens_q;
+  pa.kv_lens = kv_lens;
+  pa.n_requests = n_requests;
+  pa.pages_per_req = pages_per_req;
+  pa.page_size = page_size;
+  pa.page_shift = shift_of(page_size);
+  pa.n_pages = n_pages;
+  return pa;
+}
+
 qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, const Fp4Cache* fp4,
                       const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* page_table,
                       void* out, float* lse, int64_t n_rows, int32_t n_requests, int32_t pages_per_req,
@@ -195,14 +209,7 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   p.out = out;
   p.lse = lse;
   if (qsa::device_status_address(&p.status) != cudaSuccess) return QSA_ERR_CUDA;
-  p.pa.page_table = page_table;
-  p.pa.cu_seqlens_q = cu_seqlens_q;
-  p.pa.kv_lens = kv_lens;
-  p.pa.n_requests = n_requests;
-  p.pa.pages_per_req = pages_per_req;
-  p.pa.page_size = page_size;
-  p.pa.page_shift = shift_of(page_size);
-  p.pa.n_pages = n_pages;
+  p.pa = paged_addr(cu_seqlens_q, kv_lens, page_table, n_requests, pages_per_req, page_size, n_pages);
   p.n_rows = n_rows;
   p.n_units = w.n_units;
   p.n_qheads = n_qheads;
@@ -303,6 +310,143 @@ qsa_status qsa_window_attention_fp4_paged(const void* q, const void* k_cache, co
   return run_window(q, k_cache, v_cache, &f, cu_seqlens_q, kv_lens, page_table, out, lse, n_rows, n_requests,
                     pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim, scale, window, n_sink,
                     dtype, workspace, workspace_bytes, stream);
+}
+
+qsa_status qsa_page_bounds(const void* k_cache, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                           const int32_t* page_table, void* bounds, int32_t n_requests, int32_t pages_per_req,
+                           int32_t page_size, int64_t n_pages, int32_t n_kvheads, int32_t head_dim, int32_t dtype,
+                           void* stream) {
+  if (!k_cache || !cu_seqlens_q || !kv_lens || !page_table || !bounds) return QSA_ERR_INVALID_ARG;
+  if (!aligned_to(k_cache, 16) || !aligned_to(bounds, 16) || !aligned_to(cu_seqlens_q, 4) || !aligned_to(kv_lens, 4) ||
+      !aligned_to(page_table, 4) || (dtype != QSA_BF16 && dtype != QSA_FP16))
+    return QSA_ERR_INVALID_ARG;
+  qsa_status st = check_window(0, n_requests, pages_per_req, page_size, n_pages, n_kvheads, n_kvheads, head_dim, 0, 0,
+                               false);
+  if (st != QSA_OK) return st;
+  int32_t sms = 0;
+  st = qsa::device_sms(&sms);
+  if (st != QSA_OK) return st;
+  qsa::BoundsParams p{};
+  p.k_cache = k_cache;
+  p.bounds = bounds;
+  p.pa = paged_addr(cu_seqlens_q, kv_lens, page_table, n_requests, pages_per_req, page_size, n_pages);
+  p.n_kvheads = n_kvheads;
+  p.head_dim = head_dim;
+  if (qsa::launch_page_bounds(p, dtype == QSA_FP16, sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return QSA_ERR_CUDA;
+  qsa::count_launches(1);
+  return QSA_OK;
+}
+
+size_t qsa_page_select_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t pages_per_req, int32_t n_qheads,
+                                       int32_t n_kvheads, int32_t head_dim) {
+  return 0;
+}
+
+qsa_status qsa_page_select(const void* q, const void* bounds, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                           const int32_t* page_table, int32_t* pages, int64_t n_rows, int32_t n_requests,
+                           int32_t pages_per_req, int32_t page_size, int64_t n_pages, int32_t n_qheads,
+                           int32_t n_kvheads, int32_t head_dim, int32_t n_select, int32_t n_first, int32_t n_last,
+                           int32_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !bounds || !cu_seqlens_q || !kv_lens || !page_table || !pages) return QSA_ERR_INVALID_ARG;
+  if (!aligned_to(q, 16) || !aligned_to(bounds, 16) || !aligned_to(cu_seqlens_q, 4) || !aligned_to(kv_lens, 4) ||
+      !aligned_to(page_table, 4) || !aligned_to(pages, 4) || (dtype != QSA_BF16 && dtype != QSA_FP16))
+    return QSA_ERR_INVALID_ARG;
+  if (n_first < 0 || n_last < 1 || n_select < 1 || static_cast<int64_t>(n_first) + n_last > n_select)
+    return QSA_ERR_INVALID_ARG;
+  qsa_status st = check_window(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim, 0, 0,
+                               false);
+  if (st != QSA_OK) return st;
+  if (pages_per_req > qsa::kMaxChoosePages || n_rows > INT32_MAX / n_kvheads) return QSA_ERR_UNSUPPORTED;
+  if (n_rows == 0) return QSA_OK;
+  qsa::ChooseParams p{};
+  p.q = q;
+  p.bounds = bounds;
+  p.out = pages;
+  p.pa = paged_addr(cu_seqlens_q, kv_lens, page_table, n_requests, pages_per_req, page_size, n_pages);
+  p.n_rows = n_rows;
+  p.n_qheads = n_qheads;
+  p.n_kvheads = n_kvheads;
+  p.group = n_qheads / n_kvheads;
+  p.head_dim = head_dim;
+  p.n_select = n_select;
+  p.n_first = n_first;
+  p.n_last = n_last;
+  if (qsa::launch_page_select(p, dtype == QSA_FP16, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return QSA_ERR_CUDA;
+  qsa::count_launches(1);
+  return QSA_OK;
+}
+
+size_t qsa_selected_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t pages_per_req, int32_t page_size,
+                                    int32_t n_select, int32_t n_qheads, int32_t n_kvheads, int32_t head_dim,
+                                    int32_t num_sms) {
+  return 0;
+}
+
+qsa_status qsa_selected_attention_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* pages,
+                                        const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                                        const int32_t* page_table, void* out, float* lse, int64_t n_rows,
+                                        int32_t n_requests, int32_t pages_per_req, int32_t page_size,
+                                        int64_t n_pages, int32_t n_select, int32_t n_qheads, int32_t n_kvheads,
+                                        int32_t head_dim, float scale, int32_t dtype, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  if (!q || !k_cache || !v_cache || !pages || !cu_seqlens_q || !kv_lens || !page_table || !out) return QSA_ERR_INVALID_ARG;
+  if (!aligned_to(q, 16) || !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !aligned_to(out, 16) ||
+      !aligned_to(pages, 4) || !aligned_to(cu_seqlens_q, 4) || !aligned_to(kv_lens, 4) || !aligned_to(page_table, 4) ||
+      !aligned_to(lse, 4))
+    return QSA_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.0f) || !(scale_log2 > 0.0f) || !std::isfinite(scale_log2) || (dtype != QSA_BF16 && dtype != QSA_FP16) ||
+      n_select < 1)
+    return QSA_ERR_INVALID_ARG;
+  qsa_status st = check_window(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim, 0, 0,
+                               false);
+  if (st != QSA_OK) return st;
+  if (page_size % 8 != 0 || pages_per_req > qsa::kMaxChoosePages || n_rows > INT32_MAX / n_qheads)
+    return QSA_ERR_UNSUPPORTED;
+  if (n_rows == 0) return QSA_OK;
+  qsa::SelectedParams p{};
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.out = out;
+  p.lse = lse;
+  p.pages = pages;
+  p.pa = paged_addr(cu_seqlens_q, kv_lens, page_table, n_requests, pages_per_req, page_size, n_pages);
+  p.n_rows = n_rows;
+  p.n_qheads = n_qheads;
+  p.n_kvheads = n_kvheads;
+  p.group = n_qheads / n_kvheads;
+  p.n_select = n_select;
+  p.scale_log2 = scale_log2;
+  if (qsa::launch_selected(p, head_dim, dtype == QSA_FP16, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return QSA_ERR_CUDA;
+  qsa::count_launches(1);
+  return QSA_OK;
+}
+
+size_t qsa_prefix_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t n_groups, int32_t pages_per_req,
+                                  int32_t page_size, int32_t n_qheads, int32_t n_kvheads, int32_t head_dim,
+                                  int32_t num_sms) {
+  if (n_groups < 0) return 0;
+  return qsa_window_workspace_bytes(n_rows, n_requests, pages_per_req, page_size, n_qheads, n_kvheads, head_dim, 0, 0, 0,
+                                    num_sms);
+}
+
+qsa_status qsa_prefix_attention_paged(const void* q, const void* k_cache, const void* v_cache,
+                                      const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* page_table,
+                                      const int32_t* cu_groups, const int32_t* prefix_lens, void* out, float* lse,
+                                      int64_t n_rows, int32_t n_requests, int32_t n_groups, int32_t pages_per_req,
+                                      int32_t page_size, int64_t n_pages, int32_t n_qheads, int32_t n_kvheads,
+                                      int32_t head_dim, float scale, int32_t dtype, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  if (n_groups < 0 || (n_groups > 0 && (!cu_groups || !prefix_lens)) || !aligned_to(cu_groups, 4) ||
+      !aligned_to(prefix_lens, 4))
+    return QSA_ERR_INVALID_ARG;
+  return run_window(q, k_cache, v_cache, nullptr, cu_seqlens_q, kv_lens, page_table, out, lse, n_rows, n_requests,
+                    pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim, scale, 0, 0, dtype, workspace,
+                    workspace_bytes, stream);
 }
 
 qsa_status qsa_page_plan(const int32_t* past_lens, const int32_t* new_lens, int32_t* page_table,

@@ -356,6 +356,14 @@ PyObject* append(PyObject* args, PyObject* kw, bool fp4) {
 PyObject* rope_append(PyObject*, PyObject* args, PyObject* kw) { return append(args, kw, false); }
 PyObject* rope_append_fp4(PyObject*, PyObject* args, PyObject* kw) { return append(args, kw, true); }
 
+PyObject* out_and_lse(PyObject* out_o, const at::Tensor& out, PyObject* lse_o, const at::Tensor& lse) {
+  PyObject* const pair = PyTuple_New(2);
+  if (!pair) throw PythonError();
+  PyTuple_SET_ITEM(pair, 0, given(out_o) ? Py_NewRef(out_o) : THPVariable_Wrap(out));
+  PyTuple_SET_ITEM(pair, 1, given(lse_o) ? Py_NewRef(lse_o) : lse.defined() ? THPVariable_Wrap(lse) : Py_NewRef(Py_None));
+  return pair;
+}
+
 PyObject* window(PyObject* args, PyObject* kw, bool fp4) {
   static const char* names[] = {"q", "k_cache", "v_cache", "cu_seqlens_q", "kv_lens", "page_table", "page_size",
                                 "scale", "window", "n_sink", "out", "lse", "want_lse", "workspace", "stream", nullptr};
@@ -432,15 +440,182 @@ PyObject* window(PyObject* args, PyObject* kw, bool fp4) {
                      "qsa_window_attention_paged");
       }
     }
-    PyObject* const pair = PyTuple_New(2);
-    if (!pair) throw PythonError();
-    PyTuple_SET_ITEM(pair, 0, given(out_o) ? Py_NewRef(out_o) : THPVariable_Wrap(out));
-    PyTuple_SET_ITEM(pair, 1, given(lse_o) ? Py_NewRef(lse_o) : lse.defined() ? THPVariable_Wrap(lse) : Py_NewRef(Py_None));
-    return pair;
+    return out_and_lse(out_o, out, lse_o, lse);
   });
 }
 PyObject* window_attention_paged(PyObject*, PyObject* args, PyObject* kw) { return window(args, kw, false); }
 PyObject* window_attention_fp4_paged(PyObject*, PyObject* args, PyObject* kw) { return window(args, kw, true); }
+
+// The ragged batch over a paged cache that these calls share.
+struct Paged {
+  const at::Tensor *table, *cu, *kv;
+  int32_t n, ppr, ps;
+  Paged(PyObject* cu_o, PyObject* kv_o, PyObject* table_o, long long page_size, c10::Device dev) {
+    const int64_t rows = ranked(table_o, "page_table", 2).size(0), width = ranked(table_o, "page_table", 2).size(1);
+    table = &checked(table_o, "page_table", at::kInt, dev, {rows, width});
+    cu = &checked(cu_o, "cu_seqlens_q", at::kInt, dev, {rows + 1});
+    kv = &checked(kv_o, "kv_lens", at::kInt, dev, {rows});
+    n = int32_of(rows, "n_requests");
+    ppr = int32_of(width, "pages_per_req");
+    ps = int32_of(page_size, "page_size");
+  }
+  // Pages of a cache of so many slots.
+  int64_t pages_of(int64_t slots) const {
+    if (ps < 1 || slots % ps != 0)
+      fail(PyExc_ValueError, "the caches' " + std::to_string(slots) + " slots are not whole pages of " + std::to_string(ps));
+    return slots / ps;
+  }
+};
+const int32_t* ints(const at::Tensor& t) { return static_cast<const int32_t*>(t.data_ptr()); }
+
+// The workspace that was given, or one of `need` bytes.
+struct Workspace {
+  at::Tensor t;
+  Workspace(PyObject* o, size_t need, Launch& on, c10::Device dev) {
+    if (given(o)) {
+      t = tensor_of(o, "workspace");
+      if (t.device() != dev || !t.is_contiguous())
+        fail(PyExc_ValueError, "workspace must be contiguous and on " + dev.str());
+    } else if (need > 0) {
+      t = on.empty({static_cast<int64_t>(need)}, at::kByte);
+    }
+  }
+  void* data() const { return t.defined() ? t.data_ptr() : nullptr; }
+  size_t bytes() const { return t.defined() ? t.nbytes() : 0; }
+};
+
+PyObject* page_bounds(PyObject*, PyObject* args, PyObject* kw) {
+  static const char* names[] = {"k_cache", "cu_seqlens_q", "kv_lens", "page_table", "page_size", "bounds", "stream", nullptr};
+  PyObject *kc_o, *cu_o, *kv_o, *table_o, *bounds_o, *stream = nullptr;
+  long long page_size;
+  if (!PyArg_ParseTupleAndKeywords(args, kw, "OOOOLO|$O:page_bounds", const_cast<char**>(names), &kc_o, &cu_o, &kv_o,
+                                   &table_o, &page_size, &bounds_o, &stream))
+    return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& kc = ranked(kc_o, "k_cache", 3);
+    const c10::Device dev = kc.device();
+    const int32_t code = dtype_code(kc, "k_cache");
+    const int64_t S = kc.size(0), H = kc.size(1), D = kc.size(2);
+    checked(kc_o, "k_cache", kc.scalar_type(), dev, {S, H, D});
+    const Paged b(cu_o, kv_o, table_o, page_size, dev);
+    const int64_t pages = b.pages_of(S);
+    const at::Tensor& bounds = checked(bounds_o, "bounds", kc.scalar_type(), dev, {pages, H, 2, D});
+    Launch on(dev, stream);
+    if (b.n > 0)
+      check_status(qsa_page_bounds(kc.data_ptr(), ints(*b.cu), ints(*b.kv), ints(*b.table), bounds.data_ptr(), b.n, b.ppr,
+                                   b.ps, pages, int32_of(H, "KV heads"), int32_of(D, "head dim"), code, on.stream()),
+                   "qsa_page_bounds");
+    return Py_NewRef(bounds_o);
+  });
+}
+
+PyObject* page_select(PyObject*, PyObject* args, PyObject* kw) {
+  static const char* names[] = {"q", "bounds", "cu_seqlens_q", "kv_lens", "page_table", "page_size", "n_select", "n_first",
+                                "n_last", "out", "workspace", "stream", nullptr};
+  PyObject *q_o, *bounds_o, *cu_o, *kv_o, *table_o, *out_o = nullptr, *ws_o = nullptr, *stream = nullptr;
+  long long page_size, n_select, n_first = 1, n_last = 1;
+  if (!PyArg_ParseTupleAndKeywords(args, kw, "OOOOOLL|$LLOOO:page_select", const_cast<char**>(names), &q_o, &bounds_o,
+                                   &cu_o, &kv_o, &table_o, &page_size, &n_select, &n_first, &n_last, &out_o, &ws_o, &stream))
+    return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& q = ranked(q_o, "q", 3);
+    const c10::Device dev = q.device();
+    const at::ScalarType type = q.scalar_type();
+    const int32_t code = dtype_code(q, "q");
+    const int64_t R = q.size(0), Hq = q.size(1), D = q.size(2);
+    checked(q_o, "q", type, dev, {R, Hq, D});
+    const int64_t pages = ranked(bounds_o, "bounds", 4).size(0), H = ranked(bounds_o, "bounds", 4).size(1);
+    const at::Tensor& bounds = checked(bounds_o, "bounds", type, dev, {pages, H, 2, D});
+    const Paged b(cu_o, kv_o, table_o, page_size, dev);
+    const int32_t k = int32_of(n_select, "n_select"), first = int32_of(n_first, "n_first"), last = int32_of(n_last, "n_last");
+    if (k < 1) fail(PyExc_ValueError, "n_select must be at least 1");
+    const int32_t hq = int32_of(Hq, "query heads"), hkv = int32_of(H, "KV heads"), dim = int32_of(D, "head dim");
+    Launch on(dev, stream);
+    const at::Tensor out = given(out_o) ? checked(out_o, "out", at::kInt, dev, {R, H, n_select}) : on.empty({R, H, n_select}, at::kInt);
+    if (R > 0) {
+      const Workspace ws(ws_o, given(ws_o) ? 0 : qsa_page_select_workspace_bytes(R, b.n, b.ppr, hq, hkv, dim), on, dev);
+      check_status(qsa_page_select(q.data_ptr(), bounds.data_ptr(), ints(*b.cu), ints(*b.kv), ints(*b.table),
+                                   static_cast<int32_t*>(out.data_ptr()), R, b.n, b.ppr, b.ps, pages, hq, hkv, dim, k, first,
+                                   last, code, ws.data(), ws.bytes(), on.stream()),
+                   "qsa_page_select");
+    }
+    return given(out_o) ? Py_NewRef(out_o) : THPVariable_Wrap(out);
+  });
+}
+
+// selected_attention_paged (with the pages of each row) and prefix_attention_paged (with groups of requests).
+PyObject* context_attention(PyObject* args, PyObject* kw, bool prefix) {
+  static const char* names_s[] = {"q", "k_cache", "v_cache", "pages", "cu_seqlens_q", "kv_lens", "page_table", "page_size",
+                                  "scale", "out", "lse", "want_lse", "workspace", "stream", nullptr};
+  static const char* names_p[] = {"q", "k_cache", "v_cache", "cu_seqlens_q", "kv_lens", "page_table", "page_size", "scale",
+                                  "cu_groups", "prefix_lens", "out", "lse", "want_lse", "workspace", "stream", nullptr};
+  PyObject *q_o, *kc_o, *vc_o, *pages_o = nullptr, *cu_o, *kv_o, *table_o, *groups_o = nullptr, *prefix_o = nullptr;
+  PyObject *out_o = nullptr, *lse_o = nullptr, *ws_o = nullptr, *stream = nullptr;
+  long long page_size;
+  float scale;
+  int want_lse = 1;
+  const int ok =
+      prefix ? PyArg_ParseTupleAndKeywords(args, kw, "OOOOOOLfOO|$OOpOO:prefix_attention_paged", const_cast<char**>(names_p),
+                                           &q_o, &kc_o, &vc_o, &cu_o, &kv_o, &table_o, &page_size, &scale, &groups_o,
+                                           &prefix_o, &out_o, &lse_o, &want_lse, &ws_o, &stream)
+             : PyArg_ParseTupleAndKeywords(args, kw, "OOOOOOOLf|$OOpOO:selected_attention_paged", const_cast<char**>(names_s),
+                                           &q_o, &kc_o, &vc_o, &pages_o, &cu_o, &kv_o, &table_o, &page_size, &scale, &out_o,
+                                           &lse_o, &want_lse, &ws_o, &stream);
+  if (!ok) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& q = ranked(q_o, "q", 3);
+    const c10::Device dev = q.device();
+    const at::ScalarType type = q.scalar_type();
+    const int32_t code = dtype_code(q, "q");
+    const int64_t R = q.size(0), Hq = q.size(1), D = q.size(2);
+    const int64_t S = ranked(kc_o, "k_cache", 3).size(0), H = ranked(kc_o, "k_cache", 3).size(1);
+    checked(q_o, "q", type, dev, {R, Hq, D});
+    const at::Tensor& kc = checked(kc_o, "k_cache", type, dev, {S, H, D});
+    const at::Tensor& vc = checked(vc_o, "v_cache", type, dev, {S, H, D});
+    const Paged b(cu_o, kv_o, table_o, page_size, dev);
+    const int64_t n_pages = b.pages_of(S);
+    const int32_t hq = int32_of(Hq, "query heads"), hkv = int32_of(H, "KV heads"), dim = int32_of(D, "head dim");
+    const at::Tensor *pages = nullptr, *groups = nullptr, *lens = nullptr;
+    int32_t k = 0, n_groups = 0;
+    if (prefix) {
+      const int64_t G = ranked(prefix_o, "prefix_lens", 1).size(0);
+      lens = &checked(prefix_o, "prefix_lens", at::kInt, dev, {G});
+      groups = &checked(groups_o, "cu_groups", at::kInt, dev, {G + 1});
+      n_groups = int32_of(G, "n_groups");
+    } else {
+      const int64_t K = ranked(pages_o, "pages", 3).size(2);
+      pages = &checked(pages_o, "pages", at::kInt, dev, {R, H, K});
+      k = int32_of(K, "n_select");
+    }
+    Launch on(dev, stream);
+    const at::Tensor out = given(out_o) ? checked(out_o, "out", type, dev, {R, Hq, D}) : on.empty({R, Hq, D}, type);
+    at::Tensor lse;
+    if (given(lse_o)) lse = checked(lse_o, "lse", at::kFloat, dev, {R, Hq});
+    else if (want_lse) lse = on.empty({R, Hq}, at::kFloat);
+    if (R > 0) {
+      size_t need = 0;
+      if (!given(ws_o))
+        need = prefix ? qsa_prefix_workspace_bytes(R, b.n, n_groups, b.ppr, b.ps, hq, hkv, dim, 0)
+                      : qsa_selected_workspace_bytes(R, b.n, b.ppr, b.ps, k, hq, hkv, dim, 0);
+      const Workspace ws(ws_o, need, on, dev);
+      float* const lp = lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr;
+      if (prefix)
+        check_status(qsa_prefix_attention_paged(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), ints(*b.cu), ints(*b.kv),
+                                                ints(*b.table), ints(*groups), ints(*lens), out.data_ptr(), lp, R, b.n,
+                                                n_groups, b.ppr, b.ps, n_pages, hq, hkv, dim, scale, code, ws.data(),
+                                                ws.bytes(), on.stream()),
+                     "qsa_prefix_attention_paged");
+      else
+        check_status(qsa_selected_attention_paged(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), ints(*pages), ints(*b.cu),
+                                                  ints(*b.kv), ints(*b.table), out.data_ptr(), lp, R, b.n, b.ppr, b.ps,
+                                                  n_pages, k, hq, hkv, dim, scale, code, ws.data(), ws.bytes(), on.stream()),
+                     "qsa_selected_attention_paged");
+    }
+    return out_and_lse(out_o, out, lse_o, lse);
+  });
+}
+PyObject* selected_attention_paged(PyObject*, PyObject* args, PyObject* kw) { return context_attention(args, kw, false); }
+PyObject* prefix_attention_paged(PyObject*, PyObject* args, PyObject* kw) { return context_attention(args, kw, true); }
 
 // Signatures and documentation, as help() shows them.
 constexpr char k_doc_page_plan[] = R"doc(page_plan(past_lens, new_lens, page_table, free_pages, free_head, page_size, max_rows, *, n_pages=0, free_head_out=None, cu_seqlens_q=None, kv_lens=None, positions=None, slots=None, shortfall=None, stream=None)
@@ -495,9 +670,49 @@ window_attention_paged over a cache held in 4 bits, as rope_append_fp4 writes it
 (qsa_window_attention_fp4_paged): k_cache, v_cache [n_pages * page_size, Hkv, D / 2] uint8, k_scale,
 v_scale [n_pages * page_size, Hkv, D / 16] uint8, k_global, v_global the caches' fp32 scales.)doc";
 
+constexpr char k_doc_page_bounds[] = R"doc(page_bounds(k_cache, cu_seqlens_q, kv_lens, page_table, page_size, bounds, *, stream=None)
+--
+
+Bounds of the pages that the step's rows reach, for page_select (qsa_page_bounds).
+
+k_cache [n_pages * page_size, Hkv, D] bf16 or fp16 (D 64, 128 or 256), with the step's rows written;
+cu_seqlens_q [n_requests + 1], kv_lens [n_requests], page_table [n_requests, pages_per_req] int32;
+bounds [n_pages, Hkv, 2, D] of the cache's type: the smallest and the largest value of each key dim
+over the page's filled positions.  Other pages are left as they were.  Returns bounds.)doc";
+constexpr char k_doc_page_select[] = R"doc(page_select(q, bounds, cu_seqlens_q, kv_lens, page_table, page_size, n_select, *, n_first=1, n_last=1, out=None, workspace=None, stream=None)
+--
+
+Chooses up to n_select pages for every row and KV head by page_bounds' bounds (qsa_page_select).
+
+q [R, Hq, D], bounds [n_pages, Hkv, 2, D] of one type; the batch as in window_attention_paged.  A row
+takes the first n_first pages of its request, the last n_last up to its own, and of the others those
+with the highest score, the most that q.k can be for a key of the page and a query head of the group;
+ties go to the lower page.  Returns pages [R, Hkv, n_select] int32, places in the request's page
+table in increasing order, then -1.  Rows behind the last request are left as they were.)doc";
+constexpr char k_doc_selected_attention_paged[] = R"doc(selected_attention_paged(q, k_cache, v_cache, pages, cu_seqlens_q, kv_lens, page_table, page_size, scale, *, out=None, lse=None, want_lse=True, workspace=None, stream=None)
+--
+
+Attention of each row over the positions of its listed pages, up to its own
+(qsa_selected_attention_paged).
+
+pages [R, Hkv, n_select] int32 as page_select returns them, or in any order, with entries < 0 left
+out; page_size a multiple of 8; the rest as in window_attention_paged.  Returns out [R, Hq, D] and
+lse [R, Hq] fp32 (None unless wanted).)doc";
+constexpr char k_doc_prefix_attention_paged[] = R"doc(prefix_attention_paged(q, k_cache, v_cache, cu_seqlens_q, kv_lens, page_table, page_size, scale, cu_groups, prefix_lens, *, out=None, lse=None, want_lse=True, workspace=None, stream=None)
+--
+
+Attention of a batch whose requests begin alike: window_attention_paged without a window, with the
+shared keys read once for all requests of a group (qsa_prefix_attention_paged).
+
+cu_groups [n_groups + 1] int32: group g is the requests cu_groups[g] .. cu_groups[g + 1] - 1;
+prefix_lens [n_groups] int32: the positions below it hold the same keys for all of them.  The rest
+as in window_attention_paged.  Returns out [R, Hq, D] and lse [R, Hq] fp32 (None unless wanted).)doc";
+
 #define QSA_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_VARARGS | METH_KEYWORDS, k_doc_##f}
 PyMethodDef methods[] = {QSA_METHOD(page_plan), QSA_METHOD(rope), QSA_METHOD(rope_append), QSA_METHOD(rope_append_fp4),
                          QSA_METHOD(window_attention_paged), QSA_METHOD(window_attention_fp4_paged),
+                         QSA_METHOD(page_bounds), QSA_METHOD(page_select), QSA_METHOD(selected_attention_paged),
+                         QSA_METHOD(prefix_attention_paged),
                          {"set_plan_type", set_plan_type, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
