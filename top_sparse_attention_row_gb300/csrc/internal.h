@@ -332,6 +332,21 @@ constexpr int kWinTile = 128;                // keys per MMA tile, and rows of t
 // A wait's limit inside the kernel, and what is added to it for every key tile that a unit of the call may have: some
 // waits last as long as a unit (a tile takes 1 to 3 us).
 constexpr unsigned long long kWinWaitNs = 2000000000ull, kWinWaitNsPerTile = 20000ull;
+// Where the units of a call come from: the rows and their windows, or a list that a kernel before has written, of
+// chosen pages or of prompts that requests share and what is their own.
+enum UnitSource { kWindowRows = 0, kChosenPages = 1, kSharedPrefix = 2 };
+// A page of a unit of chosen pages: its place in the request's table, its id, and the unit's tokens that list it.
+struct PageEntry {
+  int32_t page, id;
+  uint32_t rows;
+  int32_t pad;
+};
+constexpr int kMaxListTokens = 32;           // tokens of such a unit: bits of PageEntry::rows
+// Shared prompts, of a unit of a request's own keys: the first row of its group, the unit of the group's first rows and
+// this head (-1: nothing is shared), the unit's rows.
+struct OwnUnit {
+  int32_t group_row0, prefix_unit, row0, tokens;
+};
 struct WindowParams {
   const void* q;                // [n_rows, n_qheads, D] bf16 or fp16
   void* out;
@@ -361,9 +376,42 @@ struct WindowParams {
   unsigned long long wait_ns;   // limit of the waits inside the kernel
   float scale_log2;             // scale * log2(e) (times the K cache's scale)
   float v_mult;                 // V cache's scale
+  // listed units (their number is n_tiles: KV heads are counted)
+  const void* units;            // [n_tiles] records
+  const int32_t* unit_tiles;    // [n_tiles] their key tiles (0: nothing to see, -2: no unit)
+  const PageEntry* entries;     // chosen pages: [n_tiles, list_cap]
+  int32_t list_cap;
+  float* first_o;               // shared prompts: [2, n_rows, n_qheads, D] whole units' and first parts' outputs
+  float* first_lse;             // [2, n_rows, n_qheads]
+  int2* unit_joins;             // [n_tiles] block that has a unit's first part, blocks it goes on in
 };
+// Lists the units of a call (listed.cu): rows x KV heads of chosen pages [n_rows, n_kvheads, n_select], or of groups of
+// requests that share prompts.
+struct ListParams {
+  PagedAddr pa;
+  const int32_t* pages;
+  const int32_t* cu_groups;
+  const int32_t* prefix_lens;
+  void* units;
+  int32_t* unit_tiles;
+  PageEntry* entries;
+  OwnUnit* own;                 // [request tiles, n_kvheads]
+  int2* unit_joins;             // [n_tiles]
+  int64_t n_rows;
+  int32_t n_kvheads, n_select, list_cap, tile_tokens, n_groups;
+  int32_t prefix_tiles;         // tiles of the groups, which come first; then those of the requests
+  int32_t n_tiles;              // both, or of chosen pages all
+  int32_t grain;                // keys per TMA box, or 4
+};
+cudaError_t launch_list_pages(const ListParams& p, cudaStream_t stream);
+cudaError_t launch_list_prefix(const ListParams& p, cudaStream_t stream);
+// Joins the results of shared prompts' rows.
+cudaError_t launch_join_prefix(const WindowParams& p, const ListParams& l, int head_dim, bool fp16, cudaStream_t stream);
 cudaError_t launch_window(const WindowParams& p, int head_dim, bool fp16, bool fp4, const void* k_cache,
                           const void* v_cache, cudaStream_t stream);
+// The same over listed units.  l: the list that shared prompts' rows are joined by.
+cudaError_t launch_listed(const WindowParams& p, const ListParams& l, UnitSource source, int head_dim, bool fp16,
+                          const void* k_cache, const void* v_cache, cudaStream_t stream);
 
 // Page bounds and the choice of pages by them (choose.cu).
 struct BoundsParams {
@@ -385,24 +433,10 @@ struct ChooseParams {
 };
 cudaError_t launch_page_select(const ChooseParams& p, bool fp16, cudaStream_t stream);
 
-// Attention over listed pages (selected.cu).
-struct SelectedParams {
-  const void* q;
-  const void* k_cache;
-  const void* v_cache;
-  void* out;
-  float* lse;                   // nullable
-  const int32_t* pages;         // [n_rows, n_kvheads, n_select]
-  PagedAddr pa;
-  int64_t n_rows;
-  int32_t n_qheads, n_kvheads, group, n_select;
-  float scale_log2;
-};
-cudaError_t launch_selected(const SelectedParams& p, int head_dim, bool fp16, cudaStream_t stream);
-
 // Dynamic shared-memory opt-in of a kernel to `bytes`, its largest use, once per device and kernel (so
 // calls made during a graph capture only enqueue).
-enum OptInKernel { kOptPlan, kOptWindow, kOptChoose = kOptWindow + 12, kOptCount = kOptChoose + 6 };
+enum OptInKernel { kOptPlan, kOptWindow, kOptChoose = kOptWindow + 24, kOptListPages = kOptChoose + 6,
+                    kOptCount = kOptListPages + 1 };
 cudaError_t smem_opt_in(const void* kernel, int bytes, int which);
 
 // Host helpers of api.cpp for the other units' entry points.

@@ -1,0 +1,11 @@
+// Attention kernels over listed units (chosen pages, shared prompts) of head dim 128 (window.cuh).
+#include "window.cuh"
+
+namespace qsa {
+
+cudaError_t launch_listed_d128(const WindowParams& p, bool fp16, bool prefix, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& tq1, const CUtensorMap& tqt, int grid, cudaStream_t stream) {
+  return launch_listed_dim<128>(p, fp16, prefix, tk, tv, tq1, tqt, grid, stream);
+}
+
+}  // namespace qsa

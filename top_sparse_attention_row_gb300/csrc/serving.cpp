@@ -177,23 +177,61 @@ qsa::PagedAddr paged_addr(const int32_t* cu_seqlens_q, const int32_t* kv_lens, c
   return pa;
 }
 
-qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, const Fp4Cache* fp4,
-                      const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* page_table,
-                      void* out, float* lse, int64_t n_rows, int32_t n_requests, int32_t pages_per_req,
-                      int32_t page_size, int64_t n_pages, int32_t n_qheads, int32_t n_kvheads,
-                      int32_t head_dim, float scale, int32_t window, int32_t n_sink, int32_t dtype,
-                      void* workspace, size_t workspace_bytes, void* stream_v) {
+qsa::WindowParams window_params(const void* q, void* out, float* lse, const qsa::PagedAddr& pa, int64_t n_rows,
+                                int32_t n_qheads, int32_t n_kvheads, const WindowPlan& w, float scale_log2) {
+  qsa::WindowParams p{};
+  p.q = q;
+  p.out = out;
+  p.lse = lse;
+  p.pa = pa;
+  p.n_rows = n_rows;
+  p.n_units = w.n_units;
+  p.n_qheads = n_qheads;
+  p.n_kvheads = n_kvheads;
+  p.group = n_qheads / n_kvheads;
+  p.tile_tokens = w.tile_tokens;
+  p.n_tiles = w.n_tiles;
+  p.shares = w.shares;
+  p.unit_cost = w.unit_cost;
+  p.wait_ns = qsa::kWinWaitNs + qsa::kWinWaitNsPerTile * static_cast<unsigned long long>(w.key_tiles);
+  p.out_32 = aligned_to(out, 32);
+  int32_t box = 1;      // keys per copy: the largest power of two <= 64 that divides the page size
+  while (box < 64 && pa.page_size % (2 * box) == 0) box *= 2;
+  p.box = box >= 8 ? box : 0;
+  p.n_slots = static_cast<int32_t>(pa.n_pages * pa.page_size);
+  p.scale_log2 = scale_log2;
+  p.v_mult = 1.0f;
+  return p;
+}
+
+// The query, cache and output arguments of attention over a paged cache, and its scale.
+qsa_status check_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* cu_seqlens_q,
+                           const int32_t* kv_lens, const int32_t* page_table, const void* out, const float* lse, float scale,
+                           float more_scale, int32_t dtype, float* scale_log2) {
   if (!q || !k_cache || !v_cache || !cu_seqlens_q || !kv_lens || !page_table || !out) return QSA_ERR_INVALID_ARG;
   if (!aligned_to(q, 16) || !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !aligned_to(out, 16) ||
       !aligned_to(cu_seqlens_q, 4) || !aligned_to(kv_lens, 4) || !aligned_to(page_table, 4) ||
       !aligned_to(lse, 4))
     return QSA_ERR_INVALID_ARG;
   // (scale log2(e), with a 4-bit cache's scale, is what the kernel multiplies by)
-  const float scale_log2 = scale * 1.4426950408889634f * (fp4 ? fp4->k_global : 1.0f);
-  if (!(scale > 0.0f) || !(scale_log2 > 0.0f) || !std::isfinite(scale_log2) || (dtype != QSA_BF16 && dtype != QSA_FP16))
+  *scale_log2 = scale * 1.4426950408889634f * more_scale;
+  if (!(scale > 0.0f) || !(*scale_log2 > 0.0f) || !std::isfinite(*scale_log2) || (dtype != QSA_BF16 && dtype != QSA_FP16))
     return QSA_ERR_INVALID_ARG;
-  qsa_status st = check_window(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads,
-                               head_dim, window, n_sink, fp4 != nullptr);
+  return QSA_OK;
+}
+
+qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, const Fp4Cache* fp4,
+                      const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* page_table,
+                      void* out, float* lse, int64_t n_rows, int32_t n_requests, int32_t pages_per_req,
+                      int32_t page_size, int64_t n_pages, int32_t n_qheads, int32_t n_kvheads,
+                      int32_t head_dim, float scale, int32_t window, int32_t n_sink, int32_t dtype,
+                      void* workspace, size_t workspace_bytes, void* stream_v) {
+  float scale_log2;
+  qsa_status st = check_attention(q, k_cache, v_cache, cu_seqlens_q, kv_lens, page_table, out, lse, scale,
+                                  fp4 ? fp4->k_global : 1.0f, dtype, &scale_log2);
+  if (st != QSA_OK) return st;
+  st = check_window(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads,
+                    head_dim, window, n_sink, fp4 != nullptr);
   if (st != QSA_OK) return st;
   if (n_rows == 0) return QSA_OK;
   int32_t sms = 0;
@@ -204,31 +242,12 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   const WindowPlan w = plan_window(n_rows, n_requests, n_kvheads, group, window_tile_rows(head_dim, fp4 != nullptr),
                                    static_cast<int64_t>(pages_per_req) * page_size, window, n_sink, sms);
   if (w.n_units > INT32_MAX) return QSA_ERR_UNSUPPORTED;
-  qsa::WindowParams p{};
-  p.q = q;
-  p.out = out;
-  p.lse = lse;
+  qsa::WindowParams p = window_params(
+      q, out, lse, paged_addr(cu_seqlens_q, kv_lens, page_table, n_requests, pages_per_req, page_size, n_pages), n_rows,
+      n_qheads, n_kvheads, w, scale_log2);
   if (qsa::device_status_address(&p.status) != cudaSuccess) return QSA_ERR_CUDA;
-  p.pa = paged_addr(cu_seqlens_q, kv_lens, page_table, n_requests, pages_per_req, page_size, n_pages);
-  p.n_rows = n_rows;
-  p.n_units = w.n_units;
-  p.n_qheads = n_qheads;
-  p.n_kvheads = n_kvheads;
-  p.group = group;
-  p.tile_tokens = w.tile_tokens;
-  p.n_tiles = w.n_tiles;
-  p.shares = w.shares;
-  p.unit_cost = w.unit_cost;
-  p.wait_ns = qsa::kWinWaitNs + qsa::kWinWaitNsPerTile * static_cast<unsigned long long>(w.key_tiles);
-  p.out_32 = aligned_to(out, 32);
   p.window = window;
   p.n_sink = n_sink;
-  int32_t box = 1;      // keys per copy: the largest power of two <= 64 that divides the page size
-  while (box < 64 && page_size % (2 * box) == 0) box *= 2;
-  p.box = box >= 8 ? box : 0;
-  p.n_slots = static_cast<int32_t>(n_pages * page_size);
-  p.scale_log2 = scale_log2;
-  p.v_mult = 1.0f;
   if (fp4) {
     p.k_codes = static_cast<const uint8_t*>(k_cache);
     p.v_codes = static_cast<const uint8_t*>(v_cache);
@@ -262,6 +281,128 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   if (own) cudaFreeAsync(ws, stream);
   if (e != cudaSuccess) return QSA_ERR_CUDA;
   qsa::count_launches(p.shares > 0 ? 2 : 1);
+  return QSA_OK;
+}
+
+qsa_status check_selected(int64_t n_rows, int32_t n_requests, int32_t pages_per_req, int32_t page_size, int64_t n_pages,
+                          int32_t n_qheads, int32_t n_kvheads, int32_t head_dim) {
+  const qsa_status st = check_window(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim,
+                                     0, 0, false);
+  if (st != QSA_OK) return st;
+  return page_size % 8 != 0 || pages_per_req > qsa::kMaxChoosePages ? QSA_ERR_UNSUPPORTED : QSA_OK;
+}
+
+// Attention over listed units: what is listed, how the units are dealt out, and the workspace.
+struct ListedPlan {
+  WindowPlan w;                  // n_tiles: units, KV heads counted
+  int32_t list_cap, prefix_tiles;
+  size_t tiles_at, joins_at, own_at, entries_at, first_at, parts_at, bytes;
+};
+constexpr size_t kUnitBytes = 64;
+size_t round_256(size_t n) { return (n + 255) / 256 * 256; }
+void lay_out(ListedPlan* l, int32_t head_dim, size_t unit_joins, size_t own, size_t entries, size_t first_rows,
+             size_t part_bytes) {
+  const size_t n = static_cast<size_t>(l->w.n_tiles);
+  l->tiles_at = round_256(n * kUnitBytes);
+  l->joins_at = l->tiles_at + round_256(n * sizeof(int32_t));
+  l->own_at = l->joins_at + round_256(unit_joins * sizeof(int2));
+  l->entries_at = l->own_at + round_256(own * sizeof(qsa::OwnUnit));
+  l->first_at = l->entries_at + round_256(entries * sizeof(qsa::PageEntry));
+  l->parts_at = l->first_at + round_256(first_rows * (static_cast<size_t>(head_dim) + 1) * 4);
+  l->bytes = l->parts_at + part_bytes;
+}
+
+// Chosen pages: a tile of several tokens has a few more keys than one token, since neighbours choose much the same pages
+// (1.01 to 1.23 times as many for four tokens in measured selections): taken as a tenth more for each further token.
+bool plan_pages(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, int32_t group, int32_t pages_per_req,
+                int32_t page_size, int32_t n_select, int32_t head_dim, int32_t sms, ListedPlan* l) {
+  int32_t tokens = qsa::kWinTile / group;
+  if (tokens > qsa::kMaxListTokens) tokens = qsa::kMaxListTokens;
+  const int64_t most = static_cast<int64_t>(tokens) * n_select;
+  l->list_cap = static_cast<int32_t>(most < pages_per_req ? most : pages_per_req);
+  const int64_t each = n_rows < n_requests ? 1 : n_rows / n_requests < tokens ? n_rows / n_requests : tokens;
+  int64_t pages = n_select + static_cast<int64_t>(n_select) * (each - 1) / 10;
+  if (pages > l->list_cap) pages = l->list_cap;
+  l->w = plan_window(n_rows, n_requests, n_kvheads, group, tokens * group, pages * page_size, 0, 0, sms);
+  if (l->w.n_units > INT32_MAX) return false;
+  l->w.n_tiles = static_cast<int32_t>(l->w.n_units);
+  if (l->w.n_tiles > 4 * kMaxShareTiles) l->w.shares = l->w.unit_cost = 0;
+  l->w.key_tiles = static_cast<int32_t>((static_cast<int64_t>(l->list_cap) * page_size + qsa::kWinTile - 1) / qsa::kWinTile);
+  l->prefix_tiles = 0;
+  lay_out(l, head_dim, 0, 0, static_cast<size_t>(l->w.n_tiles) * l->list_cap, 0, window_ws_bytes(head_dim, l->w.shares));
+  return true;
+}
+
+// Shared prompts: always equal shares, since a row's two results are joined anyway.
+bool plan_prefix(int64_t n_rows, int32_t n_requests, int32_t n_groups, int32_t n_kvheads, int32_t group,
+                 int32_t pages_per_req, int32_t page_size, int32_t head_dim, int32_t sms, ListedPlan* l) {
+  l->w.tile_tokens = qsa::kWinTile / group;
+  const int64_t tiles = n_rows / l->w.tile_tokens;
+  const int64_t prefix_tiles = n_groups > 0 ? tiles + n_groups : 0;
+  const int64_t units = (prefix_tiles + tiles + n_requests) * n_kvheads;
+  if (units > INT32_MAX) return false;
+  l->prefix_tiles = static_cast<int32_t>(prefix_tiles);
+  l->w.n_units = units;
+  l->w.n_tiles = static_cast<int32_t>(units);
+  l->w.shares = sms;
+  // (as plan_window) units with rows, at least the requests' own
+  l->w.unit_cost = ((n_rows + l->w.tile_tokens - 1) / l->w.tile_tokens + n_requests - 1) * n_kvheads > sms ? 3 : 0;
+  l->w.key_tiles = static_cast<int32_t>((static_cast<int64_t>(pages_per_req) * page_size + qsa::kWinTile - 1) / qsa::kWinTile);
+  const int32_t group_heads = n_kvheads * group;
+  lay_out(l, head_dim, static_cast<size_t>(units), static_cast<size_t>(tiles + n_requests) * n_kvheads, 0,
+          2 * static_cast<size_t>(n_rows) * group_heads, static_cast<size_t>(sms) * qsa::kWinTile * (static_cast<size_t>(head_dim) + 1) * 4);
+  return true;
+}
+
+qsa_status run_listed(qsa::WindowParams& p, qsa::ListParams& l, const ListedPlan& plan, qsa::UnitSource source,
+                      int32_t head_dim, int32_t dtype, const void* k_cache, const void* v_cache, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream) {
+  if (qsa::device_status_address(&p.status) != cudaSuccess) return QSA_ERR_CUDA;
+  const bool prefix = source == qsa::kSharedPrefix;
+  if (qsa::log_geometry())
+    std::fprintf(stderr, "qsa: %s d=%d rows=%lld requests=%d heads=%d/%d -> tile_tokens=%d box=%d shares=%d units=%d\n",
+                 prefix ? "prefix" : "selected", head_dim, static_cast<long long>(p.n_rows), p.pa.n_requests, p.n_qheads,
+                 p.n_kvheads, p.tile_tokens, p.box, p.shares, p.n_tiles);
+  void* ws = workspace;
+  const bool own = !ws;
+  if (own) {
+    if (qsa::ws_alloc(&ws, plan.bytes, stream) != cudaSuccess) return QSA_ERR_CUDA;
+  } else if (workspace_bytes < plan.bytes || !aligned_to(ws, 256)) {
+    return QSA_ERR_WORKSPACE;
+  }
+  uint8_t* const b = static_cast<uint8_t*>(ws);
+  l.units = b;
+  l.unit_tiles = reinterpret_cast<int32_t*>(b + plan.tiles_at);
+  l.unit_joins = reinterpret_cast<int2*>(b + plan.joins_at);
+  l.own = reinterpret_cast<qsa::OwnUnit*>(b + plan.own_at);
+  l.entries = reinterpret_cast<qsa::PageEntry*>(b + plan.entries_at);
+  l.pa = p.pa;
+  l.n_rows = p.n_rows;
+  l.n_kvheads = p.n_kvheads;
+  l.list_cap = plan.list_cap;
+  l.tile_tokens = p.tile_tokens;
+  l.prefix_tiles = plan.prefix_tiles;
+  l.n_tiles = p.n_tiles;
+  l.grain = p.box > 0 ? p.box : 4;
+  p.units = l.units;
+  p.unit_tiles = l.unit_tiles;
+  p.unit_joins = l.unit_joins;
+  p.entries = l.entries;
+  p.list_cap = l.list_cap;
+  p.part_o = reinterpret_cast<float*>(b + plan.parts_at);
+  const size_t slots = static_cast<size_t>(p.shares) * (prefix ? 1 : 2);
+  p.part_lse = p.part_o + slots * qsa::kWinTile * head_dim;
+  if (prefix) {
+    p.first_o = reinterpret_cast<float*>(b + plan.first_at);
+    p.first_lse = p.first_o + 2 * static_cast<size_t>(p.n_rows) * p.n_qheads * head_dim;
+  } else {
+    p.joins = reinterpret_cast<qsa::JoinRecord*>(p.part_lse + slots * qsa::kWinTile);
+  }
+  p.stall_first_item = qsa::take_stall_request() ? 1 : 0;
+  const cudaError_t e = qsa::launch_listed(p, l, source, head_dim, dtype == QSA_FP16, k_cache, v_cache, stream);
+  if (own) cudaFreeAsync(ws, stream);
+  if (e != cudaSuccess) return QSA_ERR_CUDA;
+  qsa::count_launches(p.shares > 0 ? 3 : 2);
   return QSA_OK;
 }
 
@@ -381,7 +522,15 @@ qsa_status qsa_page_select(const void* q, const void* bounds, const int32_t* cu_
 size_t qsa_selected_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t pages_per_req, int32_t page_size,
                                     int32_t n_select, int32_t n_qheads, int32_t n_kvheads, int32_t head_dim,
                                     int32_t num_sms) {
-  return 0;
+  if (n_select < 1 || check_selected(n_rows, n_requests, pages_per_req, page_size, 1, n_qheads, n_kvheads, head_dim) != QSA_OK ||
+      n_rows == 0)
+    return 0;
+  if (num_sms <= 0 && qsa::device_sms(&num_sms) != QSA_OK) return 0;
+  ListedPlan plan{};
+  return plan_pages(n_rows, n_requests, n_kvheads, n_qheads / n_kvheads, pages_per_req, page_size, n_select, head_dim,
+                    num_sms, &plan)
+             ? plan.bytes
+             : 0;
 }
 
 qsa_status qsa_selected_attention_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* pages,
@@ -391,47 +540,43 @@ qsa_status qsa_selected_attention_paged(const void* q, const void* k_cache, cons
                                         int64_t n_pages, int32_t n_select, int32_t n_qheads, int32_t n_kvheads,
                                         int32_t head_dim, float scale, int32_t dtype, void* workspace,
                                         size_t workspace_bytes, void* stream) {
-  if (!q || !k_cache || !v_cache || !pages || !cu_seqlens_q || !kv_lens || !page_table || !out) return QSA_ERR_INVALID_ARG;
-  if (!aligned_to(q, 16) || !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !aligned_to(out, 16) ||
-      !aligned_to(pages, 4) || !aligned_to(cu_seqlens_q, 4) || !aligned_to(kv_lens, 4) || !aligned_to(page_table, 4) ||
-      !aligned_to(lse, 4))
-    return QSA_ERR_INVALID_ARG;
-  const float scale_log2 = scale * 1.4426950408889634f;
-  if (!(scale > 0.0f) || !(scale_log2 > 0.0f) || !std::isfinite(scale_log2) || (dtype != QSA_BF16 && dtype != QSA_FP16) ||
-      n_select < 1)
-    return QSA_ERR_INVALID_ARG;
-  qsa_status st = check_window(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim, 0, 0,
-                               false);
+  float scale_log2;
+  qsa_status st = check_attention(q, k_cache, v_cache, cu_seqlens_q, kv_lens, page_table, out, lse, scale, 1.0f, dtype,
+                                  &scale_log2);
   if (st != QSA_OK) return st;
-  if (page_size % 8 != 0 || pages_per_req > qsa::kMaxChoosePages || n_rows > INT32_MAX / n_qheads)
-    return QSA_ERR_UNSUPPORTED;
+  if (!pages || !aligned_to(pages, 4) || n_select < 1) return QSA_ERR_INVALID_ARG;
+  st = check_selected(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim);
+  if (st != QSA_OK) return st;
   if (n_rows == 0) return QSA_OK;
-  qsa::SelectedParams p{};
-  p.q = q;
-  p.k_cache = k_cache;
-  p.v_cache = v_cache;
-  p.out = out;
-  p.lse = lse;
-  p.pages = pages;
-  p.pa = paged_addr(cu_seqlens_q, kv_lens, page_table, n_requests, pages_per_req, page_size, n_pages);
-  p.n_rows = n_rows;
-  p.n_qheads = n_qheads;
-  p.n_kvheads = n_kvheads;
-  p.group = n_qheads / n_kvheads;
-  p.n_select = n_select;
-  p.scale_log2 = scale_log2;
-  if (qsa::launch_selected(p, head_dim, dtype == QSA_FP16, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return QSA_ERR_CUDA;
-  qsa::count_launches(1);
-  return QSA_OK;
+  int32_t sms = 0;
+  st = qsa::device_sms(&sms);
+  if (st != QSA_OK) return st;
+  ListedPlan plan{};
+  if (!plan_pages(n_rows, n_requests, n_kvheads, n_qheads / n_kvheads, pages_per_req, page_size, n_select, head_dim, sms,
+                  &plan))
+    return QSA_ERR_UNSUPPORTED;
+  qsa::WindowParams p = window_params(
+      q, out, lse, paged_addr(cu_seqlens_q, kv_lens, page_table, n_requests, pages_per_req, page_size, n_pages), n_rows,
+      n_qheads, n_kvheads, plan.w, scale_log2);
+  qsa::ListParams l{};
+  l.pages = pages;
+  l.n_select = n_select;
+  return run_listed(p, l, plan, qsa::kChosenPages, head_dim, dtype, k_cache, v_cache, workspace, workspace_bytes,
+                    static_cast<cudaStream_t>(stream));
 }
 
 size_t qsa_prefix_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t n_groups, int32_t pages_per_req,
                                   int32_t page_size, int32_t n_qheads, int32_t n_kvheads, int32_t head_dim,
                                   int32_t num_sms) {
-  if (n_groups < 0) return 0;
-  return qsa_window_workspace_bytes(n_rows, n_requests, pages_per_req, page_size, n_qheads, n_kvheads, head_dim, 0, 0, 0,
-                                    num_sms);
+  if (n_groups < 0 || check_window(n_rows, n_requests, pages_per_req, page_size, 1, n_qheads, n_kvheads, head_dim, 0, 0,
+                                   false) != QSA_OK || n_rows == 0)
+    return 0;
+  if (num_sms <= 0 && qsa::device_sms(&num_sms) != QSA_OK) return 0;
+  ListedPlan plan{};
+  return plan_prefix(n_rows, n_requests, n_groups, n_kvheads, n_qheads / n_kvheads, pages_per_req, page_size, head_dim,
+                     num_sms, &plan)
+             ? plan.bytes
+             : 0;
 }
 
 qsa_status qsa_prefix_attention_paged(const void* q, const void* k_cache, const void* v_cache,
@@ -441,12 +586,32 @@ qsa_status qsa_prefix_attention_paged(const void* q, const void* k_cache, const 
                                       int32_t page_size, int64_t n_pages, int32_t n_qheads, int32_t n_kvheads,
                                       int32_t head_dim, float scale, int32_t dtype, void* workspace,
                                       size_t workspace_bytes, void* stream) {
+  float scale_log2;
+  qsa_status st = check_attention(q, k_cache, v_cache, cu_seqlens_q, kv_lens, page_table, out, lse, scale, 1.0f, dtype,
+                                  &scale_log2);
+  if (st != QSA_OK) return st;
   if (n_groups < 0 || (n_groups > 0 && (!cu_groups || !prefix_lens)) || !aligned_to(cu_groups, 4) ||
       !aligned_to(prefix_lens, 4))
     return QSA_ERR_INVALID_ARG;
-  return run_window(q, k_cache, v_cache, nullptr, cu_seqlens_q, kv_lens, page_table, out, lse, n_rows, n_requests,
-                    pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim, scale, 0, 0, dtype, workspace,
-                    workspace_bytes, stream);
+  st = check_window(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim, 0, 0, false);
+  if (st != QSA_OK) return st;
+  if (n_rows == 0) return QSA_OK;
+  int32_t sms = 0;
+  st = qsa::device_sms(&sms);
+  if (st != QSA_OK) return st;
+  ListedPlan plan{};
+  if (!plan_prefix(n_rows, n_requests, n_groups, n_kvheads, n_qheads / n_kvheads, pages_per_req, page_size, head_dim, sms,
+                   &plan))
+    return QSA_ERR_UNSUPPORTED;
+  qsa::WindowParams p = window_params(
+      q, out, lse, paged_addr(cu_seqlens_q, kv_lens, page_table, n_requests, pages_per_req, page_size, n_pages), n_rows,
+      n_qheads, n_kvheads, plan.w, scale_log2);
+  qsa::ListParams l{};
+  l.cu_groups = cu_groups;
+  l.prefix_lens = prefix_lens;
+  l.n_groups = n_groups;
+  return run_listed(p, l, plan, qsa::kSharedPrefix, head_dim, dtype, k_cache, v_cache, workspace, workspace_bytes,
+                    static_cast<cudaStream_t>(stream));
 }
 
 qsa_status qsa_page_plan(const int32_t* past_lens, const int32_t* new_lens, int32_t* page_table,

@@ -1,4 +1,4 @@
-// Window attention: tensor maps, kernel choice and the join of units that several blocks share.
+// Attention over paged caches: tensor maps, kernel choice and the join of units that several blocks share.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -183,42 +183,64 @@ CUresult encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, c
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-cudaError_t launch_window(const WindowParams& p, int head_dim, bool fp16, bool fp4, const void* k_cache,
-                          const void* v_cache, cudaStream_t stream) {
+namespace {
+// Tensor maps of the query rows (one token's heads, a tile's) and of the caches.
+CUresult encode_maps(const WindowParams& p, int head_dim, const void* k_cache, const void* v_cache, CUtensorMap* tk,
+                     CUtensorMap* tv, CUtensorMap* tq1, CUtensorMap* tqt) {
   // (the element type only decides how many bits are moved: 16 either way)
   const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  CUtensorMap tk{}, tv{}, tq1{}, tqt{};
-  if (!fp4) {
-    const cuuint64_t d = static_cast<cuuint64_t>(head_dim);
-    const cuuint64_t q_dims[3] = {d, static_cast<cuuint64_t>(p.n_qheads), static_cast<cuuint64_t>(p.n_rows)};
-    const cuuint64_t q_strides[2] = {d * 2, d * 2 * static_cast<cuuint64_t>(p.n_qheads)};
-    const cuuint32_t q_box1[3] = {64, static_cast<cuuint32_t>(p.group), 1};
-    const cuuint32_t q_boxt[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(p.tile_tokens)};
-    CUresult r = encode_tensor_map(&tq1, type, 3, p.q, q_dims, q_strides, q_box1);
-    if (r == CUDA_SUCCESS) r = encode_tensor_map(&tqt, type, 3, p.q, q_dims, q_strides, q_boxt);
-    const cuuint64_t slots = static_cast<cuuint64_t>(p.n_slots), heads = static_cast<cuuint64_t>(p.n_kvheads);
-    for (int i = 0; i < 2 && r == CUDA_SUCCESS; ++i) {
-      CUtensorMap* const m = i == 0 ? &tk : &tv;
-      const void* const cache = i == 0 ? k_cache : v_cache;
-      if (p.box > 0) {      // boxes of `box` slots of one KV head
-        const cuuint64_t dims[3] = {d, heads, slots};
-        const cuuint64_t strides[2] = {d * 2, d * 2 * heads};
-        const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(p.box)};
-        r = encode_tensor_map(m, type, 3, cache, dims, strides, box);
-      } else {              // gathers of four rows (slot x heads + head)
-        const cuuint64_t dims[2] = {d, slots * heads};
-        const cuuint64_t strides[1] = {d * 2};
-        const cuuint32_t box[2] = {64, 1};
-        r = encode_tensor_map(m, type, 2, cache, dims, strides, box);
-      }
+  const cuuint64_t d = static_cast<cuuint64_t>(head_dim);
+  const cuuint64_t q_dims[3] = {d, static_cast<cuuint64_t>(p.n_qheads), static_cast<cuuint64_t>(p.n_rows)};
+  const cuuint64_t q_strides[2] = {d * 2, d * 2 * static_cast<cuuint64_t>(p.n_qheads)};
+  const cuuint32_t q_box1[3] = {64, static_cast<cuuint32_t>(p.group), 1};
+  const cuuint32_t q_boxt[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(p.tile_tokens)};
+  CUresult r = encode_tensor_map(tq1, type, 3, p.q, q_dims, q_strides, q_box1);
+  if (r == CUDA_SUCCESS) r = encode_tensor_map(tqt, type, 3, p.q, q_dims, q_strides, q_boxt);
+  const cuuint64_t slots = static_cast<cuuint64_t>(p.n_slots), heads = static_cast<cuuint64_t>(p.n_kvheads);
+  for (int i = 0; i < 2 && r == CUDA_SUCCESS; ++i) {
+    CUtensorMap* const m = i == 0 ? tk : tv;
+    const void* const cache = i == 0 ? k_cache : v_cache;
+    if (p.box > 0) {      // boxes of `box` slots of one KV head
+      const cuuint64_t dims[3] = {d, heads, slots};
+      const cuuint64_t strides[2] = {d * 2, d * 2 * heads};
+      const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(p.box)};
+      r = encode_tensor_map(m, type, 3, cache, dims, strides, box);
+    } else {              // gathers of four rows (slot x heads + head)
+      const cuuint64_t dims[2] = {d, slots * heads};
+      const cuuint64_t strides[1] = {d * 2};
+      const cuuint32_t box[2] = {64, 1};
+      r = encode_tensor_map(m, type, 2, cache, dims, strides, box);
     }
-    if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
   }
+  return r;
+}
+}  // namespace
+
+cudaError_t launch_window(const WindowParams& p, int head_dim, bool fp16, bool fp4, const void* k_cache,
+                          const void* v_cache, cudaStream_t stream) {
+  CUtensorMap tk{}, tv{}, tq1{}, tqt{};
+  if (!fp4 && encode_maps(p, head_dim, k_cache, v_cache, &tk, &tv, &tq1, &tqt) != CUDA_SUCCESS) return cudaErrorInvalidValue;
   const int grid = p.shares > 0 ? p.shares : static_cast<int>(p.n_units);
   const cudaError_t e = head_dim == 64    ? launch_window_d64(p, fp16, fp4, tk, tv, tq1, tqt, grid, stream)
                         : head_dim == 128 ? launch_window_d128(p, fp16, fp4, tk, tv, tq1, tqt, grid, stream)
                                           : launch_window_d256(p, fp16, fp4, tk, tv, tq1, tqt, grid, stream);
   if (e != cudaSuccess || p.shares == 0) return e;
+  return fp16 ? launch_join<__half>(p, head_dim, stream) : launch_join<__nv_bfloat16>(p, head_dim, stream);
+}
+
+cudaError_t launch_listed(const WindowParams& p, const ListParams& l, UnitSource source, int head_dim, bool fp16,
+                          const void* k_cache, const void* v_cache, cudaStream_t stream) {
+  CUtensorMap tk{}, tv{}, tq1{}, tqt{};
+  if (encode_maps(p, head_dim, k_cache, v_cache, &tk, &tv, &tq1, &tqt) != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  const bool prefix = source == kSharedPrefix;
+  cudaError_t e = prefix ? launch_list_prefix(l, stream) : launch_list_pages(l, stream);
+  if (e != cudaSuccess) return e;
+  const int grid = p.shares > 0 ? p.shares : p.n_tiles;
+  e = head_dim == 64    ? launch_listed_d64(p, fp16, prefix, tk, tv, tq1, tqt, grid, stream)
+      : head_dim == 128 ? launch_listed_d128(p, fp16, prefix, tk, tv, tq1, tqt, grid, stream)
+                        : launch_listed_d256(p, fp16, prefix, tk, tv, tq1, tqt, grid, stream);
+  if (e != cudaSuccess || p.shares == 0) return e;
+  if (prefix) return launch_join_prefix(p, l, head_dim, fp16, stream);
   return fp16 ? launch_join<__half>(p, head_dim, stream) : launch_join<__nv_bfloat16>(p, head_dim, stream);
 }
 

@@ -267,6 +267,33 @@ __device__ __forceinline__ void cut(Unit& u, int32_t a, int32_t b) {
   u.all1 -= a;
 }
 
+// Listed units (chosen pages, shared prompts): a kernel before this one has written them, units [n_units] (in any
+// order of tiles and KV heads) and their key tiles (-2: no unit).
+__device__ __forceinline__ Unit listed_unit(const WindowParams& p, int32_t n) {
+  Unit u = load_unit(static_cast<const Unit*>(p.units) + n);
+  u.tiles = p.unit_tiles[n];
+  return u;
+}
+// Chosen pages: a unit's keys are the positions of its pages, one page after the other (virtual index v: entry v / page
+// size).  u.s0 holds their number, u.shift the unit's number.
+__device__ __forceinline__ const PageEntry* unit_entries(const WindowParams& p, const Unit& u) {
+  return p.entries + static_cast<int64_t>(u.shift) * p.list_cap;
+}
+__device__ __forceinline__ PageEntry load_entry(const PageEntry* e) {
+  const int4 x = __ldg(reinterpret_cast<const int4*>(e));
+  return PageEntry{x.x, x.y, static_cast<uint32_t>(x.z), x.w};
+}
+__device__ __forceinline__ int32_t entry_of(const WindowParams& p, int32_t v) {
+  return p.pa.page_shift >= 0 ? v >> p.pa.page_shift : v / p.pa.page_size;
+}
+// Whether some row of the unit sees key v: the last one that lists its page, if any.
+__device__ __forceinline__ bool chosen_seen(const WindowParams& p, const Unit& u, int32_t v) {
+  const int32_t e = entry_of(p, v);
+  if (e >= u.s0) return false;
+  const PageEntry x = load_entry(unit_entries(p, u) + e);
+  return x.page * p.pa.page_size + (v - e * p.pa.page_size) <= u.p_first + 31 - __clz(x.rows);
+}
+
 // Equal shares: where a block's run of the units starts.  A unit counts as unit_cost for its beginning and end,
 // then its tiles (at least one in all); a share that ends inside the former takes nothing of the unit.
 struct Share {
@@ -276,11 +303,16 @@ struct Share {
   int32_t offset;      // where the share starts in it
 };
 // Worked out by all threads of the block; `scratch` has room for 34 int64.  Ends with a barrier.
-template <int THREADS>
+template <int THREADS, UnitSource SOURCE>
 __device__ __forceinline__ void find_share(const WindowParams& p, int64_t* scratch, Share* out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t heads = SOURCE == kWindowRows ? p.n_kvheads : 1;   // (listed units are of one head each)
   auto weight = [&](int32_t tile) -> int32_t {
     if (tile >= p.n_tiles) return 0;
+    if constexpr (SOURCE != kWindowRows) {
+      const int32_t t = p.unit_tiles[tile];
+      return t == -2 ? 0 : max(t + p.unit_cost, 1);
+    }
     int32_t lo = 0, hi = p.pa.n_requests - 1;             // the last request whose first tile is <= tile
     while (lo < hi) {
       const int32_t mid = (lo + hi + 1) >> 1;
@@ -308,7 +340,7 @@ __device__ __forceinline__ void find_share(const WindowParams& p, int64_t* scrat
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) total += scratch[w];
   __syncthreads();
-  const int64_t all = total * p.n_kvheads, even = (all + p.shares - 1) / p.shares;
+  const int64_t all = total * heads, even = (all + p.shares - 1) / p.shares;
   const int64_t size = even > p.unit_cost ? even : p.unit_cost + 1;   // every share inside a unit has tiles of it
   const int64_t from = size * blockIdx.x;
   if (from < all) {                                       // uniform over the block
@@ -436,7 +468,7 @@ __device__ __forceinline__ uint32_t e2m1_scaled(uint32_t w, int k, __half2 s) {
 
 }  // namespace window_detail
 
-template <int D, typename T, bool FP4>
+template <int D, typename T, bool FP4, UnitSource SOURCE>
 __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     window_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const __grid_constant__ CUtensorMap tmQ1, const __grid_constant__ CUtensorMap tmQT,
@@ -474,7 +506,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
   if ((base & 1023u) != 0) {   // the swizzle needs 1024-byte aligned tiles; uniform over the grid
     if (threadIdx.x == 0) {
       atomicCAS(status, 0, 0x100 | kWDrain);
-      if (p.shares > 0) p.joins[blockIdx.x] = JoinRecord{-1, 0, 0, 0, 0, 0, 0, 0};
+      if (SOURCE != kSharedPrefix && p.shares > 0) p.joins[blockIdx.x] = JoinRecord{-1, 0, 0, 0, 0, 0, 0, 0};
     }
     return;
   }
@@ -515,7 +547,8 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     prefetch_tmap(&tmQT);
   }
   Share* const share = reinterpret_cast<Share*>(smem + C::kShareAt);
-  if (p.shares > 0) find_share<C::kThreads>(p, reinterpret_cast<int64_t*>(smem + C::kMaxAt), share);
+  if constexpr (SOURCE != kWindowRows) pdl_wait();   // the units are written, and what came before them
+  if (p.shares > 0) find_share<C::kThreads, SOURCE>(p, reinterpret_cast<int64_t*>(smem + C::kMaxAt), share);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -541,6 +574,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
     const float sc = p.scale_log2;
     const float raise = kRaise / sc;
+    constexpr int kPart0 = SOURCE == kSharedPrefix ? 2 : 0;   // (see shared_unit)
     constexpr float kLift = FP4 || std::is_same<T, __half>::value ? kLiftFp16 : 0.0f;
     // (loops that run once a unit, or seldom, are not unrolled: their instructions would have to be fetched anew each
     // time)
@@ -560,7 +594,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       const int tok = row / p.group;
       const int32_t pos = u.p_first + tok;    // of this thread's row
       // positions this row sees: [row_lo, pos] and those below row_sink
-      int32_t row_lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+      int32_t row_lo = SOURCE == kSharedPrefix ? u.lo : p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
       int32_t row_sink = min(p.n_sink, pos + 1);
       if (pos < 0) {
         row_lo = INT32_MAX;
@@ -571,11 +605,20 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         const uint32_t jt = js + j, sb = jt & 1;
         const uint32_t tm_s = tmem + lanes + sb * 128 + wg * 64;
         const int32_t v0 = (u.tile0 + j) * kWinTile;
+        // chosen pages: those that this half of the tile lies in (at most 8: whole 8s of keys), one a lane
+        PageEntry mine{0, 0, 0, 0};
+        const int32_t e0 = SOURCE == kChosenPages ? entry_of(p, v0 + wg * 64) : 0;
+        if constexpr (SOURCE == kChosenPages) {
+          if (lane < 8 && e0 + lane < u.s0) mine = load_entry(unit_entries(p, u) + e0 + lane);
+        }
         bad |= !wait_done(eb + k_entry(j), kWSFull);
         tc_fence_after();
         const uint32_t* const holes = bad_keys + (jt % C::kBadSlots) * 8;
-        const uint4 h0 = *reinterpret_cast<const uint4*>(holes), h1 = *reinterpret_cast<const uint4*>(holes + 4);
-        const bool any_hole = (h0.x | h0.y | h0.z | h0.w | h1.x | h1.y | h1.z | h1.w) != 0;
+        bool any_hole = false;
+        if constexpr (SOURCE != kChosenPages) {
+          const uint4 h0 = *reinterpret_cast<const uint4*>(holes), h1 = *reinterpret_cast<const uint4*>(holes + 4);
+          any_hole = (h0.x | h0.y | h0.z | h0.w | h1.x | h1.y | h1.z | h1.w) != 0;
+        }
         if (warp_live) {
           float s[64];
           tmem_ld32(tm_s, s);
@@ -584,11 +627,25 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           if (j < u.all0 || j >= u.all1 || any_hole) {
             // the keys of this thread's half that its row sees, as bits
             const int32_t c0 = v0 + wg * 64;
-            const int32_t c_lo = row_lo == INT32_MAX ? 64 : max(max(row_lo - u.shift, u.s0) - c0, 0);
-            const int32_t c_hi = pos >= 0 ? min(min(pos, u.hi - 1) - u.shift - c0, 63) : -1;
-            const int32_t c_sink = min(min(row_sink, u.hi) - c0, 64);
-            uint64_t keep = c_sink >= 64 ? ~0ull : c_sink > 0 ? (1ull << c_sink) - 1 : 0ull;
-            if (c_lo <= c_hi) keep |= (~0ull >> (63 - c_hi)) & (~0ull << c_lo);
+            uint64_t keep = 0;
+            if constexpr (SOURCE == kChosenPages) {
+#pragma unroll 1
+              for (int i = 0; i < 8; ++i) {
+                const int32_t from = (e0 + i) * p.pa.page_size - c0;          // of the page's keys in this half
+                if (from >= 64 || e0 + i >= u.s0) break;
+                const int32_t page = __shfl_sync(0xffffffffu, mine.page, i);
+                const uint32_t rows = __shfl_sync(0xffffffffu, mine.rows, i);
+                const int32_t n = rows >> (tok & 31) & 1u ? min(pos + 1 - page * p.pa.page_size, p.pa.page_size) : 0;
+                const int32_t a = max(from, 0), b = min(from + n, 64);
+                if (b > a) keep |= (~0ull >> (64 - (b - a))) << a;
+              }
+            } else {
+              const int32_t c_lo = row_lo == INT32_MAX ? 64 : max(max(row_lo - u.shift, u.s0) - c0, 0);
+              const int32_t c_hi = pos >= 0 ? min(min(pos, u.hi - 1) - u.shift - c0, 63) : -1;
+              const int32_t c_sink = min(min(row_sink, u.hi) - c0, 64);
+              keep = c_sink >= 64 ? ~0ull : c_sink > 0 ? (1ull << c_sink) - 1 : 0ull;
+              if (c_lo <= c_hi) keep |= (~0ull >> (63 - c_hi)) & (~0ull << c_lo);
+            }
             if (any_hole) {
 #pragma unroll 1
               for (int c = 0; c < 64; ++c) {
@@ -708,12 +765,15 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
       if (store && wg == 0) {
         constexpr float kUnlift = kLift > 0.0f ? 0x1p-7f : 1.0f;
         const float lse = empty ? -INFINITY : m * sc * kLn2f + logf(l * kUnlift);
-        if (u.part >= 0) p.part_lse[u.part * kWinTile + row] = lse;
+        if (SOURCE == kSharedPrefix && u.part >= 0 && u.part < 2) p.first_lse[u.part * p.n_rows * p.n_qheads + rh] = lse;
+        else if (u.part >= 0) p.part_lse[(u.part - kPart0) * kWinTile + row] = lse;
         else if (p.lse) p.lse[rh] = lse;
       }
       const uint32_t tm_row = tm_o + lanes + wg * (D / 2);
       if (warp_live && u.part >= 0) {
-        float* const part = p.part_o + static_cast<int64_t>(u.part * kWinTile + row) * D + wg * (D / 2);
+        float* const part = (SOURCE == kSharedPrefix && u.part < 2
+                                 ? p.first_o + (u.part * p.n_rows * p.n_qheads + rh) * D
+                                 : p.part_o + static_cast<int64_t>((u.part - kPart0) * kWinTile + row) * D) + wg * (D / 2);
 #pragma unroll 1
         for (int c = 0; c < D / 2; c += 32) {
           if (u.tiles == 0) break;
@@ -907,7 +967,8 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           const uint32_t e = v_entry(j, u.tiles);
           for (int k = 0; k < kWinTile / 64; ++k) {
             const int row = k * 64 + (warp - 10) * 32 + lane;
-            if (seen(p, u, position_of(u, (u.tile0 + j) * kWinTile + row))) continue;
+            const int32_t v = (u.tile0 + j) * kWinTile + row;
+            if (SOURCE == kChosenPages ? chosen_seen(p, u, v) : seen(p, u, position_of(u, v))) continue;
 #pragma unroll
             for (int b = 0; b < D / 64; ++b) {
               const uint32_t st = (st0 + e * C::kSPT + b / C::kNBS) % C::kStages;
@@ -958,6 +1019,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     // whole units: number n of the call.  A request's later tiles see more keys where there is no window: they go
     // first, of all heads
     auto whole_unit = [&](uint32_t n) -> Unit {
+      if constexpr (SOURCE != kWindowRows) return listed_unit(p, p.n_tiles - 1 - static_cast<int32_t>(n));
       const uint32_t back = n / static_cast<uint32_t>(p.n_kvheads), kvh = n - back * static_cast<uint32_t>(p.n_kvheads);
       const int32_t tile = p.n_tiles - 1 - static_cast<int32_t>(back);
       Unit u = make_unit(p, tile_owner(p, tile, lane), tile);
@@ -969,13 +1031,22 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     int64_t at = p.shares > 0 ? sh.size * blockIdx.x : 0;
     bool first_unit = true;
     JoinRecord join{-1, 0, 0, 0, 0, 0, 0, 0};
+    // A unit's part goes to slot 2 block + {0, 1}, in the order in which the block has them.  Shared prompts: a row has
+    // results of two units to be joined, so whole units are parts too (u.part as listed: 0 the prompt's, 1 the
+    // request's own keys, by row and head, or -1 if there is but one), a first part goes to the same place, and one
+    // that continues a unit of an earlier block to slot 2 + block.
     auto shared_unit = [&]() -> Unit {
       Unit u{};
       u.tiles = -1;
-      while (sh.left > 0 && sh.kvh < p.n_kvheads) {
+      const int32_t heads = SOURCE == kWindowRows ? p.n_kvheads : 1;
+      while (sh.left > 0 && sh.kvh < heads) {
         const int32_t tile = sh.tile;
-        u = make_unit(p, tile_owner(p, tile, lane), tile);
-        u.kvh = sh.kvh;
+        if constexpr (SOURCE == kWindowRows) {
+          u = make_unit(p, tile_owner(p, tile, lane), tile);
+          u.kvh = sh.kvh;
+        } else {
+          u = listed_unit(p, tile);
+        }
         if (++sh.tile == p.n_tiles) {
           sh.tile = 0;
           ++sh.kvh;
@@ -999,7 +1070,15 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           u.tiles = -1;
           continue;
         }
-        if (u.tiles > 0 && b - a < u.tiles) {
+        if constexpr (SOURCE == kSharedPrefix) {
+          const bool goes_on = u.tiles > 0 && b < u.tiles;
+          if (a > 0) u.part = 2 + static_cast<int32_t>(blockIdx.x);
+          else if (goes_on && u.part < 0) u.part = 1;
+          if (a == 0 && lane == 0)
+            p.unit_joins[tile] = make_int2(static_cast<int32_t>(blockIdx.x),
+                                           goes_on ? static_cast<int32_t>((end - 1) / sh.size - blockIdx.x) : 0);
+          if (u.tiles > 0) cut(u, a, b);
+        } else if (u.tiles > 0 && b - a < u.tiles) {
           u.part = static_cast<int32_t>(2 * blockIdx.x) + (first_unit ? 0 : 1);
           if (a == 0) {         // its later parts are the first ones of the blocks that follow
             int64_t last = (end - 1) / sh.size;
@@ -1089,7 +1168,7 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
     }
     if (!FP4 && *abort_flag && qit > 0 && lane == 0) drain(b_qfull, (qit - 1) & 1, status, kDrainNs);
     __syncwarp();
-    if (warp == 9 && lane == 0 && p.shares > 0) p.joins[blockIdx.x] = join;
+    if (SOURCE != kSharedPrefix && warp == 9 && lane == 0 && p.shares > 0) p.joins[blockIdx.x] = join;
     if (warp == 9 && p.shares == 0 && (*abort_flag || p.stall_first_item)) {
       // the call is given up: blocks that have not started are taken off the grid, so that their waits do
       // not run out one after the other
@@ -1136,6 +1215,16 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
         Rows x{};
         if (!active) return x;
         const int32_t v = (u.tile0 + j) * kWinTile + kb;
+        if constexpr (SOURCE == kChosenPages) {
+          const int32_t e = entry_of(p, v);
+          if (e < u.s0) {
+            const PageEntry y = load_entry(unit_entries(p, u) + e);
+            const int32_t o = v - e * p.pa.page_size;
+            x.wanted = y.page * p.pa.page_size + o < u.p_first + u.tokens;
+            x.r[0] = y.id * p.pa.page_size + o;
+          }
+          return x;
+        }
         const int32_t pos = position_of(u, v);
         if (p.box > 0) {
           // a box is one run of positions inside one page
@@ -1395,12 +1484,12 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------- host side
-template <int D, typename T, bool FP4>
+template <int D, typename T, bool FP4, UnitSource SOURCE = kWindowRows>
 cudaError_t launch_window_instance(const WindowParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                    const CUtensorMap& tq1, const CUtensorMap& tqt, int grid, int which,
                                    cudaStream_t stream) {
   using C = WinCfg<D, FP4>;
-  auto kern = window_attention_kernel<D, T, FP4>;
+  auto kern = window_attention_kernel<D, T, FP4, SOURCE>;
   cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern), C::kSmem, kOptWindow + which);
   if (e != cudaSuccess) return e;
   // The warpgroups' register shares add up to kThreads x kLaunchRegs: a kernel compiled to fewer would wait
@@ -1410,8 +1499,22 @@ cudaError_t launch_window_instance(const WindowParams& p, const CUtensorMap& tk,
     return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
   }();
   if (regs < C::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  kern<<<grid, C::kThreads, C::kSmem, stream>>>(tk, tv, tq1, tqt, p);
-  return cudaGetLastError();
+  if constexpr (SOURCE == kWindowRows) {
+    kern<<<grid, C::kThreads, C::kSmem, stream>>>(tk, tv, tq1, tqt, p);
+    return cudaGetLastError();
+  } else {   // starts while the kernel that lists the units runs
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, tk, tv, tq1, tqt, p);
+  }
 }
 template <int D>
 cudaError_t launch_window_dim(const WindowParams& p, bool fp16, bool fp4, const CUtensorMap& tk,
@@ -1424,12 +1527,29 @@ cudaError_t launch_window_dim(const WindowParams& p, bool fp16, bool fp4, const 
   return fp16 ? launch_window_instance<D, __half, false>(p, tk, tv, tq1, tqt, grid, at + 2, stream)
               : launch_window_instance<D, __nv_bfloat16, false>(p, tk, tv, tq1, tqt, grid, at + 3, stream);
 }
-// one translation unit per head dim
+// Listed units.
+template <int D>
+cudaError_t launch_listed_dim(const WindowParams& p, bool fp16, bool prefix, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& tq1, const CUtensorMap& tqt, int grid, cudaStream_t stream) {
+  constexpr int at = D == 64 ? 12 : D == 128 ? 16 : 20;
+  if (prefix)
+    return fp16 ? launch_window_instance<D, __half, false, kSharedPrefix>(p, tk, tv, tq1, tqt, grid, at, stream)
+                : launch_window_instance<D, __nv_bfloat16, false, kSharedPrefix>(p, tk, tv, tq1, tqt, grid, at + 1, stream);
+  return fp16 ? launch_window_instance<D, __half, false, kChosenPages>(p, tk, tv, tq1, tqt, grid, at + 2, stream)
+              : launch_window_instance<D, __nv_bfloat16, false, kChosenPages>(p, tk, tv, tq1, tqt, grid, at + 3, stream);
+}
+// one translation unit per head dim, for each of the two kinds
 cudaError_t launch_window_d64(const WindowParams&, bool, bool, const CUtensorMap&, const CUtensorMap&,
                               const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
 cudaError_t launch_window_d128(const WindowParams&, bool, bool, const CUtensorMap&, const CUtensorMap&,
                                const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
 cudaError_t launch_window_d256(const WindowParams&, bool, bool, const CUtensorMap&, const CUtensorMap&,
+                               const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+cudaError_t launch_listed_d64(const WindowParams&, bool, bool, const CUtensorMap&, const CUtensorMap&,
+                               const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+cudaError_t launch_listed_d128(const WindowParams&, bool, bool, const CUtensorMap&, const CUtensorMap&,
+                               const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+cudaError_t launch_listed_d256(const WindowParams&, bool, bool, const CUtensorMap&, const CUtensorMap&,
                                const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
 
 }  // namespace qsa
