@@ -15,37 +15,13 @@
 #include "choose.cuh"
 #include "internal.h"
 #include "paged.cuh"
+#include "ptx.cuh"
 
 namespace qsa {
 namespace {
 
-template <typename T>
-struct Pair;
-template <>
-struct Pair<__nv_bfloat16> {
-  using type = __nv_bfloat162;
-};
-template <>
-struct Pair<__half> {
-  using type = __half2;
-};
-// (NaN stays)
-template <typename T, bool MAX>
-__device__ __forceinline__ uint32_t best2(uint32_t a, uint32_t b) {
-  typename Pair<T>::type x, y;
-  memcpy(&x, &a, 4);
-  memcpy(&y, &b, 4);
-  x = MAX ? __hmax2_nan(x, y) : __hmin2_nan(x, y);
-  memcpy(&a, &x, 4);
-  return a;
-}
-template <typename T>
-__device__ __forceinline__ float2 floats_of(uint32_t a) {
-  typename Pair<T>::type x;
-  memcpy(&x, &a, 4);
-  if constexpr (std::is_same<T, __half>::value) return __half22float2(x);
-  else return __bfloat1622float2(x);
-}
+using choose::best2;
+using choose::floats_of;
 
 // ---------------------------------------------------------------------------- bounds
 constexpr int kBoundsThreads = 256;
@@ -171,79 +147,81 @@ __device__ __forceinline__ double exact_score(const T* q, const T* bounds, int g
   return nan ? __longlong_as_double(0x7ff8000000000000ll) : best;
 }
 
+// A team of threads takes a row and KV head: a warp where there are many, else a block.
 constexpr int kChooseThreads = 256;
-
-// One block a row and KV head.
-template <int D, typename T>
+constexpr int kWarpChoosePages = 2048;      // whose keys a warp holds (eight warps: 64 KB)
+template <int D, typename T, int TEAM>
 __global__ void __launch_bounds__(kChooseThreads) page_select_kernel(const __grid_constant__ ChooseParams p) {
   using namespace choose;
-  extern __shared__ uint32_t keys[];
+  extern __shared__ uint32_t key_arrays[];
   __shared__ uint32_t scratch[Team<kChooseThreads>::kScratch];
-  Team<kChooseThreads> team(scratch);
-  const int lane = team.lane, warp = team.warp;
-  const int64_t row = blockIdx.x / p.n_kvheads;
-  const int32_t kvh = static_cast<int32_t>(blockIdx.x - row * p.n_kvheads);
-  if (row >= __ldg(p.pa.cu_seqlens_q + p.pa.n_requests)) return;
+  pdl_wait();
+  constexpr int kTeams = kChooseThreads / TEAM;
+  Team<TEAM> team(scratch);
+  const int lane = team.lane, in_block = TEAM == 32 ? threadIdx.x >> 5 : 0, tid = TEAM == 32 ? lane : threadIdx.x;
+  uint32_t* const keys = key_arrays + static_cast<int64_t>(in_block) * p.pa.pages_per_req;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kTeams + in_block, row = item / p.n_kvheads;
+  const int32_t kvh = static_cast<int32_t>(item - row * p.n_kvheads);
+  if (row >= p.n_rows || row >= __ldg(p.pa.cu_seqlens_q + p.pa.n_requests)) return;
   const int32_t req = paged_request_of_row(p.pa, row, lane);
   const int64_t pos = static_cast<int64_t>(__ldg(p.pa.kv_lens + req)) - __ldg(p.pa.cu_seqlens_q + req + 1) + row;
-  int32_t* const out = p.out + static_cast<int64_t>(blockIdx.x) * p.n_select;
+  int32_t* const out = p.out + item * p.n_select;
   const int64_t mine = pos < 0 ? -1 : pos / p.pa.page_size;
   const int32_t n = static_cast<int32_t>(mine + 1 < p.pa.pages_per_req ? mine + 1 : p.pa.pages_per_req);
+  const int32_t* const table = p.pa.page_table + static_cast<int64_t>(req) * p.pa.pages_per_req;
+  if (n <= p.n_select) {                                   // every page that exists (no scores have been taken)
+    for (int32_t e = tid; e < n; e += TEAM) {
+      const int32_t page = __ldg(table + e);
+      keys[e] = page >= 0 && page < p.pa.n_pages ? kChosen : 0u;
+    }
+    team.sync();
+    emit(team, keys, n, 0u, 0u, p.n_select, out);
+    return;
+  }
+  const uint4* const src = reinterpret_cast<const uint4*>(p.keys + item * p.key_stride);
+  for (int32_t e = tid * 4; e < n; e += TEAM * 4) {
+    const uint4 x = __ldg(src + e / 4);
+    const uint32_t k[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e + i < n) keys[e + i] = k[i] != 0 && (e + i < p.n_first || e + i > mine - p.n_last) ? kChosen : k[i];
+  }
+  // (bits of non-negative floats have their order, NaN above all)
+  uint32_t most = 0;
+  const float* const largest = p.largest + (static_cast<int64_t>(req) * p.n_kvheads + kvh) * p.page_tiles;
+  for (int32_t i = lane; i * kScoreTile < n; i += 32) most = max(most, __float_as_uint(__ldg(largest + i)));
+  const float reach = __ldg(p.reach + item) * __uint_as_float(__reduce_max_sync(0xffffffffu, most));
+  const float eps = reach < 0x1p126f ? reach * kScoreError : INFINITY;
+  team.sync();
   const T* const q = static_cast<const T*>(p.q) + (row * p.n_qheads + static_cast<int64_t>(kvh) * p.group) * D;
   const T* const bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(kvh) * 2 * D;
-  const int32_t* const table = p.pa.page_table + static_cast<int64_t>(req) * p.pa.pages_per_req;
-  constexpr int kPer = D / 32;
-  uint32_t largest = 0;                                    // |q| summed, the largest bound: as bits
-  float reach = 0.0f;
-  for (int h = warp; h < p.group; h += Team<kChooseThreads>::kWarps) {
-    float s = 0.0f;
-    for (int c = 0; c < kPer; ++c) s += fabsf(static_cast<float>(q[static_cast<int64_t>(h) * D + lane * kPer + c]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    reach = s > reach || s != s ? s : reach;
-  }
-  for (int32_t e = warp; e < n; e += Team<kChooseThreads>::kWarps) {
-    const int32_t page = __ldg(table + e);
-    uint32_t key = 0;
-    if (page >= 0 && page < p.pa.n_pages) {
-      const T* const b = bounds + static_cast<int64_t>(page) * p.n_kvheads * 2 * D;
-      float best = -INFINITY;
-      bool nan = false;
-      for (int h = 0; h < p.group; ++h) {
-        float s = 0.0f;
-#pragma unroll
-        for (int c = 0; c < kPer; ++c) {
-          const int d = lane * kPer + c;
-          const float x = static_cast<float>(q[static_cast<int64_t>(h) * D + d]);
-          const float lo = static_cast<float>(b[d]), hi = static_cast<float>(b[D + d]);
-          s += x * (x > 0.0f ? hi : lo);
-          largest = max(largest, max(__float_as_uint(lo) & 0x7fffffffu, __float_as_uint(hi) & 0x7fffffffu));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        nan |= s != s;
-        best = fmaxf(best, s);
-      }
-      key = e < p.n_first || e > mine - p.n_last ? kChosen : nan ? kNan : key_of(best);
-    }
-    if (lane == 0) keys[e] = key;
-  }
-  __syncthreads();
-  // (bits of non-negative floats have their order, NaN above all)
-  reach = __uint_as_float(team.max(__float_as_uint(reach))) * __uint_as_float(team.max(largest));
-  const float eps = reach < 0x1p126f ? reach * kScoreError : INFINITY;
   choose::choose(team, keys, n, p.n_select, eps,
                  [&](int32_t e) { return exact_score<D>(q, bounds + static_cast<int64_t>(__ldg(table + e)) * p.n_kvheads * 2 * D, p.group, lane); },
                  out);
 }
 
-template <int D, typename T>
-cudaError_t launch_select_dim(const ChooseParams& p, cudaStream_t stream, int which) {
-  auto kern = page_select_kernel<D, T>;
-  const cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern), kMaxChoosePages * 4, kOptChoose + which);
+template <int D, typename T, int TEAM>
+cudaError_t launch_select_team(const ChooseParams& p, int which, cudaStream_t stream) {
+  auto kern = page_select_kernel<D, T, TEAM>;
+  constexpr int kTeams = kChooseThreads / TEAM;
+  const cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern),
+                                    4 * (TEAM == 32 ? kTeams * kWarpChoosePages : kMaxChoosePages), kOptChoose + which);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(p.n_rows * p.n_kvheads), kChooseThreads, static_cast<size_t>(p.pa.pages_per_req) * 4, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // starts while the scores are taken
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>((p.n_rows * p.n_kvheads + kTeams - 1) / kTeams));
+  cfg.blockDim = dim3(kChooseThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(kTeams) * p.pa.pages_per_req * 4;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+template <int D, typename T>
+cudaError_t launch_select_dim(const ChooseParams& p, int which, bool warps, cudaStream_t stream) {
+  return warps ? launch_select_team<D, T, 32>(p, which, stream) : launch_select_team<D, T, kChooseThreads>(p, which + 1, stream);
 }
 
 }  // namespace
@@ -263,14 +241,17 @@ cudaError_t launch_page_bounds(const BoundsParams& p, bool fp16, int num_sms, cu
                              : go(page_bounds_kernel<256, __nv_bfloat16>);
 }
 
-cudaError_t launch_page_select(const ChooseParams& p, bool fp16, cudaStream_t stream) {
+cudaError_t launch_page_select(const ChooseParams& p, bool fp16, int num_sms, cudaStream_t stream) {
+  const cudaError_t e = launch_page_score(p, fp16, num_sms, stream);
+  if (e != cudaSuccess) return e;
+  const bool warps = p.n_rows * p.n_kvheads >= 32 * static_cast<int64_t>(num_sms) && p.pa.pages_per_req <= kWarpChoosePages;
   if (fp16)
-    return p.head_dim == 64    ? launch_select_dim<64, __half>(p, stream, 0)
-           : p.head_dim == 128 ? launch_select_dim<128, __half>(p, stream, 1)
-                               : launch_select_dim<256, __half>(p, stream, 2);
-  return p.head_dim == 64    ? launch_select_dim<64, __nv_bfloat16>(p, stream, 3)
-         : p.head_dim == 128 ? launch_select_dim<128, __nv_bfloat16>(p, stream, 4)
-                             : launch_select_dim<256, __nv_bfloat16>(p, stream, 5);
+    return p.head_dim == 64    ? launch_select_dim<64, __half>(p, 0, warps, stream)
+           : p.head_dim == 128 ? launch_select_dim<128, __half>(p, 2, warps, stream)
+                               : launch_select_dim<256, __half>(p, 4, warps, stream);
+  return p.head_dim == 64    ? launch_select_dim<64, __nv_bfloat16>(p, 6, warps, stream)
+         : p.head_dim == 128 ? launch_select_dim<128, __nv_bfloat16>(p, 8, warps, stream)
+                             : launch_select_dim<256, __nv_bfloat16>(p, 10, warps, stream);
 }
 
 }  // namespace qsa

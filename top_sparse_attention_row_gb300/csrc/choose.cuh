@@ -11,10 +11,43 @@
 // steps, their upper and their lower halves, so that they need no more room than the keys, however many there are.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
 #include <cstdint>
+#include <cstring>
+#include <type_traits>
 
 namespace qsa {
 namespace choose {
+
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+};
+template <>
+struct Pair<__half> {
+  using type = __half2;
+};
+// (NaN stays)
+template <typename T, bool MAX>
+__device__ __forceinline__ uint32_t best2(uint32_t a, uint32_t b) {
+  typename Pair<T>::type x, y;
+  memcpy(&x, &a, 4);
+  memcpy(&y, &b, 4);
+  x = MAX ? __hmax2_nan(x, y) : __hmin2_nan(x, y);
+  memcpy(&a, &x, 4);
+  return a;
+}
+template <typename T>
+__device__ __forceinline__ float2 floats_of(uint32_t a) {
+  typename Pair<T>::type x;
+  memcpy(&x, &a, 4);
+  if constexpr (std::is_same<T, __half>::value) return __half22float2(x);
+  else return __bfloat1622float2(x);
+}
 
 constexpr uint32_t kChosen = 0xffffffffu;
 constexpr uint32_t kNan = 0xfffffffeu;      // a score that is NaN stands above all others

@@ -422,6 +422,7 @@ struct BoundsParams {
 };
 cudaError_t launch_page_bounds(const BoundsParams& p, bool fp16, int num_sms, cudaStream_t stream);
 constexpr int kMaxChoosePages = 32768;       // of a request
+constexpr int kScoreTile = 128;              // pages of an MMA tile, and rows of the query tile
 struct ChooseParams {
   const void* q;                // [n_rows, n_qheads, D]
   const void* bounds;
@@ -430,13 +431,27 @@ struct ChooseParams {
   int64_t n_rows;
   int32_t n_qheads, n_kvheads, group, head_dim;
   int32_t n_select, n_first, n_last;
+  // scores (score.cu)
+  uint32_t* keys;               // [n_rows, n_kvheads, key_stride]: keys of the pages' scores
+  float* reach;                 // [n_rows, n_kvheads]: largest sum of |q| over the heads
+  float* largest;               // [n_requests, n_kvheads, page_tiles]: largest |bound| of every tile of pages
+  int64_t n_items;              // query tiles x KV heads x runs
+  int32_t key_stride;           // page_tiles * kScoreTile
+  int32_t page_tiles;           // of pages_per_req
+  int32_t head_rows;            // rows of a token in the query tile: the heads rounded up to a power of two
+  int32_t tile_tokens;          // kScoreTile / head_rows
+  int32_t runs, run_tiles;      // of a query tile's pages: runs of so many tiles
+  int32_t stall_first_item;
+  int32_t* status;
+  unsigned long long wait_ns;
 };
-cudaError_t launch_page_select(const ChooseParams& p, bool fp16, cudaStream_t stream);
+cudaError_t launch_page_score(const ChooseParams& p, bool fp16, int num_sms, cudaStream_t stream);
+cudaError_t launch_page_select(const ChooseParams& p, bool fp16, int num_sms, cudaStream_t stream);
 
 // Dynamic shared-memory opt-in of a kernel to `bytes`, its largest use, once per device and kernel (so
 // calls made during a graph capture only enqueue).
-enum OptInKernel { kOptPlan, kOptWindow, kOptChoose = kOptWindow + 24, kOptListPages = kOptChoose + 6,
-                    kOptCount = kOptListPages + 1 };
+enum OptInKernel { kOptPlan, kOptWindow, kOptChoose = kOptWindow + 24, kOptScore = kOptChoose + 12,
+                    kOptListPages = kOptScore + 6, kOptCount = kOptListPages + 1 };
 cudaError_t smem_opt_in(const void* kernel, int bytes, int which);
 
 // Host helpers of api.cpp for the other units' entry points.

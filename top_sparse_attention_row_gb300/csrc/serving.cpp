@@ -284,6 +284,30 @@ qsa_status run_window(const void* q, const void* k_cache, const void* v_cache, c
   return QSA_OK;
 }
 
+qsa_status check_select(int64_t n_rows, int32_t n_requests, int32_t pages_per_req, int32_t page_size, int64_t n_pages,
+                        int32_t n_qheads, int32_t n_kvheads, int32_t head_dim) {
+  const qsa_status st = check_window(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim,
+                                     0, 0, false);
+  if (st != QSA_OK) return st;
+  // (page ids times KV heads, and one row more, are the gathers' coordinates)
+  if (pages_per_req > qsa::kMaxChoosePages || n_rows > INT32_MAX / n_kvheads) return QSA_ERR_UNSUPPORTED;
+  return QSA_OK;
+}
+struct ScorePlan {
+  int32_t page_tiles;
+  size_t reach_at, largest_at, bytes;
+};
+size_t round_256(size_t n) { return (n + 255) / 256 * 256; }
+ScorePlan plan_scores(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, int32_t pages_per_req) {
+  ScorePlan s{};
+  s.page_tiles = (pages_per_req + qsa::kScoreTile - 1) / qsa::kScoreTile;
+  const size_t rows = static_cast<size_t>(n_rows) * n_kvheads;
+  s.reach_at = rows * s.page_tiles * qsa::kScoreTile * 4;
+  s.largest_at = s.reach_at + round_256(rows * 4);
+  s.bytes = s.largest_at + round_256(static_cast<size_t>(n_requests) * n_kvheads * s.page_tiles * 4);
+  return s;
+}
+
 qsa_status check_selected(int64_t n_rows, int32_t n_requests, int32_t pages_per_req, int32_t page_size, int64_t n_pages,
                           int32_t n_qheads, int32_t n_kvheads, int32_t head_dim) {
   const qsa_status st = check_window(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim,
@@ -299,7 +323,6 @@ struct ListedPlan {
   size_t tiles_at, joins_at, own_at, entries_at, first_at, parts_at, bytes;
 };
 constexpr size_t kUnitBytes = 64;
-size_t round_256(size_t n) { return (n + 255) / 256 * 256; }
 void lay_out(ListedPlan* l, int32_t head_dim, size_t unit_joins, size_t own, size_t entries, size_t first_rows,
              size_t part_bytes) {
   const size_t n = static_cast<size_t>(l->w.n_tiles);
@@ -481,7 +504,8 @@ qsa_status qsa_page_bounds(const void* k_cache, const int32_t* cu_seqlens_q, con
 
 size_t qsa_page_select_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t pages_per_req, int32_t n_qheads,
                                        int32_t n_kvheads, int32_t head_dim) {
-  return 0;
+  if (check_select(n_rows, n_requests, pages_per_req, 1, 1, n_qheads, n_kvheads, head_dim) != QSA_OK || n_rows == 0) return 0;
+  return plan_scores(n_rows, n_requests, n_kvheads, pages_per_req).bytes;
 }
 
 qsa_status qsa_page_select(const void* q, const void* bounds, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
@@ -495,11 +519,12 @@ qsa_status qsa_page_select(const void* q, const void* bounds, const int32_t* cu_
     return QSA_ERR_INVALID_ARG;
   if (n_first < 0 || n_last < 1 || n_select < 1 || static_cast<int64_t>(n_first) + n_last > n_select)
     return QSA_ERR_INVALID_ARG;
-  qsa_status st = check_window(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim, 0, 0,
-                               false);
+  qsa_status st = check_select(n_rows, n_requests, pages_per_req, page_size, n_pages, n_qheads, n_kvheads, head_dim);
   if (st != QSA_OK) return st;
-  if (pages_per_req > qsa::kMaxChoosePages || n_rows > INT32_MAX / n_kvheads) return QSA_ERR_UNSUPPORTED;
   if (n_rows == 0) return QSA_OK;
+  int32_t sms = 0;
+  st = qsa::device_sms(&sms);
+  if (st != QSA_OK) return st;
   qsa::ChooseParams p{};
   p.q = q;
   p.bounds = bounds;
@@ -513,9 +538,37 @@ qsa_status qsa_page_select(const void* q, const void* bounds, const int32_t* cu_
   p.n_select = n_select;
   p.n_first = n_first;
   p.n_last = n_last;
-  if (qsa::launch_page_select(p, dtype == QSA_FP16, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return QSA_ERR_CUDA;
-  qsa::count_launches(1);
+  const ScorePlan plan = plan_scores(n_rows, n_requests, n_kvheads, pages_per_req);
+  p.page_tiles = plan.page_tiles;
+  p.key_stride = plan.page_tiles * qsa::kScoreTile;
+  p.head_rows = 1;
+  while (p.head_rows < p.group) p.head_rows *= 2;
+  p.tile_tokens = qsa::kScoreTile / p.head_rows;
+  // A run is as many of a query tile's page tiles as leave every SM a dozen items: long runs split the queries less often,
+  // short ones spread few query tiles over the SMs.
+  const int64_t units = (n_rows / p.tile_tokens + n_requests) * n_kvheads, each = units * plan.page_tiles / (sms * int64_t{12});
+  p.run_tiles = each < 1 ? 1 : each < plan.page_tiles ? static_cast<int32_t>(each) : plan.page_tiles;
+  p.runs = (plan.page_tiles + p.run_tiles - 1) / p.run_tiles;
+  p.n_items = units * p.runs;
+  p.wait_ns = qsa::kWinWaitNs + qsa::kWinWaitNsPerTile * static_cast<unsigned long long>(p.run_tiles);
+  if (qsa::device_status_address(&p.status) != cudaSuccess) return QSA_ERR_CUDA;
+  void* ws = workspace;
+  const bool own = !ws;
+  cudaStream_t on = static_cast<cudaStream_t>(stream);
+  if (own) {
+    if (qsa::ws_alloc(&ws, plan.bytes, on) != cudaSuccess) return QSA_ERR_CUDA;
+  } else if (workspace_bytes < plan.bytes || !aligned_to(ws, 256)) {
+    return QSA_ERR_WORKSPACE;
+  }
+  uint8_t* const b = static_cast<uint8_t*>(ws);
+  p.keys = reinterpret_cast<uint32_t*>(b);
+  p.reach = reinterpret_cast<float*>(b + plan.reach_at);
+  p.largest = reinterpret_cast<float*>(b + plan.largest_at);
+  p.stall_first_item = qsa::take_stall_request() ? 1 : 0;
+  const cudaError_t e = qsa::launch_page_select(p, dtype == QSA_FP16, sms, on);
+  if (own) cudaFreeAsync(ws, on);
+  if (e != cudaSuccess) return QSA_ERR_CUDA;
+  qsa::count_launches(2);
   return QSA_OK;
 }
 

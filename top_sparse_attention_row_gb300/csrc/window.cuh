@@ -133,9 +133,10 @@ __device__ __forceinline__ unsigned long long now_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Bounded wait for phase `parity` of a barrier.  False on timeout or abort.
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                         const WindowParams& p, int32_t site) {
+// Bounded wait for phase `parity` of a barrier.  False on timeout or abort.  (P: a kernel's parameters, with the limit
+// and the status word.)
+template <typename P>
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, const P& p, int32_t site) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = now_ns();
   while (true) {
