@@ -484,8 +484,9 @@ qsa_status qsa_page_bounds(const void* k_cache, const int32_t* cu_seqlens_q, con
  * others the ones with the highest scores,
  *   score = max over the query heads of the KV head of  sum_d max(q_d lo_d, q_d hi_d),
  * ties going to the lower page, up to n_select in all.  The sum is the most that q.k can be for a key of the page.
- * What is chosen does not depend on roundings: scores are compared as their values in 64-bit arithmetic are (those that
- * agree in all of their bits but the last count as equal).  A NaN score stands above all others.
+ * What is chosen does not depend on the roundings of 32-bit sums: where these cannot part the scores next to the last
+ * place, the scores are summed anew with an error below 2^-44 of the sum of their products' magnitudes (in 64 bits where
+ * sums leave fp32's range).  A NaN score stands above all others.
  *   q [n_rows, n_qheads, head_dim], bounds as qsa_page_bounds writes them, of type dtype
  *   pages [n_rows, n_kvheads, n_select] int32: the chosen pages of the request's table (not page ids) in increasing
  *         order, then -1.  Rows behind cu_seqlens_q[n_requests] are left as they were.

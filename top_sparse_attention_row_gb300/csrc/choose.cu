@@ -111,9 +111,19 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const __gri
 // the magnitudes, which is at most the sum of |q| times the largest bound.
 constexpr float kScoreError = 0x1p-16f;
 
-// Exact score of a page for `group` heads (whole warps): each lane takes D / 32 dims.
+// s + x as the nearest float and what is left of it (Knuth's two-sum): exact.
+__device__ __forceinline__ float two_sum(float s, float x, float* rest) {
+  const float t = s + x, z = t - s;
+  *rest = (s - (t - z)) + (x - z);
+  return t;
+}
+
+// The key of a page's score for `group` heads, to compare scores that fp32 sums cannot part (by whole warps; each lane takes
+// D / 32 dims).  A product of two 16-bit values is exact in fp32; sums are kept in two floats, whose error is below 2^-44
+// of the sum of the magnitudes.  Doubles would do too, but this GPU adds few of them (two a cycle and SM: 230 us of 468
+// for 8192 prompt rows), so they are left to scores that floats cannot hold (`wide`).
 template <int D, typename T>
-__device__ __forceinline__ double exact_score(const T* q, const T* bounds, int group, int lane) {
+__device__ __forceinline__ uint64_t exact_key(const T* q, const T* bounds, int group, int lane, bool wide) {
   constexpr int kPer = D / 32;
   float lo[kPer], hi[kPer];
 #pragma unroll
@@ -127,24 +137,44 @@ __device__ __forceinline__ double exact_score(const T* q, const T* bounds, int g
     hi[c] = y.x;
     hi[c + 1] = y.y;
   }
-  double best = -INFINITY;
-  bool nan = false;
+  uint64_t best = 0;
   for (int h = 0; h < group; ++h) {
-    double s = 0.0;
+    float x[kPer];
 #pragma unroll
     for (int c = 0; c < kPer; c += 2) {
       uint32_t a;
       memcpy(&a, q + static_cast<int64_t>(h) * D + lane * kPer + c, 4);
-      const float2 x = floats_of<T>(a);
-      s += static_cast<double>(x.x) * (x.x > 0.0f ? hi[c] : lo[c]);
-      s += static_cast<double>(x.y) * (x.y > 0.0f ? hi[c + 1] : lo[c + 1]);
+      const float2 y = floats_of<T>(a);
+      x[c] = y.x;
+      x[c + 1] = y.y;
     }
+    uint64_t key;
+    if (!wide) {
+      float s = 0.0f, rest = 0.0f, r;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    nan |= s != s;
-    best = s > best ? s : best;
+      for (int c = 0; c < kPer; ++c) {
+        s = two_sum(s, __fmul_rn(x[c], x[c] > 0.0f ? hi[c] : lo[c]), &r);
+        rest += r;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        s = two_sum(s, __shfl_xor_sync(0xffffffffu, s, o), &r);
+        rest += __shfl_xor_sync(0xffffffffu, rest, o);
+        rest += r;
+      }
+      s = two_sum(s, rest, &r);
+      key = choose::key_of(s, r);
+    } else {
+      double s = 0.0;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) s += static_cast<double>(x[c]) * (x[c] > 0.0f ? hi[c] : lo[c]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      key = choose::key_of(s);
+    }
+    best = key > best ? key : best;
   }
-  return nan ? __longlong_as_double(0x7ff8000000000000ll) : best;
+  return best;
 }
 
 // A team of threads takes a row and KV head: a warp where there are many, else a block.
@@ -190,13 +220,19 @@ __global__ void __launch_bounds__(kChooseThreads) page_select_kernel(const __gri
   uint32_t most = 0;
   const float* const largest = p.largest + (static_cast<int64_t>(req) * p.n_kvheads + kvh) * p.page_tiles;
   for (int32_t i = lane; i * kScoreTile < n; i += 32) most = max(most, __float_as_uint(__ldg(largest + i)));
-  const float reach = __ldg(p.reach + item) * __uint_as_float(__reduce_max_sync(0xffffffffu, most));
-  const float eps = reach < 0x1p126f ? reach * kScoreError : INFINITY;
+  const float q_sum = __ldg(p.reach + item), bound = __uint_as_float(__reduce_max_sync(0xffffffffu, most));
+  const float reach = q_sum * bound;
+  // beyond these, sums overflow or products lose bits in fp32 (NaN fails all comparisons)
+  const bool wide = !(reach < 0x1p126f && reach > 0x1p-80f && q_sum > 0x1p-100f && bound > 0x1p-100f);
+  const float eps = q_sum == 0.0f || bound == 0.0f ? 0.0f : wide ? INFINITY : reach * kScoreError;
   team.sync();
   const T* const q = static_cast<const T*>(p.q) + (row * p.n_qheads + static_cast<int64_t>(kvh) * p.group) * D;
   const T* const bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(kvh) * 2 * D;
   choose::choose(team, keys, n, p.n_select, eps,
-                 [&](int32_t e) { return exact_score<D>(q, bounds + static_cast<int64_t>(__ldg(table + e)) * p.n_kvheads * 2 * D, p.group, lane); },
+                 [&](int32_t e) {
+                   return exact_key<D>(q, bounds + static_cast<int64_t>(__ldg(table + e)) * p.n_kvheads * 2 * D, p.group,
+                                       lane, wide);
+                 },
                  out);
 }
 

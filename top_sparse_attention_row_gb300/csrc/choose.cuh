@@ -3,7 +3,7 @@
 // Scores come in fp32 with an error of at most eps each.  Let t be the k-th largest of them.  The k-th largest exact
 // score is then within eps of t, so an entry above t + 2 eps belongs to the k best and one below t - 2 eps does not;
 // where the entries between are more than the places left, their exact scores (64 bits) decide, equal ones by their
-// place in the list.
+// place in the list.  (eps = 0: scores that are equal are so exactly.)
 //
 // Scores are held as unsigned keys that have their order, 0 for entries that cannot be chosen and kChosen for those
 // that are in any case.  The k-th key is found by halving the range of keys and counting; the search ends as soon as a
@@ -59,6 +59,10 @@ __device__ __forceinline__ uint32_t key_of(float s) {
 }
 __device__ __forceinline__ float score_of(uint32_t key) {
   return __uint_as_float(key >> 31 ? key & 0x7fffffffu : ~key);
+}
+// A score in two floats, hi + lo with hi the nearest float: ordered like (hi, lo).
+__device__ __forceinline__ uint64_t key_of(float hi, float lo) {
+  return static_cast<uint64_t>(key_of(hi)) << 32 | key_of(lo);
 }
 __device__ __forceinline__ uint64_t key_of(double s) {
   if (s != s) return static_cast<uint64_t>(kNan) << 32;
@@ -191,7 +195,7 @@ __device__ __forceinline__ void emit(Team<THREADS>& t, const uint32_t* keys, int
 }
 
 // Chooses the k best of keys [n] (shared memory, changed by the call) and writes their places in order, then -1.
-// exact(i), called by whole warps, is entry i's score in 64 bits.
+// exact(i), called by whole warps, is the 64-bit key of entry i's score.
 template <int THREADS, typename Exact>
 __device__ __forceinline__ void choose(Team<THREADS>& t, uint32_t* keys, int32_t n, int32_t k, float eps, Exact exact,
                                        int32_t* out) {
@@ -217,6 +221,10 @@ __device__ __forceinline__ void choose(Team<THREADS>& t, uint32_t* keys, int32_t
     emit(t, keys, n, lo - 1u, 0u, k, out);
     return;
   }
+  if (eps == 0.0f) {                                       // they are equal
+    emit(t, keys, n, bar, want - sure, k, out);
+    return;
+  }
   const Run<THREADS> run(t, n);
   t.sync();                                                // the keys have been read by all
   for (int32_t i = run.from; i < run.to; i += 32) {
@@ -224,8 +232,8 @@ __device__ __forceinline__ void choose(Team<THREADS>& t, uint32_t* keys, int32_t
     uint32_t y = x > hi ? kChosen : 0u;
     for (uint32_t m = __ballot_sync(0xffffffffu, x >= lo && x <= hi); m; m &= m - 1) {
       const int j = __ffs(m) - 1;
-      const double v = exact(i + j);
-      if (t.lane == j) y = static_cast<uint32_t>(key_of(v) >> 32);
+      const uint64_t v = exact(i + j);
+      if (t.lane == j) y = static_cast<uint32_t>(v >> 32);
     }
     if (i + t.lane < run.to) keys[i + t.lane] = y;
   }
@@ -242,9 +250,9 @@ __device__ __forceinline__ void choose(Team<THREADS>& t, uint32_t* keys, int32_t
     uint32_t y = x > upper ? kChosen : 0u;
     for (uint32_t m = __ballot_sync(0xffffffffu, x == upper && i + t.lane < run.to); m; m &= m - 1) {
       const int j = __ffs(m) - 1;
-      const double v = exact(i + j);
+      const uint64_t v = exact(i + j);
       // (0 and kChosen stay free: the last of the 64 bits is left out)
-      if (t.lane == j) y = 1u + (static_cast<uint32_t>(key_of(v)) >> 1);
+      if (t.lane == j) y = 1u + (static_cast<uint32_t>(v) >> 1);
     }
     if (i + t.lane < run.to) keys[i + t.lane] = y;
   }

@@ -101,14 +101,22 @@ __device__ __forceinline__ void max_over_heads(float (&v)[32], int lane) {
     }
   }
 }
-__device__ __forceinline__ bool page_here(const uint32_t* here, int col) { return here[col & 3] >> (col >> 2) & 1u; }
-
-// Keys of a lane's columns, to the keys of its token's row (16-byte aligned for 4 columns and more).
+// Keys of a lane's N columns from col on (a multiple of N), to the keys of its token's row.  here: bit c of word k is
+// whether the page of column 4 c + k exists.
 template <int N>
-__device__ __forceinline__ void store_keys(const float* v, const uint32_t* here, int col, uint32_t* to) {
+__device__ __forceinline__ void store_keys(const float* v, const uint4& here, int col, uint32_t* to) {
   uint32_t k[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) k[i] = page_here(here, col + i) ? choose::key_of(v[i]) : 0u;
+  for (int i = 0; i < N; ++i) {
+    uint32_t word;
+    if constexpr (N >= 4) {
+      word = i % 4 == 0 ? here.x : i % 4 == 1 ? here.y : i % 4 == 2 ? here.z : here.w;
+    } else {
+      const int w = (col + i) & 3;
+      word = w == 0 ? here.x : w == 1 ? here.y : w == 2 ? here.z : here.w;
+    }
+    k[i] = word >> ((col + i) >> 2) & 1u ? choose::key_of(v[i]) : 0u;
+  }
   if constexpr (N >= 4) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4*>(to + i) = make_uint4(k[i], k[i + 1], k[i + 2], k[i + 3]);
@@ -201,14 +209,16 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
       const bool more = next(it, x);
       if (named_bar_any(1, 256, !more || bad)) break;      // all leave together
       const bool live = head < p.group && tok < x.tokens;
+      const bool warp_live = quarter * 32 / p.head_rows < x.tokens;   // (else the warp's rows are not looked at)
       // the queries: this warpgroup's half of the columns, min(q, 0) or max(q, 0)
       bad |= !wait(b_qfull, it, kPQFull);
       if (it > 0) bad |= !wait(b_adone, it - 1, kPADone);
       tc_fence_after();
       float sum = 0.0f;
       const int src = tok * p.group + head;
+      // (the sum of |q| is shared between the halves: the even and the odd blocks; one block: its even and odd words)
 #pragma unroll 1
-      for (int b = 0; b < C::kQBlocks; ++b) {
+      for (int b = 0; b < C::kQBlocks && warp_live; ++b) {
         uint32_t v[32];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -219,14 +229,19 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
           v[4 * c + 2] = y.z;
           v[4 * c + 3] = y.w;
         }
+        if (C::kQBlocks == 1 || (b & 1) == wg) {
+          float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float2 y = choose::floats_of<T>(v[c]);
-          // (NaN stays in the sums)
-          sum += (wg == 0) == (y.x < 0.0f) ? fabsf(y.x) : y.x != y.x ? y.x : 0.0f;
-          sum += (wg == 0) == (y.y < 0.0f) ? fabsf(y.y) : y.y != y.y ? y.y : 0.0f;
-          v[c] = wg == 0 ? choose::best2<T, false>(v[c], 0u) : choose::best2<T, true>(v[c], 0u);
+          for (int c = 0; c < 32; ++c) {
+            if (C::kQBlocks == 1 && (c & 1) != 0) continue;
+            const float2 y = choose::floats_of<T>(C::kQBlocks == 1 && wg == 1 ? v[c + 1] : v[c]);
+            s0 += fabsf(y.x);
+            s1 += fabsf(y.y);
+          }
+          sum += s0 + s1;
         }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = wg == 0 ? choose::best2<T, false>(v[c], 0u) : choose::best2<T, true>(v[c], 0u);
         tmem_st32(tmem + lanes + wg * (D / 2) + b * 32, v);
       }
       tc_wait_st();
@@ -250,8 +265,12 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
       for (int j = 0; j < x.tiles; ++j, ++jt) {
         bad |= !wait(b_dfull + 8 * (jt & 1), jt >> 1, kPDFull);
         tc_fence_after();
-        const uint32_t* const mine = here + (jt % C::kSlots) * 4;
-        const uint32_t exist[4] = {mine[0], mine[1], mine[2], mine[3]};
+        const uint4 exist = *reinterpret_cast<const uint4*>(here + (jt % C::kSlots) * 4);
+        if (!warp_live && p.head_rows <= 32) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_dempty + 8 * (jt & 1));
+          continue;
+        }
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           float v[32];
@@ -427,11 +446,10 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
     };
     bool ok = !p.stall_first_item;
     for (int64_t n = first; n < p.n_items && ok; n += gridDim.x) {
-      const int32_t run = static_cast<int32_t>(n % p.runs);
-      const int64_t unit = n / p.runs;
-      const int32_t tile = static_cast<int32_t>(unit / p.n_kvheads);
+      const int32_t unit = static_cast<int32_t>(n) / p.runs, run = static_cast<int32_t>(n) - unit * p.runs;
+      const int32_t tile = unit / p.n_kvheads;
       Item x{};
-      x.kvh = static_cast<int32_t>(unit - static_cast<int64_t>(tile) * p.n_kvheads);
+      x.kvh = unit - tile * p.n_kvheads;
       // (numbers of tiles as in window_detail::first_tile)
       auto first_tile = [&](int32_t i) { return __ldg(p.pa.cu_seqlens_q + i) / p.tile_tokens + i; };
       int32_t lo = 0, hi = p.pa.n_requests - 1;
@@ -453,7 +471,9 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
       x.last = r0 + t0 + x.tokens == r1;
       const int64_t p_last = kv - (r1 - r0) + t0 + x.tokens - 1;
       if (p_last < 0) continue;
-      x.pages = static_cast<int32_t>(min(p_last / p.pa.page_size + 1, static_cast<int64_t>(p.pa.pages_per_req)));
+      const int32_t own = p.pa.page_shift >= 0 ? static_cast<int32_t>(p_last >> p.pa.page_shift)
+                                               : static_cast<int32_t>(p_last) / p.pa.page_size;   // (p_last < kv)
+      x.pages = min(own + 1, p.pa.pages_per_req);
       if (x.pages <= p.n_select) continue;                 // all of them are chosen
       x.first = run == 0;
       x.tile0 = run * p.run_tiles;

@@ -550,6 +550,7 @@ qsa_status qsa_page_select(const void* q, const void* bounds, const int32_t* cu_
   p.run_tiles = each < 1 ? 1 : each < plan.page_tiles ? static_cast<int32_t>(each) : plan.page_tiles;
   p.runs = (plan.page_tiles + p.run_tiles - 1) / p.run_tiles;
   p.n_items = units * p.runs;
+  if (p.n_items > INT32_MAX) return QSA_ERR_UNSUPPORTED;
   p.wait_ns = qsa::kWinWaitNs + qsa::kWinWaitNsPerTile * static_cast<unsigned long long>(p.run_tiles);
   if (qsa::device_status_address(&p.status) != cudaSuccess) return QSA_ERR_CUDA;
   void* ws = workspace;
