@@ -118,79 +118,131 @@ __device__ __forceinline__ float two_sum(float s, float x, float* rest) {
   return t;
 }
 
-// The key of a page's score for `group` heads, to compare scores that fp32 sums cannot part (by whole warps; each lane takes
-// D / 32 dims).  A product of two 16-bit values is exact in fp32; sums are kept in two floats, whose error is below 2^-44
-// of the sum of the magnitudes.  Doubles would do too, but this GPU adds few of them (two a cycle and SM: 230 us of 468
-// for 8192 prompt rows), so they are left to scores that floats cannot hold (`wide`).
-template <int D, typename T>
-__device__ __forceinline__ uint64_t exact_key(const T* q, const T* bounds, int group, int lane, bool wide) {
-  constexpr int kPer = D / 32;
-  float lo[kPer], hi[kPer];
+// One head's score in two floats (whole warps; each lane has D / 32 dims).
+template <int PER>
+__device__ __forceinline__ uint64_t two_float_key(const float (&x)[PER], const float (&lo)[PER], const float (&hi)[PER]) {
+  float s = 0.0f, rest = 0.0f, r;
 #pragma unroll
-  for (int c = 0; c < kPer; c += 2) {
-    uint32_t a, b;
-    memcpy(&a, bounds + lane * kPer + c, 4);
-    memcpy(&b, bounds + D + lane * kPer + c, 4);
-    const float2 x = floats_of<T>(a), y = floats_of<T>(b);
-    lo[c] = x.x;
-    lo[c + 1] = x.y;
-    hi[c] = y.x;
-    hi[c + 1] = y.y;
+  for (int c = 0; c < PER; ++c) {
+    s = two_sum(s, __fmul_rn(x[c], x[c] > 0.0f ? hi[c] : lo[c]), &r);
+    rest += r;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s = two_sum(s, __shfl_xor_sync(0xffffffffu, s, o), &r);
+    rest += __shfl_xor_sync(0xffffffffu, rest, o);
+    rest += r;
+  }
+  s = two_sum(s, rest, &r);
+  return choose::key_of(s, r);
+}
+template <int PER, typename T>
+__device__ __forceinline__ void load_dims(const T* p, float (&x)[PER]) {
+  uint32_t w[PER / 2];
+  if constexpr (PER == 8) {
+    const uint4 y = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = y.x;
+    w[1] = y.y;
+    w[2] = y.z;
+    w[3] = y.w;
+  } else if constexpr (PER == 4) {
+    const uint2 y = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = y.x;
+    w[1] = y.y;
+  } else {
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  }
+#pragma unroll
+  for (int c = 0; c < PER; c += 2) {
+    const float2 y = floats_of<T>(w[c / 2]);
+    x[c] = y.x;
+    x[c + 1] = y.y;
+  }
+}
+
+// The key of a page's score for `group` heads, to compare scores that the products' fp32 sums cannot part (by whole
+// warps; each lane takes D / 32 dims).  A product of two 16-bit values is exact in fp32; sums are kept in two floats,
+// whose error is below 2^-44 of the sum of the magnitudes, for the heads that come within fp32's error of the largest:
+// eight heads' fp32 sums are taken at a time, with exchanges that halve them.  Doubles would do too, but this GPU adds
+// few of them (two a cycle and SM: 230 us of 468 for 8192 prompt rows), so they are left to scores that floats cannot hold
+// (`wide`).  reach: sum of |q| times the largest bound.
+template <int D, typename T>
+__device__ __forceinline__ uint64_t exact_key(const T* q, const T* bounds, int group, int lane, float reach, bool wide) {
+  constexpr int kPer = D / 32, kHeads = 8;
+  float lo[kPer], hi[kPer];
+  load_dims<kPer>(bounds + lane * kPer, lo);
+  load_dims<kPer>(bounds + D + lane * kPer, hi);
+  q += lane * kPer;
   uint64_t best = 0;
-  for (int h = 0; h < group; ++h) {
-    float x[kPer];
-#pragma unroll
-    for (int c = 0; c < kPer; c += 2) {
-      uint32_t a;
-      memcpy(&a, q + static_cast<int64_t>(h) * D + lane * kPer + c, 4);
-      const float2 y = floats_of<T>(a);
-      x[c] = y.x;
-      x[c + 1] = y.y;
-    }
-    uint64_t key;
-    if (!wide) {
-      float s = 0.0f, rest = 0.0f, r;
-#pragma unroll
-      for (int c = 0; c < kPer; ++c) {
-        s = two_sum(s, __fmul_rn(x[c], x[c] > 0.0f ? hi[c] : lo[c]), &r);
-        rest += r;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        s = two_sum(s, __shfl_xor_sync(0xffffffffu, s, o), &r);
-        rest += __shfl_xor_sync(0xffffffffu, rest, o);
-        rest += r;
-      }
-      s = two_sum(s, rest, &r);
-      key = choose::key_of(s, r);
-    } else {
+  if (wide) {
+    for (int h = 0; h < group; ++h) {
+      float x[kPer];
+      load_dims<kPer>(q + static_cast<int64_t>(h) * D, x);
       double s = 0.0;
 #pragma unroll
       for (int c = 0; c < kPer; ++c) s += static_cast<double>(x[c]) * (x[c] > 0.0f ? hi[c] : lo[c]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      key = choose::key_of(s);
+      const uint64_t key = choose::key_of(s);
+      best = key > best ? key : best;
     }
-    best = key > best ? key : best;
+    return best;
+  }
+  const float margin = reach * 0x1p-18f;                   // twice the error of a sum of 13 roundings
+  float most = -INFINITY;
+  for (int h0 = 0; h0 < group; h0 += kHeads) {
+    float v[kHeads];
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      float x[kPer];
+      load_dims<kPer>(q + static_cast<int64_t>(min(h0 + h, group - 1)) * D, x);
+      v[h] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) v[h] = fmaf(x[c], x[c] > 0.0f ? hi[c] : lo[c], v[h]);
+    }
+    // lane l comes out with the sum of head h0 + l / 4
+    int n = kHeads;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (o >= 4) {
+        n >>= 1;
+        const bool up = lane & o;
+#pragma unroll
+        for (int c = 0; c < kHeads / 2; ++c) {
+          if (c < n) {
+            const float send = up ? v[c] : v[c + n], keep = up ? v[c + n] : v[c];
+            v[c] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+        }
+      } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+      }
+    }
+    float m = v[0];
+#pragma unroll
+    for (int o = 16; o >= 4; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    most = fmaxf(most, m);
+    const uint32_t near = __ballot_sync(0xffffffffu, (lane & 3) == 0 && h0 + lane / 4 < group && v[0] >= most - margin);
+    for (uint32_t left = near; left; left &= left - 1) {
+      float x[kPer];
+      load_dims<kPer>(q + static_cast<int64_t>(h0 + (__ffs(left) - 1) / 4) * D, x);
+      const uint64_t key = two_float_key<kPer>(x, lo, hi);
+      best = key > best ? key : best;
+    }
   }
   return best;
 }
 
-// A team of threads takes a row and KV head: a warp where there are many, else a block.
-constexpr int kChooseThreads = 256;
-constexpr int kWarpChoosePages = 2048;      // whose keys a warp holds (eight warps: 64 KB)
-template <int D, typename T, int TEAM>
-__global__ void __launch_bounds__(kChooseThreads) page_select_kernel(const __grid_constant__ ChooseParams p) {
+// A team of threads takes a row and KV head: a warp where there are many, else a block.  A lane has N of its pages' keys.
+template <int D, typename T, int TEAM, int N>
+__global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM) page_select_kernel(const __grid_constant__ ChooseParams p) {
   using namespace choose;
-  extern __shared__ uint32_t key_arrays[];
-  __shared__ uint32_t scratch[Team<kChooseThreads>::kScratch];
+  constexpr int kTeams = TEAM == 32 ? 8 : 1;
+  __shared__ uint32_t scratch[TEAM == 32 ? 1 : Team<TEAM>::kScratch];
   pdl_wait();
-  constexpr int kTeams = kChooseThreads / TEAM;
   Team<TEAM> team(scratch);
-  const int lane = team.lane, in_block = TEAM == 32 ? threadIdx.x >> 5 : 0, tid = TEAM == 32 ? lane : threadIdx.x;
-  uint32_t* const keys = key_arrays + static_cast<int64_t>(in_block) * p.pa.pages_per_req;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kTeams + in_block, row = item / p.n_kvheads;
+  const int lane = team.lane;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kTeams + (TEAM == 32 ? threadIdx.x >> 5 : 0), row = item / p.n_kvheads;
   const int32_t kvh = static_cast<int32_t>(item - row * p.n_kvheads);
   if (row >= p.n_rows || row >= __ldg(p.pa.cu_seqlens_q + p.pa.n_requests)) return;
   const int32_t req = paged_request_of_row(p.pa, row, lane);
@@ -199,22 +251,22 @@ __global__ void __launch_bounds__(kChooseThreads) page_select_kernel(const __gri
   const int64_t mine = pos < 0 ? -1 : pos / p.pa.page_size;
   const int32_t n = static_cast<int32_t>(mine + 1 < p.pa.pages_per_req ? mine + 1 : p.pa.pages_per_req);
   const int32_t* const table = p.pa.page_table + static_cast<int64_t>(req) * p.pa.pages_per_req;
+  Keys<TEAM, N> keys(team, n);
+  const int32_t to = min(keys.from + (n + TEAM - 1) / TEAM * 32, n);   // end of this warp's run
   if (n <= p.n_select) {                                   // every page that exists (no scores have been taken)
-    for (int32_t e = tid; e < n; e += TEAM) {
-      const int32_t page = __ldg(table + e);
-      keys[e] = page >= 0 && page < p.pa.n_pages ? kChosen : 0u;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int32_t e = keys.place(team, j), page = e < to ? __ldg(table + e) : -1;
+      keys.k[j] = page >= 0 && page < p.pa.n_pages ? kChosen : 0u;
     }
-    team.sync();
-    emit(team, keys, n, 0u, 0u, p.n_select, out);
+    emit(team, keys, 0u, 0u, p.n_select, out);
     return;
   }
-  const uint4* const src = reinterpret_cast<const uint4*>(p.keys + item * p.key_stride);
-  for (int32_t e = tid * 4; e < n; e += TEAM * 4) {
-    const uint4 x = __ldg(src + e / 4);
-    const uint32_t k[4] = {x.x, x.y, x.z, x.w};
+  const uint32_t* const src = p.keys + item * p.key_stride;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (e + i < n) keys[e + i] = k[i] != 0 && (e + i < p.n_first || e + i > mine - p.n_last) ? kChosen : k[i];
+  for (int j = 0; j < N; ++j) {
+    const int32_t e = keys.place(team, j);
+    keys.k[j] = e < to ? __ldg(src + e) : 0u;
   }
   // (bits of non-negative floats have their order, NaN above all)
   uint32_t most = 0;
@@ -225,39 +277,43 @@ __global__ void __launch_bounds__(kChooseThreads) page_select_kernel(const __gri
   // beyond these, sums overflow or products lose bits in fp32 (NaN fails all comparisons)
   const bool wide = !(reach < 0x1p126f && reach > 0x1p-80f && q_sum > 0x1p-100f && bound > 0x1p-100f);
   const float eps = q_sum == 0.0f || bound == 0.0f ? 0.0f : wide ? INFINITY : reach * kScoreError;
-  team.sync();
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int32_t e = keys.place(team, j);
+    if (keys.k[j] != 0 && (e < p.n_first || e > mine - p.n_last)) keys.k[j] = kChosen;
+  }
   const T* const q = static_cast<const T*>(p.q) + (row * p.n_qheads + static_cast<int64_t>(kvh) * p.group) * D;
   const T* const bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(kvh) * 2 * D;
-  choose::choose(team, keys, n, p.n_select, eps,
+  choose::choose(team, keys, p.n_select, eps,
                  [&](int32_t e) {
                    return exact_key<D>(q, bounds + static_cast<int64_t>(__ldg(table + e)) * p.n_kvheads * 2 * D, p.group,
-                                       lane, wide);
+                                       lane, reach, wide);
                  },
                  out);
 }
 
-template <int D, typename T, int TEAM>
-cudaError_t launch_select_team(const ChooseParams& p, int which, cudaStream_t stream) {
-  auto kern = page_select_kernel<D, T, TEAM>;
-  constexpr int kTeams = kChooseThreads / TEAM;
-  const cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern),
-                                    4 * (TEAM == 32 ? kTeams * kWarpChoosePages : kMaxChoosePages), kOptChoose + which);
-  if (e != cudaSuccess) return e;
+template <int D, typename T, int TEAM, int N>
+cudaError_t launch_select_team(const ChooseParams& p, cudaStream_t stream) {
+  constexpr int kTeams = TEAM == 32 ? 8 : 1;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // starts while the scores are taken
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>((p.n_rows * p.n_kvheads + kTeams - 1) / kTeams));
-  cfg.blockDim = dim3(kChooseThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(kTeams) * p.pa.pages_per_req * 4;
+  cfg.blockDim = dim3(TEAM == 32 ? 256 : TEAM);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return cudaLaunchKernelEx(&cfg, page_select_kernel<D, T, TEAM, N>, p);
 }
 template <int D, typename T>
-cudaError_t launch_select_dim(const ChooseParams& p, int which, bool warps, cudaStream_t stream) {
-  return warps ? launch_select_team<D, T, 32>(p, which, stream) : launch_select_team<D, T, kChooseThreads>(p, which + 1, stream);
+cudaError_t launch_select_dim(const ChooseParams& p, int num_sms, cudaStream_t stream) {
+  const int32_t n = p.pa.pages_per_req;
+  if (p.n_rows * p.n_kvheads >= 32 * static_cast<int64_t>(num_sms)) {
+    if (n <= 512) return launch_select_team<D, T, 32, 16>(p, stream);
+    if (n <= 1024) return launch_select_team<D, T, 32, 32>(p, stream);
+  }
+  return n <= 2048 ? launch_select_team<D, T, 256, 8>(p, stream) : launch_select_team<D, T, 1024, 32>(p, stream);
 }
 
 }  // namespace
@@ -280,14 +336,13 @@ cudaError_t launch_page_bounds(const BoundsParams& p, bool fp16, int num_sms, cu
 cudaError_t launch_page_select(const ChooseParams& p, bool fp16, int num_sms, cudaStream_t stream) {
   const cudaError_t e = launch_page_score(p, fp16, num_sms, stream);
   if (e != cudaSuccess) return e;
-  const bool warps = p.n_rows * p.n_kvheads >= 32 * static_cast<int64_t>(num_sms) && p.pa.pages_per_req <= kWarpChoosePages;
   if (fp16)
-    return p.head_dim == 64    ? launch_select_dim<64, __half>(p, 0, warps, stream)
-           : p.head_dim == 128 ? launch_select_dim<128, __half>(p, 2, warps, stream)
-                               : launch_select_dim<256, __half>(p, 4, warps, stream);
-  return p.head_dim == 64    ? launch_select_dim<64, __nv_bfloat16>(p, 6, warps, stream)
-         : p.head_dim == 128 ? launch_select_dim<128, __nv_bfloat16>(p, 8, warps, stream)
-                             : launch_select_dim<256, __nv_bfloat16>(p, 10, warps, stream);
+    return p.head_dim == 64    ? launch_select_dim<64, __half>(p, num_sms, stream)
+           : p.head_dim == 128 ? launch_select_dim<128, __half>(p, num_sms, stream)
+                               : launch_select_dim<256, __half>(p, num_sms, stream);
+  return p.head_dim == 64    ? launch_select_dim<64, __nv_bfloat16>(p, num_sms, stream)
+         : p.head_dim == 128 ? launch_select_dim<128, __nv_bfloat16>(p, num_sms, stream)
+                             : launch_select_dim<256, __nv_bfloat16>(p, num_sms, stream);
 }
 
 }  // namespace qsa

@@ -109,43 +109,43 @@ struct Team {
   }
 };
 
-// Keys [n] in shared memory, each warp of the team owns a run of them (whole 32s).
-template <int THREADS>
-struct Run {
-  int32_t from, to;
-  __device__ __forceinline__ Run(const Team<THREADS>& t, int32_t n) {
-    const int32_t per = ((n + THREADS - 1) / THREADS) * 32;
-    from = t.warp * per;
-    to = from + per < n ? from + per : n;
+// The keys of a list, in registers: each warp of the team has a run of it, in which a lane has every 32nd entry.  Entries past
+// the list's end have key 0, which nothing below counts.
+template <int THREADS, int N>
+struct Keys {
+  uint32_t k[N];
+  int32_t from;                                            // first entry of the warp's run
+  __device__ __forceinline__ Keys(const Team<THREADS>& t, int32_t n) : from(t.warp * ((n + THREADS - 1) / THREADS) * 32) {}
+  // entry j of this lane
+  __device__ __forceinline__ int32_t place(const Team<THREADS>& t, int j) const { return from + j * 32 + t.lane; }
+  template <typename F>
+  __device__ __forceinline__ uint32_t count(Team<THREADS>& t, F f) const {
+    uint32_t c = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) c += f(k[j]) ? 1u : 0u;
+    return t.sum(c);
   }
 };
 
-template <int THREADS, typename F>
-__device__ __forceinline__ uint32_t count_if(Team<THREADS>& t, const uint32_t* keys, int32_t n, F f) {
-  const Run<THREADS> run(t, n);
-  uint32_t c = 0;
-  for (int32_t i = run.from + t.lane; i < run.to; i += 32) c += f(keys[i]) ? 1u : 0u;
-  return t.sum(c);
-}
-
-// The k-th largest key (k >= 1, at least k keys are not 0, fewer than k are kChosen).
-template <int THREADS>
-__device__ __forceinline__ uint32_t kth_largest(Team<THREADS>& t, const uint32_t* keys, int32_t n, uint32_t k) {
-  const Run<THREADS> run(t, n);
+// The want-th largest key (want >= 1, at least so many keys are not 0, fewer are kChosen).
+template <int THREADS, int N>
+__device__ __forceinline__ uint32_t kth_largest(Team<THREADS>& t, const Keys<THREADS, N>& keys, uint32_t want) {
   uint32_t top = 0, low = 0xffffffffu;
-  for (int32_t i = run.from + t.lane; i < run.to; i += 32) {
-    const uint32_t x = keys[i];
-    if (x != kChosen && x > top) top = x;
-    if (x != 0 && x < low) low = x;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const uint32_t x = keys.k[j];
+    top = x != kChosen ? max(top, x) : top;
+    low = x != 0 ? min(low, x) : low;
   }
   uint32_t hi = t.max(top), lo = ~t.max(~low);             // the answer is in [lo, hi]
   while (lo < hi) {
     const uint32_t mid = lo + (hi - lo + 1) / 2;
-    const uint32_t c = count_if(t, keys, n, [&](uint32_t x) { return x >= mid; });
-    if (c >= k) lo = mid; else hi = mid - 1;
-    if (c == k) {                                          // mid parts them: the smallest key from it on
+    const uint32_t c = keys.count(t, [&](uint32_t x) { return x >= mid; });
+    if (c >= want) lo = mid; else hi = mid - 1;
+    if (c == want) {                                       // mid parts them: the smallest key from it on
       low = 0xffffffffu;
-      for (int32_t i = run.from + t.lane; i < run.to; i += 32) low = keys[i] >= mid && keys[i] < low ? keys[i] : low;
+#pragma unroll
+      for (int j = 0; j < N; ++j) low = keys.k[j] >= mid ? min(low, keys.k[j]) : low;
       return ~t.max(~low);
     }
   }
@@ -153,16 +153,16 @@ __device__ __forceinline__ uint32_t kth_largest(Team<THREADS>& t, const uint32_t
 }
 
 // Writes the places of the keys above `bar`, and of the first `equal` ones equal to it, in order; then -1.
-template <int THREADS>
-__device__ __forceinline__ void emit(Team<THREADS>& t, const uint32_t* keys, int32_t n, uint32_t bar, uint32_t equal,
-                                     int32_t k, int32_t* out) {
-  const Run<THREADS> run(t, n);
+template <int THREADS, int N>
+__device__ __forceinline__ void emit(Team<THREADS>& t, const Keys<THREADS, N>& keys, uint32_t bar, uint32_t equal, int32_t k,
+                                     int32_t* out) {
   uint32_t above = 0, same = 0;                            // in the runs before this warp's
   if constexpr (THREADS > 32) {
     uint32_t a = 0, s = 0;
-    for (int32_t i = run.from + t.lane; i < run.to; i += 32) {
-      a += keys[i] > bar;
-      s += keys[i] == bar;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      a += keys.k[j] > bar;
+      s += keys.k[j] == bar;
     }
     a = __reduce_add_sync(0xffffffffu, a);
     s = __reduce_add_sync(0xffffffffu, s);
@@ -176,90 +176,90 @@ __device__ __forceinline__ void emit(Team<THREADS>& t, const uint32_t* keys, int
     same = __reduce_add_sync(0xffffffffu, t.lane < t.warp ? r[2 * t.lane + 1] : 0u);
   }
   const uint32_t before = (1u << t.lane) - 1u;
-  for (int32_t i = run.from; i < run.to; i += 32) {
-    const uint32_t x = i + t.lane < run.to ? keys[i + t.lane] : 0u;
-    const bool in = i + t.lane < run.to;
-    const uint32_t a = __ballot_sync(0xffffffffu, in && x > bar), s = __ballot_sync(0xffffffffu, in && x == bar);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const uint32_t x = keys.k[j];
+    const uint32_t a = __ballot_sync(0xffffffffu, x > bar), s = __ballot_sync(0xffffffffu, x == bar);
+    if ((a | s) == 0) continue;
     const uint32_t my_above = above + __popc(a & before), my_same = same + __popc(s & before);
-    const uint32_t place = my_above + (my_same < equal ? my_same : equal);
-    if (in && (x > bar || (x == bar && my_same < equal)) && place < static_cast<uint32_t>(k))
-      out[place] = i + t.lane;
+    const uint32_t place = my_above + min(my_same, equal);
+    if ((x > bar || (x == bar && my_same < equal)) && place < static_cast<uint32_t>(k)) out[place] = keys.place(t, j);
     above += __popc(a);
     same += __popc(s);
   }
   // the last warp has counted them all
   if (t.warp == Team<THREADS>::kWarps - 1) {
-    const uint32_t all = above + (same < equal ? same : equal);
-    for (int32_t i = static_cast<int32_t>(all) + t.lane; i < k; i += 32) out[i] = -1;
+    for (int32_t i = static_cast<int32_t>(above + min(same, equal)) + t.lane; i < k; i += 32) out[i] = -1;
   }
 }
 
-// Chooses the k best of keys [n] (shared memory, changed by the call) and writes their places in order, then -1.
+// Replaces the keys from lo to hi by value(place), a function of whole warps, those above by kChosen, those below by 0.
+template <int THREADS, int N, typename F>
+__device__ __forceinline__ void refine(Team<THREADS>& t, Keys<THREADS, N>& keys, uint32_t lo, uint32_t hi, F value) {
+  uint32_t open = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const uint32_t x = keys.k[j];
+    if (x >= lo && x <= hi) open |= 1u << j;
+    keys.k[j] = x > hi ? kChosen : 0u;
+  }
+  while (true) {
+    const uint32_t lanes = __ballot_sync(0xffffffffu, open != 0);
+    if (lanes == 0) break;
+    const int l = __ffs(lanes) - 1, j = __ffs(__shfl_sync(0xffffffffu, open, l)) - 1;
+    const uint32_t y = value(keys.from + j * 32 + l);
+    if (t.lane == l) {
+      open &= open - 1;
+#pragma unroll
+      for (int i = 0; i < N; ++i) keys.k[i] = i == j ? y : keys.k[i];
+    }
+  }
+}
+
+// Chooses the k best of the keys (changed by the call) and writes their places in order, then -1.
 // exact(i), called by whole warps, is the 64-bit key of entry i's score.
-template <int THREADS, typename Exact>
-__device__ __forceinline__ void choose(Team<THREADS>& t, uint32_t* keys, int32_t n, int32_t k, float eps, Exact exact,
+template <int THREADS, int N, typename Exact>
+__device__ __forceinline__ void choose(Team<THREADS>& t, Keys<THREADS, N>& keys, int32_t k, float eps, Exact exact,
                                        int32_t* out) {
+  static_assert(N <= 32, "a lane's entries as bits");
   const uint32_t want = static_cast<uint32_t>(k);
-  if (count_if(t, keys, n, [](uint32_t x) { return x != 0; }) <= want) {
-    emit(t, keys, n, 0u, 0u, k, out);
+  if (keys.count(t, [](uint32_t x) { return x != 0; }) <= want) {
+    emit(t, keys, 0u, 0u, k, out);
     return;
   }
-  if (count_if(t, keys, n, [](uint32_t x) { return x == kChosen; }) >= want) {
-    emit(t, keys, n, kChosen, want, k, out);
+  if (keys.count(t, [](uint32_t x) { return x == kChosen; }) >= want) {
+    emit(t, keys, kChosen, want, k, out);
     return;
   }
-  const uint32_t bar = kth_largest(t, keys, n, want);
+  const uint32_t bar = kth_largest(t, keys, want);
   const float s = score_of(bar), e2 = 2.0f * eps;
   uint32_t lo = 1u, hi = kNan;                             // no bound on the error: all may belong
   if (bar != kNan && isfinite(s) && isfinite(e2)) {
     lo = key_of(__fsub_rd(s, e2));
     hi = key_of(__fadd_ru(s, e2));
   }
-  const uint32_t sure = count_if(t, keys, n, [&](uint32_t x) { return x > hi; });
-  const uint32_t open = count_if(t, keys, n, [&](uint32_t x) { return x >= lo && x <= hi; });
+  const uint32_t sure = keys.count(t, [&](uint32_t x) { return x > hi; });
+  const uint32_t open = keys.count(t, [&](uint32_t x) { return x >= lo && x <= hi; });
   if (sure + open == want) {
-    emit(t, keys, n, lo - 1u, 0u, k, out);
+    emit(t, keys, lo - 1u, 0u, k, out);
     return;
   }
   if (eps == 0.0f) {                                       // they are equal
-    emit(t, keys, n, bar, want - sure, k, out);
+    emit(t, keys, bar, want - sure, k, out);
     return;
   }
-  const Run<THREADS> run(t, n);
-  t.sync();                                                // the keys have been read by all
-  for (int32_t i = run.from; i < run.to; i += 32) {
-    const uint32_t x = i + t.lane < run.to ? keys[i + t.lane] : 0u;
-    uint32_t y = x > hi ? kChosen : 0u;
-    for (uint32_t m = __ballot_sync(0xffffffffu, x >= lo && x <= hi); m; m &= m - 1) {
-      const int j = __ffs(m) - 1;
-      const uint64_t v = exact(i + j);
-      if (t.lane == j) y = static_cast<uint32_t>(v >> 32);
-    }
-    if (i + t.lane < run.to) keys[i + t.lane] = y;
-  }
-  t.sync();
-  const uint32_t upper = kth_largest(t, keys, n, want);
-  uint32_t over = count_if(t, keys, n, [&](uint32_t x) { return x > upper; });
-  if (over + count_if(t, keys, n, [&](uint32_t x) { return x == upper; }) == want) {
-    emit(t, keys, n, upper, want - over, k, out);
+  refine(t, keys, lo, hi, [&](int32_t i) { return static_cast<uint32_t>(exact(i) >> 32); });
+  const uint32_t upper = kth_largest(t, keys, want);
+  uint32_t over = keys.count(t, [&](uint32_t x) { return x > upper; });
+  if (over + keys.count(t, [&](uint32_t x) { return x == upper; }) == want) {
+    emit(t, keys, upper, want - over, k, out);
     return;
   }
-  t.sync();
-  for (int32_t i = run.from; i < run.to; i += 32) {
-    const uint32_t x = i + t.lane < run.to ? keys[i + t.lane] : 0u;
-    uint32_t y = x > upper ? kChosen : 0u;
-    for (uint32_t m = __ballot_sync(0xffffffffu, x == upper && i + t.lane < run.to); m; m &= m - 1) {
-      const int j = __ffs(m) - 1;
-      const uint64_t v = exact(i + j);
-      // (0 and kChosen stay free: the last of the 64 bits is left out)
-      if (t.lane == j) y = 1u + (static_cast<uint32_t>(v) >> 1);
-    }
-    if (i + t.lane < run.to) keys[i + t.lane] = y;
-  }
-  t.sync();
-  const uint32_t lower = kth_largest(t, keys, n, want);
-  over = count_if(t, keys, n, [&](uint32_t x) { return x > lower; });
-  emit(t, keys, n, lower, want - over, k, out);
+  // (0 and kChosen stay free: the last of the 64 bits is left out)
+  refine(t, keys, upper, upper, [&](int32_t i) { return 1u + (static_cast<uint32_t>(exact(i)) >> 1); });
+  const uint32_t lower = kth_largest(t, keys, want);
+  over = keys.count(t, [&](uint32_t x) { return x > lower; });
+  emit(t, keys, lower, want - over, k, out);
 }
 
 }  // namespace choose

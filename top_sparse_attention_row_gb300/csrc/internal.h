@@ -450,7 +450,7 @@ cudaError_t launch_page_select(const ChooseParams& p, bool fp16, int num_sms, cu
 
 // Dynamic shared-memory opt-in of a kernel to `bytes`, its largest use, once per device and kernel (so
 // calls made during a graph capture only enqueue).
-enum OptInKernel { kOptPlan, kOptWindow, kOptChoose = kOptWindow + 24, kOptScore = kOptChoose + 12,
+enum OptInKernel { kOptPlan, kOptWindow, kOptScore = kOptWindow + 24,
                     kOptListPages = kOptScore + 6, kOptCount = kOptListPages + 1 };
 cudaError_t smem_opt_in(const void* kernel, int bytes, int which);
 

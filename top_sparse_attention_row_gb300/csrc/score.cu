@@ -11,8 +11,8 @@
 //  * D = A.B^T (tcgen05, M = 128 query rows, N = 128 pages, K = 2 dims): the split queries lie in tensor memory, where
 //    they stay for the item, so that shared memory is read for the pages alone (128 bytes a cycle at the tensor core's
 //    full rate; with both operands there it would be twice as much as it has).  Two buffers of D in tensor memory.
-//  * The pages' rows are gathered by page id, four at a time (TMA), 64 dims of 128 pages a stage, by eight warps into a
-//    ring.  The next item's queries are loaded (TMA) while this one's products run.
+//  * The pages' rows are gathered by page id, four at a time (TMA), 64 dims of 128 pages a stage, by sixteen warps into
+//    a ring (a warp issues one gather after the other, ~40 ns each).  The next item's queries are loaded (TMA) while this one's products run.
 //  * Scores are written as keys that have their order (choose.cuh), 0 for a page that does not exist.  For the error bound
 //    the sum of |q| of every row is kept, and the largest |bound| of every tile of pages, taken from the ring by one warp
 //    in the items of a request's last rows (which see all of its pages).
@@ -39,8 +39,12 @@ struct ScoreCfg {
   static constexpr int kQBlocks = D / 64;
   static constexpr int kQBytes = kQBlocks * 128 * 128;
   static constexpr int kStages = D == 256 ? 9 : D == 128 ? 11 : 12;
-  static constexpr int kThreads = 640;
-  static constexpr int kGatherWarp0 = 12, kGatherWarps = 8;
+  static constexpr int kThreads = 896;
+  static constexpr int kGatherWarp0 = 12, kGatherWarps = 16;   // two a stage
+  // registers per thread at launch, and after the split: the epilogue's two warpgroups, the gathers' four (the others keep
+  // what they have)
+  static constexpr int kLaunchRegs = 72, kEpilogueRegs = 104, kGatherRegs = 56;
+  static_assert(256 * kEpilogueRegs + 128 * kLaunchRegs + 512 * kGatherRegs <= kThreads * kLaunchRegs, "register split");
   static constexpr int kRecords = 4;
   static constexpr int kSlots = 16;                        // > tiles between their gather and their scores
   static constexpr int kRingAt = kQBytes;
@@ -153,7 +157,7 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
   constexpr int kReaders = 8 + 1 + 1 + 1 + C::kGatherWarps;   // of a record: epilogue, MMA, scan, queries, gathers
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(b_full + 8 * s, 1);
+      mbar_init(b_full + 8 * s, 2);
       mbar_init(b_empty + 8 * s, 2);                       // the MMA and the scan
     }
     for (int i = 0; i < 2; ++i) {
@@ -198,6 +202,7 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
   };
 
   if (warp < 8) {
+    regs_inc<C::kEpilogueRegs>();
     // ------------------------------------------------------------ splits the queries, writes the scores
     const int wg = warp >> 2, quarter = warp & 3, row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -514,9 +519,11 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
     finish_role();
     return;
   }
-  // -------------------------------------------------------------- gathers: eight warps take the blocks in turn
-  const int gw = warp - C::kGatherWarp0;
-  constexpr int kEvery = C::kGatherWarps / C::kBlocks;     // tiles between two of a warp's
+  // -------------------------------------------------------------- gathers: pairs of warps take the blocks in turn, each
+  // half of a block's pages
+  regs_dec<C::kGatherRegs>();
+  const int gw = (warp - C::kGatherWarp0) >> 1, part = warp & 1;
+  constexpr int kPairs = C::kGatherWarps / 2, kEvery = kPairs / C::kBlocks;   // tiles between two of a pair's
   const int block = gw % C::kBlocks, tile_turn = gw / C::kBlocks;
   uint32_t jt = 0, issued = 0;
   Item x{};
@@ -527,11 +534,11 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
     int32_t r[4];
     uint32_t here;
   };
-  // page ids of this lane's four pages in tile j of item x
-  auto look_up = [&](const Item& y, int t) {
+  // page ids of the four pages of lane l (of 32) in tile t of item y
+  auto look_up = [&](const Item& y, int t, int l) {
     Rows k;
     k.here = 0;
-    const int32_t e0 = (y.tile0 + t) * kScoreTile + lane * 4;
+    const int32_t e0 = (y.tile0 + t) * kScoreTile + l * 4;
     const int32_t* const table = p.pa.page_table + static_cast<int64_t>(y.req) * p.pa.pages_per_req;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -542,7 +549,7 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
     }
     return k;
   };
-  // the warp's next tile from (it, x, j) on
+  // the pair's next tile from (it, x, j) on
   auto seek = [&]() {
     while (more) {
       if (j >= x.tiles) {
@@ -556,9 +563,10 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
       ++jt;
     }
   };
+  const int mine = part * 16 + (lane & 15);                // lanes 0-15 gather; all look up, for the pages that exist
   seek();
   Rows rows{};
-  if (more) rows = look_up(x, j);
+  if (more) rows = look_up(x, j, part == 0 && block == 0 ? lane : mine);
   while (more) {
     const uint32_t tile = jt, n = tile * C::kBlocks + block, s = n % C::kStages;
     const Rows now = rows;
@@ -566,28 +574,29 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
       stop = true;
       break;
     }
-    if (block == 0) {
+    if (block == 0 && part == 0) {
       uint32_t m[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) m[i] = __ballot_sync(0xffffffffu, now.here >> i & 1u);
       if (lane == 0) *reinterpret_cast<uint4*>(here + (tile % C::kSlots) * 4) = make_uint4(m[0], m[1], m[2], m[3]);
     }
-    if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * s, C::kStageBytes);
+    if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * s, C::kStageBytes / 2);
     __syncwarp();
-    tma_gather4(base + C::kRingAt + s * C::kStageBytes + lane * 512, &tmB, block * 64, now.r[0], now.r[1], now.r[2], now.r[3],
-                b_full + 8 * s);
+    if (lane < 16)
+      tma_gather4(base + C::kRingAt + s * C::kStageBytes + mine * 512, &tmB, block * 64, now.r[0], now.r[1], now.r[2],
+                  now.r[3], b_full + 8 * s);
     issued = n + 1;
     ++j;
     ++jt;
     seek();
-    if (more) rows = look_up(x, j);
+    if (more) rows = look_up(x, j, part == 0 && block == 0 ? lane : mine);
   }
   if (issued > 0 && lane == 0 && (stop || *abort_flag)) {
     // this warp's copies that may still be in flight: of the last ring
     const uint32_t last = issued - 1;
-    for (uint32_t n = last; last - n < static_cast<uint32_t>(C::kStages); n -= C::kGatherWarps) {
+    for (uint32_t n = last; last - n < static_cast<uint32_t>(C::kStages); n -= kPairs) {
       drain(b_full + 8 * (n % C::kStages), (n / C::kStages) & 1, status, kDrainNs / 100);
-      if (n < static_cast<uint32_t>(C::kGatherWarps)) break;
+      if (n < static_cast<uint32_t>(kPairs)) break;
     }
   }
   __syncwarp();
@@ -601,6 +610,12 @@ cudaError_t launch_score_dim(const ChooseParams& p, const CUtensorMap& tb, const
   auto kern = page_score_kernel<D, T>;
   const cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern), C::kSmem, kOptScore + which);
   if (e != cudaSuccess) return e;
+  // (the register shares add up to what the block is launched with: a kernel compiled to fewer would wait for ever)
+  static const int regs = [&] {
+    cudaFuncAttributes a{};
+    return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (regs < C::kLaunchRegs) return cudaErrorInvalidConfiguration;
   kern<<<grid, C::kThreads, C::kSmem, stream>>>(tb, tq1, tqt, p);
   return cudaGetLastError();
 }
