@@ -270,8 +270,8 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM) page_select_kernel(co
   }
   // (bits of non-negative floats have their order, NaN above all)
   uint32_t most = 0;
-  const float* const largest = p.largest + (static_cast<int64_t>(req) * p.n_kvheads + kvh) * p.page_tiles;
-  for (int32_t i = lane; i * kScoreTile < n; i += 32) most = max(most, __float_as_uint(__ldg(largest + i)));
+  const float* const largest = p.largest + (static_cast<int64_t>(req) * p.n_kvheads + kvh) * p.bound_tiles;
+  for (int32_t i = lane; i * kBoundTile < n; i += 32) most = max(most, __float_as_uint(__ldg(largest + i)));
   const float q_sum = __ldg(p.reach + item), bound = __uint_as_float(__reduce_max_sync(0xffffffffu, most));
   const float reach = q_sum * bound;
   // beyond these, sums overflow or products lose bits in fp32 (NaN fails all comparisons)

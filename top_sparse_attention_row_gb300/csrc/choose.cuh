@@ -41,6 +41,9 @@ __device__ __forceinline__ uint32_t best2(uint32_t a, uint32_t b) {
   memcpy(&a, &x, 4);
   return a;
 }
+// The larger of |a|'s and |b|'s halves (a is not negative; NaN stays).
+template <typename T>
+__device__ __forceinline__ uint32_t largest2(uint32_t a, uint32_t b) { return best2<T, true>(a, b & 0x7fff7fffu); }
 template <typename T>
 __device__ __forceinline__ float2 floats_of(uint32_t a) {
   typename Pair<T>::type x;

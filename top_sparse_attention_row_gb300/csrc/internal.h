@@ -422,7 +422,8 @@ struct BoundsParams {
 };
 cudaError_t launch_page_bounds(const BoundsParams& p, bool fp16, int num_sms, cudaStream_t stream);
 constexpr int kMaxChoosePages = 32768;       // of a request
-constexpr int kScoreTile = 128;              // pages of an MMA tile, and rows of the query tile
+constexpr int kScoreTile = 128;              // pages of an MMA tile
+constexpr int kBoundTile = 64;               // pages that share a largest bound
 struct ChooseParams {
   const void* q;                // [n_rows, n_qheads, D]
   const void* bounds;
@@ -434,13 +435,13 @@ struct ChooseParams {
   // scores (score.cu)
   uint32_t* keys;               // [n_rows, n_kvheads, key_stride]: keys of the pages' scores
   float* reach;                 // [n_rows, n_kvheads]: largest sum of |q| over the heads
-  float* largest;               // [n_requests, n_kvheads, page_tiles]: largest |bound| of every tile of pages
-  int64_t n_items;              // query tiles x KV heads x runs
-  int32_t key_stride;           // page_tiles * kScoreTile
-  int32_t page_tiles;           // of pages_per_req
-  int32_t head_rows;            // rows of a token in the query tile: the heads rounded up to a power of two
-  int32_t tile_tokens;          // kScoreTile / head_rows
-  int32_t runs, run_tiles;      // of a query tile's pages: runs of so many tiles
+  float* largest;               // [n_requests, n_kvheads, bound_tiles]: largest |bound| of every 64 pages
+  int64_t n_items;              // units x runs
+  int32_t key_stride;           // pages_per_req, rounded up to whole tiles
+  int32_t bound_tiles;          // key_stride / kBoundTile
+  int32_t tile_tokens;          // 128 / group
+  int32_t units;                // query tiles x KV heads
+  int32_t run_tiles;            // tiles of a run of a query tile's pages
   int32_t stall_first_item;
   int32_t* status;
   unsigned long long wait_ns;

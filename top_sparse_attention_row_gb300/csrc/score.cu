@@ -3,20 +3,24 @@
 // score(row, KV head, page) = max over the heads h of  sum_d max(q_hd lo_d, q_hd hi_d), and since the larger of the two
 // products is the one with hi where q is positive and with lo elsewhere,
 //   sum_d max(q lo, q hi) = sum_d min(q, 0) lo + max(q, 0) hi :
-// a matrix product of [min(q, 0) | max(q, 0)] with the pages' rows [lo | hi], which is how the bounds lie in memory.
+// a matrix product of the pages' rows [lo | hi], which is how the bounds lie in memory, with [min(q, 0) | max(q, 0)].
 //
-//  * One work item is a query tile of one request and KV head and a run of its pages' tiles.  A query tile is 128 rows:
-//    the heads of a token in a power of two of rows, so that they lie in one warp and their maximum is taken by
-//    exchanges that halve the columns each time (a group of 12 heads uses 96 of the 128 rows).
-//  * D = A.B^T (tcgen05, M = 128 query rows, N = 128 pages, K = 2 dims): the split queries lie in tensor memory, where
-//    they stay for the item, so that shared memory is read for the pages alone (128 bytes a cycle at the tensor core's
-//    full rate; with both operands there it would be twice as much as it has).  Two buffers of D in tensor memory.
-//  * The pages' rows are gathered by page id, four at a time (TMA), 64 dims of 128 pages a stage, by sixteen warps into
-//    a ring (a warp issues one gather after the other, ~40 ns each).  The next item's queries are loaded (TMA) while this one's products run.
+//  * One work item is a query tile of one request and KV head (the heads of up to 128 / group tokens) and a run of its
+//    pages' tiles.  D = pages x queries (tcgen05, M = 128 pages, N = the heads of the item's tokens, K = 2 dims), both
+//    operands in shared memory, three buffers of D in tensor memory.  A thread of the epilogue has a page, so the maximum
+//    over a token's heads is one over neighbouring columns, and 32 pages' keys are written side by side.
+//    (The other way round, with the queries as M from tensor memory, an MMA of N = 128 takes 90 to 110 cycles where this
+//    one takes 65, and the maxima go across lanes: 193 us where this takes KKK for 8192 prompt rows.)
+//  * The split queries of an item lie in shared memory until its products are done.  Eight warps have the next item's
+//    queries in registers by then, and have summed |q| for the error bound.
+//  * The pages' rows are gathered by page id, four at a time (TMA), 128 dims of 128 pages a stage, by four warps into a
+//    ring, three stages at once: a warp issues one gather after the other, ~50 ns each.  (cp.async, 16 bytes a thread,
+//    brought 30 bytes a cycle beside the building of the queries.)  A stage has eight MMAs, because a commit costs the
+//    tensor core about two of them.
 //  * Scores are written as keys that have their order (choose.cuh), 0 for a page that does not exist.  For the error bound
-//    the sum of |q| of every row is kept, and the largest |bound| of every tile of pages, taken from the ring by one warp
-//    in the items of a request's last rows (which see all of its pages).
-//  * What bounds it.  Decode: HBM.  Prompts: shared memory, 128 KB written and read a tile of 256 dims.
+//    the largest |bound| of every 64 pages is taken from the ring by two warps, in the items of a request's last rows (which
+//    see all of its pages).
+//  * What bounds it.  Decode: HBM.  Prompts: shared memory, where every MMA reads 8 KB in 65 cycles.
 //  * Every mbarrier wait is bounded; a timeout records a code in the device status word, all roles leave their loops, copies
 //    and MMAs in flight are drained, tensor memory is freed.
 #include <cuda_bf16.h>
@@ -34,36 +38,36 @@ using namespace window_detail;
 
 template <int D>
 struct ScoreCfg {
-  static constexpr int kBlocks = 2 * D / 64;               // stages of a tile of pages
-  static constexpr int kStageBytes = kScoreTile * 128;     // 64 dims of 128 pages
-  static constexpr int kQBlocks = D / 64;
-  static constexpr int kQBytes = kQBlocks * 128 * 128;
-  static constexpr int kStages = D == 256 ? 9 : D == 128 ? 11 : 12;
-  static constexpr int kThreads = 896;
-  static constexpr int kGatherWarp0 = 12, kGatherWarps = 16;   // two a stage
-  // registers per thread at launch, and after the split: the epilogue's two warpgroups, the gathers' four (the others keep
-  // what they have)
-  static constexpr int kLaunchRegs = 72, kEpilogueRegs = 104, kGatherRegs = 56;
-  static_assert(256 * kEpilogueRegs + 128 * kLaunchRegs + 512 * kGatherRegs <= kThreads * kLaunchRegs, "register split");
+  static constexpr int kPer = D / 64;                      // stages of a tile of pages: 128 of 2 D dims each
+  static constexpr int kStageBytes = kScoreTile * 256;
+  static constexpr int kBlock = 128 * 128;                 // bytes of 64 dims of 128 rows
+  static constexpr int kQBytes = 2 * D / 64 * kBlock;      // the split queries
+  static constexpr int kStages = D == 256 ? 3 : D == 128 ? 5 : 6;
+  static constexpr int kThreads = 1024;
+  static constexpr int kBuildWarp0 = 8, kMmaWarp = 16, kSchedulerWarp = 17, kScanWarp = 18, kGatherWarp0 = 20;
+  static constexpr int kGatherWarps = 12, kStageWarps = 4;
+  static constexpr int kChunks = 128 * D / 8 / 256;        // 16-byte pieces of the queries a building thread has
+  // registers per thread at launch, and after the split: epilogue and building warpgroups; the others
+  static constexpr int kLaunchRegs = 64, kWideRegs = 80, kRoleRegs = 48;
+  static_assert(512 * kWideRegs + 512 * kRoleRegs <= kThreads * kLaunchRegs, "register split");
   static constexpr int kRecords = 4;
   static constexpr int kSlots = 16;                        // > tiles between their gather and their scores
+  static constexpr int kBuffers = 3;                       // of D, 128 columns each
   static constexpr int kRingAt = kQBytes;
   static constexpr int kHereAt = kRingAt + kStages * kStageBytes;   // [kSlots][4] uint32: which pages exist
-  static constexpr int kSumAt = kHereAt + kSlots * 16;     // [2][2][128] float: sums of |q|
-  static constexpr int kCrossAt = kSumAt + 2048;           // [2][2][4][32] float: maxima of heads in several warps
-  static constexpr int kRecAt = kCrossAt + 2048;
+  static constexpr int kSumAt = kHereAt + kSlots * 16;     // [2][128] float: sums of |q|
+  static constexpr int kRecAt = kSumAt + 1024;
   static constexpr int kBarAt = kRecAt + kRecords * 64;
-  // full, empty [stages]; dfull, dempty [2]; qfull, qempty, aready, adone, fin; recfull, recempty [records]
-  static constexpr int kBars = 2 * kStages + 4 + 5 + 2 * kRecords;
+  // full, empty [stages]; dfull, dempty [buffers]; qready, adone, fin; recfull, recempty [records]
+  static constexpr int kBars = 2 * kStages + 2 * kBuffers + 3 + 2 * kRecords;
   static constexpr int kTmemSlot = (kBarAt + 8 * kBars + 15) / 16 * 16;
   static constexpr int kSmem = kTmemSlot + 16;
   static_assert(kSmem <= kSmemLimit, "shared memory");
-  static_assert(kStages / kBlocks + 4 < kSlots, "slots");
-  static_assert(2 * D / 2 + 2 * kScoreTile <= 512, "tensor memory");
+  static_assert(kStages / kPer + kBuffers + 2 < kSlots, "slots");
 };
 
 enum ScoreSite : int32_t {
-  kPRecEmpty = 0x61, kPRecFull, kPQEmpty, kPQFull, kPStageEmpty, kPStageFull, kPDFull, kPDEmpty, kPAReady, kPADone
+  kPRecEmpty = 0x61, kPRecFull, kPStageEmpty, kPStageFull, kPDFull, kPDEmpty, kPQReady, kPADone
 };
 
 // A work item, written by the scheduler warp and read by every role.
@@ -72,79 +76,37 @@ struct Item {
   int32_t tile0;       // first of them
   int32_t req, kvh, row0, tokens;
   int32_t pages;       // of the request that its last row may choose
-  int32_t last;        // the request's last rows
-  int32_t first;       // the first run of pages
-  int32_t pad[7];
+  int32_t flags;       // 1: the request's last rows; 2: the first run of pages
 };
-static_assert(sizeof(Item) == 64, "item record");
+static_assert(sizeof(Item) == 32, "item record");
+constexpr int32_t kLastRows = 1, kFirstRun = 2;
 __device__ __forceinline__ Item load_item(const Item* r) {
-  Item x;
   const int4* s = reinterpret_cast<const int4*>(r);
   const int4 a = s[0], b = s[1];
-  x.tiles = a.x; x.tile0 = a.y; x.req = a.z; x.kvh = a.w;
-  x.row0 = b.x; x.tokens = b.y; x.pages = b.z; x.last = b.w;
-  x.first = r->first;
-  return x;
+  return Item{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
-// Maxima over the GP lanes of a token, for 32 columns: each exchange halves the columns that a lane holds.  Afterwards a
-// lane has 32 / GP columns, from (lane % GP) * 32 / GP on, in v[0] ...
-template <int GP>
-__device__ __forceinline__ void max_over_heads(float (&v)[32], int lane) {
-  int n = 32;
-#pragma unroll
-  for (int d = GP / 2; d >= 1; d >>= 1) {
-    n >>= 1;
-    const bool up = lane & d;
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      if (c < n) {
-        const float send = up ? v[c] : v[c + n], keep = up ? v[c + n] : v[c];
-        v[c] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, d));
-      }
-    }
-  }
-}
-// Keys of a lane's N columns from col on (a multiple of N), to the keys of its token's row.  here: bit c of word k is
-// whether the page of column 4 c + k exists.
+// Largest of v[from .. from + N).
 template <int N>
-__device__ __forceinline__ void store_keys(const float* v, const uint4& here, int col, uint32_t* to) {
-  uint32_t k[N];
+__device__ __forceinline__ float largest_of(const float* v) {
+  float m = v[0];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    uint32_t word;
-    if constexpr (N >= 4) {
-      word = i % 4 == 0 ? here.x : i % 4 == 1 ? here.y : i % 4 == 2 ? here.z : here.w;
-    } else {
-      const int w = (col + i) & 3;
-      word = w == 0 ? here.x : w == 1 ? here.y : w == 2 ? here.z : here.w;
-    }
-    k[i] = word >> ((col + i) >> 2) & 1u ? choose::key_of(v[i]) : 0u;
-  }
-  if constexpr (N >= 4) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4*>(to + i) = make_uint4(k[i], k[i + 1], k[i + 2], k[i + 3]);
-  } else if constexpr (N == 2) {
-    *reinterpret_cast<uint2*>(to) = make_uint2(k[0], k[1]);
-  } else {
-    *to = k[0];
-  }
+  for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+  return m;
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
-    page_score_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmQ1,
-                      const __grid_constant__ CUtensorMap tmQT, const __grid_constant__ ChooseParams p) {
+__global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1) page_score_kernel(const __grid_constant__ CUtensorMap tmB,
+                                                                               const __grid_constant__ ChooseParams p) {
   using C = ScoreCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   const uint32_t b_full = base + C::kBarAt, b_empty = b_full + 8 * C::kStages;
-  const uint32_t b_dfull = b_empty + 8 * C::kStages, b_dempty = b_dfull + 16;
-  const uint32_t b_qfull = b_dempty + 16, b_qempty = b_qfull + 8, b_aready = b_qempty + 8, b_adone = b_aready + 8;
-  const uint32_t b_fin = b_adone + 8, b_recfull = b_fin + 8, b_recempty = b_recfull + 8 * C::kRecords;
+  const uint32_t b_dfull = b_empty + 8 * C::kStages, b_dempty = b_dfull + 8 * C::kBuffers;
+  const uint32_t b_qready = b_dempty + 8 * C::kBuffers, b_adone = b_qready + 8, b_fin = b_adone + 8;
+  const uint32_t b_recfull = b_fin + 8, b_recempty = b_recfull + 8 * C::kRecords;
   uint32_t* const here = reinterpret_cast<uint32_t*>(smem + C::kHereAt);
   float* const sums = reinterpret_cast<float*>(smem + C::kSumAt);
-  float* const cross = reinterpret_cast<float*>(smem + C::kCrossAt);
   Item* const recs = reinterpret_cast<Item*>(smem + C::kRecAt);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kTmemSlot);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -154,19 +116,17 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
     if (threadIdx.x == 0) atomicCAS(status, 0, 0x100 | kWDrain);
     return;
   }
-  constexpr int kReaders = 8 + 1 + 1 + 1 + C::kGatherWarps;   // of a record: epilogue, MMA, scan, queries, gathers
+  constexpr int kReaders = 8 + 8 + 1 + 2 + C::kGatherWarps;  // of a record: epilogue, build, MMA, scan, gathers
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(b_full + 8 * s, 2);
-      mbar_init(b_empty + 8 * s, 2);                       // the MMA and the scan
+      mbar_init(b_full + 8 * s, C::kStageWarps);
+      mbar_init(b_empty + 8 * s, 3);                       // the MMA and the scan
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kBuffers; ++i) {
       mbar_init(b_dfull + 8 * i, 1);
       mbar_init(b_dempty + 8 * i, 8);
     }
-    mbar_init(b_qfull, 1);
-    mbar_init(b_qempty, 8);
-    mbar_init(b_aready, 8);
+    mbar_init(b_qready, 8);
     mbar_init(b_adone, 1);
     mbar_init(b_fin, 1);
     for (int r = 0; r < C::kRecords; ++r) {
@@ -176,7 +136,7 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == C::kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -184,7 +144,7 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   pdl_launch_dependents();
-  const uint32_t tmem = *tmem_slot, tm_d = tmem + D;       // A: D columns (2 D values of 16 bits); D: 2 x 128
+  const uint32_t tmem = *tmem_slot;
 
   auto wait = [&](uint32_t bar, uint32_t parity, int32_t site) { return wait_for(bar, parity & 1, abort_flag, p, site); };
   // the record of item `it`, for a whole warp
@@ -202,191 +162,170 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
   };
 
   if (warp < 8) {
-    regs_inc<C::kEpilogueRegs>();
-    // ------------------------------------------------------------ splits the queries, writes the scores
-    const int wg = warp >> 2, quarter = warp & 3, row = threadIdx.x & 127;
+    // ------------------------------------------------------------ epilogue: two warpgroups share a tile's tokens
+    regs_inc<C::kWideRegs>();
+    const int wg = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const int tok = row / p.head_rows, head = row - tok * p.head_rows;
-    uint32_t jt = 0, turn = 0;
-    bool bad = false;
+    const int g = p.group;
+    const int64_t step = static_cast<int64_t>(p.n_kvheads) * p.key_stride;   // of a token's keys
+    uint32_t buf = 0, turn = 0, slot = 0;
+    for (uint32_t it = 0;; ++it) {
+      Item x;
+      if (!next(it, x)) break;
+      uint32_t* const keys = p.keys + (static_cast<int64_t>(x.row0) * p.n_kvheads + x.kvh) * p.key_stride +
+                             x.tile0 * kScoreTile + quarter * 32 + lane;
+      bool ok = true;
+      for (int j = 0; j < x.tiles; ++j) {
+        ok = __all_sync(0xffffffffu, wait(b_dfull + 8 * buf, turn, kPDFull));
+        if (!ok) break;
+        tc_fence_after();
+        const bool exists = here[slot * 4 + quarter] >> lane & 1u;
+        uint32_t* const to = keys + j * kScoreTile;
+        const uint32_t from = tmem + lanes + buf * 128;
+        auto put = [&](int t, float m) { to[t * step] = exists ? choose::key_of(m) : 0u; };
+        // sixteen columns at a time hold whole tokens where the group divides 16 (and reach past the tile's own columns
+        // nowhere but into the next buffer's)
+        const int columns = x.tokens * g;
+        if (g == 1 || g == 2 || g == 4 || g == 8) {
+          for (int c = wg * 16; c < columns; c += 32) {
+            float v[16];
+            tmem_ld16(from + c, v);
+            tc_wait_ld();
+            const int t = c / g;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (g == 1 && t + i < x.tokens) put(t + i, v[i]);
+              if (g == 2 && i % 2 == 0 && t + i / 2 < x.tokens) put(t + i / 2, largest_of<2>(v + i));
+              if (g == 4 && i % 4 == 0 && t + i / 4 < x.tokens) put(t + i / 4, largest_of<4>(v + i));
+              if (g == 8 && i % 8 == 0 && t + i / 8 < x.tokens) put(t + i / 8, largest_of<8>(v + i));
+            }
+          }
+        } else {
+          for (int t = wg; t < x.tokens; t += 2) {
+            float m = -INFINITY;
+            for (int h0 = 0; h0 < g; h0 += 16) {
+              float v[16];
+              tmem_ld16(from + t * g + h0, v);
+              tc_wait_ld();
+#pragma unroll
+              for (int h = 0; h < 16; ++h) m = h0 + h < g ? fmaxf(m, v[h]) : m;
+            }
+            put(t, m);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_dempty + 8 * buf);
+        if (++buf == C::kBuffers) {
+          buf = 0;
+          ++turn;
+        }
+        slot = (slot + 1) % C::kSlots;
+      }
+      if (!ok) break;
+    }
+    finish_role();
+    return;
+  }
+  if (warp < 16) {
+    // ------------------------------------------------------------ builds the split queries
+    regs_inc<C::kWideRegs>();
+    constexpr int kRowChunks = D / 8, kEvery = 256 / kRowChunks;   // 16-byte pieces of a row, rows between two of a thread's
+    const int tid = threadIdx.x - 32 * C::kBuildWarp0, chunk = tid % kRowChunks, row0 = tid / kRowChunks;
     for (uint32_t it = 0;; ++it) {
       Item x;
       const bool more = next(it, x);
-      if (named_bar_any(1, 256, !more || bad)) break;      // all leave together
-      const bool live = head < p.group && tok < x.tokens;
-      const bool warp_live = quarter * 32 / p.head_rows < x.tokens;   // (else the warp's rows are not looked at)
-      // the queries: this warpgroup's half of the columns, min(q, 0) or max(q, 0)
-      bad |= !wait(b_qfull, it, kPQFull);
-      if (it > 0) bad |= !wait(b_adone, it - 1, kPADone);
-      tc_fence_after();
-      float sum = 0.0f;
-      const int src = tok * p.group + head;
-      // (the sum of |q| is shared between the halves: the even and the odd blocks; one block: its even and odd words)
-#pragma unroll 1
-      for (int b = 0; b < C::kQBlocks && warp_live; ++b) {
-        uint32_t v[32];
+      if (named_bar_any(1, 256, *abort_flag != 0) || !more) break;   // all leave together
+      const int rows = x.tokens * p.group;
+      const T* const q = static_cast<const T*>(p.q) + (static_cast<int64_t>(x.row0) * p.n_qheads + x.kvh * p.group) * D + chunk * 8;
+      uint4 v[C::kChunks];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint4 y = make_uint4(0u, 0u, 0u, 0u);
-          if (live) y = ld_shared_v4(base + b * 16384 + src * 128 + ((c ^ (src & 7)) << 4));
-          v[4 * c] = y.x;
-          v[4 * c + 1] = y.y;
-          v[4 * c + 2] = y.z;
-          v[4 * c + 3] = y.w;
-        }
-        if (C::kQBlocks == 1 || (b & 1) == wg) {
-          float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (C::kQBlocks == 1 && (c & 1) != 0) continue;
-            const float2 y = choose::floats_of<T>(C::kQBlocks == 1 && wg == 1 ? v[c + 1] : v[c]);
-            s0 += fabsf(y.x);
-            s1 += fabsf(y.y);
-          }
-          sum += s0 + s1;
-        }
-#pragma unroll
-        for (int c = 0; c < 32; ++c) v[c] = wg == 0 ? choose::best2<T, false>(v[c], 0u) : choose::best2<T, true>(v[c], 0u);
-        tmem_st32(tmem + lanes + wg * (D / 2) + b * 32, v);
+      for (int i = 0; i < C::kChunks; ++i) {
+        const int r = row0 + i * kEvery, t = r / p.group;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows) v[i] = __ldg(reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(t) * p.n_qheads + (r - t * p.group)) * D));
       }
-      tc_wait_st();
-      sums[(it & 1) * 256 + wg * 128 + row] = sum;
-      tc_fence_before();
+      if (x.flags & kFirstRun) {
+#pragma unroll
+        for (int i = 0; i < C::kChunks; ++i) {
+          const float2 a = choose::floats_of<T>(v[i].x), b = choose::floats_of<T>(v[i].y), c = choose::floats_of<T>(v[i].z),
+                       d = choose::floats_of<T>(v[i].w);
+          float sum = ((fabsf(a.x) + fabsf(a.y)) + (fabsf(b.x) + fabsf(b.y))) + ((fabsf(c.x) + fabsf(c.y)) + (fabsf(d.x) + fabsf(d.y)));
+#pragma unroll
+          for (int o = kRowChunks / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (chunk == 0) sums[(it & 1) * 128 + row0 + i * kEvery] = sum;
+        }
+      }
+      if (it > 0) wait(b_adone, it - 1, kPADone);          // (a wait that runs out shows at the next vote)
+#pragma unroll
+      for (int i = 0; i < C::kChunks; ++i) {
+        const int r = row0 + i * kEvery;
+        if (r < rows) {
+          const uint32_t to = base + (chunk >> 3) * C::kBlock + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+          const uint4 y = v[i];
+          st_shared_v4(to, make_uint4(choose::best2<T, false>(y.x, 0u), choose::best2<T, false>(y.y, 0u),
+                                      choose::best2<T, false>(y.z, 0u), choose::best2<T, false>(y.w, 0u)));
+          st_shared_v4(to + C::kQBytes / 2, make_uint4(choose::best2<T, true>(y.x, 0u), choose::best2<T, true>(y.y, 0u),
+                                                       choose::best2<T, true>(y.z, 0u), choose::best2<T, true>(y.w, 0u)));
+        }
+      }
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(b_aready);
-        mbar_arrive(b_qempty);
-      }
-      if (x.first) {
+      if (lane == 0) mbar_arrive(b_qready);
+      if (x.flags & kFirstRun) {
         named_bar_sync(1, 256);
-        if (threadIdx.x < x.tokens) {
-          const float* const s = sums + (it & 1) * 256 + threadIdx.x * p.head_rows;
+        if (tid < x.tokens) {
+          const float* const s = sums + (it & 1) * 128 + tid * p.group;
           uint32_t most = 0;                               // (bits of non-negative floats have their order, NaN above all)
-          for (int h = 0; h < p.group; ++h) most = max(most, __float_as_uint(s[h] + s[128 + h]) & 0x7fffffffu);
-          p.reach[(static_cast<int64_t>(x.row0) + threadIdx.x) * p.n_kvheads + x.kvh] = __uint_as_float(most);
-        }
-      }
-      uint32_t* const keys = p.keys + ((static_cast<int64_t>(x.row0) + tok) * p.n_kvheads + x.kvh) * p.key_stride;
-      for (int j = 0; j < x.tiles; ++j, ++jt) {
-        bad |= !wait(b_dfull + 8 * (jt & 1), jt >> 1, kPDFull);
-        tc_fence_after();
-        const uint4 exist = *reinterpret_cast<const uint4*>(here + (jt % C::kSlots) * 4);
-        if (!warp_live && p.head_rows <= 32) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b_dempty + 8 * (jt & 1));
-          continue;
-        }
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          float v[32];
-          tmem_ld32(tm_d + lanes + (jt & 1) * kScoreTile + wg * 64 + half * 32, v);
-          tc_wait_ld();
-          if (half == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_dempty + 8 * (jt & 1));
-          }
-          if (!live) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = -INFINITY;
-          }
-          const int col = wg * 64 + half * 32;             // of the tile
-          uint32_t* const to = keys + (x.tile0 + j) * kScoreTile + col;
-          const bool store = tok < x.tokens;
-          switch (p.head_rows) {
-            case 1:
-              if (store) store_keys<32>(v, exist, col, to);
-              break;
-            case 2: {
-              max_over_heads<2>(v, lane);
-              const int c = (lane & 1) * 16;
-              if (store) store_keys<16>(v, exist, col + c, to + c);
-              break;
-            }
-            case 4: {
-              max_over_heads<4>(v, lane);
-              const int c = (lane & 3) * 8;
-              if (store) store_keys<8>(v, exist, col + c, to + c);
-              break;
-            }
-            case 8: {
-              max_over_heads<8>(v, lane);
-              const int c = (lane & 7) * 4;
-              if (store) store_keys<4>(v, exist, col + c, to + c);
-              break;
-            }
-            case 16: {
-              max_over_heads<16>(v, lane);
-              const int c = (lane & 15) * 2;
-              if (store) store_keys<2>(v, exist, col + c, to + c);
-              break;
-            }
-            case 32: {
-              max_over_heads<32>(v, lane);
-              if (store) store_keys<1>(v, exist, col + lane, to + lane);
-              break;
-            }
-            default: {                                     // 64 or 128: two or four warps hold a token's heads
-              max_over_heads<32>(v, lane);
-              float* const m = cross + ((turn & 1) * 2 + wg) * 128;
-              ++turn;
-              m[quarter * 32 + lane] = v[0];
-              named_bar_sync(2 + wg, 128);
-              if (store && head < 32) {
-                for (int w = 1; w < p.head_rows / 32; ++w) v[0] = fmaxf(v[0], m[(quarter + w) * 32 + lane]);
-                store_keys<1>(v, exist, col + lane, to + lane);
-              }
-            }
-          }
+          for (int h = 0; h < p.group; ++h) most = max(most, __float_as_uint(s[h]) & 0x7fffffffu);
+          p.reach[(static_cast<int64_t>(x.row0) + tid) * p.n_kvheads + x.kvh] = __uint_as_float(most);
         }
       }
     }
     finish_role();
     return;
-  } else if (warp == 8) {
+  }
+  regs_dec<C::kRoleRegs>();
+  if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer, tensor-memory owner
-    constexpr uint32_t kIdesc = std::is_same<T, __half>::value ? idesc_f16_f32(128, kScoreTile, false, false)
-                                                               : idesc_bf16_f32(128, kScoreTile, false, false);
+    constexpr uint32_t kIdesc = std::is_same<T, __half>::value ? idesc_f16_f32(128, 0, false, false)
+                                                               : idesc_bf16_f32(128, 0, false, false);
     constexpr uint32_t kHi = sw128_desc_hi(1024);
-    const uint32_t ring_lo = sw128_desc_lo(base + C::kRingAt, 16);
-    RingPos st;
-    uint32_t jt = 0;
-    bool stop = false;
-    for (uint32_t it = 0; !stop; ++it) {
-      Item x;
-      if (!next(it, x)) break;
-      if (!__all_sync(0xffffffffu, wait(b_aready, it, kPAReady))) {
-        stop = true;
-        break;
-      }
-      for (int j = 0; j < x.tiles && !stop; ++j, ++jt) {
-        if (jt >= 2 && !__all_sync(0xffffffffu, wait(b_dempty + 8 * (jt & 1), (jt >> 1) - 1, kPDEmpty))) {
-          stop = true;
-          break;
-        }
-        for (int b = 0; b < C::kBlocks; ++b) {
-          if (!__all_sync(0xffffffffu, wait(b_full + 8 * st.st, st.par, kPStageFull))) {
-            stop = true;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
+    const uint32_t q_lo = sw128_desc_lo(base, 16), ring_lo = sw128_desc_lo(base + C::kRingAt, 16);
+    if (lane == 0) {       // one thread issues; the others wait for it below
+      RingPos st, d;
+      uint32_t jt = 0;
+      bool go = true;
+      for (uint32_t it = 0; go; ++it) {
+        const uint32_t r = it % C::kRecords;
+        if (!wait(b_recfull + 8 * r, it / C::kRecords, kPRecFull)) break;
+        const int32_t tiles = recs[r].tiles, columns = recs[r].tokens * p.group;
+        mbar_arrive(b_recempty + 8 * r);
+        if (tiles < 0 || !wait(b_qready, it, kPQReady)) break;
+        const uint32_t idesc = kIdesc | static_cast<uint32_t>((columns + 15) / 16 * 2) << 17;   // N / 8
+        for (int j = 0; j < tiles && go; ++j, ++jt) {
+          if (jt >= C::kBuffers) go = wait(b_dempty + 8 * d.st, d.par ^ 1, kPDEmpty);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma_ta(tm_d + (jt & 1) * kScoreTile, tmem + b * 32 + k * 8,
-                        ring_lo + st.st * (C::kStageBytes >> 4) + k * 2, kHi, kIdesc, b > 0 || k > 0 ? 1u : 0u);
-            tc_commit(b_empty + 8 * st.st);
-            if (b == C::kBlocks - 1) {
-              tc_commit(b_dfull + 8 * (jt & 1));
-              if (j == x.tiles - 1) tc_commit(b_adone);
+          for (int s = 0; s < C::kPer; ++s) {
+            go = go && wait(b_full + 8 * st.st, st.par, kPStageFull);
+            if (!go) break;
+            tc_fence_after();
+            const uint32_t a = ring_lo + st.st * (C::kStageBytes >> 4), b = q_lo + s * (2 * C::kBlock >> 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
+              tc_mma_w(tmem + d.st * 128, a + off, kHi, b + off, kHi, idesc, s > 0 || k > 0 ? 1u : 0u);
             }
+            tc_commit(b_empty + 8 * st.st);
+            ring_next(st, C::kStages);
           }
-          __syncwarp();
-          ring_next(st, C::kStages);
+          if (go) {
+            tc_commit(b_dfull + 8 * d.st);
+            if (j == tiles - 1) tc_commit(b_adone);
+            ring_next(d, C::kBuffers);
+          }
         }
       }
-    }
-    if (lane == 0) {
       tc_commit(b_fin);
       drain(b_fin, 0, status, kDrainNs);
     }
@@ -395,45 +334,47 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
     return;
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ scan: the largest |bound| of every tile of pages
+  } else if (warp == C::kScanWarp || warp == C::kScanWarp + 1) {
+    // ------------------------------------------------------------ scan: the largest |bound| of every 64 pages
+    const int part = warp - C::kScanWarp;
     RingPos st;
     for (uint32_t it = 0;; ++it) {
       Item x;
       if (!next(it, x)) break;
+      const bool look = x.flags & kLastRows;
       bool ok = true;
       for (int j = 0; j < x.tiles && ok; ++j) {
-        uint32_t most = 0;                                 // two 16-bit magnitudes, in the upper halves of two words
-        uint32_t most2 = 0;
-        for (int b = 0; b < C::kBlocks && ok; ++b) {
+        uint32_t most = 0, most2 = 0;                      // of pairs
+        for (int s = 0; s < C::kPer && ok; ++s) {
           ok = __all_sync(0xffffffffu, wait(b_full + 8 * st.st, st.par, kPStageFull));
-          if (ok && x.last) {
-            const uint32_t at = base + C::kRingAt + st.st * C::kStageBytes + lane * 16;
+          if (ok && look) {
+            const uint32_t at = base + C::kRingAt + st.st * C::kStageBytes + part * 8192 + lane * 16;
 #pragma unroll 8
-            for (int i = 0; i < C::kStageBytes / 512; ++i) {
-              const uint4 y = ld_shared_v4(at + i * 512);
-              most = max(most, max(max(y.x & 0x7fff0000u, y.y & 0x7fff0000u), max(y.z & 0x7fff0000u, y.w & 0x7fff0000u)));
-              most2 = max(most2, max(max(y.x << 17, y.y << 17), max(y.z << 17, y.w << 17)));
+            for (int i = 0; i < 32; ++i) {                 // two blocks of 64 dims, 64 pages of each
+              const uint4 y = ld_shared_v4(at + (i >> 4) * C::kBlock + (i & 15) * 512);
+              most = choose::largest2<T>(most, y.x);
+              most2 = choose::largest2<T>(most2, y.y);
+              most = choose::largest2<T>(most, y.z);
+              most2 = choose::largest2<T>(most2, y.w);
             }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(b_empty + 8 * st.st);
           ring_next(st, C::kStages);
         }
-        most = max(most, most2 >> 1) >> 16;
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (x.last && lane == 0) {
-          const float2 f = choose::floats_of<T>(most);
-          p.largest[(static_cast<int64_t>(x.req) * p.n_kvheads + x.kvh) * p.page_tiles + x.tile0 + j] = f.x;
-        }
+        if (!look) continue;
+        most = choose::largest2<T>(most, most2);
+        most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));   // (as bits: NaN above all)
+        const int32_t at = (x.tile0 + j) * 2 + part;
+        if (lane == 0 && at < p.bound_tiles)
+          p.largest[(static_cast<int64_t>(x.req) * p.n_kvheads + x.kvh) * p.bound_tiles + at] = choose::floats_of<T>(most).x;
       }
       if (!ok) break;
     }
     finish_role();
     return;
-  } else if (warp == 10) {
+  } else if (warp == C::kSchedulerWarp) {
     // ------------------------------------------------------------ scheduler
-    const int64_t first = blockIdx.x;
     uint32_t it = 0;
     auto put = [&](const Item& x) -> bool {
       const uint32_t r = it % C::kRecords;
@@ -441,8 +382,7 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
       if (lane == 0) {
         int4* const to = reinterpret_cast<int4*>(recs + r);
         to[0] = make_int4(x.tiles, x.tile0, x.req, x.kvh);
-        to[1] = make_int4(x.row0, x.tokens, x.pages, x.last);
-        recs[r].first = x.first;
+        to[1] = make_int4(x.row0, x.tokens, x.pages, x.flags);
         mbar_arrive(b_recfull + 8 * r);
       }
       __syncwarp();
@@ -450,8 +390,8 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
       return true;
     };
     bool ok = !p.stall_first_item;
-    for (int64_t n = first; n < p.n_items && ok; n += gridDim.x) {
-      const int32_t unit = static_cast<int32_t>(n) / p.runs, run = static_cast<int32_t>(n) - unit * p.runs;
+    for (int64_t n = blockIdx.x; n < p.n_items && ok; n += gridDim.x) {
+      const int32_t run = static_cast<int32_t>(n) / p.units, unit = static_cast<int32_t>(n) - run * p.units;
       const int32_t tile = unit / p.n_kvheads;
       Item x{};
       x.kvh = unit - tile * p.n_kvheads;
@@ -473,14 +413,13 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
       if (r0 < 0 || t0 < 0 || r0 + t0 >= r1) continue;
       x.row0 = static_cast<int32_t>(r0 + t0);
       x.tokens = static_cast<int32_t>(min(r1 - r0 - t0, static_cast<int64_t>(p.tile_tokens)));
-      x.last = r0 + t0 + x.tokens == r1;
+      x.flags = (r0 + t0 + x.tokens == r1 ? kLastRows : 0) | (run == 0 ? kFirstRun : 0);
       const int64_t p_last = kv - (r1 - r0) + t0 + x.tokens - 1;
       if (p_last < 0) continue;
       const int32_t own = p.pa.page_shift >= 0 ? static_cast<int32_t>(p_last >> p.pa.page_shift)
                                                : static_cast<int32_t>(p_last) / p.pa.page_size;   // (p_last < kv)
       x.pages = min(own + 1, p.pa.pages_per_req);
       if (x.pages <= p.n_select) continue;                 // all of them are chosen
-      x.first = run == 0;
       x.tile0 = run * p.run_tiles;
       x.tiles = min((x.pages + kScoreTile - 1) / kScoreTile - x.tile0, p.run_tiles);
       if (x.tiles <= 0) continue;
@@ -491,112 +430,62 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
     if (ok) put(end);
     finish_role();
     return;
-  } else if (warp == 11) {
-    // ------------------------------------------------------------ queries
-    if (lane == 0) {
-      prefetch_tmap(&tmQ1);
-      prefetch_tmap(&tmQT);
-      prefetch_tmap(&tmB);
-    }
-    uint32_t loaded = 0;
-    for (uint32_t it = 0;; ++it) {
-      Item x;
-      if (!next(it, x)) break;
-      if (it > 0 && !__all_sync(0xffffffffu, wait(b_qempty, it - 1, kPQEmpty))) break;
-      const uint32_t tok_bytes = static_cast<uint32_t>(p.group) * 128u;
-      const bool whole = x.tokens == p.tile_tokens;
-      if (lane == 0) mbar_arrive_expect_tx(b_qfull, static_cast<uint32_t>(x.tokens) * tok_bytes * C::kQBlocks);
-      __syncwarp();
-      const int loads = whole ? C::kQBlocks : x.tokens * C::kQBlocks;
-      for (int i = lane; i < loads; i += 32) {
-        const int b = i % C::kQBlocks, t = i / C::kQBlocks;
-        tma_load_3d(base + b * 16384 + t * tok_bytes, whole ? &tmQT : &tmQ1, b * 64, x.kvh * p.group, x.row0 + t, b_qfull);
-      }
-      ++loaded;
-    }
-    if (*abort_flag && loaded > 0 && lane == 0) drain(b_qfull, (loaded - 1) & 1, status, kDrainNs);
-    __syncwarp();
-    finish_role();
-    return;
   }
-  // -------------------------------------------------------------- gathers: pairs of warps take the blocks in turn, each
-  // half of a block's pages
-  regs_dec<C::kGatherRegs>();
-  const int gw = (warp - C::kGatherWarp0) >> 1, part = warp & 1;
-  constexpr int kPairs = C::kGatherWarps / 2, kEvery = kPairs / C::kBlocks;   // tiles between two of a pair's
-  const int block = gw % C::kBlocks, tile_turn = gw / C::kBlocks;
-  uint32_t jt = 0, issued = 0;
-  Item x{};
-  uint32_t it = 0;
-  int j = 0;
-  bool more = next(it, x), stop = false;
-  struct Rows {
-    int32_t r[4];
-    uint32_t here;
+  // -------------------------------------------------------------- gathers: four warps a stage, each 32 of the pages
+  constexpr int kGroups = C::kGatherWarps / C::kStageWarps;
+  const int gw = warp - C::kGatherWarp0, part = gw % C::kStageWarps;
+  uint32_t n = gw / C::kStageWarps, tile = 0, it = 0, issued = 0;   // stages: n, n + kGroups ..; tiles so far; items
+  Item y{};                                                // of the next tile
+  int k = 0;
+  bool more = next(it, y), stop = false;
+  if (lane == 0) prefetch_tmap(&tmB);
+  // the page id of this lane's page in tile t of item z, or -1
+  auto look_up = [&](const Item& z, int t) -> int32_t {
+    const int32_t e = (z.tile0 + t) * kScoreTile + part * 32 + lane;
+    const int32_t id = e < z.pages ? __ldg(p.pa.page_table + static_cast<int64_t>(z.req) * p.pa.pages_per_req + e) : -1;
+    return id < p.pa.n_pages ? id : -1;
   };
-  // page ids of the four pages of lane l (of 32) in tile t of item y
-  auto look_up = [&](const Item& y, int t, int l) {
-    Rows k;
-    k.here = 0;
-    const int32_t e0 = (y.tile0 + t) * kScoreTile + l * 4;
-    const int32_t* const table = p.pa.page_table + static_cast<int64_t>(y.req) * p.pa.pages_per_req;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int32_t id = e0 + i < y.pages ? __ldg(table + e0 + i) : -1;
-      const bool in = id >= 0 && id < p.pa.n_pages;
-      k.r[i] = static_cast<int32_t>((in ? id : p.pa.n_pages) * p.n_kvheads + (in ? y.kvh : 0));   // (past the end: zeros)
-      k.here |= (in ? 1u : 0u) << i;
+  int32_t id_next = more ? look_up(y, 0) : -1;
+  const int32_t past = static_cast<int32_t>(p.pa.n_pages) * p.n_kvheads;   // (the row past the end: zeros)
+  while (!stop && more) {
+    // this tile's ids are here; the next tile's are on their way while it is gathered
+    const int32_t id = id_next, kvh = y.kvh;
+    if (++k >= y.tiles) {
+      k = 0;
+      more = next(++it, y);
     }
-    return k;
-  };
-  // the pair's next tile from (it, x, j) on
-  auto seek = [&]() {
-    while (more) {
-      if (j >= x.tiles) {
-        ++it;
-        j = 0;
-        more = next(it, x);
-        continue;
+    if (more) id_next = look_up(y, k);
+    const uint32_t exist = __ballot_sync(0xffffffffu, id >= 0);
+    const int32_t row = id >= 0 ? id * p.n_kvheads + kvh : past;
+    int32_t r[4];                                          // lanes 0-7 and 8-15: the four pages of each gather
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __shfl_sync(0xffffffffu, row, (lane & 7) * 4 + i);
+    for (; n < (tile + 1) * C::kPer; n += kGroups) {
+      const uint32_t s = n % C::kStages;
+      if (n >= C::kStages && !__all_sync(0xffffffffu, wait(b_empty + 8 * s, n / C::kStages - 1, kPStageEmpty))) {
+        stop = true;
+        break;
       }
-      if (jt % kEvery == static_cast<uint32_t>(tile_turn)) return;
-      ++j;
-      ++jt;
+      if (lane == 0) {
+        here[(tile % C::kSlots) * 4 + part] = exist;       // (each group writes the same)
+        mbar_arrive_expect_tx(b_full + 8 * s, C::kStageBytes / C::kStageWarps);
+      }
+      __syncwarp();
+      if (lane < 16) {
+        const int block = lane >> 3;
+        tma_gather4(base + C::kRingAt + s * C::kStageBytes + block * C::kBlock + part * 4096 + (lane & 7) * 512, &tmB,
+                    static_cast<int32_t>(n - tile * C::kPer) * 128 + block * 64, r[0], r[1], r[2], r[3], b_full + 8 * s);
+      }
+      issued = n + 1;
     }
-  };
-  const int mine = part * 16 + (lane & 15);                // lanes 0-15 gather; all look up, for the pages that exist
-  seek();
-  Rows rows{};
-  if (more) rows = look_up(x, j, part == 0 && block == 0 ? lane : mine);
-  while (more) {
-    const uint32_t tile = jt, n = tile * C::kBlocks + block, s = n % C::kStages;
-    const Rows now = rows;
-    if (n >= C::kStages && !__all_sync(0xffffffffu, wait(b_empty + 8 * s, n / C::kStages - 1, kPStageEmpty))) {
-      stop = true;
-      break;
-    }
-    if (block == 0 && part == 0) {
-      uint32_t m[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m[i] = __ballot_sync(0xffffffffu, now.here >> i & 1u);
-      if (lane == 0) *reinterpret_cast<uint4*>(here + (tile % C::kSlots) * 4) = make_uint4(m[0], m[1], m[2], m[3]);
-    }
-    if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * s, C::kStageBytes / 2);
-    __syncwarp();
-    if (lane < 16)
-      tma_gather4(base + C::kRingAt + s * C::kStageBytes + mine * 512, &tmB, block * 64, now.r[0], now.r[1], now.r[2],
-                  now.r[3], b_full + 8 * s);
-    issued = n + 1;
-    ++j;
-    ++jt;
-    seek();
-    if (more) rows = look_up(x, j, part == 0 && block == 0 ? lane : mine);
+    ++tile;
   }
   if (issued > 0 && lane == 0 && (stop || *abort_flag)) {
     // this warp's copies that may still be in flight: of the last ring
     const uint32_t last = issued - 1;
-    for (uint32_t n = last; last - n < static_cast<uint32_t>(C::kStages); n -= kPairs) {
-      drain(b_full + 8 * (n % C::kStages), (n / C::kStages) & 1, status, kDrainNs / 100);
-      if (n < static_cast<uint32_t>(kPairs)) break;
+    for (uint32_t m = last; last - m < static_cast<uint32_t>(C::kStages); m -= kGroups) {
+      drain(b_full + 8 * (m % C::kStages), (m / C::kStages) & 1, status, kDrainNs / 100);
+      if (m < static_cast<uint32_t>(kGroups)) break;
     }
   }
   __syncwarp();
@@ -604,8 +493,7 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1)
 }
 
 template <int D, typename T>
-cudaError_t launch_score_dim(const ChooseParams& p, const CUtensorMap& tb, const CUtensorMap& tq1, const CUtensorMap& tqt,
-                             int grid, int which, cudaStream_t stream) {
+cudaError_t launch_score_dim(const ChooseParams& p, const CUtensorMap& tb, int grid, int which, cudaStream_t stream) {
   using C = ScoreCfg<D>;
   auto kern = page_score_kernel<D, T>;
   const cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern), C::kSmem, kOptScore + which);
@@ -616,35 +504,28 @@ cudaError_t launch_score_dim(const ChooseParams& p, const CUtensorMap& tb, const
     return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
   }();
   if (regs < C::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  kern<<<grid, C::kThreads, C::kSmem, stream>>>(tb, tq1, tqt, p);
+  kern<<<grid, C::kThreads, C::kSmem, stream>>>(tb, p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_page_score(const ChooseParams& p, bool fp16, int num_sms, cudaStream_t stream) {
-  const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;   // (16 bits are moved either way)
   const cuuint64_t d = static_cast<cuuint64_t>(p.head_dim);
-  CUtensorMap tb{}, tq1{}, tqt{};
-  const cuuint64_t b_dims[2] = {2 * d, static_cast<cuuint64_t>(p.pa.n_pages) * static_cast<cuuint64_t>(p.n_kvheads)};
-  const cuuint64_t b_strides[1] = {4 * d};
-  const cuuint32_t b_box[2] = {64, 1};
-  CUresult r = encode_tensor_map(&tb, type, 2, p.bounds, b_dims, b_strides, b_box);
-  const cuuint64_t q_dims[3] = {d, static_cast<cuuint64_t>(p.n_qheads), static_cast<cuuint64_t>(p.n_rows)};
-  const cuuint64_t q_strides[2] = {d * 2, d * 2 * static_cast<cuuint64_t>(p.n_qheads)};
-  const cuuint32_t q_box1[3] = {64, static_cast<cuuint32_t>(p.group), 1};
-  const cuuint32_t q_boxt[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(p.tile_tokens)};
-  if (r == CUDA_SUCCESS) r = encode_tensor_map(&tq1, type, 3, p.q, q_dims, q_strides, q_box1);
-  if (r == CUDA_SUCCESS) r = encode_tensor_map(&tqt, type, 3, p.q, q_dims, q_strides, q_boxt);
-  if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  const cuuint64_t dims[2] = {2 * d, static_cast<cuuint64_t>(p.pa.n_pages) * static_cast<cuuint64_t>(p.n_kvheads)};
+  const cuuint64_t strides[1] = {4 * d};
+  const cuuint32_t box[2] = {64, 1};                       // (gathers of four rows; 16 bits are moved, whichever type)
+  CUtensorMap tb{};
+  if (encode_tensor_map(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.bounds, dims, strides, box) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   const int grid = static_cast<int>(p.n_items < num_sms ? p.n_items : num_sms);
   if (fp16)
-    return p.head_dim == 64    ? launch_score_dim<64, __half>(p, tb, tq1, tqt, grid, 0, stream)
-           : p.head_dim == 128 ? launch_score_dim<128, __half>(p, tb, tq1, tqt, grid, 1, stream)
-                               : launch_score_dim<256, __half>(p, tb, tq1, tqt, grid, 2, stream);
-  return p.head_dim == 64    ? launch_score_dim<64, __nv_bfloat16>(p, tb, tq1, tqt, grid, 3, stream)
-         : p.head_dim == 128 ? launch_score_dim<128, __nv_bfloat16>(p, tb, tq1, tqt, grid, 4, stream)
-                             : launch_score_dim<256, __nv_bfloat16>(p, tb, tq1, tqt, grid, 5, stream);
+    return p.head_dim == 64    ? launch_score_dim<64, __half>(p, tb, grid, 0, stream)
+           : p.head_dim == 128 ? launch_score_dim<128, __half>(p, tb, grid, 1, stream)
+                               : launch_score_dim<256, __half>(p, tb, grid, 2, stream);
+  return p.head_dim == 64    ? launch_score_dim<64, __nv_bfloat16>(p, tb, grid, 3, stream)
+         : p.head_dim == 128 ? launch_score_dim<128, __nv_bfloat16>(p, tb, grid, 4, stream)
+                             : launch_score_dim<256, __nv_bfloat16>(p, tb, grid, 5, stream);
 }
 
 }  // namespace qsa

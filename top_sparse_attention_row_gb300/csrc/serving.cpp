@@ -304,7 +304,7 @@ ScorePlan plan_scores(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, int
   const size_t rows = static_cast<size_t>(n_rows) * n_kvheads;
   s.reach_at = rows * s.page_tiles * qsa::kScoreTile * 4;
   s.largest_at = s.reach_at + round_256(rows * 4);
-  s.bytes = s.largest_at + round_256(static_cast<size_t>(n_requests) * n_kvheads * s.page_tiles * 4);
+  s.bytes = s.largest_at + round_256(static_cast<size_t>(n_requests) * n_kvheads * s.page_tiles * (qsa::kScoreTile / qsa::kBoundTile) * 4);
   return s;
 }
 
@@ -539,18 +539,17 @@ qsa_status qsa_page_select(const void* q, const void* bounds, const int32_t* cu_
   p.n_first = n_first;
   p.n_last = n_last;
   const ScorePlan plan = plan_scores(n_rows, n_requests, n_kvheads, pages_per_req);
-  p.page_tiles = plan.page_tiles;
   p.key_stride = plan.page_tiles * qsa::kScoreTile;
-  p.head_rows = 1;
-  while (p.head_rows < p.group) p.head_rows *= 2;
-  p.tile_tokens = qsa::kScoreTile / p.head_rows;
+  p.bound_tiles = p.key_stride / qsa::kBoundTile;
+  p.tile_tokens = 128 / p.group;
   // A run is as many of a query tile's page tiles as leave every SM a dozen items: long runs split the queries less often,
   // short ones spread few query tiles over the SMs.
   const int64_t units = (n_rows / p.tile_tokens + n_requests) * n_kvheads, each = units * plan.page_tiles / (sms * int64_t{12});
-  p.run_tiles = each < 1 ? 1 : each < plan.page_tiles ? static_cast<int32_t>(each) : plan.page_tiles;
-  p.runs = (plan.page_tiles + p.run_tiles - 1) / p.run_tiles;
-  p.n_items = units * p.runs;
+  const int32_t runs = each < 1 ? plan.page_tiles : each < plan.page_tiles ? (plan.page_tiles + static_cast<int32_t>(each) - 1) / static_cast<int32_t>(each) : 1;
+  p.run_tiles = (plan.page_tiles + runs - 1) / runs;
+  p.n_items = units * runs;
   if (p.n_items > INT32_MAX) return QSA_ERR_UNSUPPORTED;
+  p.units = static_cast<int32_t>(units);
   p.wait_ns = qsa::kWinWaitNs + qsa::kWinWaitNsPerTile * static_cast<unsigned long long>(p.run_tiles);
   if (qsa::device_status_address(&p.status) != cudaSuccess) return QSA_ERR_CUDA;
   void* ws = workspace;
