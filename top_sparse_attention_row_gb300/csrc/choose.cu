@@ -234,10 +234,14 @@ __device__ __forceinline__ uint64_t exact_key(const T* q, const T* bounds, int g
 }
 
 // A team of threads takes a row and KV head: a warp where there are many, else a block.  A lane has N of its pages' keys.
+// (Blocks of four warps: a row whose close scores are summed anew takes several times as long as the others, and holds up
+// few of them.)
+constexpr int kWarpTeams = 4;
 template <int D, typename T, int TEAM, int N>
-__global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM) page_select_kernel(const __grid_constant__ ChooseParams p) {
+__global__ void __launch_bounds__(TEAM == 32 ? 32 * kWarpTeams : TEAM, TEAM == 32 && N <= 16 ? 8 : 1)
+    page_select_kernel(const __grid_constant__ ChooseParams p) {
   using namespace choose;
-  constexpr int kTeams = TEAM == 32 ? 8 : 1;
+  constexpr int kTeams = TEAM == 32 ? kWarpTeams : 1;
   __shared__ uint32_t scratch[TEAM == 32 ? 1 : Team<TEAM>::kScratch];
   pdl_wait();
   Team<TEAM> team(scratch);
@@ -294,13 +298,13 @@ __global__ void __launch_bounds__(TEAM == 32 ? 256 : TEAM) page_select_kernel(co
 
 template <int D, typename T, int TEAM, int N>
 cudaError_t launch_select_team(const ChooseParams& p, cudaStream_t stream) {
-  constexpr int kTeams = TEAM == 32 ? 8 : 1;
+  constexpr int kTeams = TEAM == 32 ? kWarpTeams : 1;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // starts while the scores are taken
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>((p.n_rows * p.n_kvheads + kTeams - 1) / kTeams));
-  cfg.blockDim = dim3(TEAM == 32 ? 256 : TEAM);
+  cfg.blockDim = dim3(TEAM == 32 ? 32 * kWarpTeams : TEAM);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

@@ -368,9 +368,13 @@ bool plan_prefix(int64_t n_rows, int32_t n_requests, int32_t n_groups, int32_t n
   l->w.n_units = units;
   l->w.n_tiles = static_cast<int32_t>(units);
   l->w.shares = sms;
-  // (as plan_window) units with rows, at least the requests' own
-  l->w.unit_cost = ((n_rows + l->w.tile_tokens - 1) / l->w.tile_tokens + n_requests - 1) * n_kvheads > sms ? 3 : 0;
   l->w.key_tiles = static_cast<int32_t>((static_cast<int64_t>(pages_per_req) * page_size + qsa::kWinTile - 1) / qsa::kWinTile);
+  // (as plan_window) What a unit costs beside its tiles counts where a block has several units.  Not where there are few
+  // tiles for the SMs: then a unit's tiles are worth dividing to the last (four rows behind a prompt of 2048, 24/2 heads:
+  // 23 us), and its cost would be taken for work that other blocks cannot do.  Counted as none, a block got 25 requests' own
+  // keys where another got 25 tiles of the prompt (64 rows behind a prompt of 32k: 112 us instead of KKK).
+  const int64_t row_tiles = (n_rows + l->w.tile_tokens - 1) / l->w.tile_tokens;
+  l->w.unit_cost = row_tiles * n_kvheads * l->w.key_tiles > 4 * static_cast<int64_t>(sms) ? 3 : 0;
   const int32_t group_heads = n_kvheads * group;
   lay_out(l, head_dim, static_cast<size_t>(units), static_cast<size_t>(tiles + n_requests) * n_kvheads, 0,
           2 * static_cast<size_t>(n_rows) * group_heads, static_cast<size_t>(sms) * qsa::kWinTile * (static_cast<size_t>(head_dim) + 1) * 4);
@@ -542,10 +546,12 @@ qsa_status qsa_page_select(const void* q, const void* bounds, const int32_t* cu_
   p.key_stride = plan.page_tiles * qsa::kScoreTile;
   p.bound_tiles = p.key_stride / qsa::kBoundTile;
   p.tile_tokens = 128 / p.group;
-  // A run is as many of a query tile's page tiles as leave every SM a dozen items: long runs split the queries less often,
-  // short ones spread few query tiles over the SMs.
+  // Splitting a tile's queries takes as long as two or three of its page tiles: with units for all SMs (four each) a unit is
+  // one item.  Few units are cut into runs of page tiles, a dozen for every SM.
   const int64_t units = (n_rows / p.tile_tokens + n_requests) * n_kvheads, each = units * plan.page_tiles / (sms * int64_t{12});
-  const int32_t runs = each < 1 ? plan.page_tiles : each < plan.page_tiles ? (plan.page_tiles + static_cast<int32_t>(each) - 1) / static_cast<int32_t>(each) : 1;
+  const int32_t runs = units >= 4 * static_cast<int64_t>(sms) || each >= plan.page_tiles ? 1
+                       : each < 1 ? plan.page_tiles
+                                  : (plan.page_tiles + static_cast<int32_t>(each) - 1) / static_cast<int32_t>(each);
   p.run_tiles = (plan.page_tiles + runs - 1) / runs;
   p.n_items = units * runs;
   if (p.n_items > INT32_MAX) return QSA_ERR_UNSUPPORTED;
