@@ -625,7 +625,8 @@ qsa_status qsa_probe_gather_ceiling(const void* cache, int64_t n_rows, const int
                                     int32_t engine, float* ms_out, void* stream);
 
 /* Failure-detection test hook (no counterpart on the pages): the next attention call
- * (qsa_sparse_prefill*, qsa_sparse_mla_prefill) launches with its index warps withholding their
+ * (qsa_sparse_prefill*, qsa_sparse_mla_prefill, qsa_window_attention*, qsa_selected_attention_paged,
+ * qsa_prefix_attention_paged) or qsa_page_select launches with its index warps withholding their
  * items, so every other role's bounded wait (2 s) runs out.  The kernel records
  * 0x100 | wait site in the device status word, abandons the call (its outputs are unspecified),
  * frees its tensor memory and returns; the context stays usable and qsa_get_device_status then

@@ -289,9 +289,10 @@ __global__ void __launch_bounds__(TEAM == 32 ? 32 * kWarpTeams : TEAM, TEAM == 3
   const T* const q = static_cast<const T*>(p.q) + (row * p.n_qheads + static_cast<int64_t>(kvh) * p.group) * D;
   const T* const bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(kvh) * 2 * D;
   choose::choose(team, keys, p.n_select, eps,
-                 [&](int32_t e) {
-                   return exact_key<D>(q, bounds + static_cast<int64_t>(__ldg(table + e)) * p.n_kvheads * 2 * D, p.group,
-                                       lane, reach, wide);
+                 [&](int32_t e) -> uint64_t {
+                   const int32_t page = __ldg(table + e);
+                   if (page < 0 || page >= p.pa.n_pages) return 0;   // (has no key, unless the scores were given up)
+                   return exact_key<D>(q, bounds + static_cast<int64_t>(page) * p.n_kvheads * 2 * D, p.group, lane, reach, wide);
                  },
                  out);
 }

@@ -402,9 +402,10 @@ struct ListParams {
   int32_t prefix_tiles;         // tiles of the groups, which come first; then those of the requests
   int32_t n_tiles;              // both, or of chosen pages all
   int32_t grain;                // keys per TMA box, or 4
+  int32_t run;                  // shared prompts: tiles that a warp lists
 };
 cudaError_t launch_list_pages(const ListParams& p, cudaStream_t stream);
-cudaError_t launch_list_prefix(const ListParams& p, cudaStream_t stream);
+cudaError_t launch_list_prefix(ListParams p, cudaStream_t stream);
 // Joins the results of shared prompts' rows.
 cudaError_t launch_join_prefix(const WindowParams& p, const ListParams& l, int head_dim, bool fp16, cudaStream_t stream);
 cudaError_t launch_window(const WindowParams& p, int head_dim, bool fp16, bool fp4, const void* k_cache,

@@ -181,15 +181,15 @@ __device__ __forceinline__ Group make_group(const ListParams& p, int32_t g, int 
   return x;
 }
 
-constexpr int kPrefixWarps = 4, kPrefixRun = 4;   // warps of a block, tiles of a warp
+constexpr int kPrefixWarps = 4;   // of a block
 
 __global__ void __launch_bounds__(kPrefixWarps * 32) list_prefix_kernel(const __grid_constant__ ListParams p) {
   const int lane = threadIdx.x & 31;
   pdl_launch_dependents();
   const int32_t tiles = p.n_tiles / p.n_kvheads;
-  const int32_t t_first = (static_cast<int32_t>(blockIdx.x) * kPrefixWarps + (threadIdx.x >> 5)) * kPrefixRun;
+  const int32_t t_first = (static_cast<int32_t>(blockIdx.x) * kPrefixWarps + (threadIdx.x >> 5)) * p.run;
   Group group{-1, 0, 0, 0, 0};
-  for (int32_t t = t_first; t < min(t_first + kPrefixRun, tiles); ++t) {
+  for (int32_t t = t_first; t < min(t_first + p.run, tiles); ++t) {
     Unit u{};
     u.tiles = -2;
     OwnUnit own{0, -1, 0, 0};
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   if (own.prefix_unit >= 0) {
     const int32_t ahead = static_cast<int32_t>(token) - own.group_row0, tile = ahead / p.tile_tokens;
     const int32_t from = own.prefix_unit + tile * p.n_kvheads;
-    if (from < prefix_units) {
+    if (ahead >= 0 && from < prefix_units) {               // (offsets that do not increase)
       a = p.unit_joins[from];
       a_row = (ahead - tile * p.tile_tokens) * p.group + (row - tok * p.group);
     }
@@ -364,8 +364,11 @@ cudaError_t launch_list_pages(const ListParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_list_prefix(const ListParams& p, cudaStream_t stream) {
-  const int32_t per = kPrefixWarps * kPrefixRun, tiles = p.n_tiles / p.n_kvheads;
+cudaError_t launch_list_prefix(ListParams p, cudaStream_t stream) {
+  // a warp that lists several tiles reads its group's lengths once; few tiles are listed side by side
+  const int32_t tiles = p.n_tiles / p.n_kvheads;
+  p.run = tiles <= 2048 ? 1 : 4;
+  const int32_t per = kPrefixWarps * p.run;
   list_prefix_kernel<<<static_cast<unsigned>((tiles + per - 1) / per), kPrefixWarps * 32, 0, stream>>>(p);
   return cudaGetLastError();
 }
