@@ -440,7 +440,7 @@ struct ChooseParams {
   int64_t n_items;              // units x runs
   int32_t key_stride;           // pages_per_req, rounded up to whole tiles
   int32_t bound_tiles;          // key_stride / kBoundTile
-  int32_t tile_tokens;          // 128 / group
+  int32_t tile_tokens;          // of a query tile: at most 128 / group
   int32_t units;                // query tiles x KV heads
   int32_t run_tiles;            // tiles of a run of a query tile's pages
   int32_t stall_first_item;
@@ -453,7 +453,7 @@ cudaError_t launch_page_select(const ChooseParams& p, bool fp16, int num_sms, cu
 // Dynamic shared-memory opt-in of a kernel to `bytes`, its largest use, once per device and kernel (so
 // calls made during a graph capture only enqueue).
 enum OptInKernel { kOptPlan, kOptWindow, kOptScore = kOptWindow + 24,
-                    kOptListPages = kOptScore + 6, kOptCount = kOptListPages + 1 };
+                    kOptListPages = kOptScore + 12, kOptCount = kOptListPages + 1 };
 cudaError_t smem_opt_in(const void* kernel, int bytes, int which);
 
 // Host helpers of api.cpp for the other units' entry points.

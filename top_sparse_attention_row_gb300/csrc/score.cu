@@ -36,17 +36,20 @@ namespace {
 
 using namespace window_detail;
 
-template <int D>
+// QROWS: columns that an item's queries may have, 128, or 32 where the batch is mostly single tokens: the room goes to the
+// ring then, which HBM's latency fills (64 tokens at 64k to 128k, 24/2 heads of 256 dims: KKK us of scores, with 128: 63).
+template <int D, int QROWS>
 struct ScoreCfg {
   static constexpr int kPer = D / 64;                      // stages of a tile of pages: 128 of 2 D dims each
   static constexpr int kStageBytes = kScoreTile * 256;
   static constexpr int kBlock = 128 * 128;                 // bytes of 64 dims of 128 rows
-  static constexpr int kQBytes = 2 * D / 64 * kBlock;      // the split queries
-  static constexpr int kStages = D == 256 ? 3 : D == 128 ? 5 : 6;
+  static constexpr int kQBlock = QROWS * 128;              // of the queries
+  static constexpr int kQBytes = 2 * D / 64 * kQBlock;     // the split queries
+  static constexpr int kStages = QROWS == 32 ? 6 : D == 256 ? 3 : D == 128 ? 5 : 6;
   static constexpr int kThreads = 1024;
   static constexpr int kBuildWarp0 = 8, kMmaWarp = 16, kSchedulerWarp = 17, kScanWarp = 18, kGatherWarp0 = 20;
   static constexpr int kGatherWarps = 12, kStageWarps = 4;
-  static constexpr int kChunks = 128 * D / 8 / 256;        // 16-byte pieces of the queries a building thread has
+  static constexpr int kChunks = QROWS * D / 8 / 256;      // 16-byte pieces of the queries a building thread has
   // registers per thread at launch, and after the split: epilogue and building warpgroups; the others
   static constexpr int kLaunchRegs = 64, kWideRegs = 80, kRoleRegs = 48;
   static_assert(512 * kWideRegs + 512 * kRoleRegs <= kThreads * kLaunchRegs, "register split");
@@ -95,10 +98,10 @@ __device__ __forceinline__ float largest_of(const float* v) {
   return m;
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1) page_score_kernel(const __grid_constant__ CUtensorMap tmB,
+template <int D, typename T, int QROWS>
+__global__ void __launch_bounds__(ScoreCfg<D, QROWS>::kThreads, 1) page_score_kernel(const __grid_constant__ CUtensorMap tmB,
                                                                                const __grid_constant__ ChooseParams p) {
-  using C = ScoreCfg<D>;
+  using C = ScoreCfg<D, QROWS>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   const uint32_t b_full = base + C::kBarAt, b_empty = b_full + 8 * C::kStages;
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1) page_score_kernel(co
       for (int i = 0; i < C::kChunks; ++i) {
         const int r = row0 + i * kEvery;
         if (r < rows) {
-          const uint32_t to = base + (chunk >> 3) * C::kBlock + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+          const uint32_t to = base + (chunk >> 3) * C::kQBlock + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
           const uint4 y = v[i];
           st_shared_v4(to, make_uint4(choose::best2<T, false>(y.x, 0u), choose::best2<T, false>(y.y, 0u),
                                       choose::best2<T, false>(y.z, 0u), choose::best2<T, false>(y.w, 0u)));
@@ -310,12 +313,11 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1) page_score_kernel(co
             go = go && wait(b_full + 8 * st.st, st.par, kPStageFull);
             if (!go) break;
             tc_fence_after();
-            const uint32_t a = ring_lo + st.st * (C::kStageBytes >> 4), b = q_lo + s * (2 * C::kBlock >> 4);
+            const uint32_t a = ring_lo + st.st * (C::kStageBytes >> 4), b = q_lo + s * (2 * C::kQBlock >> 4);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
-              tc_mma_w(tmem + d.st * 128, a + off, kHi, b + off, kHi, idesc, s > 0 || k > 0 ? 1u : 0u);
-            }
+            for (int k = 0; k < 8; ++k)
+              tc_mma_w(tmem + d.st * 128, a + (((k >> 2) * C::kBlock + (k & 3) * 32) >> 4), kHi,
+                       b + (((k >> 2) * C::kQBlock + (k & 3) * 32) >> 4), kHi, idesc, s > 0 || k > 0 ? 1u : 0u);
             tc_commit(b_empty + 8 * st.st);
             ring_next(st, C::kStages);
           }
@@ -492,10 +494,10 @@ __global__ void __launch_bounds__(ScoreCfg<D>::kThreads, 1) page_score_kernel(co
   finish_role();
 }
 
-template <int D, typename T>
-cudaError_t launch_score_dim(const ChooseParams& p, const CUtensorMap& tb, int grid, int which, cudaStream_t stream) {
-  using C = ScoreCfg<D>;
-  auto kern = page_score_kernel<D, T>;
+template <int D, typename T, int QROWS>
+cudaError_t launch_score_rows(const ChooseParams& p, const CUtensorMap& tb, int grid, int which, cudaStream_t stream) {
+  using C = ScoreCfg<D, QROWS>;
+  auto kern = page_score_kernel<D, T, QROWS>;
   const cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(kern), C::kSmem, kOptScore + which);
   if (e != cudaSuccess) return e;
   // (the register shares add up to what the block is launched with: a kernel compiled to fewer would wait for ever)
@@ -506,6 +508,11 @@ cudaError_t launch_score_dim(const ChooseParams& p, const CUtensorMap& tb, int g
   if (regs < C::kLaunchRegs) return cudaErrorInvalidConfiguration;
   kern<<<grid, C::kThreads, C::kSmem, stream>>>(tb, p);
   return cudaGetLastError();
+}
+template <int D, typename T>
+cudaError_t launch_score_dim(const ChooseParams& p, const CUtensorMap& tb, int grid, int which, cudaStream_t stream) {
+  return p.tile_tokens * p.group <= 32 ? launch_score_rows<D, T, 32>(p, tb, grid, 2 * which, stream)
+                                       : launch_score_rows<D, T, 128>(p, tb, grid, 2 * which + 1, stream);
 }
 
 }  // namespace

@@ -545,7 +545,8 @@ qsa_status qsa_page_select(const void* q, const void* bounds, const int32_t* cu_
   const ScorePlan plan = plan_scores(n_rows, n_requests, n_kvheads, pages_per_req);
   p.key_stride = plan.page_tiles * qsa::kScoreTile;
   p.bound_tiles = p.key_stride / qsa::kBoundTile;
-  p.tile_tokens = 128 / p.group;
+  // mostly single tokens: narrow tiles, which leave more room for the pages
+  p.tile_tokens = (p.group <= 32 && n_rows <= 2 * static_cast<int64_t>(n_requests) ? 32 : 128) / p.group;
   // Splitting a tile's queries takes as long as two or three of its page tiles: with units for all SMs (four each) a unit is
   // one item.  Few units are cut into runs of page tiles, a dozen for every SM.
   const int64_t units = (n_rows / p.tile_tokens + n_requests) * n_kvheads, each = units * plan.page_tiles / (sms * int64_t{12});

@@ -625,6 +625,9 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           tmem_ld32(tm_s, s);
           tmem_ld32(tm_s + 32, s + 32);
           tc_wait_ld();
+          // chosen pages: which sixteens of the columns some row of the warp sees (the tile's pages are those of all its
+          // tokens, a warp's rows are of a few): the others are left out below, their weights are 0
+          uint32_t live = 15u;
           if (j < u.all0 || j >= u.all1 || any_hole) {
             // the keys of this thread's half that its row sees, as bits
             const int32_t c0 = v0 + wg * 64;
@@ -668,19 +671,28 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
               }
             }
             const uint32_t k0 = static_cast<uint32_t>(keep), k1 = static_cast<uint32_t>(keep >> 32);
+            if constexpr (SOURCE == kChosenPages) {
+              const uint32_t a0 = __reduce_or_sync(0xffffffffu, k0), a1 = __reduce_or_sync(0xffffffffu, k1);
+              live = (a0 & 0xffffu ? 1u : 0u) | (a0 >> 16 ? 2u : 0u) | (a1 & 0xffffu ? 4u : 0u) | (a1 >> 16 ? 8u : 0u);
+            }
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              s[c] = k0 & (1u << c) ? s[c] : -INFINITY;
-              s[c + 32] = k1 & (1u << c) ? s[c + 32] : -INFINITY;
+            for (int h = 0; h < 64; h += 16) {
+              if (SOURCE == kChosenPages && !(live >> (h / 16) & 1u)) continue;
+#pragma unroll
+              for (int c = h; c < h + 16; ++c) s[c] = (h < 32 ? k0 : k1) & (1u << (c & 31)) ? s[c] : -INFINITY;
             }
           }
-          float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
+          float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
 #pragma unroll
-          for (int c = 4; c < 64; c += 4) {
-            t0 = fmaxf(t0, s[c]);
-            t1 = fmaxf(t1, s[c + 1]);
-            t2 = fmaxf(t2, s[c + 2]);
-            t3 = fmaxf(t3, s[c + 3]);
+          for (int h = 0; h < 64; h += 16) {
+            if (SOURCE == kChosenPages && !(live >> (h / 16) & 1u)) continue;
+#pragma unroll
+            for (int c = h; c < h + 16; c += 4) {
+              t0 = fmaxf(t0, s[c]);
+              t1 = fmaxf(t1, s[c + 1]);
+              t2 = fmaxf(t2, s[c + 2]);
+              t3 = fmaxf(t3, s[c + 3]);
+            }
           }
           float tile_max = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
           float* const mx = maxima + sb * 256;
@@ -717,22 +729,30 @@ __global__ void __launch_bounds__(WinCfg<D, FP4>::kThreads, 1)
           uint64_t a0 = 0, a1 = 0;                 // sums of pairs
           uint32_t pk[32];
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-            float e0, e1, e2, e3;
-            split_pair(fma_pair(pair_of(s[c], s[c + 1]), sc2, neg2), e0, e1);
-            split_pair(fma_pair(pair_of(s[c + 2], s[c + 3]), sc2, neg2), e2, e3);
-            e0 = fast_exp2(e0);
-            e1 = fast_exp2(e1);
-            e2 = fast_exp2(e2);
-            e3 = fast_exp2(e3);
-            a0 = add_pair(a0, pair_of(e0, e1));
-            a1 = add_pair(a1, pair_of(e2, e3));
-            if constexpr (FP4) {
-              pk[c / 2] = pack16(e0, e1, __half{});
-              pk[c / 2 + 1] = pack16(e2, e3, __half{});
-            } else {
-              pk[c / 2] = pack16(e0, e1, T{});
-              pk[c / 2 + 1] = pack16(e2, e3, T{});
+          for (int h = 0; h < 64; h += 16) {
+            if (SOURCE == kChosenPages && !(live >> (h / 16) & 1u)) {
+#pragma unroll
+              for (int c = h; c < h + 16; c += 2) pk[c / 2] = 0u;
+              continue;
+            }
+#pragma unroll
+            for (int c = h; c < h + 16; c += 4) {
+              float e0, e1, e2, e3;
+              split_pair(fma_pair(pair_of(s[c], s[c + 1]), sc2, neg2), e0, e1);
+              split_pair(fma_pair(pair_of(s[c + 2], s[c + 3]), sc2, neg2), e2, e3);
+              e0 = fast_exp2(e0);
+              e1 = fast_exp2(e1);
+              e2 = fast_exp2(e2);
+              e3 = fast_exp2(e3);
+              a0 = add_pair(a0, pair_of(e0, e1));
+              a1 = add_pair(a1, pair_of(e2, e3));
+              if constexpr (FP4) {
+                pk[c / 2] = pack16(e0, e1, __half{});
+                pk[c / 2 + 1] = pack16(e2, e3, __half{});
+              } else {
+                pk[c / 2] = pack16(e0, e1, T{});
+                pk[c / 2 + 1] = pack16(e2, e3, T{});
+              }
             }
           }
           float l0, l1;
