@@ -199,14 +199,17 @@ def page_select(q, bounds, cu, kv_lens, table, page_size, n_select, n_first, n_l
     return out
 
 
-def selected_attention(q, k, v, pages, cu, kv_lens, table, page_size, scale):
-    """Every row over the positions up to its own whose page is listed for its KV head; rows outside every
-    request come back as NaN."""
+def selected_attention(q, k, v, pages, cu, kv_lens, table, page_size, scale, rows=None):
+    """Every row (or those of `rows`) over the positions up to its own whose page is listed for its KV head; rows
+    outside every request come back as NaN."""
     R, Hq, _ = q.shape
     Hkv, n_pages = k.shape[1], k.shape[0] // page_size
     o, lse = np.full((R, Hq, v.shape[2]), np.nan), np.full((R, Hq), np.nan)
+    wanted = None if rows is None else set(int(r) for r in rows)
     for i, kv in enumerate(kv_lens):
         for r in range(cu[i], cu[i + 1]):
+            if wanted is not None and r not in wanted:
+                continue
             p = kv - (cu[i + 1] - cu[i]) + (r - cu[i])
             for h in range(Hq):
                 g = h // (Hq // Hkv)

@@ -345,6 +345,22 @@ def test_selected_leaves_rows_behind_the_last_request(B):
     assert B.selected_attention_paged(b.q, b.k, b.v, i32(b.lists(5, seed=4)), *b.batch(), b.scale, want_lse=False)[1] is None
 
 
+def test_selected_many_rows(B):
+    """Units for all SMs, which are dealt out whole; neighbouring rows list much the same pages."""
+    b = Batch([(2500, 2400), (900, 700)], 4, 2, 64, 16, seed=12)
+    lists = np.sort(b.rng.integers(0, 57, (b.R // 50 + 1, 2, 12)), -1).repeat(50, 0)[:b.R]
+    moved = b.rng.random(lists.shape) < 0.05
+    lists = np.where(moved, b.rng.integers(-1, 160, lists.shape), lists)
+    got = B.selected_attention_paged(b.q, b.k, b.v, i32(lists), *b.batch(), b.scale)
+    finished(B)
+    for cut in (slice(0, 60), slice(1200, 1260), slice(2390, 2460), slice(3050, 3100)):
+        rows = np.arange(cut.start, cut.stop)
+        args = (lists, *b.host(), b.scale, rows)
+        o, z = S.selected_attention(f64(b.q), f64(b.k), f64(b.v), *args)
+        a, _ = S.selected_attention(f64(b.q), f64(b.k), np.abs(f64(b.v)), *args)
+        b.compare(got, o, z, a, rows)
+
+
 # ------------------------------------------------------------------------------ shared prompts
 def check_prefix(B, b, groups, prefix, **kw):
     got = B.prefix_attention_paged(b.q, b.k, b.v, *b.batch(), b.scale, i32(groups), i32(prefix), **kw)
@@ -432,6 +448,18 @@ def test_prefix_leaves_rows_behind_the_last_request(B):
     out, lse = torch.full_like(b.q, 7.0), torch.full((b.R, 4), 7.0, device="cuda")
     got = check_prefix(B, b, [0, 3], [64], out=out, lse=lse)
     assert got[0] is out and (out[9:] == 7).all() and (lse[9:] == 7).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prefix_many_rows(B, dim):
+    """More rows than the join gives four warps each."""
+    b = shared(8, 512, lambda i: 300 + 40 * i, 8, 2, dim, 16, seed=dim, new=lambda i: 260 + 5 * i)
+    got = B.prefix_attention_paged(b.q, b.k, b.v, *b.batch(), b.scale, i32([0, 8]), i32([512]))
+    finished(B)
+    rows = np.arange(0, b.R, 41)
+    o, z = S.window_attention(f64(b.q), f64(b.k), f64(b.v), *b.host(), b.scale, rows=rows)
+    a, _ = S.window_attention(f64(b.q), f64(b.k), np.abs(f64(b.v)), *b.host(), b.scale, rows=rows)
+    b.compare(got, o, z, a, rows)
 
 
 # ------------------------------------------------------------------------------ together

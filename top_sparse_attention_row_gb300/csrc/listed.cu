@@ -261,98 +261,153 @@ __global__ void __launch_bounds__(kPrefixWarps * 32) list_prefix_kernel(const __
 }
 
 // Joins the results of a row: of the shared keys and of its own, each of which may have several parts.  With L_s a
-// part's log-sum-exp and O_s its normalised output, lse = ln sum exp(L_s) and O = sum exp(L_s - lse) O_s.  A warp takes a
-// row; the parts are added in a fixed order.  A part that is NaN makes the row NaN.
+// part's log-sum-exp and O_s its normalised output, lse = ln sum exp(L_s) and O = sum exp(L_s - lse) O_s.  W warps take a
+// row and divide its parts: one where there are many rows (of two or three parts each), four where few rows have a part in
+// many blocks and the latency of one part after the other would count.  The parts are added in a fixed order.  A part that
+// is NaN makes the row NaN.
 constexpr int kJoinWarps = 8;
-template <int D, typename T>
+constexpr int64_t kJoinFewRows = 16384;
+template <int D, typename T, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     join_prefix_kernel(const __grid_constant__ WindowParams p, const OwnUnit* own_units, int32_t prefix_units) {
-  constexpr int kPer = D / 32;
+  constexpr int kPer = D / 32, kRows = kJoinWarps / W;
+  __shared__ float sums[W > 1 ? kJoinWarps : 1][W > 1 ? D : 1];
   pdl_wait();   // first thing in every thread: the grid must not end before the attention kernel has
   const OwnUnit own = own_units[blockIdx.x];
-  const int lane = threadIdx.x & 31, row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % W, rows = own.tokens * p.group;
   const int32_t unit = prefix_units + static_cast<int32_t>(blockIdx.x), kvh = unit % p.n_kvheads;
-  if (row >= own.tokens * p.group) return;
-  const int tok = row / p.group;
-  const int64_t token = static_cast<int64_t>(own.row0) + tok;
-  const int64_t rh = token * p.n_qheads + kvh * p.group + (row - tok * p.group);
-  // parts: [0, split) of the shared keys, then of the row's own; slots and rows of those after the first ones
+  const int64_t all_rows = p.n_rows * p.n_qheads;
+  if (rows == 0) return;
   const int2 b = p.unit_joins[unit];
-  int2 a = make_int2(0, -1);
-  int32_t a_row = 0;
-  if (own.prefix_unit >= 0) {
-    const int32_t ahead = static_cast<int32_t>(token) - own.group_row0, tile = ahead / p.tile_tokens;
-    const int32_t from = own.prefix_unit + tile * p.n_kvheads;
-    if (ahead >= 0 && from < prefix_units) {               // (offsets that do not increase)
-      a = p.unit_joins[from];
-      a_row = (ahead - tile * p.tile_tokens) * p.group + (row - tok * p.group);
-    }
-  }
-  const int split = a.y + 1, parts = split + b.y + 1;
-  if (parts == 0 || (split == 0 && parts == 1)) return;    // given up; written by the attention kernel
-  const int64_t rows = p.n_rows * p.n_qheads;
-  auto place = [&](int s, int64_t* first) -> int64_t {     // of a part: row of the first parts, or of the others
-    *first = s == 0 && split > 0 ? rh : s == split ? rows + rh : -1;
-    return s < split ? static_cast<int64_t>(a.x + s) * kWinTile + a_row
-                     : static_cast<int64_t>(b.x + s - split) * kWinTile + row;
-  };
-  auto lse_of = [&](int s) {
-    int64_t first;
-    const int64_t other = place(s, &first);
-    return first >= 0 ? p.first_lse[first] : p.part_lse[other];
-  };
-  float m = -INFINITY, total = 0.0f;
-  for (int s = lane; s < parts; s += 32) m = fmaxf(m, lse_of(s));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float acc[kPer];
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
-  for (int s0 = 0; s0 < parts; s0 += 32) {
-    const float l = s0 + lane < parts ? lse_of(s0 + lane) : -INFINITY;
-    const float w = l == -INFINITY ? 0.0f : __expf(l - m);
-    total += w;
-    // a part that saw nothing of this row wrote no output: whatever is there stays out
-    const uint32_t saw = __ballot_sync(0xffffffffu, l != -INFINITY);
-#pragma unroll 4
-    for (int i = 0; i < min(parts - s0, 32); ++i) {
-      const float ws = __shfl_sync(0xffffffffu, w, i);
-      int64_t first;
-      const int64_t other = place(s0 + i, &first);
-      const float* const src = (first >= 0 ? p.first_o + first * D : p.part_o + other * D) + lane * kPer;
+  for (int first = blockIdx.y * kRows; first < rows; first += gridDim.y * kRows) {   // (uniform over the block)
+    const int row = first + warp / W;
+    const bool live = row < rows;
+    const int tok = live ? row / p.group : 0;
+    const int64_t token = static_cast<int64_t>(own.row0) + tok;
+    const int64_t rh = token * p.n_qheads + kvh * p.group + (row - tok * p.group);
+    // (many rows) Most have two results that are whole: these are on their way while it is looked up whether that is so.
+    float l0 = -INFINITY, l1 = -INFINITY, x0[kPer], x1[kPer];
+    if (W == 1 && live && own.prefix_unit >= 0) {
+      l0 = p.first_lse[rh];
+      l1 = p.first_lse[all_rows + rh];
 #pragma unroll
       for (int k = 0; k < kPer; k += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(src + k);
-        if (saw >> i & 1) {
-          acc[k] += ws * x.x;
-          acc[k + 1] += ws * x.y;
+        const float2 y0 = *reinterpret_cast<const float2*>(p.first_o + rh * D + lane * kPer + k);
+        const float2 y1 = *reinterpret_cast<const float2*>(p.first_o + (all_rows + rh) * D + lane * kPer + k);
+        x0[k] = y0.x;
+        x0[k + 1] = y0.y;
+        x1[k] = y1.x;
+        x1[k + 1] = y1.y;
+      }
+    }
+    // parts: [0, split) of the shared keys, then of the row's own; slots and rows of those after the first ones
+    int2 a = make_int2(0, -1);
+    int32_t a_row = 0;
+    if (own.prefix_unit >= 0) {
+      const int32_t ahead = static_cast<int32_t>(token) - own.group_row0, tile = ahead / p.tile_tokens;
+      const int32_t from = own.prefix_unit + tile * p.n_kvheads;
+      if (ahead >= 0 && from < prefix_units) {             // (offsets that do not increase)
+        a = p.unit_joins[from];
+        a_row = (ahead - tile * p.tile_tokens) * p.group + (row - tok * p.group);
+      }
+    }
+    const int split = a.y + 1, all = split + b.y + 1;
+    // nothing to join: given up; written by the attention kernel
+    const int parts = !live || all == 0 || (split == 0 && all == 1) ? 0 : all;
+    auto place = [&](int s, int64_t* whole) -> int64_t {   // of a part: row of the first parts, or of the others
+      *whole = s == 0 && split > 0 ? rh : s == split ? all_rows + rh : -1;
+      return s < split ? static_cast<int64_t>(a.x + s) * kWinTile + a_row
+                       : static_cast<int64_t>(b.x + s - split) * kWinTile + row;
+    };
+    auto lse_of = [&](int s) {
+      int64_t whole;
+      const int64_t other = place(s, &whole);
+      return whole >= 0 ? p.first_lse[whole] : p.part_lse[other];
+    };
+    float m = -INFINITY, total = 0.0f;
+    float acc[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
+    const bool two = W == 1 && split == 1 && parts == 2;   // (uniform over the warp)
+    if (two) {
+      m = fmaxf(l0, l1);
+      // a part that saw nothing of this row wrote no output: whatever is there stays out
+      const float w0 = l0 == -INFINITY ? 0.0f : __expf(l0 - m), w1 = l1 == -INFINITY ? 0.0f : __expf(l1 - m);
+      total = lane == 0 ? w0 + w1 : 0.0f;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] = (l0 == -INFINITY ? 0.0f : w0 * x0[k]) + (l1 == -INFINITY ? 0.0f : w1 * x1[k]);
+    } else {
+      for (int s = lane; s < parts; s += 32) m = fmaxf(m, lse_of(s));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    for (int s0 = 0; s0 < parts && !two; s0 += 32) {
+      const float l = s0 + lane < parts ? lse_of(s0 + lane) : -INFINITY;
+      const float w = l == -INFINITY ? 0.0f : __expf(l - m);
+      total += w;
+      // a part that saw nothing of this row wrote no output: whatever is there stays out
+      const uint32_t saw = __ballot_sync(0xffffffffu, l != -INFINITY);
+#pragma unroll 4
+      for (int i = mine; i < min(parts - s0, 32); i += W) {
+        const float ws = __shfl_sync(0xffffffffu, w, i);
+        int64_t whole;
+        const int64_t other = place(s0 + i, &whole);
+        const float* const src = (whole >= 0 ? p.first_o + whole * D : p.part_o + other * D) + lane * kPer;
+#pragma unroll
+        for (int k = 0; k < kPer; k += 2) {
+          const float2 x = *reinterpret_cast<const float2*>(src + k);
+          if (saw >> i & 1) {
+            acc[k] += ws * x.x;
+            acc[k + 1] += ws * x.y;
+          }
         }
       }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const float inv = m == -INFINITY ? 0.0f : 1.0f / total;
+    if constexpr (W > 1) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) sums[warp][lane * kPer + k] = acc[k];
+      __syncthreads();
+      if (mine == 0) {
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) acc[k] += sums[warp + w][lane * kPer + k];
+        }
+      }
+      __syncthreads();
+    }
+    if (mine != 0 || parts == 0) continue;
+    uint32_t* const out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + rh * D + lane * kPer);
+#pragma unroll
+    for (int k = 0; k < kPer / 2; ++k) out[k] = window_detail::pack16(acc[2 * k] * inv, acc[2 * k + 1] * inv, T{});
+    if (lane == 0 && p.lse) p.lse[rh] = total == 0.0f ? -INFINITY : m + logf(total);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const float inv = m == -INFINITY ? 0.0f : 1.0f / total;
-  uint32_t* const out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + rh * D + lane * kPer);
-#pragma unroll
-  for (int k = 0; k < kPer / 2; ++k) out[k] = window_detail::pack16(acc[2 * k] * inv, acc[2 * k + 1] * inv, T{});
-  if (lane == 0 && p.lse) p.lse[rh] = total == 0.0f ? -INFINITY : m + logf(total);
 }
 
-template <int D, typename T>
-cudaError_t launch_join_prefix_dim(const WindowParams& p, const ListParams& l, cudaStream_t stream) {
+template <int D, typename T, int W>
+cudaError_t launch_join_prefix_warps(const WindowParams& p, const ListParams& l, cudaStream_t stream) {
   const int32_t prefix_units = l.prefix_tiles * l.n_kvheads;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  // as many blocks as the units have rows on average (a block of a unit with more goes over them)
+  const int64_t units = (l.n_tiles - prefix_units) / l.n_kvheads, tokens = p.n_rows > units ? (p.n_rows + units - 1) / units : 1;
   cfg.gridDim = dim3(static_cast<unsigned>(l.n_tiles - prefix_units),
-                     static_cast<unsigned>((l.tile_tokens * p.group + kJoinWarps - 1) / kJoinWarps));
+                     static_cast<unsigned>((tokens * p.group + kJoinWarps / W - 1) / (kJoinWarps / W)));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_prefix_kernel<D, T>, p, static_cast<const OwnUnit*>(l.own), prefix_units);
+  return cudaLaunchKernelEx(&cfg, join_prefix_kernel<D, T, W>, p, static_cast<const OwnUnit*>(l.own), prefix_units);
+}
+template <int D, typename T>
+cudaError_t launch_join_prefix_dim(const WindowParams& p, const ListParams& l, cudaStream_t stream) {
+  return p.n_rows * p.n_qheads <= kJoinFewRows ? launch_join_prefix_warps<D, T, 4>(p, l, stream)
+                                               : launch_join_prefix_warps<D, T, 1>(p, l, stream);
 }
 
 }  // namespace
