@@ -24,7 +24,8 @@ LIB = os.path.join(PKG, "libqsa.so")
 SOURCES = ["prefill.cu", "mla.cu", "union.cu", "api.cpp", "noalloc.cu", "probe.cu", "pages.cu",
            "serving.cpp", "plan.cu", "rope.cu", "window.cu", "window_d64.cu", "window_d128.cu",
            "window_d256.cu", "listed.cu", "listed_d64.cu", "listed_d128.cu",
-           "listed_d256.cu", "choose.cu", "score.cu"]
+           "listed_d256.cu", "bounds.cu", "score.cu",
+           "select_d64.cu", "select_d128.cu", "select_d256.cu"]
 
 EXT_SOURCE = "torch_serving.cpp"
 EXT = os.path.join(PKG, "_serving" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))

@@ -1,4 +1,4 @@
-// The k best of a list of scores, decided as the exact scores decide (page selection, choose.cu).
+// The k best of a list of scores, decided as the exact scores decide (page selection, select.cuh).
 //
 // Scores come in fp32 with an error of at most eps each.  Let t be the k-th largest of them.  The k-th largest exact
 // score is then within eps of t, so an entry above t + 2 eps belongs to the k best and one below t - 2 eps does not;

@@ -414,7 +414,7 @@ cudaError_t launch_window(const WindowParams& p, int head_dim, bool fp16, bool f
 cudaError_t launch_listed(const WindowParams& p, const ListParams& l, UnitSource source, int head_dim, bool fp16,
                           const void* k_cache, const void* v_cache, cudaStream_t stream);
 
-// Page bounds and the choice of pages by them (choose.cu).
+// Page bounds and the choice of pages by them (bounds.cu, select.cuh).
 struct BoundsParams {
   const void* k_cache;          // [n_pages * page_size, n_kvheads, D]
   void* bounds;                 // [n_pages, n_kvheads, 2, D]: minima, maxima
@@ -449,6 +449,10 @@ struct ChooseParams {
 };
 cudaError_t launch_page_score(const ChooseParams& p, bool fp16, int num_sms, cudaStream_t stream);
 cudaError_t launch_page_select(const ChooseParams& p, bool fp16, int num_sms, cudaStream_t stream);
+// (one translation unit per head dim)
+cudaError_t launch_select_d64(const ChooseParams& p, bool fp16, int num_sms, cudaStream_t stream);
+cudaError_t launch_select_d128(const ChooseParams& p, bool fp16, int num_sms, cudaStream_t stream);
+cudaError_t launch_select_d256(const ChooseParams& p, bool fp16, int num_sms, cudaStream_t stream);
 
 // Dynamic shared-memory opt-in of a kernel to `bytes`, its largest use, once per device and kernel (so
 // calls made during a graph capture only enqueue).

@@ -1,4 +1,4 @@
-// Scores of a cache's pages for the step's queries, by which page selection chooses (choose.cu).
+// Scores of a cache's pages for the step's queries, by which page selection chooses (select.cuh).
 //
 // score(row, KV head, page) = max over the heads h of  sum_d max(q_hd lo_d, q_hd hi_d), and since the larger of the two
 // products is the one with hi where q is positive and with lo elsewhere,
@@ -10,7 +10,7 @@
 //    operands in shared memory, three buffers of D in tensor memory.  A thread of the epilogue has a page, so the maximum
 //    over a token's heads is one over neighbouring columns, and 32 pages' keys are written side by side.
 //    (The other way round, with the queries as M from tensor memory, an MMA of N = 128 takes 90 to 110 cycles where this
-//    one takes 65, and the maxima go across lanes: 193 us where this takes KKK for 8192 prompt rows.)
+//    one takes 65, and the maxima go across lanes: 192 us of scores for 8192 prompt rows, 24/2 heads of 256 dims, where this takes 143.)
 //  * The split queries of an item lie in shared memory until its products are done.  Eight warps have the next item's
 //    queries in registers by then, and have summed |q| for the error bound.
 //  * The pages' rows are gathered by page id, four at a time (TMA), 128 dims of 128 pages a stage, by four warps into a
@@ -20,7 +20,10 @@
 //  * Scores are written as keys that have their order (choose.cuh), 0 for a page that does not exist.  For the error bound
 //    the largest |bound| of every 64 pages is taken from the ring by two warps, in the items of a request's last rows (which
 //    see all of its pages).
-//  * What bounds it.  Decode: HBM.  Prompts: shared memory, where every MMA reads 8 KB in 65 cycles.
+//  * What bounds it.  Prompts: shared memory.  An MMA reads 8 KB in the 65 cycles it takes alone (126 of 128 bytes a cycle),
+//    beside the gathers' writes and the queries', and a commit stands for two of them: ~4000 cycles a tile of 256 dims,
+//    2048 for its MMAs (8192 rows at 24k, 24/2 heads: 143 us, 0.63 PFLOP/s).  Decode: HBM's latency, with five or six
+//    stages of 32 KB on their way (64 rows at 64k to 128k: 47 us, 4.1 TB/s).
 //  * Every mbarrier wait is bounded; a timeout records a code in the device status word, all roles leave their loops, copies
 //    and MMAs in flight are drained, tensor memory is freed.
 #include <cuda_bf16.h>
@@ -37,7 +40,7 @@ namespace {
 using namespace window_detail;
 
 // QROWS: columns that an item's queries may have, 128, or 32 where the batch is mostly single tokens: the room goes to the
-// ring then, which HBM's latency fills (64 tokens at 64k to 128k, 24/2 heads of 256 dims: KKK us of scores, with 128: 63).
+// ring then, for HBM's latency (64 tokens at 64k to 128k, 24/2 heads of 256 dims: 47 us of scores, with 128 columns 63).
 template <int D, int QROWS>
 struct ScoreCfg {
   static constexpr int kPer = D / 64;                      // stages of a tile of pages: 128 of 2 D dims each
