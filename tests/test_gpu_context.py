@@ -216,6 +216,16 @@ def test_select_cancelling_sums(B):
     check_select(B, b, bounds, 33)
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("dim", [64, 256])
+def test_select_bounds_of_many_magnitudes(B, dim, dtype):
+    """Dims that reach from 2^-12 to 2^12: the products' fp32 sums are furthest off here."""
+    import torch
+    b = Batch([(3000, 6), (2048, 1)], 6, 1, dim, 8, dtype, seed=dim)
+    s = torch.exp2(torch.from_numpy(b.rng.integers(-12, 12, (b.n_pages, 1, 1, dim))).float()).cuda().to(b.dt)
+    check_select(B, b, b.bounds() * s, 60)
+
+
 def test_select_scores_beyond_fp32(B):
     """Sums that overflow fp32 are compared in 64 bits like any other."""
     b = Batch([(500, 4)], 3, 1, 64, 8, seed=4)

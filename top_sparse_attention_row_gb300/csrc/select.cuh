@@ -12,9 +12,13 @@ namespace qsa {
 
 using choose::floats_of;
 
-// fp32 sums of products that are exact in fp32, however they are grouped: the error stays below 2^-16 of the sum of
-// the magnitudes, which is at most the sum of |q| times the largest bound.
-constexpr float kScoreError = 0x1p-16f;
+// The tensor core's error of a score, as a part of the sum of |q| times the largest bound (which is no less than the sum of the
+// products' magnitudes).  Products are exact in fp32; 2 D / 16 times, sixteen of them and the sum so far are added and cut
+// to 24 bits, which takes off up to 2^-23 of the magnitudes each time: D 2^-26, and half as much again for the alignment
+// within the sixteen.  Measured: up to 2^-18.3 of the magnitudes for 256 dims whose bounds lie anywhere from 2^-12 to 2^12,
+// and at most 2^-21.1 of what this bound is a part of (2^-17).
+template <int D>
+constexpr float kScoreError = D * 0x1p-25f;
 
 // s + x as the nearest float and what is left of it (Knuth's two-sum): exact.
 __device__ __forceinline__ float two_sum(float s, float x, float* rest) {
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? 32 * kWarpTeams : TEAM, TEAM == 3
   const float reach = q_sum * bound;
   // beyond these, sums overflow or products lose bits in fp32 (NaN fails all comparisons)
   const bool wide = !(reach < 0x1p126f && reach > 0x1p-80f && q_sum > 0x1p-100f && bound > 0x1p-100f);
-  const float eps = q_sum == 0.0f || bound == 0.0f ? 0.0f : wide ? INFINITY : reach * kScoreError;
+  const float eps = q_sum == 0.0f || bound == 0.0f ? 0.0f : wide ? INFINITY : reach * kScoreError<D>;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     const int32_t e = keys.place(team, j);
