@@ -120,6 +120,23 @@ def test_bounds(B, ps, dim, dtype):
     assert np.array_equal(f64(bounds), want)
 
 
+def test_bounds_of_rows_that_do_not_begin_at_zero(B):
+    """The first rows of the batch belong to no request: no page but the requests' own is touched, the ones that stand
+    before the table's first row among them."""
+    import torch
+    b = Batch([(40, 20), (100, 30)], 4, 2, 64, 16, seed=4, extra_pages=40)
+    wide = b.table.shape[1]
+    ahead = np.setdiff1d(np.arange(b.n_pages), b.table)[:4 * wide].reshape(-1, wide)   # pages of nobody
+    table = i32(np.concatenate([ahead, b.table]))[len(ahead):]
+    cu, kv = i32(b.cu + 70), i32(b.kv)
+    mark = torch.full((b.n_pages, 2, 2, 64), 9, dtype=b.dt, device="cuda")
+    want = B.page_bounds(b.k, i32(b.cu), kv, table, 16, mark.clone())
+    got = B.page_bounds(b.k, cu, kv, table, 16, mark.clone())
+    finished(B)
+    assert torch.equal(got, want)
+    assert bool((got[torch.from_numpy(ahead).flatten().long().cuda()] == 9).all())
+
+
 def test_bounds_of_missing_pages_short_tables_and_short_lengths(B):
     b = Batch([(200, 70), (90, 3), (64, 100), (0, 4), (0, 0), (50, 0)], 1, 1, 64, 16, seed=5)
     b.table[0, 9], b.table[1, 5] = -1, b.n_pages           # missing and out of range

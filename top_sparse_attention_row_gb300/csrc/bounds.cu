@@ -51,14 +51,16 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const __gri
     const int64_t kv = __ldg(p.pa.kv_lens + req);
     const int64_t fresh = static_cast<int64_t>(__ldg(p.pa.cu_seqlens_q + req + 1)) - __ldg(p.pa.cu_seqlens_q + req);
     const int64_t past = kv > fresh ? kv - fresh : 0;
-    const int64_t e = past / p.pa.page_size + (number - first_page(p.pa, req)), start = e * p.pa.page_size;
-    if (fresh <= 0 || start >= kv || e >= p.pa.pages_per_req) continue;    // (uniform over the block)
+    const int64_t nth = number - first_page(p.pa, req);   // (< 0 before the first request's rows, where they do not begin at 0)
+    const int64_t e = past / p.pa.page_size + nth, start = e * p.pa.page_size;
+    // (uniform over the block)
+    if (nth < 0 || fresh <= 0 || start >= kv || e >= p.pa.pages_per_req) continue;
     const int32_t page = __ldg(p.pa.page_table + static_cast<int64_t>(req) * p.pa.pages_per_req + e);
     if (page < 0 || page >= p.pa.n_pages) continue;
     const int32_t filled = static_cast<int32_t>(kv - start < p.pa.page_size ? kv - start : p.pa.page_size);
     const T* const src = static_cast<const T*>(p.k_cache) +
                          (static_cast<int64_t>(page) * p.pa.page_size * p.n_kvheads + kvh) * D + col * 8;
-    uint4 lo, hi;
+    uint4 lo{}, hi{};
     auto take = [&](const uint4& x) {
       lo.x = best2<T, false>(lo.x, x.x);
       lo.y = best2<T, false>(lo.y, x.y);
