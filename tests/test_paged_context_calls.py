@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from oracle import serving as S
-from test_gpu_context import Batch, check_prefix, check_select, check_selected, f64, finished, i32, shared
+from test_paged_context import Batch, check_prefix, check_select, check_selected, f64, finished, i32, shared
 
 pytestmark = pytest.mark.gpu
 
@@ -138,6 +138,30 @@ def test_results_repeat(B, name):
     for _ in range(20):
         assert same(o.call(name), want)
     finished(B)
+
+
+def test_rows_that_do_not_begin_at_zero(B):
+    """Rows before the first request are left as they were, and the others get what they get without them."""
+    import torch
+    o = ops(B, seed=6)
+    b, ahead = o.b, 70
+    more = lambda t: torch.cat((torch.zeros_like(t[:1]).expand(ahead, *t.shape[1:]), t)).contiguous()  # noqa: E731
+    q, batch = more(b.q), (i32(b.cu + ahead), i32(b.kv), i32(b.table), 16)
+    pages = torch.full((ahead + b.R, 2, o.k), -5, dtype=torch.int32, device="cuda")
+    B.page_select(q, o.bounds, *batch, o.k, out=pages)
+    assert torch.equal(pages[ahead:], o.call("select")[0]) and bool((pages[:ahead] == -5).all())
+    chosen = lambda v: S.selected_attention(f64(b.q), f64(b.k), v, o.lists.cpu().numpy(), *b.host(), b.scale)  # noqa: E731
+    whole = lambda v: S.window_attention(f64(b.q), f64(b.k), v, *b.host(), b.scale)  # noqa: E731
+    for name, want in (("selected", chosen), ("prefix", whole)):
+        out = torch.full((ahead + b.R, 12, 128), 7, dtype=q.dtype, device="cuda")
+        lse = torch.full((ahead + b.R, 12), 7, dtype=torch.float32, device="cuda")
+        if name == "selected":
+            B.selected_attention_paged(q, b.k, b.v, more(o.lists), *batch, b.scale, out=out, lse=lse)
+        else:
+            B.prefix_attention_paged(q, b.k, b.v, *batch, b.scale, o.groups, o.prefix, out=out, lse=lse)
+        finished(B)
+        b.compare((out[ahead:], lse[ahead:]), *want(f64(b.v)), want(np.abs(f64(b.v)))[0])
+        assert bool((out[:ahead] == 7).all()) and bool((lse[:ahead] == 7).all())
 
 
 @pytest.mark.parametrize("name", NAMES)

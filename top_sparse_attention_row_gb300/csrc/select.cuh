@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(TEAM == 32 ? 32 * kWarpTeams : TEAM, TEAM == 3
   const int32_t kvh = static_cast<int32_t>(item - row * p.n_kvheads);
   if (row >= p.n_rows || row >= __ldg(p.pa.cu_seqlens_q + p.pa.n_requests)) return;
   const int32_t req = paged_request_of_row(p.pa, row, lane);
+  if (row < __ldg(p.pa.cu_seqlens_q + req)) return;        // before the first request
   const int64_t pos = static_cast<int64_t>(__ldg(p.pa.kv_lens + req)) - __ldg(p.pa.cu_seqlens_q + req + 1) + row;
   int32_t* const out = p.out + item * p.n_select;
   const int64_t mine = pos < 0 ? -1 : pos / p.pa.page_size;
