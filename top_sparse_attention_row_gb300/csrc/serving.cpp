@@ -370,9 +370,10 @@ bool plan_prefix(int64_t n_rows, int32_t n_requests, int32_t n_groups, int32_t n
   l->w.shares = sms;
   l->w.key_tiles = static_cast<int32_t>((static_cast<int64_t>(pages_per_req) * page_size + qsa::kWinTile - 1) / qsa::kWinTile);
   // (as plan_window) What a unit costs beside its tiles counts where a block has several units.  Not where there are few
-  // tiles for the SMs: then a unit's tiles are worth dividing to the last (four rows behind a prompt of 2048, 24/2 heads:
-  // 23 us), and its cost would be taken for work that other blocks cannot do.  Counted as none, a block got 25 requests' own
-  // keys where another got 25 tiles of the prompt (64 rows behind a prompt of 32k: 112 us instead of 76).
+  // tiles for the SMs: then a unit's tiles are worth dividing to the last, and its cost would be taken for work that other
+  // blocks cannot do (four rows behind a prompt of 2048, 24/2 heads: 19.4 us without it, 20.5 with it).  Counted as none where
+  // there are many, a block got 25 requests' own keys where another got 25 tiles of the prompt (64 rows behind a prompt of
+  // 32k: 101 us instead of 72; four prompts, 32/8 heads of 128 dims: 461 instead of 239).
   const int64_t row_tiles = (n_rows + l->w.tile_tokens - 1) / l->w.tile_tokens;
   l->w.unit_cost = row_tiles * n_kvheads * l->w.key_tiles > 4 * static_cast<int64_t>(sms) ? 3 : 0;
   const int32_t group_heads = n_kvheads * group;
