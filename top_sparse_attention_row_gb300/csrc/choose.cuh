@@ -128,6 +128,16 @@ struct Keys {
     for (int j = 0; j < N; ++j) c += f(k[j]) ? 1u : 0u;
     return t.sum(c);
   }
+  // two counts in one sum, of 16 bits each (THREADS N entries at most)
+  template <typename F, typename G>
+  __device__ __forceinline__ uint2 count(Team<THREADS>& t, F f, G g) const {
+    static_assert(THREADS * N < 65536, "counts of 16 bits");
+    uint32_t c = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) c += (f(k[j]) ? 1u : 0u) + (g(k[j]) ? 65536u : 0u);
+    c = t.sum(c);
+    return make_uint2(c & 0xffffu, c >> 16);
+  }
 };
 
 // The want-th largest key (want >= 1, at least so many keys are not 0, fewer are kChosen).
@@ -155,44 +165,51 @@ __device__ __forceinline__ uint32_t kth_largest(Team<THREADS>& t, const Keys<THR
   return lo;
 }
 
-// Writes the places of the keys above `bar`, and of the first `equal` ones equal to it, in order; then -1.
+// What the warps before this one counted (`part`: 0 or 1, each once a list).
+template <int THREADS>
+__device__ __forceinline__ uint32_t before_warp(Team<THREADS>& t, uint32_t mine, int part) {
+  if constexpr (THREADS == 32) return 0u;
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  uint32_t* const r = t.red + (2 + part) * Team<THREADS>::kWarps;
+  if (t.lane == 0) r[t.warp] = mine;
+  __syncthreads();
+  return __reduce_add_sync(0xffffffffu, t.lane < t.warp ? r[t.lane] : 0u);
+}
+
+// Writes the places of the keys above `bar`, and of the first `equal` ones equal to it, in order; then -1.  Changes the keys.
 template <int THREADS, int N>
-__device__ __forceinline__ void emit(Team<THREADS>& t, const Keys<THREADS, N>& keys, uint32_t bar, uint32_t equal, int32_t k,
+__device__ __forceinline__ void emit(Team<THREADS>& t, Keys<THREADS, N>& keys, uint32_t bar, uint32_t equal, int32_t k,
                                      int32_t* out) {
-  uint32_t above = 0, same = 0;                            // in the runs before this warp's
-  if constexpr (THREADS > 32) {
-    uint32_t a = 0, s = 0;
+  const uint32_t before = (1u << t.lane) - 1u;
+  if (equal != 0) {                                        // (rare) the first of the equal ones to kChosen, the others to 0
+    uint32_t mine = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) mine += keys.k[j] == bar;
+    uint32_t same = before_warp(t, mine, 0);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      a += keys.k[j] > bar;
-      s += keys.k[j] == bar;
+      const uint32_t s = __ballot_sync(0xffffffffu, keys.k[j] == bar);
+      if (keys.k[j] == bar) keys.k[j] = same + __popc(s & before) < equal ? kChosen : 0u;
+      same += __popc(s);
     }
-    a = __reduce_add_sync(0xffffffffu, a);
-    s = __reduce_add_sync(0xffffffffu, s);
-    uint32_t* const r = t.red + 2 * Team<THREADS>::kWarps;
-    if (t.lane == 0) {
-      r[2 * t.warp] = a;
-      r[2 * t.warp + 1] = s;
-    }
-    __syncthreads();
-    above = __reduce_add_sync(0xffffffffu, t.lane < t.warp ? r[2 * t.lane] : 0u);
-    same = __reduce_add_sync(0xffffffffu, t.lane < t.warp ? r[2 * t.lane + 1] : 0u);
+    bar = min(bar, kChosen - 1u);
   }
-  const uint32_t before = (1u << t.lane) - 1u;
+  uint32_t mine = 0;
+  if constexpr (THREADS > 32) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) mine += keys.k[j] > bar;
+  }
+  uint32_t above = before_warp(t, mine, 1);
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const uint32_t x = keys.k[j];
-    const uint32_t a = __ballot_sync(0xffffffffu, x > bar), s = __ballot_sync(0xffffffffu, x == bar);
-    if ((a | s) == 0) continue;
-    const uint32_t my_above = above + __popc(a & before), my_same = same + __popc(s & before);
-    const uint32_t place = my_above + min(my_same, equal);
-    if ((x > bar || (x == bar && my_same < equal)) && place < static_cast<uint32_t>(k)) out[place] = keys.place(t, j);
+    const bool in = keys.k[j] > bar;
+    const uint32_t a = __ballot_sync(0xffffffffu, in), place = above + __popc(a & before);
+    if (in && place < static_cast<uint32_t>(k)) out[place] = keys.place(t, j);
     above += __popc(a);
-    same += __popc(s);
   }
   // the last warp has counted them all
   if (t.warp == Team<THREADS>::kWarps - 1) {
-    for (int32_t i = static_cast<int32_t>(above + min(same, equal)) + t.lane; i < k; i += 32) out[i] = -1;
+    for (int32_t i = static_cast<int32_t>(above) + t.lane; i < k; i += 32) out[i] = -1;
   }
 }
 
@@ -226,43 +243,40 @@ __device__ __forceinline__ void choose(Team<THREADS>& t, Keys<THREADS, N>& keys,
                                        int32_t* out) {
   static_assert(N <= 32, "a lane's entries as bits");
   const uint32_t want = static_cast<uint32_t>(k);
-  if (keys.count(t, [](uint32_t x) { return x != 0; }) <= want) {
-    emit(t, keys, 0u, 0u, k, out);
-    return;
+  const uint2 n = keys.count(t, [](uint32_t x) { return x != 0; }, [](uint32_t x) { return x == kChosen; });
+  uint32_t bar = 0u, equal = 0u;                           // (all there are)
+  if (n.y >= want) {
+    bar = kChosen;
+    equal = want;
+  } else if (n.x > want) {
+    // by the scores, then by the upper halves of the exact ones that are close, then by their lower halves (one loop, so that
+    // its code is there once: written out three times it did not stay in the instruction cache)
+#pragma unroll 1
+    for (int stage = 0;; ++stage) {
+      bar = kth_largest(t, keys, want);
+      uint32_t lo = bar, hi = bar;
+      if (stage == 0) {
+        const float s = score_of(bar), e2 = 2.0f * eps;
+        const bool bounded = bar != kNan && isfinite(s) && isfinite(e2);
+        lo = bounded ? key_of(__fsub_rd(s, e2)) : 1u;      // no bound on the error: all may belong
+        hi = bounded ? key_of(__fadd_ru(s, e2)) : kNan;
+      }
+      const uint2 m = keys.count(t, [&](uint32_t x) { return x > hi; }, [&](uint32_t x) { return x >= lo; });
+      if (m.y == want) {
+        bar = lo - 1u;
+        break;
+      }
+      equal = want - m.x;
+      if (stage == 2 || eps == 0.0f) break;                // they are equal
+      equal = 0u;
+      // (0 and kChosen stay free: the last of the 64 bits is left out)
+      refine(t, keys, lo, hi, [&](int32_t i) {
+        const uint64_t x = exact(i);
+        return stage == 0 ? static_cast<uint32_t>(x >> 32) : 1u + (static_cast<uint32_t>(x) >> 1);
+      });
+    }
   }
-  if (keys.count(t, [](uint32_t x) { return x == kChosen; }) >= want) {
-    emit(t, keys, kChosen, want, k, out);
-    return;
-  }
-  const uint32_t bar = kth_largest(t, keys, want);
-  const float s = score_of(bar), e2 = 2.0f * eps;
-  uint32_t lo = 1u, hi = kNan;                             // no bound on the error: all may belong
-  if (bar != kNan && isfinite(s) && isfinite(e2)) {
-    lo = key_of(__fsub_rd(s, e2));
-    hi = key_of(__fadd_ru(s, e2));
-  }
-  const uint32_t sure = keys.count(t, [&](uint32_t x) { return x > hi; });
-  const uint32_t open = keys.count(t, [&](uint32_t x) { return x >= lo && x <= hi; });
-  if (sure + open == want) {
-    emit(t, keys, lo - 1u, 0u, k, out);
-    return;
-  }
-  if (eps == 0.0f) {                                       // they are equal
-    emit(t, keys, bar, want - sure, k, out);
-    return;
-  }
-  refine(t, keys, lo, hi, [&](int32_t i) { return static_cast<uint32_t>(exact(i) >> 32); });
-  const uint32_t upper = kth_largest(t, keys, want);
-  uint32_t over = keys.count(t, [&](uint32_t x) { return x > upper; });
-  if (over + keys.count(t, [&](uint32_t x) { return x == upper; }) == want) {
-    emit(t, keys, upper, want - over, k, out);
-    return;
-  }
-  // (0 and kChosen stay free: the last of the 64 bits is left out)
-  refine(t, keys, upper, upper, [&](int32_t i) { return 1u + (static_cast<uint32_t>(exact(i)) >> 1); });
-  const uint32_t lower = kth_largest(t, keys, want);
-  over = keys.count(t, [&](uint32_t x) { return x > lower; });
-  emit(t, keys, lower, want - over, k, out);
+  emit(t, keys, bar, equal, k, out);
 }
 
 }  // namespace choose

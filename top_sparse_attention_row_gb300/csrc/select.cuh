@@ -167,34 +167,35 @@ __global__ void __launch_bounds__(TEAM == 32 ? 32 * kWarpTeams : TEAM, TEAM == 3
   const int32_t* const table = p.pa.page_table + static_cast<int64_t>(req) * p.pa.pages_per_req;
   Keys<TEAM, N> keys(team, n);
   const int32_t to = min(keys.from + (n + TEAM - 1) / TEAM * 32, n);   // end of this warp's run
+  float reach = 0.0f, eps = 0.0f;
+  bool wide = false;
   if (n <= p.n_select) {                                   // every page that exists (no scores have been taken)
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int32_t e = keys.place(team, j), page = e < to ? __ldg(table + e) : -1;
       keys.k[j] = page >= 0 && page < p.pa.n_pages ? kChosen : 0u;
     }
-    emit(team, keys, 0u, 0u, p.n_select, out);
-    return;
-  }
-  const uint32_t* const src = p.keys + item * p.key_stride;
+  } else {
+    const uint32_t* const src = p.keys + item * p.key_stride;
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int32_t e = keys.place(team, j);
-    keys.k[j] = e < to ? __ldg(src + e) : 0u;
-  }
-  // (bits of non-negative floats have their order, NaN above all)
-  uint32_t most = 0;
-  const float* const largest = p.largest + (static_cast<int64_t>(req) * p.n_kvheads + kvh) * p.bound_tiles;
-  for (int32_t i = lane; i * kBoundTile < n; i += 32) most = max(most, __float_as_uint(__ldg(largest + i)));
-  const float q_sum = __ldg(p.reach + item), bound = __uint_as_float(__reduce_max_sync(0xffffffffu, most));
-  const float reach = q_sum * bound;
-  // beyond these, sums overflow or products lose bits in fp32 (NaN fails all comparisons)
-  const bool wide = !(reach < 0x1p126f && reach > 0x1p-80f && q_sum > 0x1p-100f && bound > 0x1p-100f);
-  const float eps = q_sum == 0.0f || bound == 0.0f ? 0.0f : wide ? INFINITY : reach * kScoreError<D>;
+    for (int j = 0; j < N; ++j) {
+      const int32_t e = keys.place(team, j);
+      keys.k[j] = e < to ? __ldg(src + e) : 0u;
+    }
+    // (bits of non-negative floats have their order, NaN above all)
+    uint32_t most = 0;
+    const float* const largest = p.largest + (static_cast<int64_t>(req) * p.n_kvheads + kvh) * p.bound_tiles;
+    for (int32_t i = lane; i * kBoundTile < n; i += 32) most = max(most, __float_as_uint(__ldg(largest + i)));
+    const float q_sum = __ldg(p.reach + item), bound = __uint_as_float(__reduce_max_sync(0xffffffffu, most));
+    reach = q_sum * bound;
+    // beyond these, sums overflow or products lose bits in fp32 (NaN fails all comparisons)
+    wide = !(reach < 0x1p126f && reach > 0x1p-80f && q_sum > 0x1p-100f && bound > 0x1p-100f);
+    eps = q_sum == 0.0f || bound == 0.0f ? 0.0f : wide ? INFINITY : reach * kScoreError<D>;
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int32_t e = keys.place(team, j);
-    if (keys.k[j] != 0 && (e < p.n_first || e > mine - p.n_last)) keys.k[j] = kChosen;
+    for (int j = 0; j < N; ++j) {
+      const int32_t e = keys.place(team, j);
+      if (keys.k[j] != 0 && (e < p.n_first || e > mine - p.n_last)) keys.k[j] = kChosen;
+    }
   }
   const T* const q = static_cast<const T*>(p.q) + (row * p.n_qheads + static_cast<int64_t>(kvh) * p.group) * D;
   const T* const bounds = static_cast<const T*>(p.bounds) + static_cast<int64_t>(kvh) * 2 * D;
@@ -224,7 +225,8 @@ cudaError_t launch_select_team(const ChooseParams& p, cudaStream_t stream) {
 // A team's size.  A warp does a row of up to 1024 pages with a fraction of a block's instructions and without its barriers,
 // but takes longer; a block is for few rows and for longer lists.  Whole calls, us, warps / blocks, 24/2 heads of 256 dims:
 // one row of 512 pages 20.7 / 15.6, 64 rows 47.9 / 33.3, 400 rows 115 / 106, 600 rows 51.3 / 53.1, 8192 rows 208 / 411;
-// 1000 rows of 110 pages 33.3 / 55.1; 300 rows of 938 pages 135 / 127, 4000 rows 220 / 279.
+// 1000 rows of 110 pages 33.3 / 55.1; 300 rows of 938 pages 135 / 127, 4000 rows 220 / 279.  (Both with the choice's steps
+// written out; with one loop and a plain emission 8192 rows take 196.)
 template <int D, typename T>
 cudaError_t launch_select_type(const ChooseParams& p, int num_sms, cudaStream_t stream) {
   const int32_t n = p.pa.pages_per_req;
