@@ -483,7 +483,8 @@ qsa_status qsa_page_bounds(const void* k_cache, const int32_t* cu_seqlens_q, con
  * with a page id from 0 to n_pages - 1).  It takes those below n_first and above p / page_size - n_last, and of the
  * others the ones with the highest scores,
  *   score = max over the query heads of the KV head of  sum_d max(q_d lo_d, q_d hi_d),
- * ties going to the lower page, up to n_select in all.  The sum is the most that q.k can be for a key of the page.
+ * ties going to the lower page, up to n_select in all.  The sum is the most that q.k can be for a key of the page.  (Of
+ * the two products it takes the one with hi_d where q_d > 0, else the one with lo_d, also where a bound is not finite.)
  * What is chosen does not depend on the roundings of 32-bit sums: where these cannot part the scores next to the last
  * place, the scores are summed anew with an error below 2^-44 of the sum of their products' magnitudes (in 64 bits where
  * sums leave fp32's range).  A NaN score stands above all others.

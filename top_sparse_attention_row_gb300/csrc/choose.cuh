@@ -255,7 +255,7 @@ __device__ __forceinline__ void choose(Team<THREADS>& t, Keys<THREADS, N>& keys,
     for (int stage = 0;; ++stage) {
       bar = kth_largest(t, keys, want);
       uint32_t lo = bar, hi = bar;
-      if (stage == 0) {
+      if (stage == 0 && eps != 0.0f) {
         const float s = score_of(bar), e2 = 2.0f * eps;
         const bool bounded = bar != kNan && isfinite(s) && isfinite(e2);
         lo = bounded ? key_of(__fsub_rd(s, e2)) : 1u;      // no bound on the error: all may belong

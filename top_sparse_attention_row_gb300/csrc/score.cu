@@ -92,12 +92,17 @@ __device__ __forceinline__ Item load_item(const Item* r) {
   return Item{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
-// Largest of v[from .. from + N).
+// The larger of two scores; NaN stays.
+__device__ __forceinline__ float larger(float a, float b) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+  return a;
+}
+// Largest of v[0 .. N).
 template <int N>
 __device__ __forceinline__ float largest_of(const float* v) {
   float m = v[0];
 #pragma unroll
-  for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+  for (int i = 1; i < N; ++i) m = larger(m, v[i]);
   return m;
 }
 
@@ -214,7 +219,7 @@ __global__ void __launch_bounds__(ScoreCfg<D, QROWS>::kThreads, 1) page_score_ke
               tmem_ld16(from + t * g + h0, v);
               tc_wait_ld();
 #pragma unroll
-              for (int h = 0; h < 16; ++h) m = h0 + h < g ? fmaxf(m, v[h]) : m;
+              for (int h = 0; h < 16; ++h) m = h0 + h < g ? larger(m, v[h]) : m;
             }
             put(t, m);
           }

@@ -190,7 +190,9 @@ __global__ void __launch_bounds__(TEAM == 32 ? 32 * kWarpTeams : TEAM, TEAM == 3
     reach = q_sum * bound;
     // beyond these, sums overflow or products lose bits in fp32 (NaN fails all comparisons)
     wide = !(reach < 0x1p126f && reach > 0x1p-80f && q_sum > 0x1p-100f && bound > 0x1p-100f);
-    eps = q_sum == 0.0f || bound == 0.0f ? 0.0f : wide ? INFINITY : reach * kScoreError<D>;
+    // sums of zeros are exact (0 times infinity or NaN is none: those scores are taken anew)
+    const bool zeros = (q_sum == 0.0f && bound < INFINITY) || (bound == 0.0f && q_sum < INFINITY);
+    eps = zeros ? 0.0f : wide ? INFINITY : reach * kScoreError<D>;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int32_t e = keys.place(team, j);
