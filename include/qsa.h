@@ -535,11 +535,11 @@ size_t qsa_selected_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t 
  * sees all positions up to its own, as in qsa_window_attention_paged without a window, but the positions that the
  * requests of a group share are read once for all of their rows.
  *   cu_groups [n_groups + 1] int32, non-decreasing: group g holds the requests cu_groups[g] .. cu_groups[g + 1] - 1;
- *             requests outside every group share nothing
+ *             requests outside every group share nothing, and those without rows in the step have no part in theirs
  *   prefix_lens [n_groups] int32: positions below prefix_lens[g] hold the same keys and values for all requests of the
- *             group; they are read through its first request's page table.  What a request of the group does not have
- *             as past (positions from the smallest kv_len - rows of the group on) is not shared, whatever
- *             prefix_lens says.
+ *             group; they are read through its first request's page table (the first one's that has rows).  What a
+ *             request of the group does not have as past (positions from the smallest kv_len - rows of the group on)
+ *             is not shared, whatever prefix_lens says.
  *   workspace: qsa_prefix_workspace_bytes, 256-byte aligned; NULL: taken from the library's pool on `stream`.
  * The other arguments, rows that see nothing, rows behind the last request, non-finite values and precision are as in
  * qsa_window_attention_paged (a non-finite value in V may also reach rows of other requests of the group).

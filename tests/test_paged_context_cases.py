@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from test_paged_context import Batch, check_select
+from test_paged_context import Batch, check_prefix, check_select
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +45,15 @@ def test_select_of_queries_that_are_not_finite(B, group):
     check_select(B, b, bounds, 9, 1, 1)
     bounds[:] = 0                                          # 0 times infinity everywhere
     check_select(B, b, bounds, 9, 1, 1)
+
+
+# ------------------------------------------------------------------------------ requests without rows
+@pytest.mark.parametrize("kv", [0, 100, 700])
+def test_prefix_group_that_begins_with_a_request_without_rows(B, kv):
+    """Such a request has no part in its group: it may have ended, its pages gone to others or not in its table at all."""
+    lens = [(kv, 0)] + [(512 + 3 + 20 * i, 1) for i in range(6)] + [(0, 0), (512 + 90, 2)]
+    b = Batch(lens, 8, 2, 128, 16, seed=kv, share=[None, None] + [(1, 512)] * 5 + [None, (1, 512)])
+    assert kv > 0 or (b.table[0] == -1).all()
+    check_prefix(B, b, [0, 9], [512])
+    check_prefix(B, b, [0, 1, 9], [512, 512])              # a group of that request alone
+    check_prefix(B, b, [7, 9], [512])

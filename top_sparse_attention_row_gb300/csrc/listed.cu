@@ -150,34 +150,37 @@ __global__ void __launch_bounds__(kListThreads) list_pages_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------------------- shared prompts
-// What a group shares: the positions below prefix_len that all of its requests with rows have as past.
+// What a group shares: the positions below prefix_len that all of its requests with rows have as past, by the page table of
+// the first of these (a request without rows may have no pages any more).
 struct Group {
-  int32_t number, begin, row0, rows, shared;
+  int32_t number, table, row0, rows, shared;
 };
 // By whole warps.  Sharing pays where it saves more key tiles than it costs: the requests' tiles each read the shared keys
 // on their own, or the fewer tiles of the group's rows do, and cost about 5 key tiles each (query tile, first softmax,
 // output in fp32, join) and one more for every tile of a request, whose output is joined too.
 __device__ __forceinline__ Group make_group(const ListParams& p, int32_t g, int lane) {
   Group x{g, 0, 0, 0, 0};
-  x.begin = group_begin(p, g);
-  const int32_t end = max(group_begin(p, g + 1), x.begin);
-  x.row0 = __ldg(p.pa.cu_seqlens_q + x.begin);
+  const int32_t begin = group_begin(p, g), end = max(group_begin(p, g + 1), begin);
+  x.row0 = __ldg(p.pa.cu_seqlens_q + begin);
   x.rows = __ldg(p.pa.cu_seqlens_q + end) - x.row0;
-  int32_t past = INT32_MAX;
+  int32_t past = INT32_MAX, first = INT32_MAX;
   uint32_t tiles = 0;
-  for (int32_t i = x.begin + lane; i < end; i += 32) {
+  for (int32_t i = begin + lane; i < end; i += 32) {
     const int32_t fresh = __ldg(p.pa.cu_seqlens_q + i + 1) - __ldg(p.pa.cu_seqlens_q + i);
     if (fresh <= 0) continue;
     past = min(past, max(__ldg(p.pa.kv_lens + i), 0) - fresh);
+    first = min(first, i);
     tiles += (fresh + p.tile_tokens - 1) / p.tile_tokens;
   }
   past = __reduce_min_sync(0xffffffffu, past);
+  first = __reduce_min_sync(0xffffffffu, first);
   const int64_t own = __reduce_add_sync(0xffffffffu, tiles);
   const int64_t cap = static_cast<int64_t>(p.pa.pages_per_req) * p.pa.page_size;
   int64_t shared = min(past, __ldg(p.prefix_lens + g));
   if (shared > cap) shared = cap;
   const int64_t all = (x.rows + p.tile_tokens - 1) / p.tile_tokens, key_tiles = (shared + kWinTile - 1) / kWinTile;
   if (x.row0 >= 0 && shared > 0 && (own - all) * key_tiles > 5 * all + own) x.shared = static_cast<int32_t>(shared);
+  if (first < end) x.table = first;                        // (else nothing is shared: no request has rows)
   return x;
 }
 
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(kPrefixWarps * 32) list_prefix_kernel(const __
       const int64_t t0 = static_cast<int64_t>(t - group_tile(p, g)) * p.tile_tokens;
       const int64_t rows = min(static_cast<int64_t>(group.rows), p.n_rows - group.row0);
       if (group.shared > 0 && t0 >= 0 && t0 < rows) {
-        u.req = group.begin;
+        u.req = group.table;
         u.part = 0;
         u.row0 = group.row0 + static_cast<int32_t>(t0);
         u.tokens = static_cast<int32_t>(rows - t0 < p.tile_tokens ? rows - t0 : p.tile_tokens);

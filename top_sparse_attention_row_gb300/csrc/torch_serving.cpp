@@ -705,8 +705,8 @@ Attention of a batch whose requests begin alike: window_attention_paged without 
 shared keys read once for all requests of a group (qsa_prefix_attention_paged).
 
 cu_groups [n_groups + 1] int32: group g is the requests cu_groups[g] .. cu_groups[g + 1] - 1;
-prefix_lens [n_groups] int32: the positions below it hold the same keys for all of them.  The rest
-as in window_attention_paged.  Returns out [R, Hq, D] and lse [R, Hq] fp32 (None unless wanted).)doc";
+prefix_lens [n_groups] int32: the positions below it hold the same keys for all of them that have rows
+in the step.  The rest as in window_attention_paged.  Returns out [R, Hq, D] and lse [R, Hq] fp32 (None unless wanted).)doc";
 
 #define QSA_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_VARARGS | METH_KEYWORDS, k_doc_##f}
 PyMethodDef methods[] = {QSA_METHOD(page_plan), QSA_METHOD(rope), QSA_METHOD(rope_append), QSA_METHOD(rope_append_fp4),
