@@ -95,7 +95,11 @@ typedef struct qsa_counters {
  *            per-token path instead and counts a fallback; the result is the same.  Union mode
  *            requires each row's valid slots to be distinct (a repeated slot is used once).
  *   Slots must be < n_slots of the caches (not checked: the signature carries no slot
- *   count; use qsa_sparse_prefill_ex with n_kv_slots to have them treated as padding).
+ *   count; use qsa_sparse_prefill_ex with n_kv_slots to have them treated as padding).  Without a count
+ *   the kernel's tensor maps have 2^31 - 1 rows (slot x KV head) from the caches' first on, and
+ *   padding is fetched as the row behind them, 512 bytes x 2^31 further on in the address space, which
+ *   the copy engine fills with zeros and does not read.  With n_kv_slots the maps end where the caches
+ *   end.  Give it wherever it is known, as the Python binding does.
  *   Union mode allocates its workspace on `stream` (cudaMallocFromPoolAsync / cudaFreeAsync) from
  *   a stream-ordered memory pool the library creates per device, whose release threshold is
  *   unbounded: freed workspaces stay in that pool for later calls (until the process exits), so
@@ -208,7 +212,7 @@ qsa_status qsa_sparse_prefill_fp8_paged(const void* q, const void* k_cache, cons
  *   d_qk must be 576 and d_v 512 (QSA_ERR_UNSUPPORTED otherwise).  union_g as in
  *   qsa_sparse_prefill; a union needs union_g * n_heads <= 32, otherwise the per-token path
  *   runs and counts a fallback.  n_kv_slots: 0 = unchecked, > 0 = slots >= n_kv_slots are
- *   padding.  q, kv_cache and out must be 16-byte aligned.  Union workspace is allocated on
+ *   padding (and the tensor map ends there, as for qsa_sparse_prefill; rows are 1152 bytes here).  q, kv_cache and out must be 16-byte aligned.  Union workspace is allocated on
  *   `stream` from the library's pool (as for qsa_sparse_prefill).  Errors, streams and
  *   determinism are as for qsa_sparse_prefill. */
 qsa_status qsa_sparse_mla_prefill(const void* q, const void* kv_cache, const int32_t* indices,

@@ -207,14 +207,28 @@ def _require(t, dtype, name, ndim=None):
         raise ValueError(f"{name} must have {ndim} dims")
 
 
+def _slots_of(cache, heads: int) -> int:
+    """Slots that a call over this cache is checked against: all it has, so that the kernels' tensor maps end where it ends.
+    0 (unchecked) where they are more rows (slot x KV head) than the library counts."""
+    n = cache.shape[0]
+    return n if n * heads < 2 ** 31 - 1 else 0
+
+
+def _pages_of(cache, heads: int, page_size: int) -> int:
+    """The same in pages; 0 where the cache is not whole pages."""
+    n = _slots_of(cache, heads)
+    return n // page_size if page_size > 0 and n % page_size == 0 else 0
+
+
 def sparse_prefill(q, k_cache, v_cache, indices, topk_len, scale: float, *, out=None, lse=None,
                    union_g: int = 0, n_kv_slots: int = 0, workspace=None, forced: Optional[dict] = None,
                    want_lse: bool = True, stream=None):
     """O (bf16 [R, Hq, D]) and LSE (fp32 [R, Hq]) of top-k sparse attention prefill.
 
     q [R, Hq, D] bf16, k_cache / v_cache [S, Hkv, D] bf16, indices [R, topk] int32 (physical
-    slots, negative = padding), topk_len [R] int32 or None.  Calls qsa_sparse_prefill (or the
-    _ex entry when n_kv_slots / workspace / forced are given) on the current stream.
+    slots, negative or >= S = padding), topk_len [R] int32 or None.  Calls qsa_sparse_prefill_ex with
+    n_kv_slots slots (0: the S of the caches) on the current stream, or qsa_sparse_prefill for caches
+    that the library does not count.
     """
     import torch
     lib = load_library()
@@ -235,6 +249,7 @@ def sparse_prefill(q, k_cache, v_cache, indices, topk_len, scale: float, *, out=
     _require(out, torch.bfloat16, "out", 3)
     _require(lse, torch.float32, "lse", 2)
     s = _stream_ptr(stream)
+    n_kv_slots = n_kv_slots or _slots_of(k_cache, Hkv)
     if n_kv_slots or workspace is not None or forced:
         g = None
         if forced:
@@ -261,7 +276,8 @@ def sparse_prefill_paged(q, k_cache, v_cache, indices, topk_len, cu_seqlens_q, k
     """Paged call (qsa_sparse_prefill_paged): indices [R, topk] int32 are logical positions in
     each row's request; cu_seqlens_q [n_requests + 1] int32 row offsets; kv_lens [n_requests]
     int32 or None; page_table [n_requests, pages_per_req] int32; k_cache / v_cache
-    [n_pages * page_size, Hkv, D] bf16.  The translation to physical slots runs in the kernels."""
+    [n_pages * page_size, Hkv, D] bf16 (n_pages 0: what the caches hold).  The translation to physical
+    slots runs in the kernels."""
     import torch
     lib = load_library()
     _require(q, torch.bfloat16, "q", 3)
@@ -289,8 +305,8 @@ def sparse_prefill_paged(q, k_cache, v_cache, indices, topk_len, cu_seqlens_q, k
     st = lib.qsa_sparse_prefill_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(indices),
                                       _ptr(topk_len), _ptr(cu_seqlens_q), _ptr(kv_lens),
                                       _ptr(page_table), _ptr(out), _ptr(lse), R, n_req,
-                                      page_table.shape[1], int(page_size), int(n_pages), Hq, Hkv,
-                                      D, topk, float(scale), int(union_g), _stream_ptr(stream))
+                                      page_table.shape[1], int(page_size),
+                                      int(n_pages) or _pages_of(k_cache, Hkv, int(page_size)), Hq, Hkv, D, topk, float(scale), int(union_g), _stream_ptr(stream))
     _check(st, "qsa_sparse_prefill_paged")
     return out, lse
 
@@ -332,8 +348,8 @@ def sparse_prefill_fp8_paged(q, k_cache, v_cache, k_scale, v_scale, fp8_page_siz
                                           _ptr(v_scale), int(fp8_page_size), _ptr(indices),
                                           _ptr(topk_len), _ptr(cu_seqlens_q), _ptr(kv_lens),
                                           _ptr(page_table), _ptr(out), _ptr(lse), R, n_req,
-                                          page_table.shape[1], int(page_size), int(n_pages), Hq,
-                                          Hkv, D, topk, float(scale), int(union_g),
+                                          page_table.shape[1], int(page_size),
+                                          int(n_pages) or _pages_of(k_cache, Hkv, int(page_size)), Hq, Hkv, D, topk, float(scale), int(union_g),
                                           _stream_ptr(stream))
     _check(st, "qsa_sparse_prefill_fp8_paged")
     return out, lse
@@ -367,7 +383,8 @@ def sparse_prefill_fp8(q, k_cache, v_cache, k_scale, v_scale, page_size: int, in
     st = lib.qsa_sparse_prefill_fp8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
                                     _ptr(v_scale), int(page_size), _ptr(indices), _ptr(topk_len),
                                     _ptr(out), _ptr(lse), R, Hq, Hkv, D, topk, float(scale),
-                                    int(union_g), int(n_kv_slots), _stream_ptr(stream))
+                                    int(union_g), int(n_kv_slots) or _slots_of(k_cache, Hkv),
+                                    _stream_ptr(stream))
     _check(st, "qsa_sparse_prefill_fp8")
     return out, lse
 
@@ -375,8 +392,8 @@ def sparse_prefill_fp8(q, k_cache, v_cache, k_scale, v_scale, page_size: int, in
 def sparse_mla_prefill(q, kv_cache, indices, topk_len, scale: float, *, out=None, lse=None,
                        union_g: int = 0, n_kv_slots: int = 0, want_lse: bool = True, stream=None):
     """MLA shape (qsa_sparse_mla_prefill): q [R, H, 576] bf16, kv_cache [S, 576] bf16 (the first
-    512 dims are the value), indices [R, topk] int32 physical slots, topk_len [R] int32 or None.
-    Returns O [R, H, 512] bf16 and LSE [R, H] fp32."""
+    512 dims are the value), indices [R, topk] int32 physical slots (negative or >= S = padding; n_kv_slots
+    puts another number in place of S), topk_len [R] int32 or None.  Returns O [R, H, 512] bf16 and LSE [R, H] fp32."""
     import torch
     lib = load_library()
     _require(q, torch.bfloat16, "q", 3)
@@ -398,7 +415,7 @@ def sparse_mla_prefill(q, kv_cache, indices, topk_len, scale: float, *, out=None
     _require(lse, torch.float32, "lse", 2)
     st = lib.qsa_sparse_mla_prefill(_ptr(q), _ptr(kv_cache), _ptr(indices), _ptr(topk_len), _ptr(out),
                                     _ptr(lse), R, H, Dqk, Dv, topk, float(scale), int(union_g),
-                                    int(n_kv_slots), _stream_ptr(stream))
+                                    int(n_kv_slots) or _slots_of(kv_cache, 1), _stream_ptr(stream))
     _check(st, "qsa_sparse_mla_prefill")
     return out, lse
 
@@ -428,7 +445,8 @@ def sparse_mla_prefill_paged(q, kv_cache, indices, topk_len, cu_seqlens_q, kv_le
     st = lib.qsa_sparse_mla_prefill_paged(_ptr(q), _ptr(kv_cache), _ptr(indices), _ptr(topk_len),
                                           _ptr(cu_seqlens_q), _ptr(kv_lens), _ptr(page_table),
                                           _ptr(out), _ptr(lse), R, n_req, page_table.shape[1],
-                                          int(page_size), int(n_pages), H, Dqk, 512,
+                                          int(page_size), int(n_pages) or _pages_of(kv_cache, 1, int(page_size)),
+                                          H, Dqk, 512,
                                           indices.shape[1], float(scale), int(union_g),
                                           _stream_ptr(stream))
     _check(st, "qsa_sparse_mla_prefill_paged")
