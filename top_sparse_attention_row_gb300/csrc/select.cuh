@@ -176,17 +176,19 @@ __global__ void __launch_bounds__(TEAM == 32 ? 32 * kWarpTeams : TEAM, TEAM == 3
       keys.k[j] = page >= 0 && page < p.pa.n_pages ? kChosen : 0u;
     }
   } else {
+    // (plain loads of what the score kernel writes, which may still run when this one starts: non-coherent ones are for
+    // what nobody writes from then on)
     const uint32_t* const src = p.keys + item * p.key_stride;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int32_t e = keys.place(team, j);
-      keys.k[j] = e < to ? __ldg(src + e) : 0u;
+      keys.k[j] = e < to ? src[e] : 0u;
     }
     // (bits of non-negative floats have their order, NaN above all)
     uint32_t most = 0;
     const float* const largest = p.largest + (static_cast<int64_t>(req) * p.n_kvheads + kvh) * p.bound_tiles;
-    for (int32_t i = lane; i * kBoundTile < n; i += 32) most = max(most, __float_as_uint(__ldg(largest + i)));
-    const float q_sum = __ldg(p.reach + item), bound = __uint_as_float(__reduce_max_sync(0xffffffffu, most));
+    for (int32_t i = lane; i * kBoundTile < n; i += 32) most = max(most, __float_as_uint(largest[i]));
+    const float q_sum = p.reach[item], bound = __uint_as_float(__reduce_max_sync(0xffffffffu, most));
     reach = q_sum * bound;
     // beyond these, sums overflow or products lose bits in fp32 (NaN fails all comparisons)
     wide = !(reach < 0x1p126f && reach > 0x1p-80f && q_sum > 0x1p-100f && bound > 0x1p-100f);

@@ -280,8 +280,10 @@ __device__ __forceinline__ Unit listed_unit(const WindowParams& p, int32_t n) {
 __device__ __forceinline__ const PageEntry* unit_entries(const WindowParams& p, const Unit& u) {
   return p.entries + static_cast<int64_t>(u.shift) * p.list_cap;
 }
+// (a plain load: the kernel before, which writes the entries, may still run when this one starts, and only what nobody
+// writes from then on may be read by non-coherent loads)
 __device__ __forceinline__ PageEntry load_entry(const PageEntry* e) {
-  const int4 x = __ldg(reinterpret_cast<const int4*>(e));
+  const int4 x = *reinterpret_cast<const int4*>(e);
   return PageEntry{x.x, x.y, static_cast<uint32_t>(x.z), x.w};
 }
 __device__ __forceinline__ int32_t entry_of(const WindowParams& p, int32_t v) {
