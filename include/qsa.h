@@ -498,7 +498,12 @@ qsa_status qsa_page_bounds(const void* k_cache, const int32_t* cu_seqlens_q, con
  *   n_first >= 0, n_last >= 1 (the row's own page, which may be partly filled, is always taken where it exists),
  *   n_first + n_last <= n_select.
  *   workspace: qsa_page_select_workspace_bytes, 256-byte aligned; NULL: taken from the library's pool on `stream`.
- *   Calls that overlap need a workspace each.
+ *   Calls that overlap need a workspace each.  It holds a score of 4 bytes for every row, KV head and page of the table:
+ *   8192 rows, 8 KV heads and tables of 8192 pages take 2.1 GB.  A prompt can be called in parts of its rows (with kv_lens to match).
+ * The time depends on the scores.  Pages whose scores lie close to the last place are summed anew, by a row's own measure:
+ * its queries times the largest bound of any page it may choose.  One page of very large bounds, or many pages of equal ones,
+ * make that many pages (8192 rows over 512 pages: 0.2 ms, up to 10 with one such page and 19 if all are equal), and
+ * a NaN or infinity in a page's bounds makes it all pages of all rows that may choose it, in 64 bits (89 ms).
  * pages_per_req <= 32768, n_qheads / n_kvheads <= 128, head_dim 64, 128 or 256; 16-byte aligned q and bounds.
  * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED (beyond the limits above, n_rows * n_kvheads of 2^31 and more),
  * QSA_ERR_WORKSPACE; a wait inside the kernel that runs out is reported by qsa_get_device_status. */
@@ -516,7 +521,8 @@ size_t qsa_page_select_workspace_bytes(int64_t n_rows, int32_t n_requests, int32
  * at position p sees, with the query heads of a KV head, the positions j <= p whose page j / page_size is in its list.
  *   pages [n_rows, n_kvheads, n_select] int32 pages of the request's table, in any order; entries < 0 or >=
  *         pages_per_req, and pages whose id is < 0 or >= n_pages, are not seen; a page that is listed twice counts once
- *   page_size is a multiple of 8, pages_per_req <= 32768.
+ *   page_size is a multiple of 8, pages_per_req <= 32768.  Up to 32 tokens of a request share a tile of the tensor cores, so
+ *   that groups of one to three query heads fill a quarter to three quarters of it at most.
  *   workspace: qsa_selected_workspace_bytes, 256-byte aligned; NULL: taken from the library's pool on `stream`.
  * The other arguments, rows that see nothing, rows behind the last request, non-finite values and precision are as in
  * qsa_window_attention_paged (a non-finite value in V may also reach the rows of up to 127 neighbouring (token, head)
@@ -544,7 +550,9 @@ size_t qsa_selected_workspace_bytes(int64_t n_rows, int32_t n_requests, int32_t 
  *             group; they are read through its first request's page table (the first one's that has rows).  What a
  *             request of the group does not have as past (positions from the smallest kv_len - rows of the group on)
  *             is not shared, whatever prefix_lens says.
- *   workspace: qsa_prefix_workspace_bytes, 256-byte aligned; NULL: taken from the library's pool on `stream`.
+ *   workspace: qsa_prefix_workspace_bytes, 256-byte aligned; NULL: taken from the library's pool on `stream`.  It holds
+ *   two outputs in fp32 for every row and query head (8192 rows of 24 heads of 256 dims: 0.4 GB), whether or not
+ *   anything is shared.
  * The other arguments, rows that see nothing, rows behind the last request, non-finite values and precision are as in
  * qsa_window_attention_paged (a non-finite value in V may also reach rows of other requests of the group).
  * Errors: as qsa_window_attention_paged. */

@@ -7,7 +7,8 @@
 //
 // Scores are held as unsigned keys that have their order, 0 for entries that cannot be chosen and kChosen for those
 // that are in any case.  The k-th key is found by halving the range of keys and counting; the search ends as soon as a
-// value parts the k best from the others, after log2(entries) + 3 or so counts.  The exact scores are taken in two
+// value parts the k best from the others: after about ten counts where scores are well spread, more where one lies far from
+// the rest, 32 where equal scores straddle the last place.  The exact scores are taken in two
 // steps, their upper and their lower halves, so that they need no more room than the keys, however many there are.
 #pragma once
 

@@ -22,8 +22,11 @@
 //    see all of its pages).
 //  * What bounds it.  Prompts: shared memory.  An MMA reads 8 KB in the 65 cycles it takes alone (126 of 128 bytes a cycle),
 //    beside the gathers' writes and the queries', and a commit stands for two of them: ~4000 cycles a tile of 256 dims,
-//    2048 for its MMAs (8192 rows at 24k, 24/2 heads: 143 us, 0.63 PFLOP/s).  Decode: HBM's latency, with five or six
-//    stages of 32 KB on their way (64 rows at 64k to 128k: 47 us, 4.1 TB/s).
+//    2048 for its MMAs (8192 rows at 24k, 24/2 heads: 143 us, 0.63 PFLOP/s).  Decode: HBM at half its rate (64 rows at
+//    64k to 128k: 47 us, 4.1 TB/s).  Six stages of 32 KB an SM are more than its latency asks for.  Items are dealt out by
+//    their numbers, a third of which have no rows, so the block with the most has 12 page tiles where the mean is 10.2; an
+//    item is one tile of its queries, which are split anew for each into the one buffer that the item before it has
+//    to leave; and a stage is free only when the scan has read all of it.
 //  * Every mbarrier wait is bounded; a timeout records a code in the device status word, all roles leave their loops, copies
 //    and MMAs in flight are drained, tensor memory is freed.
 #include <cuda_bf16.h>
@@ -40,7 +43,7 @@ namespace {
 using namespace window_detail;
 
 // QROWS: columns that an item's queries may have, 128, or 32 where the batch is mostly single tokens: the room goes to the
-// ring then, for HBM's latency (64 tokens at 64k to 128k, 24/2 heads of 256 dims: 47 us of scores, with 128 columns 63).
+// ring then (64 tokens at 64k to 128k, 24/2 heads of 256 dims: 47 us of scores, with 128 columns 63).
 template <int D, int QROWS>
 struct ScoreCfg {
   static constexpr int kPer = D / 64;                      // stages of a tile of pages: 128 of 2 D dims each

@@ -74,7 +74,8 @@ __device__ __forceinline__ void load_dims(const T* p, float (&x)[PER]) {
 // whose error is below 2^-44 of the sum of the magnitudes, for the heads that come within fp32's error of the largest:
 // eight heads' fp32 sums are taken at a time, with exchanges that halve them.  Doubles would do too, but this GPU adds
 // few of them (two a cycle and SM: 230 us of 468 for 8192 prompt rows), so they are left to scores that floats cannot hold
-// (`wide`).  reach: sum of |q| times the largest bound.
+// (`wide`): all pages of a row over whose pages a bound is not finite, for one (one infinity in a prompt of 24k: 89 ms in
+// place of 0.2 for 8192 rows; one in the context of one of 64 decode rows: 3.6 ms in place of 0.06).  reach: sum of |q| times the largest bound.
 template <int D, typename T>
 __device__ __forceinline__ uint64_t exact_key(const T* q, const T* bounds, int group, int lane, float reach, bool wide) {
   constexpr int kPer = D / 32, kHeads = 8;

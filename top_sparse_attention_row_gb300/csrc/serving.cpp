@@ -356,7 +356,9 @@ bool plan_pages(int64_t n_rows, int32_t n_requests, int32_t n_kvheads, int32_t g
   return true;
 }
 
-// Shared prompts: always equal shares, since a row's two results are joined anyway.
+// Shared prompts: always equal shares, since a row's two results are joined anyway.  That costs a batch that shares nothing
+// up to 1.4 times window attention's time (4096 single tokens at 576, 32/8 heads of 128 dims: 1.92 ms, window attention
+// 1.37, behind one prompt of 512 1.23): the deal is static, and every block sums the tiles of all units before it begins.
 bool plan_prefix(int64_t n_rows, int32_t n_requests, int32_t n_groups, int32_t n_kvheads, int32_t group,
                  int32_t pages_per_req, int32_t page_size, int32_t head_dim, int32_t sms, ListedPlan* l) {
   l->w.tile_tokens = qsa::kWinTile / group;
