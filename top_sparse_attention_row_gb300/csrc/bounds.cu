@@ -118,12 +118,4 @@ cudaError_t launch_page_bounds(const BoundsParams& p, bool fp16, int num_sms, cu
                              : go(page_bounds_kernel<256, __nv_bfloat16>);
 }
 
-cudaError_t launch_page_select(const ChooseParams& p, bool fp16, int num_sms, cudaStream_t stream) {
-  const cudaError_t e = launch_page_score(p, fp16, num_sms, stream);
-  if (e != cudaSuccess) return e;
-  return p.head_dim == 64    ? launch_select_d64(p, fp16, num_sms, stream)
-         : p.head_dim == 128 ? launch_select_d128(p, fp16, num_sms, stream)
-                             : launch_select_d256(p, fp16, num_sms, stream);
-}
-
 }  // namespace qsa

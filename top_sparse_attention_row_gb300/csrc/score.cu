@@ -546,4 +546,13 @@ cudaError_t launch_page_score(const ChooseParams& p, bool fp16, int num_sms, cud
                              : launch_score_dim<256, __nv_bfloat16>(p, tb, grid, 5, stream);
 }
 
+// Scores, then the choice by them.
+cudaError_t launch_page_select(const ChooseParams& p, bool fp16, int num_sms, cudaStream_t stream) {
+  const cudaError_t e = launch_page_score(p, fp16, num_sms, stream);
+  if (e != cudaSuccess) return e;
+  return p.head_dim == 64    ? launch_select_d64(p, fp16, num_sms, stream)
+         : p.head_dim == 128 ? launch_select_d128(p, fp16, num_sms, stream)
+                             : launch_select_d256(p, fp16, num_sms, stream);
+}
+
 }  // namespace qsa
